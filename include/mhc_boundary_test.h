@@ -25,6 +25,10 @@ extern "C" {
  * device flag cannot be set. */
 mhc_status_t mhc_test_stall_stage_copies(int32_t on);
 
+/* The same for the matmul and moe kernels of mhc_sublayer.h
+ * (mhc_sublayer_check_errors reports). */
+mhc_status_t mhc_test_stall_sublayer_copies(int32_t on);
+
 #ifdef __cplusplus
 }
 #endif

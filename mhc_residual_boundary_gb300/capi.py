@@ -1,4 +1,5 @@
-"""ctypes binding of include/mhc_boundary.h (argument marshalling only).
+"""ctypes binding of include/mhc_boundary.h and include/mhc_sublayer.h
+(argument marshalling only).
 
 The functions keep the C names; every step of the boundary runs in the CUDA
 library.  Loading fails loudly when the library has not been built: there is
@@ -66,6 +67,47 @@ class mhc_profile_t(ctypes.Structure):
                 ("mixes_ms", ctypes.c_float)]
 
 
+MHC_SCORE_SOFTMAX = 0
+MHC_SCORE_SIGMOID = 1
+MHC_SUBLAYER_FP8 = 1 << 0
+MHC_SUBLAYER_RENORMALIZE = 1 << 1
+MHC_SUBLAYER_ROUTER_F32 = 1 << 2
+
+
+class mhc_sublayer_config_t(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("hidden", "intermediate", "num_experts", "shared_experts", "top_k",
+                                              "max_moe_tokens", "score")] + [
+        ("routed_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class mhc_sublayer_norm_args_t(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int32), ("h", ctypes.c_int32), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64), ("norm_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("residual_out", ctypes.c_void_p), ("output", ctypes.c_void_p),
+                ("values", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class mhc_sublayer_quantize_args_t(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int32), ("h", ctypes.c_int32), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("output", ctypes.c_void_p), ("values", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class mhc_sublayer_matmul_args_t(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("values", ctypes.c_void_p),
+                ("values_stride", ctypes.c_int64), ("scales", ctypes.c_void_p), ("scales_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("weight_stride", ctypes.c_int64), ("weight_scales", ctypes.c_void_p),
+                ("output", ctypes.c_void_p), ("output_stride", ctypes.c_int64), ("output_f32", ctypes.c_int32)]
+
+
+class mhc_sublayer_moe_args_t(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int32)] + [(f, ctypes.c_void_p) for f in (
+        "x", "router", "bias", "gate_up", "gate_up_scales", "down", "down_scales", "output", "idx", "weights")]
+
+
+SUBLAYER_CALLS = {"add_rms_norm": mhc_sublayer_norm_args_t, "quantize": mhc_sublayer_quantize_args_t,
+                  "swiglu": mhc_sublayer_quantize_args_t, "matmul": mhc_sublayer_matmul_args_t,
+                  "moe": mhc_sublayer_moe_args_t}
+
 _lib = None
 
 
@@ -101,6 +143,17 @@ def lib() -> ctypes.CDLL:
         h.mhc_mxfp8_scale_bytes.argtypes = [ctypes.c_int32, ctypes.c_int32]
         h.mhc_test_stall_stage_copies.argtypes = [ctypes.c_int32]
         h.mhc_test_stall_stage_copies.restype = st
+        h.mhc_test_stall_sublayer_copies.argtypes = [ctypes.c_int32]
+        h.mhc_test_stall_sublayer_copies.restype = st
+        h.mhc_sublayer_create.argtypes = [ctypes.POINTER(mhc_sublayer_config_t), ctypes.c_int, ctypes.POINTER(vp)]
+        for name, args in SUBLAYER_CALLS.items():
+            getattr(h, "mhc_sublayer_" + name).argtypes = [vp, ctypes.POINTER(args), vp]
+        h.mhc_sublayer_check_errors.argtypes = [vp]
+        h.mhc_sublayer_destroy.argtypes = [vp]
+        for name in ("create", "check_errors", "destroy", *SUBLAYER_CALLS):
+            getattr(h, "mhc_sublayer_" + name).restype = st
+        h.mhc_sublayer_last_error.argtypes = [vp]
+        h.mhc_sublayer_last_error.restype = ctypes.c_char_p
         h.mhc_mxfp8_scale_bytes.restype = ctypes.c_size_t
         h.mhc_boundary_launches_per_call.argtypes = [vp]
         h.mhc_boundary_launches_per_call.restype = ctypes.c_int32
@@ -176,6 +229,53 @@ def mhc_test_stall_stage_copies(on: bool) -> None:
     status = lib().mhc_test_stall_stage_copies(1 if on else 0)
     if status != MHC_OK:
         raise MhcError(status, "could not set the stall flag")
+
+
+def mhc_test_stall_sublayer_copies(on: bool) -> None:
+    """Test hook (include/mhc_boundary_test.h): the matmul and MoE kernels
+    launched from now on issue no input copies."""
+    status = lib().mhc_test_stall_sublayer_copies(1 if on else 0)
+    if status != MHC_OK:
+        raise MhcError(status, "could not set the stall flag")
+
+
+def _check_sublayer(status: int, handle) -> None:
+    if status != MHC_OK:
+        raise MhcError(status, lib().mhc_sublayer_last_error(handle).decode())
+
+
+def mhc_sublayer_create(config: mhc_sublayer_config_t, device: int) -> ctypes.c_void_p:
+    handle = ctypes.c_void_p()
+    _check_sublayer(lib().mhc_sublayer_create(ctypes.byref(config), int(device), ctypes.byref(handle)), None)
+    return handle
+
+
+def mhc_sublayer_add_rms_norm(handle, args: mhc_sublayer_norm_args_t, stream=None) -> None:
+    _check_sublayer(lib().mhc_sublayer_add_rms_norm(handle, ctypes.byref(args), _stream_ptr(stream)), handle)
+
+
+def mhc_sublayer_quantize(handle, args: mhc_sublayer_quantize_args_t, stream=None) -> None:
+    _check_sublayer(lib().mhc_sublayer_quantize(handle, ctypes.byref(args), _stream_ptr(stream)), handle)
+
+
+def mhc_sublayer_swiglu(handle, args: mhc_sublayer_quantize_args_t, stream=None) -> None:
+    _check_sublayer(lib().mhc_sublayer_swiglu(handle, ctypes.byref(args), _stream_ptr(stream)), handle)
+
+
+def mhc_sublayer_matmul(handle, args: mhc_sublayer_matmul_args_t, stream=None) -> None:
+    _check_sublayer(lib().mhc_sublayer_matmul(handle, ctypes.byref(args), _stream_ptr(stream)), handle)
+
+
+def mhc_sublayer_moe(handle, args: mhc_sublayer_moe_args_t, stream=None) -> None:
+    _check_sublayer(lib().mhc_sublayer_moe(handle, ctypes.byref(args), _stream_ptr(stream)), handle)
+
+
+def mhc_sublayer_check_errors(handle) -> None:
+    _check_sublayer(lib().mhc_sublayer_check_errors(handle), handle)
+
+
+def mhc_sublayer_destroy(handle) -> None:
+    _check_sublayer(lib().mhc_sublayer_destroy(handle), None)
 
 
 def mhc_boundary_profile_begin(handle, max_calls: int) -> None:

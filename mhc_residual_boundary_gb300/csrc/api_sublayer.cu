@@ -1,0 +1,297 @@
+// api_sublayer.cu -- host implementation of include/mhc_sublayer.h: argument
+// checks, the handle's scratch, and one kernel launch for each call.  Every
+// launch is a programmatic dependent one, so a call's setup overlaps the end
+// of the kernel before it on the stream.
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+#include <new>
+#include <string>
+
+#include "mhc_boundary_test.h"
+#include "mhc_sublayer.h"
+#include "sublayer.cuh"
+
+using namespace mhc;
+
+struct mhc_sublayer {
+  mhc_sublayer_config_t cfg;
+  int device = 0;
+  int sm_count = 0;
+  unsigned int *err = nullptr;       // device error word
+  // matmul: FP32 sums of split tiles (at most one 128 x 128 tile for each
+  // SM) and the tiles' arrival counters
+  float *scratch = nullptr;
+  size_t scratch_floats = 0;
+  unsigned int *counters = nullptr;
+  std::string last_error;
+};
+
+namespace {
+
+thread_local std::string g_sublayer_create_error;
+
+struct DeviceGuard {
+  int prev = -1;
+  explicit DeviceGuard(int device) {
+    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+    if (prev != device) cudaSetDevice(device);
+  }
+  ~DeviceGuard() {
+    int now = -1;
+    if (prev >= 0 && cudaGetDevice(&now) == cudaSuccess && now != prev) cudaSetDevice(prev);
+  }
+};
+
+mhc_status_t fail(std::string &slot, mhc_status_t status, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  slot = buf;
+  return status;
+}
+
+// One tensor of a call: what is checked before any launch.
+struct Tensor {
+  const char *name;
+  const void *p;
+  size_t align;
+  bool required;
+};
+
+template <size_t N>
+mhc_status_t check_tensors(std::string &msg, const Tensor (&tensors)[N]) {
+  for (const Tensor &t : tensors) {
+    if (!t.p) {
+      if (t.required) return fail(msg, MHC_ERR_INVALID_ARG, "%s is NULL", t.name);
+    } else if (reinterpret_cast<uintptr_t>(t.p) % t.align) {
+      return fail(msg, MHC_ERR_INVALID_ARG, "%s is not %zu-byte aligned", t.name, t.align);
+    }
+  }
+  return MHC_OK;
+}
+
+mhc_status_t check_stride(std::string &msg, const char *name, int64_t stride, int64_t width, int64_t step) {
+  if (stride < width || stride % step || stride > (int64_t(1) << 40))
+    return fail(msg, MHC_ERR_INVALID_ARG, "%s = %lld: at least %lld and a multiple of %lld", name, (long long)stride,
+                (long long)width, (long long)step);
+  return MHC_OK;
+}
+
+mhc_status_t launched(mhc_sublayer_t *s, cudaError_t e, const char *what) {
+  if (e == cudaSuccess) return MHC_OK;
+  return fail(s->last_error, MHC_ERR_CUDA, "%s kernel: %s", what, cudaGetErrorString(e));
+}
+
+mhc_status_t quantize_call(mhc_sublayer_t *s, const mhc_sublayer_quantize_args_t *a, bool swiglu,
+                           mhc_stream_t stream) {
+  if (!s) return MHC_ERR_INVALID_ARG;
+  std::string &msg = s->last_error;
+  if (!a) return fail(msg, MHC_ERR_INVALID_ARG, "args is NULL");
+  if (a->m < 0) return fail(msg, MHC_ERR_INVALID_ARG, "m is negative");
+  if (a->h < 8 || a->h % 8) return fail(msg, MHC_ERR_INVALID_ARG, "h must be a positive multiple of 8");
+  if (a->h > (1 << 28)) return fail(msg, MHC_ERR_UNSUPPORTED, "h > 2^28");
+  if (a->m == 0) return MHC_OK;
+  if (a->output && !swiglu) return fail(msg, MHC_ERR_INVALID_ARG, "quantize has no BF16 output");
+  const Tensor tensors[] = {{swiglu ? "gate_up" : "x", a->x, 16, true}, {"output", a->output, 16, false},
+                            {"values", a->values, 16, true}, {"scales", a->scales, 4, true}};
+  mhc_status_t st = check_tensors(msg, tensors);
+  if (st == MHC_OK) st = check_stride(msg, "x_stride", a->x_stride, int64_t(a->h) * (swiglu ? 2 : 1), 8);
+  // a row's 8-bit values are stored eight at a time
+  if (st != MHC_OK) return st;
+  DeviceGuard guard(s->device);
+  QuantParams p = {};
+  p.m = a->m;
+  p.h = a->h;
+  p.x = static_cast<const uint16_t *>(a->x);
+  p.x_stride = a->x_stride;
+  p.output = static_cast<uint16_t *>(a->output);
+  p.values = a->values;
+  p.scales = a->scales;
+  return launched(s, launch_quantize(p, swiglu, s->sm_count, reinterpret_cast<cudaStream_t>(stream)),
+                  swiglu ? "swiglu" : "quantize");
+}
+
+void release(mhc_sublayer_t *s) {
+  if (s->err) cudaFree(s->err);
+  if (s->scratch) cudaFree(s->scratch);
+  if (s->counters) cudaFree(s->counters);
+}
+
+}  // namespace
+
+extern "C" {
+
+mhc_status_t mhc_sublayer_create(const mhc_sublayer_config_t *config, int device, mhc_sublayer_t **out) {
+  std::string &msg = g_sublayer_create_error;
+  msg.clear();
+  if (!config || !out) return fail(msg, MHC_ERR_INVALID_ARG, "config and out are required");
+  const mhc_sublayer_config_t &c = *config;
+  if (c.num_experts < 0) return fail(msg, MHC_ERR_INVALID_ARG, "num_experts is negative");
+  if (c.flags & ~uint32_t(MHC_SUBLAYER_FP8 | MHC_SUBLAYER_RENORMALIZE | MHC_SUBLAYER_ROUTER_F32))
+    return fail(msg, MHC_ERR_INVALID_ARG, "unknown flag bits 0x%x", c.flags);
+  int count = 0;
+  if (cudaGetDeviceCount(&count) != cudaSuccess || device < 0 || device >= count)
+    return fail(msg, MHC_ERR_CUDA, "device %d is not available", device);
+  DeviceGuard guard(device);
+  mhc_sublayer_t *s = new (std::nothrow) mhc_sublayer();
+  if (!s) return fail(msg, MHC_ERR_OOM, "host allocation failed");
+  s->cfg = c;
+  s->device = device;
+  cudaError_t e = cudaDeviceGetAttribute(&s->sm_count, cudaDevAttrMultiProcessorCount, device);
+  if (e == cudaSuccess) e = matmul_set_attributes();
+  if (e == cudaSuccess) e = cudaMalloc(&s->err, sizeof(unsigned int));
+  if (e == cudaSuccess) e = cudaMemset(s->err, 0, sizeof(unsigned int));
+  s->scratch_floats = size_t(s->sm_count) * QBLOCK * QBLOCK;
+  if (e == cudaSuccess) e = cudaMalloc(&s->scratch, s->scratch_floats * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&s->counters, size_t(s->sm_count) * sizeof(unsigned int));
+  if (e == cudaSuccess) e = cudaMemset(s->counters, 0, size_t(s->sm_count) * sizeof(unsigned int));
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) {
+    const mhc_status_t st = e == cudaErrorMemoryAllocation ? MHC_ERR_OOM : MHC_ERR_CUDA;
+    cudaGetLastError();
+    release(s);
+    delete s;
+    return fail(msg, st, "create: %s", cudaGetErrorString(e));
+  }
+  *out = s;
+  return MHC_OK;
+}
+
+mhc_status_t mhc_sublayer_add_rms_norm(mhc_sublayer_t *s, const mhc_sublayer_norm_args_t *a, mhc_stream_t stream) {
+  if (!s) return MHC_ERR_INVALID_ARG;
+  std::string &msg = s->last_error;
+  if (!a) return fail(msg, MHC_ERR_INVALID_ARG, "args is NULL");
+  if (a->m < 0) return fail(msg, MHC_ERR_INVALID_ARG, "m is negative");
+  if (a->h < 8 || a->h % 8) return fail(msg, MHC_ERR_INVALID_ARG, "h must be a positive multiple of 8");
+  if (a->h > SUB_MAX_HIDDEN) return fail(msg, MHC_ERR_UNSUPPORTED, "h > %d", SUB_MAX_HIDDEN);
+  if (a->m == 0) return MHC_OK;
+  if (!a->residual_out && !a->output && !a->values) return fail(msg, MHC_ERR_INVALID_ARG, "no output is given");
+  if (a->residual_out && !a->residual) return fail(msg, MHC_ERR_INVALID_ARG, "residual_out needs residual");
+  if (!a->values != !a->scales) return fail(msg, MHC_ERR_INVALID_ARG, "values and scales go together");
+  const Tensor tensors[] = {{"x", a->x, 16, true}, {"residual", a->residual, 16, false},
+                            {"norm_weight", a->norm_weight, 16, true}, {"residual_out", a->residual_out, 16, false},
+                            {"output", a->output, 16, false}, {"values", a->values, 16, false},
+                            {"scales", a->scales, 4, false}};
+  mhc_status_t st = check_tensors(msg, tensors);
+  if (st == MHC_OK) st = check_stride(msg, "x_stride", a->x_stride, a->h, 8);
+  if (st == MHC_OK && a->residual) st = check_stride(msg, "residual_stride", a->residual_stride, a->h, 8);
+  if (st != MHC_OK) return st;
+  DeviceGuard guard(s->device);
+  NormParams p = {};
+  p.m = a->m;
+  p.h = a->h;
+  p.x = static_cast<const uint16_t *>(a->x);
+  p.residual = static_cast<const uint16_t *>(a->residual);
+  p.weight = static_cast<const uint16_t *>(a->norm_weight);
+  p.x_stride = a->x_stride;
+  p.residual_stride = a->residual_stride;
+  p.eps = a->eps;
+  p.residual_out = static_cast<uint16_t *>(a->residual_out);
+  p.output = static_cast<uint16_t *>(a->output);
+  p.values = a->values;
+  p.scales = a->scales;
+  return launched(s, launch_add_rms_norm(p, reinterpret_cast<cudaStream_t>(stream)), "norm");
+}
+
+mhc_status_t mhc_sublayer_quantize(mhc_sublayer_t *s, const mhc_sublayer_quantize_args_t *a, mhc_stream_t stream) {
+  return quantize_call(s, a, false, stream);
+}
+
+mhc_status_t mhc_sublayer_swiglu(mhc_sublayer_t *s, const mhc_sublayer_quantize_args_t *a, mhc_stream_t stream) {
+  return quantize_call(s, a, true, stream);
+}
+
+mhc_status_t mhc_sublayer_matmul(mhc_sublayer_t *s, const mhc_sublayer_matmul_args_t *a, mhc_stream_t stream) {
+  if (!s) return MHC_ERR_INVALID_ARG;
+  std::string &msg = s->last_error;
+  if (!a) return fail(msg, MHC_ERR_INVALID_ARG, "args is NULL");
+  if (a->m < 0) return fail(msg, MHC_ERR_INVALID_ARG, "m is negative");
+  if (a->n < 1) return fail(msg, MHC_ERR_INVALID_ARG, "n must be positive");
+  if (a->k < 16 || a->k % 16) return fail(msg, MHC_ERR_INVALID_ARG, "k must be a positive multiple of 16");
+  if (a->m > (1 << 24) || a->n > (1 << 24) || a->k > (1 << 24))
+    return fail(msg, MHC_ERR_UNSUPPORTED, "m, n or k > 2^24");
+  if (a->m == 0) return MHC_OK;
+  if (int64_t((a->m + 127) / 128) * qblocks(a->n) > (1 << 30))
+    return fail(msg, MHC_ERR_UNSUPPORTED, "more than 2^30 output tiles");
+  const Tensor tensors[] = {{"values", a->values, 16, true}, {"scales", a->scales, 4, true},
+                            {"weight", a->weight, 16, true}, {"weight_scales", a->weight_scales, 4, true},
+                            {"output", a->output, size_t(a->output_f32 ? 4 : 2), true}};
+  mhc_status_t st = check_tensors(msg, tensors);
+  if (st == MHC_OK) st = check_stride(msg, "values_stride", a->values_stride, a->k, 16);
+  if (st == MHC_OK) st = check_stride(msg, "weight_stride", a->weight_stride, a->k, 16);
+  if (st == MHC_OK) st = check_stride(msg, "scales_stride", a->scales_stride, qblocks(a->k), 1);
+  if (st == MHC_OK) st = check_stride(msg, "output_stride", a->output_stride, a->n, 1);
+  if (st != MHC_OK) return st;
+  DeviceGuard guard(s->device);
+  MatmulParams p = {};
+  p.m = a->m;
+  p.n = a->n;
+  p.k = a->k;
+  p.values = a->values;
+  p.values_stride = a->values_stride;
+  p.scales = a->scales;
+  p.scales_stride = a->scales_stride;
+  p.weight = a->weight;
+  p.weight_stride = a->weight_stride;
+  p.weight_scales = a->weight_scales;
+  p.output = a->output;
+  p.output_stride = a->output_stride;
+  p.output_f32 = a->output_f32 != 0;
+  const int64_t row_step = a->output_f32 ? 4 : 8;
+  p.vector_out = reinterpret_cast<uintptr_t>(a->output) % 16 == 0 && a->output_stride % row_step == 0;
+  p.scratch = s->scratch;
+  p.scratch_floats = s->scratch_floats;
+  p.counters = s->counters;
+  p.counter_count = s->sm_count;
+  p.err = s->err;
+  return launched(s, launch_block_matmul(p, s->sm_count, reinterpret_cast<cudaStream_t>(stream)), "matmul");
+}
+
+mhc_status_t mhc_sublayer_moe(mhc_sublayer_t *s, const mhc_sublayer_moe_args_t *a, mhc_stream_t stream) {
+  if (!s) return MHC_ERR_INVALID_ARG;
+  (void)a;
+  (void)stream;
+  return fail(s->last_error, MHC_ERR_UNSUPPORTED, "created without experts");
+}
+
+mhc_status_t mhc_sublayer_check_errors(mhc_sublayer_t *s) {
+  if (!s) return MHC_ERR_INVALID_ARG;
+  DeviceGuard guard(s->device);
+  unsigned int flag = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(&flag, s->err, sizeof flag, cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && flag) {
+    // a call that gave up leaves its arrival counters half way
+    e = cudaMemset(s->err, 0, sizeof flag);
+    if (e == cudaSuccess) e = cudaMemset(s->counters, 0, size_t(s->sm_count) * sizeof(unsigned int));
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  }
+  if (e != cudaSuccess) return fail(s->last_error, MHC_ERR_CUDA, "check_errors: %s", cudaGetErrorString(e));
+  if (flag & 2u)
+    return fail(s->last_error, MHC_ERR_TIMEOUT,
+                "a kernel gave up one of its bounded waits (copies or tensor-core work); its outputs are not valid");
+  return MHC_OK;
+}
+
+mhc_status_t mhc_sublayer_destroy(mhc_sublayer_t *s) {
+  if (!s) return MHC_OK;
+  {
+    DeviceGuard guard(s->device);
+    release(s);
+  }
+  delete s;
+  return MHC_OK;
+}
+
+const char *mhc_sublayer_last_error(const mhc_sublayer_t *s) {
+  return s ? s->last_error.c_str() : g_sublayer_create_error.c_str();
+}
+
+}  // extern "C"
+
+mhc_status_t mhc_test_stall_sublayer_copies(int32_t on) {
+  return matmul_stall_copies(on ? 1 : 0) == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
+}

@@ -1,0 +1,181 @@
+// k_rowquant.cu -- RMS norm with the residual's addition, and the 8-bit
+// quantisers (plain and SwiGLU), rows in BF16, 8-bit outputs as E4M3 values
+// with one FP32 scale for each 128 values of a row.
+//
+// All are bound by memory: the norm moves 2 + 2 bytes in and up to 2 + 2 + 1
+// out for each element, quantize 2 in and 1 out, swiglu 4 in and 1 out.  Every
+// value crosses the memory once: the row stays in registers between its
+// reduction and its output.  A thread holds 16-byte fragments (8 values), so
+// 16 neighbouring lanes hold one block of 128 and its largest magnitude takes
+// four shuffles.  Magnitudes are compared as the bit patterns of |x|: their
+// order is that of the numbers, with infinity above them and NaN above that,
+// so a non-finite value always reaches the block's scale.
+#include <algorithm>
+
+#include "device_common.cuh"
+#include "sublayer.cuh"
+
+namespace mhc {
+namespace {
+
+constexpr uint32_t AMAX_FLOOR_BITS = uint32_t(127 - 100) << 23;   // 2^-100
+
+// Bit pattern of the largest |y| of this lane's block (16 lanes).
+__device__ __forceinline__ uint32_t block_amax(const float (&y)[8]) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(y[i]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+  return max(a, AMAX_FLOOR_BITS);
+}
+
+// Eight values to E4M3 at inv = 448 / amax.
+__device__ __forceinline__ uint2 quant8(const float (&y)[8], float inv) {
+  return make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                    e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+}
+
+// Quantises this lane's fragment `f` of a row (live: within the row); the
+// whole warp calls it.
+__device__ __forceinline__ void store_quant(const float (&y)[8], bool live, int f, uint8_t *values, float *scales) {
+  const float amax = __uint_as_float(block_amax(y));
+  if (live) {
+    *reinterpret_cast<uint2 *>(values + size_t(f) * 8) = quant8(y, __fdiv_rn(E4M3_MAX, amax));
+    if (f % (QBLOCK / 8) == 0) scales[f / (QBLOCK / 8)] = __fdiv_rn(amax, E4M3_MAX);
+  }
+}
+
+// One row per threadIdx.y, VPT fragments a thread.
+template <int VPT>
+__global__ void __launch_bounds__(256) k_add_rms_norm(const NormParams p) {
+  __shared__ float part[8];
+  const int tx = threadIdx.x, T = blockDim.x;
+  const int warps = T / 32, warp = threadIdx.y * warps + tx / 32;
+  const int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const bool live_row = row < p.m;
+  const int frags = p.h / 8;
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint16_t *x = p.x + size_t(live_row ? row : 0) * p.x_stride;
+  const uint16_t *res = p.residual ? p.residual + size_t(live_row ? row : 0) * p.residual_stride : nullptr;
+  uint4 xv[VPT], rv[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int f = i * T + tx;
+    const bool live = live_row && f < frags;
+    xv[i] = live ? ld_stream(x + size_t(f) * 8) : make_uint4(0, 0, 0, 0);
+    rv[i] = live && res ? ld_stream(res + size_t(f) * 8) : make_uint4(0, 0, 0, 0);
+  }
+  float r[VPT][8], ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    float b[8];
+    unpack8(xv[i], r[i]);
+    unpack8(rv[i], b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (res) r[i][k] += b[k];
+      ss = fmaf(r[i][k], r[i][k], ss);
+    }
+  }
+  ss = warp_sum(ss);
+  if (warps > 1) {
+    if (tx % 32 == 0) part[warp] = ss;
+    __syncthreads();
+    const int lane = tx % 32;
+    ss = warp_sum(lane < warps ? part[threadIdx.y * warps + lane] : 0.f);
+  }
+  const float rstd = __frsqrt_rn(__fdiv_rn(ss, float(p.h)) + p.eps);
+  const size_t base = size_t(row) * p.h;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int f = i * T + tx;
+    const bool live = live_row && f < frags;
+    const size_t at = base + size_t(f) * 8;
+    if (live && p.residual_out) st_vec(p.residual_out + at, pack8(r[i]));
+    if (!p.output && !p.values) continue;
+    float w[8];
+    unpack8(live ? ld_ro(p.weight + size_t(f) * 8) : make_uint4(0, 0, 0, 0), w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[i][k] = r[i][k] * rstd * w[k];
+    if (live && p.output) st_vec(p.output + at, pack8(r[i]));
+    if (p.values) store_quant(r[i], live, f, p.values + base, p.scales + size_t(row) * qblocks(p.h));
+  }
+}
+
+// One block of 128 per 16 lanes, grid-stride over all blocks of all rows.
+template <bool SWIGLU>
+__global__ void __launch_bounds__(256) k_quantize(const QuantParams p) {
+  const int per_row = qblocks(p.h);
+  const int64_t blocks = int64_t(p.m) * per_row;
+  const int lane16 = threadIdx.x % 16;
+  pdl_wait();
+  pdl_launch_dependents();
+  // both halves of a warp take the same number of rounds (the shuffles need
+  // all 32 lanes)
+  for (int64_t b0 = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32 * 2; b0 < blocks;
+       b0 += int64_t(gridDim.x) * blockDim.x / 16) {
+    const int64_t b = b0 + threadIdx.x % 32 / 16;
+    const int64_t row = b / per_row;
+    const int f = int(b - row * per_row) * 16 + lane16;
+    const bool live = b < blocks && f * 8 < p.h;
+    float y[8] = {};
+    if (live) {
+      const uint16_t *x = p.x + row * p.x_stride + size_t(f) * 8;
+      const uint4 g = ld_stream(x);
+      if (SWIGLU) {
+        const uint4 u = ld_stream(x + p.h);
+        float up[8];
+        unpack8(g, y);
+        unpack8(u, up);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = y[k] / (1.f + expf(-y[k])) * up[k];
+      } else {
+        unpack8(g, y);
+      }
+    }
+    if (live && p.output) st_vec(p.output + row * p.h + size_t(f) * 8, pack8(y));
+    store_quant(y, live, f, p.values + row * p.h, p.scales + row * per_row);
+  }
+}
+
+template <class Kernel, class Params>
+cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, const Params &p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, p);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rms_norm(const NormParams &p, cudaStream_t stream) {
+  const int frags = p.h / 8;
+  const int vpt = frags <= 256 ? 1 : frags <= 512 ? 2 : frags <= 1024 ? 4 : 8;
+  const int T = ((frags + vpt - 1) / vpt + 31) / 32 * 32;
+  const int rows = std::max(1, 256 / T);
+  const dim3 grid((p.m + rows - 1) / rows), block(T, rows);
+  switch (vpt) {
+    case 1: return launch_pdl(k_add_rms_norm<1>, grid, block, p, stream);
+    case 2: return launch_pdl(k_add_rms_norm<2>, grid, block, p, stream);
+    case 4: return launch_pdl(k_add_rms_norm<4>, grid, block, p, stream);
+    default: return launch_pdl(k_add_rms_norm<8>, grid, block, p, stream);
+  }
+}
+
+cudaError_t launch_quantize(const QuantParams &p, bool swiglu, int sms, cudaStream_t stream) {
+  const int64_t blocks = int64_t(p.m) * qblocks(p.h);
+  const int64_t ctas = (blocks + 15) / 16;
+  const dim3 grid(unsigned(std::min<int64_t>(ctas, int64_t(sms) * 32)));
+  return swiglu ? launch_pdl(k_quantize<true>, grid, dim3(256), p, stream)
+                : launch_pdl(k_quantize<false>, grid, dim3(256), p, stream);
+}
+
+}  // namespace mhc

@@ -1,0 +1,78 @@
+// sublayer.cuh -- parameter blocks and launchers of the sublayer operators
+// (internal to the library; the public surface is include/mhc_sublayer.h).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace mhc {
+
+constexpr int QBLOCK = 128;              // values that share a scale
+constexpr float E4M3_MAX = 448.0f;
+constexpr int SUB_MAX_HIDDEN = 16384;    // widest row of the norm's register tiling
+
+constexpr int qblocks(int n) { return (n + QBLOCK - 1) / QBLOCK; }
+
+struct NormParams {
+  int m, h;
+  const uint16_t *x, *residual, *weight;  // residual may be null
+  int64_t x_stride, residual_stride;
+  float eps;
+  uint16_t *residual_out, *output;        // null: not written
+  uint8_t *values;                        // null: not written
+  float *scales;
+};
+
+struct QuantParams {
+  int m, h;
+  const uint16_t *x;                      // [m][h], or [m][2h] gate and up
+  int64_t x_stride;
+  uint16_t *output;                       // null: not written
+  uint8_t *values;
+  float *scales;
+};
+
+struct MatmulParams {
+  int m, n, k;
+  const uint8_t *values, *weight;         // e4m3
+  int64_t values_stride, weight_stride;
+  const float *scales, *weight_scales;    // [m][k_blocks], [n_blocks][k_blocks]
+  int64_t scales_stride;
+  void *output;                           // bf16 or f32
+  int64_t output_stride;
+  int output_f32;
+  int vector_out;                         // the output's rows start on 16-byte boundaries
+  float *scratch;                         // sums of split tiles
+  size_t scratch_floats;
+  unsigned int *counters;                 // arrivals of a split tile's items, zero between calls
+  int counter_count;
+  unsigned int *err;                      // bit 1: a bounded wait gave up
+  // set by the launcher
+  int k_blocks, n_blocks, m_tiles, n_tiles, splits, stages;
+  int a_rows;                             // rows of a stage's `values` tile
+};
+
+// Work item `item` of a matmul: a tile of 128 rows by BN columns and a range
+// of its k blocks.  Neighbouring items share the weight tile.
+struct WorkItem {
+  int m0, n_tile, tile, split, kb0, kb1;
+};
+__device__ __forceinline__ WorkItem work_item(const MatmulParams &p, int item) {
+  WorkItem w;
+  w.split = item % p.splits;
+  w.tile = item / p.splits;
+  w.m0 = (w.tile % p.m_tiles) * 128;
+  w.n_tile = w.tile / p.m_tiles;
+  w.kb0 = int(int64_t(p.k_blocks) * w.split / p.splits);
+  w.kb1 = int(int64_t(p.k_blocks) * (w.split + 1) / p.splits);
+  return w;
+}
+
+cudaError_t matmul_set_attributes();
+cudaError_t matmul_stall_copies(int on);   // test hook, see include/mhc_boundary_test.h
+cudaError_t launch_block_matmul(const MatmulParams &p, int sms, cudaStream_t stream);
+
+cudaError_t launch_add_rms_norm(const NormParams &p, cudaStream_t stream);
+cudaError_t launch_quantize(const QuantParams &p, bool swiglu, int sms, cudaStream_t stream);
+
+}  // namespace mhc
