@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <new>
 #include <string>
+#include <type_traits>
 
 #include "mhc_boundary_test.h"
 #include "mhc_sublayer.h"
@@ -24,6 +25,11 @@ struct mhc_sublayer {
   float *scratch = nullptr;
   size_t scratch_floats = 0;
   unsigned int *counters = nullptr;
+  // moe (num_experts > 0): its scratch, in one allocation
+  MoeScratch moe = {};
+  unsigned char *moe_base = nullptr;
+  size_t moe_counter_bytes = 0;      // the counters are its first bytes
+  int moe_slots = 0;
   std::string last_error;
 };
 
@@ -114,7 +120,38 @@ mhc_status_t quantize_call(mhc_sublayer_t *s, const mhc_sublayer_quantize_args_t
                   swiglu ? "swiglu" : "quantize");
 }
 
+// Carves the MoE scratch out of s->moe_base (null: returns its size only).
+size_t moe_layout(mhc_sublayer_t *s) {
+  const mhc_sublayer_config_t &c = s->cfg;
+  const bool fp8 = (c.flags & MHC_SUBLAYER_FP8) != 0;
+  const size_t m = c.max_moe_tokens, slots = m * (c.top_k + c.shared_experts);
+  const size_t reached = size_t(c.shared_experts) + (size_t(c.num_experts) < m * c.top_k ? size_t(c.num_experts) : m * c.top_k);
+  const size_t ib = qblocks(c.intermediate), hb = qblocks(c.hidden);
+  size_t off = 0;
+  auto take = [&](auto *&p, size_t bytes) {
+    p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(s->moe_base + off);
+    off += (bytes + 255) / 256 * 256;
+  };
+  MoeScratch &q = s->moe;
+  take(q.control, MOE_CONTROL * 4);
+  take(q.up_counters, reached * ib * 4);
+  take(q.down_counters, hb * 4);
+  s->moe_counter_bytes = off;
+  take(q.logits, m * c.num_experts * 4);
+  take(q.x_pieces, fp8 ? 2 * m * c.hidden : 0);
+  take(q.x_scale, m * 4);
+  take(q.up, MOE_UP_FRAGMENTS * slots * 2 * ib * QBLOCK * 4);
+  unsigned char *act;
+  take(act, slots * (fp8 ? 3 : 4) * c.intermediate);
+  q.act = act;
+  take(q.act_scale, fp8 ? ib * slots * 4 : 0);
+  take(q.down, MOE_DOWN_FRAGMENTS * hb * m * QBLOCK * 4);
+  s->moe_slots = int(slots);
+  return off;
+}
+
 void release(mhc_sublayer_t *s) {
+  if (s->moe_base) cudaFree(s->moe_base);
   if (s->err) cudaFree(s->err);
   if (s->scratch) cudaFree(s->scratch);
   if (s->counters) cudaFree(s->counters);
@@ -132,6 +169,22 @@ mhc_status_t mhc_sublayer_create(const mhc_sublayer_config_t *config, int device
   if (c.num_experts < 0) return fail(msg, MHC_ERR_INVALID_ARG, "num_experts is negative");
   if (c.flags & ~uint32_t(MHC_SUBLAYER_FP8 | MHC_SUBLAYER_RENORMALIZE | MHC_SUBLAYER_ROUTER_F32))
     return fail(msg, MHC_ERR_INVALID_ARG, "unknown flag bits 0x%x", c.flags);
+  if (c.num_experts > 0) {
+    const int unit = c.flags & MHC_SUBLAYER_FP8 ? 16 : 8;
+    if (c.hidden < unit || c.hidden % unit || c.intermediate < unit || c.intermediate % unit)
+      return fail(msg, MHC_ERR_INVALID_ARG, "hidden and intermediate must be positive multiples of %d", unit);
+    if (c.hidden > SUB_MAX_HIDDEN || c.intermediate > SUB_MAX_HIDDEN)
+      return fail(msg, MHC_ERR_UNSUPPORTED, "hidden or intermediate > %d", SUB_MAX_HIDDEN);
+    if (c.num_experts > MOE_EXPERTS_MAX) return fail(msg, MHC_ERR_UNSUPPORTED, "num_experts > %d", MOE_EXPERTS_MAX);
+    if (c.shared_experts < 0 || c.shared_experts > MOE_SHARED_MAX)
+      return fail(msg, MHC_ERR_INVALID_ARG, "shared_experts must be in [0, %d]", MOE_SHARED_MAX);
+    if (c.top_k < 1 || c.top_k > MOE_TOPK_MAX || c.top_k > c.num_experts)
+      return fail(msg, MHC_ERR_INVALID_ARG, "top_k must be in [1, %d] and at most num_experts", MOE_TOPK_MAX);
+    if (c.max_moe_tokens < 1 || c.max_moe_tokens > MOE_TOKENS_MAX)
+      return fail(msg, MHC_ERR_INVALID_ARG, "max_moe_tokens must be in [1, %d]", MOE_TOKENS_MAX);
+    if (c.score != MHC_SCORE_SOFTMAX && c.score != MHC_SCORE_SIGMOID)
+      return fail(msg, MHC_ERR_INVALID_ARG, "unknown score %d", c.score);
+  }
   int count = 0;
   if (cudaGetDeviceCount(&count) != cudaSuccess || device < 0 || device >= count)
     return fail(msg, MHC_ERR_CUDA, "device %d is not available", device);
@@ -148,6 +201,14 @@ mhc_status_t mhc_sublayer_create(const mhc_sublayer_config_t *config, int device
   if (e == cudaSuccess) e = cudaMalloc(&s->scratch, s->scratch_floats * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&s->counters, size_t(s->sm_count) * sizeof(unsigned int));
   if (e == cudaSuccess) e = cudaMemset(s->counters, 0, size_t(s->sm_count) * sizeof(unsigned int));
+  if (e == cudaSuccess && c.num_experts > 0) {
+    e = moe_set_attributes();
+    if (e == cudaSuccess) e = cudaMalloc(&s->moe_base, moe_layout(s));
+    if (e == cudaSuccess) {
+      moe_layout(s);
+      e = cudaMemset(s->moe_base, 0, s->moe_counter_bytes);
+    }
+  }
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     const mhc_status_t st = e == cudaErrorMemoryAllocation ? MHC_ERR_OOM : MHC_ERR_CUDA;
@@ -252,9 +313,49 @@ mhc_status_t mhc_sublayer_matmul(mhc_sublayer_t *s, const mhc_sublayer_matmul_ar
 
 mhc_status_t mhc_sublayer_moe(mhc_sublayer_t *s, const mhc_sublayer_moe_args_t *a, mhc_stream_t stream) {
   if (!s) return MHC_ERR_INVALID_ARG;
-  (void)a;
-  (void)stream;
-  return fail(s->last_error, MHC_ERR_UNSUPPORTED, "created without experts");
+  std::string &msg = s->last_error;
+  const mhc_sublayer_config_t &c = s->cfg;
+  if (c.num_experts == 0) return fail(msg, MHC_ERR_UNSUPPORTED, "created without experts");
+  if (!a) return fail(msg, MHC_ERR_INVALID_ARG, "args is NULL");
+  if (a->m < 1 || a->m > c.max_moe_tokens)
+    return fail(msg, MHC_ERR_CAPACITY, "M=%d is outside [1, %d]", a->m, c.max_moe_tokens);
+  const bool fp8 = (c.flags & MHC_SUBLAYER_FP8) != 0;
+  if (!fp8 && (a->gate_up_scales || a->down_scales))
+    return fail(msg, MHC_ERR_INVALID_ARG, "BF16 weights have no scales");
+  const Tensor tensors[] = {{"x", a->x, 16, true}, {"router", a->router, 16, true}, {"bias", a->bias, 4, false},
+                            {"gate_up", a->gate_up, 16, true}, {"gate_up_scales", a->gate_up_scales, 4, fp8},
+                            {"down", a->down, 16, true}, {"down_scales", a->down_scales, 4, fp8},
+                            {"output", a->output, 2, true}, {"idx", a->idx, 4, false},
+                            {"weights", a->weights, 4, false}};
+  const mhc_status_t st = check_tensors(msg, tensors);
+  if (st != MHC_OK) return st;
+  DeviceGuard guard(s->device);
+  MoeParams p = {};
+  p.m = a->m;
+  p.hidden = c.hidden;
+  p.intermediate = c.intermediate;
+  p.experts = c.num_experts;
+  p.shared = c.shared_experts;
+  p.top_k = c.top_k;
+  p.fp8 = fp8;
+  p.sigmoid = c.score == MHC_SCORE_SIGMOID;
+  p.renormalize = (c.flags & MHC_SUBLAYER_RENORMALIZE) != 0;
+  p.router_f32 = (c.flags & MHC_SUBLAYER_ROUTER_F32) != 0;
+  p.routed_scale = c.routed_scale;
+  p.x = static_cast<const uint16_t *>(a->x);
+  p.router = a->router;
+  p.bias = a->bias;
+  p.gate_up = a->gate_up;
+  p.down = a->down;
+  p.gate_up_scales = a->gate_up_scales;
+  p.down_scales = a->down_scales;
+  p.output = static_cast<uint16_t *>(a->output);
+  p.idx = a->idx;
+  p.weights = a->weights;
+  p.slots = s->moe_slots;
+  p.scratch = s->moe;
+  p.err = s->err;
+  return launched(s, launch_moe(p, s->sm_count, reinterpret_cast<cudaStream_t>(stream)), "moe");
 }
 
 mhc_status_t mhc_sublayer_check_errors(mhc_sublayer_t *s) {
@@ -267,6 +368,7 @@ mhc_status_t mhc_sublayer_check_errors(mhc_sublayer_t *s) {
     // a call that gave up leaves its arrival counters half way
     e = cudaMemset(s->err, 0, sizeof flag);
     if (e == cudaSuccess) e = cudaMemset(s->counters, 0, size_t(s->sm_count) * sizeof(unsigned int));
+    if (e == cudaSuccess && s->moe_base) e = cudaMemset(s->moe_base, 0, s->moe_counter_bytes);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
   }
   if (e != cudaSuccess) return fail(s->last_error, MHC_ERR_CUDA, "check_errors: %s", cudaGetErrorString(e));
@@ -293,5 +395,7 @@ const char *mhc_sublayer_last_error(const mhc_sublayer_t *s) {
 }  // extern "C"
 
 mhc_status_t mhc_test_stall_sublayer_copies(int32_t on) {
-  return matmul_stall_copies(on ? 1 : 0) == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
+  cudaError_t e = matmul_stall_copies(on ? 1 : 0);
+  if (e == cudaSuccess) e = moe_stall_copies(on ? 1 : 0);
+  return e == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
 }

@@ -130,19 +130,20 @@ k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
         __syncwarp();
       }
     }
-    if (*abort) {
-      if (tc::elect_one()) tc::mma_commit(&c.drain);
-      __syncwarp();
-      tc::mbar_wait_bounded(&c.drain, 0u, tc::SUB_WAIT_LIMIT);
-    }
+    // no MMA is in flight when the tensor memory goes
+    if (tc::elect_one()) tc::mma_commit(&c.drain);
+    __syncwarp();
+    tc::mbar_wait_bounded(&c.drain, 0u, tc::SUB_WAIT_LIMIT);
   } else if (warp >= EPI_WARP0) {
     // ---------------------------------------------------------- epilogue
+    // After a wait gave up these warps go through the rest of their loops on
+    // whatever is there (the waits return at once), so that they meet at their
+    // barriers and every arrival is counted.
     const int sub = warp % 4, group = (warp - EPI_WARP0) / 4;
     const uint32_t lane_base = tmem + (uint32_t(sub * 32) << 16) + uint32_t(group * NC);
     const int epi_tid = threadIdx.x - EPI_WARP0 * 32;
     int n = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
       const WorkItem w = work_item(p, item);
       const int row = w.m0 + sub * 32 + lane;
       const int n0 = w.n_tile * BN + group * NC;
@@ -160,10 +161,8 @@ k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
           a_next = __ldg(sa + kb + 1);
           w_next = __ldg(sw + kb + 1);
         }
-        if (!tc::wait_or_abort(&c.acc_full[b], uint32_t((n / BUFS) & 1), abort)) {
-          ok = false;
-          break;
-        }
+        tc::wait_or_abort(&c.acc_full[b], uint32_t((n / BUFS) & 1), abort);
+        __syncwarp();
         tc::fence_after_sync();
         if (rows_live) {
           const uint64_t s2 = tc::pair(scale, scale);
@@ -189,7 +188,6 @@ k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
           tc::mbar_arrive(&c.acc_empty[b]);
         }
       }
-      if (!ok) break;
       bool finish = true;
       if (p.splits > 1) {
         // fragment [column][row], rows padded to a_rows: neighbouring lanes

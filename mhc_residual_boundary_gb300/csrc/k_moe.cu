@@ -1,0 +1,839 @@
+// k_moe.cu -- a whole mixture-of-experts layer for up to 32 tokens in one
+// kernel:
+//   route      logits = x router^T, scores, the top_k experts of each token
+//   up         g = x gate^T, u = x up^T of every reached expert, h = silu(g) u
+//   down       y = sum over a token's experts of weight * (h down^T)
+//
+// What bounds it is the read of the reached experts' weights, 3 I H values
+// each.  So the weights are the row operand of the tensor cores (tiles of 128
+// rows x 128 bytes, moved by TMA straight to where tcgen05.mma reads them) and
+// the few tokens are the columns; nothing but the tokens' columns passes
+// through registers.
+//
+// 8-bit weights against BF16 activations: the tensor core multiplies E4M3 by
+// E4M3, so an activation row is scaled by a power of two and split into E4M3
+// pieces, each holding four significant bits of what the ones before leave
+// (16 times larger than it stands for): two pieces hold a BF16 value (8 bits)
+// exactly down to 2^-13 of the row's largest and to 2^-22 of it below, three
+// hold the FP32 activation h to 12 bits.  The pieces are neighbouring
+// columns, and their products are added with factors 1, 1/16, 1/256.  The
+// weight's block scale multiplies each block of 128's sum in FP32.  BF16
+// weights take x as it is and h as two BF16 pieces (16 bits).
+//
+// One persistent CTA per SM, launched cooperatively (the CTAs wait for one
+// another twice, after `route` and between `up` and `down`).  The k blocks
+// of all tiles of a phase form one sequence that is cut into equal runs, one
+// for each CTA, so the read is balanced whatever the number of reached
+// experts.  A run's partial sums of a tile go to scratch; the last run to
+// arrive at a tile adds them in the order of the runs, so the result does not
+// depend on timing.  The producer of the weight tiles does not take part in the
+// waits after `route`: it fills the stage ring with the first `down` tiles while
+// the `up` sums are still being joined.
+//
+// Warps: 0 weight tiles, 1 MMA, 2 TMEM, 3 activation tiles, 4-7 sums.
+#include <algorithm>
+
+#include "sublayer.cuh"
+#include "sublayer_tc.cuh"
+
+namespace mhc {
+namespace {
+
+constexpr int NT = 256;
+constexpr int EPI_WARP0 = 4, EPI_THREADS = 128;
+constexpr int STAGES_MAX = 12;
+constexpr int BUFS = 4, BUF_COLS = 128;
+constexpr int A_BYTES = 128 * 128;
+constexpr int SMEM_BYTES = 227 * 1024;
+constexpr int EXPERTS = MOE_EXPERTS_MAX + MOE_SHARED_MAX;
+constexpr int SLOTS = MOE_TOKENS_MAX * (MOE_TOPK_MAX + MOE_SHARED_MAX);
+constexpr uint32_t POLL_LIMIT = 1u << 22;
+
+__device__ int g_stall_copies;   // test hook: the producers issue no copies
+
+struct Shared {
+  uint64_t full[STAGES_MAX], empty[STAGES_MAX], acc_full[BUFS], acc_empty[BUFS], drain;
+  uint32_t tmem;
+  int abort, last, active, issued_a, issued_b;
+  float red[8][8];
+  uint32_t red_max[4][4];
+  uint32_t mask[EXPERTS];       // tokens of an expert, one bit each
+  uint32_t act_mask[EXPERTS];   // the same of the reached experts, in order
+  uint16_t act_expert[EXPERTS], act_base[EXPERTS], position[EXPERTS];
+  float slot_weight[SLOTS];
+  int16_t chosen[MOE_TOKENS_MAX][MOE_TOPK_MAX];
+  float chosen_weight[MOE_TOKENS_MAX][MOE_TOPK_MAX];
+};
+constexpr int SMEM_TABLES = (int(sizeof(Shared)) + 1023) / 1024 * 1024;
+constexpr int SMEM_SLACK = 1024;   // an MMA's columns are rounded up to 16: it may read 8 rows past the last stage
+
+// ------------------------------------------------------------------ waits
+__device__ __forceinline__ unsigned ld_acquire(const unsigned *p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+// Until *p reaches `want`, another thread of the CTA gave up, or the limit.
+__device__ __noinline__ bool poll(const unsigned *p, unsigned want, volatile int *abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < POLL_LIMIT; ++i) {
+    if (ld_acquire(p) >= want) return true;
+    if (*abort) return false;
+    if (i > 256) __nanosleep(128);
+  }
+  *abort = 1;
+  return false;
+}
+// Orders generic-proxy accesses to global memory and the TMA's.
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// ------------------------------------------------------------- the sequence
+// A phase's k blocks, cut into `runs` equal runs (run c: [total c / runs,
+// total (c + 1) / runs)).
+struct Sequence {
+  int64_t total;
+  int runs;
+  __device__ int64_t begin(int c) const { return c >= runs ? total : total * c / runs; }
+  // the run that holds unit u
+  __device__ int run_of(int64_t u) const { return int(((u + 1) * runs - 1) / total); }
+  // runs that share units [u, u + n)
+  __device__ int pieces(int64_t u, int64_t n) const { return run_of(u + n - 1) - run_of(u) + 1; }
+};
+
+struct Shape {
+  int up_tiles, up_k;       // up: tiles of 128 rows of an expert's gate (and of its up) and their k blocks
+  int down_tiles, down_k;   // down: row blocks of the output, k blocks of an expert
+};
+
+template <bool FP8>
+__device__ __forceinline__ Shape shape_of(const MoeParams &p) {
+  constexpr int KB = FP8 ? 128 : 64;
+  return {(p.intermediate + 127) / 128, (p.hidden + KB - 1) / KB, (p.hidden + 127) / 128,
+          (p.intermediate + KB - 1) / KB};
+}
+// up: units (expert, tile, gate / up, k); runs of at least half a tile's k
+// blocks, so that at most MOE_UP_FRAGMENTS share a tile
+__device__ __forceinline__ Sequence up_sequence(const Shape &s, int active) {
+  Sequence q;
+  q.total = int64_t(active) * s.up_tiles * 2 * s.up_k;
+  q.runs = int(min(int64_t(gridDim.x), max(int64_t(1), q.total / ((s.up_k + 1) / 2))));
+  return q;
+}
+// down: units (row block, expert, k); at most MOE_DOWN_SPLIT runs a row block
+__device__ __forceinline__ Sequence down_sequence(const Shape &s, int active) {
+  Sequence q;
+  q.total = int64_t(s.down_tiles) * active * s.down_k;
+  q.runs = int(min(min(int64_t(gridDim.x), int64_t(s.down_tiles) * MOE_DOWN_SPLIT), q.total));
+  return q;
+}
+
+// ----------------------------------------------------------------- pieces
+// Power of two that brings a largest magnitude (bit pattern) to [128, 256);
+// NaN where it is not finite, so that the row's outputs are.
+__device__ __forceinline__ float piece_scale(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fffffffu);
+  const int e = max(int(amax_bits >> 23), 27);   // magnitudes under 2^-100 count as 2^-100
+  return __uint_as_float(uint32_t(e - 7) << 23);
+}
+// 1 / piece_scale (exact; 0 for the NaN scale)
+__device__ __forceinline__ float piece_inverse(float scale) {
+  const uint32_t e = __float_as_uint(scale) >> 23;
+  return e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
+}
+__device__ __forceinline__ uint32_t to_e4m3(float v) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(v));
+  return r & 0xffu;
+}
+__device__ __forceinline__ float from_e4m3(uint32_t b) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)b));
+  float f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h));
+  return f;
+}
+
+// ------------------------------------------------------------------ route
+// Logits of all tokens for this CTA's experts: eight tokens at a time, the
+// hidden size spread over all threads.
+__device__ __forceinline__ void route_logits(const MoeParams &p, Shared &sh) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int frags = p.hidden / 8;
+  for (int e = blockIdx.x; e < p.experts; e += gridDim.x)
+    for (int t0 = 0; t0 < p.m; t0 += 8) {
+      float acc[8] = {};
+      for (int f = threadIdx.x; f < frags; f += NT) {
+        float w[8];
+        const size_t at = size_t(e) * p.hidden + size_t(f) * 8;
+        if (p.router_f32) {
+          const float *r = static_cast<const float *>(p.router) + at;
+          const float4 a = __ldg(reinterpret_cast<const float4 *>(r)), b = __ldg(reinterpret_cast<const float4 *>(r) + 1);
+          w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+          w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+        } else {
+          unpack8(ld_ro(static_cast<const uint16_t *>(p.router) + at), w);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          if (t0 + t < p.m) {
+            float x[8];
+            unpack8(ld_ro(p.x + size_t(t0 + t) * p.hidden + size_t(f) * 8), x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[t] = fmaf(x[k], w[k], acc[t]);
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) acc[t] = warp_sum(acc[t]);
+      __syncthreads();
+      if (lane == 0)
+#pragma unroll
+        for (int t = 0; t < 8; ++t) sh.red[warp][t] = acc[t];
+      __syncthreads();
+      if (threadIdx.x < 8 && t0 + int(threadIdx.x) < p.m) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) s += sh.red[w][threadIdx.x];
+        p.scratch.logits[size_t(t0 + threadIdx.x) * p.experts + e] = s;
+      }
+    }
+}
+
+// The E4M3 pieces of x: a row a CTA, from the last CTA down (the first ones
+// have experts' logits to compute).
+__device__ __forceinline__ void split_x(const MoeParams &p, Shared &sh) {
+  const int frags = p.hidden / 8;
+  for (int t = int(gridDim.x) - 1 - int(blockIdx.x); t < p.m; t += gridDim.x) {
+    const uint16_t *x = p.x + size_t(t) * p.hidden;
+    uint32_t a = 0;
+    for (int f = threadIdx.x; f < frags; f += NT) {
+      const uint4 v = ld_ro(x + size_t(f) * 8);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a = max(a, max((w[k] << 16) & 0x7fff0000u, w[k] & 0x7fff0000u));
+    }
+    a = __reduce_max_sync(0xffffffffu, a);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) sh.red_max[threadIdx.x / 128][threadIdx.x / 32 % 4] = a;
+    __syncthreads();
+    a = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a = max(a, sh.red_max[k / 4][k % 4]);
+    const float scale = piece_scale(a), inv = piece_inverse(scale);
+    uint8_t *hi = p.scratch.x_pieces + size_t(2 * t) * p.hidden, *lo = hi + p.hidden;
+    for (int f = threadIdx.x; f < frags; f += NT) {
+      float v[8];
+      unpack8(ld_ro(x + size_t(f) * 8), v);
+      uint2 h, l;
+      uint32_t hb[8], lb[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] *= inv;
+        hb[k] = to_e4m3(v[k]);
+        lb[k] = to_e4m3((v[k] - from_e4m3(hb[k])) * 16.f);
+      }
+      h = make_uint2(hb[0] | hb[1] << 8 | hb[2] << 16 | hb[3] << 24, hb[4] | hb[5] << 8 | hb[6] << 16 | hb[7] << 24);
+      l = make_uint2(lb[0] | lb[1] << 8 | lb[2] << 16 | lb[3] << 24, lb[4] | lb[5] << 8 | lb[6] << 16 | lb[7] << 24);
+      *reinterpret_cast<uint2 *>(hi + size_t(f) * 8) = h;
+      *reinterpret_cast<uint2 *>(lo + size_t(f) * 8) = l;
+    }
+    if (threadIdx.x == 0) p.scratch.x_scale[t] = scale;
+  }
+}
+
+// Order-preserving unsigned key of a score; a NaN is below every number.
+__device__ __forceinline__ uint32_t score_key(float v) {
+  const uint32_t b = __float_as_uint(v);
+  if ((b & 0x7fffffffu) > 0x7f800000u) return 0u;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// One warp chooses token t's experts from its logits: lane l holds experts
+// l, l + 32, ...
+__device__ __forceinline__ void choose(const MoeParams &p, Shared &sh, int t) {
+  constexpr int PER = MOE_EXPERTS_MAX / 32;
+  const int lane = threadIdx.x % 32;
+  float score[PER];
+  uint32_t key[PER];
+  float peak = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * 32 + lane;
+    score[i] = e < p.experts ? __ldcg(p.scratch.logits + size_t(t) * p.experts + e) : -INFINITY;
+    peak = fmaxf(peak, score[i]);
+  }
+  if (!p.sigmoid) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      score[i] = i * 32 + lane < p.experts ? expf(score[i] - peak) : 0.f;
+      sum += score[i];
+    }
+    sum = warp_sum(sum);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) score[i] = score[i] / sum;
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) score[i] = 1.f / (1.f + expf(-score[i]));
+  }
+  uint32_t taken = 0;   // bit i: expert i * 32 + lane is chosen or does not exist
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * 32 + lane;
+    if (e >= p.experts) taken |= 1u << i;
+    key[i] = e < p.experts ? score_key(p.bias ? score[i] + __ldg(p.bias + e) : score[i]) : 0u;
+  }
+  float total = 0.f, mine = 0.f;
+  int mine_e = 0;
+  for (int k = 0; k < p.top_k; ++k) {
+    uint32_t best = 0, at = 0xffffffffu;
+    float value = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (!(taken >> i & 1u) && (at == 0xffffffffu || key[i] > best)) {
+        best = key[i];
+        at = uint32_t(i * 32 + lane);
+        value = score[i];
+      }
+    // the largest key, then the lowest expert among the lanes that hold it
+    const bool any = at != 0xffffffffu;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, any ? best : 0u);
+    const uint32_t winner = __reduce_min_sync(0xffffffffu, any && best == top ? at : 0xffffffffu);
+    const float w = __shfl_sync(0xffffffffu, value, int(winner % 32));
+    if (at == winner) taken |= 1u << (winner / 32);
+    total += w;
+    if (lane == k) {
+      mine = w;
+      mine_e = int(winner);
+    }
+  }
+  if (lane < p.top_k) {
+    const float w = (p.renormalize ? mine / total : mine) * p.routed_scale;
+    sh.chosen[t][lane] = int16_t(mine_e);
+    sh.chosen_weight[t][lane] = w;
+    atomicOr(&sh.mask[mine_e], 1u << t);
+    if (blockIdx.x == 0) {
+      if (p.idx) p.idx[t * p.top_k + lane] = mine_e;
+      if (p.weights) p.weights[t * p.top_k + lane] = w;
+    }
+  }
+}
+
+// The reached experts in order, each one's tokens and first slot (a slot is a
+// token of an expert), and the slots' weights.  Every CTA computes the same.
+__device__ __forceinline__ void build_plan(const MoeParams &p, Shared &sh) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int every = p.experts + p.shared;
+  const uint32_t all = p.m == 32 ? 0xffffffffu : (1u << p.m) - 1u;
+  for (int e = threadIdx.x; e < every; e += NT) sh.mask[e] = e < p.experts ? 0u : all;
+  __syncthreads();
+  for (int t = warp; t < p.m; t += NT / 32) choose(p, sh, t);
+  __syncthreads();
+  if (warp == 0) {
+    int active = 0, slots = 0;
+    for (int e0 = 0; e0 < every; e0 += 32) {
+      const uint32_t mask = e0 + lane < every ? sh.mask[e0 + lane] : 0u;
+      const uint32_t reached = __ballot_sync(0xffffffffu, mask != 0u);
+      const int n = __popc(mask);
+      int upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      if (mask) {
+        const int a = active + __popc(reached & ((1u << lane) - 1u));
+        sh.act_mask[a] = mask;
+        sh.act_expert[a] = uint16_t(e0 + lane);
+        sh.act_base[a] = uint16_t(slots + upto - n);
+        sh.position[e0 + lane] = uint16_t(a);
+      }
+      active += __popc(reached);
+      slots += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) sh.active = active;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.m * (p.top_k + p.shared); i += NT) {
+    const int t = i / (p.top_k + p.shared), k = i % (p.top_k + p.shared);
+    const int a = sh.position[k < p.top_k ? sh.chosen[t][k] : p.experts + k - p.top_k];
+    const int slot = sh.act_base[a] + __popc(sh.act_mask[a] & ((1u << t) - 1u));
+    sh.slot_weight[slot] = k < p.top_k ? sh.chosen_weight[t][k] : 1.f;
+  }
+  __syncthreads();
+}
+
+// --------------------------------------------------------------- sums, up
+// COLS columns of this thread's TMEM lane.
+template <int COLS>
+__device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&d)[COLS]) {
+  static_assert(COLS % 16 == 0, "16 columns a load");
+#pragma unroll
+  for (int c = 0; c < COLS; c += 16) tc::tmem_ld16_async(taddr + c, reinterpret_cast<uint32_t(&)[16]>(d[c]));
+  tc::tmem_wait_ld();
+  tc::tmem_hold(d);
+}
+
+__device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits); }
+
+// Joins a finished tile of an expert: h of its tokens from the runs' sums,
+// then h's pieces for the down product.
+template <bool FP8>
+__device__ __forceinline__ void finish_up(const MoeParams &p, Shared &sh, const Shape &s, const Sequence &q, int a,
+                                          int j) {
+  const int i = threadIdx.x - EPI_WARP0 * 32;   // row of the tile
+  const int warp = i / 32, lane = i % 32;
+  const int row = j * 128 + i;
+  const size_t width = size_t(s.up_tiles) * 128;
+  const int64_t u0 = (int64_t(a) * s.up_tiles + j) * 2 * s.up_k;
+  const int gate_pieces = q.pieces(u0, s.up_k), up_pieces = q.pieces(u0 + s.up_k, s.up_k);
+  const int n = __popc(sh.act_mask[a]), base = sh.act_base[a];
+  for (int k0 = 0; k0 < n; k0 += 4) {
+    float h[4];
+    uint32_t top[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float g = 0.f, u = 0.f;
+      if (k0 + k < n) {
+        const float *src = p.scratch.up + size_t(base + k0 + k) * 2 * width + row;
+        const size_t step = size_t(p.slots) * 2 * width;
+        for (int f = 0; f < gate_pieces; ++f) g += __ldcg(src + f * step);
+        for (int f = 0; f < up_pieces; ++f) u += __ldcg(src + f * step + width);
+      }
+      h[k] = row < p.intermediate ? g / (1.f + expf(-g)) * u : 0.f;
+    }
+    if (FP8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        top[k] = __reduce_max_sync(0xffffffffu, __float_as_uint(h[k]) & 0x7fffffffu);
+        if (lane == 0) sh.red_max[k][warp] = top[k];
+      }
+      tc::named_barrier(1, EPI_THREADS);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        top[k] = max(max(sh.red_max[k][0], sh.red_max[k][1]), max(sh.red_max[k][2], sh.red_max[k][3]));
+      tc::named_barrier(1, EPI_THREADS);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k0 + k >= n) break;
+      const int slot = base + k0 + k;
+      if (FP8) {
+        const float scale = piece_scale(top[k]);
+        float r = h[k] * piece_inverse(scale);
+        uint8_t *dst = static_cast<uint8_t *>(p.scratch.act) + size_t(slot) * 3 * p.intermediate + row;
+        if (i == 0) p.scratch.act_scale[size_t(j) * p.slots + slot] = scale;
+        if (row < p.intermediate)
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const uint32_t b = to_e4m3(r);
+            dst[size_t(c) * p.intermediate] = uint8_t(b);
+            r = (r - from_e4m3(b)) * 16.f;
+          }
+      } else if (row < p.intermediate) {
+        uint16_t *dst = static_cast<uint16_t *>(p.scratch.act) + size_t(slot) * 2 * p.intermediate + row;
+        const uint16_t hi = uint16_t(pack_bf16x2(h[k], 0.f));
+        dst[0] = hi;
+        dst[p.intermediate] = uint16_t(pack_bf16x2(h[k] - bf16_lo(hi), 0.f));
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- kernel
+template <bool FP8, int TM>
+__global__ void __launch_bounds__(NT, 1)
+k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const __grid_constant__ CUtensorMap tm_down,
+      const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_act) {
+  constexpr int KB = FP8 ? 128 : 64;                        // values of a 128-byte k block
+  constexpr int XP = FP8 ? 2 : 1, HP = FP8 ? 3 : 2;         // pieces of x and of h
+  constexpr int UP_COLS = (TM * XP + 15) / 16 * 16, DOWN_COLS = (TM * HP + 15) / 16 * 16;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Shared &sh = *reinterpret_cast<Shared *>(smem);
+  float *y_acc = reinterpret_cast<float *>(smem + SMEM_TABLES);   // [m][128]
+  unsigned char *ring = smem + SMEM_TABLES + (p.m * 512 + 1023) / 1024 * 1024;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile int *abort = &sh.abort;
+  const int stage_bytes = A_BYTES + p.b_bytes;
+  unsigned *routed = p.scratch.control, *ups_done = routed + 1, *exits = routed + 2;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      tc::mbar_init(&sh.full[i], 2);
+      tc::mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < BUFS; ++i) {
+      tc::mbar_init(&sh.acc_full[i], 1);
+      tc::mbar_init(&sh.acc_empty[i], EPI_THREADS / 32);
+    }
+    tc::mbar_init(&sh.drain, 1);
+    tc::mbar_init_fence();
+    sh.abort = 0;
+    sh.issued_a = sh.issued_b = 0;
+    tc::tma_prefetch_desc(&tm_gate_up);
+    tc::tma_prefetch_desc(&tm_down);
+    tc::tma_prefetch_desc(&tm_x);
+    tc::tma_prefetch_desc(&tm_act);
+  }
+  if (warp == 2) tc::tmem_alloc(&sh.tmem, BUFS * BUF_COLS);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+
+  // ---- route
+  route_logits(p, sh);
+  if (FP8) split_x(p, sh);
+  fence_proxy_async_global();
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    atomicAdd(routed, 1u);
+    poll(routed, gridDim.x, abort);
+  }
+  __syncthreads();
+  const bool gave_up = *abort != 0;   // the same in all threads: no role has begun
+  build_plan(p, sh);
+
+  const Shape s = shape_of<FP8>(p);
+  const Sequence up = up_sequence(s, sh.active), down = down_sequence(s, sh.active);
+  const int cta = blockIdx.x;
+  const int64_t up0 = up.begin(cta), up1 = up.begin(cta + 1), down0 = down.begin(cta), down1 = down.begin(cta + 1);
+  const int up_n = int(up1 - up0), n_all = up_n + int(down1 - down0);
+  const unsigned up_total = unsigned(sh.active) * unsigned(s.up_tiles);
+
+  if (gave_up) {
+    // the logits never came: no role begins
+  } else if (warp == 0) {
+    // ----------------------------------------------------- weight tiles
+    bool ok = !g_stall_copies;
+    int n = 0;
+    for (; n < n_all && ok; ++n) {
+      const int st = n % p.stages;
+      if (n >= p.stages && !tc::wait_or_abort(&sh.empty[st], uint32_t((n / p.stages - 1) & 1), abort)) break;
+      const void *map;
+      int kb, row;
+      if (n < up_n) {
+        const int64_t u = up0 + n;
+        const int64_t tile = u / s.up_k;                    // (expert, tile, gate / up)
+        const int a = int(tile / (2 * s.up_tiles)), r = int(tile % (2 * s.up_tiles));
+        kb = int(u % s.up_k);
+        row = sh.act_expert[a] * 2 * p.intermediate + (r & 1) * p.intermediate + (r >> 1) * 128;
+        map = &tm_gate_up;
+      } else {
+        const int64_t u = down0 + (n - up_n);
+        const int64_t tile = u / s.down_k;                  // (row block, expert)
+        const int a = int(tile % sh.active);
+        kb = int(u % s.down_k);
+        row = sh.act_expert[a] * p.hidden + int(tile / sh.active) * 128;
+        map = &tm_down;
+      }
+      if (tc::elect_one()) {
+        tc::mbar_arrive_expect_tx(&sh.full[st], A_BYTES);
+        tc::tma_load_2d(ring + size_t(st) * stage_bytes, map, kb * KB, row, &sh.full[st]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) sh.issued_a = n;
+  } else if (warp == 3) {
+    // ------------------------------------------------- activation tiles
+    bool ok = !g_stall_copies;
+    int n = 0;
+    const int x_rows = (p.m * XP + 7) / 8 * 8;
+    fence_proxy_async_global();
+    for (; n < n_all && ok; ++n) {
+      const int st = n % p.stages;
+      if (n >= p.stages && !tc::wait_or_abort(&sh.empty[st], uint32_t((n / p.stages - 1) & 1), abort)) break;
+      unsigned char *dst = ring + size_t(st) * stage_bytes + A_BYTES;
+      if (n < up_n) {
+        const int kb = int((up0 + n) % s.up_k);
+        if (tc::elect_one()) {
+          tc::mbar_arrive_expect_tx(&sh.full[st], uint32_t(x_rows) * 128);
+          tc::tma_load_2d(dst, &tm_x, kb * KB, 0, &sh.full[st]);
+        }
+      } else {
+        if (n == up_n) {
+          ok = poll(ups_done, up_total, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          fence_proxy_async_global();
+        }
+        const int64_t u = down0 + (n - up_n);
+        const int a = int(u / s.down_k % sh.active), kb = int(u % s.down_k);
+        const int boxes = (__popc(sh.act_mask[a]) * HP + 7) / 8, row = sh.act_base[a] * HP;
+        if (tc::elect_one()) {
+          tc::mbar_arrive_expect_tx(&sh.full[st], uint32_t(boxes) * 1024);
+          for (int i = 0; i < boxes; ++i)
+            tc::tma_load_2d(dst + i * 1024, &tm_act, kb * KB, row + i * 8, &sh.full[st]);
+        }
+      }
+      __syncwarp();
+    }
+    if (lane == 0) sh.issued_b = n;
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMA
+    for (int n = 0; n < n_all; ++n) {
+      const int st = n % p.stages, b = n % BUFS;
+      if (!tc::wait_or_abort(&sh.full[st], uint32_t((n / p.stages) & 1), abort)) break;
+      if (n >= BUFS && !tc::wait_or_abort(&sh.acc_empty[b], uint32_t((n / BUFS - 1) & 1), abort)) break;
+      tc::fence_after_sync();
+      int cols = p.m * XP;
+      if (n >= up_n) cols = __popc(sh.act_mask[int((down0 + (n - up_n)) / s.down_k % sh.active)]) * HP;
+      cols = (cols + 15) / 16 * 16;
+      const uint32_t idesc = FP8 ? tc::idesc_e4m3_f32(128, cols) : tc::idesc_bf16_f32(128, cols);
+      const unsigned char *src = ring + size_t(st) * stage_bytes;
+      const uint64_t ad = tc::desc_sw128(src), bd = tc::desc_sw128(src + A_BYTES);
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          if (FP8) tc::mma_e4m3(tmem + uint32_t(b * BUF_COLS), ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+          else tc::mma_bf16(tmem + uint32_t(b * BUF_COLS), ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+        }
+        tc::mma_commit(&sh.empty[st]);
+        tc::mma_commit(&sh.acc_full[b]);
+      }
+      __syncwarp();
+    }
+    // no MMA is in flight when the tensor memory goes
+    if (tc::elect_one()) tc::mma_commit(&sh.drain);
+    __syncwarp();
+    tc::mbar_wait_bounded(&sh.drain, 0u, tc::SUB_WAIT_LIMIT);
+  } else if (warp >= EPI_WARP0) {
+    // ------------------------------------------------------------- sums
+    const int i = threadIdx.x - EPI_WARP0 * 32;   // row of the tile
+    const uint32_t lane_base = tmem + (uint32_t((warp % 4) * 32) << 16);
+    const size_t width = size_t(s.up_tiles) * 128;
+    // After a wait gave up these warps go through the rest of their loops on
+    // whatever is there (the waits return at once), so that they meet at their
+    // barriers and every arrival is counted.
+    int n = 0;
+    // ---- up
+    while (n < up_n) {
+      const int64_t u = up0 + n, tile = u / s.up_k;
+      const int a = int(tile / (2 * s.up_tiles)), r = int(tile % (2 * s.up_tiles)), j = r >> 1;
+      const int kb0 = int(u % s.up_k), kb1 = min(s.up_k, kb0 + up_n - n);
+      const float *sw = p.gate_up_scales + ((size_t(sh.act_expert[a]) * 2 + (r & 1)) * s.up_tiles + j) * s.up_k;
+      float acc[TM];
+#pragma unroll
+      for (int t = 0; t < TM; ++t) acc[t] = 0.f;
+      float held = 0.f;   // lane l: the scale of k block (kb & ~31) + l
+      for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        const int b = n % BUFS;
+        if (FP8 && (kb == kb0 || kb % 32 == 0)) {
+          const int at = kb / 32 * 32 + lane;
+          held = at < s.up_k ? __ldg(sw + at) : 0.f;
+        }
+        const float scale = FP8 ? __shfl_sync(0xffffffffu, held, kb % 32) : 1.f;
+        tc::wait_or_abort(&sh.acc_full[b], uint32_t((n / BUFS) & 1), abort);
+        __syncwarp();
+        tc::fence_after_sync();
+        uint32_t d[UP_COLS];
+        load_cols(lane_base + uint32_t(b * BUF_COLS), d);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.acc_empty[b]);
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+          acc[t] = FP8 ? fmaf(fmaf(value(d[XP * t + XP - 1]), 0.0625f, value(d[XP * t])), scale, acc[t])
+                       : acc[t] + value(d[t]);
+      }
+      // this run's piece of the tile's sums
+      const uint32_t mask = sh.act_mask[a];
+      const int piece = cta - up.run_of(tile * s.up_k);
+      float *dst = p.scratch.up + (size_t(piece) * p.slots + sh.act_base[a]) * 2 * width + (r & 1) * width + j * 128 + i;
+      int slot = 0;
+#pragma unroll
+      for (int t = 0; t < TM; ++t)
+        if (mask >> t & 1u) {
+          __stcg(dst + size_t(slot) * 2 * width, FP8 ? acc[t] * __ldcg(p.scratch.x_scale + t) : acc[t]);
+          ++slot;
+        }
+      __threadfence();
+      tc::named_barrier(1, EPI_THREADS);
+      if (i == 0) {
+        const int64_t u0 = (int64_t(a) * s.up_tiles + j) * 2 * s.up_k;
+        const unsigned want = unsigned(up.pieces(u0, s.up_k) + up.pieces(u0 + s.up_k, s.up_k));
+        unsigned *counter = p.scratch.up_counters + a * s.up_tiles + j;
+        const bool last = atomicAdd(counter, 1u) == want - 1;
+        if (last) *counter = 0;
+        sh.last = last;
+      }
+      tc::named_barrier(1, EPI_THREADS);
+      const bool last = sh.last != 0;
+      tc::named_barrier(1, EPI_THREADS);   // sh.last may be written again
+      if (last) {
+        __threadfence();
+        finish_up<FP8>(p, sh, s, up, a, j);
+        fence_proxy_async_global();
+        __threadfence();
+        tc::named_barrier(1, EPI_THREADS);
+        if (i == 0) atomicAdd(ups_done, 1u);
+      }
+    }
+    // ---- down
+    if (n < n_all) poll(ups_done, up_total, abort);
+    __syncwarp();
+    while (n < n_all) {
+      const int64_t u0 = down0 + (n - up_n);
+      const int rb = int(u0 / s.down_k / sh.active);
+      const int64_t rb_u0 = int64_t(rb) * sh.active * s.down_k, rb_units = int64_t(sh.active) * s.down_k;
+      const int n1 = int(min(down1, rb_u0 + rb_units) - down0) + up_n;   // end of this row block's units here
+      for (int t = 0; t < p.m; ++t) y_acc[t * 128 + i] = 0.f;
+      while (n < n1) {
+        const int64_t u = down0 + (n - up_n);
+        const int a = int(u / s.down_k % sh.active);
+        const int kb0 = int(u % s.down_k), kb1 = min(s.down_k, kb0 + n1 - n);
+        const uint32_t mask = sh.act_mask[a];
+        const int count = __popc(mask), base = sh.act_base[a];
+        const float *sw = p.down_scales + (size_t(sh.act_expert[a]) * s.down_tiles + rb) * s.down_k;
+        float acc[TM];
+#pragma unroll
+        for (int t = 0; t < TM; ++t) acc[t] = 0.f;
+        float held = 0.f;
+        // lane l: the activation scale of the expert's token l, one block ahead
+        float h_next = FP8 && lane < count ? __ldcg(p.scratch.act_scale + size_t(kb0) * p.slots + base + lane) : 0.f;
+        for (int kb = kb0; kb < kb1; ++kb, ++n) {
+          const int b = n % BUFS;
+          if (FP8 && (kb == kb0 || kb % 32 == 0)) {
+            const int at = kb / 32 * 32 + lane;
+            held = at < s.down_k ? __ldg(sw + at) : 0.f;
+          }
+          const float h_scale = FP8 ? h_next * __shfl_sync(0xffffffffu, held, kb % 32) : 1.f;
+          if (FP8 && kb + 1 < kb1 && lane < count)
+            h_next = __ldcg(p.scratch.act_scale + size_t(kb + 1) * p.slots + base + lane);
+          tc::wait_or_abort(&sh.acc_full[b], uint32_t((n / BUFS) & 1), abort);
+          __syncwarp();
+          tc::fence_after_sync();
+          uint32_t d[DOWN_COLS];
+          load_cols(lane_base + uint32_t(b * BUF_COLS), d);
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sh.acc_empty[b]);
+#pragma unroll
+          for (int t = 0; t < TM; ++t)
+            if (t < count) {
+              if (FP8) {
+                const float v = fmaf(fmaf(value(d[HP * t + HP - 1]), 0.0625f, value(d[HP * t + 1])), 0.0625f,
+                                     value(d[HP * t]));
+                acc[t] = fmaf(v, __shfl_sync(0xffffffffu, h_scale, t), acc[t]);
+              } else {
+                acc[t] += value(d[HP * t]) + value(d[HP * t + 1]);
+              }
+            }
+        }
+        uint32_t rest = mask;
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+          if (t < count) {
+            const int token = __ffs(rest) - 1;
+            rest &= rest - 1u;
+            y_acc[token * 128 + i] = fmaf(acc[t], sh.slot_weight[base + t], y_acc[token * 128 + i]);
+          }
+      }
+      // this run's piece of the row block
+      const int pieces = down.pieces(rb_u0, rb_units);
+      const size_t step = size_t(s.down_tiles) * p.m * 128;
+      float *dst = p.scratch.down + size_t(rb) * p.m * 128 + i;
+      const int row = rb * 128 + i;
+      bool last = true;
+      if (pieces > 1) {
+        const int piece = cta - down.run_of(rb_u0);
+        for (int t = 0; t < p.m; ++t) __stcg(dst + piece * step + t * 128, y_acc[t * 128 + i]);
+        __threadfence();
+        tc::named_barrier(1, EPI_THREADS);
+        if (i == 0) {
+          unsigned *counter = p.scratch.down_counters + rb;
+          const bool is_last = atomicAdd(counter, 1u) == unsigned(pieces - 1);
+          if (is_last) *counter = 0;
+          sh.last = is_last;
+        }
+        tc::named_barrier(1, EPI_THREADS);
+        last = sh.last != 0;
+        tc::named_barrier(1, EPI_THREADS);
+        if (last) {
+          __threadfence();
+          for (int t = 0; t < p.m; ++t) {
+            float y = 0.f;
+            for (int f = 0; f < pieces; ++f) y += __ldcg(dst + f * step + t * 128);
+            y_acc[t * 128 + i] = y;
+          }
+        }
+      }
+      if (last && row < p.hidden)
+        for (int t = 0; t < p.m; ++t)
+          p.output[size_t(t) * p.hidden + row] = uint16_t(pack_bf16x2(y_acc[t * 128 + i], 0.f));
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 2) tc::tmem_dealloc(tmem, BUFS * BUF_COLS);
+  if (threadIdx.x == 0) {
+    if (*abort) {
+      atomicOr(p.err, 2u);
+      // copies in flight land before the CTA's shared memory goes: the stages
+      // that only one of the two producers filled lack one arrival
+      const int lo = min(sh.issued_a, sh.issued_b), hi = max(sh.issued_a, sh.issued_b);
+      for (int n = lo; n < hi; ++n) tc::mbar_arrive(&sh.full[n % p.stages]);
+      for (int n = max(0, hi - p.stages); n < hi; ++n)
+        tc::mbar_wait_bounded(&sh.full[n % p.stages], uint32_t((n / p.stages) & 1), tc::SUB_WAIT_LIMIT);
+    }
+    // the last CTA to leave puts the grid's counters back
+    if (atomicAdd(exits, 1u) == gridDim.x - 1) {
+      *routed = 0;
+      *ups_done = 0;
+      *exits = 0;
+    }
+  }
+}
+
+template <bool FP8, int TM>
+cudaError_t launch(const MoeParams &p, int sms, const CUtensorMap *maps, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_moe<FP8, TM>, p, maps[0], maps[1], maps[2], maps[3]);
+}
+
+}  // namespace
+
+cudaError_t moe_stall_copies(int on) { return cudaMemcpyToSymbol(g_stall_copies, &on, sizeof on); }
+
+cudaError_t moe_set_attributes() {
+  cudaError_t e = cudaSuccess;
+  for (const void *k : {(const void *)k_moe<false, 8>, (const void *)k_moe<false, 32>, (const void *)k_moe<true, 8>,
+                        (const void *)k_moe<true, 32>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  return e;
+}
+
+cudaError_t launch_moe(const MoeParams &args, int sms, cudaStream_t stream) {
+  MoeParams p = args;
+  const bool fp8 = p.fp8 != 0;
+  const int every = p.experts + p.shared, elem = fp8 ? 1 : 2, kb = fp8 ? 128 : 64;
+  const int xp = fp8 ? 2 : 1, hp = fp8 ? 3 : 2;
+  p.b_bytes = (p.m * std::max(xp, hp) + 7) / 8 * 1024;
+  p.stages = std::min(STAGES_MAX, (SMEM_BYTES - SMEM_TABLES - SMEM_SLACK - (p.m * 512 + 1023) / 1024 * 1024) /
+                                      (A_BYTES + p.b_bytes));
+  const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t H = p.hidden, I = p.intermediate;
+  const void *x = fp8 ? static_cast<const void *>(p.scratch.x_pieces) : p.x;
+  CUtensorMap maps[4];
+  if (!encode_rows_sw128(&maps[0], type, p.gate_up, uint64_t(every) * 2 * I, H, H * elem, kb, 128) ||
+      !encode_rows_sw128(&maps[1], type, p.down, uint64_t(every) * H, I, I * elem, kb, 128) ||
+      !encode_rows_sw128(&maps[2], type, x, uint64_t(p.m) * xp, H, H * elem, kb, (p.m * xp + 7) / 8 * 8) ||
+      !encode_rows_sw128(&maps[3], type, p.scratch.act, uint64_t(p.slots) * hp, I, I * elem, kb, 8))
+    return cudaErrorInvalidValue;
+  if (fp8) return p.m <= 8 ? launch<true, 8>(p, sms, maps, stream) : launch<true, 32>(p, sms, maps, stream);
+  return p.m <= 8 ? launch<false, 8>(p, sms, maps, stream) : launch<false, 32>(p, sms, maps, stream);
+}
+
+}  // namespace mhc

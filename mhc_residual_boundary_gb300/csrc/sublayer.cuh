@@ -72,6 +72,56 @@ cudaError_t matmul_set_attributes();
 cudaError_t matmul_stall_copies(int on);   // test hook, see include/mhc_boundary_test.h
 cudaError_t launch_block_matmul(const MatmulParams &p, int sms, cudaStream_t stream);
 
+// MoE layer of up to MOE_TOKENS_MAX tokens (k_moe.cu).
+constexpr int MOE_TOKENS_MAX = 32;
+constexpr int MOE_EXPERTS_MAX = 512;
+constexpr int MOE_SHARED_MAX = 8;
+constexpr int MOE_TOPK_MAX = 16;
+// Pieces of a row of sums that its work items leave in scratch: at most
+// MOE_UP_FRAGMENTS for a tile of the gate and up products, MOE_DOWN_FRAGMENTS
+// for a row block of the output.
+constexpr int MOE_UP_FRAGMENTS = 3;
+constexpr int MOE_DOWN_SPLIT = 8;
+constexpr int MOE_DOWN_FRAGMENTS = MOE_DOWN_SPLIT + 1;
+
+// Scratch of one MoE handle, by its capacity.
+struct MoeScratch {
+  unsigned int *control;      // MOE_CONTROL words: grid counters, zero between calls
+  unsigned int *up_counters;  // [active experts][I / 128]
+  unsigned int *down_counters;// [H / 128]
+  float *logits;              // [tokens][E]
+  uint8_t *x_pieces;          // [2 tokens][H] e4m3 (8-bit weights)
+  float *x_scale;             // [tokens]
+  float *up;                  // [MOE_UP_FRAGMENTS][slots][2][I rounded up to 128]
+  void *act;                  // [slots * pieces][I]: e4m3 x 3 or bf16 x 2
+  float *act_scale;           // [I / 128][slots] (8-bit weights)
+  float *down;                // [MOE_DOWN_FRAGMENTS][H / 128][tokens][128]
+};
+constexpr int MOE_CONTROL = 4;
+
+struct MoeParams {
+  int m, hidden, intermediate, experts, shared, top_k;
+  int fp8, sigmoid, renormalize, router_f32;
+  float routed_scale;
+  const uint16_t *x;
+  const void *router;
+  const float *bias;
+  const void *gate_up, *down;
+  const float *gate_up_scales, *down_scales;
+  uint16_t *output;
+  int32_t *idx;
+  float *weights;
+  int slots;                  // slots of the scratch tensors
+  MoeScratch scratch;
+  unsigned int *err;
+  // set by the launcher
+  int stages, b_bytes;
+};
+
+cudaError_t moe_set_attributes();
+cudaError_t moe_stall_copies(int on);   // test hook
+cudaError_t launch_moe(const MoeParams &p, int sms, cudaStream_t stream);
+
 cudaError_t launch_add_rms_norm(const NormParams &p, cudaStream_t stream);
 cudaError_t launch_quantize(const QuantParams &p, bool swiglu, int sms, cudaStream_t stream);
 
