@@ -127,6 +127,45 @@ __device__ __forceinline__ Sequence down_sequence(const Shape &s, int active) {
   return q;
 }
 
+// The position of a unit in its sequence: stepped, because a 64-bit division
+// for each k block would take longer than the block's read.
+struct UpCursor {     // (expert, gate / up tile, k)
+  int a, r, kb;
+  __device__ UpCursor(const Shape &s, int64_t u) {
+    const int64_t tile = u / s.up_k;
+    kb = int(u - tile * s.up_k);
+    a = int(tile / (2 * s.up_tiles));
+    r = int(tile - int64_t(a) * 2 * s.up_tiles);
+  }
+  __device__ void next(const Shape &s) {
+    if (++kb == s.up_k) {
+      kb = 0;
+      if (++r == 2 * s.up_tiles) {
+        r = 0;
+        ++a;
+      }
+    }
+  }
+};
+struct DownCursor {   // (row block, expert, k)
+  int rb, a, kb;
+  __device__ DownCursor(const Shape &s, int active, int64_t u) {
+    const int64_t tile = u / s.down_k;
+    kb = int(u - tile * s.down_k);
+    rb = int(tile / active);
+    a = int(tile - int64_t(rb) * active);
+  }
+  __device__ void next(const Shape &s, int active) {
+    if (++kb == s.down_k) {
+      kb = 0;
+      if (++a == active) {
+        a = 0;
+        ++rb;
+      }
+    }
+  }
+};
+
 // ----------------------------------------------------------------- pieces
 // Power of two that brings a largest magnitude (bit pattern) to [128, 256);
 // NaN where it is not finite, so that the row's outputs are.
@@ -497,11 +536,14 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   build_plan(p, sh);
 
   const Shape s = shape_of<FP8>(p);
-  const Sequence up = up_sequence(s, sh.active), down = down_sequence(s, sh.active);
+  const int active = sh.active;
+  const Sequence up = up_sequence(s, active), down = down_sequence(s, active);
   const int cta = blockIdx.x;
   const int64_t up0 = up.begin(cta), up1 = up.begin(cta + 1), down0 = down.begin(cta), down1 = down.begin(cta + 1);
   const int up_n = int(up1 - up0), n_all = up_n + int(down1 - down0);
-  const unsigned up_total = unsigned(sh.active) * unsigned(s.up_tiles);
+  UpCursor uc(s, up0);
+  DownCursor dc(s, active, down0);
+  const unsigned up_total = unsigned(active) * unsigned(s.up_tiles);
 
   if (gave_up) {
     // the logits never came: no role begins
@@ -515,19 +557,15 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       const void *map;
       int kb, row;
       if (n < up_n) {
-        const int64_t u = up0 + n;
-        const int64_t tile = u / s.up_k;                    // (expert, tile, gate / up)
-        const int a = int(tile / (2 * s.up_tiles)), r = int(tile % (2 * s.up_tiles));
-        kb = int(u % s.up_k);
-        row = sh.act_expert[a] * 2 * p.intermediate + (r & 1) * p.intermediate + (r >> 1) * 128;
+        kb = uc.kb;
+        row = sh.act_expert[uc.a] * 2 * p.intermediate + (uc.r & 1) * p.intermediate + (uc.r >> 1) * 128;
         map = &tm_gate_up;
+        uc.next(s);
       } else {
-        const int64_t u = down0 + (n - up_n);
-        const int64_t tile = u / s.down_k;                  // (row block, expert)
-        const int a = int(tile % sh.active);
-        kb = int(u % s.down_k);
-        row = sh.act_expert[a] * p.hidden + int(tile / sh.active) * 128;
+        kb = dc.kb;
+        row = sh.act_expert[dc.a] * p.hidden + dc.rb * 128;
         map = &tm_down;
+        dc.next(s, active);
       }
       if (tc::elect_one()) {
         tc::mbar_arrive_expect_tx(&sh.full[st], A_BYTES);
@@ -547,11 +585,11 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       if (n >= p.stages && !tc::wait_or_abort(&sh.empty[st], uint32_t((n / p.stages - 1) & 1), abort)) break;
       unsigned char *dst = ring + size_t(st) * stage_bytes + A_BYTES;
       if (n < up_n) {
-        const int kb = int((up0 + n) % s.up_k);
         if (tc::elect_one()) {
           tc::mbar_arrive_expect_tx(&sh.full[st], uint32_t(x_rows) * 128);
-          tc::tma_load_2d(dst, &tm_x, kb * KB, 0, &sh.full[st]);
+          tc::tma_load_2d(dst, &tm_x, uc.kb * KB, 0, &sh.full[st]);
         }
+        uc.next(s);
       } else {
         if (n == up_n) {
           ok = poll(ups_done, up_total, abort);
@@ -559,14 +597,13 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
           if (!ok) break;
           fence_proxy_async_global();
         }
-        const int64_t u = down0 + (n - up_n);
-        const int a = int(u / s.down_k % sh.active), kb = int(u % s.down_k);
-        const int boxes = (__popc(sh.act_mask[a]) * HP + 7) / 8, row = sh.act_base[a] * HP;
+        const int boxes = (__popc(sh.act_mask[dc.a]) * HP + 7) / 8, row = sh.act_base[dc.a] * HP;
         if (tc::elect_one()) {
           tc::mbar_arrive_expect_tx(&sh.full[st], uint32_t(boxes) * 1024);
           for (int i = 0; i < boxes; ++i)
-            tc::tma_load_2d(dst + i * 1024, &tm_act, kb * KB, row + i * 8, &sh.full[st]);
+            tc::tma_load_2d(dst + i * 1024, &tm_act, dc.kb * KB, row + i * 8, &sh.full[st]);
         }
+        dc.next(s, active);
       }
       __syncwarp();
     }
@@ -579,7 +616,10 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       if (n >= BUFS && !tc::wait_or_abort(&sh.acc_empty[b], uint32_t((n / BUFS - 1) & 1), abort)) break;
       tc::fence_after_sync();
       int cols = p.m * XP;
-      if (n >= up_n) cols = __popc(sh.act_mask[int((down0 + (n - up_n)) / s.down_k % sh.active)]) * HP;
+      if (n >= up_n) {
+        cols = __popc(sh.act_mask[dc.a]) * HP;
+        dc.next(s, active);
+      }
       cols = (cols + 15) / 16 * 16;
       const uint32_t idesc = FP8 ? tc::idesc_e4m3_f32(128, cols) : tc::idesc_bf16_f32(128, cols);
       const unsigned char *src = ring + size_t(st) * stage_bytes;
@@ -610,9 +650,9 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     int n = 0;
     // ---- up
     while (n < up_n) {
-      const int64_t u = up0 + n, tile = u / s.up_k;
-      const int a = int(tile / (2 * s.up_tiles)), r = int(tile % (2 * s.up_tiles)), j = r >> 1;
-      const int kb0 = int(u % s.up_k), kb1 = min(s.up_k, kb0 + up_n - n);
+      const UpCursor at(s, up0 + n);
+      const int a = at.a, r = at.r, j = r >> 1, kb0 = at.kb, kb1 = min(s.up_k, kb0 + up_n - n);
+      const int64_t tile = int64_t(a) * 2 * s.up_tiles + r;
       const float *sw = p.gate_up_scales + ((size_t(sh.act_expert[a]) * 2 + (r & 1)) * s.up_tiles + j) * s.up_k;
       float acc[TM];
 #pragma unroll
@@ -621,8 +661,8 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       for (int kb = kb0; kb < kb1; ++kb, ++n) {
         const int b = n % BUFS;
         if (FP8 && (kb == kb0 || kb % 32 == 0)) {
-          const int at = kb / 32 * 32 + lane;
-          held = at < s.up_k ? __ldg(sw + at) : 0.f;
+          const int k = kb / 32 * 32 + lane;
+          held = k < s.up_k ? __ldg(sw + k) : 0.f;
         }
         const float scale = FP8 ? __shfl_sync(0xffffffffu, held, kb % 32) : 1.f;
         tc::wait_or_abort(&sh.acc_full[b], uint32_t((n / BUFS) & 1), abort);
@@ -675,15 +715,12 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     if (n < n_all) poll(ups_done, up_total, abort);
     __syncwarp();
     while (n < n_all) {
-      const int64_t u0 = down0 + (n - up_n);
-      const int rb = int(u0 / s.down_k / sh.active);
-      const int64_t rb_u0 = int64_t(rb) * sh.active * s.down_k, rb_units = int64_t(sh.active) * s.down_k;
+      const int rb = dc.rb;
+      const int64_t rb_u0 = int64_t(rb) * active * s.down_k, rb_units = int64_t(active) * s.down_k;
       const int n1 = int(min(down1, rb_u0 + rb_units) - down0) + up_n;   // end of this row block's units here
       for (int t = 0; t < p.m; ++t) y_acc[t * 128 + i] = 0.f;
       while (n < n1) {
-        const int64_t u = down0 + (n - up_n);
-        const int a = int(u / s.down_k % sh.active);
-        const int kb0 = int(u % s.down_k), kb1 = min(s.down_k, kb0 + n1 - n);
+        const int a = dc.a, kb0 = dc.kb, kb1 = min(s.down_k, kb0 + n1 - n);
         const uint32_t mask = sh.act_mask[a];
         const int count = __popc(mask), base = sh.act_base[a];
         const float *sw = p.down_scales + (size_t(sh.act_expert[a]) * s.down_tiles + rb) * s.down_k;
@@ -696,8 +733,8 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
         for (int kb = kb0; kb < kb1; ++kb, ++n) {
           const int b = n % BUFS;
           if (FP8 && (kb == kb0 || kb % 32 == 0)) {
-            const int at = kb / 32 * 32 + lane;
-            held = at < s.down_k ? __ldg(sw + at) : 0.f;
+            const int k = kb / 32 * 32 + lane;
+            held = k < s.down_k ? __ldg(sw + k) : 0.f;
           }
           const float h_scale = FP8 ? h_next * __shfl_sync(0xffffffffu, held, kb % 32) : 1.f;
           if (FP8 && kb + 1 < kb1 && lane < count)
@@ -722,6 +759,8 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
               }
             }
         }
+        dc.kb = kb1 - 1;
+        dc.next(s, active);
         uint32_t rest = mask;
 #pragma unroll
         for (int t = 0; t < TM; ++t)
