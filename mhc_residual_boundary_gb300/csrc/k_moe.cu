@@ -28,10 +28,14 @@
 // arrive at a tile adds them in the order of the runs, so the result does not
 // depend on timing.  The producer of the weight tiles does not take part in the
 // waits after `route`: it fills the stage ring with the first `down` tiles while
-// the `up` sums are still being joined.
+// the `up` sums are still being joined; and the warps that join the pieces are
+// not those that take the sums out of the tensor memory, so neither does the
+// ring wait for a join.
 //
-// Warps: 0 weight tiles, 1 MMA, 2 TMEM, 3 activation tiles, 4-7 sums.
+// Warps: 0 weight tiles, 1 MMA, 2 TMEM, 3 activation tiles, 4-7 sums, 8-11
+// joins.
 #include <algorithm>
+#include <type_traits>
 
 #include "sublayer.cuh"
 #include "sublayer_tc.cuh"
@@ -39,8 +43,8 @@
 namespace mhc {
 namespace {
 
-constexpr int NT = 256;
-constexpr int EPI_WARP0 = 4, EPI_THREADS = 128;
+constexpr int NT = 384, WARPS = NT / 32;
+constexpr int SUM_WARP0 = 4, JOIN_WARP0 = 8;
 constexpr int STAGES_MAX = 12;
 constexpr int BUFS = 4, BUF_COLS = 128;
 constexpr int A_BYTES = 128 * 128;
@@ -52,11 +56,12 @@ constexpr uint32_t POLL_LIMIT = 1u << 22;
 __device__ int g_stall_copies;   // test hook: the producers issue no copies
 
 struct Shared {
-  uint64_t full[STAGES_MAX], empty[STAGES_MAX], acc_full[BUFS], acc_empty[BUFS], drain;
+  uint64_t full[STAGES_MAX], empty[STAGES_MAX], acc_full[BUFS], acc_empty[BUFS], sum_full[2], sum_empty[2], drain;
   uint32_t tmem;
   int abort, last, active, issued_a, issued_b;
-  float red[8][8];
-  uint32_t red_max[4][4];
+  float red[WARPS][8];
+  uint32_t red_max[WARPS];
+  float x_scale[MOE_TOKENS_MAX];
   uint32_t mask[EXPERTS];       // tokens of an expert, one bit each
   uint32_t act_mask[EXPERTS];   // the same of the reached experts, in order
   uint16_t act_expert[EXPERTS], act_base[EXPERTS], position[EXPERTS];
@@ -179,11 +184,6 @@ __device__ __forceinline__ float piece_inverse(float scale) {
   const uint32_t e = __float_as_uint(scale) >> 23;
   return e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
 }
-__device__ __forceinline__ uint32_t to_e4m3(float v) {
-  unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(v));
-  return r & 0xffu;
-}
 __device__ __forceinline__ float from_e4m3(uint32_t b) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)b));
@@ -201,9 +201,14 @@ __device__ __forceinline__ void route_logits(const MoeParams &p, Shared &sh) {
   for (int e = blockIdx.x; e < p.experts; e += gridDim.x)
     for (int t0 = 0; t0 < p.m; t0 += 8) {
       float acc[8] = {};
+#pragma unroll 2
       for (int f = threadIdx.x; f < frags; f += NT) {
         float w[8];
+        uint4 xv[8];
         const size_t at = size_t(e) * p.hidden + size_t(f) * 8;
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          xv[t] = t0 + t < p.m ? ld_ro(p.x + size_t(t0 + t) * p.hidden + size_t(f) * 8) : make_uint4(0, 0, 0, 0);
         if (p.router_f32) {
           const float *r = static_cast<const float *>(p.router) + at;
           const float4 a = __ldg(reinterpret_cast<const float4 *>(r)), b = __ldg(reinterpret_cast<const float4 *>(r) + 1);
@@ -216,13 +221,14 @@ __device__ __forceinline__ void route_logits(const MoeParams &p, Shared &sh) {
         for (int t = 0; t < 8; ++t)
           if (t0 + t < p.m) {
             float x[8];
-            unpack8(ld_ro(p.x + size_t(t0 + t) * p.hidden + size_t(f) * 8), x);
+            unpack8(xv[t], x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) acc[t] = fmaf(x[k], w[k], acc[t]);
           }
       }
 #pragma unroll
-      for (int t = 0; t < 8; ++t) acc[t] = warp_sum(acc[t]);
+      for (int t = 0; t < 8; ++t)
+        if (t0 + t < p.m) acc[t] = warp_sum(acc[t]);
       __syncthreads();
       if (lane == 0)
 #pragma unroll
@@ -231,7 +237,7 @@ __device__ __forceinline__ void route_logits(const MoeParams &p, Shared &sh) {
       if (threadIdx.x < 8 && t0 + int(threadIdx.x) < p.m) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) s += sh.red[w][threadIdx.x];
+        for (int w = 0; w < WARPS; ++w) s += sh.red[w][threadIdx.x];
         p.scratch.logits[size_t(t0 + threadIdx.x) * p.experts + e] = s;
       }
     }
@@ -240,41 +246,50 @@ __device__ __forceinline__ void route_logits(const MoeParams &p, Shared &sh) {
 // The E4M3 pieces of x: a row a CTA, from the last CTA down (the first ones
 // have experts' logits to compute).
 __device__ __forceinline__ void split_x(const MoeParams &p, Shared &sh) {
+  constexpr int HELD = 4;   // fragments a thread keeps in registers between the two passes
   const int frags = p.hidden / 8;
   for (int t = int(gridDim.x) - 1 - int(blockIdx.x); t < p.m; t += gridDim.x) {
     const uint16_t *x = p.x + size_t(t) * p.hidden;
     uint32_t a = 0;
-    for (int f = threadIdx.x; f < frags; f += NT) {
-      const uint4 v = ld_ro(x + size_t(f) * 8);
+    auto peak = [&](const uint4 &v) {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) a = max(a, max((w[k] << 16) & 0x7fff0000u, w[k] & 0x7fff0000u));
+    };
+    uint4 held[HELD];
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) {
+      const int f = threadIdx.x + k * NT;
+      held[k] = f < frags ? ld_ro(x + size_t(f) * 8) : make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) peak(held[k]);
+    for (int f = threadIdx.x + HELD * NT; f < frags; f += NT) peak(ld_ro(x + size_t(f) * 8));
     a = __reduce_max_sync(0xffffffffu, a);
     __syncthreads();
-    if (threadIdx.x % 32 == 0) sh.red_max[threadIdx.x / 128][threadIdx.x / 32 % 4] = a;
+    if (threadIdx.x % 32 == 0) sh.red_max[threadIdx.x / 32] = a;
     __syncthreads();
     a = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) a = max(a, sh.red_max[k / 4][k % 4]);
+    for (int k = 0; k < WARPS; ++k) a = max(a, sh.red_max[k]);
     const float scale = piece_scale(a), inv = piece_inverse(scale);
     uint8_t *hi = p.scratch.x_pieces + size_t(2 * t) * p.hidden, *lo = hi + p.hidden;
-    for (int f = threadIdx.x; f < frags; f += NT) {
+    auto split = [&](const uint4 &x8, int f) {
       float v[8];
-      unpack8(ld_ro(x + size_t(f) * 8), v);
-      uint2 h, l;
-      uint32_t hb[8], lb[8];
+      unpack8(x8, v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[k] *= inv;
-        hb[k] = to_e4m3(v[k]);
-        lb[k] = to_e4m3((v[k] - from_e4m3(hb[k])) * 16.f);
-      }
-      h = make_uint2(hb[0] | hb[1] << 8 | hb[2] << 16 | hb[3] << 24, hb[4] | hb[5] << 8 | hb[6] << 16 | hb[7] << 24);
-      l = make_uint2(lb[0] | lb[1] << 8 | lb[2] << 16 | lb[3] << 24, lb[4] | lb[5] << 8 | lb[6] << 16 | lb[7] << 24);
+      for (int k = 0; k < 8; ++k) v[k] *= inv;
+      const uint2 h = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = (v[k] - from_e4m3((k < 4 ? h.x : h.y) >> (k % 4 * 8) & 0xffu)) * 16.f;
       *reinterpret_cast<uint2 *>(hi + size_t(f) * 8) = h;
-      *reinterpret_cast<uint2 *>(lo + size_t(f) * 8) = l;
-    }
+      *reinterpret_cast<uint2 *>(lo + size_t(f) * 8) =
+          make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+    };
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+      if (int(threadIdx.x) + k * NT < frags) split(held[k], threadIdx.x + k * NT);
+    for (int f = threadIdx.x + HELD * NT; f < frags; f += NT) split(ld_ro(x + size_t(f) * 8), f);
     if (threadIdx.x == 0) p.scratch.x_scale[t] = scale;
   }
 }
@@ -287,9 +302,9 @@ __device__ __forceinline__ uint32_t score_key(float v) {
 }
 
 // One warp chooses token t's experts from its logits: lane l holds experts
-// l, l + 32, ...
-__device__ __forceinline__ void choose(const MoeParams &p, Shared &sh, int t) {
-  constexpr int PER = MOE_EXPERTS_MAX / 32;
+// l, l + 32, ... (PER of them).
+template <int PER>
+__device__ __noinline__ void choose(const MoeParams &p, Shared &sh, int t) {
   const int lane = threadIdx.x % 32;
   float score[PER];
   uint32_t key[PER];
@@ -367,7 +382,12 @@ __device__ __forceinline__ void build_plan(const MoeParams &p, Shared &sh) {
   const uint32_t all = p.m == 32 ? 0xffffffffu : (1u << p.m) - 1u;
   for (int e = threadIdx.x; e < every; e += NT) sh.mask[e] = e < p.experts ? 0u : all;
   __syncthreads();
-  for (int t = warp; t < p.m; t += NT / 32) choose(p, sh, t);
+  for (int t = warp; t < p.m; t += WARPS) {
+    if (p.experts <= 64) choose<2>(p, sh, t);
+    else if (p.experts <= 256) choose<8>(p, sh, t);
+    else choose<MOE_EXPERTS_MAX / 32>(p, sh, t);
+  }
+  if (p.fp8 && threadIdx.x < p.m) sh.x_scale[threadIdx.x] = __ldcg(p.scratch.x_scale + threadIdx.x);
   __syncthreads();
   if (warp == 0) {
     int active = 0, slots = 0;
@@ -394,16 +414,16 @@ __device__ __forceinline__ void build_plan(const MoeParams &p, Shared &sh) {
     if (lane == 0) sh.active = active;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.m * (p.top_k + p.shared); i += NT) {
-    const int t = i / (p.top_k + p.shared), k = i % (p.top_k + p.shared);
-    const int a = sh.position[k < p.top_k ? sh.chosen[t][k] : p.experts + k - p.top_k];
-    const int slot = sh.act_base[a] + __popc(sh.act_mask[a] & ((1u << t) - 1u));
-    sh.slot_weight[slot] = k < p.top_k ? sh.chosen_weight[t][k] : 1.f;
+  // a token a lane, a route a warp
+  for (int k = warp; lane < p.m && k < p.top_k + p.shared; k += WARPS) {
+    const int a = sh.position[k < p.top_k ? sh.chosen[lane][k] : p.experts + k - p.top_k];
+    const int slot = sh.act_base[a] + __popc(sh.act_mask[a] & ((1u << lane) - 1u));
+    sh.slot_weight[slot] = k < p.top_k ? sh.chosen_weight[lane][k] : 1.f;
   }
   __syncthreads();
 }
 
-// --------------------------------------------------------------- sums, up
+// -------------------------------------------------------------------- sums
 // COLS columns of this thread's TMEM lane.
 template <int COLS>
 __device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&d)[COLS]) {
@@ -416,82 +436,159 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&d)[COLS]) {
 
 __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits); }
 
-// Joins a finished tile of an expert: h of its tokens from the runs' sums,
-// then h's pieces for the down product.
-template <bool FP8>
-__device__ __forceinline__ void finish_up(const MoeParams &p, Shared &sh, const Shape &s, const Sequence &q, int a,
-                                          int j) {
-  const int i = threadIdx.x - EPI_WARP0 * 32;   // row of the tile
-  const int warp = i / 32, lane = i % 32;
-  const int row = j * 128 + i;
-  const size_t width = size_t(s.up_tiles) * 128;
-  const int64_t u0 = (int64_t(a) * s.up_tiles + j) * 2 * s.up_k;
-  const int gate_pieces = q.pieces(u0, s.up_k), up_pieces = q.pieces(u0 + s.up_k, s.up_k);
-  const int n = __popc(sh.act_mask[a]), base = sh.act_base[a];
-  for (int k0 = 0; k0 < n; k0 += 4) {
-    float h[4];
-    uint32_t top[4];
+// Sums of the k blocks [kb0, kb1) of a tile for this thread's row and CT
+// columns' tokens (P pieces each): block sums from the accumulator ring
+// (position n, stepped), their pieces added, times the weight's block scale
+// and, where `act` is given, the activation's (`count` of them a block,
+// `act_step` apart from block to block).  What lies beyond `count` is not
+// used.
+template <bool FP8, int P, int CT>
+__device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, int &n, int kb0, int kb1, const float *sw,
+                                           int sw_count, const float *act, int act_step, int count,
+                                           float (&acc)[CT]) {
+  constexpr int COLS = (CT * P + 15) / 16 * 16;
+  const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float g = 0.f, u = 0.f;
-      if (k0 + k < n) {
-        const float *src = p.scratch.up + size_t(base + k0 + k) * 2 * width + row;
-        const size_t step = size_t(p.slots) * 2 * width;
-        for (int f = 0; f < gate_pieces; ++f) g += __ldcg(src + f * step);
-        for (int f = 0; f < up_pieces; ++f) u += __ldcg(src + f * step + width);
-      }
-      h[k] = row < p.intermediate ? g / (1.f + expf(-g)) * u : 0.f;
-    }
+  for (int t = 0; t < CT; ++t) acc[t] = 0.f;
+  float held = 0.f;     // lane l: the weight scale of block (kb & ~31) + l
+  // lane l: the activation scale of token l, one block ahead
+  float next = FP8 && act && lane < count ? __ldcg(act + size_t(kb0) * act_step + lane) : 0.f;
+  for (int kb = kb0; kb < kb1; ++kb, ++n) {
+    const int b = n % BUFS;
+    float scale = 1.f;
     if (FP8) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        top[k] = __reduce_max_sync(0xffffffffu, __float_as_uint(h[k]) & 0x7fffffffu);
-        if (lane == 0) sh.red_max[k][warp] = top[k];
+      if (kb == kb0 || kb % 32 == 0) {
+        const int k = kb / 32 * 32 + lane;
+        held = k < sw_count ? __ldg(sw + k) : 0.f;
       }
-      tc::named_barrier(1, EPI_THREADS);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        top[k] = max(max(sh.red_max[k][0], sh.red_max[k][1]), max(sh.red_max[k][2], sh.red_max[k][3]));
-      tc::named_barrier(1, EPI_THREADS);
+      scale = __shfl_sync(0xffffffffu, held, kb % 32);
+      if (act) {
+        scale *= next;
+        if (kb + 1 < kb1 && lane < count) next = __ldcg(act + size_t(kb + 1) * act_step + lane);
+      }
     }
+    tc::wait_or_abort(&sh.acc_full[b], uint32_t((n / BUFS) & 1), &sh.abort);
+    __syncwarp();
+    tc::fence_after_sync();
+    uint32_t d[COLS];
+    load_cols(lane_base + uint32_t(b * BUF_COLS), d);
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sh.acc_empty[b]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k0 + k >= n) break;
-      const int slot = base + k0 + k;
+    for (int t = 0; t < CT; ++t) {
       if (FP8) {
-        const float scale = piece_scale(top[k]);
-        float r = h[k] * piece_inverse(scale);
-        uint8_t *dst = static_cast<uint8_t *>(p.scratch.act) + size_t(slot) * 3 * p.intermediate + row;
-        if (i == 0) p.scratch.act_scale[size_t(j) * p.slots + slot] = scale;
-        if (row < p.intermediate)
+        float v = value(d[P * t + P - 1]);
 #pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const uint32_t b = to_e4m3(r);
-            dst[size_t(c) * p.intermediate] = uint8_t(b);
-            r = (r - from_e4m3(b)) * 16.f;
-          }
-      } else if (row < p.intermediate) {
-        uint16_t *dst = static_cast<uint16_t *>(p.scratch.act) + size_t(slot) * 2 * p.intermediate + row;
-        const uint16_t hi = uint16_t(pack_bf16x2(h[k], 0.f));
-        dst[0] = hi;
-        dst[p.intermediate] = uint16_t(pack_bf16x2(h[k] - bf16_lo(hi), 0.f));
+        for (int c = P - 2; c >= 0; --c) v = fmaf(v, 0.0625f, value(d[P * t + c]));
+        acc[t] = fmaf(v, act ? __shfl_sync(0xffffffffu, scale, t) : scale, acc[t]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < P; ++c) acc[t] += value(d[P * t + c]);
       }
     }
   }
 }
 
+// Takes the sums of a tile's run for `count` tokens and gives token t's to
+// emit(t, sum); the width of the work follows the count.
+template <bool FP8, int P, class Emit>
+__device__ __forceinline__ void sum_tile(Shared &sh, uint32_t lane_base, int &n, int kb0, int kb1, const float *sw,
+                                         int sw_count, const float *act, int act_step, int count, const Emit &emit) {
+  auto with = [&](auto ct) {
+    constexpr int CT = decltype(ct)::value;
+    float acc[CT];
+    sum_blocks<FP8, P, CT>(sh, lane_base, n, kb0, kb1, sw, sw_count, act, act_step, count, acc);
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+      if (t < count) emit(t, acc[t]);
+  };
+  if (count <= 5) with(std::integral_constant<int, 5>());
+  else if (count <= 10) with(std::integral_constant<int, 10>());
+  else with(std::integral_constant<int, MOE_TOKENS_MAX>());
+}
+
+// ------------------------------------------------------------------- joins
+// h = silu(g) u of one token's 128 rows (four a lane) to its pieces for the
+// down product.
+template <bool FP8>
+__device__ __forceinline__ void store_act(const MoeParams &p, int slot, int j, const float4 &g4, const float4 &u4) {
+  const int lane = threadIdx.x % 32, row = j * 128 + lane * 4;
+  const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+  const bool live = row < p.intermediate;   // four rows are in or out together
+  float h[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    h[k] = live ? g[k] / (1.f + expf(-g[k])) * u[k] : 0.f;
+    top = max(top, __float_as_uint(h[k]) & 0x7fffffffu);
+  }
+  if (FP8) {
+    const float scale = piece_scale(__reduce_max_sync(0xffffffffu, top)), inv = piece_inverse(scale);
+    if (lane == 0) p.scratch.act_scale[size_t(j) * p.slots + slot] = scale;
+    uint8_t *dst = static_cast<uint8_t *>(p.scratch.act) + size_t(slot) * 3 * p.intermediate + row;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] *= inv;
+    if (live)
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const uint32_t b = e4m3x4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint32_t *>(dst + size_t(c) * p.intermediate) = b;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = (h[k] - from_e4m3(b >> (8 * k) & 0xffu)) * 16.f;
+      }
+  } else if (live) {
+    uint16_t *dst = static_cast<uint16_t *>(p.scratch.act) + size_t(slot) * 2 * p.intermediate + row;
+    const uint2 hi = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+    *reinterpret_cast<uint2 *>(dst) = hi;
+    *reinterpret_cast<uint2 *>(dst + p.intermediate) =
+        make_uint2(pack_bf16x2(h[0] - bf16_lo(hi.x), h[1] - bf16_hi(hi.x)),
+                   pack_bf16x2(h[2] - bf16_lo(hi.y), h[3] - bf16_hi(hi.y)));
+  }
+}
+
+__device__ __forceinline__ float4 add4(const float4 &a, const float4 &b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ float4 ldcg4(const float *p) { return __ldcg(reinterpret_cast<const float4 *>(p)); }
+
+// A finished tile of an expert from the runs' pieces in scratch, added in the
+// order of the runs; a warp a token.
+template <bool FP8>
+__device__ __forceinline__ void finish_up(const MoeParams &p, int base, int count, int j, int up_tiles, int gate_pieces,
+                                          int up_pieces) {
+  const int warp = threadIdx.x / 32 - JOIN_WARP0, lane = threadIdx.x % 32;
+  const size_t width = size_t(up_tiles) * 128, step = size_t(p.slots) * 2 * width;
+#pragma unroll 2
+  for (int t = warp; t < count; t += 4) {
+    const float *src = p.scratch.up + size_t(base + t) * 2 * width + j * 128 + lane * 4;
+    float4 g[MOE_UP_FRAGMENTS], u[MOE_UP_FRAGMENTS];
+#pragma unroll
+    for (int f = 0; f < MOE_UP_FRAGMENTS; ++f) {
+      g[f] = f < gate_pieces ? ldcg4(src + f * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+      u[f] = f < up_pieces ? ldcg4(src + f * step + width) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int f = 1; f < MOE_UP_FRAGMENTS; ++f) {
+      if (f < gate_pieces) g[0] = add4(g[0], g[f]);
+      if (f < up_pieces) u[0] = add4(u[0], u[f]);
+    }
+    store_act<FP8>(p, base + t, j, g[0], u[0]);
+  }
+}
+
 // ----------------------------------------------------------------- kernel
-template <bool FP8, int TM>
+template <bool FP8>
 __global__ void __launch_bounds__(NT, 1)
 k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const __grid_constant__ CUtensorMap tm_down,
-      const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_act) {
+      const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x_token,
+      const __grid_constant__ CUtensorMap tm_act) {
   constexpr int KB = FP8 ? 128 : 64;                        // values of a 128-byte k block
   constexpr int XP = FP8 ? 2 : 1, HP = FP8 ? 3 : 2;         // pieces of x and of h
-  constexpr int UP_COLS = (TM * XP + 15) / 16 * 16, DOWN_COLS = (TM * HP + 15) / 16 * 16;
   extern __shared__ __align__(1024) unsigned char smem[];
   Shared &sh = *reinterpret_cast<Shared *>(smem);
-  float *y_acc = reinterpret_cast<float *>(smem + SMEM_TABLES);   // [m][128]
-  unsigned char *ring = smem + SMEM_TABLES + (p.m * 512 + 1023) / 1024 * 1024;
+  float *sums = reinterpret_cast<float *>(smem + SMEM_TABLES);   // two buffers [m][128] from the sums to the joins
+  unsigned char *ring = smem + SMEM_TABLES + p.m * 1024;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort = &sh.abort;
   const int stage_bytes = A_BYTES + p.b_bytes;
@@ -504,7 +601,11 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     }
     for (int i = 0; i < BUFS; ++i) {
       tc::mbar_init(&sh.acc_full[i], 1);
-      tc::mbar_init(&sh.acc_empty[i], EPI_THREADS / 32);
+      tc::mbar_init(&sh.acc_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sh.sum_full[i], 4);
+      tc::mbar_init(&sh.sum_empty[i], 4);
     }
     tc::mbar_init(&sh.drain, 1);
     tc::mbar_init_fence();
@@ -513,6 +614,7 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     tc::tma_prefetch_desc(&tm_gate_up);
     tc::tma_prefetch_desc(&tm_down);
     tc::tma_prefetch_desc(&tm_x);
+    tc::tma_prefetch_desc(&tm_x_token);
     tc::tma_prefetch_desc(&tm_act);
   }
   if (warp == 2) tc::tmem_alloc(&sh.tmem, BUFS * BUF_COLS);
@@ -585,9 +687,19 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       if (n >= p.stages && !tc::wait_or_abort(&sh.empty[st], uint32_t((n / p.stages - 1) & 1), abort)) break;
       unsigned char *dst = ring + size_t(st) * stage_bytes + A_BYTES;
       if (n < up_n) {
+        const uint32_t mask = sh.act_mask[uc.a];
         if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&sh.full[st], uint32_t(x_rows) * 128);
-          tc::tma_load_2d(dst, &tm_x, uc.kb * KB, 0, &sh.full[st]);
+          if (__popc(mask) == p.m) {
+            tc::mbar_arrive_expect_tx(&sh.full[st], uint32_t(x_rows) * 128);
+            tc::tma_load_2d(dst, &tm_x, uc.kb * KB, 0, &sh.full[st]);
+          } else {
+            // the expert's tokens only, a copy each: their rows' swizzle goes by
+            // their place in shared memory, as the tensor core reads them
+            tc::mbar_arrive_expect_tx(&sh.full[st], uint32_t(__popc(mask)) * XP * 128);
+            int at = 0;
+            for (uint32_t rest = mask; rest; rest &= rest - 1u, at += XP * 128)
+              tc::tma_load_2d(dst + at, &tm_x_token, uc.kb * KB, (__ffs(rest) - 1) * XP, &sh.full[st]);
+          }
         }
         uc.next(s);
       } else {
@@ -615,8 +727,11 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       if (!tc::wait_or_abort(&sh.full[st], uint32_t((n / p.stages) & 1), abort)) break;
       if (n >= BUFS && !tc::wait_or_abort(&sh.acc_empty[b], uint32_t((n / BUFS - 1) & 1), abort)) break;
       tc::fence_after_sync();
-      int cols = p.m * XP;
-      if (n >= up_n) {
+      int cols;
+      if (n < up_n) {
+        cols = __popc(sh.act_mask[uc.a]) * XP;
+        uc.next(s);
+      } else {
         cols = __popc(sh.act_mask[dc.a]) * HP;
         dc.next(s, active);
       }
@@ -639,169 +754,188 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     if (tc::elect_one()) tc::mma_commit(&sh.drain);
     __syncwarp();
     tc::mbar_wait_bounded(&sh.drain, 0u, tc::SUB_WAIT_LIMIT);
-  } else if (warp >= EPI_WARP0) {
+  } else if (warp >= SUM_WARP0 && warp < JOIN_WARP0) {
     // ------------------------------------------------------------- sums
-    const int i = threadIdx.x - EPI_WARP0 * 32;   // row of the tile
+    // After a wait gave up these warps and the joins go through the rest of
+    // their loops on whatever is there (the waits return at once), so that they
+    // meet at their barriers and every arrival is counted.
+    const int i = threadIdx.x - SUM_WARP0 * 32;   // row of the tile
     const uint32_t lane_base = tmem + (uint32_t((warp % 4) * 32) << 16);
-    const size_t width = size_t(s.up_tiles) * 128;
-    // After a wait gave up these warps go through the rest of their loops on
-    // whatever is there (the waits return at once), so that they meet at their
-    // barriers and every arrival is counted.
-    int n = 0;
+    int n = 0, given = 0;
+    auto take = [&]() {   // the next buffer, once the joins have emptied it
+      if (given >= 2) tc::wait_or_abort(&sh.sum_empty[given % 2], uint32_t((given / 2 - 1) & 1), abort);
+      __syncwarp();
+      return sums + size_t(given % 2) * p.m * 128 + i;
+    };
+    auto give = [&]() {
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.sum_full[given % 2]);
+      ++given;
+    };
     // ---- up
     while (n < up_n) {
-      const UpCursor at(s, up0 + n);
-      const int a = at.a, r = at.r, j = r >> 1, kb0 = at.kb, kb1 = min(s.up_k, kb0 + up_n - n);
-      const int64_t tile = int64_t(a) * 2 * s.up_tiles + r;
-      const float *sw = p.gate_up_scales + ((size_t(sh.act_expert[a]) * 2 + (r & 1)) * s.up_tiles + j) * s.up_k;
-      float acc[TM];
-#pragma unroll
-      for (int t = 0; t < TM; ++t) acc[t] = 0.f;
-      float held = 0.f;   // lane l: the scale of k block (kb & ~31) + l
-      for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const int b = n % BUFS;
-        if (FP8 && (kb == kb0 || kb % 32 == 0)) {
-          const int k = kb / 32 * 32 + lane;
-          held = k < s.up_k ? __ldg(sw + k) : 0.f;
-        }
-        const float scale = FP8 ? __shfl_sync(0xffffffffu, held, kb % 32) : 1.f;
-        tc::wait_or_abort(&sh.acc_full[b], uint32_t((n / BUFS) & 1), abort);
-        __syncwarp();
-        tc::fence_after_sync();
-        uint32_t d[UP_COLS];
-        load_cols(lane_base + uint32_t(b * BUF_COLS), d);
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.acc_empty[b]);
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-          acc[t] = FP8 ? fmaf(fmaf(value(d[XP * t + XP - 1]), 0.0625f, value(d[XP * t])), scale, acc[t])
-                       : acc[t] + value(d[t]);
-      }
-      // this run's piece of the tile's sums
+      const int a = uc.a, r = uc.r, kb0 = uc.kb, kb1 = min(s.up_k, kb0 + up_n - n);
+      const float *sw = p.gate_up_scales + ((size_t(sh.act_expert[a]) * 2 + (r & 1)) * s.up_tiles + (r >> 1)) * s.up_k;
       const uint32_t mask = sh.act_mask[a];
-      const int piece = cta - up.run_of(tile * s.up_k);
-      float *dst = p.scratch.up + (size_t(piece) * p.slots + sh.act_base[a]) * 2 * width + (r & 1) * width + j * 128 + i;
-      int slot = 0;
-#pragma unroll
-      for (int t = 0; t < TM; ++t)
-        if (mask >> t & 1u) {
-          __stcg(dst + size_t(slot) * 2 * width, FP8 ? acc[t] * __ldcg(p.scratch.x_scale + t) : acc[t]);
-          ++slot;
+      uint32_t rest = mask;
+      float *dst = nullptr;
+      sum_tile<FP8, XP>(sh, lane_base, n, kb0, kb1, sw, s.up_k, nullptr, 0, __popc(mask), [&](int t, float v) {
+        if (t == 0) dst = take();
+        if (FP8) {
+          v *= sh.x_scale[__ffs(rest) - 1];
+          rest &= rest - 1u;
         }
-      __threadfence();
-      tc::named_barrier(1, EPI_THREADS);
-      if (i == 0) {
-        const int64_t u0 = (int64_t(a) * s.up_tiles + j) * 2 * s.up_k;
-        const unsigned want = unsigned(up.pieces(u0, s.up_k) + up.pieces(u0 + s.up_k, s.up_k));
-        unsigned *counter = p.scratch.up_counters + a * s.up_tiles + j;
-        const bool last = atomicAdd(counter, 1u) == want - 1;
-        if (last) *counter = 0;
-        sh.last = last;
-      }
-      tc::named_barrier(1, EPI_THREADS);
-      const bool last = sh.last != 0;
-      tc::named_barrier(1, EPI_THREADS);   // sh.last may be written again
-      if (last) {
-        __threadfence();
-        finish_up<FP8>(p, sh, s, up, a, j);
-        fence_proxy_async_global();
-        __threadfence();
-        tc::named_barrier(1, EPI_THREADS);
-        if (i == 0) atomicAdd(ups_done, 1u);
-      }
+        dst[t * 128] = v;
+      });
+      give();
+      uc.kb = kb1 - 1;
+      uc.next(s);
     }
     // ---- down
     if (n < n_all) poll(ups_done, up_total, abort);
     __syncwarp();
     while (n < n_all) {
       const int rb = dc.rb;
-      const int64_t rb_u0 = int64_t(rb) * active * s.down_k, rb_units = int64_t(active) * s.down_k;
-      const int n1 = int(min(down1, rb_u0 + rb_units) - down0) + up_n;   // end of this row block's units here
-      for (int t = 0; t < p.m; ++t) y_acc[t * 128 + i] = 0.f;
+      // end of this row block's units in this run
+      const int n1 = int(min(down1, int64_t(rb + 1) * active * s.down_k) - down0) + up_n;
+      float *y = take();
+      for (int t = 0; t < p.m; ++t) y[t * 128] = 0.f;
       while (n < n1) {
         const int a = dc.a, kb0 = dc.kb, kb1 = min(s.down_k, kb0 + n1 - n);
         const uint32_t mask = sh.act_mask[a];
-        const int count = __popc(mask), base = sh.act_base[a];
+        const int base = sh.act_base[a];
         const float *sw = p.down_scales + (size_t(sh.act_expert[a]) * s.down_tiles + rb) * s.down_k;
-        float acc[TM];
-#pragma unroll
-        for (int t = 0; t < TM; ++t) acc[t] = 0.f;
-        float held = 0.f;
-        // lane l: the activation scale of the expert's token l, one block ahead
-        float h_next = FP8 && lane < count ? __ldcg(p.scratch.act_scale + size_t(kb0) * p.slots + base + lane) : 0.f;
-        for (int kb = kb0; kb < kb1; ++kb, ++n) {
-          const int b = n % BUFS;
-          if (FP8 && (kb == kb0 || kb % 32 == 0)) {
-            const int k = kb / 32 * 32 + lane;
-            held = k < s.down_k ? __ldg(sw + k) : 0.f;
-          }
-          const float h_scale = FP8 ? h_next * __shfl_sync(0xffffffffu, held, kb % 32) : 1.f;
-          if (FP8 && kb + 1 < kb1 && lane < count)
-            h_next = __ldcg(p.scratch.act_scale + size_t(kb + 1) * p.slots + base + lane);
-          tc::wait_or_abort(&sh.acc_full[b], uint32_t((n / BUFS) & 1), abort);
-          __syncwarp();
-          tc::fence_after_sync();
-          uint32_t d[DOWN_COLS];
-          load_cols(lane_base + uint32_t(b * BUF_COLS), d);
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sh.acc_empty[b]);
-#pragma unroll
-          for (int t = 0; t < TM; ++t)
-            if (t < count) {
-              if (FP8) {
-                const float v = fmaf(fmaf(value(d[HP * t + HP - 1]), 0.0625f, value(d[HP * t + 1])), 0.0625f,
-                                     value(d[HP * t]));
-                acc[t] = fmaf(v, __shfl_sync(0xffffffffu, h_scale, t), acc[t]);
-              } else {
-                acc[t] += value(d[HP * t]) + value(d[HP * t + 1]);
-              }
-            }
-        }
+        uint32_t rest = mask;
+        sum_tile<FP8, HP>(sh, lane_base, n, kb0, kb1, sw, s.down_k, p.scratch.act_scale + base, p.slots, __popc(mask),
+                          [&](int t, float v) {
+                            float *at = y + (__ffs(rest) - 1) * 128;
+                            rest &= rest - 1u;
+                            *at = fmaf(v, sh.slot_weight[base + t], *at);
+                          });
         dc.kb = kb1 - 1;
         dc.next(s, active);
-        uint32_t rest = mask;
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-          if (t < count) {
-            const int token = __ffs(rest) - 1;
-            rest &= rest - 1u;
-            y_acc[token * 128 + i] = fmaf(acc[t], sh.slot_weight[base + t], y_acc[token * 128 + i]);
-          }
       }
-      // this run's piece of the row block
-      const int pieces = down.pieces(rb_u0, rb_units);
-      const size_t step = size_t(s.down_tiles) * p.m * 128;
-      float *dst = p.scratch.down + size_t(rb) * p.m * 128 + i;
-      const int row = rb * 128 + i;
-      bool last = true;
-      if (pieces > 1) {
-        const int piece = cta - down.run_of(rb_u0);
-        for (int t = 0; t < p.m; ++t) __stcg(dst + piece * step + t * 128, y_acc[t * 128 + i]);
+      give();
+    }
+  } else if (warp >= JOIN_WARP0) {
+    // ------------------------------------------------------------ joins
+    const int jw = warp - JOIN_WARP0;
+    const size_t width = size_t(s.up_tiles) * 128;
+    int taken = 0;
+    auto wait_sum = [&](int k) {
+      tc::wait_or_abort(&sh.sum_full[k % 2], uint32_t((k / 2) & 1), abort);
+      __syncwarp();
+      return sums + size_t(k % 2) * p.m * 128;
+    };
+    auto release = [&](int k) {
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.sum_empty[k % 2]);
+    };
+    // whether this run is the last of `want` to arrive at a counter, what all
+    // have written then being visible; the whole warps' threads call it
+    auto arrive = [&](unsigned *counter, unsigned want) {
+      __threadfence();
+      tc::named_barrier(1, 128);
+      if (threadIdx.x == JOIN_WARP0 * 32) {
+        const bool last = atomicAdd(counter, 1u) == want - 1;
+        if (last) *counter = 0;
+        sh.last = last;
+      }
+      tc::named_barrier(1, 128);
+      const bool last = sh.last != 0;
+      if (last) __threadfence();
+      return last;
+    };
+    // ---- up
+    for (int n = 0; n < up_n;) {
+      const int a = uc.a, r = uc.r, j = r >> 1, kb0 = uc.kb;
+      const int base = sh.act_base[a], count = __popc(sh.act_mask[a]);
+      bool done = true;
+      if (!(r & 1) && kb0 == 0 && n + 2 * s.up_k <= up_n) {
+        // gate and up of the tile lie in this run: no scratch
+        const float *g = wait_sum(taken), *u = wait_sum(taken + 1);
+        for (int t = jw; t < count; t += 4)
+          store_act<FP8>(p, base + t, j, reinterpret_cast<const float4 *>(g + t * 128)[lane],
+                         reinterpret_cast<const float4 *>(u + t * 128)[lane]);
+        release(taken);
+        release(taken + 1);
+        taken += 2;
+        n += 2 * s.up_k;
+        uc.r = r + 1;
+        uc.kb = s.up_k - 1;
+      } else {
+        const int kb1 = min(s.up_k, kb0 + up_n - n);
+        const int64_t u0 = (int64_t(a) * s.up_tiles + j) * 2 * s.up_k;
+        const int gate_pieces = up.pieces(u0, s.up_k), up_pieces = up.pieces(u0 + s.up_k, s.up_k);
+        const int piece = cta - up.run_of(u0 + (r & 1) * s.up_k);
+        float *dst = p.scratch.up + (size_t(piece) * p.slots + base) * 2 * width + (r & 1) * width + j * 128;
+        const float *src = wait_sum(taken);
+        for (int t = jw; t < count; t += 4)
+          __stcg(reinterpret_cast<float4 *>(dst + size_t(t) * 2 * width) + lane,
+                 reinterpret_cast<const float4 *>(src + t * 128)[lane]);
+        release(taken++);
+        done = arrive(p.scratch.up_counters + a * s.up_tiles + j, unsigned(gate_pieces + up_pieces));
+        if (done) finish_up<FP8>(p, base, count, j, s.up_tiles, gate_pieces, up_pieces);
+        n += kb1 - kb0;
+        uc.kb = kb1 - 1;
+      }
+      if (done) {
+        fence_proxy_async_global();
         __threadfence();
-        tc::named_barrier(1, EPI_THREADS);
-        if (i == 0) {
-          unsigned *counter = p.scratch.down_counters + rb;
-          const bool is_last = atomicAdd(counter, 1u) == unsigned(pieces - 1);
-          if (is_last) *counter = 0;
-          sh.last = is_last;
-        }
-        tc::named_barrier(1, EPI_THREADS);
-        last = sh.last != 0;
-        tc::named_barrier(1, EPI_THREADS);
-        if (last) {
-          __threadfence();
-          for (int t = 0; t < p.m; ++t) {
-            float y = 0.f;
-            for (int f = 0; f < pieces; ++f) y += __ldcg(dst + f * step + t * 128);
-            y_acc[t * 128 + i] = y;
+        tc::named_barrier(1, 128);
+        if (threadIdx.x == JOIN_WARP0 * 32) atomicAdd(ups_done, 1u);
+      }
+      uc.next(s);
+    }
+    // ---- down
+    const int64_t rb_units = int64_t(active) * s.down_k;
+    for (int64_t u = down0; u < down1;) {
+      const int rb = dc.rb;
+      const int64_t rb_u0 = rb * rb_units;
+      const int pieces = down.pieces(rb_u0, rb_units);
+      const float *src = wait_sum(taken);
+      // an item: a token's four neighbouring rows
+      const size_t step = size_t(s.down_tiles) * p.m * 128;
+      float *part = p.scratch.down + size_t(rb) * p.m * 128;
+      auto store_y = [&](int k, const float4 &y) {
+        const int row = rb * 128 + k % 32 * 4;   // hidden is a multiple of 8: four rows are in or out together
+        if (row < p.hidden) {
+          uint16_t *out = p.output + size_t(k / 32) * p.hidden + row;
+          const uint32_t lo = pack_bf16x2(y.x, y.y), hi = pack_bf16x2(y.z, y.w);
+          if (p.vector_out) {
+            *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
+          } else {
+            out[0] = uint16_t(lo);
+            out[1] = uint16_t(lo >> 16);
+            out[2] = uint16_t(hi);
+            out[3] = uint16_t(hi >> 16);
           }
         }
+      };
+      const int items = p.m * 32, first = threadIdx.x - JOIN_WARP0 * 32;
+      if (pieces == 1) {
+        for (int k = first; k < items; k += 128) store_y(k, reinterpret_cast<const float4 *>(src)[k]);
+        release(taken++);
+      } else {
+        float *dst = part + (cta - down.run_of(rb_u0)) * step;
+        for (int k = first; k < items; k += 128)
+          __stcg(reinterpret_cast<float4 *>(dst) + k, reinterpret_cast<const float4 *>(src)[k]);
+        release(taken++);
+        if (arrive(p.scratch.down_counters + rb, unsigned(pieces)))
+#pragma unroll 2
+          for (int k = first; k < items; k += 128) {
+            float4 y[MOE_DOWN_FRAGMENTS];
+#pragma unroll
+            for (int f = 0; f < MOE_DOWN_FRAGMENTS; ++f)
+              y[f] = f < pieces ? ldcg4(part + f * step + size_t(k) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int f = 1; f < MOE_DOWN_FRAGMENTS; ++f)
+              if (f < pieces) y[0] = add4(y[0], y[f]);
+            store_y(k, y[0]);
+          }
       }
-      if (last && row < p.hidden)
-        for (int t = 0; t < p.m; ++t)
-          p.output[size_t(t) * p.hidden + row] = uint16_t(pack_bf16x2(y_acc[t * 128 + i], 0.f));
+      u = min(down1, rb_u0 + rb_units);
+      ++dc.rb;
     }
   }
   tc::fence_before_sync();
@@ -827,7 +961,7 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   }
 }
 
-template <bool FP8, int TM>
+template <bool FP8>
 cudaError_t launch(const MoeParams &p, int sms, const CUtensorMap *maps, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms);
@@ -839,7 +973,7 @@ cudaError_t launch(const MoeParams &p, int sms, const CUtensorMap *maps, cudaStr
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_moe<FP8, TM>, p, maps[0], maps[1], maps[2], maps[3]);
+  return cudaLaunchKernelEx(&cfg, k_moe<FP8>, p, maps[0], maps[1], maps[2], maps[3], maps[4]);
 }
 
 }  // namespace
@@ -848,8 +982,7 @@ cudaError_t moe_stall_copies(int on) { return cudaMemcpyToSymbol(g_stall_copies,
 
 cudaError_t moe_set_attributes() {
   cudaError_t e = cudaSuccess;
-  for (const void *k : {(const void *)k_moe<false, 8>, (const void *)k_moe<false, 32>, (const void *)k_moe<true, 8>,
-                        (const void *)k_moe<true, 32>})
+  for (const void *k : {(const void *)k_moe<false>, (const void *)k_moe<true>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   return e;
 }
@@ -860,19 +993,19 @@ cudaError_t launch_moe(const MoeParams &args, int sms, cudaStream_t stream) {
   const int every = p.experts + p.shared, elem = fp8 ? 1 : 2, kb = fp8 ? 128 : 64;
   const int xp = fp8 ? 2 : 1, hp = fp8 ? 3 : 2;
   p.b_bytes = (p.m * std::max(xp, hp) + 7) / 8 * 1024;
-  p.stages = std::min(STAGES_MAX, (SMEM_BYTES - SMEM_TABLES - SMEM_SLACK - (p.m * 512 + 1023) / 1024 * 1024) /
-                                      (A_BYTES + p.b_bytes));
+  p.stages = std::min(STAGES_MAX, (SMEM_BYTES - SMEM_TABLES - SMEM_SLACK - p.m * 1024) / (A_BYTES + p.b_bytes));
+  p.vector_out = reinterpret_cast<uintptr_t>(p.output) % 8 == 0;
   const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t H = p.hidden, I = p.intermediate;
   const void *x = fp8 ? static_cast<const void *>(p.scratch.x_pieces) : p.x;
-  CUtensorMap maps[4];
+  CUtensorMap maps[5];
   if (!encode_rows_sw128(&maps[0], type, p.gate_up, uint64_t(every) * 2 * I, H, H * elem, kb, 128) ||
       !encode_rows_sw128(&maps[1], type, p.down, uint64_t(every) * H, I, I * elem, kb, 128) ||
       !encode_rows_sw128(&maps[2], type, x, uint64_t(p.m) * xp, H, H * elem, kb, (p.m * xp + 7) / 8 * 8) ||
-      !encode_rows_sw128(&maps[3], type, p.scratch.act, uint64_t(p.slots) * hp, I, I * elem, kb, 8))
+      !encode_rows_sw128(&maps[3], type, x, uint64_t(p.m) * xp, H, H * elem, kb, xp) ||
+      !encode_rows_sw128(&maps[4], type, p.scratch.act, uint64_t(p.slots) * hp, I, I * elem, kb, 8))
     return cudaErrorInvalidValue;
-  if (fp8) return p.m <= 8 ? launch<true, 8>(p, sms, maps, stream) : launch<true, 32>(p, sms, maps, stream);
-  return p.m <= 8 ? launch<false, 8>(p, sms, maps, stream) : launch<false, 32>(p, sms, maps, stream);
+  return fp8 ? launch<true>(p, sms, maps, stream) : launch<false>(p, sms, maps, stream);
 }
 
 }  // namespace mhc

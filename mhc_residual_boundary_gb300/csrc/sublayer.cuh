@@ -116,6 +116,7 @@ struct MoeParams {
   unsigned int *err;
   // set by the launcher
   int stages, b_bytes;
+  int vector_out;             // the output starts on an 8-byte boundary
 };
 
 cudaError_t moe_set_attributes();
