@@ -132,8 +132,9 @@ __device__ __forceinline__ Sequence down_sequence(const Shape &s, int active) {
   return q;
 }
 
-// The position of a unit in its sequence: stepped, because a 64-bit division
-// for each k block would take longer than the block's read.
+// The position in a sequence: a tile's run of k blocks at a time, so that the
+// loops over k blocks hold nothing but steps (a division for each block would
+// take as long as the block's read).
 struct UpCursor {     // (expert, gate / up tile, k)
   int a, r, kb;
   __device__ UpCursor(const Shape &s, int64_t u) {
@@ -142,8 +143,11 @@ struct UpCursor {     // (expert, gate / up tile, k)
     a = int(tile / (2 * s.up_tiles));
     r = int(tile - int64_t(a) * 2 * s.up_tiles);
   }
-  __device__ void next(const Shape &s) {
-    if (++kb == s.up_k) {
+  // k blocks of this tile among the next `left` units
+  __device__ int run(const Shape &s, int left) const { return min(s.up_k - kb, left); }
+  __device__ void step(const Shape &s, int blocks) {
+    kb += blocks;
+    if (kb == s.up_k) {
       kb = 0;
       if (++r == 2 * s.up_tiles) {
         r = 0;
@@ -160,13 +164,29 @@ struct DownCursor {   // (row block, expert, k)
     rb = int(tile / active);
     a = int(tile - int64_t(rb) * active);
   }
-  __device__ void next(const Shape &s, int active) {
-    if (++kb == s.down_k) {
+  __device__ int run(const Shape &s, int left) const { return min(s.down_k - kb, left); }
+  __device__ void step(const Shape &s, int active, int blocks) {
+    kb += blocks;
+    if (kb == s.down_k) {
       kb = 0;
       if (++a == active) {
         a = 0;
         ++rb;
       }
+    }
+  }
+};
+
+// A place in a ring of barriers and the phase of its current round.  A
+// producer waits for a slot's release with the other parity: that wait
+// returns at once in the first round.
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ void next(int size) {
+    if (++at == size) {
+      at = 0;
+      phase ^= 1u;
     }
   }
 };
@@ -437,13 +457,13 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&d)[COLS]) {
 __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits); }
 
 // Sums of the k blocks [kb0, kb1) of a tile for this thread's row and CT
-// columns' tokens (P pieces each): block sums from the accumulator ring
-// (position n, stepped), their pieces added, times the weight's block scale
+// columns' tokens (P pieces each): block sums from the accumulator ring,
+// their pieces added, times the weight's block scale
 // and, where `act` is given, the activation's (`count` of them a block,
 // `act_step` apart from block to block).  What lies beyond `count` is not
 // used.
 template <bool FP8, int P, int CT>
-__device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, int &n, int kb0, int kb1, const float *sw,
+__device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, Ring &ring, int kb0, int kb1, const float *sw,
                                            int sw_count, const float *act, int act_step, int count,
                                            float (&acc)[CT]) {
   constexpr int COLS = (CT * P + 15) / 16 * 16;
@@ -453,8 +473,7 @@ __device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, int &
   float held = 0.f;     // lane l: the weight scale of block (kb & ~31) + l
   // lane l: the activation scale of token l, one block ahead
   float next = FP8 && act && lane < count ? __ldcg(act + size_t(kb0) * act_step + lane) : 0.f;
-  for (int kb = kb0; kb < kb1; ++kb, ++n) {
-    const int b = n % BUFS;
+  for (int kb = kb0; kb < kb1; ++kb) {
     float scale = 1.f;
     if (FP8) {
       if (kb == kb0 || kb % 32 == 0) {
@@ -467,14 +486,15 @@ __device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, int &
         if (kb + 1 < kb1 && lane < count) next = __ldcg(act + size_t(kb + 1) * act_step + lane);
       }
     }
-    tc::wait_or_abort(&sh.acc_full[b], uint32_t((n / BUFS) & 1), &sh.abort);
+    tc::wait_or_abort(&sh.acc_full[ring.at], ring.phase, &sh.abort);
     __syncwarp();
     tc::fence_after_sync();
     uint32_t d[COLS];
-    load_cols(lane_base + uint32_t(b * BUF_COLS), d);
+    load_cols(lane_base + uint32_t(ring.at * BUF_COLS), d);
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&sh.acc_empty[b]);
+    if (lane == 0) tc::mbar_arrive(&sh.acc_empty[ring.at]);
+    ring.next(BUFS);
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
       if (FP8) {
@@ -493,12 +513,12 @@ __device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, int &
 // Takes the sums of a tile's run for `count` tokens and gives token t's to
 // emit(t, sum); the width of the work follows the count.
 template <bool FP8, int P, class Emit>
-__device__ __forceinline__ void sum_tile(Shared &sh, uint32_t lane_base, int &n, int kb0, int kb1, const float *sw,
+__device__ __forceinline__ void sum_tile(Shared &sh, uint32_t lane_base, Ring &ring, int kb0, int kb1, const float *sw,
                                          int sw_count, const float *act, int act_step, int count, const Emit &emit) {
   auto with = [&](auto ct) {
     constexpr int CT = decltype(ct)::value;
     float acc[CT];
-    sum_blocks<FP8, P, CT>(sh, lane_base, n, kb0, kb1, sw, sw_count, act, act_step, count, acc);
+    sum_blocks<FP8, P, CT>(sh, lane_base, ring, kb0, kb1, sw, sw_count, act, act_step, count, acc);
 #pragma unroll
     for (int t = 0; t < CT; ++t)
       if (t < count) emit(t, acc[t]);
@@ -642,7 +662,7 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   const Sequence up = up_sequence(s, active), down = down_sequence(s, active);
   const int cta = blockIdx.x;
   const int64_t up0 = up.begin(cta), up1 = up.begin(cta + 1), down0 = down.begin(cta), down1 = down.begin(cta + 1);
-  const int up_n = int(up1 - up0), n_all = up_n + int(down1 - down0);
+  const int up_n = int(up1 - up0), down_n = int(down1 - down0);
   UpCursor uc(s, up0);
   DownCursor dc(s, active, down0);
   const unsigned up_total = unsigned(active) * unsigned(s.up_tiles);
@@ -651,107 +671,122 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     // the logits never came: no role begins
   } else if (warp == 0) {
     // ----------------------------------------------------- weight tiles
+    Ring at;
+    int issued = 0;
     bool ok = !g_stall_copies;
-    int n = 0;
-    for (; n < n_all && ok; ++n) {
-      const int st = n % p.stages;
-      if (n >= p.stages && !tc::wait_or_abort(&sh.empty[st], uint32_t((n / p.stages - 1) & 1), abort)) break;
-      const void *map;
-      int kb, row;
-      if (n < up_n) {
-        kb = uc.kb;
-        row = sh.act_expert[uc.a] * 2 * p.intermediate + (uc.r & 1) * p.intermediate + (uc.r >> 1) * 128;
-        map = &tm_gate_up;
-        uc.next(s);
-      } else {
-        kb = dc.kb;
-        row = sh.act_expert[dc.a] * p.hidden + dc.rb * 128;
-        map = &tm_down;
-        dc.next(s, active);
+    const bool leader = tc::elect_one();
+    auto load = [&](const CUtensorMap *map, int kb, int row, int blocks) {
+      for (int k = 0; k < blocks; ++k) {
+        ok = ok && tc::wait_or_abort(&sh.empty[at.at], at.phase ^ 1u, abort);
+        if (!ok) return;
+        if (leader) {
+          tc::mbar_arrive_expect_tx(&sh.full[at.at], A_BYTES);
+          tc::tma_load_2d(ring + size_t(at.at) * stage_bytes, map, (kb + k) * KB, row, &sh.full[at.at]);
+        }
+        __syncwarp();
+        at.next(p.stages);
+        ++issued;
       }
-      if (tc::elect_one()) {
-        tc::mbar_arrive_expect_tx(&sh.full[st], A_BYTES);
-        tc::tma_load_2d(ring + size_t(st) * stage_bytes, map, kb * KB, row, &sh.full[st]);
-      }
-      __syncwarp();
+    };
+    for (int n = 0, run; n < up_n && ok; n += run) {
+      run = uc.run(s, up_n - n);
+      load(&tm_gate_up, uc.kb, (sh.act_expert[uc.a] * 2 + (uc.r & 1)) * p.intermediate + (uc.r >> 1) * 128, run);
+      uc.step(s, run);
     }
-    if (lane == 0) sh.issued_a = n;
+    for (int n = 0, run; n < down_n && ok; n += run) {
+      run = dc.run(s, down_n - n);
+      load(&tm_down, dc.kb, sh.act_expert[dc.a] * p.hidden + dc.rb * 128, run);
+      dc.step(s, active, run);
+    }
+    if (lane == 0) sh.issued_a = issued;
   } else if (warp == 3) {
     // ------------------------------------------------- activation tiles
+    Ring at;
+    int issued = 0;
     bool ok = !g_stall_copies;
-    int n = 0;
-    const int x_rows = (p.m * XP + 7) / 8 * 8;
-    fence_proxy_async_global();
-    for (; n < n_all && ok; ++n) {
-      const int st = n % p.stages;
-      if (n >= p.stages && !tc::wait_or_abort(&sh.empty[st], uint32_t((n / p.stages - 1) & 1), abort)) break;
-      unsigned char *dst = ring + size_t(st) * stage_bytes + A_BYTES;
-      if (n < up_n) {
-        const uint32_t mask = sh.act_mask[uc.a];
-        if (tc::elect_one()) {
-          if (__popc(mask) == p.m) {
-            tc::mbar_arrive_expect_tx(&sh.full[st], uint32_t(x_rows) * 128);
-            tc::tma_load_2d(dst, &tm_x, uc.kb * KB, 0, &sh.full[st]);
-          } else {
-            // the expert's tokens only, a copy each: their rows' swizzle goes by
-            // their place in shared memory, as the tensor core reads them
-            tc::mbar_arrive_expect_tx(&sh.full[st], uint32_t(__popc(mask)) * XP * 128);
-            int at = 0;
-            for (uint32_t rest = mask; rest; rest &= rest - 1u, at += XP * 128)
-              tc::tma_load_2d(dst + at, &tm_x_token, uc.kb * KB, (__ffs(rest) - 1) * XP, &sh.full[st]);
-          }
-        }
-        uc.next(s);
-      } else {
-        if (n == up_n) {
-          ok = poll(ups_done, up_total, abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          fence_proxy_async_global();
-        }
-        const int boxes = (__popc(sh.act_mask[dc.a]) * HP + 7) / 8, row = sh.act_base[dc.a] * HP;
-        if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&sh.full[st], uint32_t(boxes) * 1024);
-          for (int i = 0; i < boxes; ++i)
-            tc::tma_load_2d(dst + i * 1024, &tm_act, dc.kb * KB, row + i * 8, &sh.full[st]);
-        }
-        dc.next(s, active);
+    // `copies` copies of a k block, one a lane, of `bytes` in all: this lane's
+    // from row `row` to byte `place` of the stage
+    auto load = [&](const CUtensorMap *map, int kb, int blocks, int copies, int bytes, int row, int place) {
+      for (int k = 0; k < blocks; ++k) {
+        ok = ok && tc::wait_or_abort(&sh.empty[at.at], at.phase ^ 1u, abort);
+        if (!ok) return;
+        if (lane == 0) tc::mbar_arrive_expect_tx(&sh.full[at.at], uint32_t(bytes));
+        __syncwarp();
+        if (lane < copies)
+          tc::tma_load_2d(ring + size_t(at.at) * stage_bytes + A_BYTES + place, map, (kb + k) * KB, row,
+                          &sh.full[at.at]);
+        __syncwarp();
+        at.next(p.stages);
+        ++issued;
       }
-      __syncwarp();
+    };
+    fence_proxy_async_global();
+    const int x_rows = (p.m * XP + 7) / 8 * 8;
+    for (int n = 0, run; n < up_n && ok; n += run) {
+      run = uc.run(s, up_n - n);
+      const uint32_t mask = sh.act_mask[uc.a];
+      const int count = __popc(mask);
+      // all tokens in one copy; else the expert's tokens only, a copy each:
+      // their rows' swizzle goes by their place in shared memory, as the
+      // tensor core reads them
+      if (count == p.m) load(&tm_x, uc.kb, run, 1, x_rows * 128, 0, 0);
+      else load(&tm_x_token, uc.kb, run, count, count * XP * 128, __fns(mask, 0, lane + 1) * XP, lane * XP * 128);
+      uc.step(s, run);
     }
-    if (lane == 0) sh.issued_b = n;
+    if (down_n > 0 && ok) {
+      ok = poll(ups_done, up_total, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      fence_proxy_async_global();
+    }
+    for (int n = 0, run; n < down_n && ok; n += run) {
+      run = dc.run(s, down_n - n);
+      const int boxes = (__popc(sh.act_mask[dc.a]) * HP + 7) / 8;
+      load(&tm_act, dc.kb, run, boxes, boxes * 1024, sh.act_base[dc.a] * HP + lane * 8, lane * 1024);
+      dc.step(s, active, run);
+    }
+    if (lane == 0) sh.issued_b = issued;
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA
-    for (int n = 0; n < n_all; ++n) {
-      const int st = n % p.stages, b = n % BUFS;
-      if (!tc::wait_or_abort(&sh.full[st], uint32_t((n / p.stages) & 1), abort)) break;
-      if (n >= BUFS && !tc::wait_or_abort(&sh.acc_empty[b], uint32_t((n / BUFS - 1) & 1), abort)) break;
-      tc::fence_after_sync();
-      int cols;
-      if (n < up_n) {
-        cols = __popc(sh.act_mask[uc.a]) * XP;
-        uc.next(s);
-      } else {
-        cols = __popc(sh.act_mask[dc.a]) * HP;
-        dc.next(s, active);
-      }
-      cols = (cols + 15) / 16 * 16;
+    Ring at, acc;
+    bool ok = true;
+    const bool leader = tc::elect_one();
+    const uint64_t a0 = tc::desc_sw128(ring), b0 = tc::desc_sw128(ring + A_BYTES);
+    auto multiply = [&](int columns, int blocks) {
+      const int cols = (columns + 15) / 16 * 16;
       const uint32_t idesc = FP8 ? tc::idesc_e4m3_f32(128, cols) : tc::idesc_bf16_f32(128, cols);
-      const unsigned char *src = ring + size_t(st) * stage_bytes;
-      const uint64_t ad = tc::desc_sw128(src), bd = tc::desc_sw128(src + A_BYTES);
-      if (tc::elect_one()) {
+      for (int k = 0; k < blocks; ++k) {
+        ok = ok && tc::wait_or_abort(&sh.full[at.at], at.phase, abort) &&
+             tc::wait_or_abort(&sh.acc_empty[acc.at], acc.phase ^ 1u, abort);
+        if (!ok) return;
+        tc::fence_after_sync();
+        const uint64_t step = uint64_t(at.at * (stage_bytes >> 4));
+        const uint32_t d = tmem + uint32_t(acc.at * BUF_COLS);
+        if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          if (FP8) tc::mma_e4m3(tmem + uint32_t(b * BUF_COLS), ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
-          else tc::mma_bf16(tmem + uint32_t(b * BUF_COLS), ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+          for (int ks = 0; ks < 4; ++ks) {
+            if (FP8) tc::mma_e4m3(d, a0 + step + 2 * ks, b0 + step + 2 * ks, idesc, ks != 0);
+            else tc::mma_bf16(d, a0 + step + 2 * ks, b0 + step + 2 * ks, idesc, ks != 0);
+          }
+          tc::mma_commit(&sh.empty[at.at]);
+          tc::mma_commit(&sh.acc_full[acc.at]);
         }
-        tc::mma_commit(&sh.empty[st]);
-        tc::mma_commit(&sh.acc_full[b]);
+        __syncwarp();
+        at.next(p.stages);
+        acc.next(BUFS);
       }
-      __syncwarp();
+    };
+    for (int n = 0, run; n < up_n && ok; n += run) {
+      run = uc.run(s, up_n - n);
+      multiply(__popc(sh.act_mask[uc.a]) * XP, run);
+      uc.step(s, run);
+    }
+    for (int n = 0, run; n < down_n && ok; n += run) {
+      run = dc.run(s, down_n - n);
+      multiply(__popc(sh.act_mask[dc.a]) * HP, run);
+      dc.step(s, active, run);
     }
     // no MMA is in flight when the tensor memory goes
-    if (tc::elect_one()) tc::mma_commit(&sh.drain);
+    if (leader) tc::mma_commit(&sh.drain);
     __syncwarp();
     tc::mbar_wait_bounded(&sh.drain, 0u, tc::SUB_WAIT_LIMIT);
   } else if (warp >= SUM_WARP0 && warp < JOIN_WARP0) {
@@ -761,7 +796,8 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     // meet at their barriers and every arrival is counted.
     const int i = threadIdx.x - SUM_WARP0 * 32;   // row of the tile
     const uint32_t lane_base = tmem + (uint32_t((warp % 4) * 32) << 16);
-    int n = 0, given = 0;
+    Ring acc;
+    int given = 0;
     auto take = [&]() {   // the next buffer, once the joins have emptied it
       if (given >= 2) tc::wait_or_abort(&sh.sum_empty[given % 2], uint32_t((given / 2 - 1) & 1), abort);
       __syncwarp();
@@ -773,47 +809,43 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       ++given;
     };
     // ---- up
-    while (n < up_n) {
-      const int a = uc.a, r = uc.r, kb0 = uc.kb, kb1 = min(s.up_k, kb0 + up_n - n);
-      const float *sw = p.gate_up_scales + ((size_t(sh.act_expert[a]) * 2 + (r & 1)) * s.up_tiles + (r >> 1)) * s.up_k;
-      const uint32_t mask = sh.act_mask[a];
-      uint32_t rest = mask;
+    for (int n = 0, run; n < up_n; n += run) {
+      run = uc.run(s, up_n - n);
+      const float *sw = p.gate_up_scales +
+                        ((size_t(sh.act_expert[uc.a]) * 2 + (uc.r & 1)) * s.up_tiles + (uc.r >> 1)) * s.up_k;
+      uint32_t rest = sh.act_mask[uc.a];
       float *dst = nullptr;
-      sum_tile<FP8, XP>(sh, lane_base, n, kb0, kb1, sw, s.up_k, nullptr, 0, __popc(mask), [&](int t, float v) {
-        if (t == 0) dst = take();
-        if (FP8) {
-          v *= sh.x_scale[__ffs(rest) - 1];
-          rest &= rest - 1u;
-        }
-        dst[t * 128] = v;
-      });
+      sum_tile<FP8, XP>(sh, lane_base, acc, uc.kb, uc.kb + run, sw, s.up_k, nullptr, 0, __popc(rest),
+                        [&](int t, float v) {
+                          if (t == 0) dst = take();
+                          if (FP8) {
+                            v *= sh.x_scale[__ffs(rest) - 1];
+                            rest &= rest - 1u;
+                          }
+                          dst[t * 128] = v;
+                        });
       give();
-      uc.kb = kb1 - 1;
-      uc.next(s);
+      uc.step(s, run);
     }
     // ---- down
-    if (n < n_all) poll(ups_done, up_total, abort);
+    if (down_n > 0) poll(ups_done, up_total, abort);
     __syncwarp();
-    while (n < n_all) {
+    for (int n = 0; n < down_n;) {
       const int rb = dc.rb;
-      // end of this row block's units in this run
-      const int n1 = int(min(down1, int64_t(rb + 1) * active * s.down_k) - down0) + up_n;
       float *y = take();
       for (int t = 0; t < p.m; ++t) y[t * 128] = 0.f;
-      while (n < n1) {
-        const int a = dc.a, kb0 = dc.kb, kb1 = min(s.down_k, kb0 + n1 - n);
-        const uint32_t mask = sh.act_mask[a];
-        const int base = sh.act_base[a];
-        const float *sw = p.down_scales + (size_t(sh.act_expert[a]) * s.down_tiles + rb) * s.down_k;
-        uint32_t rest = mask;
-        sum_tile<FP8, HP>(sh, lane_base, n, kb0, kb1, sw, s.down_k, p.scratch.act_scale + base, p.slots, __popc(mask),
-                          [&](int t, float v) {
+      for (int run; n < down_n && dc.rb == rb; n += run) {
+        run = dc.run(s, down_n - n);
+        const int base = sh.act_base[dc.a];
+        const float *sw = p.down_scales + (size_t(sh.act_expert[dc.a]) * s.down_tiles + rb) * s.down_k;
+        uint32_t rest = sh.act_mask[dc.a];
+        sum_tile<FP8, HP>(sh, lane_base, acc, dc.kb, dc.kb + run, sw, s.down_k, p.scratch.act_scale + base, p.slots,
+                          __popc(rest), [&](int t, float v) {
                             float *at = y + (__ffs(rest) - 1) * 128;
                             rest &= rest - 1u;
                             *at = fmaf(v, sh.slot_weight[base + t], *at);
                           });
-        dc.kb = kb1 - 1;
-        dc.next(s, active);
+        dc.step(s, active, run);
       }
       give();
     }
@@ -848,10 +880,10 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     };
     // ---- up
     for (int n = 0; n < up_n;) {
-      const int a = uc.a, r = uc.r, j = r >> 1, kb0 = uc.kb;
+      const int a = uc.a, r = uc.r, j = r >> 1;
       const int base = sh.act_base[a], count = __popc(sh.act_mask[a]);
       bool done = true;
-      if (!(r & 1) && kb0 == 0 && n + 2 * s.up_k <= up_n) {
+      if (!(r & 1) && uc.kb == 0 && n + 2 * s.up_k <= up_n) {
         // gate and up of the tile lie in this run: no scratch
         const float *g = wait_sum(taken), *u = wait_sum(taken + 1);
         for (int t = jw; t < count; t += 4)
@@ -862,9 +894,9 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
         taken += 2;
         n += 2 * s.up_k;
         uc.r = r + 1;
-        uc.kb = s.up_k - 1;
+        uc.step(s, s.up_k);
       } else {
-        const int kb1 = min(s.up_k, kb0 + up_n - n);
+        const int run = uc.run(s, up_n - n);
         const int64_t u0 = (int64_t(a) * s.up_tiles + j) * 2 * s.up_k;
         const int gate_pieces = up.pieces(u0, s.up_k), up_pieces = up.pieces(u0 + s.up_k, s.up_k);
         const int piece = cta - up.run_of(u0 + (r & 1) * s.up_k);
@@ -876,8 +908,8 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
         release(taken++);
         done = arrive(p.scratch.up_counters + a * s.up_tiles + j, unsigned(gate_pieces + up_pieces));
         if (done) finish_up<FP8>(p, base, count, j, s.up_tiles, gate_pieces, up_pieces);
-        n += kb1 - kb0;
-        uc.kb = kb1 - 1;
+        n += run;
+        uc.step(s, run);
       }
       if (done) {
         fence_proxy_async_global();
@@ -885,7 +917,6 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
         tc::named_barrier(1, 128);
         if (threadIdx.x == JOIN_WARP0 * 32) atomicAdd(ups_done, 1u);
       }
-      uc.next(s);
     }
     // ---- down
     const int64_t rb_units = int64_t(active) * s.down_k;
