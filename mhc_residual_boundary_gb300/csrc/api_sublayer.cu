@@ -135,17 +135,17 @@ size_t moe_layout(mhc_sublayer_t *s) {
   MoeScratch &q = s->moe;
   take(q.control, MOE_CONTROL * 4);
   take(q.up_counters, reached * ib * 4);
-  take(q.down_counters, hb * 4);
+  take(q.up_done, reached * 4);
   s->moe_counter_bytes = off;
   take(q.logits, m * c.num_experts * 4);
   take(q.x_pieces, fp8 ? 2 * m * c.hidden : 0);
   take(q.x_scale, m * 4);
-  take(q.up, MOE_UP_FRAGMENTS * slots * 2 * ib * QBLOCK * 4);
+  take(q.up, MOE_CHUNKS * slots * 2 * ib * QBLOCK * 4);
   unsigned char *act;
   take(act, slots * (fp8 ? 3 : 4) * c.intermediate);
   q.act = act;
   take(q.act_scale, fp8 ? ib * slots * 4 : 0);
-  take(q.down, MOE_DOWN_FRAGMENTS * hb * m * QBLOCK * 4);
+  take(q.down, MOE_CHUNKS * slots * hb * QBLOCK * 4);
   s->moe_slots = int(slots);
   return off;
 }

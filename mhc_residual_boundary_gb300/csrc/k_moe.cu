@@ -20,20 +20,19 @@
 // weight's block scale multiplies each block of 128's sum in FP32.  BF16
 // weights take x as it is and h as two BF16 pieces (16 bits).
 //
-// One persistent CTA per SM, launched cooperatively (the CTAs wait for one
-// another twice, after `route` and between `up` and `down`).  The k blocks
-// of all tiles of a phase form one sequence that is cut into equal runs, one
-// for each CTA, so the read is balanced whatever the number of reached
-// experts.  A run's partial sums of a tile go to scratch; the last run to
-// arrive at a tile adds them in the order of the runs, so the result does not
-// depend on timing.  The producer of the weight tiles does not take part in the
-// waits after `route`: it fills the stage ring with the first `down` tiles while
-// the `up` sums are still being joined; and the warps that join the pieces are
-// not those that take the sums out of the tensor memory, so neither does the
-// ring wait for a join.
+// One persistent CTA per SM, launched cooperatively (after `route` the CTAs wait
+// for one another).  The work is one list of items, a tile's chunk of k blocks
+// each: first all of `up`, then all of `down`, both expert by expert.  A CTA
+// takes the next item when its producer comes to it, so CTAs with experts of
+// many tokens, whose blocks take longer, take fewer.  An item waits only for
+// items before it (a `down` item for its expert's `up` tiles, which were taken
+// long before), so the memory is read without a break from the first item to
+// the last.  An item's sums go to scratch, by the item's place, and are added in
+// the order of the chunks by whoever finds a tile complete: the result does not
+// depend on who took which item when.
 //
-// Warps: 0 weight tiles, 1 MMA, 2 TMEM, 3 activation tiles, 4-7 sums, 8-11
-// joins.
+// Warps: 0 items and weight tiles, 1 MMA, 2 scales, 3 activation tiles, 4-7 sums
+// (tensor memory to buffers), 8-11 joins (buffers to scratch, activations).
 #include <algorithm>
 #include <type_traits>
 
@@ -46,28 +45,31 @@ namespace {
 constexpr int NT = 384, WARPS = NT / 32;
 constexpr int SUM_WARP0 = 4, JOIN_WARP0 = 8;
 constexpr int STAGES_MAX = 12;
+constexpr int ITEMS = 4;        // items between their taking and the last warp that reads them
 constexpr int BUFS = 4, BUF_COLS = 128;
 constexpr int A_BYTES = 128 * 128;
 constexpr int SMEM_BYTES = 227 * 1024;
 constexpr int EXPERTS = MOE_EXPERTS_MAX + MOE_SHARED_MAX;
-constexpr int SLOTS = MOE_TOKENS_MAX * (MOE_TOPK_MAX + MOE_SHARED_MAX);
 constexpr uint32_t POLL_LIMIT = 1u << 22;
 
 __device__ int g_stall_copies;   // test hook: the producers issue no copies
 
 struct Shared {
-  uint64_t full[STAGES_MAX], empty[STAGES_MAX], acc_full[BUFS], acc_empty[BUFS], sum_full[2], sum_empty[2], drain;
+  uint64_t full[STAGES_MAX], empty[STAGES_MAX], acc_full[BUFS], acc_empty[BUFS], sum_full[4], sum_empty[2],
+      item_full[ITEMS], item_empty[ITEMS], scale_full[ITEMS], drain;
   uint32_t tmem;
-  int abort, last, active, issued_a, issued_b;
+  int abort, active, issued_a, issued_b;
+  int item[ITEMS];
   float red[WARPS][8];
   uint32_t red_max[WARPS];
   float x_scale[MOE_TOKENS_MAX];
-  uint32_t mask[EXPERTS];       // tokens of an expert, one bit each
-  uint32_t act_mask[EXPERTS];   // the same of the reached experts, in order
+  int warp_active[WARPS], warp_slots[WARPS];
+  uint32_t mask[EXPERTS];       // tokens of an expert, one bit each; the shared experts come first
+  uint32_t act_mask[EXPERTS];   // the same of the reached experts, in that order
   uint16_t act_expert[EXPERTS], act_base[EXPERTS], position[EXPERTS];
-  float slot_weight[SLOTS];
-  int16_t chosen[MOE_TOKENS_MAX][MOE_TOPK_MAX];
-  float chosen_weight[MOE_TOKENS_MAX][MOE_TOPK_MAX];
+  int16_t route_expert[MOE_TOKENS_MAX][MOE_TOPK_MAX];               // a token's chosen experts
+  int16_t route_slot[MOE_TOKENS_MAX][MOE_TOPK_MAX + MOE_SHARED_MAX];  // the slots of its chosen and shared experts
+  float route_weight[MOE_TOKENS_MAX][MOE_TOPK_MAX];
 };
 constexpr int SMEM_TABLES = (int(sizeof(Shared)) + 1023) / 1024 * 1024;
 constexpr int SMEM_SLACK = 1024;   // an MMA's columns are rounded up to 16: it may read 8 rows past the last stage
@@ -89,93 +91,80 @@ __device__ __noinline__ bool poll(const unsigned *p, unsigned want, volatile int
   *abort = 1;
   return false;
 }
+// Until experts [ready, need) are complete: the whole warp looks at the next 32
+// counters with one read (it takes microseconds while the memory is busy) and
+// returns how many experts, in order, are.
+__device__ __noinline__ int poll_experts(const unsigned *done, unsigned tiles, int ready, int need, int active,
+                                         volatile int *abort) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll 1
+  for (uint32_t i = 0; i < POLL_LIMIT; ++i) {
+    const bool complete = ready + lane >= active || ld_acquire(done + ready + lane) >= tiles;
+    const uint32_t missing = ~__ballot_sync(0xffffffffu, complete);
+    ready += missing ? __ffs(missing) - 1 : 32;
+    if (ready >= need || __any_sync(0xffffffffu, *abort != 0)) break;
+    if (i > 256) __nanosleep(128);
+  }
+  if (ready < need) *abort = 1;
+  return ready;
+}
 // Orders generic-proxy accesses to global memory and the TMA's.
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-// ------------------------------------------------------------- the sequence
-// A phase's k blocks, cut into `runs` equal runs (run c: [total c / runs,
-// total (c + 1) / runs)).
-struct Sequence {
-  int64_t total;
-  int runs;
-  __device__ int64_t begin(int c) const { return c >= runs ? total : total * c / runs; }
-  // the run that holds unit u
-  __device__ int run_of(int64_t u) const { return int(((u + 1) * runs - 1) / total); }
-  // runs that share units [u, u + n)
-  __device__ int pieces(int64_t u, int64_t n) const { return run_of(u + n - 1) - run_of(u) + 1; }
-};
-
+// ---------------------------------------------------------------- the items
 struct Shape {
   int up_tiles, up_k;       // up: tiles of 128 rows of an expert's gate (and of its up) and their k blocks
   int down_tiles, down_k;   // down: row blocks of the output, k blocks of an expert
+  int up_chunks, down_chunks;
+  int up_items, items;      // of `up`, of both
 };
 
 template <bool FP8>
-__device__ __forceinline__ Shape shape_of(const MoeParams &p) {
+__device__ __forceinline__ Shape shape_of(const MoeParams &p, int active) {
   constexpr int KB = FP8 ? 128 : 64;
-  return {(p.intermediate + 127) / 128, (p.hidden + KB - 1) / KB, (p.hidden + 127) / 128,
-          (p.intermediate + KB - 1) / KB};
-}
-// up: units (expert, tile, gate / up, k); runs of at least half a tile's k
-// blocks, so that at most MOE_UP_FRAGMENTS share a tile
-__device__ __forceinline__ Sequence up_sequence(const Shape &s, int active) {
-  Sequence q;
-  q.total = int64_t(active) * s.up_tiles * 2 * s.up_k;
-  q.runs = int(min(int64_t(gridDim.x), max(int64_t(1), q.total / ((s.up_k + 1) / 2))));
-  return q;
-}
-// down: units (row block, expert, k); at most MOE_DOWN_SPLIT runs a row block
-__device__ __forceinline__ Sequence down_sequence(const Shape &s, int active) {
-  Sequence q;
-  q.total = int64_t(s.down_tiles) * active * s.down_k;
-  q.runs = int(min(min(int64_t(gridDim.x), int64_t(s.down_tiles) * MOE_DOWN_SPLIT), q.total));
-  return q;
+  Shape s;
+  s.up_tiles = (p.intermediate + 127) / 128;
+  s.up_k = (p.hidden + KB - 1) / KB;
+  s.down_tiles = (p.hidden + 127) / 128;
+  s.down_k = (p.intermediate + KB - 1) / KB;
+  s.up_chunks = p.up_chunks;
+  s.down_chunks = p.down_chunks;
+  s.up_items = active * s.up_tiles * 2 * s.up_chunks;
+  s.items = s.up_items + active * s.down_tiles * s.down_chunks;
+  return s;
 }
 
-// The position in a sequence: a tile's run of k blocks at a time, so that the
-// loops over k blocks hold nothing but steps (a division for each block would
-// take as long as the block's read).
-struct UpCursor {     // (expert, gate / up tile, k)
-  int a, r, kb;
-  __device__ UpCursor(const Shape &s, int64_t u) {
-    const int64_t tile = u / s.up_k;
-    kb = int(u - tile * s.up_k);
-    a = int(tile / (2 * s.up_tiles));
-    r = int(tile - int64_t(a) * 2 * s.up_tiles);
-  }
-  // k blocks of this tile among the next `left` units
-  __device__ int run(const Shape &s, int left) const { return min(s.up_k - kb, left); }
-  __device__ void step(const Shape &s, int blocks) {
-    kb += blocks;
-    if (kb == s.up_k) {
-      kb = 0;
-      if (++r == 2 * s.up_tiles) {
-        r = 0;
-        ++a;
-      }
-    }
-  }
+struct Item {
+  bool down;
+  int a;        // reached expert
+  int tile;     // up: tile of the intermediate size; down: row block of the output
+  int half;     // up: 0 gate, 1 up
+  int chunk, kb0, blocks;
 };
-struct DownCursor {   // (row block, expert, k)
-  int rb, a, kb;
-  __device__ DownCursor(const Shape &s, int active, int64_t u) {
-    const int64_t tile = u / s.down_k;
-    kb = int(u - tile * s.down_k);
-    rb = int(tile / active);
-    a = int(tile - int64_t(rb) * active);
+__device__ __forceinline__ Item item_at(const Shape &s, int i) {
+  Item it;
+  it.down = i >= s.up_items;
+  if (!it.down) {
+    int q = i / s.up_chunks;
+    it.chunk = i - q * s.up_chunks;
+    it.half = q & 1;
+    q >>= 1;
+    it.a = q / s.up_tiles;
+    it.tile = q - it.a * s.up_tiles;
+    it.kb0 = s.up_k * it.chunk / s.up_chunks;
+    it.blocks = s.up_k * (it.chunk + 1) / s.up_chunks - it.kb0;
+  } else {
+    i -= s.up_items;
+    const int q = i / s.down_chunks;
+    it.chunk = i - q * s.down_chunks;
+    it.half = 0;
+    it.a = q / s.down_tiles;
+    it.tile = q - it.a * s.down_tiles;
+    it.kb0 = s.down_k * it.chunk / s.down_chunks;
+    it.blocks = s.down_k * (it.chunk + 1) / s.down_chunks - it.kb0;
   }
-  __device__ int run(const Shape &s, int left) const { return min(s.down_k - kb, left); }
-  __device__ void step(const Shape &s, int active, int blocks) {
-    kb += blocks;
-    if (kb == s.down_k) {
-      kb = 0;
-      if (++a == active) {
-        a = 0;
-        ++rb;
-      }
-    }
-  }
-};
+  return it;
+}
 
 // A place in a ring of barriers and the phase of its current round.  A
 // producer waits for a slot's release with the other parity: that wait
@@ -213,16 +202,21 @@ __device__ __forceinline__ float from_e4m3(uint32_t b) {
 }
 
 // ------------------------------------------------------------------ route
-// Logits of all tokens for this CTA's experts: eight tokens at a time, the
-// hidden size spread over all threads.
+// Logits.  An item is an expert and eight tokens; a CTA's warps take as many
+// items at a time (1, 2, 3 or 6) as spread them over all CTAs, the hidden size
+// being spread over the warps of an item.
 __device__ __forceinline__ void route_logits(const MoeParams &p, Shared &sh) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int frags = p.hidden / 8;
-  for (int e = blockIdx.x; e < p.experts; e += gridDim.x)
-    for (int t0 = 0; t0 < p.m; t0 += 8) {
-      float acc[8] = {};
+  const int frags = p.hidden / 8, items = p.experts * ((p.m + 7) / 8);
+  int groups = 1;
+  while (groups < 6 && items > groups * int(gridDim.x)) groups = groups == 3 ? 6 : groups + 1;
+  const int warps = WARPS / groups, group = warp / warps;
+  for (int i0 = blockIdx.x * groups; i0 < items; i0 += gridDim.x * groups) {
+    const int item = i0 + group, e = item % p.experts, t0 = item / p.experts * 8;
+    float acc[8] = {};
+    if (item < items) {
 #pragma unroll 2
-      for (int f = threadIdx.x; f < frags; f += NT) {
+      for (int f = threadIdx.x - group * warps * 32; f < frags; f += warps * 32) {
         float w[8];
         uint4 xv[8];
         const size_t at = size_t(e) * p.hidden + size_t(f) * 8;
@@ -249,18 +243,18 @@ __device__ __forceinline__ void route_logits(const MoeParams &p, Shared &sh) {
 #pragma unroll
       for (int t = 0; t < 8; ++t)
         if (t0 + t < p.m) acc[t] = warp_sum(acc[t]);
-      __syncthreads();
-      if (lane == 0)
-#pragma unroll
-        for (int t = 0; t < 8; ++t) sh.red[warp][t] = acc[t];
-      __syncthreads();
-      if (threadIdx.x < 8 && t0 + int(threadIdx.x) < p.m) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) s += sh.red[w][threadIdx.x];
-        p.scratch.logits[size_t(t0 + threadIdx.x) * p.experts + e] = s;
-      }
     }
+    __syncthreads();
+    if (lane == 0)
+#pragma unroll
+      for (int t = 0; t < 8; ++t) sh.red[warp][t] = acc[t];
+    __syncthreads();
+    if (warp == group * warps && lane < 8 && item < items && t0 + lane < p.m) {
+      float s = 0.f;
+      for (int w = 0; w < warps; ++w) s += sh.red[warp + w][lane];
+      p.scratch.logits[size_t(t0 + lane) * p.experts + e] = s;
+    }
+  }
 }
 
 // The E4M3 pieces of x: a row a CTA, from the last CTA down (the first ones
@@ -321,10 +315,10 @@ __device__ __forceinline__ uint32_t score_key(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One warp chooses token t's experts from its logits: lane l holds experts
-// l, l + 32, ... (PER of them).
+// One warp chooses token t's experts from its logits (in scratch, or in shared
+// memory): lane l holds experts l, l + 32, ... (PER of them).
 template <int PER>
-__device__ __noinline__ void choose(const MoeParams &p, Shared &sh, int t) {
+__device__ __noinline__ void choose(const MoeParams &p, Shared &sh, int t, const float *logits) {
   const int lane = threadIdx.x % 32;
   float score[PER];
   uint32_t key[PER];
@@ -332,7 +326,7 @@ __device__ __noinline__ void choose(const MoeParams &p, Shared &sh, int t) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = i * 32 + lane;
-    score[i] = e < p.experts ? __ldcg(p.scratch.logits + size_t(t) * p.experts + e) : -INFINITY;
+    score[i] = e < p.experts ? *static_cast<const volatile float *>(logits + e) : -INFINITY;
     peak = fmaxf(peak, score[i]);
   }
   if (!p.sigmoid) {
@@ -384,9 +378,9 @@ __device__ __noinline__ void choose(const MoeParams &p, Shared &sh, int t) {
   }
   if (lane < p.top_k) {
     const float w = (p.renormalize ? mine / total : mine) * p.routed_scale;
-    sh.chosen[t][lane] = int16_t(mine_e);
-    sh.chosen_weight[t][lane] = w;
-    atomicOr(&sh.mask[mine_e], 1u << t);
+    sh.route_expert[t][lane] = int16_t(mine_e);
+    sh.route_weight[t][lane] = w;
+    atomicOr(&sh.mask[p.shared + mine_e], 1u << t);
     if (blockIdx.x == 0) {
       if (p.idx) p.idx[t * p.top_k + lane] = mine_e;
       if (p.weights) p.weights[t * p.top_k + lane] = w;
@@ -394,51 +388,68 @@ __device__ __noinline__ void choose(const MoeParams &p, Shared &sh, int t) {
   }
 }
 
-// The reached experts in order, each one's tokens and first slot (a slot is a
-// token of an expert), and the slots' weights.  Every CTA computes the same.
-__device__ __forceinline__ void build_plan(const MoeParams &p, Shared &sh) {
+// The reached experts in order (the shared ones first), each one's tokens and
+// first slot (a slot is a token of an expert), and the tokens' slots.  Every
+// CTA computes the same.
+template <class Begin>
+__device__ __forceinline__ void build_plan(const MoeParams &p, Shared &sh, float *held, const Begin &begin) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int every = p.experts + p.shared;
-  const uint32_t all = p.m == 32 ? 0xffffffffu : (1u << p.m) - 1u;
-  for (int e = threadIdx.x; e < every; e += NT) sh.mask[e] = e < p.experts ? 0u : all;
-  __syncthreads();
-  for (int t = warp; t < p.m; t += WARPS) {
-    if (p.experts <= 64) choose<2>(p, sh, t);
-    else if (p.experts <= 256) choose<8>(p, sh, t);
-    else choose<MOE_EXPERTS_MAX / 32>(p, sh, t);
-  }
+  // the logits of all tokens into shared memory (256 floats a token), where
+  // they fit, before `begin` makes the memory busy
+  const bool fit = p.experts <= 256;
+  if (fit)
+    for (int i = threadIdx.x; i < p.m * p.experts; i += NT) held[i] = __ldcg(p.scratch.logits + i);
   if (p.fp8 && threadIdx.x < p.m) sh.x_scale[threadIdx.x] = __ldcg(p.scratch.x_scale + threadIdx.x);
   __syncthreads();
-  if (warp == 0) {
-    int active = 0, slots = 0;
-    for (int e0 = 0; e0 < every; e0 += 32) {
-      const uint32_t mask = e0 + lane < every ? sh.mask[e0 + lane] : 0u;
-      const uint32_t reached = __ballot_sync(0xffffffffu, mask != 0u);
-      const int n = __popc(mask);
-      int upto = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      if (mask) {
-        const int a = active + __popc(reached & ((1u << lane) - 1u));
-        sh.act_mask[a] = mask;
-        sh.act_expert[a] = uint16_t(e0 + lane);
-        sh.act_base[a] = uint16_t(slots + upto - n);
-        sh.position[e0 + lane] = uint16_t(a);
-      }
-      active += __popc(reached);
-      slots += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (lane == 0) sh.active = active;
+  begin();
+  for (int t = warp; t < p.m; t += WARPS) {
+    const float *logits = (fit ? held : p.scratch.logits) + size_t(t) * p.experts;
+    if (p.experts <= 64) choose<2>(p, sh, t, logits);
+    else if (p.experts <= 256) choose<8>(p, sh, t, logits);
+    else choose<MOE_EXPERTS_MAX / 32>(p, sh, t, logits);
   }
   __syncthreads();
+  int active0 = 0, slots0 = 0;   // before this round of one expert a thread
+  for (int e0 = 0; e0 < every; e0 += NT) {
+    const int e = e0 + threadIdx.x;
+    const uint32_t mask = e < every ? sh.mask[e] : 0u;
+    const uint32_t reached = __ballot_sync(0xffffffffu, mask != 0u);
+    const int n = __popc(mask);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) {
+      sh.warp_active[warp] = __popc(reached);
+      sh.warp_slots[warp] = upto;
+    }
+    __syncthreads();
+    int a = active0 + __popc(reached & ((1u << lane) - 1u)), slot = slots0 + upto - n;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) {
+        a += sh.warp_active[w];
+        slot += sh.warp_slots[w];
+      }
+      active0 += sh.warp_active[w];
+      slots0 += sh.warp_slots[w];
+    }
+    if (mask) {
+      sh.act_mask[a] = mask;
+      sh.act_expert[a] = uint16_t(e < p.shared ? p.experts + e : e - p.shared);
+      sh.act_base[a] = uint16_t(slot);
+      sh.position[e] = uint16_t(a);
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) sh.active = active0;
   // a token a lane, a route a warp
   for (int k = warp; lane < p.m && k < p.top_k + p.shared; k += WARPS) {
-    const int a = sh.position[k < p.top_k ? sh.chosen[lane][k] : p.experts + k - p.top_k];
-    const int slot = sh.act_base[a] + __popc(sh.act_mask[a] & ((1u << lane) - 1u));
-    sh.slot_weight[slot] = k < p.top_k ? sh.chosen_weight[lane][k] : 1.f;
+    const int a = sh.position[k < p.top_k ? p.shared + sh.route_expert[lane][k] : k - p.top_k];
+    sh.route_slot[lane][k] = int16_t(sh.act_base[a] + __popc(sh.act_mask[a] & ((1u << lane) - 1u)));
   }
   __syncthreads();
 }
@@ -456,36 +467,19 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&d)[COLS]) {
 
 __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits); }
 
-// Sums of the k blocks [kb0, kb1) of a tile for this thread's row and CT
-// columns' tokens (P pieces each): block sums from the accumulator ring,
-// their pieces added, times the weight's block scale
-// and, where `act` is given, the activation's (`count` of them a block,
-// `act_step` apart from block to block).  What lies beyond `count` is not
-// used.
+// Sums of an item's k blocks for this thread's row and CT columns' tokens (P
+// pieces each): block sums from the accumulator ring, their pieces added, times
+// the block's scale (8-bit weights): `scales` of m floats a block, the first
+// for all tokens (P = 2, `up`) or one a token (P = 3, `down`).  What lies
+// beyond the expert's tokens is not used.
 template <bool FP8, int P, int CT>
-__device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, Ring &ring, int kb0, int kb1, const float *sw,
-                                           int sw_count, const float *act, int act_step, int count,
-                                           float (&acc)[CT]) {
+__device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, Ring &ring, int blocks, const float *scales,
+                                           int m, float (&acc)[CT]) {
   constexpr int COLS = (CT * P + 15) / 16 * 16;
   const int lane = threadIdx.x % 32;
 #pragma unroll
   for (int t = 0; t < CT; ++t) acc[t] = 0.f;
-  float held = 0.f;     // lane l: the weight scale of block (kb & ~31) + l
-  // lane l: the activation scale of token l, one block ahead
-  float next = FP8 && act && lane < count ? __ldcg(act + size_t(kb0) * act_step + lane) : 0.f;
-  for (int kb = kb0; kb < kb1; ++kb) {
-    float scale = 1.f;
-    if (FP8) {
-      if (kb == kb0 || kb % 32 == 0) {
-        const int k = kb / 32 * 32 + lane;
-        held = k < sw_count ? __ldg(sw + k) : 0.f;
-      }
-      scale = __shfl_sync(0xffffffffu, held, kb % 32);
-      if (act) {
-        scale *= next;
-        if (kb + 1 < kb1 && lane < count) next = __ldcg(act + size_t(kb + 1) * act_step + lane);
-      }
-    }
+  for (int k = 0; k < blocks; ++k, scales += m) {
     tc::wait_or_abort(&sh.acc_full[ring.at], ring.phase, &sh.abort);
     __syncwarp();
     tc::fence_after_sync();
@@ -501,7 +495,7 @@ __device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, Ring 
         float v = value(d[P * t + P - 1]);
 #pragma unroll
         for (int c = P - 2; c >= 0; --c) v = fmaf(v, 0.0625f, value(d[P * t + c]));
-        acc[t] = fmaf(v, act ? __shfl_sync(0xffffffffu, scale, t) : scale, acc[t]);
+        acc[t] = fmaf(v, scales[P == 2 ? 0 : t], acc[t]);
       } else {
 #pragma unroll
         for (int c = 0; c < P; ++c) acc[t] += value(d[P * t + c]);
@@ -510,15 +504,15 @@ __device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, Ring 
   }
 }
 
-// Takes the sums of a tile's run for `count` tokens and gives token t's to
+// Takes the sums of an item for `count` tokens and gives token t's to
 // emit(t, sum); the width of the work follows the count.
 template <bool FP8, int P, class Emit>
-__device__ __forceinline__ void sum_tile(Shared &sh, uint32_t lane_base, Ring &ring, int kb0, int kb1, const float *sw,
-                                         int sw_count, const float *act, int act_step, int count, const Emit &emit) {
+__device__ __forceinline__ void sum_item(Shared &sh, uint32_t lane_base, Ring &ring, int blocks, const float *scales,
+                                         int m, int count, const Emit &emit) {
   auto with = [&](auto ct) {
     constexpr int CT = decltype(ct)::value;
     float acc[CT];
-    sum_blocks<FP8, P, CT>(sh, lane_base, ring, kb0, kb1, sw, sw_count, act, act_step, count, acc);
+    sum_blocks<FP8, P, CT>(sh, lane_base, ring, blocks, scales, m, acc);
 #pragma unroll
     for (int t = 0; t < CT; ++t)
       if (t < count) emit(t, acc[t]);
@@ -572,28 +566,27 @@ __device__ __forceinline__ float4 add4(const float4 &a, const float4 &b) {
 }
 __device__ __forceinline__ float4 ldcg4(const float *p) { return __ldcg(reinterpret_cast<const float4 *>(p)); }
 
-// A finished tile of an expert from the runs' pieces in scratch, added in the
-// order of the runs; a warp a token.
+// The sum of a row piece's chunks, `step` apart, in their order.
+__device__ __forceinline__ float4 add_chunks(const float *src, size_t step, int chunks) {
+  float4 v[MOE_CHUNKS];
+#pragma unroll
+  for (int c = 0; c < MOE_CHUNKS; ++c) v[c] = c < chunks ? ldcg4(src + c * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int c = 1; c < MOE_CHUNKS; ++c)
+    if (c < chunks) v[0] = add4(v[0], v[c]);
+  return v[0];
+}
+
+// A complete tile of an expert: its tokens' activations; one warp.
 template <bool FP8>
-__device__ __forceinline__ void finish_up(const MoeParams &p, int base, int count, int j, int up_tiles, int gate_pieces,
-                                          int up_pieces) {
-  const int warp = threadIdx.x / 32 - JOIN_WARP0, lane = threadIdx.x % 32;
-  const size_t width = size_t(up_tiles) * 128, step = size_t(p.slots) * 2 * width;
+__device__ __forceinline__ void finish_up(const MoeParams &p, const Shape &s, int base, int count, int j) {
+  const int lane = threadIdx.x % 32;
+  const size_t width = size_t(s.up_tiles) * 128, step = size_t(p.slots) * 2 * width;
 #pragma unroll 2
-  for (int t = warp; t < count; t += 4) {
+  for (int t = 0; t < count; ++t) {
     const float *src = p.scratch.up + size_t(base + t) * 2 * width + j * 128 + lane * 4;
-    float4 g[MOE_UP_FRAGMENTS], u[MOE_UP_FRAGMENTS];
-#pragma unroll
-    for (int f = 0; f < MOE_UP_FRAGMENTS; ++f) {
-      g[f] = f < gate_pieces ? ldcg4(src + f * step) : make_float4(0.f, 0.f, 0.f, 0.f);
-      u[f] = f < up_pieces ? ldcg4(src + f * step + width) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int f = 1; f < MOE_UP_FRAGMENTS; ++f) {
-      if (f < gate_pieces) g[0] = add4(g[0], g[f]);
-      if (f < up_pieces) u[0] = add4(u[0], u[f]);
-    }
-    store_act<FP8>(p, base + t, j, g[0], u[0]);
+    const float4 g = add_chunks(src, step, s.up_chunks), u = add_chunks(src + width, step, s.up_chunks);
+    store_act<FP8>(p, base + t, j, g, u);
   }
 }
 
@@ -609,10 +602,12 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   float *sums = reinterpret_cast<float *>(smem + SMEM_TABLES);   // two buffers [m][128] from the sums to the joins
   unsigned char *ring = smem + SMEM_TABLES + p.m * 1024;
+  // scales of the items in flight (8-bit weights)
+  float *scales = reinterpret_cast<float *>(ring + size_t(p.stages) * (A_BYTES + p.b_bytes) + SMEM_SLACK);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort = &sh.abort;
   const int stage_bytes = A_BYTES + p.b_bytes;
-  unsigned *routed = p.scratch.control, *ups_done = routed + 1, *exits = routed + 2;
+  unsigned *routed = p.scratch.control, *tickets = routed + 1, *downs_done = routed + 2, *exits = routed + 3;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -623,9 +618,12 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       tc::mbar_init(&sh.acc_full[i], 1);
       tc::mbar_init(&sh.acc_empty[i], 4);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sh.sum_full[i], 4);
-      tc::mbar_init(&sh.sum_empty[i], 4);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&sh.sum_full[i], 4);   // one a join warp
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.sum_empty[i], 1);  // one a buffer
+    for (int i = 0; i < ITEMS; ++i) {
+      tc::mbar_init(&sh.item_full[i], 1);
+      tc::mbar_init(&sh.item_empty[i], 11);   // scale, activation, MMA, four sum and four join warps
+      tc::mbar_init(&sh.scale_full[i], 1);
     }
     tc::mbar_init(&sh.drain, 1);
     tc::mbar_init_fence();
@@ -642,6 +640,10 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem;
+  const bool stall = g_stall_copies != 0;
+
+  for (int e = threadIdx.x; e < p.experts + p.shared; e += NT)
+    sh.mask[e] = e < p.shared ? (p.m == 32 ? 0xffffffffu : (1u << p.m) - 1u) : 0u;
 
   // ---- route
   route_logits(p, sh);
@@ -655,109 +657,185 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   }
   __syncthreads();
   const bool gave_up = *abort != 0;   // the same in all threads: no role has begun
-  build_plan(p, sh);
+  // The first items are the shared experts': their weights are requested while
+  // the experts are chosen (not before: the router's own reads would wait
+  // behind them).
+  int ahead = 0;   // blocks of this CTA's first item that are already requested
+  build_plan(p, sh, sums, [&]() {
+    if (warp != 0 || gave_up || int(blockIdx.x) >= p.shared * ((p.intermediate + 127) / 128) * 2 * p.up_chunks) return;
+    const Item it = item_at(shape_of<FP8>(p, p.shared), blockIdx.x);
+    ahead = min(it.blocks, p.stages);
+    if (!stall && tc::elect_one())
+      for (int k = 0; k < ahead; ++k) {
+        tc::mbar_arrive_expect_tx(&sh.full[k], A_BYTES);
+        tc::tma_load_2d(ring + size_t(k) * stage_bytes, &tm_gate_up, (it.kb0 + k) * KB,
+                        ((p.experts + it.a) * 2 + it.half) * p.intermediate + it.tile * 128, &sh.full[k]);
+      }
+    __syncwarp();
+  });
 
-  const Shape s = shape_of<FP8>(p);
   const int active = sh.active;
-  const Sequence up = up_sequence(s, active), down = down_sequence(s, active);
-  const int cta = blockIdx.x;
-  const int64_t up0 = up.begin(cta), up1 = up.begin(cta + 1), down0 = down.begin(cta), down1 = down.begin(cta + 1);
-  const int up_n = int(up1 - up0), down_n = int(down1 - down0);
-  UpCursor uc(s, up0);
-  DownCursor dc(s, active, down0);
-  const unsigned up_total = unsigned(active) * unsigned(s.up_tiles);
+  const Shape s = shape_of<FP8>(p, active);
+  const size_t up_width = size_t(s.up_tiles) * 128, down_width = size_t(s.down_tiles) * 128;
+
+  // the next item of this CTA, -1 after the last (and once a wait gave up)
+  Ring items;
+  auto next_item = [&]() {
+    const bool ok = tc::wait_or_abort(&sh.item_full[items.at], items.phase, abort);
+    if (!__all_sync(0xffffffffu, ok)) return -1;
+    const int item = sh.item[items.at];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sh.item_empty[items.at]);
+    items.next(ITEMS);
+    return item;
+  };
 
   if (gave_up) {
     // the logits never came: no role begins
   } else if (warp == 0) {
-    // ----------------------------------------------------- weight tiles
+    // ------------------------------------------- items and weight tiles
     Ring at;
-    int issued = 0;
-    bool ok = !g_stall_copies;
+    int issued = stall ? 0 : ahead, item = blockIdx.x;
+    bool ok = true;
     const bool leader = tc::elect_one();
-    auto load = [&](const CUtensorMap *map, int kb, int row, int blocks) {
-      for (int k = 0; k < blocks; ++k) {
-        ok = ok && tc::wait_or_abort(&sh.empty[at.at], at.phase ^ 1u, abort);
-        if (!ok) return;
-        if (leader) {
-          tc::mbar_arrive_expect_tx(&sh.full[at.at], A_BYTES);
-          tc::tma_load_2d(ring + size_t(at.at) * stage_bytes, map, (kb + k) * KB, row, &sh.full[at.at]);
-        }
-        __syncwarp();
-        at.next(p.stages);
-        ++issued;
+    while (true) {
+      ok = ok && tc::wait_or_abort(&sh.item_empty[items.at], items.phase ^ 1u, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      const bool live = ok && item < s.items;
+      if (lane == 0) {
+        sh.item[items.at] = live ? item : -1;
+        if (ok) tc::mbar_arrive(&sh.item_full[items.at]);
       }
-    };
-    for (int n = 0, run; n < up_n && ok; n += run) {
-      run = uc.run(s, up_n - n);
-      load(&tm_gate_up, uc.kb, (sh.act_expert[uc.a] * 2 + (uc.r & 1)) * p.intermediate + (uc.r >> 1) * 128, run);
-      uc.step(s, run);
+      if (!live) break;
+      items.next(ITEMS);
+      const Item it = item_at(s, item);
+      int next = 0;
+      if (lane == 0) next = int(atomicAdd(tickets, 1u) + gridDim.x);
+      const int e = sh.act_expert[it.a];
+      const int row = it.down ? e * p.hidden + it.tile * 128 : (e * 2 + it.half) * p.intermediate + it.tile * 128;
+      const CUtensorMap *map = it.down ? &tm_down : &tm_gate_up;
+      for (int k = 0; k < it.blocks && ok; ++k) {
+        if (ahead > 0) {
+          // already requested; no wait for the stage, which may have been
+          // released by now
+          --ahead;
+        } else {
+          ok = tc::wait_or_abort(&sh.empty[at.at], at.phase ^ 1u, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && leader && !stall) {
+            tc::mbar_arrive_expect_tx(&sh.full[at.at], A_BYTES);
+            tc::tma_load_2d(ring + size_t(at.at) * stage_bytes, map, (it.kb0 + k) * KB, row, &sh.full[at.at]);
+            ++issued;
+          }
+          __syncwarp();
+        }
+        at.next(p.stages);
+      }
+      item = __shfl_sync(0xffffffffu, next, 0);
     }
-    for (int n = 0, run; n < down_n && ok; n += run) {
-      run = dc.run(s, down_n - n);
-      load(&tm_down, dc.kb, sh.act_expert[dc.a] * p.hidden + dc.rb * 128, run);
-      dc.step(s, active, run);
-    }
-    if (lane == 0) sh.issued_a = issued;
+    if (leader) sh.issued_a = issued;
   } else if (warp == 3) {
     // ------------------------------------------------- activation tiles
     Ring at;
-    int issued = 0;
-    bool ok = !g_stall_copies;
-    // `copies` copies of a k block, one a lane, of `bytes` in all: this lane's
-    // from row `row` to byte `place` of the stage
-    auto load = [&](const CUtensorMap *map, int kb, int blocks, int copies, int bytes, int row, int place) {
-      for (int k = 0; k < blocks; ++k) {
-        ok = ok && tc::wait_or_abort(&sh.empty[at.at], at.phase ^ 1u, abort);
-        if (!ok) return;
-        if (lane == 0) tc::mbar_arrive_expect_tx(&sh.full[at.at], uint32_t(bytes));
-        __syncwarp();
-        if (lane < copies)
-          tc::tma_load_2d(ring + size_t(at.at) * stage_bytes + A_BYTES + place, map, (kb + k) * KB, row,
-                          &sh.full[at.at]);
-        __syncwarp();
-        at.next(p.stages);
-        ++issued;
-      }
-    };
+    int issued = 0, ready = 0;
+    bool ok = true;
     fence_proxy_async_global();
     const int x_rows = (p.m * XP + 7) / 8 * 8;
-    for (int n = 0, run; n < up_n && ok; n += run) {
-      run = uc.run(s, up_n - n);
-      const uint32_t mask = sh.act_mask[uc.a];
+    while (ok) {
+      const int item = next_item();
+      if (item < 0) break;
+      const Item it = item_at(s, item);
+      const uint32_t mask = sh.act_mask[it.a];
       const int count = __popc(mask);
-      // all tokens in one copy; else the expert's tokens only, a copy each:
-      // their rows' swizzle goes by their place in shared memory, as the
-      // tensor core reads them
-      if (count == p.m) load(&tm_x, uc.kb, run, 1, x_rows * 128, 0, 0);
-      else load(&tm_x_token, uc.kb, run, count, count * XP * 128, __fns(mask, 0, lane + 1) * XP, lane * XP * 128);
-      uc.step(s, run);
-    }
-    if (down_n > 0 && ok) {
-      ok = poll(ups_done, up_total, abort);
-      ok = __all_sync(0xffffffffu, ok);
-      fence_proxy_async_global();
-    }
-    for (int n = 0, run; n < down_n && ok; n += run) {
-      run = dc.run(s, down_n - n);
-      const int boxes = (__popc(sh.act_mask[dc.a]) * HP + 7) / 8;
-      load(&tm_act, dc.kb, run, boxes, boxes * 1024, sh.act_base[dc.a] * HP + lane * 8, lane * 1024);
-      dc.step(s, active, run);
+      // a block's copies, one a lane: all tokens in one; or the expert's tokens
+      // only, a copy each (their rows' swizzle goes by their place in shared
+      // memory, as the tensor core reads them); or the expert's activations
+      const CUtensorMap *map;
+      int copies, bytes, row, place;
+      if (it.down) {
+        if (ready <= it.a) {
+          ready = poll_experts(p.scratch.up_done, unsigned(s.up_tiles), ready, it.a + 1, active, abort);
+          ok = ready > it.a;
+          __syncwarp();
+          fence_proxy_async_global();
+        }
+        map = &tm_act;
+        copies = (count * HP + 7) / 8;
+        bytes = copies * 1024;
+        row = sh.act_base[it.a] * HP + lane * 8;
+        place = lane * 1024;
+      } else if (count == p.m) {
+        map = &tm_x;
+        copies = 1;
+        bytes = x_rows * 128;
+        row = place = 0;
+      } else {
+        map = &tm_x_token;
+        copies = count;
+        bytes = count * XP * 128;
+        row = lane < count ? int(__fns(mask, 0, lane + 1)) * XP : 0;
+        place = lane * XP * 128;
+      }
+      for (int k = 0; k < it.blocks && ok; ++k) {
+        ok = tc::wait_or_abort(&sh.empty[at.at], at.phase ^ 1u, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && !stall) {
+          if (lane == 0) tc::mbar_arrive_expect_tx(&sh.full[at.at], uint32_t(bytes));
+          __syncwarp();
+          if (lane < copies)
+            tc::tma_load_2d(ring + size_t(at.at) * stage_bytes + A_BYTES + place, map, (it.kb0 + k) * KB, row,
+                            &sh.full[at.at]);
+          ++issued;
+        }
+        __syncwarp();
+        at.next(p.stages);
+      }
     }
     if (lane == 0) sh.issued_b = issued;
+  } else if (warp == 2) {
+    // ----------------------------------------------------------- scales
+    // Read here, some items ahead: a read takes longer than several blocks.
+    int ready = 0;
+    while (true) {
+      const int slot = items.at, item = next_item();
+      if (item < 0) break;
+      if (!FP8) continue;
+      const Item it = item_at(s, item);
+      const int count = it.down ? __popc(sh.act_mask[it.a]) : 1, e = sh.act_expert[it.a];
+      const float *sw = it.down ? p.down_scales + (size_t(e) * s.down_tiles + it.tile) * s.down_k
+                                : p.gate_up_scales + ((size_t(e) * 2 + it.half) * s.up_tiles + it.tile) * s.up_k;
+      const float *act = p.scratch.act_scale + size_t(it.kb0) * p.slots + sh.act_base[it.a];
+      if (it.down && ready <= it.a) {
+        ready = poll_experts(p.scratch.up_done, unsigned(s.up_tiles), ready, it.a + 1, active, abort);
+        __syncwarp();
+      }
+      float *dst = scales + size_t(slot) * p.scale_blocks * p.m;
+      // blocks in lanes; all reads of a token are under way together
+      if (lane < it.blocks) {
+        const float w = __ldg(sw + it.kb0 + lane);
+#pragma unroll 4
+        for (int t = 0; t < count; ++t) dst[lane * p.m + t] = it.down ? w * __ldcg(act + size_t(lane) * p.slots + t) : w;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.scale_full[slot]);
+    }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA
     Ring at, acc;
     bool ok = true;
     const bool leader = tc::elect_one();
     const uint64_t a0 = tc::desc_sw128(ring), b0 = tc::desc_sw128(ring + A_BYTES);
-    auto multiply = [&](int columns, int blocks) {
-      const int cols = (columns + 15) / 16 * 16;
+    while (ok) {
+      const int item = next_item();
+      if (item < 0) break;
+      const Item it = item_at(s, item);
+      const int cols = (__popc(sh.act_mask[it.a]) * (it.down ? HP : XP) + 15) / 16 * 16;
       const uint32_t idesc = FP8 ? tc::idesc_e4m3_f32(128, cols) : tc::idesc_bf16_f32(128, cols);
-      for (int k = 0; k < blocks; ++k) {
-        ok = ok && tc::wait_or_abort(&sh.full[at.at], at.phase, abort) &&
+      for (int k = 0; k < it.blocks && ok; ++k) {
+        ok = tc::wait_or_abort(&sh.full[at.at], at.phase, abort) &&
              tc::wait_or_abort(&sh.acc_empty[acc.at], acc.phase ^ 1u, abort);
-        if (!ok) return;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc::fence_after_sync();
         const uint64_t step = uint64_t(at.at * (stage_bytes >> 4));
         const uint32_t d = tmem + uint32_t(acc.at * BUF_COLS);
@@ -774,16 +852,6 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
         at.next(p.stages);
         acc.next(BUFS);
       }
-    };
-    for (int n = 0, run; n < up_n && ok; n += run) {
-      run = uc.run(s, up_n - n);
-      multiply(__popc(sh.act_mask[uc.a]) * XP, run);
-      uc.step(s, run);
-    }
-    for (int n = 0, run; n < down_n && ok; n += run) {
-      run = dc.run(s, down_n - n);
-      multiply(__popc(sh.act_mask[dc.a]) * HP, run);
-      dc.step(s, active, run);
     }
     // no MMA is in flight when the tensor memory goes
     if (leader) tc::mma_commit(&sh.drain);
@@ -791,182 +859,128 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     tc::mbar_wait_bounded(&sh.drain, 0u, tc::SUB_WAIT_LIMIT);
   } else if (warp >= SUM_WARP0 && warp < JOIN_WARP0) {
     // ------------------------------------------------------------- sums
-    // After a wait gave up these warps and the joins go through the rest of
-    // their loops on whatever is there (the waits return at once), so that they
-    // meet at their barriers and every arrival is counted.
     const int i = threadIdx.x - SUM_WARP0 * 32;   // row of the tile
     const uint32_t lane_base = tmem + (uint32_t((warp % 4) * 32) << 16);
-    Ring acc;
-    int given = 0;
-    auto take = [&]() {   // the next buffer, once the joins have emptied it
-      if (given >= 2) tc::wait_or_abort(&sh.sum_empty[given % 2], uint32_t((given / 2 - 1) & 1), abort);
-      __syncwarp();
-      return sums + size_t(given % 2) * p.m * 128 + i;
-    };
-    auto give = [&]() {
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sh.sum_full[given % 2]);
-      ++given;
-    };
-    // ---- up
-    for (int n = 0, run; n < up_n; n += run) {
-      run = uc.run(s, up_n - n);
-      const float *sw = p.gate_up_scales +
-                        ((size_t(sh.act_expert[uc.a]) * 2 + (uc.r & 1)) * s.up_tiles + (uc.r >> 1)) * s.up_k;
-      uint32_t rest = sh.act_mask[uc.a];
-      float *dst = nullptr;
-      sum_tile<FP8, XP>(sh, lane_base, acc, uc.kb, uc.kb + run, sw, s.up_k, nullptr, 0, __popc(rest),
-                        [&](int t, float v) {
-                          if (t == 0) dst = take();
-                          if (FP8) {
-                            v *= sh.x_scale[__ffs(rest) - 1];
-                            rest &= rest - 1u;
-                          }
-                          dst[t * 128] = v;
-                        });
-      give();
-      uc.step(s, run);
-    }
-    // ---- down
-    if (down_n > 0) poll(ups_done, up_total, abort);
-    __syncwarp();
-    for (int n = 0; n < down_n;) {
-      const int rb = dc.rb;
-      float *y = take();
-      for (int t = 0; t < p.m; ++t) y[t * 128] = 0.f;
-      for (int run; n < down_n && dc.rb == rb; n += run) {
-        run = dc.run(s, down_n - n);
-        const int base = sh.act_base[dc.a];
-        const float *sw = p.down_scales + (size_t(sh.act_expert[dc.a]) * s.down_tiles + rb) * s.down_k;
-        uint32_t rest = sh.act_mask[dc.a];
-        sum_tile<FP8, HP>(sh, lane_base, acc, dc.kb, dc.kb + run, sw, s.down_k, p.scratch.act_scale + base, p.slots,
-                          __popc(rest), [&](int t, float v) {
-                            float *at = y + (__ffs(rest) - 1) * 128;
-                            rest &= rest - 1u;
-                            *at = fmaf(v, sh.slot_weight[base + t], *at);
-                          });
-        dc.step(s, active, run);
+    Ring acc, out, join;
+    while (true) {
+      const Ring from = items;
+      // the item's slot is given back after its scales are read
+      const bool ok = tc::wait_or_abort(&sh.item_full[from.at], from.phase, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int item = sh.item[from.at];
+      if (item < 0) break;
+      const Item it = item_at(s, item);
+      uint32_t rest = sh.act_mask[it.a];
+      const int count = __popc(rest);
+      float *dst = sums + size_t(out.at) * p.m * 128 + i;
+      const float *scale = scales + size_t(from.at) * p.scale_blocks * p.m;
+      if (FP8) {
+        tc::wait_or_abort(&sh.scale_full[from.at], from.phase, abort);
+        __syncwarp();
       }
-      give();
+      // emit(t, sum): into the buffer, once the joins have emptied it
+      auto emit = [&](int t, float v) {
+        if (t == 0) {
+          tc::wait_or_abort(&sh.sum_empty[out.at], out.phase ^ 1u, abort);
+          __syncwarp();
+        }
+        if (FP8 && !it.down) {
+          v *= sh.x_scale[__ffs(rest) - 1];
+          rest &= rest - 1u;
+        }
+        dst[t * 128] = v;
+      };
+      if (it.down) sum_item<FP8, HP>(sh, lane_base, acc, it.blocks, scale, p.m, count, emit);
+      else sum_item<FP8, XP>(sh, lane_base, acc, it.blocks, scale, p.m, count, emit);
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&sh.sum_full[join.at]);
+        tc::mbar_arrive(&sh.item_empty[from.at]);
+      }
+      out.next(2);
+      join.next(4);
+      items.next(ITEMS);
     }
   } else if (warp >= JOIN_WARP0) {
     // ------------------------------------------------------------ joins
+    // Each warp takes every fourth item: a join is a chain of accesses that
+    // other SMs must see, each of them microseconds long while the memory is
+    // busy, so four are under way at a time.
     const int jw = warp - JOIN_WARP0;
-    const size_t width = size_t(s.up_tiles) * 128;
-    int taken = 0;
-    auto wait_sum = [&](int k) {
-      tc::wait_or_abort(&sh.sum_full[k % 2], uint32_t((k / 2) & 1), abort);
+    for (int n = 0;; ++n) {
+      const int item = next_item();
+      if (item < 0) break;
+      if (n % 4 != jw) continue;
+      const Item it = item_at(s, item);
+      const int base = sh.act_base[it.a], count = __popc(sh.act_mask[it.a]);
+      tc::wait_or_abort(&sh.sum_full[jw], uint32_t(n / 4 & 1), abort);
       __syncwarp();
-      return sums + size_t(k % 2) * p.m * 128;
-    };
-    auto release = [&](int k) {
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sh.sum_empty[k % 2]);
-    };
-    // whether this run is the last of `want` to arrive at a counter, what all
-    // have written then being visible; the whole warps' threads call it
-    auto arrive = [&](unsigned *counter, unsigned want) {
-      __threadfence();
-      tc::named_barrier(1, 128);
-      if (threadIdx.x == JOIN_WARP0 * 32) {
-        const bool last = atomicAdd(counter, 1u) == want - 1;
-        if (last) *counter = 0;
-        sh.last = last;
-      }
-      tc::named_barrier(1, 128);
-      const bool last = sh.last != 0;
-      if (last) __threadfence();
-      return last;
-    };
-    // ---- up
-    for (int n = 0; n < up_n;) {
-      const int a = uc.a, r = uc.r, j = r >> 1;
-      const int base = sh.act_base[a], count = __popc(sh.act_mask[a]);
-      bool done = true;
-      if (!(r & 1) && uc.kb == 0 && n + 2 * s.up_k <= up_n) {
-        // gate and up of the tile lie in this run: no scratch
-        const float *g = wait_sum(taken), *u = wait_sum(taken + 1);
-        for (int t = jw; t < count; t += 4)
-          store_act<FP8>(p, base + t, j, reinterpret_cast<const float4 *>(g + t * 128)[lane],
-                         reinterpret_cast<const float4 *>(u + t * 128)[lane]);
-        release(taken);
-        release(taken + 1);
-        taken += 2;
-        n += 2 * s.up_k;
-        uc.r = r + 1;
-        uc.step(s, s.up_k);
+      const float *src = sums + size_t(n % 2) * p.m * 128;
+      float *dst;
+      size_t row;
+      if (!it.down) {
+        row = 2 * up_width;
+        dst = p.scratch.up + (size_t(it.chunk) * p.slots + base) * row + it.half * up_width + it.tile * 128;
       } else {
-        const int run = uc.run(s, up_n - n);
-        const int64_t u0 = (int64_t(a) * s.up_tiles + j) * 2 * s.up_k;
-        const int gate_pieces = up.pieces(u0, s.up_k), up_pieces = up.pieces(u0 + s.up_k, s.up_k);
-        const int piece = cta - up.run_of(u0 + (r & 1) * s.up_k);
-        float *dst = p.scratch.up + (size_t(piece) * p.slots + base) * 2 * width + (r & 1) * width + j * 128;
-        const float *src = wait_sum(taken);
-        for (int t = jw; t < count; t += 4)
-          __stcg(reinterpret_cast<float4 *>(dst + size_t(t) * 2 * width) + lane,
-                 reinterpret_cast<const float4 *>(src + t * 128)[lane]);
-        release(taken++);
-        done = arrive(p.scratch.up_counters + a * s.up_tiles + j, unsigned(gate_pieces + up_pieces));
-        if (done) finish_up<FP8>(p, base, count, j, s.up_tiles, gate_pieces, up_pieces);
-        n += run;
-        uc.step(s, run);
+        row = down_width;
+        dst = p.scratch.down + (size_t(it.chunk) * p.slots + base) * row + it.tile * 128;
       }
-      if (done) {
+#pragma unroll 4
+      for (int t = 0; t < count; ++t)
+        __stcg(reinterpret_cast<float4 *>(dst + size_t(t) * row) + lane,
+               reinterpret_cast<const float4 *>(src + t * 128)[lane]);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.sum_empty[n % 2]);
+      if (it.down) continue;
+      // a tile of `up` is complete with its last chunk
+      __threadfence();
+      __syncwarp();
+      unsigned there = 0, *counter = p.scratch.up_counters + it.a * s.up_tiles + it.tile;
+      if (lane == 0) there = atomicAdd(counter, 1u) + 1;
+      if (__shfl_sync(0xffffffffu, there, 0) == unsigned(2 * s.up_chunks)) {
+        __threadfence();
+        finish_up<FP8>(p, s, base, count, it.tile);
         fence_proxy_async_global();
         __threadfence();
-        tc::named_barrier(1, 128);
-        if (threadIdx.x == JOIN_WARP0 * 32) atomicAdd(ups_done, 1u);
+        __syncwarp();
+        if (lane == 0) {
+          *counter = 0;
+          atomicAdd(p.scratch.up_done + it.a, 1u);
+        }
       }
     }
-    // ---- down
-    const int64_t rb_units = int64_t(active) * s.down_k;
-    for (int64_t u = down0; u < down1;) {
-      const int rb = dc.rb;
-      const int64_t rb_u0 = rb * rb_units;
-      const int pieces = down.pieces(rb_u0, rb_units);
-      const float *src = wait_sum(taken);
-      // an item: a token's four neighbouring rows
-      const size_t step = size_t(s.down_tiles) * p.m * 128;
-      float *part = p.scratch.down + size_t(rb) * p.m * 128;
-      auto store_y = [&](int k, const float4 &y) {
-        const int row = rb * 128 + k % 32 * 4;   // hidden is a multiple of 8: four rows are in or out together
-        if (row < p.hidden) {
-          uint16_t *out = p.output + size_t(k / 32) * p.hidden + row;
-          const uint32_t lo = pack_bf16x2(y.x, y.y), hi = pack_bf16x2(y.z, y.w);
-          if (p.vector_out) {
-            *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
-          } else {
-            out[0] = uint16_t(lo);
-            out[1] = uint16_t(lo >> 16);
-            out[2] = uint16_t(hi);
-            out[3] = uint16_t(hi >> 16);
-          }
-        }
-      };
-      const int items = p.m * 32, first = threadIdx.x - JOIN_WARP0 * 32;
-      if (pieces == 1) {
-        for (int k = first; k < items; k += 128) store_y(k, reinterpret_cast<const float4 *>(src)[k]);
-        release(taken++);
+    __threadfence();
+  }
+  // ---- the output, once every CTA's sums are there: a warp a token's 128
+  // columns
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    atomicAdd(downs_done, 1u);
+    poll(downs_done, gridDim.x, abort);
+  }
+  __syncthreads();
+  __threadfence();
+  for (int n = blockIdx.x + warp * gridDim.x; n < p.m * s.down_tiles; n += gridDim.x * WARPS) {
+    const int t = n / s.down_tiles, col = (n - t * s.down_tiles) * 128 + lane * 4;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 5
+    for (int k = 0; k < p.top_k + p.shared; ++k) {
+      const float w = k < p.top_k ? sh.route_weight[t][k] : 1.f;
+      const float4 v = add_chunks(p.scratch.down + size_t(sh.route_slot[t][k]) * down_width + col,
+                                  size_t(p.slots) * down_width, s.down_chunks);
+      y = make_float4(fmaf(w, v.x, y.x), fmaf(w, v.y, y.y), fmaf(w, v.z, y.z), fmaf(w, v.w, y.w));
+    }
+    if (col < p.hidden) {   // hidden is a multiple of 8: four columns are in or out together
+      uint16_t *out = p.output + size_t(t) * p.hidden + col;
+      const uint32_t lo = pack_bf16x2(y.x, y.y), hi = pack_bf16x2(y.z, y.w);
+      if (p.vector_out) {
+        *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
       } else {
-        float *dst = part + (cta - down.run_of(rb_u0)) * step;
-        for (int k = first; k < items; k += 128)
-          __stcg(reinterpret_cast<float4 *>(dst) + k, reinterpret_cast<const float4 *>(src)[k]);
-        release(taken++);
-        if (arrive(p.scratch.down_counters + rb, unsigned(pieces)))
-#pragma unroll 2
-          for (int k = first; k < items; k += 128) {
-            float4 y[MOE_DOWN_FRAGMENTS];
-#pragma unroll
-            for (int f = 0; f < MOE_DOWN_FRAGMENTS; ++f)
-              y[f] = f < pieces ? ldcg4(part + f * step + size_t(k) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int f = 1; f < MOE_DOWN_FRAGMENTS; ++f)
-              if (f < pieces) y[0] = add4(y[0], y[f]);
-            store_y(k, y[0]);
-          }
+        out[0] = uint16_t(lo);
+        out[1] = uint16_t(lo >> 16);
+        out[2] = uint16_t(hi);
+        out[3] = uint16_t(hi >> 16);
       }
-      u = min(down1, rb_u0 + rb_units);
-      ++dc.rb;
     }
   }
   tc::fence_before_sync();
@@ -986,8 +1000,10 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     // the last CTA to leave puts the grid's counters back
     if (atomicAdd(exits, 1u) == gridDim.x - 1) {
       *routed = 0;
-      *ups_done = 0;
+      *tickets = 0;
+      *downs_done = 0;
       *exits = 0;
+      for (int a = 0; a < sh.active; ++a) p.scratch.up_done[a] = 0;
     }
   }
 }
@@ -1024,7 +1040,22 @@ cudaError_t launch_moe(const MoeParams &args, int sms, cudaStream_t stream) {
   const int every = p.experts + p.shared, elem = fp8 ? 1 : 2, kb = fp8 ? 128 : 64;
   const int xp = fp8 ? 2 : 1, hp = fp8 ? 3 : 2;
   p.b_bytes = (p.m * std::max(xp, hp) + 7) / 8 * 1024;
-  p.stages = std::min(STAGES_MAX, (SMEM_BYTES - SMEM_TABLES - SMEM_SLACK - p.m * 1024) / (A_BYTES + p.b_bytes));
+  // Chunks of a tile's k blocks: of about ten blocks (`up`) or six (`down`,
+  // whose last items decide when the kernel ends), or fewer blocks where the
+  // tiles of the experts that are reached at least do not give every CTA an
+  // item.
+  auto chunks = [&](int k, int blocks, int tiles) {
+    const int by_size = (k + blocks - 1) / blocks, by_ctas = std::min(sms / tiles, k / 2);
+    return std::max(1, std::min(MOE_CHUNKS, std::max(by_size, by_ctas)));
+  };
+  const int up_k = (p.hidden + kb - 1) / kb, down_k = (p.intermediate + kb - 1) / kb;
+  const int least = p.top_k + p.shared;
+  p.up_chunks = chunks(up_k, 10, least * qblocks(p.intermediate) * 2);
+  p.down_chunks = chunks(down_k, 6, least * qblocks(p.hidden));
+  p.scale_blocks = std::max((up_k + p.up_chunks - 1) / p.up_chunks, (down_k + p.down_chunks - 1) / p.down_chunks);
+  const int scale_bytes = fp8 ? ITEMS * p.scale_blocks * p.m * 4 : 0;
+  p.stages = std::min(STAGES_MAX, (SMEM_BYTES - SMEM_TABLES - SMEM_SLACK - p.m * 1024 - scale_bytes) /
+                                      (A_BYTES + p.b_bytes));
   p.vector_out = reinterpret_cast<uintptr_t>(p.output) % 8 == 0;
   const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t H = p.hidden, I = p.intermediate;

@@ -77,25 +77,21 @@ constexpr int MOE_TOKENS_MAX = 32;
 constexpr int MOE_EXPERTS_MAX = 512;
 constexpr int MOE_SHARED_MAX = 8;
 constexpr int MOE_TOPK_MAX = 16;
-// Pieces of a row of sums that its work items leave in scratch: at most
-// MOE_UP_FRAGMENTS for a tile of the gate and up products, MOE_DOWN_FRAGMENTS
-// for a row block of the output.
-constexpr int MOE_UP_FRAGMENTS = 3;
-constexpr int MOE_DOWN_SPLIT = 8;
-constexpr int MOE_DOWN_FRAGMENTS = MOE_DOWN_SPLIT + 1;
+// Chunks of k blocks that a tile's work is cut into, at most.
+constexpr int MOE_CHUNKS = 4;
 
 // Scratch of one MoE handle, by its capacity.
 struct MoeScratch {
-  unsigned int *control;      // MOE_CONTROL words: grid counters, zero between calls
-  unsigned int *up_counters;  // [active experts][I / 128]
-  unsigned int *down_counters;// [H / 128]
+  unsigned int *control;      // MOE_CONTROL words: grid counters (all counters are zero between calls)
+  unsigned int *up_counters;  // [reached experts][I / 128] chunks of a tile that are there
+  unsigned int *up_done;      // [reached experts] complete tiles
   float *logits;              // [tokens][E]
   uint8_t *x_pieces;          // [2 tokens][H] e4m3 (8-bit weights)
   float *x_scale;             // [tokens]
-  float *up;                  // [MOE_UP_FRAGMENTS][slots][2][I rounded up to 128]
+  float *up;                  // [MOE_CHUNKS][slots][2][I rounded up to 128]
   void *act;                  // [slots * pieces][I]: e4m3 x 3 or bf16 x 2
   float *act_scale;           // [I / 128][slots] (8-bit weights)
-  float *down;                // [MOE_DOWN_FRAGMENTS][H / 128][tokens][128]
+  float *down;                // [MOE_CHUNKS][slots][H rounded up to 128]
 };
 constexpr int MOE_CONTROL = 4;
 
@@ -116,6 +112,8 @@ struct MoeParams {
   unsigned int *err;
   // set by the launcher
   int stages, b_bytes;
+  int up_chunks, down_chunks; // chunks of a tile's k blocks
+  int scale_blocks;           // k blocks of an item at most
   int vector_out;             // the output starts on an 8-byte boundary
 };
 

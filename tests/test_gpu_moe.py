@@ -284,3 +284,18 @@ def test_stalled_copies_report_a_timeout_and_the_handle_recovers(fp8):
     for name in good:
         assert torch.equal(good[name], again[name])
     c.layer.check_errors()
+
+
+def test_many_calls_one_after_another():
+    """The shapes that keep every part of the pipeline busy, many times: the
+    CTAs' order in time changes, the result may not."""
+    for args in ((1, 5120, 2048, 16, 1, 8, True), (32, 1024, 1024, 32, 1, 8, True), (5, 1024, 512, 16, 0, 2, False)):
+        c = Case(*args)
+        first = c.run()
+        out = c.layer.empty_outputs("moe", c.m)
+        for _ in range(20):
+            for _ in range(25):
+                c.layer.moe(c.inputs, out)
+            for name in first:
+                assert torch.equal(first[name], out[name])
+        c.layer.check_errors()
