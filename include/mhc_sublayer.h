@@ -25,9 +25,9 @@
  * Matrices are row-major with contiguous rows; a *_stride is the distance of
  * two rows in elements.  BF16 and 8-bit rows start on 16-byte boundaries.
  * Calls with m = 0 succeed and launch nothing (but for moe, whose m is in
- * [1, max_moe_tokens]).  A handle owns scratch that its matmul and moe calls
- * use: its calls run one after another, on one stream or on streams that the
- * caller orders.
+ * [1, max_moe_tokens]).  A handle owns scratch that its moe calls use: its
+ * calls run one after another, on one stream or on streams that the caller
+ * orders.
  */
 #ifndef MHC_SUBLAYER_H
 #define MHC_SUBLAYER_H

@@ -20,11 +20,7 @@ struct mhc_sublayer {
   int device = 0;
   int sm_count = 0;
   unsigned int *err = nullptr;       // device error word
-  // matmul: FP32 sums of split tiles (at most one 128 x 128 tile for each
-  // SM) and the tiles' arrival counters
-  float *scratch = nullptr;
-  size_t scratch_floats = 0;
-  unsigned int *counters = nullptr;
+  MatmulPlan matmul = {};
   // moe (num_experts > 0): its scratch, in one allocation
   MoeScratch moe = {};
   unsigned char *moe_base = nullptr;
@@ -153,8 +149,6 @@ size_t moe_layout(mhc_sublayer_t *s) {
 void release(mhc_sublayer_t *s) {
   if (s->moe_base) cudaFree(s->moe_base);
   if (s->err) cudaFree(s->err);
-  if (s->scratch) cudaFree(s->scratch);
-  if (s->counters) cudaFree(s->counters);
 }
 
 }  // namespace
@@ -194,13 +188,9 @@ mhc_status_t mhc_sublayer_create(const mhc_sublayer_config_t *config, int device
   s->cfg = c;
   s->device = device;
   cudaError_t e = cudaDeviceGetAttribute(&s->sm_count, cudaDevAttrMultiProcessorCount, device);
-  if (e == cudaSuccess) e = matmul_set_attributes();
+  if (e == cudaSuccess) e = matmul_setup(s->sm_count, &s->matmul);
   if (e == cudaSuccess) e = cudaMalloc(&s->err, sizeof(unsigned int));
   if (e == cudaSuccess) e = cudaMemset(s->err, 0, sizeof(unsigned int));
-  s->scratch_floats = size_t(s->sm_count) * QBLOCK * QBLOCK;
-  if (e == cudaSuccess) e = cudaMalloc(&s->scratch, s->scratch_floats * sizeof(float));
-  if (e == cudaSuccess) e = cudaMalloc(&s->counters, size_t(s->sm_count) * sizeof(unsigned int));
-  if (e == cudaSuccess) e = cudaMemset(s->counters, 0, size_t(s->sm_count) * sizeof(unsigned int));
   if (e == cudaSuccess && c.num_experts > 0) {
     e = moe_set_attributes();
     if (e == cudaSuccess) e = cudaMalloc(&s->moe_base, moe_layout(s));
@@ -303,12 +293,8 @@ mhc_status_t mhc_sublayer_matmul(mhc_sublayer_t *s, const mhc_sublayer_matmul_ar
   p.output_f32 = a->output_f32 != 0;
   const int64_t row_step = a->output_f32 ? 4 : 8;
   p.vector_out = reinterpret_cast<uintptr_t>(a->output) % 16 == 0 && a->output_stride % row_step == 0;
-  p.scratch = s->scratch;
-  p.scratch_floats = s->scratch_floats;
-  p.counters = s->counters;
-  p.counter_count = s->sm_count;
   p.err = s->err;
-  return launched(s, launch_block_matmul(p, s->sm_count, reinterpret_cast<cudaStream_t>(stream)), "matmul");
+  return launched(s, launch_block_matmul(p, s->matmul, reinterpret_cast<cudaStream_t>(stream)), "matmul");
 }
 
 mhc_status_t mhc_sublayer_moe(mhc_sublayer_t *s, const mhc_sublayer_moe_args_t *a, mhc_stream_t stream) {
@@ -367,7 +353,6 @@ mhc_status_t mhc_sublayer_check_errors(mhc_sublayer_t *s) {
   if (e == cudaSuccess && flag) {
     // a call that gave up leaves its arrival counters half way
     e = cudaMemset(s->err, 0, sizeof flag);
-    if (e == cudaSuccess) e = cudaMemset(s->counters, 0, size_t(s->sm_count) * sizeof(unsigned int));
     if (e == cudaSuccess && s->moe_base) e = cudaMemset(s->moe_base, 0, s->moe_counter_bytes);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
   }

@@ -3,22 +3,24 @@
 //   out[m][n] = sum_kb sa[m][kb] sw[n/128][kb] * sum_{k in kb} a[m][k] w[n][k]
 //
 // The inner sums (128 E4M3 products) run on the tensor cores into tensor
-// memory; the scaled outer sum runs in FP32 registers.  A CTA's tile is 128
-// rows of `a` (a TMEM lane each, so the row's scale is one register of one
-// thread) by BN rows of `w`; an epilogue warp group owns 128 (BN = 256) or 64
-// columns, so the weight's scale is one value for all of them, and the outer
-// sum is one packed FP32 fused multiply-add for every two elements and block.
+// memory; the scaled outer sum runs in FP32 registers.  A row of `a` is a TMEM
+// lane, so its scale is one register of one thread, and the columns of an
+// epilogue warp lie in one block of `w`, so the outer sum is one packed FP32
+// fused multiply-add for every two elements and block.
 //
-// Roles (12 warps): TMA producer, MMA issuer, TMEM owner, and eight epilogue
-// warps (two per TMEM sub-partition).  Operands arrive in a ring of stages of
-// one k block (128 bytes a row, 128-byte swizzled); the accumulator is a ring
-// of 512 / BN buffers, so the tensor cores work on one block while the
+// Two kernels share this.  Few rows, where the read of `w` bounds the call: a
+// tile of 128 rows x BN columns a cluster, its k blocks cut over the cluster's
+// CTAs, whose sums meet through distributed shared memory (no scratch, and the
+// order of addition is that of the ranks).  Many rows, where the tensor cores
+// do: a pair of CTAs works on a tile of 256 x 256 with cta_group::2 MMAs, each
+// CTA loading half of both operands, persistent over the tiles.
+//
+// Roles (12 warps): 0 operand copies, 1 MMA, 2-3 scales (read some blocks ahead
+// into shared memory: a read takes longer than a block's products), 4-11
+// epilogue, two warps for each TMEM sub-partition.  Operands arrive in a ring of
+// stages of one k block (128 bytes a row, 128-byte swizzled); the accumulator
+// is a ring of buffers, so the tensor cores work on one block while the
 // epilogue warps add the one before.
-//
-// Few tiles: each tile's k blocks are split over `splits` work items.  Every
-// item then writes its FP32 sums to scratch, and the last of a tile's items
-// to arrive adds them in split order, so the result does not depend on the
-// order of arrival.
 #include <algorithm>
 
 #include "sublayer.cuh"
@@ -27,51 +29,292 @@
 namespace mhc {
 namespace {
 
-constexpr int BM = 128;
+constexpr int BM = 128;                  // rows of a CTA
 constexpr int NT = 384;
-constexpr int EPI_WARP0 = 4, EPI_THREADS = 256;
+constexpr int SCALE_WARP0 = 2, EPI_WARP0 = 4, EPI_WARPS = 8;
 constexpr int STAGES_MAX = 12;
+constexpr int CHUNK = 8, CHUNKS = 4;     // k blocks of a chunk of scales, chunks in flight
 constexpr int SMEM_CTRL = 1024;
+constexpr int SMEM_SCALES = CHUNKS * CHUNK * (BM + 2) * 4 + 1024;   // and the ring's alignment
 constexpr int SMEM_BYTES = 227 * 1024;
+constexpr int RING_BYTES = (SMEM_BYTES - SMEM_CTRL - SMEM_SCALES) / 1024 * 1024;
 
 __device__ int g_stall_copies;   // test hook: the producer issues no copies
 
 struct Control {
-  uint64_t full[STAGES_MAX], empty[STAGES_MAX], acc_full[4], acc_empty[4], drain;
+  uint64_t full[STAGES_MAX], empty[STAGES_MAX], peer_full[STAGES_MAX], acc_full[4], acc_empty[4];
+  uint64_t scale_full[CHUNKS], scale_empty[CHUNKS], drain;
   uint32_t tmem;
-  int abort, last;
+  int abort;
 };
 static_assert(sizeof(Control) <= SMEM_CTRL, "control block");
 
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_peer(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void arrive_peer(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A wait for arrivals of the other CTA: acquire at cluster scope.
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(tc::smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __noinline__ bool wait_cluster_poll(uint64_t *bar, uint32_t parity, volatile int *abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < tc::SUB_WAIT_LIMIT; ++i) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if (*abort) return false;
+    if (i > 64) __nanosleep(64);
+  }
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  return try_wait_cluster(bar, parity) || wait_cluster_poll(bar, parity, abort);
+}
+
+// ------------------------------------------------- cta_group::2 instructions
+__device__ __forceinline__ void tmem_alloc2(uint32_t *slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_addr(slot)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma2_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// One arrival on the barrier at this place in both CTAs of the pair.
+__device__ __forceinline__ void mma2_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          tc::smem_addr(bar)),
+      "h"((unsigned short)3)
+      : "memory");
+}
+
+// A place in a ring of barriers and the phase of its current round; a producer
+// waits for a slot's release with the other parity, which returns at once in
+// the first round.
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ void next(int size) {
+    if (++at == size) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Scales of the k blocks [kb0, kb1): [block][row] of this CTA's rows, and the
+// weight's [block][2]; one of the two scale warps writes 64 rows.
+struct Scales {
+  float *a;   // [CHUNKS][CHUNK][BM]
+  float *w;   // [CHUNKS][CHUNK][2]
+};
+
+__device__ __forceinline__ void load_scales(const MatmulParams &p, Control &c, const Scales &sc, Ring &ring, int m0,
+                                            int n_block, int kb0, int kb1, int warp, int lane) {
+  volatile int *abort = &c.abort;
+  for (int kb = kb0; kb < kb1; kb += CHUNK) {
+    tc::wait_or_abort(&c.scale_empty[ring.at], ring.phase ^ 1u, abort);
+    __syncwarp();
+    float *a = sc.a + ring.at * CHUNK * BM, *w = sc.w + ring.at * CHUNK * 2;
+    float v[2][CHUNK];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = m0 + warp * 64 + h * 32 + lane;
+      const float *src = p.scales + size_t(row < p.m ? row : 0) * p.scales_stride + kb;
+#pragma unroll
+      for (int k = 0; k < CHUNK; ++k) v[h][k] = row < p.m && kb + k < kb1 ? __ldg(src + k) : 0.f;
+    }
+    // lane 8 b + k: block n_block + b
+    float sw = 0.f;
+    if (warp == 0 && lane < 2 * CHUNK && kb + lane % CHUNK < kb1)
+      sw = __ldg(p.weight_scales + size_t(min(n_block + lane / CHUNK, p.n_blocks - 1)) * p.k_blocks + kb + lane % CHUNK);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < CHUNK; ++k) a[k * BM + warp * 64 + h * 32 + lane] = v[h][k];
+    if (warp == 0 && lane < 2 * CHUNK) w[lane % CHUNK * 2 + lane / CHUNK] = sw;
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&c.scale_full[ring.at]);
+    ring.next(CHUNKS);
+  }
+}
+
+// Adds the scaled block sums of `blocks` k blocks to acc: NC columns of this
+// thread's row, from TMEM columns `col` of each accumulator buffer of
+// buf_cols; `released` tells the MMA warp that a buffer is read.
+template <int NC, class Release>
+__device__ __forceinline__ void add_blocks(Control &c, const Scales &sc, Ring &acc_ring, Ring &scale_ring, int bufs,
+                                           int buf_cols, uint32_t taddr, int row, int w_block, int blocks, bool rows_live,
+                                           int lane, const Release &release, uint64_t (&acc)[NC / 2]) {
+  volatile int *abort = &c.abort;
+  for (int k = 0; k < blocks; ++k) {
+    const int in_chunk = k % CHUNK;
+    if (in_chunk == 0) {
+      tc::wait_or_abort_inline(&c.scale_full[scale_ring.at], scale_ring.phase, abort);
+      __syncwarp();
+    }
+    const int at = scale_ring.at * CHUNK + in_chunk;
+    const float scale = sc.a[at * BM + row] * sc.w[at * 2 + w_block];
+    if (in_chunk == CHUNK - 1 || k == blocks - 1) {
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&c.scale_empty[scale_ring.at]);
+      scale_ring.next(CHUNKS);
+    }
+    tc::wait_or_abort_inline(&c.acc_full[acc_ring.at], acc_ring.phase, abort);
+    __syncwarp();
+    tc::fence_after_sync();
+    if (rows_live) {
+      const uint64_t s2 = tc::pair(scale, scale);
+      const uint32_t src = taddr + uint32_t(acc_ring.at * buf_cols);
+      constexpr int STEP = NC > 64 ? 32 : NC;   // what the registers beside acc hold
+#pragma unroll
+      for (int h = 0; h < NC; h += STEP) {
+        uint32_t d[STEP / 32][32];
+#pragma unroll
+        for (int q = 0; q < STEP / 32; ++q) tc::tmem_ld32_async(src + uint32_t(h + q * 32), d[q]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < STEP / 32; ++q) tc::tmem_hold(d[q]);
+        if (h + STEP == NC) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) release(acc_ring.at);
+        }
+#pragma unroll
+        for (int q = 0; q < STEP / 32; ++q)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            tc::fma_pair(acc[h / 2 + q * 16 + i], d[q][2 * i], d[q][2 * i + 1], s2);
+      }
+    } else if (lane == 0) {
+      release(acc_ring.at);
+    }
+    acc_ring.next(bufs);
+  }
+}
+
+// Eight neighbouring columns of a row to the output.
+__device__ __forceinline__ void store8(const MatmulParams &p, int row, int col, const float (&v)[8]) {
+  const size_t at = size_t(row) * p.output_stride + col;
+  const bool whole = p.vector_out && col + 8 <= p.n;
+  if (p.output_f32) {
+    float *out = static_cast<float *>(p.output) + at;
+    if (whole) {
+      reinterpret_cast<float4 *>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4 *>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (col + k < p.n) out[k] = v[k];
+    }
+  } else {
+    uint16_t *out = static_cast<uint16_t *>(p.output) + at;
+    const uint4 w = pack8(v);
+    if (whole) {
+      st_vec(out, w);
+    } else {
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (col + k < p.n) out[k] = uint16_t(u[k / 2] >> (k % 2 * 16));
+    }
+  }
+}
+
+template <int NC>
+__device__ __forceinline__ void store_row(const MatmulParams &p, int row, int col, const uint64_t (&acc)[NC / 2]) {
+#pragma unroll
+  for (int i = 0; i < NC / 2; i += 4) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = tc::pair_lo(acc[i + k]);
+      v[2 * k + 1] = tc::pair_hi(acc[i + k]);
+    }
+    if (col + 2 * i < p.n) store8(p, row, col + 2 * i, v);
+  }
+}
+
+__device__ __forceinline__ void init_control(Control &c, int stages, int bufs, uint32_t acc_empty_count) {
+  for (int i = 0; i < stages; ++i) {
+    tc::mbar_init(&c.full[i], 1);
+    tc::mbar_init(&c.empty[i], 1);
+    tc::mbar_init(&c.peer_full[i], 1);
+  }
+  for (int i = 0; i < bufs; ++i) {
+    tc::mbar_init(&c.acc_full[i], 1);
+    tc::mbar_init(&c.acc_empty[i], acc_empty_count);
+  }
+  for (int i = 0; i < CHUNKS; ++i) {
+    tc::mbar_init(&c.scale_full[i], 2);
+    tc::mbar_init(&c.scale_empty[i], EPI_WARPS);
+  }
+  tc::mbar_init(&c.drain, 1);
+  tc::mbar_init_fence();
+  c.abort = 0;
+}
+
+// ------------------------------------------------------------ split kernel
+// Cluster `tile` of p.splits CTAs: BM rows by BN columns, CTA r the k blocks
+// [k_blocks r / splits, k_blocks (r + 1) / splits).
 template <int BN>
 __global__ void __launch_bounds__(NT, 1)
-k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w) {
-  constexpr int BUFS = 512 / BN;
+k_matmul_split(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w) {
+  constexpr int BUFS = 4;
   constexpr int NC = BN / 2;             // columns of an epilogue warp group
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char *smem = smem_raw;
+  extern __shared__ __align__(1024) unsigned char smem[];
   Control &c = *reinterpret_cast<Control *>(smem);
   unsigned char *ring = smem + SMEM_CTRL;
+  const Scales sc = {reinterpret_cast<float *>(ring + RING_BYTES),
+                     reinterpret_cast<float *>(ring + RING_BYTES) + CHUNKS * CHUNK * BM};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort = &c.abort;
   const int a_bytes = p.a_rows * 128, stage_bytes = a_bytes + BN * 128;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      tc::mbar_init(&c.full[i], 1);
-      tc::mbar_init(&c.empty[i], 1);
-    }
-    for (int i = 0; i < BUFS; ++i) {
-      tc::mbar_init(&c.acc_full[i], 1);
-      tc::mbar_init(&c.acc_empty[i], EPI_THREADS / 32);
-    }
-    tc::mbar_init(&c.drain, 1);
-    tc::mbar_init_fence();
-    c.abort = 0;
+    init_control(c, p.stages, BUFS, EPI_WARPS);
     tc::tma_prefetch_desc(&tm_a);
     tc::tma_prefetch_desc(&tm_w);
   }
-  if (warp == 2) tc::tmem_alloc(&c.tmem, 512);
+  if (warp == SCALE_WARP0) tc::tmem_alloc(&c.tmem, BUFS * BN);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -79,248 +322,351 @@ k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
   pdl_wait();
   pdl_launch_dependents();
 
-  const int items = p.m_tiles * p.n_tiles * p.splits;
+  const int rank = p.splits > 1 ? int(cluster_rank()) : 0, tile = int(blockIdx.x) / p.splits;
+  const int m0 = tile % p.m_tiles * BM, n0 = tile / p.m_tiles * BN;
+  const int kb0 = p.k_blocks * rank / p.splits, kb1 = p.k_blocks * (rank + 1) / p.splits;
+  const int rows = min(BM, p.m - m0);    // of the tile
+
   if (warp == 0) {
     // ---------------------------------------------------------- producer
-    int n = 0;
-    bool ok = !g_stall_copies;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const WorkItem w = work_item(p, item);
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++n) {
-        const int s = n % p.stages;
-        if (n >= p.stages && !tc::wait_or_abort(&c.empty[s], uint32_t((n / p.stages - 1) & 1), abort)) {
-          ok = false;
-          break;
-        }
-        if (tc::elect_one()) {
-          unsigned char *dst = ring + size_t(s) * stage_bytes;
-          tc::mbar_arrive_expect_tx(&c.full[s], uint32_t(stage_bytes));
-          tc::tma_load_2d(dst, &tm_a, kb * 128, w.m0, &c.full[s]);
-          tc::tma_load_2d(dst + a_bytes, &tm_w, kb * 128, w.n_tile * BN, &c.full[s]);
+    Ring at;
+    bool ok = true;
+    const bool leader = tc::elect_one();
+    int issued = 0;
+    if (!g_stall_copies)
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = tc::wait_or_abort(&c.empty[at.at], at.phase ^ 1u, abort);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (leader) {
+          unsigned char *dst = ring + size_t(at.at) * stage_bytes;
+          tc::mbar_arrive_expect_tx(&c.full[at.at], uint32_t(stage_bytes));
+          tc::tma_load_2d(dst + a_bytes, &tm_w, kb * 128, n0, &c.full[at.at]);
+          tc::tma_load_2d(dst, &tm_a, kb * 128, m0, &c.full[at.at]);
         }
         __syncwarp();
+        at.next(p.stages);
+        ++issued;
       }
-    }
     // copies in flight land before the CTA's shared memory goes
     if (*abort)
-      for (int i = max(0, n - p.stages); i < n; ++i)
+      for (int i = max(0, issued - p.stages); i < issued; ++i)
         tc::mbar_wait_bounded(&c.full[i % p.stages], uint32_t((i / p.stages) & 1), tc::SUB_WAIT_LIMIT);
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer
+    Ring at, acc;
+    const bool leader = tc::elect_one();
     const uint32_t idesc = tc::idesc_e4m3_f32(BM, BN);
-    int n = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const WorkItem w = work_item(p, item);
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++n) {
-        const int s = n % p.stages, b = n % BUFS;
-        ok = tc::wait_or_abort(&c.full[s], uint32_t((n / p.stages) & 1), abort) &&
-             (n < BUFS || tc::wait_or_abort(&c.acc_empty[b], uint32_t((n / BUFS - 1) & 1), abort));
-        if (!ok) break;
-        tc::fence_after_sync();
-        const unsigned char *src = ring + size_t(s) * stage_bytes;
-        const uint64_t ad = tc::desc_sw128(src), bd = tc::desc_sw128(src + a_bytes);
-        if (tc::elect_one()) {
+    const uint64_t a0 = tc::desc_sw128(ring), b0 = tc::desc_sw128(ring + a_bytes);
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const bool ok = tc::wait_or_abort(&c.full[at.at], at.phase, abort) &&
+                      tc::wait_or_abort(&c.acc_empty[acc.at], acc.phase ^ 1u, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc::fence_after_sync();
+      const uint64_t step = uint64_t(at.at * (stage_bytes >> 4));
+      if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc::mma_e4m3(tmem + uint32_t(b * BN), ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
-          tc::mma_commit(&c.empty[s]);
-          tc::mma_commit(&c.acc_full[b]);
-        }
-        __syncwarp();
+        for (int ks = 0; ks < 4; ++ks)
+          tc::mma_e4m3(tmem + uint32_t(acc.at * BN), a0 + step + 2 * ks, b0 + step + 2 * ks, idesc, ks != 0);
+        tc::mma_commit(&c.empty[at.at]);
+        tc::mma_commit(&c.acc_full[acc.at]);
       }
+      __syncwarp();
+      at.next(p.stages);
+      acc.next(BUFS);
     }
     // no MMA is in flight when the tensor memory goes
-    if (tc::elect_one()) tc::mma_commit(&c.drain);
+    if (leader) tc::mma_commit(&c.drain);
     __syncwarp();
     tc::mbar_wait_bounded(&c.drain, 0u, tc::SUB_WAIT_LIMIT);
-  } else if (warp >= EPI_WARP0) {
+  } else if (warp < EPI_WARP0) {
+    Ring scales;
+    load_scales(p, c, sc, scales, m0, n0 / QBLOCK, kb0, kb1, warp - SCALE_WARP0, lane);
+  } else {
     // ---------------------------------------------------------- epilogue
     // After a wait gave up these warps go through the rest of their loops on
-    // whatever is there (the waits return at once), so that they meet at their
-    // barriers and every arrival is counted.
-    const int sub = warp % 4, group = (warp - EPI_WARP0) / 4;
-    const uint32_t lane_base = tmem + (uint32_t(sub * 32) << 16) + uint32_t(group * NC);
-    const int epi_tid = threadIdx.x - EPI_WARP0 * 32;
-    int n = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-      const WorkItem w = work_item(p, item);
-      const int row = w.m0 + sub * 32 + lane;
-      const int n0 = w.n_tile * BN + group * NC;
-      const bool rows_live = w.m0 + sub * 32 < p.m, live = row < p.m;
-      const float *sa = p.scales + size_t(live ? row : 0) * p.scales_stride;
-      const float *sw = p.weight_scales + size_t(min(n0 / QBLOCK, p.n_blocks - 1)) * p.k_blocks;
-      uint64_t acc[NC / 2];
+    // whatever is there (the waits return at once).
+    const int sub = warp % 4, group = (warp - EPI_WARP0) / 4, r = sub * 32 + lane;
+    const int col = group * NC;
+    Ring acc_ring, scale_ring;
+    uint64_t acc[NC / 2];
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
-      float a_next = __ldg(sa + w.kb0), w_next = __ldg(sw + w.kb0);
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++n) {
-        const int b = n % BUFS;
-        const float scale = a_next * w_next;
-        if (kb + 1 < w.kb1) {
-          a_next = __ldg(sa + kb + 1);
-          w_next = __ldg(sw + kb + 1);
-        }
-        tc::wait_or_abort(&c.acc_full[b], uint32_t((n / BUFS) & 1), abort);
-        __syncwarp();
-        tc::fence_after_sync();
-        if (rows_live) {
-          const uint64_t s2 = tc::pair(scale, scale);
+    for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
+    add_blocks<NC>(c, sc, acc_ring, scale_ring, BUFS, BN, tmem + (uint32_t(sub * 32) << 16) + uint32_t(col), r, 0,
+                   kb1 - kb0, sub * 32 < rows, lane, [&](int b) { tc::mbar_arrive(&c.acc_empty[b]); }, acc);
+    if (p.splits == 1) {
+      if (r < rows) store_row<NC>(p, m0 + r, n0 + col, acc);
+    } else if (r < rows) {
+      // every MMA has completed, so the stages are free: [column][row]
+      float *part = reinterpret_cast<float *>(ring) + size_t(col) * p.a_rows + r;
 #pragma unroll
-          for (int h = 0; h < NC; h += 64) {
-            uint32_t d0[32], d1[32];
-            tc::tmem_ld32_async(lane_base + uint32_t(b * BN + h), d0);
-            tc::tmem_ld32_async(lane_base + uint32_t(b * BN + h + 32), d1);
-            tc::tmem_wait_ld();
-            tc::tmem_hold(d0);
-            tc::tmem_hold(d1);
-            if (h + 64 == NC) {
-              tc::fence_before_sync();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive(&c.acc_empty[b]);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) tc::fma_pair(acc[h / 2 + i], d0[2 * i], d0[2 * i + 1], s2);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) tc::fma_pair(acc[h / 2 + 16 + i], d1[2 * i], d1[2 * i + 1], s2);
-          }
-        } else if (lane == 0) {
-          tc::mbar_arrive(&c.acc_empty[b]);
-        }
-      }
-      bool finish = true;
-      if (p.splits > 1) {
-        // fragment [column][row], rows padded to a_rows: neighbouring lanes
-        // write neighbouring words
-        const int tile = w.tile;
-        const size_t frag = size_t(BN) * p.a_rows;
-        float *mine = p.scratch + (size_t(tile) * p.splits + w.split) * frag;
-        const int r = sub * 32 + lane;
-        if (live) {
-#pragma unroll
-          for (int i = 0; i < NC / 2; ++i) {
-            __stcg(mine + size_t(group * NC + 2 * i) * p.a_rows + r, tc::pair_lo(acc[i]));
-            __stcg(mine + size_t(group * NC + 2 * i + 1) * p.a_rows + r, tc::pair_hi(acc[i]));
-          }
-        }
-        __threadfence();
-        tc::named_barrier(1, EPI_THREADS);
-        if (epi_tid == 0) c.last = atomicAdd(p.counters + tile, 1u) == unsigned(p.splits - 1);
-        tc::named_barrier(1, EPI_THREADS);
-        finish = c.last != 0;
-        tc::named_barrier(1, EPI_THREADS);   // c.last may be written again
-        if (finish) {
-          __threadfence();
-          if (epi_tid == 0) p.counters[tile] = 0;
-          if (live) {
-            const float *all = p.scratch + size_t(tile) * p.splits * frag + r;
-#pragma unroll
-            for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
-            for (int s = 0; s < p.splits; ++s) {
-#pragma unroll
-              for (int i = 0; i < NC / 2; ++i) {
-                const float *src = all + s * frag + size_t(group * NC + 2 * i) * p.a_rows;
-                acc[i] = tc::pair(tc::pair_lo(acc[i]) + __ldcg(src), tc::pair_hi(acc[i]) + __ldcg(src + p.a_rows));
-              }
-            }
-          }
-        }
-      }
-      if (finish && live) {
-        const size_t at = size_t(row) * p.output_stride;
-        if (p.output_f32) {
-          float *out = reinterpret_cast<float *>(p.output) + at;
-#pragma unroll
-          for (int i = 0; i < NC / 2; i += 2) {
-            const int col = n0 + 2 * i;
-            const float v[4] = {tc::pair_lo(acc[i]), tc::pair_hi(acc[i]), tc::pair_lo(acc[i + 1]), tc::pair_hi(acc[i + 1])};
-            if (p.vector_out && col + 4 <= p.n) {
-              *reinterpret_cast<float4 *>(out + col) = make_float4(v[0], v[1], v[2], v[3]);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (col + k < p.n) out[col + k] = v[k];
-            }
-          }
-        } else {
-          uint16_t *out = reinterpret_cast<uint16_t *>(p.output) + at;
-#pragma unroll
-          for (int i = 0; i < NC / 2; i += 4) {
-            const int col = n0 + 2 * i;
-            uint32_t v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = pack_bf16x2(tc::pair_lo(acc[i + k]), tc::pair_hi(acc[i + k]));
-            if (p.vector_out && col + 8 <= p.n) {
-              st_vec(out + col, make_uint4(v[0], v[1], v[2], v[3]));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (col + k < p.n) out[col + k] = uint16_t(v[k / 2] >> (k % 2 * 16));
-            }
-          }
-        }
+      for (int i = 0; i < NC / 2; ++i) {
+        part[size_t(2 * i) * p.a_rows] = tc::pair_lo(acc[i]);
+        part[size_t(2 * i + 1) * p.a_rows] = tc::pair_hi(acc[i]);
       }
     }
+  }
+  if (p.splits > 1) {
+    __syncwarp();
+    cluster_sync();
+    // this CTA's share of the tile: items of a row's eight columns
+    const int items = rows * (BN / 8);
+    const int i1 = items * (rank + 1) / p.splits;
+    for (int i = items * rank / p.splits + threadIdx.x; i < i1; i += NT) {
+      const int cg = i / rows, row = i - cg * rows;
+      const float *at = reinterpret_cast<const float *>(ring) + size_t(cg) * 8 * p.a_rows + row;
+      float v[8] = {};
+#pragma unroll 4
+      for (int s = 0; s < p.splits; ++s) {
+        const uint32_t src = peer_addr(at, uint32_t(s));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += ld_peer(src + uint32_t(k * p.a_rows * 4));
+      }
+      if (n0 + cg * 8 < p.n) store8(p, m0 + row, n0 + cg * 8, v);
+    }
+    cluster_sync();   // no CTA leaves while another reads its sums
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 2) tc::tmem_dealloc(tmem, 512);
+  if (warp == SCALE_WARP0) tc::tmem_dealloc(tmem, BUFS * BN);
   if (threadIdx.x == 0 && c.abort) atomicOr(p.err, 2u);
 }
 
-template <int BN>
-cudaError_t launch(const MatmulParams &p, const CUtensorMap &tm_a, const CUtensorMap &tm_w, int grid,
-                   cudaStream_t stream) {
+// ------------------------------------------------------------- pair kernel
+// CTA pair: tiles of 256 rows x 256 columns; CTA r has rows 128 r .. and loads
+// rows 128 r .. of the tile's part of w.  The MMAs, issued by rank 0, read both
+// CTAs' stages and write both tensor memories.  Rank 1 tells rank 0 when its
+// part of a stage has arrived; a stage's or buffer's release reaches both.
+constexpr int PAIR_N = 256;
+constexpr int PAIR_STAGE = 2 * BM * 128;
+constexpr int PAIR_STAGES = RING_BYTES / PAIR_STAGE;
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
+k_matmul_pair(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w) {
+  constexpr int BUFS = 2;
+  constexpr int NC = PAIR_N / 2;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Control &c = *reinterpret_cast<Control *>(smem);
+  unsigned char *ring = smem + SMEM_CTRL;
+  const Scales sc = {reinterpret_cast<float *>(ring + RING_BYTES),
+                     reinterpret_cast<float *>(ring + RING_BYTES) + CHUNKS * CHUNK * BM};
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile int *abort = &c.abort;
+  const uint32_t rank = cluster_rank();
+
+  if (threadIdx.x == 0) {
+    init_control(c, PAIR_STAGES, BUFS, 2 * EPI_WARPS);
+    tc::tma_prefetch_desc(&tm_a);
+    tc::tma_prefetch_desc(&tm_w);
+  }
+  if (warp == SCALE_WARP0) tmem_alloc2(&c.tmem, BUFS * PAIR_N);
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = c.tmem;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tiles = p.m_tiles * p.n_tiles, pairs = int(gridDim.x) / 2, first = int(blockIdx.x) / 2;
+
+  if (warp < EPI_WARP0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) {
+      // -------------------------------------------------------- producer
+      Ring at;
+      bool ok = true;
+      const bool leader = tc::elect_one();
+      int issued = 0;
+      if (!g_stall_copies)
+        for (int tile = first; tile < tiles && ok; tile += pairs) {
+          const int m0 = tile % p.m_tiles * 256 + int(rank) * BM, n0 = tile / p.m_tiles * PAIR_N + int(rank) * BM;
+          for (int kb = 0; kb < p.k_blocks; ++kb) {
+            ok = wait_cluster(&c.empty[at.at], at.phase ^ 1u, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (leader) {
+              unsigned char *dst = ring + size_t(at.at) * PAIR_STAGE;
+              tc::mbar_arrive_expect_tx(&c.full[at.at], PAIR_STAGE);
+              tc::tma_load_2d(dst, &tm_a, kb * 128, m0, &c.full[at.at]);
+              tc::tma_load_2d(dst + BM * 128, &tm_w, kb * 128, n0, &c.full[at.at]);
+            }
+            __syncwarp();
+            at.next(PAIR_STAGES);
+            ++issued;
+          }
+        }
+      if (*abort)
+        for (int i = max(0, issued - PAIR_STAGES); i < issued; ++i)
+          tc::mbar_wait_bounded(&c.full[i % PAIR_STAGES], uint32_t((i / PAIR_STAGES) & 1), tc::SUB_WAIT_LIMIT);
+    } else if (warp == 1) {
+      // ------------------------------------------- MMA issuer / its peer
+      Ring at, acc;
+      bool ok = true;
+      const bool leader = tc::elect_one();
+      const uint32_t idesc = tc::idesc_e4m3_f32(256, PAIR_N);
+      const uint64_t a0 = tc::desc_sw128(ring), b0 = tc::desc_sw128(ring + BM * 128);
+      for (int tile = first; tile < tiles && ok; tile += pairs)
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          ok = tc::wait_or_abort(&c.full[at.at], at.phase, abort);
+          if (rank == 0)
+            ok = ok && wait_cluster(&c.peer_full[at.at], at.phase, abort) &&
+                 wait_cluster(&c.acc_empty[acc.at], acc.phase ^ 1u, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (leader) {
+            if (rank == 0) {
+              const uint64_t step = uint64_t(at.at * (PAIR_STAGE >> 4));
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma2_e4m3(tmem + uint32_t(acc.at * PAIR_N), a0 + step + 2 * ks, b0 + step + 2 * ks, idesc, ks != 0);
+              mma2_commit(&c.empty[at.at]);
+              mma2_commit(&c.acc_full[acc.at]);
+            } else {
+              arrive_peer(peer_addr(&c.peer_full[at.at], 0));
+            }
+          }
+          __syncwarp();
+          at.next(PAIR_STAGES);
+          acc.next(BUFS);
+        }
+      // no MMA is in flight when the tensor memory goes
+      if (rank == 0 && leader) mma2_commit(&c.drain);
+      __syncwarp();
+      if (rank == 0) tc::mbar_wait_bounded(&c.drain, 0u, tc::SUB_WAIT_LIMIT);
+    } else {
+      Ring scales;
+      for (int tile = first; tile < tiles; tile += pairs)
+        load_scales(p, c, sc, scales, tile % p.m_tiles * 256 + int(rank) * BM, tile / p.m_tiles * 2, 0, p.k_blocks,
+                    warp - SCALE_WARP0, lane);
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int sub = warp % 4, group = (warp - EPI_WARP0) / 4, r = sub * 32 + lane;
+    const int col = group * NC;
+    const uint32_t release0 = peer_addr(&c.acc_empty[0], 0);
+    Ring acc_ring, scale_ring;
+    for (int tile = first; tile < tiles; tile += pairs) {
+      const int m0 = tile % p.m_tiles * 256 + int(rank) * BM, n0 = tile / p.m_tiles * PAIR_N;
+      uint64_t acc[NC / 2];
+#pragma unroll
+      for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
+      add_blocks<NC>(c, sc, acc_ring, scale_ring, BUFS, PAIR_N, tmem + (uint32_t(sub * 32) << 16) + uint32_t(col), r,
+                     group, p.k_blocks, m0 + sub * 32 < p.m, lane,
+                     [&](int b) { arrive_peer(release0 + uint32_t(b) * 8); }, acc);
+      if (m0 + r < p.m) store_row<NC>(p, m0 + r, n0 + col, acc);
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  cluster_sync();   // neither CTA leaves while the other's MMAs or arrivals reach it
+  tc::fence_after_sync();
+  if (warp == SCALE_WARP0) tmem_dealloc2(tmem, BUFS * PAIR_N);
+  if (threadIdx.x == 0 && c.abort) atomicOr(p.err, 2u);
+}
+
+template <class Kernel>
+cudaError_t launch(Kernel k, const MatmulParams &p, const CUtensorMap &tm_a, const CUtensorMap &tm_w, int grid,
+                   int cluster, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_block_matmul<BN>, p, tm_a, tm_w);
+  if (cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, k, p, tm_a, tm_w);
+}
+
+template <class Kernel>
+cudaError_t active_clusters(Kernel k, int cluster, int *out) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(cluster));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(out, k, &cfg);
 }
 
 }  // namespace
 
 cudaError_t matmul_stall_copies(int on) { return cudaMemcpyToSymbol(g_stall_copies, &on, sizeof on); }
 
-cudaError_t matmul_set_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(k_block_matmul<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_block_matmul<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+cudaError_t matmul_setup(int sms, MatmulPlan *plan) {
+  cudaError_t e = cudaSuccess;
+  for (const void *k : {(const void *)k_matmul_split<64>, (const void *)k_matmul_split<128>, (const void *)k_matmul_pair})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  plan->clusters[1] = sms;
+  for (int s = 2; s <= MATMUL_SPLITS_MAX && e == cudaSuccess; ++s)
+    e = active_clusters(k_matmul_split<128>, s, &plan->clusters[s]);
+  if (e == cudaSuccess) e = active_clusters(k_matmul_pair, 2, &plan->pairs);
+  if (e == cudaSuccess && plan->pairs < 1) e = cudaErrorNotSupported;
   return e;
 }
 
-cudaError_t launch_block_matmul(const MatmulParams &args, int sms, cudaStream_t stream) {
+cudaError_t launch_block_matmul(const MatmulParams &args, const MatmulPlan &plan, cudaStream_t stream) {
   MatmulParams p = args;
   p.k_blocks = qblocks(p.k);
   p.n_blocks = qblocks(p.n);
   p.m_tiles = (p.m + BM - 1) / BM;
-  const int64_t tiles128 = int64_t(p.m_tiles) * p.n_blocks, tiles256 = int64_t(p.m_tiles) * ((p.n + 255) / 256);
-  const bool wide = tiles256 >= sms;
-  const int bn = wide ? 256 : 128;
+  // The form that takes the fewest clocks: waves of clusters, a block's clocks
+  // for each of a CTA's k blocks (measured: the tile's products, or the read
+  // of its weights where all CTAs stream), and what a wave costs beside them
+  // (start, pipeline fill, the meeting of the sums).
+  const double PAIR_BLOCK = 560, PAIR_WAVE = 3000, WAVE = 2500, MEET = 1500;
+  const int64_t pair_tiles = int64_t((p.m + 255) / 256) * ((p.n + PAIR_N - 1) / PAIR_N);
+  double best = double((pair_tiles + plan.pairs - 1) / plan.pairs) * (p.k_blocks * PAIR_BLOCK + PAIR_WAVE);
+  int bn = 0;
+  p.splits = 1;
+  for (int n : {128, 64})
+    for (int s = 1; s <= std::min(MATMUL_SPLITS_MAX, p.k_blocks); ++s) {
+      if (plan.clusters[s] < 1) continue;
+      const int64_t tiles = int64_t(p.m_tiles) * ((p.n + n - 1) / n);
+      const double block = n == 128 ? 700 : 400;
+      const double clocks = double((tiles + plan.clusters[s] - 1) / plan.clusters[s]) *
+                            (double((p.k_blocks + s - 1) / s) * block + WAVE + (s > 1 ? MEET : 0));
+      if (clocks < best) {
+        best = clocks;
+        bn = n;
+        p.splits = s;
+      }
+    }
+  CUtensorMap tm_a, tm_w;
+  if (bn == 0) {
+    p.m_tiles = (p.m + 255) / 256;
+    p.n_tiles = (p.n + PAIR_N - 1) / PAIR_N;
+    if (!encode_rows_sw128(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.values, p.m, p.k, p.values_stride, 128, BM) ||
+        !encode_rows_sw128(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weight, p.n, p.k, p.weight_stride, 128, BM))
+      return cudaErrorInvalidValue;
+    const int pairs = int(std::min<int64_t>(pair_tiles, plan.pairs));
+    return launch(k_matmul_pair, p, tm_a, tm_w, 2 * pairs, 1, stream);   // the kernel's own cluster size
+  }
   p.n_tiles = (p.n + bn - 1) / bn;
   p.a_rows = std::min(BM, (p.m + 7) / 8 * 8);
-  p.splits = 1;
-  if (tiles128 < sms) {
-    // as many items as SMs, of at least two k blocks, within the scratch
-    p.splits = int(std::min<int64_t>({sms / tiles128, std::max(1, p.k_blocks / 2),
-                                      int64_t(p.scratch_floats / (size_t(tiles128) * bn * p.a_rows))}));
-    if (p.splits < 1 || tiles128 > p.counter_count) p.splits = 1;
-  }
-  p.stages = std::min(STAGES_MAX, (SMEM_BYTES - SMEM_CTRL) / (p.a_rows * 128 + bn * 128));
-  CUtensorMap tm_a, tm_w;
+  p.stages = std::min(STAGES_MAX, RING_BYTES / (p.a_rows * 128 + bn * 128));
   if (!encode_rows_sw128(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.values, p.m, p.k, p.values_stride, 128, p.a_rows) ||
       !encode_rows_sw128(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weight, p.n, p.k, p.weight_stride, 128, bn))
     return cudaErrorInvalidValue;
-  const int64_t items = int64_t(p.m_tiles) * p.n_tiles * p.splits;
-  const int grid = int(std::min<int64_t>(items, sms));
-  return wide ? launch<256>(p, tm_a, tm_w, grid, stream) : launch<128>(p, tm_a, tm_w, grid, stream);
+  const int grid = p.m_tiles * p.n_tiles * p.splits;
+  return bn == 128 ? launch(k_matmul_split<128>, p, tm_a, tm_w, grid, p.splits, stream)
+                   : launch(k_matmul_split<64>, p, tm_a, tm_w, grid, p.splits, stream);
 }
 
 }  // namespace mhc

@@ -42,35 +42,22 @@ struct MatmulParams {
   int64_t output_stride;
   int output_f32;
   int vector_out;                         // the output's rows start on 16-byte boundaries
-  float *scratch;                         // sums of split tiles
-  size_t scratch_floats;
-  unsigned int *counters;                 // arrivals of a split tile's items, zero between calls
-  int counter_count;
   unsigned int *err;                      // bit 1: a bounded wait gave up
   // set by the launcher
   int k_blocks, n_blocks, m_tiles, n_tiles, splits, stages;
   int a_rows;                             // rows of a stage's `values` tile
 };
 
-// Work item `item` of a matmul: a tile of 128 rows by BN columns and a range
-// of its k blocks.  Neighbouring items share the weight tile.
-struct WorkItem {
-  int m0, n_tile, tile, split, kb0, kb1;
+constexpr int MATMUL_SPLITS_MAX = 8;
+// What runs at once on this GPU.
+struct MatmulPlan {
+  int clusters[MATMUL_SPLITS_MAX + 1];    // clusters of that many CTAs (split kernel)
+  int pairs;                              // CTA pairs (pair kernel)
 };
-__device__ __forceinline__ WorkItem work_item(const MatmulParams &p, int item) {
-  WorkItem w;
-  w.split = item % p.splits;
-  w.tile = item / p.splits;
-  w.m0 = (w.tile % p.m_tiles) * 128;
-  w.n_tile = w.tile / p.m_tiles;
-  w.kb0 = int(int64_t(p.k_blocks) * w.split / p.splits);
-  w.kb1 = int(int64_t(p.k_blocks) * (w.split + 1) / p.splits);
-  return w;
-}
 
-cudaError_t matmul_set_attributes();
-cudaError_t matmul_stall_copies(int on);   // test hook, see include/mhc_boundary_test.h
-cudaError_t launch_block_matmul(const MatmulParams &p, int sms, cudaStream_t stream);
+cudaError_t matmul_setup(int sms, MatmulPlan *plan);
+cudaError_t matmul_stall_copies(int on);  // test hook, see include/mhc_boundary_test.h
+cudaError_t launch_block_matmul(const MatmulParams &p, const MatmulPlan &plan, cudaStream_t stream);
 
 // MoE layer of up to MOE_TOKENS_MAX tokens (k_moe.cu).
 constexpr int MOE_TOKENS_MAX = 32;

@@ -32,6 +32,16 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
   return mbar_try_wait(bar, parity) || wait_poll(bar, parity, abort);
 }
 
+// The same without a call: for code that holds most registers.
+__device__ __forceinline__ void wait_or_abort_inline(uint64_t *bar, uint32_t parity, volatile int *abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
+    if (*abort) break;
+    if (i > 64) __nanosleep(64);
+    if (i > SUB_WAIT_LIMIT) *abort = 1;
+  }
+}
+
 // Instruction descriptor of kind::f8f6f4: FP32 accumulator, E4M3 A and B,
 // both K-major, M x N.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n) {

@@ -33,8 +33,8 @@ class Sublayer:
     "sigmoid"; renormalize: divide the chosen scores by their sum;
     router_f32: the router weight is FP32.
 
-    The handle owns scratch that matmul and moe use, so its calls run one
-    after another: on one stream, or on streams that the caller orders."""
+    The handle owns scratch that moe uses, so its calls run one after another:
+    on one stream, or on streams that the caller orders."""
 
     def __init__(self, *, hidden: int = 0, intermediate: int = 0, experts: int = 0, shared_experts: int = 0,
                  top_k: int = 0, max_moe_tokens: int = 0, fp8: bool = True, score: str = "softmax",
