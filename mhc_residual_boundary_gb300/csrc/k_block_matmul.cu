@@ -69,33 +69,14 @@ __device__ __forceinline__ float ld_peer(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+// An arrival on another CTA's barrier.  What it tells of lies in tensor memory
+// (read, ordered by the tcgen05 fences) or came by asynchronous copies (ordered
+// by their own completion), not in memory that this thread wrote, so it has no
+// release at cluster scope, nor its wait an acquire: each costs hundreds of
+// clocks, several times a block (matmul of 4096 x 4096 x 6144: 242 us with
+// them).
 __device__ __forceinline__ void arrive_peer(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// A wait for arrivals of the other CTA: acquire at cluster scope.
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(tc::smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-__device__ __noinline__ bool wait_cluster_poll(uint64_t *bar, uint32_t parity, volatile int *abort) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < tc::SUB_WAIT_LIMIT; ++i) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if (*abort) return false;
-    if (i > 64) __nanosleep(64);
-  }
-  *abort = 1;
-  return false;
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  return try_wait_cluster(bar, parity) || wait_cluster_poll(bar, parity, abort);
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ------------------------------------------------- cta_group::2 instructions
@@ -481,7 +462,7 @@ k_matmul_pair(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, co
         for (int tile = first; tile < tiles && ok; tile += pairs) {
           const int m0 = tile % p.m_tiles * 256 + int(rank) * BM, n0 = tile / p.m_tiles * PAIR_N + int(rank) * BM;
           for (int kb = 0; kb < p.k_blocks; ++kb) {
-            ok = wait_cluster(&c.empty[at.at], at.phase ^ 1u, abort);
+            ok = tc::wait_or_abort(&c.empty[at.at], at.phase ^ 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (leader) {
@@ -509,8 +490,8 @@ k_matmul_pair(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, co
         for (int kb = 0; kb < p.k_blocks; ++kb) {
           ok = tc::wait_or_abort(&c.full[at.at], at.phase, abort);
           if (rank == 0)
-            ok = ok && wait_cluster(&c.peer_full[at.at], at.phase, abort) &&
-                 wait_cluster(&c.acc_empty[acc.at], acc.phase ^ 1u, abort);
+            ok = ok && tc::wait_or_abort(&c.peer_full[at.at], at.phase, abort) &&
+                 tc::wait_or_abort(&c.acc_empty[acc.at], acc.phase ^ 1u, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc::fence_after_sync();
