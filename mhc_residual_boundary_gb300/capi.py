@@ -244,6 +244,15 @@ def _check_sublayer(status: int, handle) -> None:
         raise MhcError(status, lib().mhc_sublayer_last_error(handle).decode())
 
 
+def sublayer_calls() -> dict:
+    """The sublayer operators as functions of (handle, argument struct as bytes,
+    stream): the struct packed by the caller in one step."""
+    vp = ctypes.c_void_p
+    lib()
+    proto = ctypes.CFUNCTYPE(ctypes.c_int, vp, ctypes.c_char_p, vp)
+    return {name: proto(("mhc_sublayer_" + name, _lib)) for name in SUBLAYER_CALLS}
+
+
 def mhc_sublayer_create(config: mhc_sublayer_config_t, device: int) -> ctypes.c_void_p:
     handle = ctypes.c_void_p()
     _check_sublayer(lib().mhc_sublayer_create(ctypes.byref(config), int(device), ctypes.byref(handle)), None)

@@ -10,12 +10,20 @@ the latter; an optional output that the dict lacks is not computed.
 """
 from __future__ import annotations
 
+import struct
+
 import torch
 
 from . import capi
 
 QBLOCK = 128
 F8, BF16, F32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
+
+# the argument structs of include/mhc_sublayer.h (native sizes and alignment)
+NORM_ARGS = struct.Struct("@iiPqPqPfPPPP")
+QUANTIZE_ARGS = struct.Struct("@iiPqPPP")
+MATMUL_ARGS = struct.Struct("@iiiPqPqPqPPqi")
+MOE_ARGS = struct.Struct("@iPPPPPPPPPP")
 
 
 def scale_blocks(n: int) -> int:
@@ -52,6 +60,10 @@ class Sublayer:
                                                  max_moe_tokens, scores[score], routed_scale, flags)
         self.hidden, self.intermediate, self.experts, self.shared = hidden, intermediate, experts, shared_experts
         self.top_k, self.fp8, self.router_f32 = top_k, fp8, router_f32
+        self._index = self.device.index
+        lib = capi.sublayer_calls()
+        self._norm, self._quantize, self._swiglu = lib["add_rms_norm"], lib["quantize"], lib["swiglu"]
+        self._matmul, self._moe = lib["matmul"], lib["moe"]
         self.handle = capi.mhc_sublayer_create(self.config, self.device.index)
 
     # ------------------------------------------------------------ lifecycle
@@ -93,26 +105,45 @@ class Sublayer:
             raise ValueError(f"unknown operator {op!r}")
         return out
 
+    # A call's checks run on every call, beside kernels of a few microseconds, so
+    # they are written for their own time: one test a tensor for the usual case,
+    # the message in a function that only a refusal reaches, the arguments packed
+    # in one step.
     def _ptr(self, name: str, t: torch.Tensor, dtype, shape: tuple) -> int:
         """Pointer of a dense tensor."""
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: expected contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-        if t.device != self.device:
-            raise ValueError(f"{name} must be a tensor on {self.device}, got {t.device}")
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._index:
+            self._refuse(name, t, dtype, shape, "contiguous ")
         return t.data_ptr()
 
-    def _rows(self, name: str, t: torch.Tensor, dtype, shape: tuple) -> tuple:
-        """(pointer, row stride) of a matrix with contiguous rows."""
-        if t.dtype != dtype or t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name}: expected {dtype} {shape} with contiguous rows, got {t.dtype} {tuple(t.shape)} "
-                             f"strides {t.stride()}")
+    def _stride(self, name: str, t: torch.Tensor, dtype, shape: tuple) -> int:
+        """Row stride of a matrix with contiguous rows."""
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index:
+            self._refuse(name, t, dtype, shape, "")
+        if t.is_contiguous() and shape[0] > 1:
+            return shape[1]
+        if shape[1] > 1 and t.stride(1) != 1:
+            self._refuse(name, t, dtype, shape, "contiguous rows, ")
+        # a single row's stride is never used: give one that suits every type
+        return t.stride(0) if shape[0] > 1 else -(-shape[1] // 16) * 16
+
+    def _refuse(self, name: str, t: torch.Tensor, dtype, shape: tuple, what: str) -> None:
         if t.device != self.device:
             raise ValueError(f"{name} must be a tensor on {self.device}, got {t.device}")
-        # a single row's stride is never used: give the dense one
-        return t.data_ptr(), t.stride(0) if shape[0] > 1 else -(-shape[1] // 16) * 16
+        raise ValueError(f"{name}: expected {what}{dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)} "
+                         f"strides {t.stride()}")
+
+    def _call(self, fn, args: bytes, stream) -> None:
+        """One library call: `args` is its argument struct, laid out as in C."""
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(self._index)
+        elif isinstance(stream, torch.cuda.Stream):
+            stream = stream.cuda_stream
+        status = fn(self.handle, args, stream)
+        if status:
+            capi._check_sublayer(status, self.handle)
 
     @staticmethod
-    def _names(outputs: dict, allowed: tuple) -> None:
+    def _unknown(outputs: dict, allowed: tuple) -> None:
         for name in outputs:
             if name not in allowed:
                 raise ValueError(f"unknown output {name!r}: expected some of {allowed}")
@@ -123,54 +154,54 @@ class Sublayer:
         inputs: x [m][h], norm_weight [h] and optionally residual [m][h];
         outputs: some of residual_out (r), output (y), values with scales (y
         in 8 bits)."""
-        x = inputs["x"]
-        m, h = x.shape
-        a = capi.mhc_sublayer_norm_args_t()
-        a.m, a.h, a.eps = m, h, eps
-        a.x, a.x_stride = self._rows("x", x, BF16, (m, h))
-        residual = inputs.get("residual")
+        x, weight, residual = inputs["x"], inputs["norm_weight"], inputs.get("residual")
+        shape = x.shape
+        m, h = shape
+        x_stride = self._stride("x", x, BF16, shape)
+        res = res_stride = 0
         if residual is not None:
-            a.residual, a.residual_stride = self._rows("residual", residual, BF16, (m, h))
-        a.norm_weight = self._ptr("norm_weight", inputs["norm_weight"], BF16, (h,))
-        self._names(outputs, ("residual_out", "output", "values", "scales"))
-        self._quantized(a, outputs, m, h)
-        for name in ("residual_out", "output"):
-            if name in outputs:
-                setattr(a, name, self._ptr(name, outputs[name], BF16, (m, h)))
-        capi.mhc_sublayer_add_rms_norm(self.handle, a, stream)
+            res_stride = self._stride("residual", residual, BF16, shape)
+            res = residual.data_ptr()
+        gamma = self._ptr("norm_weight", weight, BF16, (h,))
+        known = 0
+        ptrs = [0, 0, 0, 0]
+        for i, (name, dtype, width) in enumerate((("residual_out", BF16, h), ("output", BF16, h), ("values", F8, h),
+                                                  ("scales", F32, (h + 127) // 128))):
+            t = outputs.get(name)
+            if t is not None:
+                ptrs[i] = self._ptr(name, t, dtype, (m, width))
+                known += 1
+        if known != len(outputs):
+            self._unknown(outputs, ("residual_out", "output", "values", "scales"))
+        self._call(self._norm, NORM_ARGS.pack(m, h, x.data_ptr(), x_stride, res, res_stride, gamma, eps, *ptrs), stream)
         return outputs
-
-    def _quantized(self, a, outputs: dict, m: int, h: int) -> None:
-        if "values" in outputs:
-            a.values = self._ptr("values", outputs["values"], F8, (m, h))
-        if "scales" in outputs:
-            a.scales = self._ptr("scales", outputs["scales"], F32, (m, scale_blocks(h)))
 
     def quantize(self, inputs: dict, outputs: dict, *, stream=None) -> dict:
         """x [m][h] BF16 to 8 bits: values, scales."""
-        x = inputs["x"]
-        m, h = x.shape
-        a = capi.mhc_sublayer_quantize_args_t()
-        a.m, a.h = m, h
-        a.x, a.x_stride = self._rows("x", x, BF16, (m, h))
-        self._names(outputs, ("values", "scales"))
-        self._quantized(a, outputs, m, h)
-        capi.mhc_sublayer_quantize(self.handle, a, stream)
+        x, values, scales = inputs["x"], outputs["values"], outputs["scales"]
+        shape = x.shape
+        m, h = shape
+        stride = self._stride("x", x, BF16, shape)
+        v = self._ptr("values", values, F8, shape)
+        s = self._ptr("scales", scales, F32, (m, (h + 127) // 128))
+        if len(outputs) != 2:
+            self._unknown(outputs, ("values", "scales"))
+        self._call(self._quantize, QUANTIZE_ARGS.pack(m, h, x.data_ptr(), stride, 0, v, s), stream)
         return outputs
 
     def swiglu(self, inputs: dict, outputs: dict, *, stream=None) -> dict:
         """silu(gate) * up of gate_up [m][2h] (gate, then up) to 8 bits:
         values, scales and optionally output (BF16)."""
-        x = inputs["gate_up"]
-        m, h = x.shape[0], x.shape[1] // 2
-        a = capi.mhc_sublayer_quantize_args_t()
-        a.m, a.h = m, h
-        a.x, a.x_stride = self._rows("gate_up", x, BF16, (m, 2 * h))
-        self._names(outputs, ("output", "values", "scales"))
-        self._quantized(a, outputs, m, h)
-        if "output" in outputs:
-            a.output = self._ptr("output", outputs["output"], BF16, (m, h))
-        capi.mhc_sublayer_swiglu(self.handle, a, stream)
+        x, values, scales, out = inputs["gate_up"], outputs["values"], outputs["scales"], outputs.get("output")
+        m, h2 = x.shape
+        h = h2 // 2
+        stride = self._stride("gate_up", x, BF16, (m, 2 * h))
+        v = self._ptr("values", values, F8, (m, h))
+        s = self._ptr("scales", scales, F32, (m, (h + 127) // 128))
+        o = 0 if out is None else self._ptr("output", out, BF16, (m, h))
+        if len(outputs) != (2 if out is None else 3):
+            self._unknown(outputs, ("output", "values", "scales"))
+        self._call(self._swiglu, QUANTIZE_ARGS.pack(m, h, x.data_ptr(), stride, o, v, s), stream)
         return outputs
 
     def matmul(self, inputs: dict, outputs: dict, *, stream=None) -> dict:
@@ -178,20 +209,22 @@ class Sublayer:
         (weight * weight_scales)^T: values [m][k] and weight [n][k] in 8 bits,
         scales [m][ceil(k/128)], weight_scales [ceil(n/128)][ceil(k/128)]."""
         values, weight, out = inputs["values"], inputs["weight"], outputs["output"]
+        scales, weight_scales = inputs["scales"], inputs["weight_scales"]
         m, k = values.shape
-        n = weight.shape[0]
-        a = capi.mhc_sublayer_matmul_args_t()
-        a.m, a.n, a.k = m, n, k
-        a.values, a.values_stride = self._rows("values", values, F8, (m, k))
-        a.scales, a.scales_stride = self._rows("scales", inputs["scales"], F32, (m, scale_blocks(k)))
-        a.weight, a.weight_stride = self._rows("weight", weight, F8, (n, k))
-        a.weight_scales = self._ptr("weight_scales", inputs["weight_scales"], F32, (scale_blocks(n), scale_blocks(k)))
-        self._names(outputs, ("output",))
-        if out.dtype not in (BF16, F32):
-            raise ValueError(f"output: expected {BF16} or {F32}, got {out.dtype}")
-        a.output_f32 = out.dtype == F32
-        a.output, a.output_stride = self._rows("output", out, out.dtype, (m, n))
-        capi.mhc_sublayer_matmul(self.handle, a, stream)
+        n, kb = weight.shape[0], (k + 127) // 128
+        v_stride = self._stride("values", values, F8, (m, k))
+        s_stride = self._stride("scales", scales, F32, (m, kb))
+        w_stride = self._stride("weight", weight, F8, (n, k))
+        ws = self._ptr("weight_scales", weight_scales, F32, ((n + 127) // 128, kb))
+        dtype = out.dtype
+        if dtype is not BF16 and dtype is not F32:
+            raise ValueError(f"output: expected {BF16} or {F32}, got {dtype}")
+        o_stride = self._stride("output", out, dtype, (m, n))
+        if len(outputs) != 1:
+            self._unknown(outputs, ("output",))
+        self._call(self._matmul, MATMUL_ARGS.pack(m, n, k, values.data_ptr(), v_stride, scales.data_ptr(), s_stride,
+                                                  weight.data_ptr(), w_stride, ws, out.data_ptr(), o_stride,
+                                                  dtype is F32), stream)
         return outputs
 
     def moe(self, inputs: dict, outputs: dict, *, stream=None) -> dict:
@@ -201,28 +234,26 @@ class Sublayer:
         [E+S][2][ceil(I/128)][ceil(H/128)] and down_scales
         [E+S][ceil(H/128)][ceil(I/128)]; outputs: output [m][H] BF16 and
         optionally idx [m][top_k] int32 and weights [m][top_k] FP32."""
-        x = inputs["x"]
-        m, H, I, E, S = x.shape[0], self.hidden, self.intermediate, self.experts, self.shared
-        a = capi.mhc_sublayer_moe_args_t()
-        a.m = m
-        a.x = self._ptr("x", x, BF16, (m, H))
-        a.router = self._ptr("router", inputs["router"], F32 if self.router_f32 else BF16, (E, H))
-        if inputs.get("bias") is not None:
-            a.bias = self._ptr("bias", inputs["bias"], F32, (E,))
+        x, bias = inputs["x"], inputs.get("bias")
+        m, H, I, E, every = x.shape[0], self.hidden, self.intermediate, self.experts, self.experts + self.shared
+        xp = self._ptr("x", x, BF16, (m, H))
+        router = self._ptr("router", inputs["router"], F32 if self.router_f32 else BF16, (E, H))
+        bp = 0 if bias is None else self._ptr("bias", bias, F32, (E,))
         wt = F8 if self.fp8 else BF16
-        a.gate_up = self._ptr("gate_up", inputs["gate_up"], wt, (E + S, 2 * I, H))
-        a.down = self._ptr("down", inputs["down"], wt, (E + S, H, I))
+        gate_up = self._ptr("gate_up", inputs["gate_up"], wt, (every, 2 * I, H))
+        down = self._ptr("down", inputs["down"], wt, (every, H, I))
+        gs = ds = 0
         if self.fp8:
-            hb, ib = scale_blocks(H), scale_blocks(I)
-            a.gate_up_scales = self._ptr("gate_up_scales", inputs["gate_up_scales"], F32, (E + S, 2, ib, hb))
-            a.down_scales = self._ptr("down_scales", inputs["down_scales"], F32, (E + S, hb, ib))
-        self._names(outputs, ("output", "idx", "weights"))
-        a.output = self._ptr("output", outputs["output"], BF16, (m, H))
-        if "idx" in outputs:
-            a.idx = self._ptr("idx", outputs["idx"], torch.int32, (m, self.top_k))
-        if "weights" in outputs:
-            a.weights = self._ptr("weights", outputs["weights"], F32, (m, self.top_k))
-        capi.mhc_sublayer_moe(self.handle, a, stream)
+            hb, ib = (H + 127) // 128, (I + 127) // 128
+            gs = self._ptr("gate_up_scales", inputs["gate_up_scales"], F32, (every, 2, ib, hb))
+            ds = self._ptr("down_scales", inputs["down_scales"], F32, (every, hb, ib))
+        out, idx, weights = outputs["output"], outputs.get("idx"), outputs.get("weights")
+        op = self._ptr("output", out, BF16, (m, H))
+        ip = 0 if idx is None else self._ptr("idx", idx, torch.int32, (m, self.top_k))
+        wp = 0 if weights is None else self._ptr("weights", weights, F32, (m, self.top_k))
+        if len(outputs) != 1 + (idx is not None) + (weights is not None):
+            self._unknown(outputs, ("output", "idx", "weights"))
+        self._call(self._moe, MOE_ARGS.pack(m, xp, router, bp, gate_up, gs, down, ds, op, ip, wp), stream)
         return outputs
 
     def check_errors(self) -> None:
