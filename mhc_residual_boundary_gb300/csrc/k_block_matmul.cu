@@ -38,6 +38,9 @@ constexpr int SMEM_CTRL = 1024;
 constexpr int SMEM_SCALES = CHUNKS * CHUNK * (BM + 2) * 4 + 1024;   // and the ring's alignment
 constexpr int SMEM_BYTES = 227 * 1024;
 constexpr int RING_BYTES = (SMEM_BYTES - SMEM_CTRL - SMEM_SCALES) / 1024 * 1024;
+// Shared memory of a CTA of which an SM holds two: the next call's CTAs set up
+// beside this one's.
+constexpr int SMEM_HALF = 113 * 1024;
 
 __device__ int g_stall_copies;   // test hook: the producer issues no copies
 
@@ -124,8 +127,9 @@ struct Ring {
 // Scales of the k blocks [kb0, kb1): [block][row] of this CTA's rows, and the
 // weight's [block][2]; one of the two scale warps writes 64 rows.
 struct Scales {
-  float *a;   // [CHUNKS][CHUNK][BM]
+  float *a;   // [CHUNKS][CHUNK][rows]
   float *w;   // [CHUNKS][CHUNK][2]
+  int rows;   // of the tile, at most BM
 };
 
 __device__ __forceinline__ void load_scales(const MatmulParams &p, Control &c, const Scales &sc, Ring &ring, int m0,
@@ -134,7 +138,7 @@ __device__ __forceinline__ void load_scales(const MatmulParams &p, Control &c, c
   for (int kb = kb0; kb < kb1; kb += CHUNK) {
     tc::wait_or_abort(&c.scale_empty[ring.at], ring.phase ^ 1u, abort);
     __syncwarp();
-    float *a = sc.a + ring.at * CHUNK * BM, *w = sc.w + ring.at * CHUNK * 2;
+    float *a = sc.a + ring.at * CHUNK * sc.rows, *w = sc.w + ring.at * CHUNK * 2;
     float v[2][CHUNK];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -150,7 +154,10 @@ __device__ __forceinline__ void load_scales(const MatmulParams &p, Control &c, c
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int k = 0; k < CHUNK; ++k) a[k * BM + warp * 64 + h * 32 + lane] = v[h][k];
+      for (int k = 0; k < CHUNK; ++k) {
+        const int row = warp * 64 + h * 32 + lane;
+        if (row < sc.rows) a[k * sc.rows + row] = v[h][k];
+      }
     if (warp == 0 && lane < 2 * CHUNK) w[lane % CHUNK * 2 + lane / CHUNK] = sw;
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&c.scale_full[ring.at]);
@@ -173,7 +180,7 @@ __device__ __forceinline__ void add_blocks(Control &c, const Scales &sc, Ring &a
       __syncwarp();
     }
     const int at = scale_ring.at * CHUNK + in_chunk;
-    const float scale = sc.a[at * BM + row] * sc.w[at * 2 + w_block];
+    const float scale = sc.a[at * sc.rows + row] * sc.w[at * 2 + w_block];
     if (in_chunk == CHUNK - 1 || k == blocks - 1) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&c.scale_empty[scale_ring.at]);
@@ -279,13 +286,13 @@ __device__ __forceinline__ void init_control(Control &c, int stages, int bufs, u
 template <int BN>
 __global__ void __launch_bounds__(NT, 1)
 k_matmul_split(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w) {
-  constexpr int BUFS = 4;
+  constexpr int BUFS = 256 / BN;         // half of the tensor memory: the other is the next call's
   constexpr int NC = BN / 2;             // columns of an epilogue warp group
   extern __shared__ __align__(1024) unsigned char smem[];
   Control &c = *reinterpret_cast<Control *>(smem);
   unsigned char *ring = smem + SMEM_CTRL;
-  const Scales sc = {reinterpret_cast<float *>(ring + RING_BYTES),
-                     reinterpret_cast<float *>(ring + RING_BYTES) + CHUNKS * CHUNK * BM};
+  float *scales_at = reinterpret_cast<float *>(ring + p.ring_bytes);
+  const Scales sc = {scales_at, scales_at + CHUNKS * CHUNK * p.a_rows, p.a_rows};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort = &c.abort;
   const int a_bytes = p.a_rows * 128, stage_bytes = a_bytes + BN * 128;
@@ -372,8 +379,8 @@ k_matmul_split(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
     uint64_t acc[NC / 2];
 #pragma unroll
     for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
-    add_blocks<NC>(c, sc, acc_ring, scale_ring, BUFS, BN, tmem + (uint32_t(sub * 32) << 16) + uint32_t(col), r, 0,
-                   kb1 - kb0, sub * 32 < rows, lane, [&](int b) { tc::mbar_arrive(&c.acc_empty[b]); }, acc);
+    add_blocks<NC>(c, sc, acc_ring, scale_ring, BUFS, BN, tmem + (uint32_t(sub * 32) << 16) + uint32_t(col),
+                   min(r, p.a_rows - 1), 0, kb1 - kb0, sub * 32 < rows, lane, [&](int b) { tc::mbar_arrive(&c.acc_empty[b]); }, acc);
     if (p.splits == 1) {
       if (r < rows) store_row<NC>(p, m0 + r, n0 + col, acc);
     } else if (r < rows) {
@@ -430,7 +437,7 @@ k_matmul_pair(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, co
   Control &c = *reinterpret_cast<Control *>(smem);
   unsigned char *ring = smem + SMEM_CTRL;
   const Scales sc = {reinterpret_cast<float *>(ring + RING_BYTES),
-                     reinterpret_cast<float *>(ring + RING_BYTES) + CHUNKS * CHUNK * BM};
+                     reinterpret_cast<float *>(ring + RING_BYTES) + CHUNKS * CHUNK * BM, BM};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort = &c.abort;
   const uint32_t rank = cluster_rank();
@@ -549,11 +556,11 @@ k_matmul_pair(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, co
 
 template <class Kernel>
 cudaError_t launch(Kernel k, const MatmulParams &p, const CUtensorMap &tm_a, const CUtensorMap &tm_w, int grid,
-                   int cluster, cudaStream_t stream) {
+                   int cluster, int smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -637,17 +644,30 @@ cudaError_t launch_block_matmul(const MatmulParams &args, const MatmulPlan &plan
         !encode_rows_sw128(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weight, p.n, p.k, p.weight_stride, 128, BM))
       return cudaErrorInvalidValue;
     const int pairs = int(std::min<int64_t>(pair_tiles, plan.pairs));
-    return launch(k_matmul_pair, p, tm_a, tm_w, 2 * pairs, 1, stream);   // the kernel's own cluster size
+    return launch(k_matmul_pair, p, tm_a, tm_w, 2 * pairs, 1, SMEM_BYTES, stream);   // the kernel's own cluster size
   }
   p.n_tiles = (p.n + bn - 1) / bn;
   p.a_rows = std::min(BM, (p.m + 7) / 8 * 8);
-  p.stages = std::min(STAGES_MAX, RING_BYTES / (p.a_rows * 128 + bn * 128));
+  // The stages that fit into half of an SM's shared memory, if they hold the
+  // bytes that keep the memory busy (64 KB of weights an SM), else all of it;
+  // a split tile's sums need BN x a_rows floats of them afterwards, and the
+  // tensor core reads 128 rows of `values` whatever their number.
+  const int stage_bytes = p.a_rows * 128 + bn * 128;
+  const int scale_bytes = CHUNKS * CHUNK * (p.a_rows + 2) * 4;
+  const int slack = std::max(0, BM * 128 - stage_bytes);
+  int smem = SMEM_HALF;
+  auto stages = [&](int bytes) {
+    return std::min(STAGES_MAX, (bytes - SMEM_CTRL - scale_bytes - slack - 1024) / stage_bytes);
+  };
+  p.stages = stages(smem);
+  if (p.stages * bn * 128 < 64 * 1024 || p.stages * stage_bytes < bn * p.a_rows * 4) p.stages = stages(smem = SMEM_BYTES);
+  p.ring_bytes = p.stages * stage_bytes + slack;
   if (!encode_rows_sw128(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.values, p.m, p.k, p.values_stride, 128, p.a_rows) ||
       !encode_rows_sw128(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weight, p.n, p.k, p.weight_stride, 128, bn))
     return cudaErrorInvalidValue;
   const int grid = p.m_tiles * p.n_tiles * p.splits;
-  return bn == 128 ? launch(k_matmul_split<128>, p, tm_a, tm_w, grid, p.splits, stream)
-                   : launch(k_matmul_split<64>, p, tm_a, tm_w, grid, p.splits, stream);
+  return bn == 128 ? launch(k_matmul_split<128>, p, tm_a, tm_w, grid, p.splits, smem, stream)
+                   : launch(k_matmul_split<64>, p, tm_a, tm_w, grid, p.splits, smem, stream);
 }
 
 }  // namespace mhc
