@@ -38,9 +38,6 @@ constexpr int SMEM_CTRL = 1024;
 constexpr int SMEM_SCALES = CHUNKS * CHUNK * (BM + 2) * 4 + 1024;   // and the ring's alignment
 constexpr int SMEM_BYTES = 227 * 1024;
 constexpr int RING_BYTES = (SMEM_BYTES - SMEM_CTRL - SMEM_SCALES) / 1024 * 1024;
-// Shared memory of a CTA of which an SM holds two: the next call's CTAs set up
-// beside this one's.
-constexpr int SMEM_HALF = 113 * 1024;
 
 __device__ int g_stall_copies;   // test hook: the producer issues no copies
 
@@ -282,27 +279,31 @@ __device__ __forceinline__ void init_control(Control &c, int stages, int bufs, u
 
 // ------------------------------------------------------------ split kernel
 // Cluster `tile` of p.splits CTAs: BM rows by BN columns, CTA r the k blocks
-// [k_blocks r / splits, k_blocks (r + 1) / splits).
-template <int BN>
+// [k_blocks r / splits, k_blocks (r + 1) / splits).  The roles hand each other
+// groups of G blocks, each block with an accumulator of its own: a wait between
+// two roles takes some hundred clocks, as long as the few rows' work for a block
+// (one row of 6144 x 5120, a wait for each block: 11.0 us).
+template <int BN, int G>
 __global__ void __launch_bounds__(NT, 1)
 k_matmul_split(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w) {
-  constexpr int BUFS = 256 / BN;         // half of the tensor memory: the other is the next call's
+  constexpr int BUFS = 2;                // accumulators of two groups
   constexpr int NC = BN / 2;             // columns of an epilogue warp group
+  static_assert(BUFS * G * BN == 512 && CHUNK % G == 0, "all of the tensor memory; a group lies in a chunk of scales");
   extern __shared__ __align__(1024) unsigned char smem[];
   Control &c = *reinterpret_cast<Control *>(smem);
   unsigned char *ring = smem + SMEM_CTRL;
-  float *scales_at = reinterpret_cast<float *>(ring + p.ring_bytes);
-  const Scales sc = {scales_at, scales_at + CHUNKS * CHUNK * p.a_rows, p.a_rows};
+  const Scales sc = {reinterpret_cast<float *>(ring + RING_BYTES),
+                     reinterpret_cast<float *>(ring + RING_BYTES) + CHUNKS * CHUNK * BM, BM};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort = &c.abort;
-  const int a_bytes = p.a_rows * 128, stage_bytes = a_bytes + BN * 128;
+  const int a_bytes = p.a_rows * 128, block_bytes = a_bytes + BN * 128;
 
   if (threadIdx.x == 0) {
     init_control(c, p.stages, BUFS, EPI_WARPS);
     tc::tma_prefetch_desc(&tm_a);
     tc::tma_prefetch_desc(&tm_w);
   }
-  if (warp == SCALE_WARP0) tc::tmem_alloc(&c.tmem, BUFS * BN);
+  if (warp == SCALE_WARP0) tc::tmem_alloc(&c.tmem, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -315,57 +316,64 @@ k_matmul_split(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
   const int kb0 = p.k_blocks * rank / p.splits, kb1 = p.k_blocks * (rank + 1) / p.splits;
   const int rows = min(BM, p.m - m0);    // of the tile
 
+  // The copies and the MMAs are issued by one thread that runs their whole
+  // loop: under a predicate carried from outside a loop an MMA takes some 25
+  // clocks more to issue (its operands leave the uniform registers).
   if (warp == 0) {
     // ---------------------------------------------------------- producer
-    Ring at;
-    bool ok = true;
-    const bool leader = tc::elect_one();
-    int issued = 0;
-    if (!g_stall_copies)
-      for (int kb = kb0; kb < kb1; ++kb) {
-        ok = tc::wait_or_abort(&c.empty[at.at], at.phase ^ 1u, abort);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        if (leader) {
-          unsigned char *dst = ring + size_t(at.at) * stage_bytes;
-          tc::mbar_arrive_expect_tx(&c.full[at.at], uint32_t(stage_bytes));
-          tc::tma_load_2d(dst + a_bytes, &tm_w, kb * 128, n0, &c.full[at.at]);
-          tc::tma_load_2d(dst, &tm_a, kb * 128, m0, &c.full[at.at]);
+    if (tc::elect_one()) {
+      Ring at;
+      int issued = 0;
+      if (!g_stall_copies)
+        for (int kb = kb0; kb < kb1; kb += G) {
+          if (!tc::wait_or_abort(&c.empty[at.at], at.phase ^ 1u, abort)) break;
+          const int blocks = min(G, kb1 - kb);
+          unsigned char *dst = ring + size_t(at.at) * G * block_bytes;
+          tc::mbar_arrive_expect_tx(&c.full[at.at], uint32_t(blocks * block_bytes));
+          for (int q = 0; q < blocks; ++q, dst += block_bytes) {
+            tc::tma_load_2d(dst + a_bytes, &tm_w, (kb + q) * 128, n0, &c.full[at.at]);
+            tc::tma_load_2d(dst, &tm_a, (kb + q) * 128, m0, &c.full[at.at]);
+          }
+          at.next(p.stages);
+          ++issued;
         }
-        __syncwarp();
-        at.next(p.stages);
-        ++issued;
-      }
-    // copies in flight land before the CTA's shared memory goes
-    if (*abort)
-      for (int i = max(0, issued - p.stages); i < issued; ++i)
-        tc::mbar_wait_bounded(&c.full[i % p.stages], uint32_t((i / p.stages) & 1), tc::SUB_WAIT_LIMIT);
+      // copies in flight land before the CTA's shared memory goes
+      if (*abort)
+        for (int i = max(0, issued - p.stages); i < issued; ++i)
+          tc::mbar_wait_bounded(&c.full[i % p.stages], uint32_t((i / p.stages) & 1), tc::SUB_WAIT_LIMIT);
+    }
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer
-    Ring at, acc;
-    const bool leader = tc::elect_one();
     const uint32_t idesc = tc::idesc_e4m3_f32(BM, BN);
     const uint64_t a0 = tc::desc_sw128(ring), b0 = tc::desc_sw128(ring + a_bytes);
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const bool ok = tc::wait_or_abort(&c.full[at.at], at.phase, abort) &&
-                      tc::wait_or_abort(&c.acc_empty[acc.at], acc.phase ^ 1u, abort);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc::fence_after_sync();
-      const uint64_t step = uint64_t(at.at * (stage_bytes >> 4));
-      if (leader) {
+    if (tc::elect_one()) {
+      Ring at, acc;
+      bool full = false, released = false;   // the next group's barriers, tested beside this one's products
+      for (int kb = kb0; kb < kb1; kb += G) {
+        if (!tc::wait_or_abort(full, &c.full[at.at], at.phase, abort) ||
+            !tc::wait_or_abort(released, &c.acc_empty[acc.at], acc.phase ^ 1u, abort))
+          break;
+        const Ring at0 = at, acc0 = acc;
+        at.next(p.stages);
+        acc.next(BUFS);
+        full = tc::mbar_try_wait(&c.full[at.at], at.phase);
+        released = tc::mbar_try_wait(&c.acc_empty[acc.at], acc.phase ^ 1u);
+        tc::fence_after_sync();
+        const int blocks = min(G, kb1 - kb);
+        for (int q = 0; q < blocks; ++q) {
+          const uint64_t step = uint64_t((at0.at * G + q) * (block_bytes >> 4));
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc::mma_e4m3(tmem + uint32_t(acc.at * BN), a0 + step + 2 * ks, b0 + step + 2 * ks, idesc, ks != 0);
-        tc::mma_commit(&c.empty[at.at]);
-        tc::mma_commit(&c.acc_full[acc.at]);
+          for (int ks = 0; ks < 4; ++ks)
+            tc::mma_e4m3(tmem + uint32_t((acc0.at * G + q) * BN), a0 + step + 2 * ks, b0 + step + 2 * ks, idesc,
+                         ks != 0);
+        }
+        tc::mma_commit(&c.empty[at0.at]);
+        tc::mma_commit(&c.acc_full[acc0.at]);
       }
-      __syncwarp();
-      at.next(p.stages);
-      acc.next(BUFS);
+      // no MMA is in flight when the tensor memory goes
+      tc::mma_commit(&c.drain);
+      tc::mbar_wait_bounded(&c.drain, 0u, tc::SUB_WAIT_LIMIT);
     }
-    // no MMA is in flight when the tensor memory goes
-    if (leader) tc::mma_commit(&c.drain);
-    __syncwarp();
-    tc::mbar_wait_bounded(&c.drain, 0u, tc::SUB_WAIT_LIMIT);
   } else if (warp < EPI_WARP0) {
     Ring scales;
     load_scales(p, c, sc, scales, m0, n0 / QBLOCK, kb0, kb1, warp - SCALE_WARP0, lane);
@@ -375,12 +383,53 @@ k_matmul_split(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
     // whatever is there (the waits return at once).
     const int sub = warp % 4, group = (warp - EPI_WARP0) / 4, r = sub * 32 + lane;
     const int col = group * NC;
-    Ring acc_ring, scale_ring;
+    const bool rows_live = sub * 32 < rows;
+    const uint32_t lane_base = tmem + (uint32_t(sub * 32) << 16) + uint32_t(col);
+    Ring buf, chunk;
     uint64_t acc[NC / 2];
 #pragma unroll
     for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
-    add_blocks<NC>(c, sc, acc_ring, scale_ring, BUFS, BN, tmem + (uint32_t(sub * 32) << 16) + uint32_t(col),
-                   min(r, p.a_rows - 1), 0, kb1 - kb0, sub * 32 < rows, lane, [&](int b) { tc::mbar_arrive(&c.acc_empty[b]); }, acc);
+    for (int k = 0; k < kb1 - kb0; k += G) {
+      const int blocks = min(G, kb1 - kb0 - k);
+      if (k % CHUNK == 0) {
+        tc::wait_or_abort_inline(&c.scale_full[chunk.at], chunk.phase, abort);
+        __syncwarp();
+      }
+      const int s0 = chunk.at * CHUNK + k % CHUNK;
+      float scale[G];
+#pragma unroll
+      for (int q = 0; q < G; ++q) scale[q] = sc.a[(s0 + q) * BM + r] * sc.w[(s0 + q) * 2];
+      if (k % CHUNK + G == CHUNK || k + G >= kb1 - kb0) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&c.scale_empty[chunk.at]);
+        chunk.next(CHUNKS);
+      }
+      tc::wait_or_abort_inline(&c.acc_full[buf.at], buf.phase, abort);
+      __syncwarp();
+      tc::fence_after_sync();
+      if (rows_live) {
+#pragma unroll
+        for (int q = 0; q < G; ++q)
+          if (q < blocks) {
+            uint32_t d[NC / 32][32];
+#pragma unroll
+            for (int h = 0; h < NC / 32; ++h)
+              tc::tmem_ld32_async(lane_base + uint32_t((buf.at * G + q) * BN + h * 32), d[h]);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < NC / 32; ++h) tc::tmem_hold(d[h]);
+            const uint64_t s2 = tc::pair(scale[q], scale[q]);
+#pragma unroll
+            for (int h = 0; h < NC / 32; ++h)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) tc::fma_pair(acc[h * 16 + i], d[h][2 * i], d[h][2 * i + 1], s2);
+          }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&c.acc_empty[buf.at]);
+      buf.next(BUFS);
+    }
     if (p.splits == 1) {
       if (r < rows) store_row<NC>(p, m0 + r, n0 + col, acc);
     } else if (r < rows) {
@@ -416,7 +465,7 @@ k_matmul_split(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == SCALE_WARP0) tc::tmem_dealloc(tmem, BUFS * BN);
+  if (warp == SCALE_WARP0) tc::tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0 && c.abort) atomicOr(p.err, 2u);
 }
 
@@ -599,11 +648,11 @@ cudaError_t matmul_stall_copies(int on) { return cudaMemcpyToSymbol(g_stall_copi
 
 cudaError_t matmul_setup(int sms, MatmulPlan *plan) {
   cudaError_t e = cudaSuccess;
-  for (const void *k : {(const void *)k_matmul_split<64>, (const void *)k_matmul_split<128>, (const void *)k_matmul_pair})
+  for (const void *k : {(const void *)k_matmul_split<64, 4>, (const void *)k_matmul_split<128, 2>, (const void *)k_matmul_pair})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   plan->clusters[1] = sms;
   for (int s = 2; s <= MATMUL_SPLITS_MAX && e == cudaSuccess; ++s)
-    e = active_clusters(k_matmul_split<128>, s, &plan->clusters[s]);
+    e = active_clusters(k_matmul_split<128, 2>, s, &plan->clusters[s]);
   if (e == cudaSuccess) e = active_clusters(k_matmul_pair, 2, &plan->pairs);
   if (e == cudaSuccess && plan->pairs < 1) e = cudaErrorNotSupported;
   return e;
@@ -648,26 +697,16 @@ cudaError_t launch_block_matmul(const MatmulParams &args, const MatmulPlan &plan
   }
   p.n_tiles = (p.n + bn - 1) / bn;
   p.a_rows = std::min(BM, (p.m + 7) / 8 * 8);
-  // The stages that fit into half of an SM's shared memory, if they hold the
-  // bytes that keep the memory busy (64 KB of weights an SM), else all of it;
-  // a split tile's sums need BN x a_rows floats of them afterwards, and the
-  // tensor core reads 128 rows of `values` whatever their number.
-  const int stage_bytes = p.a_rows * 128 + bn * 128;
-  const int scale_bytes = CHUNKS * CHUNK * (p.a_rows + 2) * 4;
-  const int slack = std::max(0, BM * 128 - stage_bytes);
-  int smem = SMEM_HALF;
-  auto stages = [&](int bytes) {
-    return std::min(STAGES_MAX, (bytes - SMEM_CTRL - scale_bytes - slack - 1024) / stage_bytes);
-  };
-  p.stages = stages(smem);
-  if (p.stages * bn * 128 < 64 * 1024 || p.stages * stage_bytes < bn * p.a_rows * 4) p.stages = stages(smem = SMEM_BYTES);
-  p.ring_bytes = p.stages * stage_bytes + slack;
+  // the tensor core reads 128 rows of `values` whatever their number: the last
+  // block's may reach past its own end
+  const int block_bytes = p.a_rows * 128 + bn * 128, group = 256 / bn;
+  p.stages = std::min(STAGES_MAX, (RING_BYTES - std::max(0, BM * 128 - block_bytes)) / (group * block_bytes));
   if (!encode_rows_sw128(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.values, p.m, p.k, p.values_stride, 128, p.a_rows) ||
       !encode_rows_sw128(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weight, p.n, p.k, p.weight_stride, 128, bn))
     return cudaErrorInvalidValue;
   const int grid = p.m_tiles * p.n_tiles * p.splits;
-  return bn == 128 ? launch(k_matmul_split<128>, p, tm_a, tm_w, grid, p.splits, smem, stream)
-                   : launch(k_matmul_split<64>, p, tm_a, tm_w, grid, p.splits, smem, stream);
+  return bn == 128 ? launch(k_matmul_split<128, 2>, p, tm_a, tm_w, grid, p.splits, SMEM_BYTES, stream)
+                   : launch(k_matmul_split<64, 4>, p, tm_a, tm_w, grid, p.splits, SMEM_BYTES, stream);
 }
 
 }  // namespace mhc

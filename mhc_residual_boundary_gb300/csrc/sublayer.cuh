@@ -46,7 +46,6 @@ struct MatmulParams {
   // set by the launcher
   int k_blocks, n_blocks, m_tiles, n_tiles, splits, stages;
   int a_rows;                             // rows of a stage's `values` tile
-  int ring_bytes;                         // of the stages
 };
 
 constexpr int MATMUL_SPLITS_MAX = 8;

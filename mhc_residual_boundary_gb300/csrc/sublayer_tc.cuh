@@ -32,6 +32,11 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
   return mbar_try_wait(bar, parity) || wait_poll(bar, parity, abort);
 }
 
+// A wait in two parts: a test, whose answer arrives (some hundred clocks later)
+// while the thread goes on, and the wait for it.
+__device__ __forceinline__ bool wait_or_abort(bool tested, uint64_t *bar, uint32_t parity, volatile int *abort) {
+  return tested || wait_poll(bar, parity, abort);
+}
 // The same without a call: for code that holds most registers.
 __device__ __forceinline__ void wait_or_abort_inline(uint64_t *bar, uint32_t parity, volatile int *abort) {
 #pragma unroll 1
@@ -95,8 +100,7 @@ __device__ __forceinline__ void tmem_hold(uint32_t (&r)[N]) {
 
 // acc += d * s on a pair of FP32 values (two IEEE fused multiply-adds).
 __device__ __forceinline__ void fma_pair(uint64_t &acc, uint32_t d0, uint32_t d1, uint64_t s) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
+  const uint64_t d = uint64_t(d1) << 32 | d0;
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(s));
 }
 __device__ __forceinline__ uint64_t pair(float a, float b) {
