@@ -507,70 +507,70 @@ k_matmul_pair(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, co
   const int tiles = p.m_tiles * p.n_tiles, pairs = int(gridDim.x) / 2, first = int(blockIdx.x) / 2;
 
   if (warp < EPI_WARP0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // -------------------------------------------------------- producer
-      Ring at;
-      bool ok = true;
-      const bool leader = tc::elect_one();
-      int issued = 0;
-      if (!g_stall_copies)
+      if (tc::elect_one()) {
+        Ring at;
+        int issued = 0;
+        bool ok = !g_stall_copies;
         for (int tile = first; tile < tiles && ok; tile += pairs) {
           const int m0 = tile % p.m_tiles * 256 + int(rank) * BM, n0 = tile / p.m_tiles * PAIR_N + int(rank) * BM;
           for (int kb = 0; kb < p.k_blocks; ++kb) {
             ok = tc::wait_or_abort(&c.empty[at.at], at.phase ^ 1u, abort);
-            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            if (leader) {
-              unsigned char *dst = ring + size_t(at.at) * PAIR_STAGE;
-              tc::mbar_arrive_expect_tx(&c.full[at.at], PAIR_STAGE);
-              tc::tma_load_2d(dst, &tm_a, kb * 128, m0, &c.full[at.at]);
-              tc::tma_load_2d(dst + BM * 128, &tm_w, kb * 128, n0, &c.full[at.at]);
-            }
-            __syncwarp();
+            unsigned char *dst = ring + size_t(at.at) * PAIR_STAGE;
+            tc::mbar_arrive_expect_tx(&c.full[at.at], PAIR_STAGE);
+            tc::tma_load_2d(dst, &tm_a, kb * 128, m0, &c.full[at.at]);
+            tc::tma_load_2d(dst + BM * 128, &tm_w, kb * 128, n0, &c.full[at.at]);
             at.next(PAIR_STAGES);
             ++issued;
           }
         }
-      if (*abort)
-        for (int i = max(0, issued - PAIR_STAGES); i < issued; ++i)
-          tc::mbar_wait_bounded(&c.full[i % PAIR_STAGES], uint32_t((i / PAIR_STAGES) & 1), tc::SUB_WAIT_LIMIT);
+        if (*abort)
+          for (int i = max(0, issued - PAIR_STAGES); i < issued; ++i)
+            tc::mbar_wait_bounded(&c.full[i % PAIR_STAGES], uint32_t((i / PAIR_STAGES) & 1), tc::SUB_WAIT_LIMIT);
+      }
     } else if (warp == 1) {
       // ------------------------------------------- MMA issuer / its peer
-      Ring at, acc;
-      bool ok = true;
-      const bool leader = tc::elect_one();
       const uint32_t idesc = tc::idesc_e4m3_f32(256, PAIR_N);
       const uint64_t a0 = tc::desc_sw128(ring), b0 = tc::desc_sw128(ring + BM * 128);
-      for (int tile = first; tile < tiles && ok; tile += pairs)
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
-          ok = tc::wait_or_abort(&c.full[at.at], at.phase, abort);
-          if (rank == 0)
-            ok = ok && tc::wait_or_abort(&c.peer_full[at.at], at.phase, abort) &&
-                 tc::wait_or_abort(&c.acc_empty[acc.at], acc.phase ^ 1u, abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc::fence_after_sync();
-          if (leader) {
-            if (rank == 0) {
-              const uint64_t step = uint64_t(at.at * (PAIR_STAGE >> 4));
+      const int blocks = (tiles - first + pairs - 1) / pairs * p.k_blocks;
+      if (tc::elect_one()) {
+        Ring at, acc;
+        if (rank == 0) {
+          bool full = false, peer = false, released = false;   // the next block's, tested beside this one's products
+          for (int n = 0; n < blocks; ++n) {
+            if (!tc::wait_or_abort(full, &c.full[at.at], at.phase, abort) ||
+                !tc::wait_or_abort(peer, &c.peer_full[at.at], at.phase, abort) ||
+                !tc::wait_or_abort(released, &c.acc_empty[acc.at], acc.phase ^ 1u, abort))
+              break;
+            const Ring at0 = at, acc0 = acc;
+            at.next(PAIR_STAGES);
+            acc.next(BUFS);
+            full = tc::mbar_test_wait(&c.full[at.at], at.phase);
+            peer = tc::mbar_test_wait(&c.peer_full[at.at], at.phase);
+            released = tc::mbar_test_wait(&c.acc_empty[acc.at], acc.phase ^ 1u);
+            tc::fence_after_sync();
+            const uint64_t step = uint64_t(at0.at * (PAIR_STAGE >> 4));
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                mma2_e4m3(tmem + uint32_t(acc.at * PAIR_N), a0 + step + 2 * ks, b0 + step + 2 * ks, idesc, ks != 0);
-              mma2_commit(&c.empty[at.at]);
-              mma2_commit(&c.acc_full[acc.at]);
-            } else {
-              arrive_peer(peer_addr(&c.peer_full[at.at], 0));
-            }
+            for (int ks = 0; ks < 4; ++ks)
+              mma2_e4m3(tmem + uint32_t(acc0.at * PAIR_N), a0 + step + 2 * ks, b0 + step + 2 * ks, idesc, ks != 0);
+            mma2_commit(&c.empty[at0.at]);
+            mma2_commit(&c.acc_full[acc0.at]);
           }
-          __syncwarp();
-          at.next(PAIR_STAGES);
-          acc.next(BUFS);
+          // no MMA is in flight when the tensor memory goes
+          mma2_commit(&c.drain);
+          tc::mbar_wait_bounded(&c.drain, 0u, tc::SUB_WAIT_LIMIT);
+        } else {
+          const uint32_t told = peer_addr(&c.peer_full[0], 0);
+          for (int n = 0; n < blocks; ++n) {
+            if (!tc::wait_or_abort(&c.full[at.at], at.phase, abort)) break;
+            arrive_peer(told + uint32_t(at.at) * 8);
+            at.next(PAIR_STAGES);
+          }
         }
-      // no MMA is in flight when the tensor memory goes
-      if (rank == 0 && leader) mma2_commit(&c.drain);
-      __syncwarp();
-      if (rank == 0) tc::mbar_wait_bounded(&c.drain, 0u, tc::SUB_WAIT_LIMIT);
+      }
     } else {
       Ring scales;
       for (int tile = first; tile < tiles; tile += pairs)
@@ -579,7 +579,7 @@ k_matmul_pair(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, co
     }
   } else {
     // ---------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int sub = warp % 4, group = (warp - EPI_WARP0) / 4, r = sub * 32 + lane;
     const int col = group * NC;
     const uint32_t release0 = peer_addr(&c.acc_empty[0], 0);

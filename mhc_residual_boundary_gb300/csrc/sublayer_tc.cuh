@@ -33,7 +33,19 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
 }
 
 // A wait in two parts: a test, whose answer arrives (some hundred clocks later)
-// while the thread goes on, and the wait for it.
+// while the thread goes on, and the wait for it.  The test is test_wait: a
+// try_wait may suspend the thread until the phase completes.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool wait_or_abort(bool tested, uint64_t *bar, uint32_t parity, volatile int *abort) {
   return tested || wait_poll(bar, parity, abort);
 }
