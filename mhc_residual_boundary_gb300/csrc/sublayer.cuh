@@ -51,8 +51,7 @@ struct MatmulParams {
 constexpr int MATMUL_SPLITS_MAX = 8;
 // What runs at once on this GPU.
 struct MatmulPlan {
-  int clusters[MATMUL_SPLITS_MAX + 1];    // clusters of that many CTAs (split kernel)
-  int pairs;                              // CTA pairs (pair kernel)
+  int clusters[MATMUL_SPLITS_MAX + 1];    // clusters of that many CTAs
 };
 
 cudaError_t matmul_setup(int sms, MatmulPlan *plan);
