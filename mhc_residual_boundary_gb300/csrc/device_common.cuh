@@ -305,4 +305,12 @@ __device__ __forceinline__ void post_and_sinkhorn4(const MixArgs p, int t, const
   }
 }
 
+// 1 / x within one unit in the last place, subnormal results included: the
+// correctly rounded division costs as much as all else in a SiLU.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 }  // namespace mhc

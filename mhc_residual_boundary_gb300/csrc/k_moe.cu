@@ -202,14 +202,18 @@ __device__ __forceinline__ float from_e4m3(uint32_t b) {
 }
 
 // ------------------------------------------------------------------ route
-// Logits.  An item is an expert and eight tokens; a CTA's warps take as many
-// items at a time (1, 2, 3 or 6) as spread them over all CTAs, the hidden size
-// being spread over the warps of an item.
+// An item is an expert and eight tokens; a CTA's warps take as many items at a
+// time (1, 2, 3 or 6) as spread them over all CTAs.
+__device__ __forceinline__ int router_groups(const MoeParams &p) {
+  int groups = 1;
+  while (groups < 6 && p.experts * ((p.m + 7) / 8) > groups * int(gridDim.x)) groups = groups == 3 ? 6 : groups + 1;
+  return groups;
+}
+// Logits, the hidden size being spread over the warps of an item.
 __device__ __forceinline__ void route_logits(const MoeParams &p, Shared &sh) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int frags = p.hidden / 8, items = p.experts * ((p.m + 7) / 8);
-  int groups = 1;
-  while (groups < 6 && items > groups * int(gridDim.x)) groups = groups == 3 ? 6 : groups + 1;
+  const int groups = router_groups(p);
   const int warps = WARPS / groups, group = warp / warps;
   for (int i0 = blockIdx.x * groups; i0 < items; i0 += gridDim.x * groups) {
     const int item = i0 + group, e = item % p.experts, t0 = item / p.experts * 8;
@@ -255,6 +259,22 @@ __device__ __forceinline__ void route_logits(const MoeParams &p, Shared &sh) {
       p.scratch.logits[size_t(t0 + lane) * p.experts + e] = s;
     }
   }
+}
+
+// Asks for the router's rows of this CTA's first items and for the bias: they
+// come from memory while the CTA sets itself up.
+__device__ __forceinline__ void request_router(const MoeParams &p) {
+  const int groups = router_groups(p), lines = (p.hidden * (p.router_f32 ? 4 : 2) + 127) / 128;
+  const size_t row = size_t(p.hidden) * (p.router_f32 ? 4 : 2);
+  const int items = min(groups, p.experts * ((p.m + 7) / 8) - int(blockIdx.x) * groups);
+  for (int l = threadIdx.x; l < items * lines; l += NT) {
+    const int g = l / lines, e = (int(blockIdx.x) * groups + g) % p.experts;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p.router) + size_t(e) * row +
+                                                 min(size_t(l - g * lines) * 128, row - 1)));
+  }
+  if (p.bias)
+    for (int e = threadIdx.x * 32; e < p.experts; e += NT * 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.bias + e));
 }
 
 // The E4M3 pieces of x: a row a CTA, from the last CTA down (the first ones
@@ -308,10 +328,11 @@ __device__ __forceinline__ void split_x(const MoeParams &p, Shared &sh) {
   }
 }
 
-// Order-preserving unsigned key of a score; a NaN is below every number.
+// Order-preserving unsigned key of a score, never 0; a NaN is below every
+// number.
 __device__ __forceinline__ uint32_t score_key(float v) {
   const uint32_t b = __float_as_uint(v);
-  if ((b & 0x7fffffffu) > 0x7f800000u) return 0u;
+  if ((b & 0x7fffffffu) > 0x7f800000u) return 1u;
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
@@ -338,38 +359,41 @@ __device__ __noinline__ void choose(const MoeParams &p, Shared &sh, int t, const
       score[i] = i * 32 + lane < p.experts ? expf(score[i] - peak) : 0.f;
       sum += score[i];
     }
-    sum = warp_sum(sum);
+    const float inverse = 1.f / warp_sum(sum);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) score[i] = score[i] / sum;
+    for (int i = 0; i < PER; ++i) score[i] *= inverse;
   } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) score[i] = 1.f / (1.f + expf(-score[i]));
+    for (int i = 0; i < PER; ++i) score[i] = rcp_approx(1.f + expf(-score[i]));
   }
-  uint32_t taken = 0;   // bit i: expert i * 32 + lane is chosen or does not exist
+  // key 0: the expert is chosen already, or does not exist
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = i * 32 + lane;
-    if (e >= p.experts) taken |= 1u << i;
     key[i] = e < p.experts ? score_key(p.bias ? score[i] + __ldg(p.bias + e) : score[i]) : 0u;
   }
   float total = 0.f, mine = 0.f;
   int mine_e = 0;
+#pragma unroll 1
   for (int k = 0; k < p.top_k; ++k) {
-    uint32_t best = 0, at = 0xffffffffu;
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) best = max(best, key[i]);
+    // the largest key, then the lowest expert that has it
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    uint32_t at = 0xffffffffu;
     float value = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (!(taken >> i & 1u) && (at == 0xffffffffu || key[i] > best)) {
-        best = key[i];
+    for (int i = PER - 1; i >= 0; --i)
+      if (key[i] == top) {
         at = uint32_t(i * 32 + lane);
         value = score[i];
       }
-    // the largest key, then the lowest expert among the lanes that hold it
-    const bool any = at != 0xffffffffu;
-    const uint32_t top = __reduce_max_sync(0xffffffffu, any ? best : 0u);
-    const uint32_t winner = __reduce_min_sync(0xffffffffu, any && best == top ? at : 0xffffffffu);
+    const uint32_t winner = __reduce_min_sync(0xffffffffu, at);
     const float w = __shfl_sync(0xffffffffu, value, int(winner % 32));
-    if (at == winner) taken |= 1u << (winner / 32);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (winner == uint32_t(i * 32 + lane)) key[i] = 0u;
     total += w;
     if (lane == k) {
       mine = w;
@@ -396,19 +420,19 @@ __device__ __forceinline__ void build_plan(const MoeParams &p, Shared &sh, float
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int every = p.experts + p.shared;
   // the logits of all tokens into shared memory (256 floats a token), where
-  // they fit, before `begin` makes the memory busy
+  // they fit
   const bool fit = p.experts <= 256;
   if (fit)
     for (int i = threadIdx.x; i < p.m * p.experts; i += NT) held[i] = __ldcg(p.scratch.logits + i);
   if (p.fp8 && threadIdx.x < p.m) sh.x_scale[threadIdx.x] = __ldcg(p.scratch.x_scale + threadIdx.x);
   __syncthreads();
-  begin();
   for (int t = warp; t < p.m; t += WARPS) {
     const float *logits = (fit ? held : p.scratch.logits) + size_t(t) * p.experts;
     if (p.experts <= 64) choose<2>(p, sh, t, logits);
     else if (p.experts <= 256) choose<8>(p, sh, t, logits);
     else choose<MOE_EXPERTS_MAX / 32>(p, sh, t, logits);
   }
+  begin();
   __syncthreads();
   int active0 = 0, slots0 = 0;   // before this round of one expert a thread
   for (int e0 = 0; e0 < every; e0 += NT) {
@@ -591,6 +615,43 @@ __device__ __forceinline__ void finish_up(const MoeParams &p, const Shape &s, in
 }
 
 // ----------------------------------------------------------------- kernel
+// ---------------------------------------------------------------- the output
+// y[t] = the sum over t's routes of weight * (the pieces of the route's slot).
+// A thread has V columns and asks for nine pieces at a time.
+template <int V>
+__device__ __forceinline__ void combine(const MoeParams &p, const Shared &sh, const Shape &s, size_t width) {
+  using Vec = typename std::conditional<V == 4, float4, float>::type;
+  const int lane = threadIdx.x % 32, per_token = s.down_tiles * (4 / V);
+  const int terms = (p.top_k + p.shared) * s.down_chunks;
+  for (int n = blockIdx.x + threadIdx.x / 32 * gridDim.x; n < p.m * per_token; n += gridDim.x * WARPS) {
+    const int t = n / per_token, col = ((n - t * per_token) * 32 + lane) * V;
+    float y[V] = {};
+    int k = 0, c = 0;
+    for (int j0 = 0; j0 < terms; j0 += 9) {
+      Vec v[9];
+      float w[9];
+#pragma unroll
+      for (int j = 0; j < 9; ++j) {
+        const float *piece = p.scratch.down + (size_t(c) * p.slots + sh.route_slot[t][k]) * width + col;
+        v[j] = __ldcg(reinterpret_cast<const Vec *>(piece));
+        w[j] = k < p.top_k ? sh.route_weight[t][k] : 1.f;
+        if (j0 + j + 1 < terms && ++c == s.down_chunks) {
+          c = 0;
+          ++k;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 9; ++j)
+        if (j0 + j < terms)
+#pragma unroll
+          for (int i = 0; i < V; ++i) y[i] = fmaf(w[j], reinterpret_cast<const float *>(&v[j])[i], y[i]);
+    }
+    if (col < p.hidden)   // hidden is a multiple of 8: four columns are in or out together
+#pragma unroll
+      for (int i = 0; i < V; ++i) p.output[size_t(t) * p.hidden + col + i] = uint16_t(pack_bf16x2(y[i], 0.f));
+  }
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(NT, 1)
 k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const __grid_constant__ CUtensorMap tm_down,
@@ -609,31 +670,33 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   const int stage_bytes = A_BYTES + p.b_bytes;
   unsigned *routed = p.scratch.control, *tickets = routed + 1, *downs_done = routed + 2, *exits = routed + 3;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      tc::mbar_init(&sh.full[i], 2);
-      tc::mbar_init(&sh.empty[i], 1);
+  request_router(p);
+  // a barrier a lane: one after another they would take a microsecond
+  if (warp == 0) {
+    if (lane < p.stages) {
+      tc::mbar_init(&sh.full[lane], 2);
+      tc::mbar_init(&sh.empty[lane], 1);
     }
-    for (int i = 0; i < BUFS; ++i) {
-      tc::mbar_init(&sh.acc_full[i], 1);
-      tc::mbar_init(&sh.acc_empty[i], 4);
+    if (lane < BUFS) {
+      tc::mbar_init(&sh.acc_full[lane], 1);
+      tc::mbar_init(&sh.acc_empty[lane], 4);
     }
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&sh.sum_full[i], 4);   // one a join warp
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.sum_empty[i], 1);  // one a buffer
-    for (int i = 0; i < ITEMS; ++i) {
-      tc::mbar_init(&sh.item_full[i], 1);
-      tc::mbar_init(&sh.item_empty[i], 11);   // scale, activation, MMA, four sum and four join warps
-      tc::mbar_init(&sh.scale_full[i], 1);
+    if (lane < 4) tc::mbar_init(&sh.sum_full[lane], 4);   // one a join warp
+    if (lane < 2) tc::mbar_init(&sh.sum_empty[lane], 1);  // one a buffer
+    if (lane < ITEMS) {
+      tc::mbar_init(&sh.item_full[lane], 1);
+      tc::mbar_init(&sh.item_empty[lane], 11);   // scale, activation, MMA, four sum and four join warps
+      tc::mbar_init(&sh.scale_full[lane], 1);
     }
-    tc::mbar_init(&sh.drain, 1);
+    if (lane == 0) {
+      tc::mbar_init(&sh.drain, 1);
+      sh.abort = 0;
+      sh.issued_a = sh.issued_b = 0;
+    }
     tc::mbar_init_fence();
-    sh.abort = 0;
-    sh.issued_a = sh.issued_b = 0;
-    tc::tma_prefetch_desc(&tm_gate_up);
-    tc::tma_prefetch_desc(&tm_down);
-    tc::tma_prefetch_desc(&tm_x);
-    tc::tma_prefetch_desc(&tm_x_token);
-    tc::tma_prefetch_desc(&tm_act);
+  } else if (warp == 1 && lane < 5) {
+    tc::tma_prefetch_desc(lane == 0 ? &tm_gate_up : lane == 1 ? &tm_down : lane == 2 ? &tm_x : lane == 3 ? &tm_x_token
+                                                                                                       : &tm_act);
   }
   if (warp == 2) tc::tmem_alloc(&sh.tmem, BUFS * BUF_COLS);
   tc::fence_before_sync();
@@ -657,9 +720,9 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   }
   __syncthreads();
   const bool gave_up = *abort != 0;   // the same in all threads: no role has begun
-  // The first items are the shared experts': their weights are requested while
-  // the experts are chosen (not before: the router's own reads would wait
-  // behind them).
+  // The first items are the shared experts': their weights are requested before
+  // the list of the reached experts is made (not earlier: with the memory busy the
+  // choice itself, its instructions included, takes three times as long).
   int ahead = 0;   // blocks of this CTA's first item that are already requested
   build_plan(p, sh, sums, [&]() {
     if (warp != 0 || gave_up || int(blockIdx.x) >= p.shared * ((p.intermediate + 127) / 128) * 2 * p.up_chunks) return;
@@ -951,8 +1014,7 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
     }
     __threadfence();
   }
-  // ---- the output, once every CTA's sums are there: a warp a token's 128
-  // columns
+  // ---- the output, once every CTA's sums are there
   __syncthreads();
   if (threadIdx.x == 0) {
     atomicAdd(downs_done, 1u);
@@ -960,29 +1022,9 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   }
   __syncthreads();
   __threadfence();
-  for (int n = blockIdx.x + warp * gridDim.x; n < p.m * s.down_tiles; n += gridDim.x * WARPS) {
-    const int t = n / s.down_tiles, col = (n - t * s.down_tiles) * 128 + lane * 4;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 5
-    for (int k = 0; k < p.top_k + p.shared; ++k) {
-      const float w = k < p.top_k ? sh.route_weight[t][k] : 1.f;
-      const float4 v = add_chunks(p.scratch.down + size_t(sh.route_slot[t][k]) * down_width + col,
-                                  size_t(p.slots) * down_width, s.down_chunks);
-      y = make_float4(fmaf(w, v.x, y.x), fmaf(w, v.y, y.y), fmaf(w, v.z, y.z), fmaf(w, v.w, y.w));
-    }
-    if (col < p.hidden) {   // hidden is a multiple of 8: four columns are in or out together
-      uint16_t *out = p.output + size_t(t) * p.hidden + col;
-      const uint32_t lo = pack_bf16x2(y.x, y.y), hi = pack_bf16x2(y.z, y.w);
-      if (p.vector_out) {
-        *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
-      } else {
-        out[0] = uint16_t(lo);
-        out[1] = uint16_t(lo >> 16);
-        out[2] = uint16_t(hi);
-        out[3] = uint16_t(hi >> 16);
-      }
-    }
-  }
+  // few tokens: a column a thread, so that more warps wait at a time; many: four
+  if (p.m * s.down_tiles * 4 <= int(gridDim.x) * WARPS) combine<1>(p, sh, s, down_width);
+  else combine<4>(p, sh, s, down_width);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -1056,7 +1098,6 @@ cudaError_t launch_moe(const MoeParams &args, int sms, cudaStream_t stream) {
   const int scale_bytes = fp8 ? ITEMS * p.scale_blocks * p.m * 4 : 0;
   p.stages = std::min(STAGES_MAX, (SMEM_BYTES - SMEM_TABLES - SMEM_SLACK - p.m * 1024 - scale_bytes) /
                                       (A_BYTES + p.b_bytes));
-  p.vector_out = reinterpret_cast<uintptr_t>(p.output) % 8 == 0;
   const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t H = p.hidden, I = p.intermediate;
   const void *x = fp8 ? static_cast<const void *>(p.scratch.x_pieces) : p.x;

@@ -104,14 +104,6 @@ __global__ void __launch_bounds__(256) k_add_rms_norm(const NormParams p) {
   }
 }
 
-// 1 / x within one unit in the last place, subnormal results included: the
-// correctly rounded division costs as much as all else in swiglu.
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // One block of 128 per 16 lanes.  A thread takes U blocks a round, all of their
 // reads under way together; Index: int while the blocks can be counted in one
 // (a 64-bit division for each block costs more than its bytes).

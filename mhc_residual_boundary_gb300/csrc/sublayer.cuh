@@ -100,7 +100,6 @@ struct MoeParams {
   int stages, b_bytes;
   int up_chunks, down_chunks; // chunks of a tile's k blocks
   int scale_blocks;           // k blocks of an item at most
-  int vector_out;             // the output starts on an 8-byte boundary
 };
 
 cudaError_t moe_set_attributes();
