@@ -617,24 +617,51 @@ __device__ __forceinline__ void finish_up(const MoeParams &p, const Shape &s, in
 // ----------------------------------------------------------------- kernel
 // ---------------------------------------------------------------- the output
 // y[t] = the sum over t's routes of weight * (the pieces of the route's slot).
-// A thread has V columns and asks for nine pieces at a time.
-template <int V>
-__device__ __forceinline__ void combine(const MoeParams &p, const Shared &sh, const Shape &s, size_t width) {
-  using Vec = typename std::conditional<V == 4, float4, float>::type;
-  const int lane = threadIdx.x % 32, per_token = s.down_tiles * (4 / V);
-  const int terms = (p.top_k + p.shared) * s.down_chunks;
+__device__ __forceinline__ float route_factor(const MoeParams &p, const Shared &sh, int t, int k) {
+  return k < p.top_k ? sh.route_weight[t][k] : 1.f;
+}
+// Few tokens: eight columns a warp, the routes over four groups of its lanes,
+// three routes' pieces asked for at a time.
+__device__ __forceinline__ void combine_few(const MoeParams &p, const Shared &sh, const Shape &s, size_t width) {
+  const int lane = threadIdx.x % 32, per_token = s.down_tiles * 16, routes = p.top_k + p.shared;
   for (int n = blockIdx.x + threadIdx.x / 32 * gridDim.x; n < p.m * per_token; n += gridDim.x * WARPS) {
-    const int t = n / per_token, col = ((n - t * per_token) * 32 + lane) * V;
-    float y[V] = {};
+    const int t = n / per_token, col = (n - t * per_token) * 8 + lane % 8;
+    float y = 0.f;
+    for (int k0 = lane / 8; k0 < routes; k0 += 12) {
+      float v[3][MOE_CHUNKS];
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+#pragma unroll
+        for (int c = 0; c < MOE_CHUNKS; ++c)
+          v[j][c] = k0 + 4 * j < routes && c < s.down_chunks
+                        ? __ldcg(p.scratch.down + (size_t(c) * p.slots + sh.route_slot[t][k0 + 4 * j]) * width + col)
+                        : 0.f;
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+#pragma unroll
+        for (int c = 1; c < MOE_CHUNKS; ++c) v[j][0] += v[j][c];
+        if (k0 + 4 * j < routes) y = fmaf(route_factor(p, sh, t, k0 + 4 * j), v[j][0], y);
+      }
+    }
+    y += __shfl_xor_sync(0xffffffffu, y, 8);
+    y += __shfl_xor_sync(0xffffffffu, y, 16);
+    if (lane < 8 && col < p.hidden) p.output[size_t(t) * p.hidden + col] = uint16_t(pack_bf16x2(y, 0.f));
+  }
+}
+// Many: four columns a thread, nine pieces at a time.
+__device__ __forceinline__ void combine_many(const MoeParams &p, const Shared &sh, const Shape &s, size_t width) {
+  const int lane = threadIdx.x % 32, terms = (p.top_k + p.shared) * s.down_chunks;
+  for (int n = blockIdx.x + threadIdx.x / 32 * gridDim.x; n < p.m * s.down_tiles; n += gridDim.x * WARPS) {
+    const int t = n / s.down_tiles, col = (n - t * s.down_tiles) * 128 + lane * 4;
+    float y[4] = {};
     int k = 0, c = 0;
     for (int j0 = 0; j0 < terms; j0 += 9) {
-      Vec v[9];
+      float4 v[9];
       float w[9];
 #pragma unroll
       for (int j = 0; j < 9; ++j) {
-        const float *piece = p.scratch.down + (size_t(c) * p.slots + sh.route_slot[t][k]) * width + col;
-        v[j] = __ldcg(reinterpret_cast<const Vec *>(piece));
-        w[j] = k < p.top_k ? sh.route_weight[t][k] : 1.f;
+        v[j] = ldcg4(p.scratch.down + (size_t(c) * p.slots + sh.route_slot[t][k]) * width + col);
+        w[j] = route_factor(p, sh, t, k);
         if (j0 + j + 1 < terms && ++c == s.down_chunks) {
           c = 0;
           ++k;
@@ -642,13 +669,16 @@ __device__ __forceinline__ void combine(const MoeParams &p, const Shared &sh, co
       }
 #pragma unroll
       for (int j = 0; j < 9; ++j)
-        if (j0 + j < terms)
-#pragma unroll
-          for (int i = 0; i < V; ++i) y[i] = fmaf(w[j], reinterpret_cast<const float *>(&v[j])[i], y[i]);
+        if (j0 + j < terms) {
+          y[0] = fmaf(w[j], v[j].x, y[0]);
+          y[1] = fmaf(w[j], v[j].y, y[1]);
+          y[2] = fmaf(w[j], v[j].z, y[2]);
+          y[3] = fmaf(w[j], v[j].w, y[3]);
+        }
     }
     if (col < p.hidden)   // hidden is a multiple of 8: four columns are in or out together
 #pragma unroll
-      for (int i = 0; i < V; ++i) p.output[size_t(t) * p.hidden + col + i] = uint16_t(pack_bf16x2(y[i], 0.f));
+      for (int i = 0; i < 4; ++i) p.output[size_t(t) * p.hidden + col + i] = uint16_t(pack_bf16x2(y[i], 0.f));
   }
 }
 
@@ -758,7 +788,9 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   } else if (warp == 0) {
     // ------------------------------------------- items and weight tiles
     Ring at;
-    int issued = stall ? 0 : ahead, item = blockIdx.x;
+    // The first two items go by the CTA's place; a later one is asked for two
+    // items ahead, as the answer takes longer than a small item's requests.
+    int issued = stall ? 0 : ahead, item = blockIdx.x, next = item + int(gridDim.x);
     bool ok = true;
     const bool leader = tc::elect_one();
     while (true) {
@@ -772,8 +804,8 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       if (!live) break;
       items.next(ITEMS);
       const Item it = item_at(s, item);
-      int next = 0;
-      if (lane == 0) next = int(atomicAdd(tickets, 1u) + gridDim.x);
+      int after = 0;
+      if (lane == 0) after = int(atomicAdd(tickets, 1u) + 2 * gridDim.x);
       const int e = sh.act_expert[it.a];
       const int row = it.down ? e * p.hidden + it.tile * 128 : (e * 2 + it.half) * p.intermediate + it.tile * 128;
       const CUtensorMap *map = it.down ? &tm_down : &tm_gate_up;
@@ -795,6 +827,7 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
         at.next(p.stages);
       }
       item = __shfl_sync(0xffffffffu, next, 0);
+      next = after;
     }
     if (leader) sh.issued_a = issued;
   } else if (warp == 3) {
@@ -1022,9 +1055,9 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   }
   __syncthreads();
   __threadfence();
-  // few tokens: a column a thread, so that more warps wait at a time; many: four
-  if (p.m * s.down_tiles * 4 <= int(gridDim.x) * WARPS) combine<1>(p, sh, s, down_width);
-  else combine<4>(p, sh, s, down_width);
+  // few: while a pass of the wide form would leave most warps idle
+  if (p.m * s.down_tiles * 4 <= int(gridDim.x) * WARPS) combine_few(p, sh, s, down_width);
+  else combine_many(p, sh, s, down_width);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
