@@ -195,6 +195,71 @@ __device__ __forceinline__ void store_row(const MatmulParams &p, int row, int co
   }
 }
 
+// Sixteen bytes of a row to the output.
+template <bool F32>
+__device__ __forceinline__ void store_piece(const MatmulParams &p, int row, int col, const uint4 &v) {
+  constexpr int W = F32 ? 4 : 8;
+  if (row >= p.m) return;
+  const size_t at = size_t(row) * p.output_stride + col;
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  if (col + W <= p.n) {
+    st_vec(static_cast<char *>(p.output) + at * (F32 ? 4 : 2), v);
+  } else if (F32) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (col + k < p.n) static_cast<uint32_t *>(p.output)[at + k] = u[k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (col + k < p.n) static_cast<uint16_t *>(p.output)[at + k] = uint16_t(u[k / 2] >> (k % 2 * 16));
+  }
+}
+
+// A warp's 32 rows, one a lane, to the output where it takes 16 bytes at a
+// time.  Four lanes exchange their rows' pieces (two rounds of a transposition)
+// so that they write 64 neighbouring bytes: a lane for itself would write half a
+// sector of each of 32 lines.
+template <int NC, bool F32>
+__device__ __forceinline__ void store_rows(const MatmulParams &p, int row0, int col, int lane,
+                                           const uint64_t (&acc)[NC / 2]) {
+  constexpr int W = F32 ? 4 : 8;   // columns of a piece
+#pragma unroll
+  for (int g = 0; g < NC / (4 * W); ++g) {
+    uint4 piece[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t *a = acc + (g * 4 + k) * W / 2;
+      if (F32) {
+        piece[k] = make_uint4(uint32_t(a[0]), uint32_t(a[0] >> 32), uint32_t(a[1]), uint32_t(a[1] >> 32));
+      } else {
+        const float v[8] = {tc::pair_lo(a[0]), tc::pair_hi(a[0]), tc::pair_lo(a[1]), tc::pair_hi(a[1]),
+                            tc::pair_lo(a[2]), tc::pair_hi(a[2]), tc::pair_lo(a[3]), tc::pair_hi(a[3])};
+        piece[k] = pack8(v);
+      }
+    }
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit <<= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (!(k & bit)) {
+          const bool odd = lane & bit;
+          uint4 &lo = piece[k], &hi = piece[k | bit];
+          auto swap = [&](uint32_t &x, uint32_t &y) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? x : y, bit);
+            if (odd) x = got;
+            else y = got;
+          };
+          swap(lo.x, hi.x);
+          swap(lo.y, hi.y);
+          swap(lo.z, hi.z);
+          swap(lo.w, hi.w);
+        }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      store_piece<F32>(p, row0 + (lane & ~3) + k, col + (g * 4 + lane % 4) * W, piece[k]);
+  }
+}
+
 __device__ __forceinline__ void init_control(Control &c, int stages, int bufs) {
   for (int i = 0; i < stages; ++i) {
     tc::mbar_init(&c.full[i], 1);
@@ -369,7 +434,13 @@ k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
         buf.next(BUFS);
       }
       if (p.splits == 1) {
-        if (live) store_row<NC>(p, m0 + r, n0 + col, acc);
+        if (!p.vector_out) {
+          if (live) store_row<NC>(p, m0 + r, n0 + col, acc);
+        } else if (p.output_f32) {
+          store_rows<NC, true>(p, m0 + sub * 32, n0 + col, lane, acc);
+        } else {
+          store_rows<NC, false>(p, m0 + sub * 32, n0 + col, lane, acc);
+        }
       } else if (live) {
         // every MMA has completed, so the stages are free: [column][row]
         float *part = reinterpret_cast<float *>(ring) + size_t(col) * p.a_rows + r;
