@@ -410,27 +410,43 @@ k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
         tc::wait_or_abort_inline(&c.acc_full[buf.at], buf.phase, abort);
         __syncwarp();
         tc::fence_after_sync();
-        if (rows_live) {
+        // parts of 32 columns: the next one is read while this one is added
+        constexpr int H = NC / 32;
+        const uint32_t from = lane_base + uint32_t(buf.at * G * BN);
+        auto release = [&]() {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&c.acc_empty[buf.at]);
+        };
+        auto add = [&](int j, const uint32_t (&d)[32]) {
+          const uint64_t s2 = tc::pair(scale[j / H], scale[j / H]);
 #pragma unroll
-          for (int q = 0; q < G; ++q)
-            if (q < blocks) {
-              uint32_t d[(NC + 31) / 32][32];
+          for (int i = 0; i < 16; ++i) tc::fma_pair(acc[j % H * 16 + i], d[2 * i], d[2 * i + 1], s2);
+        };
+        if (rows_live && blocks == G) {
+          uint32_t d[2][32];
+          tc::tmem_ld32_async(from, d[0]);
 #pragma unroll
-              for (int h = 0; h < NC / 32; ++h)
-                tc::tmem_ld32_async(lane_base + uint32_t((buf.at * G + q) * BN + h * 32), d[h]);
-              tc::tmem_wait_ld();
+          for (int j = 0; j < G * H; ++j) {
+            tc::tmem_wait_ld();
+            tc::tmem_hold(d[j % 2]);
+            if (j + 1 < G * H) tc::tmem_ld32_async(from + uint32_t((j + 1) / H * BN + (j + 1) % H * 32), d[(j + 1) % 2]);
+            else release();
+            add(j, d[j % 2]);
+          }
+        } else {
+          if (rows_live)
 #pragma unroll
-              for (int h = 0; h < NC / 32; ++h) tc::tmem_hold(d[h]);
-              const uint64_t s2 = tc::pair(scale[q], scale[q]);
-#pragma unroll
-              for (int h = 0; h < NC / 32; ++h)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) tc::fma_pair(acc[h * 16 + i], d[h][2 * i], d[h][2 * i + 1], s2);
-            }
+            for (int j = 0; j < G * H; ++j)
+              if (j / H < blocks) {
+                uint32_t d[32];
+                tc::tmem_ld32_async(from + uint32_t(j / H * BN + j % H * 32), d);
+                tc::tmem_wait_ld();
+                tc::tmem_hold(d);
+                add(j, d);
+              }
+          release();
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&c.acc_empty[buf.at]);
         buf.next(BUFS);
       }
       if (p.splits == 1) {
