@@ -30,6 +30,8 @@ struct QuantParams {
   uint16_t *output;                       // null: not written
   uint8_t *values;
   float *scales;
+  uint32_t row_mul;                       // division of a block's number by the blocks of a row
+  int row_shift;
 };
 
 struct MatmulParams {
