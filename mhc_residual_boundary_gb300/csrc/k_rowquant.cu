@@ -2,10 +2,18 @@
 // quantisers (plain and SwiGLU), rows in BF16, 8-bit outputs as E4M3 values
 // with one FP32 scale for each 128 values of a row.
 //
-// All are bound by memory: the norm moves 2 + 2 bytes in and up to 2 + 2 + 1
-// out for each element, quantize 2 in and 1 out, swiglu 4 in and 1 out.  Every
-// value crosses the memory once: the row stays in registers between its
-// reduction and its output.  A thread holds 16-byte fragments (8 values), so
+//   r = x + residual; y = r * rsqrt(mean(r^2) + eps) * w
+//   scale = max(amax, 2^-100) / 448, value = x * (448 / amax)
+// The norm moves 2 + 2 bytes in and up to 2 + 2 + 1 out for each element,
+// quantize 2 in and 1 out, swiglu 4 in and 1 out.  Every value crosses the memory
+// once: the row stays in registers between its reduction and its output.
+//
+// Measured (a call among others in a graph): norm of 4096 x 6144 with all outputs
+// 37.5 us, 6.05 TB/s, bound by memory; one row of 5120 2.7 us, a launch and a
+// chain of two memory trips; quantize 1999 x 5064 7.9 us, 3.9 TB/s; swiglu 4096 x
+// 2048 11.6 us, 3.6 TB/s, of which some 2.5 us are launch and ramp and the rest
+// the SiLU's instructions (its counters: a warp is ready to issue in most clocks)
+// as much as the bytes.  A thread holds 16-byte fragments (8 values), so
 // 16 neighbouring lanes hold one block of 128 and its largest magnitude takes
 // four shuffles.  Magnitudes are compared as the bit patterns of |x|: their
 // order is that of the numbers, with infinity above them and NaN above that,

@@ -163,17 +163,16 @@ class Sublayer:
             res_stride = self._stride("residual", residual, BF16, shape)
             res = residual.data_ptr()
         gamma = self._ptr("norm_weight", weight, BF16, (h,))
-        known = 0
-        ptrs = [0, 0, 0, 0]
-        for i, (name, dtype, width) in enumerate((("residual_out", BF16, h), ("output", BF16, h), ("values", F8, h),
-                                                  ("scales", F32, (h + 127) // 128))):
-            t = outputs.get(name)
-            if t is not None:
-                ptrs[i] = self._ptr(name, t, dtype, (m, width))
-                known += 1
-        if known != len(outputs):
+        get, ptr, blocks = outputs.get, self._ptr, (m, (h + 127) // 128)
+        r, y, v, s = get("residual_out"), get("output"), get("values"), get("scales")
+        rp = 0 if r is None else ptr("residual_out", r, BF16, shape)
+        yp = 0 if y is None else ptr("output", y, BF16, shape)
+        vp = 0 if v is None else ptr("values", v, F8, shape)
+        sp = 0 if s is None else ptr("scales", s, F32, blocks)
+        if len(outputs) != (r is not None) + (y is not None) + (v is not None) + (s is not None):
             self._unknown(outputs, ("residual_out", "output", "values", "scales"))
-        self._call(self._norm, NORM_ARGS.pack(m, h, x.data_ptr(), x_stride, res, res_stride, gamma, eps, *ptrs), stream)
+        self._call(self._norm, NORM_ARGS.pack(m, h, x.data_ptr(), x_stride, res, res_stride, gamma, eps, rp, yp, vp, sp),
+                   stream)
         return outputs
 
     def quantize(self, inputs: dict, outputs: dict, *, stream=None) -> dict:
