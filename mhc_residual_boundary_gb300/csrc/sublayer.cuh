@@ -48,6 +48,7 @@ struct MatmulParams {
   // set by the launcher
   int k_blocks, n_blocks, m_tiles, n_tiles, splits, stages;
   int a_rows;                             // rows of a stage's `values` tile
+  int parts_at;                           // offset of a split tile's sums; 0: where the stages are
 };
 
 constexpr int MATMUL_SPLITS_MAX = 8;
