@@ -488,11 +488,14 @@ k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
         }
       } else {
         if (!first_pass) meet();
+        int owner = col / 8 * p.splits / GROUPS, place = col / 8 - first_group(owner);
 #pragma unroll
-        for (int g = 0; g < NC / 8; ++g) {
-          const int cg = col / 8 + g, owner = cg * p.splits / GROUPS;
-          const uint32_t at = peer_addr(
-              parts + (size_t((cg - first_group(owner)) * p.splits + rank) * p.a_rows + r) * 8, uint32_t(owner));
+        for (int g = 0; g < NC / 8; ++g, ++place) {
+          const int to = (col / 8 + g) * p.splits / GROUPS;
+          if (to != owner) place = 0;
+          owner = to;
+          const uint32_t at =
+              peer_addr(parts + (size_t(place * p.splits + rank) * p.a_rows + r) * 8, uint32_t(owner));
           if (live) {
             st_peer(at, acc[g * 4], acc[g * 4 + 1]);
             st_peer(at + 16, acc[g * 4 + 2], acc[g * 4 + 3]);
