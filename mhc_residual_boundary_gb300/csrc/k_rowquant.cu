@@ -10,14 +10,14 @@
 //
 // Measured (a call among others in a graph): norm of 4096 x 6144 with all outputs
 // 37.5 us, 6.05 TB/s, bound by memory; one row of 5120 2.7 us, a launch and a
-// chain of two memory trips; quantize 1999 x 5064 7.9 us, 3.9 TB/s; swiglu 4096 x
-// 2048 11.6 us, 3.6 TB/s, of which some 2.5 us are launch and ramp and the rest
-// the SiLU's instructions (its counters: a warp is ready to issue in most clocks)
-// as much as the bytes.  A thread holds 16-byte fragments (8 values), so
-// 16 neighbouring lanes hold one block of 128 and its largest magnitude takes
-// four shuffles.  Magnitudes are compared as the bit patterns of |x|: their
-// order is that of the numbers, with infinity above them and NaN above that,
-// so a non-finite value always reaches the block's scale.
+// chain of two memory trips; quantize 1999 x 5064 7.4 us, 4.2 TB/s; swiglu 4096 x
+// 2048 9.8 us, 4.3 TB/s, of which some 2.5 us are launch and ramp and the rest the
+// SiLU's instructions as much as the bytes.  A thread holds
+// one or two 16-byte fragments (8 values each), so 16 or 8 neighbouring lanes
+// hold a block of 128 and its largest magnitude takes four shuffles or three.
+// Magnitudes are compared as the bit patterns of |x|: their order is that of the
+// numbers, with infinity above them and NaN above that, so a non-finite value
+// always reaches the block's scale.
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -28,18 +28,20 @@ namespace {
 
 constexpr uint32_t AMAX_FLOOR_BITS = uint32_t(127 - 100) << 23;   // 2^-100
 
-// Bit pattern of the largest |y| of this lane's block (16 lanes).
-__device__ __forceinline__ uint32_t block_amax(const float (&y)[8]) {
+// Bit pattern of the largest |y| of this lane's block (N values in each of 128 /
+// N lanes).
+template <int N>
+__device__ __forceinline__ uint32_t block_amax(const float (&y)[N]) {
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(y[i]) & 0x7fffffffu);
+  for (int i = 0; i < N; ++i) a = max(a, __float_as_uint(y[i]) & 0x7fffffffu);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+  for (int o = QBLOCK / N / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
   return max(a, AMAX_FLOOR_BITS);
 }
 
 // Eight values to E4M3 at inv = 448 / amax.
-__device__ __forceinline__ uint2 quant8(const float (&y)[8], float inv) {
+__device__ __forceinline__ uint2 quant8(const float *y, float inv) {
   return make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
                     e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
 }
@@ -114,47 +116,81 @@ __global__ void __launch_bounds__(256) k_add_rms_norm(const NormParams p) {
   }
 }
 
-// One block of 128 per 16 lanes.  A thread takes U blocks a round, all of their
-// reads under way together; Index: 32 bits while the blocks can be counted in
-// them, with the division by the blocks of a row as a product (a 64-bit division
-// for each block costs more than its bytes).
-template <bool SWIGLU, int U, class Index>
-__global__ void __launch_bounds__(256, 6) k_quantize(const QuantParams p) {
+// 32 bytes, read once.
+__device__ __forceinline__ void ld_stream32(const void *p, uint4 (&v)[2]) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z),
+                 "=r"(v[1].w)
+               : "l"(p));
+}
+
+// A lane has FR fragments of a block, 16 / FR lanes a block, and takes U blocks
+// a round, all of their reads under way together.  WIDE: rows are read 32 bytes
+// at a time.  Index: 32 bits while the blocks can be counted in them, with the
+// division by the blocks of a row as a product (a 64-bit division for each block
+// costs more than its bytes).
+template <bool SWIGLU, int FR, int U, bool WIDE, class Index>
+__global__ void __launch_bounds__(256) k_quantize(const QuantParams p) {
+  constexpr int L = 16 / FR, WARP_BLOCKS = 32 / L, CTA_BLOCKS = 8 * WARP_BLOCKS;
   const Index per_row = qblocks(p.h), blocks = Index(p.m) * per_row;
-  const int lane16 = threadIdx.x % 16;
   pdl_wait();
   pdl_launch_dependents();
-  // both halves of a warp take the same number of rounds (the shuffles need
-  // all 32 lanes)
-  const Index step = Index(gridDim.x) * 16;
-  for (Index b0 = Index(blockIdx.x) * 16 + threadIdx.x / 32 * 2; b0 < blocks; b0 += step * U) {
-    uint4 g[U], u[U];
+  // all of a warp takes the same number of rounds (the shuffles need all 32
+  // lanes)
+  const Index step = Index(gridDim.x) * CTA_BLOCKS;
+  for (Index b0 = Index(blockIdx.x) * CTA_BLOCKS + threadIdx.x / 32 * WARP_BLOCKS; b0 < blocks; b0 += step * U) {
+    uint4 g[U][FR], u[U][FR];
     Index row[U];
-    int f[U];
-    bool live[U];
+    int f[U], left[U];   // first fragment; this lane's fragments inside the row
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const Index b = b0 + i * step + threadIdx.x % 32 / 16;
+      const Index b = b0 + i * step + threadIdx.x % 32 / L;
       row[i] = sizeof(Index) == 4 ? Index((__umulhi(uint32_t(b), p.row_mul) + uint32_t(b)) >> p.row_shift) : b / per_row;
-      f[i] = int(b - row[i] * per_row) * 16 + lane16;
-      live[i] = b < blocks && f[i] * 8 < p.h;
-      const uint16_t *x = p.x + (live[i] ? int64_t(row[i]) * p.x_stride + f[i] * 8 : 0);
-      g[i] = live[i] ? ld_stream(x) : make_uint4(0, 0, 0, 0);
-      if (SWIGLU) u[i] = live[i] ? ld_stream(x + p.h) : make_uint4(0, 0, 0, 0);
+      f[i] = int(b - row[i] * per_row) * 16 + threadIdx.x % L * FR;
+      left[i] = b < blocks ? p.h / 8 - f[i] : 0;
+      const uint16_t *x = p.x + int64_t(row[i]) * p.x_stride + f[i] * 8;
+      if (WIDE) {
+        g[i][0] = g[i][FR - 1] = u[i][0] = u[i][FR - 1] = make_uint4(0, 0, 0, 0);
+        if (left[i] > 0) {
+          ld_stream32(x, reinterpret_cast<uint4(&)[2]>(g[i]));
+          if (SWIGLU) ld_stream32(x + p.h, reinterpret_cast<uint4(&)[2]>(u[i]));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < FR; ++e) {
+          g[i][e] = left[i] > e ? ld_stream(x + e * 8) : make_uint4(0, 0, 0, 0);
+          if (SWIGLU) u[i][e] = left[i] > e ? ld_stream(x + p.h + e * 8) : make_uint4(0, 0, 0, 0);
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      float y[8];
-      unpack8(g[i], y);
-      if (SWIGLU) {
-        float up[8];
-        unpack8(u[i], up);
+      float y[FR * 8];
+      const int64_t at = int64_t(row[i]) * p.h + f[i] * 8;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = y[k] * rcp_approx(1.f + expf(-y[k])) * up[k];
+      for (int e = 0; e < FR; ++e) {
+        float v[8];
+        unpack8(g[i][e], v);
+        if (SWIGLU) {
+          float up[8];
+          unpack8(u[i][e], up);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = v[k] * rcp_approx(1.f + expf(-v[k])) * up[k];
+        }
+        if (p.output && left[i] > e) st_vec(p.output + at + e * 8, pack8(v));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[e * 8 + k] = v[k];
       }
-      const int64_t at = int64_t(row[i]) * p.h;
-      if (live[i] && p.output) st_vec(p.output + at + f[i] * 8, pack8(y));
-      store_quant(y, live[i], f[i], p.values + at, p.scales + int64_t(row[i]) * per_row);
+      const float amax = __uint_as_float(block_amax(y)), inv = E4M3_MAX * rcp_approx(amax);
+      if (WIDE) {
+        const uint2 a = quant8(y, inv), c = quant8(y + (FR - 1) * 8, inv);
+        if (left[i] > 0) *reinterpret_cast<uint4 *>(p.values + at) = make_uint4(a.x, a.y, c.x, c.y);
+      } else {
+#pragma unroll
+        for (int e = 0; e < FR; ++e)
+          if (left[i] > e) *reinterpret_cast<uint2 *>(p.values + at + e * 8) = quant8(y + e * 8, inv);
+      }
+      if (left[i] > 0 && f[i] % 16 == 0) p.scales[int64_t(row[i]) * per_row + f[i] / 16] = amax * (1.f / E4M3_MAX);
     }
   }
 }
@@ -199,15 +235,23 @@ cudaError_t launch_quantize_as(const QuantParams &args, int sms, cudaStream_t st
   p.row_shift = 0;
   while ((uint64_t(1) << p.row_shift) < d) ++p.row_shift;
   p.row_mul = uint32_t((uint64_t(1) << 32) * ((uint64_t(1) << p.row_shift) - d) / d + 1);
-  // Two blocks a thread, for more bytes under way, once that leaves every SM
-  // full; no loop over a resident grid, whose reads and writes would not overlap
-  // (1999 rows of 5064: 9.5 us against 8.4; swiglu 4096 x 2048: 17 us).
-  const int64_t blocks = int64_t(p.m) * qblocks(p.h), ctas = (blocks + 15) / 16;
+  const int64_t blocks = int64_t(p.m) * qblocks(p.h);
   const dim3 block(256);
-  if (blocks > (int64_t(1) << 30)) return launch_pdl(k_quantize<SWIGLU, 2, int64_t>, dim3(1 << 22), block, p, stream);
-  if (ctas >= int64_t(sms) * 8)
-    return launch_pdl(k_quantize<SWIGLU, 2, int>, dim3(unsigned((ctas + 1) / 2)), block, p, stream);
-  return launch_pdl(k_quantize<SWIGLU, 1, int>, dim3(unsigned(ctas)), block, p, stream);
+  auto ctas = [&](int per) { return dim3(unsigned((blocks + per - 1) / per)); };
+  // Once every SM is full: two fragments a lane, which halves what a block costs
+  // beside its values, and 64 bytes under way a lane (swiglu 4096 x 2048: one
+  // fragment 11.5 us, two 9.8, four 11.8; quantize 1999 x 5064: 7.9, one pair of
+  // fragments 7.5, two 7.35).  Rows that allow it are read 32 bytes at a time.  No
+  // loop over a resident grid, whose reads and writes would not overlap (quantize
+  // 1999 x 5064: 9.5 us against 8.4).
+  if (blocks > (int64_t(1) << 30))
+    return launch_pdl(k_quantize<SWIGLU, 1, 2, false, int64_t>, dim3(1 << 22), block, p, stream);
+  if (blocks < int64_t(sms) * 128) return launch_pdl(k_quantize<SWIGLU, 1, 1, false, int>, ctas(16), block, p, stream);
+  constexpr int U = SWIGLU ? 1 : 2;
+  const bool wide = reinterpret_cast<uintptr_t>(p.x) % 32 == 0 && p.x_stride % 16 == 0 && p.h % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(p.values) % 16 == 0;
+  if (wide) return launch_pdl(k_quantize<SWIGLU, 2, U, true, int>, ctas(32 * U), block, p, stream);
+  return launch_pdl(k_quantize<SWIGLU, 2, U, false, int>, ctas(32 * U), block, p, stream);
 }
 
 }  // namespace

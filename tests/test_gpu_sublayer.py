@@ -160,6 +160,27 @@ def test_quantisers(sub, op, m, h):
     check_quantized(out, y)
 
 
+# enough blocks for the wide form: rows of whole and of half 32-byte pieces, of
+# one block, of less than one
+@pytest.mark.parametrize("m,h", [(600, 5120), (700, 4088), (2500, 1000), (20000, 8), (20000, 16), (5000, 520)])
+@pytest.mark.parametrize("op", ["quantize", "swiglu"])
+@pytest.mark.parametrize("offset", [0, 8])
+def test_quantisers_many_blocks(sub, op, m, h, offset):
+    g = gen(m + h)
+    width = 2 * h if op == "swiglu" else h
+    wide = torch.full((m, offset + width), float("nan"), device="cuda").bfloat16()
+    x = wide[:, offset:]
+    x.copy_(2 * randn(g, m, width))
+    out = sub.empty_outputs(op, m, h)
+    out["values"].view(torch.uint8).fill_(0x7f)
+    out["scales"].fill_(float("nan"))
+    getattr(sub, op)({"gate_up" if op == "swiglu" else "x": x}, out)
+    y = silu_product(x) if op == "swiglu" else x.double()
+    check_quantized(out, y)
+    if op == "swiglu":
+        check_bf16(out["output"], y, "output")
+
+
 def test_quantize_strided_rows(sub):
     g = gen(9)
     wide = randn(g, 6, 640).bfloat16()
