@@ -59,11 +59,6 @@ __device__ __forceinline__ void wait_or_abort_inline(uint64_t *bar, uint32_t par
   }
 }
 
-// Asks for a box of a tensor map in L2.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
-}
-
 // Instruction descriptor of kind::f8f6f4: FP32 accumulator, E4M3 A and B,
 // both K-major, M x N.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n) {
