@@ -11,6 +11,7 @@
 #define MHC_BOUNDARY_TEST_H
 
 #include "mhc_boundary.h"
+#include "mhc_sublayer.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -28,6 +29,17 @@ mhc_status_t mhc_test_stall_stage_copies(int32_t on);
 /* The same for the matmul and moe kernels of mhc_sublayer.h
  * (mhc_sublayer_check_errors reports). */
 mhc_status_t mhc_test_stall_sublayer_copies(int32_t on);
+
+/* Where things lie in the shared memory of a CTA of the moe kernel, in bytes,
+ * for a call of m tokens on a GPU of that many SMs.  Needs no GPU. */
+typedef struct {
+  int32_t size;         /* of the allocation */
+  int32_t ring_at, stages, stage_bytes;
+  int32_t weight_bytes; /* a stage's first part; the tokens' rows of 128 bytes follow */
+  int32_t scales_at;    /* [items][scale_blocks][m] float, 8-bit weights only */
+  int32_t items, scale_blocks;
+} mhc_test_moe_form_t;
+mhc_status_t mhc_test_moe_form(const mhc_sublayer_config_t *config, int32_t m, int32_t sms, mhc_test_moe_form_t *out);
 
 #ifdef __cplusplus
 }

@@ -104,6 +104,11 @@ class mhc_sublayer_moe_args_t(ctypes.Structure):
         "x", "router", "bias", "gate_up", "gate_up_scales", "down", "down_scales", "output", "idx", "weights")]
 
 
+class mhc_test_moe_form_t(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("size", "ring_at", "stages", "stage_bytes", "weight_bytes", "scales_at",
+                                              "items", "scale_blocks")]
+
+
 SUBLAYER_CALLS = {"add_rms_norm": mhc_sublayer_norm_args_t, "quantize": mhc_sublayer_quantize_args_t,
                   "swiglu": mhc_sublayer_quantize_args_t, "matmul": mhc_sublayer_matmul_args_t,
                   "moe": mhc_sublayer_moe_args_t}
@@ -145,6 +150,9 @@ def lib() -> ctypes.CDLL:
         h.mhc_test_stall_stage_copies.restype = st
         h.mhc_test_stall_sublayer_copies.argtypes = [ctypes.c_int32]
         h.mhc_test_stall_sublayer_copies.restype = st
+        h.mhc_test_moe_form.argtypes = [ctypes.POINTER(mhc_sublayer_config_t), ctypes.c_int32, ctypes.c_int32,
+                                        ctypes.POINTER(mhc_test_moe_form_t)]
+        h.mhc_test_moe_form.restype = st
         h.mhc_sublayer_create.argtypes = [ctypes.POINTER(mhc_sublayer_config_t), ctypes.c_int, ctypes.POINTER(vp)]
         for name, args in SUBLAYER_CALLS.items():
             getattr(h, "mhc_sublayer_" + name).argtypes = [vp, ctypes.POINTER(args), vp]
@@ -237,6 +245,15 @@ def mhc_test_stall_sublayer_copies(on: bool) -> None:
     status = lib().mhc_test_stall_sublayer_copies(1 if on else 0)
     if status != MHC_OK:
         raise MhcError(status, "could not set the stall flag")
+
+
+def mhc_test_moe_form(config: mhc_sublayer_config_t, m: int, sms: int) -> mhc_test_moe_form_t:
+    """Test hook: the layout of a moe CTA's shared memory (needs no GPU)."""
+    out = mhc_test_moe_form_t()
+    status = lib().mhc_test_moe_form(ctypes.byref(config), int(m), int(sms), ctypes.byref(out))
+    if status != MHC_OK:
+        raise MhcError(status, "m or sms out of range")
+    return out
 
 
 def _check_sublayer(status: int, handle) -> None:

@@ -384,3 +384,17 @@ mhc_status_t mhc_test_stall_sublayer_copies(int32_t on) {
   if (e == cudaSuccess) e = moe_stall_copies(on ? 1 : 0);
   return e == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
 }
+
+mhc_status_t mhc_test_moe_form(const mhc_sublayer_config_t *config, int32_t m, int32_t sms, mhc_test_moe_form_t *out) {
+  if (!config || !out || m < 1 || m > MOE_TOKENS_MAX || sms < 1) return MHC_ERR_INVALID_ARG;
+  MoeParams p = {};
+  p.m = m;
+  p.hidden = config->hidden;
+  p.intermediate = config->intermediate;
+  p.top_k = config->top_k;
+  p.shared = config->shared_experts;
+  p.fp8 = (config->flags & MHC_SUBLAYER_FP8) != 0;
+  moe_form(p, sms);
+  *out = {MOE_SMEM, p.ring_at, p.stages, MOE_STAGE_A + p.b_bytes, MOE_STAGE_A, p.scales_at, MOE_ITEMS, p.scale_blocks};
+  return MHC_OK;
+}

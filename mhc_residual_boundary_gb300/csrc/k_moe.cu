@@ -53,10 +53,10 @@ namespace {
 constexpr int NT = 384, WARPS = NT / 32;
 constexpr int SUM_WARP0 = 4, JOIN_WARP0 = 8;
 constexpr int STAGES_MAX = 12;
-constexpr int ITEMS = 4;        // items between their taking and the last warp that reads them
+constexpr int ITEMS = MOE_ITEMS;
 constexpr int BUFS = 4, BUF_COLS = 128;
-constexpr int A_BYTES = 128 * 128;
-constexpr int SMEM_BYTES = 227 * 1024;
+constexpr int A_BYTES = MOE_STAGE_A;
+constexpr int SMEM_BYTES = MOE_SMEM;
 constexpr int EXPERTS = MOE_EXPERTS_MAX + MOE_SHARED_MAX;
 constexpr uint32_t POLL_LIMIT = 1u << 22;
 
@@ -81,6 +81,9 @@ struct Shared {
 };
 constexpr int SMEM_TABLES = (int(sizeof(Shared)) + 1023) / 1024 * 1024;
 constexpr int SMEM_SLACK = 1024;   // an MMA's columns are rounded up to 16: it may read 8 rows past the last stage
+// The sums read a block's scales for 5, 10 or 32 tokens, however many it has (what
+// is read for the others is not used): so many words lie after the last block's.
+constexpr int SCALE_SLACK = MOE_TOKENS_MAX * 4;
 
 // ------------------------------------------------------------------ waits
 __device__ __forceinline__ unsigned ld_acquire(const unsigned *p) {
@@ -700,9 +703,9 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
   extern __shared__ __align__(1024) unsigned char smem[];
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   float *sums = reinterpret_cast<float *>(smem + SMEM_TABLES);   // two buffers [m][128] from the sums to the joins
-  unsigned char *ring = smem + SMEM_TABLES + p.m * 1024;
+  unsigned char *ring = smem + p.ring_at;
   // scales of the items in flight (8-bit weights)
-  float *scales = reinterpret_cast<float *>(ring + size_t(p.stages) * (A_BYTES + p.b_bytes) + SMEM_SLACK);
+  float *scales = reinterpret_cast<float *>(smem + p.scales_at);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort = &sh.abort;
   const int stage_bytes = A_BYTES + p.b_bytes;
@@ -1117,11 +1120,9 @@ cudaError_t moe_set_attributes() {
   return e;
 }
 
-cudaError_t launch_moe(const MoeParams &args, int sms, cudaStream_t stream) {
-  MoeParams p = args;
+void moe_form(MoeParams &p, int sms) {
   const bool fp8 = p.fp8 != 0;
-  const int every = p.experts + p.shared, elem = fp8 ? 1 : 2, kb = fp8 ? 128 : 64;
-  const int xp = fp8 ? 2 : 1, hp = fp8 ? 3 : 2;
+  const int kb = fp8 ? 128 : 64, xp = fp8 ? 2 : 1, hp = fp8 ? 3 : 2;
   p.b_bytes = (p.m * std::max(xp, hp) + 7) / 8 * 1024;
   // Chunks of a tile's k blocks: of about ten blocks (`up`) or six (`down`,
   // whose last items decide when the kernel ends), or fewer blocks where the
@@ -1136,9 +1137,18 @@ cudaError_t launch_moe(const MoeParams &args, int sms, cudaStream_t stream) {
   p.up_chunks = chunks(up_k, 10, least * qblocks(p.intermediate) * 2);
   p.down_chunks = chunks(down_k, 6, least * qblocks(p.hidden));
   p.scale_blocks = std::max((up_k + p.up_chunks - 1) / p.up_chunks, (down_k + p.down_chunks - 1) / p.down_chunks);
-  const int scale_bytes = fp8 ? ITEMS * p.scale_blocks * p.m * 4 : 0;
-  p.stages = std::min(STAGES_MAX, (SMEM_BYTES - SMEM_TABLES - SMEM_SLACK - p.m * 1024 - scale_bytes) /
-                                      (A_BYTES + p.b_bytes));
+  const int scale_bytes = fp8 ? ITEMS * p.scale_blocks * p.m * 4 + SCALE_SLACK : 0;
+  p.ring_at = SMEM_TABLES + p.m * 1024;
+  p.stages = std::min(STAGES_MAX, (SMEM_BYTES - p.ring_at - SMEM_SLACK - scale_bytes) / (A_BYTES + p.b_bytes));
+  p.scales_at = p.ring_at + p.stages * (A_BYTES + p.b_bytes) + SMEM_SLACK;
+}
+
+cudaError_t launch_moe(const MoeParams &args, int sms, cudaStream_t stream) {
+  MoeParams p = args;
+  moe_form(p, sms);
+  const bool fp8 = p.fp8 != 0;
+  const int every = p.experts + p.shared, elem = fp8 ? 1 : 2, kb = fp8 ? 128 : 64;
+  const int xp = fp8 ? 2 : 1, hp = fp8 ? 3 : 2;
   const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t H = p.hidden, I = p.intermediate;
   const void *x = fp8 ? static_cast<const void *>(p.scratch.x_pieces) : p.x;

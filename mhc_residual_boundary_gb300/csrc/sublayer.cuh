@@ -99,12 +99,19 @@ struct MoeParams {
   int slots;                  // slots of the scratch tensors
   MoeScratch scratch;
   unsigned int *err;
-  // set by the launcher
+  // set by the launcher: how the work is cut and where things lie in a CTA's
+  // shared memory
   int stages, b_bytes;
   int up_chunks, down_chunks; // chunks of a tile's k blocks
   int scale_blocks;           // k blocks of an item at most
+  int ring_at, scales_at;     // offsets of the stages and of the items' scales
 };
+constexpr int MOE_ITEMS = 4;  // items between their taking and the last warp that reads them
+constexpr int MOE_SMEM = 227 * 1024;
+constexpr int MOE_STAGE_A = 128 * 128;   // bytes of a stage's weight tile
 
+// The launcher's fields of p, on a GPU of that many SMs.
+void moe_form(MoeParams &p, int sms);
 cudaError_t moe_set_attributes();
 cudaError_t moe_stall_copies(int on);   // test hook
 cudaError_t launch_moe(const MoeParams &p, int sms, cudaStream_t stream);

@@ -299,3 +299,11 @@ def test_many_calls_one_after_another():
             for name in first:
                 assert torch.equal(first[name], out[name])
         c.layer.check_errors()
+
+
+def test_the_widest_scales_of_many_tokens():
+    """32 k blocks an item and 30 tokens an expert: the stages leave the scales
+    no room beyond what the layout reserves after them."""
+    c = Case(30, 128, 16384, 2, 0, 2, True)
+    c.check(c.run())
+    c.layer.check_errors()
