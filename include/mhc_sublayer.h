@@ -130,9 +130,13 @@ typedef struct {
  *   expert(x) = (silu(x gate^T) * (x up^T)) down^T;
  *   output = sum of weight * expert over the chosen, plus the S shared
  *   experts (the last S of the weight tensors) with weight 1.
- * The products take the BF16 x exactly and sum in FP32; the activation
- * between them is held to 12 (8-bit weights) or 16 (BF16 weights)
- * significant bits. */
+ * The products sum in FP32 and take the BF16 x exactly with BF16 weights; with
+ * 8-bit weights exactly down to 2^-17 of its row's largest magnitude, or of
+ * 2^-100 where that is larger, and off by at most 2^-25 of it below.  The
+ * activation between them is held to 16 significant bits with BF16 weights; with
+ * 8-bit weights it is off by at most 2^-12 of itself or 2^-25 of the largest of
+ * its block of 128.  A row of x with an infinity or a NaN has no finite
+ * output. */
 typedef struct {
   int32_t m;
   const void *x;               /* [m][H] bf16 */

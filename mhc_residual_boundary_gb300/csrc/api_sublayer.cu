@@ -134,7 +134,7 @@ size_t moe_layout(mhc_sublayer_t *s) {
   take(q.up_done, reached * 4);
   s->moe_counter_bytes = off;
   take(q.logits, m * c.num_experts * 4);
-  take(q.x_pieces, fp8 ? 2 * m * c.hidden : 0);
+  take(q.x_pieces, fp8 ? 3 * m * c.hidden : 0);
   take(q.x_scale, m * 4);
   take(q.up, MOE_CHUNKS * slots * 2 * ib * QBLOCK * 4);
   unsigned char *act;

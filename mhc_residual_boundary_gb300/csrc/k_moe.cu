@@ -13,9 +13,11 @@
 // 8-bit weights against BF16 activations: the tensor core multiplies E4M3 by
 // E4M3, so an activation row is scaled by a power of two and split into E4M3
 // pieces, each holding four significant bits of what the ones before leave
-// (16 times larger than it stands for): two pieces hold a BF16 value (8 bits)
-// exactly down to 2^-13 of the row's largest and to 2^-22 of it below, three
-// hold the FP32 activation h to 12 bits.  The pieces are neighbouring
+// (16 times larger than it stands for).  Three pieces hold a BF16 value (8 bits)
+// exactly down to 2^-17 of the row's largest (2^-10 where that is in [128, 256):
+// the last piece's smallest step, 2^-9, stands for 2^-17, an ulp of 2^-10) and
+// to half that step, 2^-25 of the largest, below; two would end at 2^-13 and
+// 2^-21.  Three hold the FP32 activation h to 12 bits.  The pieces are neighbouring
 // columns, and their products are added with factors 1, 1/16, 1/256.  The
 // weight's block scale multiplies each block of 128's sum in FP32.  BF16
 // weights take x as it is and h as two BF16 pieces (16 bits).
@@ -318,18 +320,19 @@ __device__ __forceinline__ void split_x(const MoeParams &p, Shared &sh) {
 #pragma unroll
     for (int k = 0; k < WARPS; ++k) a = max(a, sh.red_max[k]);
     const float scale = piece_scale(a), inv = piece_inverse(scale);
-    uint8_t *hi = p.scratch.x_pieces + size_t(2 * t) * p.hidden, *lo = hi + p.hidden;
+    uint8_t *pieces = p.scratch.x_pieces + size_t(3 * t) * p.hidden;
     auto split = [&](const uint4 &x8, int f) {
       float v[8];
       unpack8(x8, v);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] *= inv;
-      const uint2 h = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = (v[k] - from_e4m3((k < 4 ? h.x : h.y) >> (k % 4 * 8) & 0xffu)) * 16.f;
-      *reinterpret_cast<uint2 *>(hi + size_t(f) * 8) = h;
-      *reinterpret_cast<uint2 *>(lo + size_t(f) * 8) =
-          make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+      for (int c = 0; c < 3; ++c) {
+        const uint2 b = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+        *reinterpret_cast<uint2 *>(pieces + size_t(c) * p.hidden + size_t(f) * 8) = b;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = (v[k] - from_e4m3((k < 4 ? b.x : b.y) >> (k % 4 * 8) & 0xffu)) * 16.f;
+      }
     };
 #pragma unroll
     for (int k = 0; k < HELD; ++k)
@@ -504,9 +507,8 @@ __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(b
 
 // Sums of an item's k blocks for this thread's row and CT columns' tokens (P
 // pieces each): block sums from the accumulator ring, their pieces added, times
-// the block's scale (8-bit weights): `scales` of m floats a block, the first
-// for all tokens (P = 2, `up`) or one a token (P = 3, `down`).  What lies
-// beyond the expert's tokens is not used.
+// the block's scale (8-bit weights): `scales` of m floats a block, one a token.
+// What lies beyond the expert's tokens is not used.
 template <bool FP8, int P, int CT>
 __device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, Ring &ring, int blocks, const float *scales,
                                            int m, float (&acc)[CT]) {
@@ -530,7 +532,7 @@ __device__ __forceinline__ void sum_blocks(Shared &sh, uint32_t lane_base, Ring 
         float v = value(d[P * t + P - 1]);
 #pragma unroll
         for (int c = P - 2; c >= 0; --c) v = fmaf(v, 0.0625f, value(d[P * t + c]));
-        acc[t] = fmaf(v, scales[P == 2 ? 0 : t], acc[t]);
+        acc[t] = fmaf(v, scales[t], acc[t]);
       } else {
 #pragma unroll
         for (int c = 0; c < P; ++c) acc[t] += value(d[P * t + c]);
@@ -699,7 +701,7 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x_token,
       const __grid_constant__ CUtensorMap tm_act) {
   constexpr int KB = FP8 ? 128 : 64;                        // values of a 128-byte k block
-  constexpr int XP = FP8 ? 2 : 1, HP = FP8 ? 3 : 2;         // pieces of x and of h
+  constexpr int XP = FP8 ? 3 : 1, HP = FP8 ? 3 : 2;         // pieces of x and of h
   extern __shared__ __align__(1024) unsigned char smem[];
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   float *sums = reinterpret_cast<float *>(smem + SMEM_TABLES);   // two buffers [m][128] from the sums to the joins
@@ -908,7 +910,7 @@ k_moe(const MoeParams p, const __grid_constant__ CUtensorMap tm_gate_up, const _
       if (item < 0) break;
       if (!FP8) continue;
       const Item it = item_at(s, item);
-      const int count = it.down ? __popc(sh.act_mask[it.a]) : 1, e = sh.act_expert[it.a];
+      const int count = __popc(sh.act_mask[it.a]), e = sh.act_expert[it.a];
       const float *sw = it.down ? p.down_scales + (size_t(e) * s.down_tiles + it.tile) * s.down_k
                                 : p.gate_up_scales + ((size_t(e) * 2 + it.half) * s.up_tiles + it.tile) * s.up_k;
       const float *act = p.scratch.act_scale + size_t(it.kb0) * p.slots + sh.act_base[it.a];
@@ -1122,8 +1124,8 @@ cudaError_t moe_set_attributes() {
 
 void moe_form(MoeParams &p, int sms) {
   const bool fp8 = p.fp8 != 0;
-  const int kb = fp8 ? 128 : 64, xp = fp8 ? 2 : 1, hp = fp8 ? 3 : 2;
-  p.b_bytes = (p.m * std::max(xp, hp) + 7) / 8 * 1024;
+  const int kb = fp8 ? 128 : 64, pieces = fp8 ? 3 : 2;   // of x or h, at most
+  p.b_bytes = (p.m * pieces + 7) / 8 * 1024;
   // Chunks of a tile's k blocks: of about ten blocks (`up`) or six (`down`,
   // whose last items decide when the kernel ends), or fewer blocks where the
   // tiles of the experts that are reached at least do not give every CTA an
@@ -1148,7 +1150,7 @@ cudaError_t launch_moe(const MoeParams &args, int sms, cudaStream_t stream) {
   moe_form(p, sms);
   const bool fp8 = p.fp8 != 0;
   const int every = p.experts + p.shared, elem = fp8 ? 1 : 2, kb = fp8 ? 128 : 64;
-  const int xp = fp8 ? 2 : 1, hp = fp8 ? 3 : 2;
+  const int xp = fp8 ? 3 : 1, hp = fp8 ? 3 : 2;
   const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t H = p.hidden, I = p.intermediate;
   const void *x = fp8 ? static_cast<const void *>(p.scratch.x_pieces) : p.x;

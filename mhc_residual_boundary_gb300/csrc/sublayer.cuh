@@ -75,7 +75,7 @@ struct MoeScratch {
   unsigned int *up_counters;  // [reached experts][I / 128] chunks of a tile that are there
   unsigned int *up_done;      // [reached experts] complete tiles
   float *logits;              // [tokens][E]
-  uint8_t *x_pieces;          // [2 tokens][H] e4m3 (8-bit weights)
+  uint8_t *x_pieces;          // [3 tokens][H] e4m3 (8-bit weights)
   float *x_scale;             // [tokens]
   float *up;                  // [MOE_CHUNKS][slots][2][I rounded up to 128]
   void *act;                  // [slots * pieces][I]: e4m3 x 3 or bf16 x 2
