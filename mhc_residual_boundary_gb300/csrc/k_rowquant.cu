@@ -3,7 +3,8 @@
 // with one FP32 scale for each 128 values of a row.
 //
 //   r = x + residual; y = r * rsqrt(mean(r^2) + eps) * w
-//   scale = max(amax, 2^-100) / 448, value = x * (448 / amax)
+//   scale = max(amax, 2^-100) / 448, value = x * (448 / amax), both quotients
+//   correctly rounded (e4m3_scale.h)
 // The norm moves 2 + 2 bytes in and up to 2 + 2 + 1 out for each element,
 // quantize 2 in and 1 out, swiglu 4 in and 1 out.  Every value crosses the memory
 // once: the row stays in registers between its reduction and its output.
@@ -21,6 +22,7 @@
 #include <algorithm>
 
 #include "device_common.cuh"
+#include "e4m3_scale.h"
 #include "sublayer.cuh"
 
 namespace mhc {
@@ -40,22 +42,12 @@ __device__ __forceinline__ uint32_t block_amax(const float (&y)[N]) {
   return max(a, AMAX_FLOOR_BITS);
 }
 
+__device__ __forceinline__ float inverse_of(float amax) { return e4m3_inverse(amax, rcp_fast(e4m3_divisor(amax))); }
+
 // Eight values to E4M3 at inv = 448 / amax.
 __device__ __forceinline__ uint2 quant8(const float *y, float inv) {
   return make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
                     e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-}
-
-// Quantises this lane's fragment `f` of a row (live: within the row); the
-// whole warp calls it.
-__device__ __forceinline__ void store_quant(const float (&y)[8], bool live, int f, uint8_t *values, float *scales) {
-  const float amax = __uint_as_float(block_amax(y));
-  if (live) {
-    // within two units in the last place of 448 / amax and amax / 448: two
-    // correctly rounded divisions take as many instructions as the eight values
-    *reinterpret_cast<uint2 *>(values + size_t(f) * 8) = quant8(y, E4M3_MAX * rcp_approx(amax));
-    if (f % (QBLOCK / 8) == 0) scales[f / (QBLOCK / 8)] = amax * (1.f / E4M3_MAX);
-  }
 }
 
 // One row per threadIdx.y, VPT fragments a thread.
@@ -112,7 +104,24 @@ __global__ void __launch_bounds__(256) k_add_rms_norm(const NormParams p) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) r[i][k] = r[i][k] * rstd * w[k];
     if (live && p.output) st_vec(p.output + at, pack8(r[i]));
-    if (p.values) store_quant(r[i], live, f, p.values + base, p.scales + size_t(row) * qblocks(p.h));
+  }
+  if (!p.values) return;
+  // the fragments' chains (shuffles, quotients) run side by side
+  float amax[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) amax[i] = __uint_as_float(block_amax(r[i]));
+  float inv[VPT], scale[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    inv[i] = inverse_of(amax[i]);
+    scale[i] = e4m3_scale(amax[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int f = i * T + tx;
+    if (!live_row || f >= frags) continue;
+    *reinterpret_cast<uint2 *>(p.values + base + size_t(f) * 8) = quant8(r[i], inv[i]);
+    if (f % (QBLOCK / 8) == 0) p.scales[size_t(row) * qblocks(p.h) + f / (QBLOCK / 8)] = scale[i];
   }
 }
 
@@ -181,7 +190,7 @@ __global__ void __launch_bounds__(256) k_quantize(const QuantParams p) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[e * 8 + k] = v[k];
       }
-      const float amax = __uint_as_float(block_amax(y)), inv = E4M3_MAX * rcp_approx(amax);
+      const float amax = __uint_as_float(block_amax(y)), inv = inverse_of(amax);
       if (WIDE) {
         const uint2 a = quant8(y, inv), c = quant8(y + (FR - 1) * 8, inv);
         if (left[i] > 0) *reinterpret_cast<uint4 *>(p.values + at) = make_uint4(a.x, a.y, c.x, c.y);
@@ -190,7 +199,7 @@ __global__ void __launch_bounds__(256) k_quantize(const QuantParams p) {
         for (int e = 0; e < FR; ++e)
           if (left[i] > e) *reinterpret_cast<uint2 *>(p.values + at + e * 8) = quant8(y + e * 8, inv);
       }
-      if (left[i] > 0 && f[i] % 16 == 0) p.scales[int64_t(row[i]) * per_row + f[i] / 16] = amax * (1.f / E4M3_MAX);
+      if (left[i] > 0 && f[i] % 16 == 0) p.scales[int64_t(row[i]) * per_row + f[i] / 16] = e4m3_scale(amax);
     }
   }
 }
