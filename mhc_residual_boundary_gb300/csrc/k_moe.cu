@@ -378,7 +378,7 @@ __device__ __noinline__ void choose(const MoeParams &p, Shared &sh, int t, const
     for (int i = 0; i < PER; ++i) score[i] *= inverse;
   } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) score[i] = rcp_approx(1.f + expf(-score[i]));
+    for (int i = 0; i < PER; ++i) score[i] = sigmoid(score[i]);
   }
   // key 0: the expert is chosen already, or does not exist
 #pragma unroll
