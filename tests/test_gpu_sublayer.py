@@ -405,3 +405,17 @@ def test_stalled_copies_report_a_timeout_and_the_handle_recovers(sub):
     sub.check_errors()
     sub.matmul(inp, out)
     check_product(out["output"], inp)
+
+
+# tiles whose k blocks' scales come in more than one chunk of 32: whole chunks,
+# ragged ones, several tiles a CTA, and split tiles with more than 32 blocks a CTA
+@pytest.mark.parametrize("m,n,k", [(2048, 2500, 4096), (2048, 2500, 4240), (1100, 4000, 8336), (1300, 2100, 8192),
+                                   (4096, 4096, 6144), (3, 100, 40976), (64, 136, 65536), (128, 200, 49168),
+                                   (300, 1500, 33008)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_matmul_long_rows(sub, m, n, k, dtype):
+    inp = matmul_inputs(gen(m + n + k), m, n, k)
+    out = sub.empty_outputs("matmul", m, n, dtype=dtype)
+    out["output"].fill_(float("nan"))
+    sub.matmul(inp, out)
+    check_product(out["output"], inp)
