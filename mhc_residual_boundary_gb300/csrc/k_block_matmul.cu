@@ -97,9 +97,9 @@ constexpr int CHUNK = 32, CHUNKS = CHUNKS_MAX;   // k blocks of a chunk, chunks 
 constexpr int SCALE_ROW = BM + 1;        // words from block to block: no bank conflicts
 struct Scales {
   float *a;   // [CHUNKS][CHUNK][SCALE_ROW]
-  float *w;   // [CHUNKS][CHUNK][2]: of two neighbouring column blocks
+  float *w;   // [CHUNKS][CHUNK]: of the column block that the tile lies in
 };
-static_assert(CHUNKS * CHUNK * (SCALE_ROW + 2) * 4 <= SMEM_SCALES, "scales");
+static_assert(CHUNKS * CHUNK * (SCALE_ROW + 1) * 4 <= SMEM_SCALES, "scales");
 
 // One word to shared memory without passing through a register, and the
 // barrier's arrival once all of this thread's are there.
@@ -121,8 +121,8 @@ __device__ __forceinline__ void load_scales(const MatmulParams &p, Control &c, c
     if (kb + lane < kb1) {
       float *a = sc.a + (ring.at * CHUNK + lane) * SCALE_ROW + half * 64;
       const float *src = p.scales + size_t(m0 + half * 64) * p.scales_stride + kb + lane;
-      copy_word(sc.w + (ring.at * CHUNK + lane) * 2 + half,
-                p.weight_scales + size_t(min(n_block + half, p.n_blocks - 1)) * p.k_blocks + kb + lane);
+      if (half == 1)   // up to 64 rows leave this warp without any
+        copy_word(sc.w + ring.at * CHUNK + lane, p.weight_scales + size_t(n_block) * p.k_blocks + kb + lane);
 #pragma unroll 8
       for (int r = 0; r < rows; ++r, src += p.scales_stride) copy_word(a + r, src);
     }
@@ -132,12 +132,12 @@ __device__ __forceinline__ void load_scales(const MatmulParams &p, Control &c, c
 }
 
 // An epilogue warp's way through the chunks: the scales of this thread's row
-// and of column block w_block, G blocks (G divides CHUNK) at a time.
+// and of the tile's column block, G blocks (G divides CHUNK) at a time.
 struct ScaleReader {
   Ring ring;
   int k = 0;   // blocks taken of this chunk
   template <int G>
-  __device__ __forceinline__ void take(Control &c, const Scales &sc, int row, int w_block, bool last, int lane,
+  __device__ __forceinline__ void take(Control &c, const Scales &sc, int row, bool last, int lane,
                                        float (&scale)[G]) {
     if (k == 0) {
       tc::wait_or_abort_inline(&c.scale_full[ring.at], ring.phase, &c.abort);
@@ -145,7 +145,7 @@ struct ScaleReader {
     }
     const int at = ring.at * CHUNK + k;
 #pragma unroll
-    for (int q = 0; q < G; ++q) scale[q] = sc.a[(at + q) * SCALE_ROW + row] * sc.w[(at + q) * 2 + w_block];
+    for (int q = 0; q < G; ++q) scale[q] = sc.a[(at + q) * SCALE_ROW + row] * sc.w[at + q];
     k += G;
     if (k == CHUNK || last) {
       __syncwarp();
@@ -433,7 +433,7 @@ k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
       for (int k = first_pass ? kb1 : 0; k < kb1 - kb0; k += G) {
         const int blocks = min(G, kb1 - kb0 - k);
         float scale[G];
-        scales.take(c, sc, r, 0, k + G >= kb1 - kb0, lane, scale);
+        scales.take(c, sc, r, k + G >= kb1 - kb0, lane, scale);
         tc::wait_or_abort_inline(&c.acc_full[buf.at], buf.phase, abort);
         __syncwarp();
         tc::fence_after_sync();
@@ -588,7 +588,6 @@ cudaError_t matmul_setup(int sms, MatmulPlan *plan) {
 cudaError_t launch_block_matmul(const MatmulParams &args, const MatmulPlan &plan, cudaStream_t stream) {
   MatmulParams p = args;
   p.k_blocks = qblocks(p.k);
-  p.n_blocks = qblocks(p.n);
   p.m_tiles = (p.m + BM - 1) / BM;
   // The form that takes the fewest clocks: rounds of clusters, a block's clocks
   // for each of a CTA's k blocks, and what a call and a split tile cost beside

@@ -38,7 +38,7 @@ struct MatmulParams {
   int m, n, k;
   const uint8_t *values, *weight;         // e4m3
   int64_t values_stride, weight_stride;
-  const float *scales, *weight_scales;    // [m][k_blocks], [n_blocks][k_blocks]
+  const float *scales, *weight_scales;    // [m][k_blocks], [n / 128 rounded up][k_blocks]
   int64_t scales_stride;
   void *output;                           // bf16 or f32
   int64_t output_stride;
@@ -46,7 +46,7 @@ struct MatmulParams {
   int vector_out;                         // the output's rows start on 16-byte boundaries
   unsigned int *err;                      // bit 1: a bounded wait gave up
   // set by the launcher
-  int k_blocks, n_blocks, m_tiles, n_tiles, splits, stages;
+  int k_blocks, m_tiles, n_tiles, splits, stages;
   int a_rows;                             // rows of a stage's `values` tile
   int parts_at;                           // offset of a split tile's sums; 0: where the stages are
 };
