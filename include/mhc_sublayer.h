@@ -24,6 +24,7 @@
  * every argument checked before the first launch, nothing aborts or traps).
  * Matrices are row-major with contiguous rows; a *_stride is the distance of
  * two rows in elements.  BF16 and 8-bit rows start on 16-byte boundaries.
+ * Outputs overlap neither inputs nor one another, but where a call allows it.
  * Calls with m = 0 succeed and launch nothing (but for moe, whose m is in
  * [1, max_moe_tokens]).  A handle owns scratch that its moe calls use: its
  * calls run one after another, on one stream or on streams that the caller
@@ -77,7 +78,9 @@ typedef struct mhc_sublayer mhc_sublayer_t; /* opaque, library-owned */
  * r = x + residual (x where residual is NULL) in FP32, not rounded before the
  * norm.  Outputs, each optional but at least one given: residual_out [m][h]
  * bf16 (needs residual), output [m][h] bf16, values and scales (both or
- * neither).  residual_out may be residual and output may be x. */
+ * neither).  residual_out and output may each be x or residual itself where
+ * that is dense (its stride h, or m = 1); no output may overlap an input in
+ * another way. */
 typedef struct {
   int32_t m, h;
   const void *x;           /* [m][h] bf16 */

@@ -82,6 +82,14 @@ mhc_status_t check_stride(std::string &msg, const char *name, int64_t stride, in
   return MHC_OK;
 }
 
+// Whether a dense output of `bytes` bytes meets one of `m` rows of an input, `row`
+// bytes each and `stride` bytes apart.
+bool meets(const void *out, int64_t bytes, const void *in, int64_t row, int64_t stride, int64_t m) {
+  const int64_t at = int64_t(reinterpret_cast<uintptr_t>(in) - reinterpret_cast<uintptr_t>(out));
+  const int64_t first = at + row > 0 ? 0 : (-at - row) / stride + 1;   // the first row that ends after the output begins
+  return first < m && at + first * stride < bytes;
+}
+
 mhc_status_t launched(mhc_sublayer_t *s, cudaError_t e, const char *what) {
   if (e == cudaSuccess) return MHC_OK;
   return fail(s->last_error, MHC_ERR_CUDA, "%s kernel: %s", what, cudaGetErrorString(e));
@@ -230,6 +238,22 @@ mhc_status_t mhc_sublayer_add_rms_norm(mhc_sublayer_t *s, const mhc_sublayer_nor
   if (st == MHC_OK) st = check_stride(msg, "x_stride", a->x_stride, a->h, 8);
   if (st == MHC_OK && a->residual) st = check_stride(msg, "residual_stride", a->residual_stride, a->h, 8);
   if (st != MHC_OK) return st;
+  // A row's block reads its inputs before it writes, and other rows not at all:
+  // a BF16 output may take the place of a dense input, row for row, and meet an
+  // input in no other way.
+  const int64_t m = a->m, h = a->h;
+  const struct { const char *name; const void *p; int64_t bytes; bool rows; } outs[] = {
+      {"residual_out", a->residual_out, m * h * 2, true}, {"output", a->output, m * h * 2, true},
+      {"values", a->values, m * h, false}, {"scales", a->scales, m * qblocks(a->h) * 4, false}};
+  const struct { const char *name; const void *p; int64_t stride, m; } ins[] = {
+      {"x", a->x, a->x_stride, m}, {"residual", a->residual, a->residual_stride, m}, {"norm_weight", a->norm_weight, h, 1}};
+  for (const auto &o : outs)
+    for (int i = 0; o.p && i < 3; ++i) {
+      if (!ins[i].p || !meets(o.p, o.bytes, ins[i].p, h * 2, ins[i].stride * 2, ins[i].m)) continue;
+      if (i < 2 && o.rows && o.p == ins[i].p && (m == 1 || ins[i].stride == h)) continue;
+      return fail(msg, MHC_ERR_INVALID_ARG, "%s overlaps %s (only residual_out and output may be a dense x or residual)",
+                  o.name, ins[i].name);
+    }
   DeviceGuard guard(s->device);
   NormParams p = {};
   p.m = a->m;

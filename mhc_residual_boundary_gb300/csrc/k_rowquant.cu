@@ -50,6 +50,17 @@ __device__ __forceinline__ uint2 quant8(const float *y, float inv) {
                     e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
 }
 
+// 16 bytes, read once, of a row that this thread may write later (residual_out may
+// be residual): not through the read-only path.
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // One row per threadIdx.y, VPT fragments a thread.
 template <int VPT>
 __global__ void __launch_bounds__(256) k_add_rms_norm(const NormParams p) {
@@ -68,8 +79,8 @@ __global__ void __launch_bounds__(256) k_add_rms_norm(const NormParams p) {
   for (int i = 0; i < VPT; ++i) {
     const int f = i * T + tx;
     const bool live = live_row && f < frags;
-    xv[i] = live ? ld_stream(x + size_t(f) * 8) : make_uint4(0, 0, 0, 0);
-    rv[i] = live && res ? ld_stream(res + size_t(f) * 8) : make_uint4(0, 0, 0, 0);
+    xv[i] = live ? ld_once(x + size_t(f) * 8) : make_uint4(0, 0, 0, 0);
+    rv[i] = live && res ? ld_once(res + size_t(f) * 8) : make_uint4(0, 0, 0, 0);
   }
   float r[VPT][8], ss = 0.f;
 #pragma unroll

@@ -419,3 +419,71 @@ def test_matmul_long_rows(sub, m, n, k, dtype):
     out["output"].fill_(float("nan"))
     sub.matmul(inp, out)
     check_product(out["output"], inp)
+
+
+def test_norm_in_place_of_dense_inputs(sub):
+    """Each BF16 output in the place of each input, alone and both at once."""
+    g = gen(21)
+    for m, h in ((9, 520), (1, 264), (300, 5120), (5, 16384)):
+        x, res = randn(g, m, h).bfloat16(), randn(g, m, h).bfloat16()
+        w = randn(g, h).bfloat16()
+        want = sub.empty_outputs("add_rms_norm", m, h)
+        sub.add_rms_norm({"x": x, "residual": res, "norm_weight": w}, want)
+        for places in (("x", None), ("residual", None), (None, "x"), (None, "residual"), ("x", "residual"),
+                       ("residual", "x")):
+            inp = {"x": x.clone(), "residual": res.clone(), "norm_weight": w}
+            out = sub.empty_outputs("add_rms_norm", m, h)
+            for name, place in zip(("residual_out", "output"), places):
+                if place:
+                    out[name] = inp[place]
+            sub.add_rms_norm(inp, out)
+            for name in want:
+                assert torch.equal(out[name].view(torch.uint8), want[name].view(torch.uint8)), (m, h, places, name)
+
+
+def test_norm_overlap_refusals(sub):
+    """Outputs that overlap an input but in the allowed way are refused; those
+    that only lie between its rows are not."""
+    from mhc_residual_boundary_gb300 import capi
+    g = gen(22)
+    h, w = 256, torch.ones(256, dtype=BF16, device="cuda")
+    buffer = torch.zeros(64 * 1024, dtype=BF16, device="cuda")
+
+    def dense(at, m, dtype=BF16, width=h):
+        size = torch.tensor([], dtype=dtype).element_size()
+        return buffer.view(torch.uint8)[2 * at:2 * at + m * width * size].view(dtype).view(m, width)
+
+    def strided(at, m, stride):
+        return buffer[at:].as_strided((m, h), (stride, 1))
+
+    def norm(x, residual, out):
+        sub.add_rms_norm({"x": x, "norm_weight": w, **({} if residual is None else {"residual": residual})}, out)
+
+    other = torch.zeros(8, h, dtype=BF16, device="cuda")
+    values, scales = torch.zeros(8, h, device="cuda").to(F8), torch.zeros(8, 2, device="cuda")
+    refused = [
+        (strided(0, 8, 512), None, {"output": dense(0, 8)}),                       # the same start, another stride
+        (other, strided(0, 8, 264), {"residual_out": dense(0, 8)}),
+        (dense(0, 8), None, {"output": dense(8, 8)}),                              # shifted by a fragment
+        (dense(2048, 8), None, {"output": dense(8, 8)}),                           # ends inside the first row
+        (strided(4096, 4, 1024), None, {"output": dense(4096 + 3 * 1024 + 248, 4)}),   # only the last row's end
+        (dense(0, 8), None, {"values": dense(0, 8, F8), "scales": scales}),
+        (dense(0, 8), None, {"values": values, "scales": dense(2040, 8, F32, 2)}),
+        (other, dense(0, 8), {"residual_out": torch.zeros_like(other), "output": dense(1024, 8)}),
+    ]
+    for x, residual, out in refused:
+        with pytest.raises(capi.MhcError, match="overlaps"):
+            norm(x, residual, out)
+    with pytest.raises(capi.MhcError, match="output overlaps norm_weight"):
+        sub.add_rms_norm({"x": other, "norm_weight": dense(0, 1)[0]}, {"output": dense(0, 8)})
+    rows = randn(g, 8, h).bfloat16()
+    want = torch.zeros(8, h, dtype=BF16, device="cuda")
+    norm(rows, None, {"output": want})
+    for x, out in ((strided(0, 2, 8192), dense(256, 2)),                           # between two rows
+                   (strided(4096, 2, 8192), dense(4096 + 8192 + 256, 2)),          # right after the last
+                   (dense(4096, 8), dense(2048, 8)), (dense(2048, 8), dense(4096, 8)),   # side by side
+                   (strided(0, 1, 8192), dense(0, 1))):                            # one row
+        m = x.shape[0]
+        x.copy_(rows[:m])
+        norm(x, None, {"output": out})
+        assert torch.equal(out, want[:m])
