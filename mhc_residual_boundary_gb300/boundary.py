@@ -9,6 +9,8 @@ deepseek_v41.nvidia.ops.cute_dsl.all_reduce_mhc).
 """
 from __future__ import annotations
 
+import operator
+
 import torch
 
 from . import capi
@@ -49,6 +51,18 @@ OUTPUT_SPECS = {
 REQUIRED_OUTPUTS = ("residual_out", "layer_input", "post_out", "comb_out")
 
 
+def cuda_device(device=None) -> torch.device:
+    """The CUDA device that a handle is made on, with its index: `device` is an
+    index, a string or a torch.device; without one, or without an index, it is
+    the current device."""
+    if device is None or isinstance(device, (str, torch.device)):
+        d = torch.device("cuda" if device is None else device)
+        if d.type != "cuda":
+            raise ValueError(f"device: expected a CUDA device, got {d}")
+        return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
+    return torch.device("cuda", operator.index(device))
+
+
 class Boundary:
     """One boundary instance: it serves every call of up to max_num_tokens
     tokens ([GLM] AllReduceMhcBoundary: one instance serves every boundary
@@ -67,10 +81,7 @@ class Boundary:
                  post_mult: float = 2.0, norm_eps: float = 1e-6, mxfp8: bool = False,
                  sync_mixes: bool = False, side_mixes: bool = False, host_staging: bool = False,
                  static_weight: bool = False, owner_reduce: bool = False, device=None):
-        if device is None:
-            device = torch.cuda.current_device()
-        self.device = torch.device("cuda", int(torch.device("cuda", device).index
-                                               if not isinstance(device, int) else device))
+        self.device = cuda_device(device)
         flags = ((capi.MHC_FLAG_MXFP8 if mxfp8 else 0) | (capi.MHC_FLAG_SYNC_MIXES if sync_mixes else 0)
                  | (capi.MHC_FLAG_HOST_STAGING if host_staging else 0)
                  | (capi.MHC_FLAG_SIDE_MIXES if side_mixes else 0)

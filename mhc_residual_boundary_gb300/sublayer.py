@@ -15,6 +15,7 @@ import struct
 import torch
 
 from . import capi
+from .boundary import cuda_device
 
 QBLOCK = 128
 F8, BF16, F32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
@@ -47,10 +48,7 @@ class Sublayer:
     def __init__(self, *, hidden: int = 0, intermediate: int = 0, experts: int = 0, shared_experts: int = 0,
                  top_k: int = 0, max_moe_tokens: int = 0, fp8: bool = True, score: str = "softmax",
                  renormalize: bool = True, routed_scale: float = 1.0, router_f32: bool = False, device=None):
-        if device is None:
-            device = torch.cuda.current_device()
-        self.device = torch.device("cuda", int(torch.device("cuda", device).index
-                                               if not isinstance(device, int) else device))
+        self.device = cuda_device(device)
         scores = {"softmax": capi.MHC_SCORE_SOFTMAX, "sigmoid": capi.MHC_SCORE_SIGMOID}
         if score not in scores:
             raise ValueError(f"score: expected one of {sorted(scores)}, got {score!r}")

@@ -487,3 +487,12 @@ def test_norm_overlap_refusals(sub):
         x.copy_(rows[:m])
         norm(x, None, {"output": out})
         assert torch.equal(out, want[:m])
+
+
+def test_device_argument(sub):
+    from mhc_residual_boundary_gb300 import Sublayer
+    x = torch.zeros(2, 128, dtype=BF16, device="cuda")
+    for device in (None, 0, "cuda", "cuda:0", x.device, torch.device("cuda")):
+        with Sublayer(device=device) as s:
+            assert s.device == x.device
+            s.quantize({"x": x}, s.empty_outputs("quantize", 2, 128))
