@@ -1,7 +1,8 @@
 // api_sublayer.cu -- host implementation of include/mhc_sublayer.h: argument
-// checks, the handle's scratch, and one kernel launch for each call.  Every
-// launch is a programmatic dependent one, so a call's setup overlaps the end
-// of the kernel before it on the stream.
+// checks, the handle's scratch, and one kernel launch for each call.  All but
+// moe's are programmatic dependent launches, so a call's setup overlaps the end
+// of the kernel before it on the stream; moe's is a cooperative one (its CTAs
+// wait for one another) and begins when that kernel is done.
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -109,7 +110,6 @@ mhc_status_t quantize_call(mhc_sublayer_t *s, const mhc_sublayer_quantize_args_t
                             {"values", a->values, 16, true}, {"scales", a->scales, 4, true}};
   mhc_status_t st = check_tensors(msg, tensors);
   if (st == MHC_OK) st = check_stride(msg, "x_stride", a->x_stride, int64_t(a->h) * (swiglu ? 2 : 1), 8);
-  // a row's 8-bit values are stored eight at a time
   if (st != MHC_OK) return st;
   DeviceGuard guard(s->device);
   QuantParams p = {};
