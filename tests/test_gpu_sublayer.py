@@ -496,3 +496,50 @@ def test_device_argument(sub):
         with Sublayer(device=device) as s:
             assert s.device == x.device
             s.quantize({"x": x}, s.empty_outputs("quantize", 2, 128))
+
+
+def test_the_c_entry_points_by_struct(sub):
+    """The binding's functions of the C names, with argument structs: the same
+    bits as the wrapper's calls, which pack the structs themselves."""
+    from mhc_residual_boundary_gb300 import capi
+    g = gen(31)
+    m, h = 11, 264
+    x, res, w = randn(g, m, h).bfloat16(), randn(g, m, h).bfloat16(), randn(g, h).bfloat16()
+    gate_up = randn(g, m, 2 * h).bfloat16()
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def fields(a, **kw):
+        for name, v in kw.items():
+            setattr(a, name, v.data_ptr() if isinstance(v, torch.Tensor) else v)
+        return a
+
+    def same(got, want):
+        for name in want:
+            assert torch.equal(got[name].view(torch.uint8), want[name].view(torch.uint8)), name
+
+    want = sub.add_rms_norm({"x": x, "residual": res, "norm_weight": w}, sub.empty_outputs("add_rms_norm", m, h), eps=1e-5)
+    got = sub.empty_outputs("add_rms_norm", m, h)
+    capi.mhc_sublayer_add_rms_norm(sub.handle, fields(
+        capi.mhc_sublayer_norm_args_t(), m=m, h=h, x=x, x_stride=h, residual=res, residual_stride=h, norm_weight=w,
+        eps=1e-5, **got), stream)
+    same(got, want)
+    want = sub.quantize({"x": x}, sub.empty_outputs("quantize", m, h))
+    got = sub.empty_outputs("quantize", m, h)
+    capi.mhc_sublayer_quantize(sub.handle, fields(capi.mhc_sublayer_quantize_args_t(), m=m, h=h, x=x, x_stride=h, **got),
+                               stream)
+    same(got, want)
+    a = fields(capi.mhc_sublayer_quantize_args_t(), m=m, h=h, x=x, x_stride=h, output=x.clone(), **got)
+    with pytest.raises(capi.MhcError, match="no BF16 output"):
+        capi.mhc_sublayer_quantize(sub.handle, a, stream)
+    want = sub.swiglu({"gate_up": gate_up}, sub.empty_outputs("swiglu", m, h))
+    got = sub.empty_outputs("swiglu", m, h)
+    capi.mhc_sublayer_swiglu(sub.handle, fields(capi.mhc_sublayer_quantize_args_t(), m=m, h=h, x=gate_up, x_stride=2 * h,
+                                                **got), stream)
+    same(got, want)
+    inp = matmul_inputs(g, m, 72, h - 8)
+    want = sub.matmul(inp, sub.empty_outputs("matmul", m, 72, dtype=F32))
+    got = sub.empty_outputs("matmul", m, 72, dtype=F32)
+    capi.mhc_sublayer_matmul(sub.handle, fields(
+        capi.mhc_sublayer_matmul_args_t(), m=m, n=72, k=h - 8, values_stride=h - 8, scales_stride=2, weight_stride=h - 8,
+        output_stride=72, output_f32=1, **inp, **got), stream)
+    same(got, want)
