@@ -2,12 +2,15 @@
 dense MLP and one with a mixture of experts, boundaries between the sublayers,
 and the output head.
 
-    attention partials -> boundary -> quantize -> matmul -> swiglu -> matmul
-                       -> boundary -> moe
-                       -> boundary -> add_rms_norm -> matmul -> logits
+    attention partials -> boundary -> quantize -> matmul -> swiglu -> matmul -> MLP output
+            MLP output -> boundary -> moe ----------v
+            MLP output -> boundary (the head's) -> add_rms_norm -> matmul -> logits
 
 The MLP's output is the (only) partial of the next boundary, which adds it to
-the residual streams and hands the next sublayer its normalised input.  All
+the residual streams and hands the next sublayer its normalised input.  The
+last sublayer has no boundary behind it: its output is not spread over the
+streams once more, but added, in the final norm, to what the head reads of them,
+which the head's boundary takes from the streams as the MoE layer found them.  All
 buffers are made once; a step is launches only, so it can be captured in a
 CUDA graph.  The weights and the attention's partials are random.
 
@@ -97,9 +100,10 @@ class DecoderStep:
                          "weight_scales": weight[1]}, out)
 
     def boundary(self, k: int, partials: torch.Tensor) -> torch.Tensor:
-        """Boundary k: the state of the one before and a sublayer's partials in, the next sublayer's input out."""
-        state = self.start if k == 0 else {"residual": self.at[k - 1]["residual_out"],
-                                           "post": self.at[k - 1]["post_out"], "comb": self.at[k - 1]["comb_out"]}
+        """Boundary k: the streams' state and a sublayer's partials in, the next sublayer's input out.  The first
+        one begins from `start`, the others from the first."""
+        state = self.start if k == 0 else {"residual": self.at[0]["residual_out"], "post": self.at[0]["post_out"],
+                                           "comb": self.at[0]["comb_out"]}
         b = self.after_attention if k == 0 else self.after_mlp
         b.run({**state, **self.parameters[k], "partials": partials}, self.at[k])
         b.join()
@@ -116,8 +120,8 @@ class DecoderStep:
         # a mixture of experts
         x = self.boundary(1, self.mlp_out["output"][None])
         sub.moe({"x": x, "router": self.router, "bias": self.bias, **self.experts}, self.moe_out)
-        # the head: the layer's output and the collapsed streams, normalised
-        x = self.boundary(2, self.moe_out["output"][None])
+        # the head: the streams that the MoE layer found, collapsed for the head, and its output, normalised
+        x = self.boundary(2, self.mlp_out["output"][None])
         sub.add_rms_norm({"x": self.moe_out["output"], "residual": x, "norm_weight": self.norm_weight}, self.final)
         self.matmul(self.final, self.head, self.logits)
         return self.logits["output"]

@@ -56,3 +56,26 @@ def test_step(example, m):
     torch.cuda.synchronize()
     assert torch.equal(s.logits["output"], logits)
     s.check_errors()
+
+
+def test_the_last_sublayer_counts_once(example):
+    """The head's boundary is not given the MoE layer's output, which the final
+    norm adds: other experts change that output and the sum by the same, and
+    nothing that it is added to."""
+    def step(change):
+        s = example.DecoderStep(5, hidden=1024, tp=2, mlp=640, intermediate=384, experts=8, shared_experts=1, top_k=2,
+                                vocab=512, seed=3)
+        if change:
+            s.experts["down_scales"] *= -3.0
+        s.step()
+        s.check_errors()
+        return s
+
+    a, b = step(False), step(True)
+    assert not torch.equal(a.moe_out["output"], b.moe_out["output"])
+    for k in range(3):
+        for name in a.at[k]:
+            assert torch.equal(a.at[k][name], b.at[k][name]), (k, name)
+    for s in (a, b):
+        r = s.moe_out["output"].double() + s.at[2]["layer_input"].double()
+        check_bf16(s.final["residual_out"], r, "residual_out")
