@@ -54,6 +54,7 @@ struct Control {
   uint64_t scale_full[CHUNKS_MAX], scale_empty[CHUNKS_MAX], drain;
   uint32_t tmem;
   int abort;
+  int issued;   // stages that the producer asked for
 };
 static_assert(sizeof(Control) <= SMEM_CTRL, "control block");
 
@@ -280,6 +281,7 @@ __device__ __forceinline__ void init_control(Control &c, int stages, int bufs) {
   tc::mbar_init(&c.drain, 1);
   tc::mbar_init_fence();
   c.abort = 0;
+  c.issued = 0;
 }
 
 // Clusters of p.splits CTAs, tile after tile: CTA r of a cluster has the k blocks
@@ -364,10 +366,7 @@ k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
           ++issued;
         }
       }
-      // copies in flight land before the CTA's shared memory goes
-      if (*abort)
-        for (int i = max(0, issued - p.stages); i < issued; ++i)
-          tc::mbar_wait_bounded(&c.full[i % p.stages], uint32_t((i / p.stages) & 1), tc::SUB_WAIT_LIMIT);
+      c.issued = issued;
     }
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer
@@ -529,7 +528,13 @@ k_block_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap tm_a, c
   __syncthreads();
   tc::fence_after_sync();
   if (warp == TMEM_WARP) tc::tmem_dealloc(tmem, 512);
-  if (threadIdx.x == 0 && c.abort) atomicOr(p.err, 2u);
+  if (threadIdx.x == 0 && c.abort) {
+    atomicOr(p.err, 2u);
+    // copies in flight land before the CTA's shared memory goes, whoever gave up
+    // and whenever (the producer may have left by then)
+    for (int i = max(0, c.issued - p.stages); i < c.issued; ++i)
+      tc::mbar_wait_bounded(&c.full[i % p.stages], uint32_t((i / p.stages) & 1), tc::SUB_WAIT_LIMIT);
+  }
 }
 
 template <class Kernel>
