@@ -17,8 +17,10 @@
  * each 128 x 128 block, [ceil(n/128)][ceil(k/128)].  A value stands for
  * value * scale.  The quantisers take scale = amax / 448 with the block's
  * largest magnitude, floored at 2^-100, as amax, and round x * (448 / amax)
- * to nearest-even; both quotients and the product are FP32, correctly rounded.
- * A block that holds an infinity or a NaN has a non-finite scale.
+ * to nearest-even.  The quotients are taken as amax * (1 / 448) and (1 / amax) *
+ * 448, every step rounded to nearest in FP32 (but 1 / amax may be the neighbour
+ * below where amax has 24 significant bits, all ones).  A block that holds an infinity or
+ * a NaN has a non-finite scale.
  *
  * Conventions: as in mhc_boundary.h (device pointers, caller-owned buffers,
  * every argument checked before the first launch, nothing aborts or traps).

@@ -3,8 +3,8 @@
 // with one FP32 scale for each 128 values of a row.
 //
 //   r = x + residual; y = r * rsqrt(mean(r^2) + eps) * w
-//   scale = max(amax, 2^-100) / 448, value = x * (448 / amax), both quotients
-//   correctly rounded (e4m3_scale.h)
+//   scale = max(amax, 2^-100) / 448, value = x * (448 / amax), the quotients by
+//   rounded reciprocals (e4m3_scale.h)
 // The norm moves 2 + 2 bytes in and up to 2 + 2 + 1 out for each element,
 // quantize 2 in and 1 out, swiglu 4 in and 1 out.  Every value crosses the memory
 // once: the row stays in registers between its reduction and its output.

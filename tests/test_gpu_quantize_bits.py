@@ -1,6 +1,7 @@
-"""The 8-bit values and the scales of the quantisers, bit for bit: scale =
-amax / 448 and value = x * (448 / amax), both quotients and the product rounded
-to nearest-even in FP32, the value then to E4M3.
+"""The 8-bit values and the scales of the quantisers, bit for bit: scale = amax *
+(1 / 448) and value = x * ((1 / amax) * 448), every step rounded to nearest in
+FP32, the value then to E4M3; and the same bits from the short form in PyTorch,
+amax / 448 and x * (448 / amax).
 
 The inputs make every step before the quantisation exact: the norm's rows have
 a mean square of one and are multiplied by BF16 weights, and a SiLU's gate is
@@ -42,8 +43,10 @@ def plain(y):
     """The definition on exact FP32 values [m][128 n]."""
     b = y.float().view(y.shape[0], -1, 128)
     amax = b.abs().amax(2).clamp(min=2.0 ** -100)
-    inv = torch.full_like(amax, 448.0) / amax
-    return (b * inv[:, :, None]).to(F8).view(y.shape), amax / torch.full_like(amax, 448.0)
+    one, top = torch.ones_like(amax), torch.full_like(amax, 448.0)
+    inv, scales = (one / amax) * top, amax * (one / top)
+    assert torch.equal(448.0 / amax, inv) and torch.equal(amax / 448.0, scales)
+    return (b * inv[:, :, None]).to(F8).view(y.shape), scales
 
 
 def check(out, y):
