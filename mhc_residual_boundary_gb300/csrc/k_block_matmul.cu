@@ -20,8 +20,8 @@
 //
 // Measured (a call among others in a graph): 4096 x 4096 x 6144 102 us, 2020
 // TFLOP/s (without its stores 96 us, without its copies 92, without its additions
-// 95); one row of 6144 x 5120 10.1 us, 3.1 TB/s of weights (6.1
-// once they flow); 37 rows of 2120 x 5120 7.0 us.
+// 95); one row of 6144 x 5120 10.2 us, 3.1 TB/s of weights (6.1
+// once they flow); 37 rows of 2120 x 5120 7.1 us.
 //
 // Roles: warp 0 operand copies, 1 MMA, 2-3 scales and tensor memory, 4-11
 // epilogue, two warps for each TMEM sub-partition (with four of half the columns

@@ -34,12 +34,13 @@
 // depend on who took which item when.
 //
 // Measured (a call among others in a graph; H 5120, I 2048, 64 experts, the best 8
-// and a shared one, 8-bit weights): one token 62 us, 4.6 TB/s of weights, of which
+// and a shared one, 8-bit weights): one token 63 us, 4.5 TB/s of weights, of which
 // some 9 us pass before the first item's weights are asked for (logits, a meeting
 // of all CTAs, the choice, each of them first fetches of code and memory trips) and
-// 7 us after the last are there; 32 tokens, which reach nearly every expert, 340
-// us, 5.9 TB/s or 0.88 of a copy.  Five tokens of a small BF16 layer (1024 x 512, 16
-// experts) take 23 us, a chain of such trips.
+// 7 us after the last are there; 32 tokens, which reach nearly every expert, 342
+// us, 5.9 TB/s or 0.87 of a copy.  With BF16 weights 94 us and 596 us, 6.0 and 6.8
+// TB/s.  Five tokens of a small BF16 layer (1024 x 512, 16 experts) take 24 us, a
+// chain of such trips.
 //
 // Warps: 0 items and weight tiles, 1 MMA, 2 scales, 3 activation tiles, 4-7 sums
 // (tensor memory to buffers), 8-11 joins (buffers to scratch, activations).
