@@ -19,8 +19,8 @@
  * largest magnitude, floored at 2^-100, as amax, and round x * (448 / amax)
  * to nearest-even.  The quotients are taken as amax * (1 / 448) and (1 / amax) *
  * 448, every step rounded to nearest in FP32 (but 1 / amax may be the neighbour
- * below where amax has 24 significant bits, all ones).  A block that holds an infinity or
- * a NaN has a non-finite scale.
+ * below where amax has 24 significant bits, all ones).  A block that holds an
+ * infinity or a NaN has a non-finite scale.
  *
  * Conventions: as in mhc_boundary.h (device pointers, caller-owned buffers,
  * every argument checked before the first launch, nothing aborts or traps).

@@ -252,7 +252,7 @@ def mhc_test_moe_form(config: mhc_sublayer_config_t, m: int, sms: int) -> mhc_te
     out = mhc_test_moe_form_t()
     status = lib().mhc_test_moe_form(ctypes.byref(config), int(m), int(sms), ctypes.byref(out))
     if status != MHC_OK:
-        raise MhcError(status, "m or sms out of range")
+        raise MhcError(status, "config, m or sms out of range")
     return out
 
 

@@ -410,7 +410,9 @@ mhc_status_t mhc_test_stall_sublayer_copies(int32_t on) {
 }
 
 mhc_status_t mhc_test_moe_form(const mhc_sublayer_config_t *config, int32_t m, int32_t sms, mhc_test_moe_form_t *out) {
-  if (!config || !out || m < 1 || m > MOE_TOKENS_MAX || sms < 1) return MHC_ERR_INVALID_ARG;
+  if (!config || !out || m < 1 || m > MOE_TOKENS_MAX || sms < 1 || config->hidden < 1 || config->intermediate < 1 ||
+      config->top_k < 1 || config->shared_experts < 0)
+    return MHC_ERR_INVALID_ARG;
   MoeParams p = {};
   p.m = m;
   p.hidden = config->hidden;

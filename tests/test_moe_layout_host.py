@@ -47,3 +47,12 @@ def test_every_read_lies_inside(capi, sms, fp8):
                         first = (f.items * f.scale_blocks - 1) * m   # the last block's
                         assert f.scales_at + 4 * (first + max(widths(m))) <= f.size, what
                         assert f.scale_blocks <= 32, what            # a block a lane
+
+
+def test_the_hook_refuses_what_no_call_has(capi):
+    good = (256, 128, 8, 1, 2, 4, 0, 1.0, capi.MHC_SUBLAYER_FP8)
+    capi.mhc_test_moe_form(capi.mhc_sublayer_config_t(*good), 4, 152)
+    for config, m, sms in ((good, 0, 152), (good, 33, 152), (good, 4, 0), ((0,) + good[1:], 4, 152),
+                           (good[:4] + (0,) + good[5:], 4, 152)):
+        with pytest.raises(capi.MhcError, match="MHC_ERR_INVALID_ARG"):
+            capi.mhc_test_moe_form(capi.mhc_sublayer_config_t(*config), m, sms)
