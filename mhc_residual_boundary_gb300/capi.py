@@ -1,5 +1,5 @@
-"""ctypes binding of include/mhc_boundary.h and include/mhc_sublayer.h
-(argument marshalling only).
+"""ctypes binding of include/mhc_boundary.h, include/mhc_sublayer.h and
+include/mhc_attention.h (argument marshalling only).
 
 The functions keep the C names; every step of the boundary runs in the CUDA
 library.  Loading fails loudly when the library has not been built: there is
@@ -104,6 +104,35 @@ class mhc_sublayer_moe_args_t(ctypes.Structure):
         "x", "router", "bias", "gate_up", "gate_up_scales", "down", "down_scales", "output", "idx", "weights")]
 
 
+MHC_ATTENTION_FP8 = 1 << 0
+MHC_ATTENTION_INTERLEAVED = 1 << 1
+
+
+class mhc_attention_config_t(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("heads", "kv_heads", "head_dim", "page_size", "rotary_dim")] + [
+        ("flags", ctypes.c_uint32), ("theta", ctypes.c_double), ("frequencies", ctypes.POINTER(ctypes.c_double))]
+
+
+class mhc_attention_append_args_t(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("pages", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+                ("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64),
+                ("k_cache", ctypes.c_void_p), ("k_page_stride", ctypes.c_int64), ("v_cache", ctypes.c_void_p),
+                ("v_page_stride", ctypes.c_int64), ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class mhc_attention_attend_args_t(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("sequences", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("q_starts", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("k_cache", ctypes.c_void_p), ("k_page_stride", ctypes.c_int64),
+                ("v_cache", ctypes.c_void_p), ("v_page_stride", ctypes.c_int64), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("scale", ctypes.c_float), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("output", ctypes.c_void_p), ("output_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p)]
+
+
 class mhc_test_moe_form_t(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int32) for f in ("size", "ring_at", "stages", "stage_bytes", "weight_bytes", "scales_at",
                                               "items", "scale_blocks")]
@@ -112,6 +141,7 @@ class mhc_test_moe_form_t(ctypes.Structure):
 SUBLAYER_CALLS = {"add_rms_norm": mhc_sublayer_norm_args_t, "quantize": mhc_sublayer_quantize_args_t,
                   "swiglu": mhc_sublayer_quantize_args_t, "matmul": mhc_sublayer_matmul_args_t,
                   "moe": mhc_sublayer_moe_args_t}
+ATTENTION_CALLS = {"append": mhc_attention_append_args_t, "attend": mhc_attention_attend_args_t}
 
 _lib = None
 
@@ -162,6 +192,15 @@ def lib() -> ctypes.CDLL:
             getattr(h, "mhc_sublayer_" + name).restype = st
         h.mhc_sublayer_last_error.argtypes = [vp]
         h.mhc_sublayer_last_error.restype = ctypes.c_char_p
+        h.mhc_attention_create.argtypes = [ctypes.POINTER(mhc_attention_config_t), ctypes.c_int, ctypes.POINTER(vp)]
+        for name, args in ATTENTION_CALLS.items():
+            getattr(h, "mhc_attention_" + name).argtypes = [vp, ctypes.POINTER(args), vp]
+        h.mhc_attention_check_errors.argtypes = [vp]
+        h.mhc_attention_destroy.argtypes = [vp]
+        for name in ("create", "check_errors", "destroy", *ATTENTION_CALLS):
+            getattr(h, "mhc_attention_" + name).restype = st
+        h.mhc_attention_last_error.argtypes = [vp]
+        h.mhc_attention_last_error.restype = ctypes.c_char_p
         h.mhc_mxfp8_scale_bytes.restype = ctypes.c_size_t
         h.mhc_boundary_launches_per_call.argtypes = [vp]
         h.mhc_boundary_launches_per_call.restype = ctypes.c_int32
@@ -302,6 +341,41 @@ def mhc_sublayer_check_errors(handle) -> None:
 
 def mhc_sublayer_destroy(handle) -> None:
     _check_sublayer(lib().mhc_sublayer_destroy(handle), None)
+
+
+def _check_attention(status: int, handle) -> None:
+    if status != MHC_OK:
+        raise MhcError(status, lib().mhc_attention_last_error(handle).decode())
+
+
+def attention_calls() -> dict:
+    """As sublayer_calls, for the attention's."""
+    vp = ctypes.c_void_p
+    lib()
+    proto = ctypes.CFUNCTYPE(ctypes.c_int, vp, ctypes.c_char_p, vp)
+    return {name: proto(("mhc_attention_" + name, _lib)) for name in ATTENTION_CALLS}
+
+
+def mhc_attention_create(config: mhc_attention_config_t, device: int) -> ctypes.c_void_p:
+    handle = ctypes.c_void_p()
+    _check_attention(lib().mhc_attention_create(ctypes.byref(config), int(device), ctypes.byref(handle)), None)
+    return handle
+
+
+def mhc_attention_append(handle, args: mhc_attention_append_args_t, stream=None) -> None:
+    _check_attention(lib().mhc_attention_append(handle, ctypes.byref(args), _stream_ptr(stream)), handle)
+
+
+def mhc_attention_attend(handle, args: mhc_attention_attend_args_t, stream=None) -> None:
+    _check_attention(lib().mhc_attention_attend(handle, ctypes.byref(args), _stream_ptr(stream)), handle)
+
+
+def mhc_attention_check_errors(handle) -> None:
+    _check_attention(lib().mhc_attention_check_errors(handle), handle)
+
+
+def mhc_attention_destroy(handle) -> None:
+    _check_attention(lib().mhc_attention_destroy(handle), None)
 
 
 def mhc_boundary_profile_begin(handle, max_calls: int) -> None:

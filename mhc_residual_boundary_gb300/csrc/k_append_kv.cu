@@ -1,0 +1,147 @@
+// k_append_kv.cu -- new tokens' queries and keys rotated by their positions, keys
+// and values written to their slots of a paged cache (BF16, or E4M3 with one
+// FP32 scale for each position and head).
+//
+//   pair i of a rotated head: (a, b) -> (a cos w - b sin w, b cos w + a sin w),
+//   w = position * f(i)
+// The angle in turns is position * (f(i) / 2 pi); only its part behind the point
+// matters.  f(i) / 2 pi is held as a 64-bit binary fraction, so the product in 64
+// bits, which drops the whole turns, is exact but for the fraction's own last bit
+// times the position: no position is so far that the angle loses anything.  Its
+// upper 32 bits, signed, give the angle between -pi and pi.
+#include "attention.cuh"
+#include "device_common.cuh"
+#include "e4m3_scale.h"
+
+namespace mhc {
+namespace {
+
+constexpr int APPEND_THREADS = 256;
+
+// 16 bytes of a row that this thread may write later (q_out may be q).
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint2 quant8(const float (&y)[8], float inv) {
+  return make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                    e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+}
+
+// One token a blockIdx.x; a thread takes 16 elements of one head: two 16-byte
+// fragments that a rotation pairs.
+template <int DIM>
+__global__ void __launch_bounds__(APPEND_THREADS) k_append_kv(const AppendParams p) {
+  constexpr int UNITS = DIM / 16;   // threads a head
+  __shared__ float2 turn[DIM / 2];  // cos, sin
+  const int token = blockIdx.x, item = blockIdx.y * APPEND_THREADS + threadIdx.x;
+  const int unit = item % UNITS, row = item / UNITS;
+  const int heads = p.q ? p.heads : 0;
+  const bool live = row < heads + 2 * p.kv_heads;
+  const bool is_q = row < heads, is_v = row >= heads + p.kv_heads;
+  const int head = is_q ? row : is_v ? row - heads - p.kv_heads : row - heads;
+  // its fragments: those that a rotation pairs, else the next two
+  const bool rotated = unit < p.rotary / 16;
+  const int fa = rotated && !p.interleaved ? unit : 2 * unit, fb = rotated && !p.interleaved ? unit + p.rotary / 16 : fa + 1;
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint16_t *x = is_q ? p.q + token * p.q_stride : is_v ? p.v + token * p.v_stride : p.k + token * p.k_stride;
+  x += int64_t(head) * DIM;
+  uint4 va = make_uint4(0, 0, 0, 0), vb = va;
+  if (live) {
+    va = ld_once(x + fa * 8);
+    vb = ld_once(x + fb * 8);
+  }
+  const int slot = p.slots[token];
+  for (int i = threadIdx.x; i < p.rotary / 2; i += APPEND_THREADS) {
+    const uint64_t w = uint64_t(int64_t(p.positions[token])) * p.turns[i];
+    float s, c;
+    sincospif(float(int32_t(w >> 32)) * 0x1p-31f, &s, &c);
+    turn[i] = make_float2(c, s);
+  }
+  __syncthreads();
+  float a[8], b[8];
+  unpack8(va, a);
+  unpack8(vb, b);
+  if (rotated && !is_v) {
+    if (p.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float2 ta = turn[unit * 8 + i / 2], tb = turn[unit * 8 + 4 + i / 2];
+        const float a0 = a[i], b0 = b[i];
+        a[i] = a0 * ta.x - a[i + 1] * ta.y;
+        a[i + 1] = a[i + 1] * ta.x + a0 * ta.y;
+        b[i] = b0 * tb.x - b[i + 1] * tb.y;
+        b[i + 1] = b[i + 1] * tb.x + b0 * tb.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 t = turn[unit * 8 + i];
+        const float a0 = a[i];
+        a[i] = a0 * t.x - b[i] * t.y;
+        b[i] = b[i] * t.x + a0 * t.y;
+      }
+    }
+  }
+  if (live && is_q) {
+    uint16_t *y = p.q_out + token * p.q_out_stride + int64_t(head) * DIM;
+    st_vec(y + fa * 8, pack8(a));
+    st_vec(y + fb * 8, pack8(b));
+  }
+  const int64_t rows = int64_t(p.pages) << p.page_shift;
+  const bool keep = live && !is_q && slot >= 0 && slot < rows;
+  if (slot < -1 || slot >= rows) {
+    if (threadIdx.x == 0) atomicOr(p.err, ATTN_ERR_INDEX);
+  }
+  const CacheParams &cache = is_v ? p.values : p.keys;
+  const int page = slot >> p.page_shift;
+  const int64_t in_page = (int64_t(head) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+  const int64_t at = page * cache.page_stride + in_page * DIM;
+  if (!p.fp8) {
+    if (keep) {
+      uint16_t *y = static_cast<uint16_t *>(cache.data) + at;
+      st_vec(y + fa * 8, pack8(a));
+      st_vec(y + fb * 8, pack8(b));
+    }
+    return;
+  }
+  // magnitudes compare as bit patterns: a NaN reaches the scale
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    top = max(top, max(__float_as_uint(a[i]) & 0x7fffffffu, __float_as_uint(b[i]) & 0x7fffffffu));
+#pragma unroll
+  for (int o = UNITS / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float amax = __uint_as_float(max(top, uint32_t(127 - 100) << 23));
+  const float inv = e4m3_inverse(amax, rcp_fast(e4m3_divisor(amax)));
+  if (keep) {
+    uint8_t *y = static_cast<uint8_t *>(cache.data) + at;
+    *reinterpret_cast<uint2 *>(y + fa * 8) = quant8(a, inv);
+    *reinterpret_cast<uint2 *>(y + fb * 8) = quant8(b, inv);
+    if (unit == 0) cache.scales[((int64_t(page) * p.kv_heads) << p.page_shift) + in_page] = e4m3_scale(amax);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams &p, cudaStream_t stream) {
+  const int items = ((p.q ? p.heads : 0) + 2 * p.kv_heads) * (p.dim / 16);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.tokens, (items + APPEND_THREADS - 1) / APPEND_THREADS);
+  cfg.blockDim = dim3(APPEND_THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return p.dim == 128 ? cudaLaunchKernelEx(&cfg, k_append_kv<128>, p) : cudaLaunchKernelEx(&cfg, k_append_kv<64>, p);
+}
+
+}  // namespace mhc
