@@ -22,6 +22,8 @@ struct mhc_attention {
   int page_shift = 0;
   unsigned int *err = nullptr;       // device error word
   uint64_t *turns = nullptr;         // [rotary_dim / 2], see k_append_kv.cu
+  unsigned int *counters = nullptr;  // attend's scratch, see AttendParams
+  float *parts = nullptr;
   std::string last_error;
 };
 
@@ -121,6 +123,8 @@ mhc_status_t check_cache(mhc_attention_t *a, int pages, const void *k, int64_t k
 
 void release(mhc_attention_t *a) {
   if (a->turns) cudaFree(a->turns);
+  if (a->counters) cudaFree(a->counters);
+  if (a->parts) cudaFree(a->parts);
   if (a->err) cudaFree(a->err);
 }
 
@@ -170,6 +174,10 @@ mhc_status_t mhc_attention_create(const mhc_attention_config_t *config, int devi
     e = cudaMalloc(&a->turns, turns.size() * sizeof(uint64_t));
     if (e == cudaSuccess) e = cudaMemcpy(a->turns, turns.data(), turns.size() * sizeof(uint64_t), cudaMemcpyHostToDevice);
   }
+  if (e == cudaSuccess) e = attend_one_setup();
+  if (e == cudaSuccess) e = cudaMalloc(&a->parts, attend_one_scratch(a->sm_count));
+  if (e == cudaSuccess) e = cudaMalloc(&a->counters, a->sm_count * sizeof(unsigned int));
+  if (e == cudaSuccess) e = cudaMemset(a->counters, 0, a->sm_count * sizeof(unsigned int));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     const mhc_status_t st = e == cudaErrorMemoryAllocation ? MHC_ERR_OOM : MHC_ERR_CUDA;
@@ -302,8 +310,12 @@ mhc_status_t mhc_attention_attend(mhc_attention_t *a, const mhc_attention_attend
   p.sinks = g->window ? g->sinks : 0;
   p.output = static_cast<uint16_t *>(g->output);
   p.lse = g->lse;
+  p.parts = a->parts;
+  p.counters = a->counters;
   p.err = a->err;
-  return launched(a, launch_attend(p, reinterpret_cast<cudaStream_t>(stream)), "attend");
+  const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
+  const bool one = !g->q_starts && c.heads / c.kv_heads <= ATTEND_ONE_GROUP;
+  return launched(a, one ? launch_attend_one(p, a->sm_count, on) : launch_attend(p, on), "attend");
 }
 
 mhc_status_t mhc_attention_check_errors(mhc_attention_t *a) {

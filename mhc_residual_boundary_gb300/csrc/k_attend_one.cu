@@ -1,0 +1,636 @@
+// k_attend_one.cu -- attention of one query a sequence over a paged cache, up to
+// 16 query heads for each key and value head.
+//
+// The work is the reading of the cache: 4 d flops for every 2 d bytes (BF16) and
+// head of a group, far below what the tensor cores do in that time.  So:
+//  * Every row of the cache is read once, for all heads of its group, by 16-byte
+//    asynchronous copies into shared memory; a warp keeps STAGES - 1 tiles (about
+//    16 KB) on their way while it works on one.  Copies of places that are not there
+//    (behind the end, a page out of range) read nothing and leave zeros.
+//  * A sequence and kv head's visible positions (the first ones and the window, one
+//    behind the other) are cut into units of 8 warps' tiles.  The call's units form one
+//    line, which is divided evenly over one CTA an SM, whatever the lengths are; a
+//    CTA's part of a (sequence, head) is a segment.  Copies run on across the
+//    segments' ends.
+//  * Warps work alone, each on its own tiles with its own running maximum, sum and
+//    output (16 rows x head_dim in registers), and meet at a segment's end.
+//  * A segment that is not a whole (sequence, head) goes to scratch; the CTA that
+//    comes last joins the parts, in their order, so that the bits do not depend on it.
+//
+// Products are m16n8k16 with the 16 rows the group's heads: S = Q K^T and O = P V.
+// The order of the products' inner indexes is free as long as both factors use the
+// same: lanes take their B fragments as whole 16-byte pieces of K's and V's rows, and
+// the fragments of Q and the columns of O follow.  Over a BF16 cache P goes in as two
+// BF16 pieces (16 bits of it), over an 8-bit one everything is FP16: E4M3 fits it,
+// Q is taken with a power of two off each row, and P carries the value's scale,
+// 2^(x + log2 scale - its own running maximum), so that it uses FP16's upper range.
+#include <algorithm>
+
+#include "attention.cuh"
+#include "device_common.cuh"
+
+namespace mhc {
+namespace {
+
+constexpr int WARPS = 8, THREADS = WARPS * 32;
+
+template <int D, bool FP8>
+struct One {
+  static constexpr int ROW = FP8 ? D : 2 * D;             // bytes of a cache row
+  static constexpr int CHUNKS = ROW / 16;
+  static constexpr int KEYS = !FP8 && D == 128 ? 16 : 32; // of a warp's tile
+  static constexpr int TILE = KEYS * ROW;                 // bytes, keys or values
+  static constexpr int STAGE = 2 * TILE + (FP8 ? KEYS * 8 : 0);
+  static constexpr int STAGES = STAGE > 5000 ? 3 : 6;
+  static constexpr int UNIT = WARPS * KEYS;
+  static constexpr int PASS = FP8 ? 4 : 8;                // rows that the warps meet over at a time
+  static constexpr int MEET_ROW = D;                      // floats
+  static constexpr int RING = WARPS * STAGES * STAGE;
+  static constexpr int SMEM = RING + WARPS * PASS * MEET_ROW * 4 + WARPS * 16 * 16 + WARPS * STAGES * 4;
+  static_assert(SMEM <= 227 * 1024, "a CTA's shared memory");
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
+// 16 or 4 bytes to shared memory; zeros where `there` is false (nothing is read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+template <bool FP8>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (FP8)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two E4M3 values (the lower or upper half of w) as an FP16 pair.
+__device__ __forceinline__ uint32_t f16_lower(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(w)));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16_upper(uint32_t w) { return f16_lower(w >> 16); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// What one query of a sequence sees: `count` positions, the first `sinks` and the
+// ones from `first` on.
+struct Seen {
+  int count, sinks, first;
+};
+__device__ __forceinline__ Seen seen_by_last(const AttendParams &p, int length) {
+  Seen v;
+  v.first = p.window && length > p.window ? length - p.window : 0;
+  v.sinks = min(p.sinks, v.first);
+  v.count = v.sinks + length - v.first;
+  return v;
+}
+
+// A place on the line of units: unit `unit` of `units` of (sequence s, head h).
+struct Cursor {
+  int s, h, unit, units;
+  Seen seen;
+};
+
+template <int D, bool FP8>
+__device__ __forceinline__ int units_of(const Seen &v) {
+  return (v.count + One<D, FP8>::UNIT - 1) / One<D, FP8>::UNIT;
+}
+
+// To the first unit of the next (sequence, head); there has to be one.
+template <int D, bool FP8>
+__device__ __forceinline__ void next_head(const AttendParams &p, Cursor &c) {
+  c.unit = 0;
+  if (++c.h < p.kv_heads) return;
+  c.h = 0;
+  bool bad = false;
+  do {
+    c.seen = seen_by_last(p, sequence_length(p, ++c.s, bad));
+    c.units = units_of<D, FP8>(c.seen);
+  } while (c.units == 0);
+}
+
+// One part of a (sequence, head) in scratch: [16][D] of output, then [16] of
+// (maximum, sum, maximum of the output's weights, -).
+template <int D>
+constexpr int part_floats() { return 16 * (D + 4); }
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p) {
+  using F = One<D, FP8>;
+  constexpr int N_TILES = D / 8;       // of 8 output columns
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int64_t warp_total[WARPS];
+  __shared__ Cursor begin_shared;
+  __shared__ int last_shared;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const int group = p.heads / p.kv_heads;
+  bool bad = false;
+
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- this CTA's part of the line
+  const int chunk = (p.sequences + THREADS - 1) / THREADS;
+  int64_t mine = 0;
+  bool empty = false;
+  for (int i = 0; i < chunk; ++i) {
+    const int s = tid * chunk + i;
+    if (s >= p.sequences) break;
+    const int units = units_of<D, FP8>(seen_by_last(p, sequence_length(p, s, bad)));
+    empty |= units == 0;
+    mine += int64_t(units) * p.kv_heads;
+  }
+  int64_t upto = mine;   // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) warp_total[warp] = upto;
+  const bool any_empty = __syncthreads_or(empty);
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) upto += warp_total[w];
+    total += warp_total[w];
+  }
+  // CTAs that work: no more than there are units, so that each of them has some
+  const int64_t grid = max(int64_t(1), min(int64_t(gridDim.x), total)), cta = min(int64_t(blockIdx.x), grid);
+  const int64_t line0 = cta * total / grid, line1 = min(cta + 1, grid) * total / grid;
+  if (line0 < line1 && upto - mine <= line0 && line0 < upto) {
+    int64_t at = upto - mine;
+    bool seen_before = false;
+    for (int s = tid * chunk;; ++s) {
+      Cursor c;
+      c.s = s;
+      c.seen = seen_by_last(p, sequence_length(p, s, seen_before));
+      c.units = units_of<D, FP8>(c.seen);
+      const int64_t n = int64_t(c.units) * p.kv_heads;
+      if (line0 < at + n) {
+        c.h = int((line0 - at) / c.units);
+        c.unit = int((line0 - at) % c.units);
+        begin_shared = c;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+
+  unsigned char *ring = smem + warp * F::STAGES * F::STAGE;
+  const uint32_t ring_at = smem_u32(ring);
+  float *meet = reinterpret_cast<float *>(smem + F::RING);             // [WARPS][PASS][MEET_ROW]
+  float4 *stats = reinterpret_cast<float4 *>(meet + WARPS * F::PASS * F::MEET_ROW);   // [WARPS][16]
+  uint32_t *masks = reinterpret_cast<uint32_t *>(stats + WARPS * 16) + warp * F::STAGES;
+
+  Cursor at = begin_shared, ahead = at;
+  int64_t left = line1 - line0, left_ahead = left;
+
+  // ---- copies: the tile of this warp at `ahead`, whose page number was read one step before
+  int page_ahead = -1, key_ahead = 0;
+  auto look = [&]() {
+    page_ahead = -1;
+    if (left_ahead <= 0) return;
+    const int v = ahead.unit * F::UNIT + warp * F::KEYS + lane;
+    if (lane < F::KEYS && v < ahead.seen.count) {
+      key_ahead = v < ahead.seen.sinks ? v : v - ahead.seen.sinks + ahead.seen.first;
+      page_ahead = p.page_table[ahead.s * p.table_stride + (key_ahead >> p.page_shift)];
+      if (page_ahead < 0 || page_ahead >= p.pages) {
+        bad = true;
+        page_ahead = -1;
+      }
+    }
+  };
+  const int page_mask = (1 << p.page_shift) - 1;
+  auto issue = [&](int stage) {
+    if (left_ahead > 0) {
+      const int offset = (ahead.h << p.page_shift) + (key_ahead & page_mask);
+      const uint32_t to = ring_at + stage * F::STAGE;
+      const uint32_t there = __ballot_sync(0xffffffffu, page_ahead >= 0);
+      if (lane == 0) masks[stage] = there;
+#pragma unroll
+      for (int i = 0; i < F::KEYS * F::CHUNKS / 32; ++i) {
+        const int row = (i * 32 + lane) / F::CHUNKS, c = (i * 32 + lane) % F::CHUNKS;
+        const int page = __shfl_sync(0xffffffffu, page_ahead, row), in_page = __shfl_sync(0xffffffffu, offset, row);
+        const bool ok = page >= 0;
+        const int64_t k = ok ? page * p.keys.page_stride + int64_t(in_page) * D : 0;
+        const int64_t v = ok ? page * p.values.page_stride + int64_t(in_page) * D : 0;
+        const int ck = F::CHUNKS >= 8 ? c ^ ((row & 1) << 2) : c;
+        const int cv = F::CHUNKS >= 8 ? c ^ ((row >> 1 & 3) << 1) : c ^ (row >> 1 & 3);
+        copy16(to + row * F::ROW + ck * 16, static_cast<const unsigned char *>(p.keys.data) + k * (FP8 ? 1 : 2) + c * 16, ok);
+        copy16(to + F::TILE + row * F::ROW + cv * 16, static_cast<const unsigned char *>(p.values.data) + v * (FP8 ? 1 : 2) + c * 16, ok);
+      }
+      if (FP8) {
+        const bool ok = page_ahead >= 0;
+        const int64_t from = ok ? ((int64_t(page_ahead) * p.kv_heads) << p.page_shift) + offset : 0;
+        copy4(to + 2 * F::TILE + lane * 4, p.keys.scales + from, ok);
+        copy4(to + 2 * F::TILE + (F::KEYS + lane) * 4, p.values.scales + from, ok);
+      }
+      --left_ahead;
+      if (++ahead.unit == ahead.units && left_ahead > 0) next_head<D, FP8>(p, ahead);
+      look();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  look();
+  for (int i = 0; i < F::STAGES; ++i) issue(i);
+
+  // ---- sequences that see nothing
+  if (any_empty) {
+    for (int s = blockIdx.x; s < p.sequences; s += gridDim.x) {
+      if (sequence_length(p, s, bad) > 0) continue;
+      for (int i = tid; i < p.heads * D / 8; i += THREADS)
+        st_vec(p.output + s * p.output_stride + i * 8, make_uint4(0, 0, 0, 0));
+      for (int i = tid; p.lse && i < p.heads; i += THREADS) p.lse[int64_t(s) * p.heads + i] = -INFINITY;
+    }
+  }
+
+  int stage = 0;
+  while (left > 0) {
+    // ---- a segment: units at.unit .. of (at.s, at.h), as far as this CTA's part goes
+    const int unit0 = at.unit, count = int(left < at.units - at.unit ? left : int64_t(at.units - at.unit));
+    const uint16_t *q = p.q + at.s * p.q_stride + int64_t(at.h) * group * D;
+    uint32_t qa[D / 16][4];
+    float row_scale[2] = {p.scale_log2, p.scale_log2};
+    if (!FP8) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const uint4 lo = g < group ? ld_vec(q + g * D + (4 * i + t) * 8) : zero;
+        const uint4 hi = g + 8 < group ? ld_vec(q + (g + 8) * D + (4 * i + t) * 8) : zero;
+        qa[2 * i][0] = lo.x; qa[2 * i][1] = hi.x; qa[2 * i][2] = lo.y; qa[2 * i][3] = hi.y;
+        qa[2 * i + 1][0] = lo.z; qa[2 * i + 1][1] = hi.z; qa[2 * i + 1][2] = lo.w; qa[2 * i + 1][3] = hi.w;
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float x[D / 64][2][8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = g + 8 * r;
+            unpack8(row < group ? ld_vec(q + row * D + (4 * i + t) * 16 + e * 8) : make_uint4(0, 0, 0, 0), x[i][e]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[i][e][k]) & 0x7fffffffu);
+          }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the row's largest magnitude to [1, 2)
+        const int e2 = min(max(int(top >> 23) - 127, -126), 126);
+        const float down = __uint_as_float(uint32_t(127 - e2) << 23);
+        row_scale[r] = p.scale_log2 * __uint_as_float(uint32_t(127 + e2) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float *y = x[i][k / 2] + k % 2 * 4;
+            qa[4 * i + k][r] = pack_f16x2(y[0] * down, y[1] * down);
+            qa[4 * i + k][2 + r] = pack_f16x2(y[2] * down, y[3] * down);
+          }
+      }
+    }
+    float acc[N_TILES][4];
+#pragma unroll
+    for (int i = 0; i < N_TILES; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    float top[2] = {-INFINITY, -INFINITY}, top_out[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+
+    for (int u = 0; u < count; ++u) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(F::STAGES - 1) : "memory");
+      __syncwarp();
+      const uint32_t from = ring_at + stage * F::STAGE;
+      const uint32_t there = masks[stage];
+      if (there) {
+        // ---- x = scale (q k) log2(e)
+        float x[F::KEYS / 8][4];
+#pragma unroll
+        for (int n = 0; n < F::KEYS / 8; ++n) {
+          x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+          const int row = n * 8 + g;
+#pragma unroll
+          for (int i = 0; i < F::CHUNKS / 4; ++i) {
+            const int c = 4 * i + t, ck = F::CHUNKS >= 8 ? c ^ ((row & 1) << 2) : c;
+            const uint4 w = lds16(from + row * F::ROW + ck * 16);
+            if (FP8) {
+              mma<FP8>(x[n], qa[4 * i], f16_lower(w.x), f16_upper(w.x));
+              mma<FP8>(x[n], qa[4 * i + 1], f16_lower(w.y), f16_upper(w.y));
+              mma<FP8>(x[n], qa[4 * i + 2], f16_lower(w.z), f16_upper(w.z));
+              mma<FP8>(x[n], qa[4 * i + 3], f16_lower(w.w), f16_upper(w.w));
+            } else {
+              mma<FP8>(x[n], qa[2 * i], w.x, w.y);
+              mma<FP8>(x[n], qa[2 * i + 1], w.z, w.w);
+            }
+          }
+        }
+        float y[FP8 ? F::KEYS / 8 : 1][4];   // x + log2 of the value's scale
+        float now[2] = {-INFINITY, -INFINITY}, now_out[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < F::KEYS / 8; ++n) {
+          float2 ks, vs;
+          if (FP8) {
+            const uint2 a = lds8(from + 2 * F::TILE + (n * 8 + 2 * t) * 4), b = lds8(from + 2 * F::TILE + (F::KEYS + n * 8 + 2 * t) * 4);
+            ks = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+            vs = make_float2(log2_fast(__uint_as_float(b.x)), log2_fast(__uint_as_float(b.y)));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool ok = there >> (n * 8 + 2 * t + (e & 1)) & 1;
+            float v = x[n][e] * row_scale[e / 2];
+            if (FP8) v *= e & 1 ? ks.y : ks.x;
+            x[n][e] = ok ? v : -INFINITY;
+            now[e / 2] = fmaxf(now[e / 2], x[n][e]);
+            if (FP8) {
+              y[n][e] = ok ? v + (e & 1 ? vs.y : vs.x) : -INFINITY;
+              now_out[e / 2] = fmaxf(now_out[e / 2], y[n][e]);
+            }
+          }
+        }
+        // ---- the running maxima, over the four lanes of a row
+        float base[2], base_out[2];
+        bool grew = false;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          now[r] = fmaxf(now[r], __shfl_xor_sync(0xffffffffu, now[r], 1));
+          now[r] = fmaxf(now[r], __shfl_xor_sync(0xffffffffu, now[r], 2));
+          now[r] = fmaxf(now[r], top[r]);
+          grew |= now[r] != top[r];
+          base[r] = now[r] == -INFINITY ? 0.f : now[r];
+          base_out[r] = base[r];
+          if (FP8) {
+            now_out[r] = fmaxf(now_out[r], __shfl_xor_sync(0xffffffffu, now_out[r], 1));
+            now_out[r] = fmaxf(now_out[r], __shfl_xor_sync(0xffffffffu, now_out[r], 2));
+            now_out[r] = fmaxf(now_out[r], top_out[r]);
+            grew |= now_out[r] != top_out[r];
+            base_out[r] = now_out[r] == -INFINITY ? 0.f : now_out[r];
+          }
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float f = exp2_fast(top[r] - base[r]);
+            const float fo = FP8 ? exp2_fast(top_out[r] - base_out[r]) : f;
+            sum[r] *= f;
+            top[r] = now[r];
+            if (FP8) top_out[r] = now_out[r];
+#pragma unroll
+            for (int i = 0; i < N_TILES; ++i) {
+              acc[i][2 * r] *= fo;
+              acc[i][2 * r + 1] *= fo;
+            }
+          }
+        }
+        // ---- weights and their sum, weights times values, 16 positions at a time
+#pragma unroll
+        for (int j = 0; j < F::KEYS / 16; ++j) {
+          uint32_t pa[4], pb[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int n = 2 * j + k / 2, r = k % 2;
+            const float w0 = exp2_fast(x[n][2 * r] - base[r]), w1 = exp2_fast(x[n][2 * r + 1] - base[r]);
+            sum[r] += w0 + w1;
+            if (FP8) {
+              pa[k] = pack_f16x2(exp2_fast(y[n][2 * r] - base_out[r]), exp2_fast(y[n][2 * r + 1] - base_out[r]));
+            } else {
+              pa[k] = pack_bf16x2(w0, w1);
+              pb[k] = pack_bf16x2(w0 - bf16_lo(pa[k]), w1 - bf16_hi(pa[k]));
+            }
+          }
+          const int row = j * 16 + 2 * t;   // this lane's positions: row, row + 1, row + 8, row + 9
+          if (!FP8) {
+#pragma unroll
+            for (int hh = 0; hh < D / 64; ++hh) {
+              uint32_t v[4][4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int rr = row + (i & 1) + (i >> 1) * 8;
+                const uint4 w = lds16(from + F::TILE + rr * F::ROW + ((hh * 8 + g) ^ ((rr >> 1 & 3) << 1)) * 16);
+                v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
+              }
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t e0 = __byte_perm(v[0][w], v[1][w], 0x5410), e1 = __byte_perm(v[2][w], v[3][w], 0x5410);
+                const uint32_t o0 = __byte_perm(v[0][w], v[1][w], 0x7632), o1 = __byte_perm(v[2][w], v[3][w], 0x7632);
+                mma<FP8>(acc[hh * 8 + 2 * w], pa, e0, e1);
+                mma<FP8>(acc[hh * 8 + 2 * w + 1], pa, o0, o1);
+                mma<FP8>(acc[hh * 8 + 2 * w], pb, e0, e1);
+                mma<FP8>(acc[hh * 8 + 2 * w + 1], pb, o0, o1);
+              }
+            }
+          } else {
+            uint32_t v[4][D / 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int rr = row + (i & 1) + (i >> 1) * 8;
+              if (D == 128) {
+                const uint4 w = lds16(from + F::TILE + rr * F::ROW + (g ^ ((rr >> 1 & 3) << 1)) * 16);
+                v[i][0] = w.x; v[i][1] = w.y; v[i][D / 32 - 2] = w.z; v[i][D / 32 - 1] = w.w;
+              } else {
+                const uint2 w = lds8(from + F::TILE + rr * F::ROW + ((g >> 1) ^ (rr >> 1 & 3)) * 16 + (g & 1) * 8);
+                v[i][0] = w.x; v[i][1] = w.y;
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+              const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[2][w], v[3][w], 0x5140);
+              const uint32_t b0 = __byte_perm(v[0][w], v[1][w], 0x7362), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+              mma<FP8>(acc[4 * w], pa, f16_lower(a0), f16_lower(a1));
+              mma<FP8>(acc[4 * w + 1], pa, f16_upper(a0), f16_upper(a1));
+              mma<FP8>(acc[4 * w + 2], pa, f16_lower(b0), f16_lower(b1));
+              mma<FP8>(acc[4 * w + 3], pa, f16_upper(b0), f16_upper(b1));
+            }
+          }
+        }
+      }
+      __syncwarp();
+      issue(stage);
+      if (++stage == F::STAGES) stage = 0;
+    }
+
+    // ---- the warps meet: rows PASS at a time, weighted to the common maximum
+    const bool whole = count == at.units;
+    // CTAs that have units of this (sequence, head), and where their parts are
+    const int64_t seg0 = line1 - left - unit0;   // its first unit on the line
+    const int cta0 = int(((seg0 + 1) * grid - 1) / total), cta1 = int(((seg0 + at.units) * grid - 1) / total);
+    float *parts = p.parts;
+    const int slot = 2 * blockIdx.x + (int(blockIdx.x) == cta0);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+      if (t == 0) stats[warp * 16 + 8 * r + g] = make_float4(top[r], sum[r], FP8 ? top_out[r] : top[r], 0.f);
+    }
+    for (int r0 = 0; r0 < group; r0 += F::PASS) {
+      __syncthreads();   // stats are there; the buffer's last readers are done
+      if (g + (r0 & 8) >= r0 && g + (r0 & 8) < r0 + F::PASS) {
+        float *m = meet + (warp * F::PASS + g + (r0 & 8) - r0) * F::MEET_ROW;
+        const int r = r0 >> 3;
+#pragma unroll
+        for (int i = 0; i < N_TILES; i += 4) {
+          // columns of tile i: 2 t and 2 t + 1 stand for whole pieces of a row
+          constexpr int PIECE = FP8 && D == 128 ? 16 : 8;
+          const int d = !FP8 && D == 128 ? i / 8 * 64 + i % 8 : i;
+          const float4 a = r ? make_float4(acc[i][2], acc[i + 1][2], acc[i + 2][2], acc[i + 3][2])
+                             : make_float4(acc[i][0], acc[i + 1][0], acc[i + 2][0], acc[i + 3][0]);
+          const float4 b = r ? make_float4(acc[i][3], acc[i + 1][3], acc[i + 2][3], acc[i + 3][3])
+                             : make_float4(acc[i][1], acc[i + 1][1], acc[i + 2][1], acc[i + 3][1]);
+          *reinterpret_cast<float4 *>(m + d + 2 * t * PIECE) = a;
+          *reinterpret_cast<float4 *>(m + d + (2 * t + 1) * PIECE) = b;
+        }
+      }
+      __syncthreads();
+      const int row = r0 + tid / (D / 4), col = tid % (D / 4) * 4;
+      if (row < r0 + F::PASS && row < group) {
+        float all = -INFINITY, all_out = -INFINITY, n = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          all = fmaxf(all, stats[w * 16 + row].x);
+          all_out = fmaxf(all_out, stats[w * 16 + row].z);
+        }
+        const float b = all == -INFINITY ? 0.f : all, bo = all_out == -INFINITY ? 0.f : all_out;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float4 st = stats[w * 16 + row];
+          const float4 v = *reinterpret_cast<const float4 *>(meet + (w * F::PASS + row - r0) * F::MEET_ROW + col);
+          n += st.y * exp2_fast(st.x - b);
+          const float f = exp2_fast(st.z - bo);
+          o.x += v.x * f;
+          o.y += v.y * f;
+          o.z += v.z * f;
+          o.w += v.w * f;
+        }
+        const int head = at.h * group + row;
+        if (whole) {
+          const float f = n != 0.f ? (FP8 ? exp2_fast(bo - b) : 1.f) / n : 0.f;
+          *reinterpret_cast<uint2 *>(p.output + at.s * p.output_stride + int64_t(head) * D + col) =
+              make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+          if (p.lse && col == 0) p.lse[int64_t(at.s) * p.heads + head] = n != 0.f ? (b + log2f(n)) * 0.69314718056f : -INFINITY;
+        } else {
+          float *part = parts + int64_t(slot) * part_floats<D>();
+          *reinterpret_cast<float4 *>(part + row * D + col) = o;
+          if (col == 0) *reinterpret_cast<float4 *>(part + 16 * D + row * 4) = make_float4(all, n, all_out, 0.f);
+        }
+      }
+    }
+    if (!whole) {
+      // ---- the last CTA of this (sequence, head) joins the parts
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) last_shared = atomicAdd(p.counters + cta0, 1u) == unsigned(cta1 - cta0);
+      __syncthreads();
+      if (last_shared) {
+        __threadfence();
+        for (int item = tid; item < group * (D / 4); item += THREADS) {
+          const int row = item / (D / 4), col = item % (D / 4) * 4;
+          auto part = [&](int c) { return parts + int64_t(2 * c + (c == cta0)) * part_floats<D>(); };
+          float all = -INFINITY, all_out = -INFINITY, n = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int c = cta0; c <= cta1; ++c) {
+            const float4 st = __ldcg(reinterpret_cast<const float4 *>(part(c) + 16 * D + row * 4));
+            all = fmaxf(all, st.x);
+            all_out = fmaxf(all_out, st.z);
+          }
+          const float b = all == -INFINITY ? 0.f : all, bo = all_out == -INFINITY ? 0.f : all_out;
+#pragma unroll 8
+          for (int c = cta0; c <= cta1; ++c) {
+            const float4 st = __ldcg(reinterpret_cast<const float4 *>(part(c) + 16 * D + row * 4));
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(c) + row * D + col));
+            n += st.y * exp2_fast(st.x - b);
+            const float f = exp2_fast(st.z - bo);
+            o.x += v.x * f;
+            o.y += v.y * f;
+            o.z += v.z * f;
+            o.w += v.w * f;
+          }
+          const int head = at.h * group + row;
+          const float f = n != 0.f ? (FP8 ? exp2_fast(bo - b) : 1.f) / n : 0.f;
+          *reinterpret_cast<uint2 *>(p.output + at.s * p.output_stride + int64_t(head) * D + col) =
+              make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+          if (p.lse && col == 0) p.lse[int64_t(at.s) * p.heads + head] = n != 0.f ? (b + log2f(n)) * 0.69314718056f : -INFINITY;
+        }
+        if (tid == 0) p.counters[cta0] = 0;
+      }
+    }
+    __syncthreads();   // stats may be written again
+    left -= count;
+    at.unit += count;
+    if (at.unit == at.units && left > 0) next_head<D, FP8>(p, at);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
+}
+
+template <int D, bool FP8>
+cudaError_t launch(const AttendParams &p, int sms, cudaStream_t stream) {
+  // what a sequence can see at most, in units
+  int64_t most = int64_t(p.table_width) << p.page_shift;
+  if (p.window) most = std::min(most, int64_t(p.window) + p.sinks);
+  const int64_t units = (most + One<D, FP8>::UNIT - 1) / One<D, FP8>::UNIT * p.kv_heads * p.sequences;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(units, sms)));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = One<D, FP8>::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_attend_one<D, FP8>, p);
+}
+
+template <int D, bool FP8>
+cudaError_t allow() {
+  return cudaFuncSetAttribute(k_attend_one<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, One<D, FP8>::SMEM);
+}
+
+}  // namespace
+
+cudaError_t attend_one_setup() {
+  cudaError_t e = allow<128, false>();
+  if (e == cudaSuccess) e = allow<128, true>();
+  if (e == cudaSuccess) e = allow<64, false>();
+  if (e == cudaSuccess) e = allow<64, true>();
+  return e;
+}
+
+size_t attend_one_scratch(int sms) { return size_t(2) * sms * part_floats<128>() * sizeof(float); }
+
+cudaError_t launch_attend_one(const AttendParams &p, int sms, cudaStream_t stream) {
+  if (p.dim == 128) return p.fp8 ? launch<128, true>(p, sms, stream) : launch<128, false>(p, sms, stream);
+  return p.fp8 ? launch<64, true>(p, sms, stream) : launch<64, false>(p, sms, stream);
+}
+
+}  // namespace mhc
