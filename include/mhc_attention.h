@@ -26,8 +26,8 @@
  * Conventions: as in mhc_boundary.h (device pointers, caller-owned buffers,
  * every argument checked before the first launch, nothing aborts or traps).
  * A token's heads are contiguous; a *_stride is the distance of two tokens (or
- * of two rows of the page table) in elements.  BF16 and 8-bit rows start on
- * 16-byte boundaries.  Calls without tokens succeed and launch nothing.  What
+ * of two rows of the page table) in elements.  BF16 and 8-bit rows and
+ * the scales start on 16-byte boundaries.  Calls without tokens succeed and launch nothing.  What
  * lies in device memory is checked by the kernels: a page, slot, length or
  * start that is out of range is never followed, what it stands for is taken
  * as not there, and mhc_attention_check_errors reports it.  A handle owns

@@ -22,8 +22,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libmhc_boundary.so")
 
 SOURCES = ["api.cu", "k_stage.cu", "k_stage_tc.cu", "k_finish.cu", "k_mixes.cu", "k_moe_fold.cu", "k_owner_reduce.cu",
            "static_entry.cu", "k_small.cu", "api_sublayer.cu", "k_rowquant.cu", "k_block_matmul.cu",
-           "k_moe.cu", "api_attention.cu", "k_append_kv.cu", "k_attend.cu",
-           "k_attend_one.cu"]
+           "k_moe.cu", "api_attention.cu", "k_append_kv.cu", "k_attend_one.cu", "k_attend_many.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -2,6 +2,7 @@
 // checks, the handle's scratch, and one kernel launch for each call, each a
 // programmatic dependent one, so that a call's setup overlaps the end of the
 // kernel before it on the stream.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
@@ -113,13 +114,15 @@ mhc_status_t check_cache(mhc_attention_t *a, int pages, const void *k, int64_t k
   if (int64_t(pages) * c.page_size > INT32_MAX) return fail(msg, MHC_ERR_UNSUPPORTED, "more than 2^31 - 1 slots");
   if (!fp8 && (k_scales || v_scales)) return fail(msg, MHC_ERR_INVALID_ARG, "a BF16 cache has no scales");
   const Tensor tensors[] = {{"k_cache", k, 16, true}, {"v_cache", v, 16, true},
-                            {"k_scales", k_scales, 4, fp8}, {"v_scales", v_scales, 4, fp8}};
+                            {"k_scales", k_scales, 16, fp8}, {"v_scales", v_scales, 16, fp8}};
   mhc_status_t st = check_tensors(msg, tensors);
   if (st != MHC_OK) return st;
   const int64_t page = int64_t(c.kv_heads) * c.page_size * c.head_dim;
   const Stride strides[] = {{"k_page_stride", k_stride, page, fp8 ? 16 : 8}, {"v_page_stride", v_stride, page, fp8 ? 16 : 8}};
   return check_strides(msg, strides);
 }
+
+size_t counter_bytes(const mhc_attention_t *a) { return size_t(8) * a->sm_count * sizeof(unsigned int); }
 
 void release(mhc_attention_t *a) {
   if (a->turns) cudaFree(a->turns);
@@ -175,9 +178,11 @@ mhc_status_t mhc_attention_create(const mhc_attention_config_t *config, int devi
     if (e == cudaSuccess) e = cudaMemcpy(a->turns, turns.data(), turns.size() * sizeof(uint64_t), cudaMemcpyHostToDevice);
   }
   if (e == cudaSuccess) e = attend_one_setup();
-  if (e == cudaSuccess) e = cudaMalloc(&a->parts, attend_one_scratch(a->sm_count));
-  if (e == cudaSuccess) e = cudaMalloc(&a->counters, a->sm_count * sizeof(unsigned int));
-  if (e == cudaSuccess) e = cudaMemset(a->counters, 0, a->sm_count * sizeof(unsigned int));
+  if (e == cudaSuccess) e = attend_many_setup();
+  if (e == cudaSuccess)
+    e = cudaMalloc(&a->parts, std::max(attend_one_scratch(a->sm_count), attend_many_scratch(a->sm_count)));
+  if (e == cudaSuccess) e = cudaMalloc(&a->counters, counter_bytes(a));
+  if (e == cudaSuccess) e = cudaMemset(a->counters, 0, counter_bytes(a));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     const mhc_status_t st = e == cudaErrorMemoryAllocation ? MHC_ERR_OOM : MHC_ERR_CUDA;
@@ -315,7 +320,7 @@ mhc_status_t mhc_attention_attend(mhc_attention_t *a, const mhc_attention_attend
   p.err = a->err;
   const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
   const bool one = !g->q_starts && c.heads / c.kv_heads <= ATTEND_ONE_GROUP;
-  return launched(a, one ? launch_attend_one(p, a->sm_count, on) : launch_attend(p, on), "attend");
+  return launched(a, one ? launch_attend_one(p, a->sm_count, on) : launch_attend_many(p, a->sm_count, on), "attend");
 }
 
 mhc_status_t mhc_attention_check_errors(mhc_attention_t *a) {
@@ -325,7 +330,9 @@ mhc_status_t mhc_attention_check_errors(mhc_attention_t *a) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(&flag, a->err, sizeof flag, cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && flag) {
+    // a call that gave up leaves its counters half way
     e = cudaMemset(a->err, 0, sizeof flag);
+    if (e == cudaSuccess) e = cudaMemset(a->counters, 0, counter_bytes(a));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
   }
   if (e != cudaSuccess) return fail(a->last_error, MHC_ERR_CUDA, "check_errors: %s", cudaGetErrorString(e));

@@ -43,20 +43,28 @@ struct AttendParams {
   uint16_t *output;
   float *lse;                // may be null
   // scratch of the handle: parts of rows that several CTAs work on, and counters of
-  // the parts that are there (zero between calls), one for each CTA
+  // the parts that are there (zero between calls), eight for each CTA
   float *parts;
   unsigned int *counters;
   unsigned int *err;
+  // set by the launcher of attend_many
+  int tile_queries;          // queries of a tile
+  uint32_t all_pages;        // a bit for each page of a unit
 };
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
-cudaError_t launch_attend(const AttendParams &p, cudaStream_t stream);
 
 // One query a sequence, up to 16 heads for each kv head.
 constexpr int ATTEND_ONE_GROUP = 16;
 cudaError_t attend_one_setup();
 size_t attend_one_scratch(int sms);   // bytes of parts
 cudaError_t launch_attend_one(const AttendParams &p, int sms, cudaStream_t stream);
+
+// Any number of queries a sequence.
+cudaError_t attend_many_setup();
+size_t attend_many_scratch(int sms);
+cudaError_t attend_stall_copies(int on);   // test hook, see include/mhc_boundary_test.h
+cudaError_t launch_attend_many(const AttendParams &p, int sms, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // A sequence's positions in the cache, within what its row of the table holds.

@@ -1,0 +1,1142 @@
+// k_attend_many.cu -- attention of any number of queries a sequence over a paged
+// cache, on the tensor cores: prompts, chunks of them, a few proposed tokens, and
+// single tokens of more than 16 heads a kv head.
+//
+// A row of the products is a (query, head of the group): 128 / group queries make a
+// tile of up to 128 rows, two tiles (A and B) an item of one sequence and kv head.
+// Items read the same keys and values 128 positions at a time (a unit); what no row of
+// an item sees is not read.  The call's units form one line, sequence after sequence,
+// head after head, item after item, which is divided evenly over one CTA an SM: long
+// prompts and few rows over a long cache use every SM alike.  An item that lies in
+// several CTAs' parts goes to scratch; the CTA that comes last joins the parts in their
+// order, so that the bits do not depend on it.
+//
+// A CTA's warps:
+//  0-3, 4-7  softmax of tile A, of tile B: a thread has a row.  S = Q K^T comes from
+//            tensor memory, P = exp(S - m) goes back over it in BF16; the output stays
+//            in tensor memory for the whole item and is rescaled only when the running
+//            maximum grows by more than 2^8 (P is then at most 2^8, and the sum of P
+//            is held in FP32).  At the item's end the thread writes its row.
+//  8         copies: queries, keys and values by TMA, page by page
+//  9         the products: O_A += P_A V(j), S_A(j + 1), O_B += P_B V(j), S_B(j + 1), so that
+//            one tile's softmax runs beside the other's products
+//  10, 11    values of units that are hidden from some rows: P is zero there, but zero
+//            times an infinity is not.  Infinities and NaN in such units are set to zero
+//            before the product, and the rows that do see them are told (poison).
+//  12-15     over an 8-bit cache: keys and values to BF16 (exactly), and the task of 10
+//            and 11; the scales go to the columns of S and of P.
+#include <algorithm>
+
+#include "attention.cuh"
+#include "device_common.cuh"
+#include "sublayer_tc.cuh"
+
+namespace mhc {
+namespace {
+
+constexpr int KEYS = 128;            // positions of a unit
+constexpr int ROWS = 128;            // rows of a tile
+constexpr int INFOS = 8;             // units whose notes are kept
+constexpr int SEGMENTS = 4;          // the same of segments: queries of two are there at most, beside the one that is written out
+constexpr int READY = 4;             // units whose values may be looked through
+constexpr float GROWTH = 8.f;        // log2 of what P may reach
+
+__device__ int g_stall_copies;       // test hook: the copying warp issues no copies
+
+template <int D, bool FP8>
+struct Many {
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int SLOT = KEYS * 2 * D;             // keys or values of a unit in BF16
+  static constexpr int SLOTS = D == 128 ? (FP8 ? 3 : 5) : (FP8 ? 6 : 8);
+  static constexpr int RAW = FP8 ? KEYS * D : 0;        // the same as they are in an 8-bit cache
+  static constexpr int RAWS = FP8 ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int Q = ROWS * 2 * D;                // a tile's queries
+  static constexpr int Q_AT = 0, SLOTS_AT = 2 * Q, RAW_AT = SLOTS_AT + SLOTS * SLOT;
+  static constexpr int SCALES_AT = RAW_AT + RAWS * RAW; // [INFOS][keys, values][KEYS]
+  static constexpr int CONTROL_AT = SCALES_AT + (FP8 ? INFOS * 2 * KEYS * 4 : 0);
+  static_assert((SLOTS + RAWS) / 2 + 2 <= INFOS && SLOTS / 2 <= READY, "notes outlive their unit");
+};
+
+// Notes of a unit, which the copying warp writes for the others.
+enum : uint32_t {
+  LAST = 16,             // of a segment
+  STOP = 32              // no unit: the CTA's part is done
+};
+struct Info {
+  uint32_t flags;        // bits X: tile X has rows that see some of it, 2 + X: all rows see all of it
+  int key0, end;         // positions [key0, key0 + KEYS), those before `end` there
+  uint32_t pages;        // bit i: page i is there
+  uint32_t poison[4];    // positions whose values were set to zero in part
+};
+// Notes of a segment: units from .. to of an item's.
+struct Segment {
+  int s, h, token;       // sequence, kv head, first query's row
+  int count[2], position;
+  int from, to, units;
+  int cta0, cta1;        // CTAs that the item lies in
+};
+
+// What one item is.  Tiles: X = 0 (A), 1 (B).
+struct Item {
+  int s, h, block;       // sequence, kv head, block of queries
+  int queries, length, query0, blocks;   // the sequence's
+  int count[2];          // queries of the tiles
+  int position;          // of the first query (may be negative)
+  int sink_end, sink_units, first, end, units;   // positions [0, sink_end) and [first, end), in units
+};
+
+struct Control {
+  uint64_t full[8], empty[8], raw_full[8], raw_empty[8], info_full[INFOS], ready[READY];
+  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], drain;
+  Info info[INFOS];
+  Segment segment[SEGMENTS];
+  uint32_t tmem;
+  int abort;
+  int issued, q_issued;  // copies into the ring, of queries
+  int64_t warp_total[16];
+  Item begin;
+  int begin_unit;
+};
+
+template <int D, bool FP8>
+constexpr int smem_bytes() { return Many<D, FP8>::CONTROL_AT + int(sizeof(Control)); }
+static_assert(smem_bytes<128, false>() <= 227 * 1024 && smem_bytes<128, true>() <= 227 * 1024 &&
+              smem_bytes<64, false>() <= 227 * 1024 && smem_bytes<64, true>() <= 227 * 1024, "a CTA's shared memory");
+
+// ----------------------------------------------------------------- items
+__device__ __forceinline__ void load_sequence(const AttendParams &p, Item &it, int s, bool &bad) {
+  it.s = s;
+  it.length = sequence_length(p, s, bad);
+  it.query0 = query_start(p, s, bad);
+  const int to = query_start(p, s + 1, bad);
+  bad |= to < it.query0;
+  it.queries = max(to - it.query0, 0);
+  const int per = 2 * p.tile_queries;
+  it.blocks = (it.queries + per - 1) / per;
+}
+
+__device__ __forceinline__ void load_block(const AttendParams &p, Item &it, int block) {
+  const int per = p.tile_queries, i0 = block * 2 * per;
+  it.block = block;
+  it.count[0] = min(per, it.queries - i0);
+  it.count[1] = max(0, min(per, it.queries - i0 - per));
+  it.position = it.length - it.queries + i0;
+  const int low = p.window && it.position >= p.window ? it.position - p.window + 1 : 0;
+  it.first = low >> p.page_shift << p.page_shift;
+  it.end = max(0, it.position + it.count[0] + it.count[1]);
+  it.sink_end = min(min(p.sinks, low), it.first);
+  it.sink_units = (it.sink_end + KEYS - 1) / KEYS;
+  it.units = it.end > 0 ? it.sink_units + (it.end - it.first + KEYS - 1) / KEYS : 0;
+}
+
+// To the next item with units; false if there is none.
+__device__ __forceinline__ bool next_item(const AttendParams &p, Item &it) {
+  bool bad = false;
+  int block = it.block + 1;
+  for (;;) {
+    for (; block < it.blocks; ++block) {
+      load_block(p, it, block);
+      if (it.units > 0) return true;
+    }
+    block = 0;
+    // a sequence whose last block sees nothing has no units
+    if (it.blocks > 0 && it.length > 0 && ++it.h < p.kv_heads) continue;
+    it.h = 0;
+    if (it.s + 1 >= p.sequences) return false;
+    load_sequence(p, it, it.s + 1, bad);
+    if (it.length == 0) it.blocks = 0;
+  }
+}
+
+struct Unit {
+  int key0, end;         // positions [key0, key0 + KEYS), those before `end` there
+  bool sink;
+};
+__device__ __forceinline__ Unit unit_of(const Item &it, int j) {
+  Unit u;
+  u.sink = j < it.sink_units;
+  u.key0 = u.sink ? j * KEYS : it.first + (j - it.sink_units) * KEYS;
+  u.end = u.sink ? it.sink_end : it.end;
+  return u;
+}
+// Whether some row of tile X sees something of the unit.
+__device__ __forceinline__ bool active(const AttendParams &p, const Item &it, const Unit &u, int X) {
+  const int n = it.count[X], from = it.position + X * p.tile_queries, to = from + n - 1;
+  return n > 0 && u.key0 <= to && (!p.window || u.key0 < p.sinks || u.key0 + KEYS > from - p.window + 1);
+}
+// Whether every row of tile X sees all of it.
+__device__ __forceinline__ bool whole(const AttendParams &p, const Item &it, const Unit &u, int X) {
+  const int from = it.position + X * p.tile_queries, to = from + it.count[X] - 1;
+  return u.key0 + KEYS - 1 <= from && u.key0 + KEYS <= u.end &&
+         (!p.window || u.key0 >= to - p.window + 1 || u.key0 + KEYS <= p.sinks);
+}
+
+// A CTA's part of the line.
+struct Line {
+  int64_t begin, end, total, grid;
+};
+
+struct Ring {
+  uint32_t at = 0, phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++at == uint32_t(n)) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Goes through a part's segments: units from .. to of item `it`.
+struct Segments {
+  Item it;
+  int from, to;
+  int64_t left;
+  __device__ __forceinline__ Segments(const Control &c, const Line &line) : it(c.begin), from(c.begin_unit), left(line.end - line.begin) {
+    cut();
+  }
+  __device__ __forceinline__ void cut() { to = int(min(int64_t(it.units), from + left)); }
+  __device__ __forceinline__ void next(const AttendParams &p) {
+    left -= to - from;
+    if (left <= 0) return;
+    if (!next_item(p, it)) left = 0;
+    from = 0;
+    cut();
+  }
+};
+
+// -------------------------------------------------------------- tensor cores
+// BF16 A in tensor memory (K-major), B in shared memory with its columns
+// contiguous, FP32 accumulator.
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t *r);
+template <>
+__device__ __forceinline__ void tmem_st<16>(uint32_t at, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_st<32>(uint32_t at, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Tensor memory: S (and P over its first half) of A and B, then the outputs.
+constexpr uint32_t S_COL(int X) { return X * 128; }
+constexpr uint32_t O_COL(int X) { return 256 + X * 128; }
+
+// Instruction descriptors: S = Q K^T, both K-major; O = P V, V's columns contiguous.
+constexpr uint32_t IDESC_S = tc::idesc_bf16_f32(ROWS, KEYS);
+template <int D>
+constexpr uint32_t idesc_o() { return tc::idesc_bf16_f32(ROWS, D) | 1u << 16; }
+
+// ------------------------------------------------------------------ softmax
+// lowest n bits
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// The columns of the positions `which` of a unit whose values are not finite: bits of +infinity [0, D / 32) and -infinity [4, 4 + D / 32), NaN both.
+template <int D, bool FP8>
+__device__ __noinline__ void read_poison(const AttendParams &p, int s, int h, int key0, uint4 which,
+                                         uint32_t *bits) {
+  const uint32_t words[4] = {which.x, which.y, which.z, which.w};
+  for (int w = 0; w < 4; ++w)
+    for (uint32_t m = words[w]; m; m &= m - 1) {
+      const int key = key0 + w * 32 + __ffs(m) - 1;
+      const int page = p.page_table[s * p.table_stride + (key >> p.page_shift)];
+      const int64_t at = page * p.values.page_stride +
+                         ((int64_t(h) << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D;
+      for (int d = 0; d < D; ++d) {
+        const uint32_t v = FP8 ? static_cast<const uint8_t *>(p.values.data)[at + d] : static_cast<const uint16_t *>(p.values.data)[at + d];
+        const bool nan = FP8 ? (v & 0x7fu) == 0x7fu : (v & 0x7fffu) > 0x7f80u;
+        if (nan || (!FP8 && v == 0x7f80u)) bits[d / 32] |= 1u << d % 32;
+        if (nan || (!FP8 && v == 0xff80u)) bits[4 + d / 32] |= 1u << d % 32;
+      }
+    }
+}
+
+// 32 columns of a row's output from column c0 on.
+__device__ __forceinline__ void store32(uint16_t *out, int c0, const float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    const float *x = v + i;
+    st_vec(out + c0 + i, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                    pack_bf16x2(x[6], x[7])));
+  }
+}
+
+constexpr int part_floats(int dim) { return (dim + 2) * ROWS; }   // of one tile: [dim][row], maxima, sums
+
+template <int D, bool FP8>
+__device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned char *smem, Control &c, uint32_t tmem, int X) {
+  using F = Many<D, FP8>;
+  const int tid = threadIdx.x % 128, warp = tid / 32, lane = tid % 32;
+  volatile int *abort = &c.abort;
+  const uint32_t lanes = uint32_t(warp * 32) << 16;
+  const uint32_t s_at = tmem + S_COL(X) + lanes, o_at = tmem + O_COL(X) + lanes;
+  const int group = p.heads / p.kv_heads, query = tid / group, head = tid % group;
+  const float scale = p.scale_log2, slack = GROWTH / scale;
+  const float *scales = reinterpret_cast<const float *>(smem + F::SCALES_AT);
+  uint32_t s_phase = 0, o_phase = 0;
+  Ring info, ready, slot;   // `slot`: the next unit's keys
+  uint32_t bits[8];
+  bool poisoned = false, any = false;
+  float top = -INFINITY, sum = 0.f;
+
+  for (uint32_t segment = 0;;) {
+    const Ring my_info = info, my_ready = ready;
+    info.next(INFOS);
+    ready.next(READY);
+    slot.next(F::SLOTS);
+    const Ring my_value = slot;
+    slot.next(F::SLOTS);
+    tc::wait_or_abort_inline(&c.info_full[my_info.at], my_info.phase, abort);
+    __syncwarp();
+    const Info &u = c.info[my_info.at];
+    const uint32_t flags = u.flags;
+    if (__any_sync(0xffffffffu, *abort) || (flags & STOP)) break;
+    const Segment &seg = c.segment[segment % SEGMENTS];
+    if (flags >> X & 1) {
+      const uint32_t pages = u.pages;
+      tc::wait_or_abort_inline(&c.s_full[X], s_phase, abort);
+      s_phase ^= 1u;
+      __syncwarp();
+      tc::fence_after_sync();
+      const float *ks = scales + my_info.at * 2 * KEYS, *vs = ks + KEYS;
+      const bool whole = flags >> (2 + X) & 1, masked = !whole || pages != p.all_pages;
+      // columns 32 k .. of the unit that this row sees
+      const int position = seg.position + X * p.tile_queries + query;
+      const int upto = min(position, u.end - 1) - u.key0 + 1;
+      const int low = p.window ? position - p.window + 1 - u.key0 : 0, sinks = p.sinks - u.key0;
+      auto seen = [&](int k) {
+        uint32_t w = low_bits(upto - 32 * k) & (~low_bits(low - 32 * k) | low_bits(sinks - 32 * k));
+        for (uint32_t m = ~pages & p.all_pages; m; m &= m - 1) {
+          const int at = ((__ffs(m) - 1) << p.page_shift) - 32 * k;
+          w &= ~low_bits(at + (1 << p.page_shift)) | low_bits(at);
+        }
+        return w;
+      };
+      if (!whole) {
+        // values that were set to zero (the product needs them there as well, so that
+        // nothing is waited for that is not needed anyway)
+        if (FP8) tc::wait_or_abort_inline(&c.full[my_value.at], my_value.phase, abort);
+        else tc::wait_or_abort_inline(&c.ready[my_ready.at], my_ready.phase, abort);
+        const volatile uint32_t *q = u.poison;
+        const uint4 poison = make_uint4(q[0], q[1], q[2], q[3]);
+        if (poison.x | poison.y | poison.z | poison.w) {
+          if (!poisoned) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bits[i] = 0;
+            poisoned = true;
+          }
+          if (query < seg.count[X])
+            read_poison<D, FP8>(p, seg.s, seg.h, u.key0,
+                                make_uint4(poison.x & seen(0), poison.y & seen(1), poison.z & seen(2), poison.w & seen(3)), bits);
+        }
+        __syncwarp();
+      }
+      // Columns k .. k + 31 of this row of S, with the keys' scales and without what
+      // the row does not see.  A BF16 cache's call keeps all four in registers; with
+      // the scales beside them there is no room, so an 8-bit one reads them twice.
+      auto finish = [&](uint32_t (&r)[32], int k) {
+        float (&y)[32] = reinterpret_cast<float (&)[32]>(r);
+        if (FP8) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(ks + k * 32 + i);
+            y[i] *= f.x;
+            y[i + 1] *= f.y;
+            y[i + 2] *= f.z;
+            y[i + 3] *= f.w;
+          }
+        }
+        if (masked) {
+          const uint32_t w = seen(k);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = w >> i & 1 ? y[i] : -INFINITY;
+        }
+      };
+      constexpr int KEPT = FP8 ? 1 : 4;
+      uint32_t x[KEPT][32];
+      float now = -INFINITY;
+      if (!FP8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::tmem_ld32_async(s_at + k * 32, x[k % KEPT]);
+        tc::tmem_wait_ld();
+      }
+#pragma unroll KEPT
+      for (int k = 0; k < 4; ++k) {
+        if (FP8) {
+          tc::tmem_ld32_async(s_at + k * 32, x[0]);
+          tc::tmem_wait_ld();
+        }
+        tc::tmem_hold(x[k % KEPT]);
+        finish(x[k % KEPT], k);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) now = fmaxf(now, __uint_as_float(x[k % KEPT][i]));
+      }
+      // the reference of the exponentials follows the maximum when it has grown far
+      const bool grew = now > top + slack;
+      const bool first = !any;
+      any = true;
+      if (__any_sync(0xffffffffu, grew)) {
+        const float f = grew ? exp2_fast((top - now) * scale) : 1.f;
+        if (grew) top = now;
+        sum *= f;
+        if (!first) {
+          // the product before this one is complete: S of this unit was issued behind it
+#pragma unroll
+          for (int k = 0; k < D; k += 32) {
+            uint32_t r[32];
+            tc::tmem_ld32_async(o_at + k, r);
+            tc::tmem_wait_ld();
+            tc::tmem_hold(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+            tmem_st<32>(o_at + k, r);
+          }
+        }
+      }
+      const float base = top == -INFINITY ? 0.f : -top * scale;
+      const uint64_t scale2 = tc::pair(scale, scale), base2 = tc::pair(base, base);
+      uint64_t sums[2] = {0ull, 0ull};
+#pragma unroll KEPT
+      for (int k = 0; k < 4; ++k) {
+        uint32_t (&v)[32] = x[k % KEPT];
+        if (FP8) {
+          // P's columns go over those of S that have been read: 16 k .. 16 k + 15
+          tc::tmem_ld32_async(s_at + k * 32, v);
+          tc::tmem_wait_ld();
+          tc::tmem_hold(v);
+          finish(v, k);
+        }
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          uint64_t y = base2;
+          tc::fma_pair(y, v[2 * i], v[2 * i + 1], scale2);
+          float a = exp2_fast(tc::pair_lo(y)), b = exp2_fast(tc::pair_hi(y));
+          const uint64_t w = tc::pair(a, b);
+          asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sums[i % 2]) : "l"(w));
+          if (FP8) {
+            // a scale that is not finite must not reach weights of zero
+            const float2 f = *reinterpret_cast<const float2 *>(vs + k * 32 + 2 * i);
+            a = a != 0.f ? a * f.x : 0.f;
+            b = b != 0.f ? b * f.y : 0.f;
+          }
+          r[i] = pack_bf16x2(a, b);
+        }
+        tmem_st<16>(s_at + k * 16, r);
+      }
+      tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&c.p_ready[X]);
+      sum += (tc::pair_lo(sums[0]) + tc::pair_hi(sums[0])) + (tc::pair_lo(sums[1]) + tc::pair_hi(sums[1]));
+    }
+    if (!(flags & LAST)) continue;
+    // ---- the segment's end
+    ++segment;
+    const bool had = any, live = query < seg.count[X];
+    const float top_now = top, sum_now = sum;
+    any = false;
+    top = -INFINITY;
+    sum = 0.f;
+    if (seg.count[X] == 0) continue;
+    if (had) {
+      tc::wait_or_abort_inline(&c.o_full[X], o_phase, abort);
+      o_phase ^= 1u;
+      __syncwarp();
+      tc::fence_after_sync();
+    }
+    const bool item_whole = seg.from == 0 && seg.to == seg.units;
+    const int64_t token = seg.token + X * p.tile_queries + query;
+    uint16_t *out = p.output + token * p.output_stride + (int64_t(seg.h) * group + head) * D;
+    float *lse = p.lse ? p.lse + token * p.heads + seg.h * group + head : nullptr;
+    const float inverse = sum_now != 0.f ? 1.f / sum_now : 0.f;
+    const int cta0 = seg.cta0, cta1 = seg.cta1;
+    auto part = [&](int cta) {
+      return p.parts + (int64_t(2 * cta + (cta == cta0)) * 2 + X) * part_floats(D);
+    };
+    float *mine = part(blockIdx.x);
+#pragma unroll
+    for (int k = 0; k < D; k += 32) {
+      float v[32];
+      if (had) {
+        uint32_t (&r)[32] = reinterpret_cast<uint32_t (&)[32]>(v);
+        tc::tmem_ld32_async(o_at + k, r);
+        tc::tmem_wait_ld();
+        tc::tmem_hold(r);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      }
+      if (poisoned) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (bits[k / 32] >> i & 1) v[i] += INFINITY;
+          if (bits[4 + k / 32] >> i & 1) v[i] -= INFINITY;
+        }
+      }
+      if (!live) continue;
+      if (item_whole) {
+        if (inverse == 0.f) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= inverse;
+        }
+        store32(out, k, v);
+      } else if (had) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mine[(k + i) * ROWS + tid] = v[i];
+      }
+    }
+    poisoned = false;
+    if (item_whole) {
+      if (live && lse) *lse = sum_now != 0.f ? (top_now * scale + log2f(sum_now)) * 0.69314718056f : -INFINITY;
+      tc::fence_before_sync();
+      continue;
+    }
+    tc::fence_before_sync();
+    if (live) {
+      mine[D * ROWS + tid] = had ? top_now : -INFINITY;
+      mine[(D + 1) * ROWS + tid] = sum_now;
+    }
+    // a warp's rows are joined by the same warp of the CTA that comes last
+    __threadfence();
+    __syncwarp();
+    unsigned int *counter = p.counters + (2 * cta0 + X) * 4 + warp;
+    unsigned int before = 0;
+    if (lane == 0) before = atomicAdd(counter, 1u);
+    if (__shfl_sync(0xffffffffu, before, 0) != unsigned(cta1 - cta0)) continue;
+    __threadfence();
+    if (lane == 0) *counter = 0;
+    if (!live) continue;
+    float all = -INFINITY, total = 0.f;
+    for (int k = cta0; k <= cta1; ++k) all = fmaxf(all, __ldcg(part(k) + D * ROWS + tid));
+    const float b = all == -INFINITY ? 0.f : all;
+    for (int k = cta0; k <= cta1; ++k)
+      total += __ldcg(part(k) + (D + 1) * ROWS + tid) * exp2_fast((__ldcg(part(k) + D * ROWS + tid) - b) * scale);
+    const float f = total != 0.f ? 1.f / total : 0.f;
+#pragma unroll 1
+    for (int k = 0; k < D; k += 32) {
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      for (int q = cta0; q <= cta1; ++q) {
+        const float *from = part(q);
+        const float m = __ldcg(from + D * ROWS + tid);
+        if (m == -INFINITY) continue;   // saw nothing: it has no output
+        const float w = exp2_fast((m - b) * scale);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += __ldcg(from + (k + i) * ROWS + tid) * w;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= f;
+      store32(out, k, v);
+    }
+    if (lse) *lse = total != 0.f ? (b * scale + log2f(total)) * 0.69314718056f : -INFINITY;
+  }
+}
+
+// ------------------------------------------------------------------- copies
+template <int D, bool FP8>
+__device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *smem, Control &c, const Line &line,
+                                          const CUtensorMap *tm_q, const CUtensorMap *tm_k, const CUtensorMap *tm_v) {
+  using F = Many<D, FP8>;
+  constexpr int COLS = FP8 ? D : 64, HALVES = FP8 ? 1 : D / 64;   // a box: page rows of COLS values
+  const int lane = threadIdx.x % 32;
+  volatile int *abort = &c.abort;
+  const int unit_pages = KEYS >> p.page_shift, box = COLS * (FP8 ? 1 : 2) << p.page_shift;
+  uint64_t *full = FP8 ? c.raw_full : c.full, *empty = FP8 ? c.raw_empty : c.empty;
+  const int slots = FP8 ? F::RAWS : F::SLOTS;
+  const int slot_bytes = FP8 ? F::RAW : F::SLOT;
+  unsigned char *ring = smem + (FP8 ? F::RAW_AT : F::SLOTS_AT);
+  Ring at, info;
+  uint32_t q_phase = 1;
+  int issued = 0, q_issued = 0;
+  bool ok = !*static_cast<volatile int *>(&g_stall_copies), bad = false;
+  // a unit's page numbers, one a lane; -1: not there
+  auto look = [&](const Item &it, int j) {
+    const Unit u = unit_of(it, j);
+    const int key = u.key0 + (lane << p.page_shift);
+    if (lane >= unit_pages || key >= u.end) return -1;
+    const int page = p.page_table[it.s * p.table_stride + (key >> p.page_shift)];
+    const bool there = page >= 0 && page < p.pages;
+    bad |= !there;
+    return there ? page : -1;
+  };
+  uint32_t segment = 0;
+  for (Segments seg(c, line); seg.left > 0 && ok; seg.next(p), ++segment) {
+    const Item &it = seg.it;
+    int page = look(it, seg.from);
+    ok = tc::wait_or_abort(&c.q_empty, q_phase, abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    q_phase ^= 1u;
+    if (lane == 0) {
+      Segment &n = c.segment[segment % SEGMENTS];
+      n.s = it.s;
+      n.h = it.h;
+      n.token = it.query0 + it.block * 2 * p.tile_queries;
+      n.count[0] = it.count[0];
+      n.count[1] = it.count[1];
+      n.position = it.position;
+      n.from = seg.from;
+      n.to = seg.to;
+      n.units = it.units;
+      const int64_t at0 = line.end - seg.left - seg.from;   // the item's first unit on the line
+      n.cta0 = int(((at0 + 1) * line.grid - 1) / line.total);
+      n.cta1 = int(((at0 + it.units) * line.grid - 1) / line.total);
+    }
+    if (lane == 0) {
+      const int tiles = it.count[1] > 0 ? 2 : 1;
+      const int group = p.heads / p.kv_heads;
+      tc::mbar_arrive_expect_tx(&c.q_full, uint32_t(tiles * p.tile_queries * group * 2 * D));
+      for (int X = 0; X < tiles; ++X)
+        for (int k = 0; k < D / 64; ++k)
+          tc::tma_load_3d(smem + F::Q_AT + X * F::Q + k * ROWS * 128, tm_q, k * 64, it.h * group,
+                          it.query0 + (it.block * 2 + X) * p.tile_queries, &c.q_full);
+    }
+    ++q_issued;
+    for (int j = seg.from; j < seg.to; ++j) {
+      const int next_page = j + 1 < seg.to ? look(it, j + 1) : -1;
+      const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+      // places behind the end count as there: rows do not see them
+      const Unit u = unit_of(it, j);
+      const uint32_t inside = __ballot_sync(0xffffffffu, lane < unit_pages && u.key0 + (lane << p.page_shift) < u.end);
+      for (int kv = 0; kv < 2; ++kv) {
+        ok = tc::wait_or_abort(&empty[at.at], at.phase ^ 1u, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (kv == 0) {
+          if (lane == 0) {
+            Info &n = c.info[info.at];
+            uint32_t flags = j + 1 == seg.to ? LAST : 0u;
+            for (int X = 0; X < 2; ++X)
+              flags |= (active(p, it, u, X) ? 1u : 0u) << X | (whole(p, it, u, X) ? 4u : 0u) << X;
+            n.flags = flags;
+            n.key0 = u.key0;
+            n.end = u.end;
+            n.pages = (there | ~inside) & p.all_pages;
+            n.poison[0] = n.poison[1] = n.poison[2] = n.poison[3] = 0;
+            if (FP8) tc::mbar_arrive_expect_tx(&c.info_full[info.at], uint32_t(__popc(there) * 8 << p.page_shift));
+            else tc::mbar_arrive(&c.info_full[info.at]);
+          }
+          __syncwarp();
+          if (FP8 && page >= 0) {
+            const int64_t from = (int64_t(page) * p.kv_heads + it.h) << p.page_shift;
+            float *to = reinterpret_cast<float *>(smem + F::SCALES_AT) + info.at * 2 * KEYS + (lane << p.page_shift);
+            tc::bulk_load(to, p.keys.scales + from, 4u << p.page_shift, &c.info_full[info.at]);
+            tc::bulk_load(to + KEYS, p.values.scales + from, 4u << p.page_shift, &c.info_full[info.at]);
+          }
+        }
+        if (lane == 0) tc::mbar_arrive_expect_tx(&full[at.at], uint32_t(slot_bytes));
+        __syncwarp();
+        if (lane < unit_pages) {
+          unsigned char *to = ring + size_t(at.at) * slot_bytes + lane * box;
+          for (int k = 0; k < HALVES; ++k)   // a page that is not there: zeros
+            tc::tma_load_3d(to + k * KEYS * 128, kv ? tm_v : tm_k, k * 64, it.h << p.page_shift, page, &full[at.at]);
+        }
+        at.next(slots);
+        ++issued;
+      }
+      if (!ok) break;
+      info.next(INFOS);
+      page = next_page;
+    }
+  }
+  // the others end (after a wait that gave up they have seen that as well)
+  if (lane == 0) {
+    c.issued = issued;
+    c.q_issued = q_issued;
+    if (ok) {
+      c.info[info.at].flags = STOP;
+      tc::mbar_arrive(&c.info_full[info.at]);
+    }
+  }
+  if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
+}
+
+// ----------------------------------------------------------------- products
+template <int D, bool FP8>
+__device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32_t tmem) {
+  using F = Many<D, FP8>;
+  volatile int *abort = &c.abort;
+  const uint64_t q_desc = tc::desc_sw128(smem + F::Q_AT), k_desc = tc::desc_sw128(smem + F::SLOTS_AT);
+  // values: 64 columns of 8 positions are 1024 bytes, the next 8 positions behind them, the
+  // next 64 columns KEYS * 128 bytes on
+  const uint64_t v_desc = tc::smem_desc(tc::smem_addr(smem + F::SLOTS_AT), KEYS * 128, 1024) | uint64_t(2) << 61;
+  Ring at, info, ready, value, value_ready;   // the next unit's keys; the unit before's values
+  uint32_t q_phase = 0, p_phase[2] = {0, 0};
+  bool ok = true, pending[2] = {false, false}, any[2] = {false, false};
+  bool first = true, flush = false;           // a segment's first unit; the step behind its last one
+  while (ok) {
+    uint32_t flags = 0;
+    if (!flush) {
+      ok = tc::wait_or_abort(&c.info_full[info.at], info.phase, abort);
+      if (!ok) break;
+      flags = c.info[info.at].flags;
+      info.next(INFOS);
+      if (flags & STOP) break;
+      if (first) {
+        ok = tc::wait_or_abort(&c.q_full, q_phase, abort);
+        q_phase ^= 1u;
+      }
+      ok = ok && tc::wait_or_abort(&c.full[at.at], at.phase, abort);
+      if (!ok) break;
+    }
+    if (!first) {
+      ok = FP8 ? tc::wait_or_abort(&c.full[value.at], value.phase, abort)
+               : tc::wait_or_abort(&c.ready[value_ready.at], value_ready.phase, abort);
+      if (!ok) break;
+    }
+#pragma unroll
+    for (int X = 0; X < 2; ++X) {
+      if (pending[X]) {
+        ok = tc::wait_or_abort(&c.p_ready[X], p_phase[X], abort);
+        if (!ok) break;
+        p_phase[X] ^= 1u;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < KEYS / 16; ++k)
+          mma_tmem(tmem + O_COL(X), tmem + S_COL(X) + k * 8, v_desc + value.at * (F::SLOT >> 4) + k * 128, idesc_o<D>(),
+                   any[X] || k != 0);
+        any[X] = true;
+        pending[X] = false;
+      }
+      if (X == 1 && !first) tc::mma_commit(&c.empty[value.at]);
+      if (flush) {
+        if (any[X]) tc::mma_commit(&c.o_full[X]);
+        any[X] = false;
+      } else if (flags >> X & 1) {
+        tc::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = k / 4 * (ROWS * 128 >> 4) + k % 4 * 2;
+          tc::mma_bf16(tmem + S_COL(X), q_desc + X * (F::Q >> 4) + step, k_desc + at.at * (F::SLOT >> 4) + step, IDESC_S, k != 0);
+        }
+        tc::mma_commit(&c.s_full[X]);
+        pending[X] = true;
+      }
+    }
+    if (!ok) break;
+    if (!flush) {
+      tc::mma_commit(&c.empty[at.at]);
+      if (flags & LAST) tc::mma_commit(&c.q_empty);
+      at.next(F::SLOTS);
+      value = at;
+      at.next(F::SLOTS);
+      value_ready = ready;
+      ready.next(READY);
+    }
+    first = flush;
+    flush = !flush && (flags & LAST);
+  }
+  // no product is in flight when the tensor memory goes
+  tc::mma_commit(&c.drain);
+  tc::mbar_wait_bounded(&c.drain, 0u, tc::SUB_WAIT_LIMIT);
+}
+
+// Whether a BF16 pair holds an infinity or a NaN (in bits 15 and 31).
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// Positions of the unit with values that are not finite: those values to zero, the
+// positions to `poison`.  `row`: 16-byte pieces of a row of 64 columns, as a thread of
+// `threads` finds them.
+template <int D>
+__device__ __forceinline__ void clean_values(unsigned char *slot, uint32_t *poison, int thread, int threads) {
+  for (int i = thread; i < KEYS * (D / 8); i += threads) {
+    uint4 *at = reinterpret_cast<uint4 *>(slot) + i;
+    uint4 v = *at;
+    if ((not_finite2(v.x) | not_finite2(v.y) | not_finite2(v.z) | not_finite2(v.w)) == 0) continue;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t bad = not_finite2(w[k]);
+      if (bad & 0x8000u) w[k] &= 0xffff0000u;
+      if (bad & 0x80000000u) w[k] &= 0x0000ffffu;
+    }
+    *at = v;
+    const int row = i / 8 % KEYS;
+    atomicOr(poison + row / 32, 1u << row % 32);
+  }
+}
+
+// Whether some row of a tile that sees some of a unit does not see all of it.
+__device__ __forceinline__ bool hides(uint32_t flags) { return (flags & 3u & ~(flags >> 2)) != 0; }
+
+// Values that some row of a tile does not see (BF16 cache).
+template <int D>
+__device__ __forceinline__ void clean_role(unsigned char *smem, Control &c) {
+  using F = Many<D, false>;
+  const int thread = threadIdx.x % 64, lane = threadIdx.x % 32;
+  volatile int *abort = &c.abort;
+  Ring slot, info, ready;
+  for (;;) {
+    if (!__all_sync(0xffffffffu, tc::wait_or_abort(&c.info_full[info.at], info.phase, abort))) break;
+    const uint32_t flags = c.info[info.at].flags;
+    if (flags & STOP) break;
+    slot.next(F::SLOTS);
+    if (!__all_sync(0xffffffffu, tc::wait_or_abort(&c.full[slot.at], slot.phase, abort))) break;
+    if (hides(flags)) {
+      clean_values<D>(smem + F::SLOTS_AT + slot.at * F::SLOT, c.info[info.at].poison, thread, 64);
+      tc::fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&c.ready[ready.at]);
+    slot.next(F::SLOTS);
+    info.next(INFOS);
+    ready.next(READY);
+  }
+}
+
+// 8-bit keys and values to BF16, a row a thread; the values' NaN as clean_values.
+template <int D>
+__device__ __forceinline__ void convert_role(unsigned char *smem, Control &c) {
+  using F = Many<D, true>;
+  const int row = threadIdx.x % 128, lane = threadIdx.x % 32;
+  volatile int *abort = &c.abort;
+  Ring raw, slot, info;
+  for (bool ok = true; ok;) {
+    if (!__all_sync(0xffffffffu, tc::wait_or_abort(&c.info_full[info.at], info.phase, abort))) break;
+    const uint32_t flags = c.info[info.at].flags;
+    if (flags & STOP) break;
+    const bool hidden = hides(flags);
+    {
+      for (int kv = 0; kv < 2; ++kv) {
+        ok = __all_sync(0xffffffffu, tc::wait_or_abort(&c.raw_full[raw.at], raw.phase, abort) &&
+                                         tc::wait_or_abort(&c.empty[slot.at], slot.phase ^ 1u, abort));
+        if (!ok) break;
+        const unsigned char *from = smem + F::RAW_AT + raw.at * F::RAW + row * D;
+        unsigned char *to = smem + F::SLOTS_AT + slot.at * F::SLOT + row * 128;
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int chunk = D == 128 ? i ^ (row & 7) : i ^ (row >> 1 & 3);   // as the copies laid them
+          const uint4 v = *reinterpret_cast<const uint4 *>(from + chunk * 16);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(w[k / 2] >> k % 2 * 16)));
+            float a, b;
+            asm("{.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;}" : "=f"(a), "=f"(b) : "r"(h));
+            o[k] = pack_bf16x2(a, b);
+          }
+          if (kv && hidden) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t bad = not_finite2(o[k]);
+              if (bad & 0x8000u) o[k] &= 0xffff0000u;
+              if (bad & 0x80000000u) o[k] &= 0x0000ffffu;
+              nan |= bad != 0;
+            }
+          }
+          unsigned char *half = to + i / 4 * KEYS * 128;
+          const int c0 = i % 4 * 2;
+          *reinterpret_cast<uint4 *>(half + ((c0 ^ (row & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(half + (((c0 + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        if (nan) atomicOr(c.info[info.at].poison + row / 32, 1u << row % 32);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&c.full[slot.at]);
+          tc::mbar_arrive(&c.raw_empty[raw.at]);
+        }
+        raw.next(F::RAWS);
+        slot.next(F::SLOTS);
+      }
+      info.next(INFOS);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- kernel
+template <int D, bool FP8>
+__global__ void __launch_bounds__((Many<D, FP8>::THREADS), 1)
+k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __grid_constant__ CUtensorMap tm_v) {
+  using F = Many<D, FP8>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Control &c = *reinterpret_cast<Control *>(smem + F::CONTROL_AT);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  constexpr int T = F::THREADS;
+
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) {
+      tc::mbar_init(&c.full[i], FP8 ? 4 : 1);
+      tc::mbar_init(&c.empty[i], 1);
+      tc::mbar_init(&c.raw_full[i], 1);
+      tc::mbar_init(&c.raw_empty[i], 4);
+    }
+    for (int i = 0; i < INFOS; ++i) tc::mbar_init(&c.info_full[i], 1);
+    for (int i = 0; i < READY; ++i) tc::mbar_init(&c.ready[i], 2);
+    tc::mbar_init(&c.q_full, 1);
+    tc::mbar_init(&c.q_empty, 1);
+    for (int X = 0; X < 2; ++X) {
+      tc::mbar_init(&c.s_full[X], 1);
+      tc::mbar_init(&c.p_ready[X], 4);
+      tc::mbar_init(&c.o_full[X], 1);
+    }
+    tc::mbar_init(&c.drain, 1);
+    tc::mbar_init_fence();
+    c.abort = c.issued = c.q_issued = 0;
+  }
+  if (warp == 9) tc::tmem_alloc(&c.tmem, 512);
+  if (warp == 8 && lane == 0) {
+    tc::tma_prefetch_desc(&tm_q);
+    tc::tma_prefetch_desc(&tm_k);
+    tc::tma_prefetch_desc(&tm_v);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- this CTA's part of the line: a thread has `chunk` sequences; those of many
+  // blocks are gone through by their warp
+  const int chunk = (p.sequences + T - 1) / T;
+  bool bad = false, hidden = false;
+  int64_t mine = 0;
+  for (int i = 0; i < chunk; ++i) {
+    const int s = tid * chunk + i;
+    Item it;
+    it.blocks = it.queries = it.length = 0;
+    if (s < p.sequences) load_sequence(p, it, s, bad);
+    hidden |= it.queries > it.length;   // queries that see nothing
+    int units = 0;
+    const bool many = it.blocks > 4;
+    for (int b = 0; b < it.blocks && !many; ++b) {
+      load_block(p, it, b);
+      units += it.units;
+    }
+    for (uint32_t m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
+      const int from = __ffs(m) - 1;
+      Item other;
+      other.queries = __shfl_sync(0xffffffffu, it.queries, from);
+      other.length = __shfl_sync(0xffffffffu, it.length, from);
+      const int blocks = __shfl_sync(0xffffffffu, it.blocks, from);
+      int n = 0;
+      for (int b = lane; b < blocks; b += 32) {
+        load_block(p, other, b);
+        n += other.units;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (lane == from) units = n;
+    }
+    mine += int64_t(units) * p.kv_heads;
+  }
+  int64_t upto = mine;   // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) c.warp_total[warp] = upto;
+  tc::fence_before_sync();
+  const bool any_hidden = __syncthreads_or(hidden);
+  tc::fence_after_sync();
+  const uint32_t tmem = c.tmem;
+  Line line;
+  line.total = 0;
+  for (int w = 0; w < T / 32; ++w) {
+    if (w < warp) upto += c.warp_total[w];
+    line.total += c.warp_total[w];
+  }
+  // CTAs that work: no more than there are units, so that each of them has some
+  line.grid = max(int64_t(1), min(int64_t(gridDim.x), line.total));
+  const int64_t cta = min(int64_t(blockIdx.x), line.grid);
+  line.begin = cta * line.total / line.grid;
+  line.end = min(cta + 1, line.grid) * line.total / line.grid;
+  const bool owner = line.begin < line.end && upto - mine <= line.begin && line.begin < upto;
+  if (uint32_t m = __ballot_sync(0xffffffffu, owner)) {
+    // the owner's warp finds the unit: its sequence, head, block
+    const int from = __ffs(m) - 1;
+    int64_t rest = line.begin - (upto - mine);
+    rest = int64_t(__shfl_sync(0xffffffffu, rest, from));
+    bool seen_before = false;
+    for (int s = (warp * 32 + from) * chunk;; ++s) {
+      Item it;
+      load_sequence(p, it, s, seen_before);
+      int n = 0;
+      for (int b = lane; b < it.blocks; b += 32) {
+        load_block(p, it, b);
+        n += it.units;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (rest >= int64_t(n) * p.kv_heads) {
+        rest -= int64_t(n) * p.kv_heads;
+        continue;
+      }
+      it.h = int(rest / n);
+      int in_head = int(rest % n);
+      for (int b0 = 0;; b0 += 32) {
+        it.units = 0;
+        if (b0 + lane < it.blocks) load_block(p, it, b0 + lane);
+        int to = it.units;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int v = __shfl_up_sync(0xffffffffu, to, o);
+          if (lane >= o) to += v;
+        }
+        const uint32_t behind = __ballot_sync(0xffffffffu, to > in_head);
+        if (behind) {
+          if (lane == __ffs(behind) - 1) {
+            c.begin = it;
+            c.begin_unit = in_head - (to - it.units);
+          }
+          break;
+        }
+        in_head -= __shfl_sync(0xffffffffu, to, 31);
+      }
+      break;
+    }
+  }
+  __syncthreads();
+
+  if (line.begin < line.end) {
+    if (warp < 8) {
+      softmax_role<D, FP8>(p, smem, c, tmem, warp / 4);
+    } else if (warp < 12) {
+      if (warp == 8) {
+        load_role<D, FP8>(p, smem, c, line, &tm_q, &tm_k, &tm_v);
+      } else if (warp == 9) {
+        if (tc::elect_one()) mma_role<D, FP8>(smem, c, tmem);
+      } else if (!FP8) {
+        clean_role<D>(smem, c);
+      }
+    } else if (FP8) {
+      convert_role<D>(smem, c);
+    }
+  }
+
+  // ---- queries before their sequence's first position see nothing
+  if (any_hidden) {
+    for (int s = blockIdx.x; s < p.sequences; s += gridDim.x) {
+      Item it;
+      load_sequence(p, it, s, bad);
+      const int n = min(it.queries, it.queries - it.length);
+      const int row = p.heads * D / 8;
+      for (int i = tid; i < n * row; i += T)
+        st_vec(p.output + (it.query0 + i / row) * p.output_stride + i % row * 8, make_uint4(0, 0, 0, 0));
+      for (int i = tid; p.lse && i < n * p.heads; i += T) p.lse[int64_t(it.query0) * p.heads + i] = -INFINITY;
+    }
+  }
+  if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+  if (tid == 0 && c.abort) {
+    atomicOr(p.err, ATTN_ERR_WAIT);
+    // copies in flight land before the CTA's shared memory goes
+    uint64_t *full = FP8 ? c.raw_full : c.full;
+    const int slots = FP8 ? F::RAWS : F::SLOTS;
+    for (int i = max(0, c.issued - slots); i < c.issued; ++i)
+      tc::mbar_wait_bounded(&full[i % slots], uint32_t(i / slots & 1), tc::SUB_WAIT_LIMIT);
+    if (c.q_issued > 0) tc::mbar_wait_bounded(&c.q_full, uint32_t(c.q_issued - 1 & 1), tc::SUB_WAIT_LIMIT);
+    const int units = (c.issued + 1) / 2;
+    for (int i = max(0, units - INFOS); FP8 && i < units; ++i)
+      tc::mbar_wait_bounded(&c.info_full[i % INFOS], uint32_t(i / INFOS & 1), tc::SUB_WAIT_LIMIT);
+  }
+}
+
+// A tensor map of three dimensions (the innermost contiguous) for boxes of them.
+bool encode_3d(CUtensorMap *map, CUtensorMapDataType type, const void *base, const uint64_t (&dims)[3],
+               const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+  const auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, s[2] = {strides[0], strides[1]};
+  const cuuint32_t b[3] = {box[0], box[1], box[2]}, ones[3] = {1, 1, 1};
+  return fn(map, type, 3, const_cast<void *>(base), d, s, b, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool FP8>
+cudaError_t launch(const AttendParams &args, int sms, cudaStream_t stream) {
+  using F = Many<D, FP8>;
+  AttendParams p = args;
+  const int group = p.heads / p.kv_heads, page = 1 << p.page_shift;
+  p.tile_queries = ROWS / group;
+  p.all_pages = uint32_t((uint64_t(1) << (KEYS >> p.page_shift)) - 1);
+  const int size = FP8 ? 1 : 2;
+  CUtensorMap tm_q, tm_k, tm_v;
+  const auto type = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto swizzle = FP8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  auto cache = [&](CUtensorMap *map, const CacheParams &c) {
+    return encode_3d(map, type, c.data, {uint64_t(D), uint64_t(p.kv_heads) * page, uint64_t(p.pages)},
+                     {uint64_t(D) * size, uint64_t(c.page_stride) * size}, {FP8 ? uint32_t(D) : 64u, uint32_t(page), 1u}, swizzle);
+  };
+  if (!encode_3d(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.q, {uint64_t(D), uint64_t(p.heads), uint64_t(p.tokens)},
+                 {uint64_t(D) * 2, uint64_t(p.q_stride) * 2}, {64u, uint32_t(group), uint32_t(p.tile_queries)},
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !cache(&tm_k, p.keys) || !cache(&tm_v, p.values))
+    return cudaErrorInvalidValue;
+  // no more CTAs than there can be units
+  int64_t most = int64_t(p.table_width) << p.page_shift;
+  if (p.window) most = std::min(most, int64_t(p.window) + p.sinks + 2 * p.tile_queries + 2 * KEYS);
+  const int64_t blocks = std::min<int64_t>(p.tokens, p.tokens / (2 * p.tile_queries) + p.sequences);
+  const int64_t units = (most + KEYS - 1) / KEYS * blocks * p.kv_heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(units, sms)));
+  cfg.blockDim = dim3(F::THREADS);
+  cfg.dynamicSmemBytes = smem_bytes<D, FP8>();
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_attend_many<D, FP8>, p, tm_q, tm_k, tm_v);
+}
+
+template <int D, bool FP8>
+cudaError_t allow() {
+  return cudaFuncSetAttribute(k_attend_many<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D, FP8>());
+}
+
+}  // namespace
+
+cudaError_t attend_many_setup() {
+  cudaError_t e = allow<128, false>();
+  if (e == cudaSuccess) e = allow<128, true>();
+  if (e == cudaSuccess) e = allow<64, false>();
+  if (e == cudaSuccess) e = allow<64, true>();
+  return e;
+}
+
+cudaError_t attend_stall_copies(int on) { return cudaMemcpyToSymbol(g_stall_copies, &on, sizeof on); }
+
+size_t attend_many_scratch(int sms) { return size_t(4) * sms * part_floats(128) * sizeof(float); }
+
+cudaError_t launch_attend_many(const AttendParams &p, int sms, cudaStream_t stream) {
+  if (p.dim == 128) return p.fp8 ? launch<128, true>(p, sms, stream) : launch<128, false>(p, sms, stream);
+  return p.fp8 ? launch<64, true>(p, sms, stream) : launch<64, false>(p, sms, stream);
+}
+
+}  // namespace mhc

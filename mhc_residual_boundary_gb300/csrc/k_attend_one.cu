@@ -134,6 +134,7 @@ __device__ __forceinline__ void next_head(const AttendParams &p, Cursor &c) {
   c.h = 0;
   bool bad = false;
   do {
+    if (c.s + 1 >= p.sequences) break;   // only if lengths change under the call
     c.seen = seen_by_last(p, sequence_length(p, ++c.s, bad));
     c.units = units_of<D, FP8>(c.seen);
   } while (c.units == 0);

@@ -125,11 +125,8 @@ __device__ __forceinline__ float pair_hi(uint64_t v) { return __uint_as_float(ui
 
 }  // namespace tc
 
-// Tensor map of a row-major [rows][cols] matrix (row_bytes apart) for boxes
-// of box_rows rows x 128 bytes in the 128-byte swizzled layout; what a box
-// covers outside the matrix reads as zero.  False if the driver refuses it.
-inline bool encode_rows_sw128(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t rows,
-                              uint64_t cols, uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows) {
+// The driver's encoder of tensor maps; null if there is none.
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -140,6 +137,15 @@ inline bool encode_rows_sw128(CUtensorMap *map, CUtensorMapDataType type, const 
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
   });
+  return fn;
+}
+
+// Tensor map of a row-major [rows][cols] matrix (row_bytes apart) for boxes
+// of box_rows rows x 128 bytes in the 128-byte swizzled layout; what a box
+// covers outside the matrix reads as zero.  False if the driver refuses it.
+inline bool encode_rows_sw128(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t rows,
+                              uint64_t cols, uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows) {
+  const auto fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t dims[2] = {cols, rows}, strides[1] = {row_bytes};
   const cuuint32_t box[2] = {box_cols, box_rows}, ones[2] = {1, 1};
