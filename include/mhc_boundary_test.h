@@ -30,6 +30,10 @@ mhc_status_t mhc_test_stall_stage_copies(int32_t on);
  * (mhc_sublayer_check_errors reports). */
 mhc_status_t mhc_test_stall_sublayer_copies(int32_t on);
 
+/* The same for attend's kernel of several queries a sequence
+ * (mhc_attention_check_errors reports). */
+mhc_status_t mhc_test_stall_attention_copies(int32_t on);
+
 /* Where things lie in the shared memory of a CTA of the moe kernel, in bytes,
  * for a call of m tokens on a GPU of that many SMs.  Needs no GPU. */
 typedef struct {

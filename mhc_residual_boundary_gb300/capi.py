@@ -180,6 +180,8 @@ def lib() -> ctypes.CDLL:
         h.mhc_test_stall_stage_copies.restype = st
         h.mhc_test_stall_sublayer_copies.argtypes = [ctypes.c_int32]
         h.mhc_test_stall_sublayer_copies.restype = st
+        h.mhc_test_stall_attention_copies.argtypes = [ctypes.c_int32]
+        h.mhc_test_stall_attention_copies.restype = st
         h.mhc_test_moe_form.argtypes = [ctypes.POINTER(mhc_sublayer_config_t), ctypes.c_int32, ctypes.c_int32,
                                         ctypes.POINTER(mhc_test_moe_form_t)]
         h.mhc_test_moe_form.restype = st
@@ -282,6 +284,14 @@ def mhc_test_stall_sublayer_copies(on: bool) -> None:
     """Test hook (include/mhc_boundary_test.h): the matmul and MoE kernels
     launched from now on issue no input copies."""
     status = lib().mhc_test_stall_sublayer_copies(1 if on else 0)
+    if status != MHC_OK:
+        raise MhcError(status, "could not set the stall flag")
+
+
+def mhc_test_stall_attention_copies(on: bool) -> None:
+    """Test hook: attend's kernels of several queries launched from now on issue
+    no copies."""
+    status = lib().mhc_test_stall_attention_copies(1 if on else 0)
     if status != MHC_OK:
         raise MhcError(status, "could not set the stall flag")
 

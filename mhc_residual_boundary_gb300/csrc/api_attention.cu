@@ -13,6 +13,7 @@
 
 #include "attention.cuh"
 #include "mhc_attention.h"
+#include "mhc_boundary_test.h"
 
 using namespace mhc;
 
@@ -359,3 +360,7 @@ const char *mhc_attention_last_error(const mhc_attention_t *a) {
 }
 
 }  // extern "C"
+
+mhc_status_t mhc_test_stall_attention_copies(int32_t on) {
+  return attend_stall_copies(on ? 1 : 0) == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
+}

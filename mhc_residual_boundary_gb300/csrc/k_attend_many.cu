@@ -355,9 +355,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         }
         __syncwarp();
       }
-      // Columns k .. k + 31 of this row of S, with the keys' scales and without what
-      // the row does not see.  A BF16 cache's call keeps all four in registers; with
-      // the scales beside them there is no room, so an 8-bit one reads them twice.
+      // The row of S is read twice, 32 columns at a time, the next ones while these are
+      // worked on: for the maximum and for the exponentials (128 columns of a thread
+      // in registers leave too little for the rest).  Columns 32 k .., with the keys'
+      // scales and without what the row does not see:
       auto finish = [&](uint32_t (&r)[32], int k) {
         float (&y)[32] = reinterpret_cast<float (&)[32]>(r);
         if (FP8) {
@@ -376,24 +377,23 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
           for (int i = 0; i < 32; ++i) y[i] = w >> i & 1 ? y[i] : -INFINITY;
         }
       };
-      constexpr int KEPT = FP8 ? 1 : 4;
-      uint32_t x[KEPT][32];
+      uint32_t x[2][32];
       float now = -INFINITY;
-      if (!FP8) {
+      tc::tmem_ld32_async(s_at, x[0]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tc::tmem_ld32_async(s_at + k * 32, x[k % KEPT]);
-        tc::tmem_wait_ld();
-      }
-#pragma unroll KEPT
       for (int k = 0; k < 4; ++k) {
-        if (FP8) {
-          tc::tmem_ld32_async(s_at + k * 32, x[0]);
-          tc::tmem_wait_ld();
-        }
-        tc::tmem_hold(x[k % KEPT]);
-        finish(x[k % KEPT], k);
+        uint32_t (&v)[32] = x[k % 2];
+        tc::tmem_wait_ld();
+        tc::tmem_hold(v);
+        tc::tmem_ld32_async(s_at + (k + 1) % 4 * 32, x[(k + 1) % 2]);
+        finish(v, k);
+        float m[2] = {__uint_as_float(v[0]), __uint_as_float(v[1])};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) now = fmaxf(now, __uint_as_float(x[k % KEPT][i]));
+        for (int i = 2; i < 32; i += 2) {
+          m[0] = fmaxf(m[0], __uint_as_float(v[i]));
+          m[1] = fmaxf(m[1], __uint_as_float(v[i + 1]));
+        }
+        now = fmaxf(now, fmaxf(m[0], m[1]));
       }
       // the reference of the exponentials follows the maximum when it has grown far
       const bool grew = now > top + slack;
@@ -420,16 +420,14 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       const float base = top == -INFINITY ? 0.f : -top * scale;
       const uint64_t scale2 = tc::pair(scale, scale), base2 = tc::pair(base, base);
       uint64_t sums[2] = {0ull, 0ull};
-#pragma unroll KEPT
+#pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint32_t (&v)[32] = x[k % KEPT];
-        if (FP8) {
-          // P's columns go over those of S that have been read: 16 k .. 16 k + 15
-          tc::tmem_ld32_async(s_at + k * 32, v);
-          tc::tmem_wait_ld();
-          tc::tmem_hold(v);
-          finish(v, k);
-        }
+        uint32_t (&v)[32] = x[k % 2];
+        // P's columns go over those of S that have been read: 16 k .. 16 k + 15
+        tc::tmem_wait_ld();
+        tc::tmem_hold(v);
+        if (k < 3) tc::tmem_ld32_async(s_at + (k + 1) * 32, x[(k + 1) % 2]);
+        finish(v, k);
         uint32_t r[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {

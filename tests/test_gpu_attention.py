@@ -162,6 +162,80 @@ def test_hidden_places_hold_anything(handles, several, fp8):
     a.check_errors()
 
 
+@pytest.mark.parametrize("d,window,sinks", [(128, 0, 0), (128, 70, 2), (64, 0, 0), (64, 33, 5)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_values_that_some_rows_do_not_see(handles, fp8, d, window, sinks):
+    """Infinities and NaN among the values reach the rows that see them, in their columns, and no others: neither
+    earlier queries nor later ones that a window keeps from them, in one tile with those that do."""
+    page, lengths, queries = 16, [300, 260, 40], [300, 90, 40]
+    inputs = make_inputs(59, lengths=lengths, queries=queries, heads=8, kv=2, d=d, page=page, fp8=fp8)
+    values = inputs["v_cache"]
+    spots = [(0, 100, 3, math.inf), (0, 101, 7, math.nan), (0, 40, d - 1, -math.inf), (0, 1, 5, math.inf),
+             (0, 2, 5, -math.inf), (1, 200, 0, math.nan), (1, 259, 33, -math.inf), (2, 39, 1, math.inf)]
+    for s, position, column, value in spots:
+        at = int(inputs["pages"][s, position // page]), 1, position % page, column
+        if fp8:
+            values.view(torch.uint8)[at] = 0x7f   # NaN: E4M3 has no infinities
+        else:
+            values[at] = value
+    out, lse, mag, size = define(inputs, window=window, sinks=sinks, page=page)
+    a, got = attend(handles, inputs, page, window=window, sinks=sinks)
+    assert torch.equal(torch.isfinite(got["output"]), torch.isfinite(out))
+    assert torch.equal(torch.isnan(got["output"]), torch.isnan(out)) and torch.isnan(out).any()
+    infinite = torch.isinf(out)
+    assert torch.equal(got["output"][infinite].double(), out[infinite])
+    fine = torch.isfinite(out)
+    got["output"] = torch.where(fine, got["output"], 0.0)
+    check(got, inputs, page=page, want=(torch.where(fine, out, 0.0), lse, torch.where(fine, mag, 0.0), size))
+    a.check_errors()
+
+
+@pytest.mark.parametrize("several", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_queries_and_keys_that_are_not_finite(handles, several, fp8):
+    """A NaN among the queries, or in a key that a query sees, makes that query and head NaN and no other."""
+    inputs = make_inputs(61, lengths=[200, 150], queries=[150, 9] if several else None, heads=8, kv=2, d=128, page=32,
+                         fp8=fp8)
+    want = define(inputs, page=32)
+    inputs["q"][1, 3, 77] = math.nan
+    # the last position's key of sequence 0: seen by its last query only
+    at = int(inputs["pages"][0, 199 // 32]), 1, 199 % 32, 5
+    if fp8:
+        inputs["k_cache"].view(torch.uint8)[at] = 0x7f
+    else:
+        inputs["k_cache"][at] = math.nan
+    a, got = attend(handles, inputs, 32)
+    nan = torch.zeros(got["lse"].shape, dtype=torch.bool, device="cuda")
+    nan[1, 3] = True
+    nan[149 if several else 0, 4:] = True
+    assert torch.equal(torch.isnan(got["lse"]), nan) and torch.isnan(got["output"][nan]).all()
+    got = {"output": torch.where(nan[..., None], want[0].to(BF16), got["output"]),
+           "lse": torch.where(nan, want[1].float(), got["lse"])}
+    check(got, inputs, page=32, want=want)
+    a.check_errors()
+
+
+@pytest.mark.parametrize("d,fp8", [(128, False), (128, True), (64, False), (64, True)])
+def test_a_wait_that_gives_up(d, fp8):
+    """Without its copies the kernel gives up, check_errors says so once, and the next call is right."""
+    from mhc_residual_boundary_gb300 import Attention, capi
+    a = Attention(heads=8, kv_heads=2, head_dim=d, page_size=16, fp8=fp8)
+    inputs = make_inputs(67, lengths=[300, 5000], queries=[300, 4], heads=8, kv=2, d=d, page=16, fp8=fp8)
+    out = a.empty_outputs(304)
+    capi.mhc_test_stall_attention_copies(True)
+    try:
+        a.attend(inputs, out)
+        with pytest.raises(capi.MhcError, match="TIMEOUT"):
+            a.check_errors()
+    finally:
+        capi.mhc_test_stall_attention_copies(False)
+    a.check_errors()
+    a.attend(inputs, out)
+    a.check_errors()
+    check(out, inputs, page=16)
+    a.close()
+
+
 def test_strides(handles):
     """Queries inside a packed projection, output inside wider rows, a table of wider rows, a cache whose pages hold
     keys and values side by side."""
