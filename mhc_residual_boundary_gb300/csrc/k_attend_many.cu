@@ -22,9 +22,9 @@
 //            one tile's softmax runs beside the other's products
 //  10, 11    values of units that are hidden from some rows: P is zero there, but zero
 //            times an infinity is not.  Infinities and NaN in such units are set to zero
-//            before the product, and the rows that do see them are told (poison).
-//  12-15     over an 8-bit cache: keys and values to BF16 (exactly), and the task of 10
-//            and 11; the scales go to the columns of S and of P.
+//            before the product, and the rows that do see them are told (poison).  Over
+//            an 8-bit cache also keys and values to BF16 (exactly); the scales go to the
+//            columns of S and of P.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -40,12 +40,13 @@ constexpr int INFOS = 8;             // units whose notes are kept
 constexpr int SEGMENTS = 4;          // the same of segments: queries of two are there at most, beside the one that is written out
 constexpr int READY = 4;             // units whose values may be looked through
 constexpr float GROWTH = 8.f;        // log2 of what P may reach
+constexpr int EXTRA = 3;             // places on the line that an item takes besides its units, for its beginning and end
 
 __device__ int g_stall_copies;       // test hook: the copying warp issues no copies
 
 template <int D, bool FP8>
 struct Many {
-  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int THREADS = 384;
   static constexpr int SLOT = KEYS * 2 * D;             // keys or values of a unit in BF16
   static constexpr int SLOTS = D == 128 ? (FP8 ? 3 : 5) : (FP8 ? 6 : 8);
   static constexpr int RAW = FP8 ? KEYS * D : 0;        // the same as they are in an 8-bit cache
@@ -54,6 +55,9 @@ struct Many {
   static constexpr int Q_AT = 0, SLOTS_AT = 2 * Q, RAW_AT = SLOTS_AT + SLOTS * SLOT;
   static constexpr int SCALES_AT = RAW_AT + RAWS * RAW; // [INFOS][keys, values][KEYS]
   static constexpr int CONTROL_AT = SCALES_AT + (FP8 ? INFOS * 2 * KEYS * 4 : 0);
+  // registers a thread: at the launch, then the softmax warps', the others'
+  static constexpr int R_START = 168, R_SOFT = 208, R_REST = 88;
+  static_assert(256 * R_SOFT + 128 * R_REST <= THREADS * R_START, "registers of a CTA");
   static_assert((SLOTS + RAWS) / 2 + 2 <= INFOS && SLOTS / 2 <= READY, "notes outlive their unit");
 };
 
@@ -83,11 +87,12 @@ struct Item {
   int count[2];          // queries of the tiles
   int position;          // of the first query (may be negative)
   int sink_end, sink_units, first, end, units;   // positions [0, sink_end) and [first, end), in units
+  __device__ __forceinline__ int places() const;
 };
 
 struct Control {
   uint64_t full[8], empty[8], raw_full[8], raw_empty[8], info_full[INFOS], ready[READY];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_ready[2][2], o_full[2], drain;
   Info info[INFOS];
   Segment segment[SEGMENTS];
   uint32_t tmem;
@@ -95,7 +100,7 @@ struct Control {
   int issued, q_issued;  // copies into the ring, of queries
   int64_t warp_total[16];
   Item begin;
-  int begin_unit;
+  int begin_place;
 };
 
 template <int D, bool FP8>
@@ -148,6 +153,8 @@ __device__ __forceinline__ bool next_item(const AttendParams &p, Item &it) {
   }
 }
 
+__device__ __forceinline__ int Item::places() const { return units > 0 ? EXTRA + units : 0; }
+
 struct Unit {
   int key0, end;         // positions [key0, key0 + KEYS), those before `end` there
   bool sink;
@@ -186,22 +193,36 @@ struct Ring {
   }
 };
 
-// Goes through a part's segments: units from .. to of item `it`.
+// Goes through a part's segments: units from .. to of item `it`.  An item's places on
+// the line are EXTRA without units, then its units.
 struct Segments {
   Item it;
+  int at;                // place in the item that the part begins (or goes on) at
   int from, to;
-  int64_t left;
-  __device__ __forceinline__ Segments(const Control &c, const Line &line) : it(c.begin), from(c.begin_unit), left(line.end - line.begin) {
-    cut();
+  int64_t left;          // places of the part that are left
+  __device__ __forceinline__ Segments(const AttendParams &p, const Control &c, const Line &line)
+      : it(c.begin), at(c.begin_place), left(line.end - line.begin) {
+    cut(p);
   }
-  __device__ __forceinline__ void cut() { to = int(min(int64_t(it.units), from + left)); }
+  __device__ __forceinline__ void cut(const AttendParams &p) {
+    while (left > 0) {
+      from = max(at - EXTRA, 0);
+      to = int(min(int64_t(it.units), at - EXTRA + left));
+      if (to > from) return;
+      advance(p);
+    }
+  }
+  __device__ __forceinline__ void advance(const AttendParams &p) {
+    left -= min(left, int64_t(EXTRA + it.units - at));
+    at = 0;
+    if (left > 0 && !next_item(p, it)) left = 0;
+  }
   __device__ __forceinline__ void next(const AttendParams &p) {
-    left -= to - from;
-    if (left <= 0) return;
-    if (!next_item(p, it)) left = 0;
-    from = 0;
-    cut();
+    advance(p);
+    cut(p);
   }
+  // The place of the item's first unit on the line.
+  __device__ __forceinline__ int64_t first(const Line &line) const { return line.end - left - at + EXTRA; }
 };
 
 // -------------------------------------------------------------- tensor cores
@@ -237,6 +258,23 @@ __device__ __forceinline__ void tmem_st<32>(uint32_t at, const uint32_t *r) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// A warp's registers a thread, drawn on (or given back to) what the CTA started with.
+template <int N>
+__device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// (a, b) times a pair.
+__device__ __forceinline__ void mul_pair(uint32_t &a, uint32_t &b, uint64_t f) {
+  uint64_t v = uint64_t(b) << 32 | a;
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(f));
+  a = uint32_t(v);
+  b = uint32_t(v >> 32);
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -252,6 +290,9 @@ template <int D>
 constexpr uint32_t idesc_o() { return tc::idesc_bf16_f32(ROWS, D) | 1u << 16; }
 
 // ------------------------------------------------------------------ softmax
+// Whether some row of a tile that sees some of a unit does not see all of it.
+__device__ __forceinline__ bool hides(uint32_t flags) { return (flags & 3u & ~(flags >> 2)) != 0; }
+
 // lowest n bits
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
@@ -275,14 +316,36 @@ __device__ __noinline__ void read_poison(const AttendParams &p, int s, int h, in
     }
 }
 
-// 32 columns of a row's output from column c0 on.
-__device__ __forceinline__ void store32(uint16_t *out, int c0, const float (&v)[32]) {
+// 32 columns of this lane's row of output from column c0 on.  Four lanes exchange
+// their rows' 16-byte pieces (two rounds of a transposition), so that they write 64
+// neighbouring bytes: rows[k] is the row of lane (lane & ~3) + k, null if it has none.
+__device__ __forceinline__ void store32(uint16_t *const (&rows)[4], int c0, int lane, const float (&v)[32]) {
+  uint4 piece[4];
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    const float *x = v + i;
-    st_vec(out + c0 + i, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                    pack_bf16x2(x[6], x[7])));
+  for (int k = 0; k < 4; ++k) {
+    const float *x = v + 8 * k;
+    piece[k] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
   }
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (!(k & bit)) {
+        const bool odd = lane & bit;
+        uint4 &lo = piece[k], &hi = piece[k | bit];
+        auto swap = [&](uint32_t &x, uint32_t &y) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? x : y, bit);
+          if (odd) x = got;
+          else y = got;
+        };
+        swap(lo.x, hi.x);
+        swap(lo.y, hi.y);
+        swap(lo.z, hi.z);
+        swap(lo.w, hi.w);
+      }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (rows[k]) st_vec(rows[k] + c0 + lane % 4 * 8, piece[k]);
 }
 
 constexpr int part_floats(int dim) { return (dim + 2) * ROWS; }   // of one tile: [dim][row], maxima, sums
@@ -336,7 +399,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         }
         return w;
       };
-      if (!whole) {
+      if (hides(flags)) {
         // values that were set to zero (the product needs them there as well, so that
         // nothing is waited for that is not needed anyway)
         if (FP8) tc::wait_or_abort_inline(&c.full[my_value.at], my_value.phase, abort);
@@ -355,45 +418,40 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         }
         __syncwarp();
       }
-      // The row of S is read twice, 32 columns at a time, the next ones while these are
-      // worked on: for the maximum and for the exponentials (128 columns of a thread
-      // in registers leave too little for the rest).  Columns 32 k .., with the keys'
-      // scales and without what the row does not see:
-      auto finish = [&](uint32_t (&r)[32], int k) {
-        float (&y)[32] = reinterpret_cast<float (&)[32]>(r);
-        if (FP8) {
+      // the row of S, 64 columns on their way while the others are worked on
+      uint32_t x[4][32];
+      float now = -INFINITY;
+      tc::tmem_ld32_async(s_at, x[0]);
+      tc::tmem_ld32_async(s_at + 32, x[1]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t (&v)[32] = x[k];
+        if (k % 2 == 0) {
+          tc::tmem_wait_ld();
+          tc::tmem_hold(x[k]);
+          tc::tmem_hold(x[k + 1]);
+          if (k == 0) {
+            tc::tmem_ld32_async(s_at + 64, x[2]);
+            tc::tmem_ld32_async(s_at + 96, x[3]);
+          }
+        }
+        if (FP8) {   // the keys' scales
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(ks + k * 32 + i);
-            y[i] *= f.x;
-            y[i + 1] *= f.y;
-            y[i + 2] *= f.z;
-            y[i + 3] *= f.w;
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(ks + k * 32 + i);
+            mul_pair(v[i], v[i + 1], f.x);
+            mul_pair(v[i + 2], v[i + 3], f.y);
           }
         }
         if (masked) {
           const uint32_t w = seen(k);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = w >> i & 1 ? y[i] : -INFINITY;
+          for (int i = 0; i < 32; ++i) v[i] = w >> i & 1 ? v[i] : 0xff800000u;   // minus infinity
         }
-      };
-      uint32_t x[2][32];
-      float now = -INFINITY;
-      tc::tmem_ld32_async(s_at, x[0]);
+        float m[2] = {now, __uint_as_float(v[0])};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t (&v)[32] = x[k % 2];
-        tc::tmem_wait_ld();
-        tc::tmem_hold(v);
-        tc::tmem_ld32_async(s_at + (k + 1) % 4 * 32, x[(k + 1) % 2]);
-        finish(v, k);
-        float m[2] = {__uint_as_float(v[0]), __uint_as_float(v[1])};
-#pragma unroll
-        for (int i = 2; i < 32; i += 2) {
-          m[0] = fmaxf(m[0], __uint_as_float(v[i]));
-          m[1] = fmaxf(m[1], __uint_as_float(v[i + 1]));
-        }
-        now = fmaxf(now, fmaxf(m[0], m[1]));
+        for (int i = 1; i < 31; i += 2) m[i / 2 % 2] = max3(m[i / 2 % 2], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+        now = max3(m[0], m[1], __uint_as_float(v[31]));
       }
       // the reference of the exponentials follows the maximum when it has grown far
       const bool grew = now > top + slack;
@@ -405,7 +463,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         sum *= f;
         if (!first) {
           // the product before this one is complete: S of this unit was issued behind it
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < D; k += 32) {
             uint32_t r[32];
             tc::tmem_ld32_async(o_at + k, r);
@@ -422,34 +480,31 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       uint64_t sums[2] = {0ull, 0ull};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint32_t (&v)[32] = x[k % 2];
-        // P's columns go over those of S that have been read: 16 k .. 16 k + 15
-        tc::tmem_wait_ld();
-        tc::tmem_hold(v);
-        if (k < 3) tc::tmem_ld32_async(s_at + (k + 1) * 32, x[(k + 1) % 2]);
-        finish(v, k);
+        uint32_t (&v)[32] = x[k];
         uint32_t r[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           uint64_t y = base2;
           tc::fma_pair(y, v[2 * i], v[2 * i + 1], scale2);
-          float a = exp2_fast(tc::pair_lo(y)), b = exp2_fast(tc::pair_hi(y));
-          const uint64_t w = tc::pair(a, b);
+          uint32_t a = __float_as_uint(exp2_fast(tc::pair_lo(y))), b = __float_as_uint(exp2_fast(tc::pair_hi(y)));
+          const uint64_t w = uint64_t(b) << 32 | a;
           asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sums[i % 2]) : "l"(w));
-          if (FP8) {
-            // a scale that is not finite must not reach weights of zero
-            const float2 f = *reinterpret_cast<const float2 *>(vs + k * 32 + 2 * i);
-            a = a != 0.f ? a * f.x : 0.f;
-            b = b != 0.f ? b * f.y : 0.f;
+          if (FP8) {   // the values' scales
+            const bool none[2] = {masked && a == 0, masked && b == 0};   // what is hidden has none
+            mul_pair(a, b, *reinterpret_cast<const uint64_t *>(vs + k * 32 + 2 * i));
+            if (none[0]) a = 0;
+            if (none[1]) b = 0;
           }
-          r[i] = pack_bf16x2(a, b);
+          r[i] = pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
         }
         tmem_st<16>(s_at + k * 16, r);
+        if (k % 2) {   // half of P is there: its product can begin
+          tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&c.p_ready[X][k / 2]);
+        }
       }
-      tmem_wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&c.p_ready[X]);
       sum += (tc::pair_lo(sums[0]) + tc::pair_hi(sums[0])) + (tc::pair_lo(sums[1]) + tc::pair_hi(sums[1]));
     }
     if (!(flags & LAST)) continue;
@@ -469,7 +524,11 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     }
     const bool item_whole = seg.from == 0 && seg.to == seg.units;
     const int64_t token = seg.token + X * p.tile_queries + query;
-    uint16_t *out = p.output + token * p.output_stride + (int64_t(seg.h) * group + head) * D;
+    const uint64_t out = live ? reinterpret_cast<uint64_t>(p.output + token * p.output_stride + (int64_t(seg.h) * group + head) * D) : 0;
+    uint16_t *rows[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      rows[k] = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, out, (lane & ~3) + k));
     float *lse = p.lse ? p.lse + token * p.heads + seg.h * group + head : nullptr;
     const float inverse = sum_now != 0.f ? 1.f / sum_now : 0.f;
     const int cta0 = seg.cta0, cta1 = seg.cta1;
@@ -477,38 +536,31 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       return p.parts + (int64_t(2 * cta + (cta == cta0)) * 2 + X) * part_floats(D);
     };
     float *mine = part(blockIdx.x);
-#pragma unroll
-    for (int k = 0; k < D; k += 32) {
+    // not unrolled: code that runs once an item comes from far, line after line
+#pragma unroll 1
+    for (int k = 0; k < D / 32; ++k) {
       float v[32];
-      if (had) {
+      {
         uint32_t (&r)[32] = reinterpret_cast<uint32_t (&)[32]>(v);
-        tc::tmem_ld32_async(o_at + k, r);
+        tc::tmem_ld32_async(o_at + k * 32, r);
         tc::tmem_wait_ld();
         tc::tmem_hold(r);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.f;
       }
       if (poisoned) {
+        const uint32_t plus = bits[k], minus = bits[4 + k];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          if (bits[k / 32] >> i & 1) v[i] += INFINITY;
-          if (bits[4 + k / 32] >> i & 1) v[i] -= INFINITY;
+          if (plus >> i & 1) v[i] += INFINITY;
+          if (minus >> i & 1) v[i] -= INFINITY;
         }
       }
-      if (!live) continue;
       if (item_whole) {
-        if (inverse == 0.f) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        } else {
+        for (int i = 0; i < 32; ++i) v[i] = inverse == 0.f ? 0.f : v[i] * inverse;
+        store32(rows, k * 32, lane, v);
+      } else if (had && live) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= inverse;
-        }
-        store32(out, k, v);
-      } else if (had) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) mine[(k + i) * ROWS + tid] = v[i];
+        for (int i = 0; i < 32; ++i) mine[(k * 32 + i) * ROWS + tid] = v[i];
       }
     }
     poisoned = false;
@@ -531,11 +583,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     if (__shfl_sync(0xffffffffu, before, 0) != unsigned(cta1 - cta0)) continue;
     __threadfence();
     if (lane == 0) *counter = 0;
-    if (!live) continue;
     float all = -INFINITY, total = 0.f;
-    for (int k = cta0; k <= cta1; ++k) all = fmaxf(all, __ldcg(part(k) + D * ROWS + tid));
+    for (int k = cta0; k <= cta1 && live; ++k) all = fmaxf(all, __ldcg(part(k) + D * ROWS + tid));
     const float b = all == -INFINITY ? 0.f : all;
-    for (int k = cta0; k <= cta1; ++k)
+    for (int k = cta0; k <= cta1 && live; ++k)
       total += __ldcg(part(k) + (D + 1) * ROWS + tid) * exp2_fast((__ldcg(part(k) + D * ROWS + tid) - b) * scale);
     const float f = total != 0.f ? 1.f / total : 0.f;
 #pragma unroll 1
@@ -543,7 +594,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       float v[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0.f;
-      for (int q = cta0; q <= cta1; ++q) {
+      for (int q = cta0; q <= cta1 && live; ++q) {
         const float *from = part(q);
         const float m = __ldcg(from + D * ROWS + tid);
         if (m == -INFINITY) continue;   // saw nothing: it has no output
@@ -551,11 +602,12 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] += __ldcg(from + (k + i) * ROWS + tid) * w;
       }
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= f;
-      store32(out, k, v);
+      store32(rows, k, lane, v);
     }
-    if (lse) *lse = total != 0.f ? (b * scale + log2f(total)) * 0.69314718056f : -INFINITY;
+    if (live && lse) *lse = total != 0.f ? (b * scale + log2f(total)) * 0.69314718056f : -INFINITY;
   }
 }
 
@@ -587,7 +639,7 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
     return there ? page : -1;
   };
   uint32_t segment = 0;
-  for (Segments seg(c, line); seg.left > 0 && ok; seg.next(p), ++segment) {
+  for (Segments seg(p, c, line); seg.left > 0 && ok; seg.next(p), ++segment) {
     const Item &it = seg.it;
     int page = look(it, seg.from);
     ok = tc::wait_or_abort(&c.q_empty, q_phase, abort);
@@ -605,7 +657,7 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
       n.from = seg.from;
       n.to = seg.to;
       n.units = it.units;
-      const int64_t at0 = line.end - seg.left - seg.from;   // the item's first unit on the line
+      const int64_t at0 = seg.first(line);
       n.cta0 = int(((at0 + 1) * line.grid - 1) / line.total);
       n.cta1 = int(((at0 + it.units) * line.grid - 1) / line.total);
     }
@@ -714,14 +766,18 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
 #pragma unroll
     for (int X = 0; X < 2; ++X) {
       if (pending[X]) {
-        ok = tc::wait_or_abort(&c.p_ready[X], p_phase[X], abort);
+#pragma unroll
+        for (int half = 0; half < 2 && ok; ++half) {
+          ok = tc::wait_or_abort(&c.p_ready[X][half], p_phase[X], abort);
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int k = half * 4; k < half * 4 + 4; ++k)
+            mma_tmem(tmem + O_COL(X), tmem + S_COL(X) + k * 8, v_desc + value.at * (F::SLOT >> 4) + k * 128, idesc_o<D>(),
+                     any[X] || k != 0);
+        }
         if (!ok) break;
         p_phase[X] ^= 1u;
-        tc::fence_after_sync();
-#pragma unroll
-        for (int k = 0; k < KEYS / 16; ++k)
-          mma_tmem(tmem + O_COL(X), tmem + S_COL(X) + k * 8, v_desc + value.at * (F::SLOT >> 4) + k * 128, idesc_o<D>(),
-                   any[X] || k != 0);
         any[X] = true;
         pending[X] = false;
       }
@@ -783,9 +839,6 @@ __device__ __forceinline__ void clean_values(unsigned char *slot, uint32_t *pois
   }
 }
 
-// Whether some row of a tile that sees some of a unit does not see all of it.
-__device__ __forceinline__ bool hides(uint32_t flags) { return (flags & 3u & ~(flags >> 2)) != 0; }
-
 // Values that some row of a tile does not see (BF16 cache).
 template <int D>
 __device__ __forceinline__ void clean_role(unsigned char *smem, Control &c) {
@@ -811,11 +864,11 @@ __device__ __forceinline__ void clean_role(unsigned char *smem, Control &c) {
   }
 }
 
-// 8-bit keys and values to BF16, a row a thread; the values' NaN as clean_values.
+// 8-bit keys and values to BF16, two rows a thread; the values' NaN as clean_values.
 template <int D>
 __device__ __forceinline__ void convert_role(unsigned char *smem, Control &c) {
   using F = Many<D, true>;
-  const int row = threadIdx.x % 128, lane = threadIdx.x % 32;
+  const int thread = threadIdx.x % 64, lane = threadIdx.x % 32;
   volatile int *abort = &c.abort;
   Ring raw, slot, info;
   for (bool ok = true; ok;) {
@@ -823,11 +876,12 @@ __device__ __forceinline__ void convert_role(unsigned char *smem, Control &c) {
     const uint32_t flags = c.info[info.at].flags;
     if (flags & STOP) break;
     const bool hidden = hides(flags);
-    {
-      for (int kv = 0; kv < 2; ++kv) {
-        ok = __all_sync(0xffffffffu, tc::wait_or_abort(&c.raw_full[raw.at], raw.phase, abort) &&
-                                         tc::wait_or_abort(&c.empty[slot.at], slot.phase ^ 1u, abort));
-        if (!ok) break;
+    for (int kv = 0; kv < 2; ++kv) {
+      ok = __all_sync(0xffffffffu, tc::wait_or_abort(&c.raw_full[raw.at], raw.phase, abort) &&
+                                       tc::wait_or_abort(&c.empty[slot.at], slot.phase ^ 1u, abort));
+      if (!ok) break;
+#pragma unroll 1
+      for (int row = thread; row < KEYS; row += 64) {
         const unsigned char *from = smem + F::RAW_AT + raw.at * F::RAW + row * D;
         unsigned char *to = smem + F::SLOTS_AT + slot.at * F::SLOT + row * 128;
         bool nan = false;
@@ -860,17 +914,17 @@ __device__ __forceinline__ void convert_role(unsigned char *smem, Control &c) {
           *reinterpret_cast<uint4 *>(half + (((c0 + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
         if (nan) atomicOr(c.info[info.at].poison + row / 32, 1u << row % 32);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(&c.full[slot.at]);
-          tc::mbar_arrive(&c.raw_empty[raw.at]);
-        }
-        raw.next(F::RAWS);
-        slot.next(F::SLOTS);
       }
-      info.next(INFOS);
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&c.full[slot.at]);
+        tc::mbar_arrive(&c.raw_empty[raw.at]);
+      }
+      raw.next(F::RAWS);
+      slot.next(F::SLOTS);
     }
+    info.next(INFOS);
   }
 }
 
@@ -887,10 +941,10 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
 
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
-      tc::mbar_init(&c.full[i], FP8 ? 4 : 1);
+      tc::mbar_init(&c.full[i], FP8 ? 2 : 1);
       tc::mbar_init(&c.empty[i], 1);
       tc::mbar_init(&c.raw_full[i], 1);
-      tc::mbar_init(&c.raw_empty[i], 4);
+      tc::mbar_init(&c.raw_empty[i], 2);
     }
     for (int i = 0; i < INFOS; ++i) tc::mbar_init(&c.info_full[i], 1);
     for (int i = 0; i < READY; ++i) tc::mbar_init(&c.ready[i], 2);
@@ -898,7 +952,8 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     tc::mbar_init(&c.q_empty, 1);
     for (int X = 0; X < 2; ++X) {
       tc::mbar_init(&c.s_full[X], 1);
-      tc::mbar_init(&c.p_ready[X], 4);
+      tc::mbar_init(&c.p_ready[X][0], 4);
+      tc::mbar_init(&c.p_ready[X][1], 4);
       tc::mbar_init(&c.o_full[X], 1);
     }
     tc::mbar_init(&c.drain, 1);
@@ -929,7 +984,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     const bool many = it.blocks > 4;
     for (int b = 0; b < it.blocks && !many; ++b) {
       load_block(p, it, b);
-      units += it.units;
+      units += it.places();
     }
     for (uint32_t m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
       const int from = __ffs(m) - 1;
@@ -940,7 +995,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
       int n = 0;
       for (int b = lane; b < blocks; b += 32) {
         load_block(p, other, b);
-        n += other.units;
+        n += other.places();
       }
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -983,7 +1038,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
       int n = 0;
       for (int b = lane; b < it.blocks; b += 32) {
         load_block(p, it, b);
-        n += it.units;
+        n += it.places();
       }
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -996,7 +1051,8 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
       for (int b0 = 0;; b0 += 32) {
         it.units = 0;
         if (b0 + lane < it.blocks) load_block(p, it, b0 + lane);
-        int to = it.units;
+        const int mine_here = it.places();
+        int to = mine_here;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
           const int v = __shfl_up_sync(0xffffffffu, to, o);
@@ -1006,7 +1062,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
         if (behind) {
           if (lane == __ffs(behind) - 1) {
             c.begin = it;
-            c.begin_unit = in_head - (to - it.units);
+            c.begin_place = in_head - (to - mine_here);
           }
           break;
         }
@@ -1016,22 +1072,6 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     }
   }
   __syncthreads();
-
-  if (line.begin < line.end) {
-    if (warp < 8) {
-      softmax_role<D, FP8>(p, smem, c, tmem, warp / 4);
-    } else if (warp < 12) {
-      if (warp == 8) {
-        load_role<D, FP8>(p, smem, c, line, &tm_q, &tm_k, &tm_v);
-      } else if (warp == 9) {
-        if (tc::elect_one()) mma_role<D, FP8>(smem, c, tmem);
-      } else if (!FP8) {
-        clean_role<D>(smem, c);
-      }
-    } else if (FP8) {
-      convert_role<D>(smem, c);
-    }
-  }
 
   // ---- queries before their sequence's first position see nothing
   if (any_hidden) {
@@ -1046,10 +1086,28 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     }
   }
   if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
+
+  if (line.begin < line.end) {
+    if (warp < 8) {
+      registers_up<F::R_SOFT>();
+      softmax_role<D, FP8>(p, smem, c, tmem, warp / 4);
+    } else {
+      registers_down<F::R_REST>();
+      if (warp == 8) {
+        load_role<D, FP8>(p, smem, c, line, &tm_q, &tm_k, &tm_v);
+      } else if (warp == 9) {
+        if (tc::elect_one()) mma_role<D, FP8>(smem, c, tmem);
+      } else if (FP8) {
+        convert_role<D>(smem, c);
+      } else {
+        clean_role<D>(smem, c);
+      }
+    }
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+  if (warp == 9) tc::tmem_dealloc(c.tmem, 512);
   if (tid == 0 && c.abort) {
     atomicOr(p.err, ATTN_ERR_WAIT);
     // copies in flight land before the CTA's shared memory goes
@@ -1115,6 +1173,12 @@ cudaError_t launch(const AttendParams &args, int sms, cudaStream_t stream) {
 
 template <int D, bool FP8>
 cudaError_t allow() {
+  using F = Many<D, FP8>;
+  cudaFuncAttributes a;
+  cudaError_t e = cudaFuncGetAttributes(&a, k_attend_many<D, FP8>);
+  if (e != cudaSuccess) return e;
+  // the warps' shares are drawn on what the CTA starts with: never wait for more
+  if (a.numRegs != F::R_START) return cudaErrorInvalidKernelImage;
   return cudaFuncSetAttribute(k_attend_many<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D, FP8>());
 }
 
