@@ -268,12 +268,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-// (a, b) times a pair.
+// (a, b) times a pair; x * f + g; acc + (a, b).
 __device__ __forceinline__ void mul_pair(uint32_t &a, uint32_t &b, uint64_t f) {
-  uint64_t v = uint64_t(b) << 32 | a;
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(f));
-  a = uint32_t(v);
-  b = uint32_t(v >> 32);
+  asm("{.reg .b64 t;\n\tmov.b64 t, {%0, %1};\n\tmul.rn.f32x2 t, t, %2;\n\tmov.b64 {%0, %1}, t;}" : "+r"(a), "+r"(b) : "l"(f));
+}
+__device__ __forceinline__ void fma_pair(float &y0, float &y1, uint32_t x0, uint32_t x1, uint64_t f, uint64_t g) {
+  asm("{.reg .b64 t;\n\tmov.b64 t, {%2, %3};\n\tfma.rn.f32x2 t, t, %4, %5;\n\tmov.b64 {%0, %1}, t;}"
+      : "=f"(y0), "=f"(y1)
+      : "r"(x0), "r"(x1), "l"(f), "l"(g));
+}
+__device__ __forceinline__ void add_pair(uint64_t &acc, float a, float b) {
+  asm("{.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tadd.rn.f32x2 %0, %0, t;}" : "+l"(acc) : "f"(a), "f"(b));
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -420,7 +425,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       }
       // the row of S, 64 columns on their way while the others are worked on
       uint32_t x[4][32];
-      float now = -INFINITY;
+      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       tc::tmem_ld32_async(s_at, x[0]);
       tc::tmem_ld32_async(s_at + 32, x[1]);
 #pragma unroll
@@ -448,11 +453,14 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = w >> i & 1 ? v[i] : 0xff800000u;   // minus infinity
         }
-        float m[2] = {now, __uint_as_float(v[0])};
+        // four chains
 #pragma unroll
-        for (int i = 1; i < 31; i += 2) m[i / 2 % 2] = max3(m[i / 2 % 2], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-        now = max3(m[0], m[1], __uint_as_float(v[31]));
+        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m[e] = max3(m[e], __uint_as_float(v[i + 2 * e]), __uint_as_float(v[i + 2 * e + 1]));
       }
+      const float now = max3(m[0], m[1], fmaxf(m[2], m[3]));
       // the reference of the exponentials follows the maximum when it has grown far
       const bool grew = now > top + slack;
       const bool first = !any;
@@ -484,18 +492,19 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         uint32_t r[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          uint64_t y = base2;
-          tc::fma_pair(y, v[2 * i], v[2 * i + 1], scale2);
-          uint32_t a = __float_as_uint(exp2_fast(tc::pair_lo(y))), b = __float_as_uint(exp2_fast(tc::pair_hi(y)));
-          const uint64_t w = uint64_t(b) << 32 | a;
-          asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sums[i % 2]) : "l"(w));
+          float a, b;
+          fma_pair(a, b, v[2 * i], v[2 * i + 1], scale2, base2);
+          a = exp2_fast(a);
+          b = exp2_fast(b);
+          add_pair(sums[i % 2], a, b);
           if (FP8) {   // the values' scales
-            const bool none[2] = {masked && a == 0, masked && b == 0};   // what is hidden has none
-            mul_pair(a, b, *reinterpret_cast<const uint64_t *>(vs + k * 32 + 2 * i));
-            if (none[0]) a = 0;
-            if (none[1]) b = 0;
+            uint32_t wa = __float_as_uint(a), wb = __float_as_uint(b);
+            mul_pair(wa, wb, *reinterpret_cast<const uint64_t *>(vs + k * 32 + 2 * i));
+            // what is hidden has none
+            a = masked && a == 0.f ? 0.f : __uint_as_float(wa);
+            b = masked && b == 0.f ? 0.f : __uint_as_float(wb);
           }
-          r[i] = pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
+          r[i] = pack_bf16x2(a, b);
         }
         tmem_st<16>(s_at + k * 16, r);
         if (k % 2) {   // half of P is there: its product can begin
@@ -818,24 +827,29 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
 // Positions of the unit with values that are not finite: those values to zero, the
-// positions to `poison`.  `row`: 16-byte pieces of a row of 64 columns, as a thread of
-// `threads` finds them.
+// positions to `poison`.
 template <int D>
 __device__ __forceinline__ void clean_values(unsigned char *slot, uint32_t *poison, int thread, int threads) {
-  for (int i = thread; i < KEYS * (D / 8); i += threads) {
-    uint4 *at = reinterpret_cast<uint4 *>(slot) + i;
-    uint4 v = *at;
-    if ((not_finite2(v.x) | not_finite2(v.y) | not_finite2(v.z) | not_finite2(v.w)) == 0) continue;
-    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll 1
+  for (int i0 = thread; i0 < KEYS * (D / 8); i0 += 8 * threads) {
+    uint32_t any = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t bad = not_finite2(w[k]);
-      if (bad & 0x8000u) w[k] &= 0xffff0000u;
-      if (bad & 0x80000000u) w[k] &= 0x0000ffffu;
+    for (int i = 0; i < 8; ++i) {
+      const uint4 v = reinterpret_cast<const uint4 *>(slot)[i0 + i * threads];
+      any |= not_finite2(v.x) | not_finite2(v.y) | not_finite2(v.z) | not_finite2(v.w);
     }
-    *at = v;
-    const int row = i / 8 % KEYS;
-    atomicOr(poison + row / 32, 1u << row % 32);
+    if (any == 0) continue;
+#pragma unroll 1
+    for (int i = i0; i < i0 + 8 * threads; i += threads) {
+      uint32_t *w = reinterpret_cast<uint32_t *>(slot) + i * 4;
+      const int row = i / 8 % KEYS;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t bad = not_finite2(w[k]);
+        if (bad & 0x8000u) w[k] &= 0xffff0000u;
+        if (bad & 0x80000000u) w[k] &= 0x0000ffffu;
+        if (bad) atomicOr(poison + row / 32, 1u << row % 32);
+      }
+    }
   }
 }
 
