@@ -12,18 +12,19 @@
 //    line, which is divided evenly over one CTA an SM, whatever the lengths are; a
 //    CTA's part of a (sequence, head) is a segment.  Copies run on across the
 //    segments' ends.
-//  * Warps work alone, each on its own tiles with its own running maximum, sum and
-//    output (16 rows x head_dim in registers), and meet at a segment's end.
+//  * Warps work alone, each on its own tiles with its own running maxima, sums and
+//    outputs (heads x head_dim in registers), and meet at a segment's end.
 //  * A segment that is not a whole (sequence, head) goes to scratch; the CTA that
 //    comes last joins the parts, in their order, so that the bits do not depend on it.
 //
-// Products are m16n8k16 with the 16 rows the group's heads: S = Q K^T and O = P V.
-// The order of the products' inner indexes is free as long as both factors use the
-// same: lanes take their B fragments as whole 16-byte pieces of K's and V's rows, and
-// the fragments of Q and the columns of O follow.  Over a BF16 cache P goes in as two
-// BF16 pieces (16 bits of it), over an 8-bit one everything is FP16: E4M3 fits it,
-// Q is taken with a power of two off each row, and P carries the value's scale,
-// 2^(x + log2 scale - its own running maximum), so that it uses FP16's upper range.
+// Products are m16n8k16, turned so that the positions are the 16 rows and the heads
+// the 8 columns (one or two groups of them): S^T = K Q^T and O^T = V^T P^T.  The order of
+// the products' inner indexes is free as long as both factors use the same, and so is
+// that of O's rows: lanes take their fragments as whole 16-byte pieces of K's and V's
+// rows, and the fragments of Q and the rows of O^T follow.  Over a BF16 cache P goes in
+// as two BF16 pieces (16 bits of it), over an 8-bit one everything is FP16: E4M3 fits
+// it, Q is taken with a power of two off each head's row, and P carries the value's
+// scale, 2^(x + log2 scale - its own running maximum), so that it uses FP16's upper range.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -73,6 +74,11 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
   return v;
 }
+__device__ __forceinline__ float lds4(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
 __device__ __forceinline__ uint2 lds8(uint32_t at) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
@@ -88,6 +94,12 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// A transposed 8 x 8 matrix of 16-bit values, a row's pair a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 // Two E4M3 values (the lower or upper half of w) as an FP16 pair.
 __device__ __forceinline__ uint32_t f16_lower(uint32_t w) {
@@ -145,10 +157,10 @@ __device__ __forceinline__ void next_head(const AttendParams &p, Cursor &c) {
 template <int D>
 constexpr int part_floats() { return 16 * (D + 4); }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p) {
   using F = One<D, FP8>;
-  constexpr int N_TILES = D / 8;       // of 8 output columns
+  constexpr int M_TILES = D / 16;      // of 16 elements of a row of output
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int64_t warp_total[WARPS];
   __shared__ Cursor begin_shared;
@@ -281,51 +293,63 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
     // ---- a segment: units at.unit .. of (at.s, at.h), as far as this CTA's part goes
     const int unit0 = at.unit, count = int(left < at.units - at.unit ? left : int64_t(at.units - at.unit));
     const uint16_t *q = p.q + at.s * p.q_stride + int64_t(at.h) * group * D;
-    uint32_t qa[D / 16][4];
-    float row_scale[2] = {p.scale_log2, p.scale_log2};
-    if (!FP8) {
+    uint32_t qb[NT][D / 16][2];          // of head 8 n + g
+    float head_scale[NT][2];             // of heads 8 n + 2 t, + 1
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        const uint4 lo = g < group ? ld_vec(q + g * D + (4 * i + t) * 8) : zero;
-        const uint4 hi = g + 8 < group ? ld_vec(q + (g + 8) * D + (4 * i + t) * 8) : zero;
-        qa[2 * i][0] = lo.x; qa[2 * i][1] = hi.x; qa[2 * i][2] = lo.y; qa[2 * i][3] = hi.y;
-        qa[2 * i + 1][0] = lo.z; qa[2 * i + 1][1] = hi.z; qa[2 * i + 1][2] = lo.w; qa[2 * i + 1][3] = hi.w;
-      }
-    } else {
+    for (int n = 0; n < NT; ++n) {
+      const int head = 8 * n + g;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      if (!FP8) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 v = head < group ? ld_vec(q + head * D + (4 * i + t) * 8) : zero;
+          qb[n][2 * i][0] = v.x;
+          qb[n][2 * i][1] = v.y;
+          qb[n][2 * i + 1][0] = v.z;
+          qb[n][2 * i + 1][1] = v.w;
+        }
+        head_scale[n][0] = head_scale[n][1] = p.scale_log2;
+      } else {
         float x[D / 64][2][8];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int row = g + 8 * r;
-            unpack8(row < group ? ld_vec(q + row * D + (4 * i + t) * 16 + e * 8) : make_uint4(0, 0, 0, 0), x[i][e]);
+            unpack8(head < group ? ld_vec(q + head * D + (4 * i + t) * 16 + e * 8) : zero, x[i][e]);
 #pragma unroll
             for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[i][e][k]) & 0x7fffffffu);
           }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the row's largest magnitude to [1, 2)
+        // the head's largest magnitude to [1, 2)
         const int e2 = min(max(int(top >> 23) - 127, -126), 126);
         const float down = __uint_as_float(uint32_t(127 - e2) << 23);
-        row_scale[r] = p.scale_log2 * __uint_as_float(uint32_t(127 + e2) << 23);
+        const float up = p.scale_log2 * __uint_as_float(uint32_t(127 + e2) << 23);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) head_scale[n][e] = __shfl_sync(0xffffffffu, up, (2 * t + e) * 4);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float *y = x[i][k / 2] + k % 2 * 4;
-            qa[4 * i + k][r] = pack_f16x2(y[0] * down, y[1] * down);
-            qa[4 * i + k][2 + r] = pack_f16x2(y[2] * down, y[3] * down);
+            qb[n][4 * i + k][0] = pack_f16x2(y[0] * down, y[1] * down);
+            qb[n][4 * i + k][1] = pack_f16x2(y[2] * down, y[3] * down);
           }
       }
     }
-    float acc[N_TILES][4];
+    float acc[NT][M_TILES][4];
+    float top[NT][2], top_out[NT][2], sum[NT][2];
 #pragma unroll
-    for (int i = 0; i < N_TILES; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    float top[2] = {-INFINITY, -INFINITY}, top_out[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < M_TILES; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top[n][e] = top_out[n][e] = -INFINITY;
+        sum[n][e] = 0.f;
+      }
+    }
 
     for (int u = 0; u < count; ++u) {
       asm volatile("cp.async.wait_group %0;" ::"n"(F::STAGES - 1) : "memory");
@@ -333,100 +357,122 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
       const uint32_t from = ring_at + stage * F::STAGE;
       const uint32_t there = masks[stage];
       if (there) {
+        constexpr int BLOCKS = F::KEYS / 16;   // of 16 positions: rows g and g + 8 are this lane's
         // ---- x = scale (q k) log2(e)
-        float x[F::KEYS / 8][4];
+        float x[NT][BLOCKS][4];
 #pragma unroll
-        for (int n = 0; n < F::KEYS / 8; ++n) {
-          x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
-          const int row = n * 8 + g;
+        for (int j = 0; j < BLOCKS; ++j) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) x[n][j][0] = x[n][j][1] = x[n][j][2] = x[n][j][3] = 0.f;
+          const int row = j * 16 + g;
 #pragma unroll
           for (int i = 0; i < F::CHUNKS / 4; ++i) {
             const int c = 4 * i + t, ck = F::CHUNKS >= 8 ? c ^ ((row & 1) << 2) : c;
-            const uint4 w = lds16(from + row * F::ROW + ck * 16);
+            const uint4 v = lds16(from + row * F::ROW + ck * 16), w = lds16(from + (row + 8) * F::ROW + ck * 16);
+            const uint32_t a[4] = {v.x, v.y, v.z, v.w}, b[4] = {w.x, w.y, w.z, w.w};
             if (FP8) {
-              mma<FP8>(x[n], qa[4 * i], f16_lower(w.x), f16_upper(w.x));
-              mma<FP8>(x[n], qa[4 * i + 1], f16_lower(w.y), f16_upper(w.y));
-              mma<FP8>(x[n], qa[4 * i + 2], f16_lower(w.z), f16_upper(w.z));
-              mma<FP8>(x[n], qa[4 * i + 3], f16_lower(w.w), f16_upper(w.w));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t ka[4] = {f16_lower(a[k]), f16_lower(b[k]), f16_upper(a[k]), f16_upper(b[k])};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma<FP8>(x[n][j], ka, qb[n][4 * i + k][0], qb[n][4 * i + k][1]);
+              }
             } else {
-              mma<FP8>(x[n], qa[2 * i], w.x, w.y);
-              mma<FP8>(x[n], qa[2 * i + 1], w.z, w.w);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t ka[4] = {a[2 * k], b[2 * k], a[2 * k + 1], b[2 * k + 1]};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma<FP8>(x[n][j], ka, qb[n][2 * i + k][0], qb[n][2 * i + k][1]);
+              }
             }
           }
         }
-        float y[FP8 ? F::KEYS / 8 : 1][4];   // x + log2 of the value's scale
-        float now[2] = {-INFINITY, -INFINITY}, now_out[2] = {-INFINITY, -INFINITY};
+        float y[FP8 ? NT : 1][FP8 ? BLOCKS : 1][4];   // x + log2 of the value's scale
+        float now[NT][2], now_out[NT][2];
 #pragma unroll
-        for (int n = 0; n < F::KEYS / 8; ++n) {
-          float2 ks, vs;
-          if (FP8) {
-            const uint2 a = lds8(from + 2 * F::TILE + (n * 8 + 2 * t) * 4), b = lds8(from + 2 * F::TILE + (F::KEYS + n * 8 + 2 * t) * 4);
-            ks = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
-            vs = make_float2(log2_fast(__uint_as_float(b.x)), log2_fast(__uint_as_float(b.y)));
-          }
+        for (int n = 0; n < NT; ++n) now[n][0] = now[n][1] = now_out[n][0] = now_out[n][1] = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool ok = there >> (n * 8 + 2 * t + (e & 1)) & 1;
-            float v = x[n][e] * row_scale[e / 2];
-            if (FP8) v *= e & 1 ? ks.y : ks.x;
-            x[n][e] = ok ? v : -INFINITY;
-            now[e / 2] = fmaxf(now[e / 2], x[n][e]);
-            if (FP8) {
-              y[n][e] = ok ? v + (e & 1 ? vs.y : vs.x) : -INFINITY;
-              now_out[e / 2] = fmaxf(now_out[e / 2], y[n][e]);
-            }
-          }
-        }
-        // ---- the running maxima, over the four lanes of a row
-        float base[2], base_out[2];
-        bool grew = false;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          now[r] = fmaxf(now[r], __shfl_xor_sync(0xffffffffu, now[r], 1));
-          now[r] = fmaxf(now[r], __shfl_xor_sync(0xffffffffu, now[r], 2));
-          now[r] = fmaxf(now[r], top[r]);
-          grew |= now[r] != top[r];
-          base[r] = now[r] == -INFINITY ? 0.f : now[r];
-          base_out[r] = base[r];
-          if (FP8) {
-            now_out[r] = fmaxf(now_out[r], __shfl_xor_sync(0xffffffffu, now_out[r], 1));
-            now_out[r] = fmaxf(now_out[r], __shfl_xor_sync(0xffffffffu, now_out[r], 2));
-            now_out[r] = fmaxf(now_out[r], top_out[r]);
-            grew |= now_out[r] != top_out[r];
-            base_out[r] = now_out[r] == -INFINITY ? 0.f : now_out[r];
-          }
-        }
-        if (__any_sync(0xffffffffu, grew)) {
+        for (int j = 0; j < BLOCKS; ++j)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float f = exp2_fast(top[r] - base[r]);
-            const float fo = FP8 ? exp2_fast(top_out[r] - base_out[r]) : f;
-            sum[r] *= f;
-            top[r] = now[r];
-            if (FP8) top_out[r] = now_out[r];
-#pragma unroll
-            for (int i = 0; i < N_TILES; ++i) {
-              acc[i][2 * r] *= fo;
-              acc[i][2 * r + 1] *= fo;
-            }
-          }
-        }
-        // ---- weights and their sum, weights times values, 16 positions at a time
-#pragma unroll
-        for (int j = 0; j < F::KEYS / 16; ++j) {
-          uint32_t pa[4], pb[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int n = 2 * j + k / 2, r = k % 2;
-            const float w0 = exp2_fast(x[n][2 * r] - base[r]), w1 = exp2_fast(x[n][2 * r + 1] - base[r]);
-            sum[r] += w0 + w1;
+            const int row = j * 16 + 8 * r + g;
+            const bool ok = there >> row & 1;
+            float ks = 1.f, vs = 0.f;
             if (FP8) {
-              pa[k] = pack_f16x2(exp2_fast(y[n][2 * r] - base_out[r]), exp2_fast(y[n][2 * r + 1] - base_out[r]));
-            } else {
-              pa[k] = pack_bf16x2(w0, w1);
-              pb[k] = pack_bf16x2(w0 - bf16_lo(pa[k]), w1 - bf16_hi(pa[k]));
+              ks = lds4(from + 2 * F::TILE + row * 4);
+              vs = log2_fast(lds4(from + 2 * F::TILE + (F::KEYS + row) * 4));
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float v = x[n][j][2 * r + e] * head_scale[n][e];
+                if (FP8) v *= ks;
+                x[n][j][2 * r + e] = ok ? v : -INFINITY;
+                now[n][e] = fmaxf(now[n][e], x[n][j][2 * r + e]);
+                if (FP8) {
+                  y[n][j][2 * r + e] = ok ? v + vs : -INFINITY;
+                  now_out[n][e] = fmaxf(now_out[n][e], y[n][j][2 * r + e]);
+                }
+              }
+          }
+        // ---- the running maxima, over the eight lanes of a head
+        float base[NT][2], base_out[NT][2];
+        bool grew = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) {
+              now[n][e] = fmaxf(now[n][e], __shfl_xor_sync(0xffffffffu, now[n][e], o));
+              if (FP8) now_out[n][e] = fmaxf(now_out[n][e], __shfl_xor_sync(0xffffffffu, now_out[n][e], o));
+            }
+            now[n][e] = fmaxf(now[n][e], top[n][e]);
+            grew |= now[n][e] != top[n][e];
+            base_out[n][e] = base[n][e] = now[n][e] == -INFINITY ? 0.f : now[n][e];
+            if (FP8) {
+              now_out[n][e] = fmaxf(now_out[n][e], top_out[n][e]);
+              grew |= now_out[n][e] != top_out[n][e];
+              base_out[n][e] = now_out[n][e] == -INFINITY ? 0.f : now_out[n][e];
             }
           }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float f = exp2_fast(top[n][e] - base[n][e]);
+              const float fo = FP8 ? exp2_fast(top_out[n][e] - base_out[n][e]) : f;
+              sum[n][e] *= f;
+              top[n][e] = now[n][e];
+              if (FP8) top_out[n][e] = now_out[n][e];
+#pragma unroll
+              for (int i = 0; i < M_TILES; ++i) {
+                acc[n][i][e] *= fo;
+                acc[n][i][2 + e] *= fo;
+              }
+            }
+        }
+        // ---- weights and their sum, values times weights, 16 positions at a time
+#pragma unroll
+        for (int j = 0; j < BLOCKS; ++j) {
+          uint32_t pa[NT][2], pb[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float w0 = exp2_fast(x[n][j][2 * r] - base[n][0]), w1 = exp2_fast(x[n][j][2 * r + 1] - base[n][1]);
+              sum[n][0] += w0;
+              sum[n][1] += w1;
+              if (FP8) {
+                pa[n][r] = transpose8(pack_f16x2(exp2_fast(y[n][j][2 * r] - base_out[n][0]), exp2_fast(y[n][j][2 * r + 1] - base_out[n][1])));
+              } else {
+                const uint32_t w = pack_bf16x2(w0, w1);
+                pa[n][r] = transpose8(w);
+                pb[n][r] = transpose8(pack_bf16x2(w0 - bf16_lo(w), w1 - bf16_hi(w)));
+              }
+            }
           const int row = j * 16 + 2 * t;   // this lane's positions: row, row + 1, row + 8, row + 9
           if (!FP8) {
 #pragma unroll
@@ -440,12 +486,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
               }
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
-                const uint32_t e0 = __byte_perm(v[0][w], v[1][w], 0x5410), e1 = __byte_perm(v[2][w], v[3][w], 0x5410);
-                const uint32_t o0 = __byte_perm(v[0][w], v[1][w], 0x7632), o1 = __byte_perm(v[2][w], v[3][w], 0x7632);
-                mma<FP8>(acc[hh * 8 + 2 * w], pa, e0, e1);
-                mma<FP8>(acc[hh * 8 + 2 * w + 1], pa, o0, o1);
-                mma<FP8>(acc[hh * 8 + 2 * w], pb, e0, e1);
-                mma<FP8>(acc[hh * 8 + 2 * w + 1], pb, o0, o1);
+                const uint32_t va[4] = {__byte_perm(v[0][w], v[1][w], 0x5410), __byte_perm(v[0][w], v[1][w], 0x7632),
+                                        __byte_perm(v[2][w], v[3][w], 0x5410), __byte_perm(v[2][w], v[3][w], 0x7632)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  mma<FP8>(acc[n][hh * 4 + w], va, pa[n][0], pa[n][1]);
+                  mma<FP8>(acc[n][hh * 4 + w], va, pb[n][0], pb[n][1]);
+                }
               }
             }
           } else {
@@ -465,10 +512,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
             for (int w = 0; w < D / 32; ++w) {
               const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[2][w], v[3][w], 0x5140);
               const uint32_t b0 = __byte_perm(v[0][w], v[1][w], 0x7362), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-              mma<FP8>(acc[4 * w], pa, f16_lower(a0), f16_lower(a1));
-              mma<FP8>(acc[4 * w + 1], pa, f16_upper(a0), f16_upper(a1));
-              mma<FP8>(acc[4 * w + 2], pa, f16_lower(b0), f16_lower(b1));
-              mma<FP8>(acc[4 * w + 3], pa, f16_upper(b0), f16_upper(b1));
+              const uint32_t va[4] = {f16_lower(a0), f16_upper(a0), f16_lower(a1), f16_upper(a1)};
+              const uint32_t vb[4] = {f16_lower(b0), f16_upper(b0), f16_lower(b1), f16_upper(b1)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma<FP8>(acc[n][2 * w], va, pa[n][0], pa[n][1]);
+                mma<FP8>(acc[n][2 * w + 1], vb, pa[n][0], pa[n][1]);
+              }
             }
           }
         }
@@ -486,29 +536,30 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
     float *parts = p.parts;
     const int slot = 2 * blockIdx.x + (int(blockIdx.x) == cta0);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-      if (t == 0) stats[warp * 16 + 8 * r + g] = make_float4(top[r], sum[r], FP8 ? top_out[r] : top[r], 0.f);
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) sum[n][e] += __shfl_xor_sync(0xffffffffu, sum[n][e], o);
+        if (g == 0) stats[warp * 16 + 8 * n + 2 * t + e] = make_float4(top[n][e], sum[n][e], FP8 ? top_out[n][e] : top[n][e], 0.f);
+      }
     for (int r0 = 0; r0 < group; r0 += F::PASS) {
       __syncthreads();   // stats are there; the buffer's last readers are done
-      if (g + (r0 & 8) >= r0 && g + (r0 & 8) < r0 + F::PASS) {
-        float *m = meet + (warp * F::PASS + g + (r0 & 8) - r0) * F::MEET_ROW;
-        const int r = r0 >> 3;
 #pragma unroll
-        for (int i = 0; i < N_TILES; i += 4) {
-          // columns of tile i: 2 t and 2 t + 1 stand for whole pieces of a row
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * n + 2 * t + e - r0;
+          if (row < 0 || row >= F::PASS) continue;
+          // a lane's elements: whole pieces of PIECE, the rows of its tiles in pairs
           constexpr int PIECE = FP8 && D == 128 ? 16 : 8;
-          const int d = !FP8 && D == 128 ? i / 8 * 64 + i % 8 : i;
-          const float4 a = r ? make_float4(acc[i][2], acc[i + 1][2], acc[i + 2][2], acc[i + 3][2])
-                             : make_float4(acc[i][0], acc[i + 1][0], acc[i + 2][0], acc[i + 3][0]);
-          const float4 b = r ? make_float4(acc[i][3], acc[i + 1][3], acc[i + 2][3], acc[i + 3][3])
-                             : make_float4(acc[i][1], acc[i + 1][1], acc[i + 2][1], acc[i + 3][1]);
-          *reinterpret_cast<float4 *>(m + d + 2 * t * PIECE) = a;
-          *reinterpret_cast<float4 *>(m + d + (2 * t + 1) * PIECE) = b;
+          float *m = meet + (warp * F::PASS + row) * F::MEET_ROW + g * PIECE;
+#pragma unroll
+          for (int i = 0; i < M_TILES; i += 2) {
+            const int d = i * 2 / PIECE * 64 + i * 2 % PIECE;
+            *reinterpret_cast<float4 *>(m + d) = make_float4(acc[n][i][e], acc[n][i][2 + e], acc[n][i + 1][e], acc[n][i + 1][2 + e]);
+          }
         }
-      }
       __syncthreads();
       const int row = r0 + tid / (D / 4), col = tid % (D / 4) * 4;
       if (row < r0 + F::PASS && row < group) {
@@ -593,7 +644,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
   if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NT>
 cudaError_t launch(const AttendParams &p, int sms, cudaStream_t stream) {
   // what a sequence can see at most, in units
   int64_t most = int64_t(p.table_width) << p.page_shift;
@@ -609,12 +660,20 @@ cudaError_t launch(const AttendParams &p, int sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attend_one<D, FP8>, p);
+  return cudaLaunchKernelEx(&cfg, k_attend_one<D, FP8, NT>, p);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_groups(const AttendParams &p, int sms, cudaStream_t stream) {
+  return p.heads / p.kv_heads <= 8 ? launch<D, FP8, 1>(p, sms, stream) : launch<D, FP8, 2>(p, sms, stream);
 }
 
 template <int D, bool FP8>
 cudaError_t allow() {
-  return cudaFuncSetAttribute(k_attend_one<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, One<D, FP8>::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(k_attend_one<D, FP8, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, One<D, FP8>::SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_attend_one<D, FP8, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, One<D, FP8>::SMEM);
+  return e;
 }
 
 }  // namespace
@@ -630,8 +689,8 @@ cudaError_t attend_one_setup() {
 size_t attend_one_scratch(int sms) { return size_t(2) * sms * part_floats<128>() * sizeof(float); }
 
 cudaError_t launch_attend_one(const AttendParams &p, int sms, cudaStream_t stream) {
-  if (p.dim == 128) return p.fp8 ? launch<128, true>(p, sms, stream) : launch<128, false>(p, sms, stream);
-  return p.fp8 ? launch<64, true>(p, sms, stream) : launch<64, false>(p, sms, stream);
+  if (p.dim == 128) return p.fp8 ? launch_groups<128, true>(p, sms, stream) : launch_groups<128, false>(p, sms, stream);
+  return p.fp8 ? launch_groups<64, true>(p, sms, stream) : launch_groups<64, false>(p, sms, stream);
 }
 
 }  // namespace mhc
