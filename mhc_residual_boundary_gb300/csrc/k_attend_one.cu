@@ -8,8 +8,8 @@
 //    16 KB) on their way while it works on one.  Copies of places that are not there
 //    (behind the end, a page out of range) read nothing and leave zeros.
 //  * A sequence and kv head's visible positions (the first ones and the window, one
-//    behind the other) are cut into units of 8 warps' tiles.  The call's units form one
-//    line, which is divided evenly over one CTA an SM, whatever the lengths are; a
+//    behind the other) are cut into units of the warps' tiles.  The call's units form one
+//    line, which is divided evenly over the CTAs, whatever the lengths are; a
 //    CTA's part of a (sequence, head) is a segment.  Copies run on across the
 //    segments' ends.
 //  * Warps work alone, each on its own tiles with its own running maxima, sums and
@@ -33,22 +33,25 @@
 namespace mhc {
 namespace {
 
-constexpr int WARPS = 8, THREADS = WARPS * 32;
+constexpr int EXTRA = 1;   // places on the line that a (sequence, head) takes besides its units
 
 template <int D, bool FP8>
 struct One {
+  // CTAs an SM and warps of one
+  static constexpr int SM_CTAS = 2, WARPS = 8 / SM_CTAS, THREADS = WARPS * 32;
   static constexpr int ROW = FP8 ? D : 2 * D;             // bytes of a cache row
   static constexpr int CHUNKS = ROW / 16;
   static constexpr int KEYS = !FP8 && D == 128 ? 16 : 32; // of a warp's tile
   static constexpr int TILE = KEYS * ROW;                 // bytes, keys or values
   static constexpr int STAGE = 2 * TILE + (FP8 ? KEYS * 8 : 0);
-  static constexpr int STAGES = STAGE > 5000 ? 3 : 6;
+  static constexpr int STAGES = STAGE > 5000 ? 2 : 4;
   static constexpr int UNIT = WARPS * KEYS;
-  static constexpr int PASS = FP8 ? 4 : 8;                // rows that the warps meet over at a time
+  static constexpr int PASS = SM_CTAS == 1 && !FP8 ? 6 : 4;                          // rows that the warps meet over at a time
   static constexpr int MEET_ROW = D;                      // floats
   static constexpr int RING = WARPS * STAGES * STAGE;
-  static constexpr int SMEM = RING + WARPS * PASS * MEET_ROW * 4 + WARPS * 16 * 16 + WARPS * STAGES * 4;
-  static_assert(SMEM <= 227 * 1024, "a CTA's shared memory");
+  static constexpr int LOOK = 2 * KEYS * 4;                 // bytes: a tile's page numbers and places
+  static constexpr int SMEM = RING + WARPS * (PASS * MEET_ROW * 4 + 16 * 16 + STAGES * (LOOK + 4));
+  static_assert(SM_CTAS * (SMEM + 1024 + 256) <= 228 * 1024, "an SM's shared memory");
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -114,20 +117,30 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// What one query of a sequence sees: `count` positions, the first `sinks` and the
-// ones from `first` on.
+// What one query of a sequence sees: positions [0, sinks) and [first, length), the
+// latter from `start` = first rounded down to a block of 16 (which lies in one page), the
+// former up to there; in blocks of 16, the sinks' before the others.
+constexpr int BLOCK = 16;
 struct Seen {
-  int count, sinks, first;
+  int length, first, start, sinks, sink_blocks, blocks;
 };
 __device__ __forceinline__ Seen seen_by_last(const AttendParams &p, int length) {
   Seen v;
+  v.length = length;
   v.first = p.window && length > p.window ? length - p.window : 0;
+  v.start = v.first / BLOCK * BLOCK;
   v.sinks = min(p.sinks, v.first);
-  v.count = v.sinks + length - v.first;
+  v.sink_blocks = (min(v.sinks, v.start) + BLOCK - 1) / BLOCK;
+  v.blocks = v.sink_blocks + (length - v.start + BLOCK - 1) / BLOCK;
   return v;
 }
+// First position of block i.
+__device__ __forceinline__ int block_position(const Seen &v, int i) {
+  return i < v.sink_blocks ? i * BLOCK : v.start + (i - v.sink_blocks) * BLOCK;
+}
 
-// A place on the line of units: unit `unit` of `units` of (sequence s, head h).
+// A place on the line: unit `unit` of `units` of (sequence s, head h); the EXTRA places before
+// a pair's first unit have none (-EXTRA .. -1).
 struct Cursor {
   int s, h, unit, units;
   Seen seen;
@@ -135,13 +148,14 @@ struct Cursor {
 
 template <int D, bool FP8>
 __device__ __forceinline__ int units_of(const Seen &v) {
-  return (v.count + One<D, FP8>::UNIT - 1) / One<D, FP8>::UNIT;
+  constexpr int N = One<D, FP8>::UNIT / BLOCK;
+  return (v.blocks + N - 1) / N;
 }
 
 // To the first unit of the next (sequence, head); there has to be one.
 template <int D, bool FP8>
 __device__ __forceinline__ void next_head(const AttendParams &p, Cursor &c) {
-  c.unit = 0;
+  c.unit = -EXTRA;
   if (++c.h < p.kv_heads) return;
   c.h = 0;
   bool bad = false;
@@ -152,130 +166,196 @@ __device__ __forceinline__ void next_head(const AttendParams &p, Cursor &c) {
   } while (c.units == 0);
 }
 
+// Over the places without a unit.
+__device__ __forceinline__ void skip_extra(Cursor &c, int &left) {
+  const int n = min(left, max(-c.unit, 0));
+  c.unit += n;
+  left -= n;
+}
+
+// A (sequence, head) whose parts are with the CTAs cta0 .. cta1.
+struct Join {
+  int s, h, cta0, cta1;
+};
+
+// Four elements of a head's output from its sums.
+template <bool FP8>
+__device__ __forceinline__ void store_row4(const AttendParams &p, int s, int head, int col, int dim, float all, float n,
+                                           float all_out, const float4 &o) {
+  const float b = all == -INFINITY ? 0.f : all, bo = all_out == -INFINITY ? 0.f : all_out;
+  const float f = n != 0.f ? (FP8 ? exp2_fast(bo - b) : 1.f) / n : 0.f;
+  *reinterpret_cast<uint2 *>(p.output + s * p.output_stride + int64_t(head) * dim + col) =
+      make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+  if (p.lse && col == 0) p.lse[int64_t(s) * p.heads + head] = n != 0.f ? (b + log2f(n)) * 0.69314718056f : -INFINITY;
+}
+
+// Places of the line's CTA c: `total` divided by `grid`, the rest to the first ones.
+struct Line {
+  unsigned total, grid, each, more;
+  __device__ __forceinline__ unsigned begin(unsigned c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int cta(unsigned place) const {
+    const unsigned bound = more * (each + 1);
+    return int(place < bound ? place / (each + 1) : more + (place - bound) / each);
+  }
+};
+
 // One part of a (sequence, head) in scratch: [16][D] of output, then [16] of
 // (maximum, sum, maximum of the output's weights, -).
 template <int D>
 constexpr int part_floats() { return 16 * (D + 4); }
 
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p) {
+__global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)) k_attend_one(const AttendParams p) {
   using F = One<D, FP8>;
   constexpr int M_TILES = D / 16;      // of 16 elements of a row of output
+  constexpr int WARPS = F::WARPS, THREADS = F::THREADS;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ int64_t warp_total[WARPS];
+  __shared__ int warp_total[WARPS];
   __shared__ Cursor begin_shared;
-  __shared__ int last_shared;
+  __shared__ Join joins[2];   // of the part's first and last (sequence, head)
+  __shared__ int join_count;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int group = p.heads / p.kv_heads;
   bool bad = false;
+  if (tid == 0) join_count = 0;
 
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- this CTA's part of the line
+  // ---- this CTA's part of the line.  Code that runs once comes from far, line after
+  // line (a call's first microseconds are that): it is kept short.
   const int chunk = (p.sequences + THREADS - 1) / THREADS;
-  int64_t mine = 0;
+  auto places_of = [&](int s, Cursor &c, bool &wrong) {
+    c.s = s;
+    c.seen = seen_by_last(p, sequence_length(p, s, wrong));
+    c.units = units_of<D, FP8>(c.seen);
+    return c.units ? EXTRA + c.units : 0;
+  };
+  int mine = 0;
   bool empty = false;
-  for (int i = 0; i < chunk; ++i) {
-    const int s = tid * chunk + i;
-    if (s >= p.sequences) break;
-    const int units = units_of<D, FP8>(seen_by_last(p, sequence_length(p, s, bad)));
-    empty |= units == 0;
-    mine += int64_t(units) * p.kv_heads;
+#pragma unroll 1
+  for (int s = tid * chunk; s < min(p.sequences, (tid + 1) * chunk); ++s) {
+    Cursor c;
+    const int n = places_of(s, c, bad);
+    empty |= n == 0;
+    mine += n * p.kv_heads;
   }
-  int64_t upto = mine;   // inclusive
+  int upto = mine;   // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
   if (lane == 31) warp_total[warp] = upto;
   const bool any_empty = __syncthreads_or(empty);
-  int64_t total = 0;
+  Line line;
+  line.total = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) upto += warp_total[w];
-    total += warp_total[w];
+    line.total += warp_total[w];
   }
-  // CTAs that work: no more than there are units, so that each of them has some
-  const int64_t grid = max(int64_t(1), min(int64_t(gridDim.x), total)), cta = min(int64_t(blockIdx.x), grid);
-  const int64_t line0 = cta * total / grid, line1 = min(cta + 1, grid) * total / grid;
-  if (line0 < line1 && upto - mine <= line0 && line0 < upto) {
-    int64_t at = upto - mine;
+  // CTAs that work: no more than there are places, so that each of them has some
+  line.grid = max(1u, min(gridDim.x, line.total));
+  line.each = line.total / line.grid;
+  line.more = line.total - line.each * line.grid;
+  const int begin = int(line.begin(min(blockIdx.x, line.grid))), end = int(line.begin(min(blockIdx.x + 1, line.grid)));
+  if (begin < end && upto - mine <= begin && begin < upto) {
+    int rest = begin - (upto - mine);
     bool seen_before = false;
+    Cursor c;
+#pragma unroll 1
     for (int s = tid * chunk;; ++s) {
-      Cursor c;
-      c.s = s;
-      c.seen = seen_by_last(p, sequence_length(p, s, seen_before));
-      c.units = units_of<D, FP8>(c.seen);
-      const int64_t n = int64_t(c.units) * p.kv_heads;
-      if (line0 < at + n) {
-        c.h = int((line0 - at) / c.units);
-        c.unit = int((line0 - at) % c.units);
-        begin_shared = c;
+      const int n = places_of(s, c, seen_before);
+      if (rest < n * p.kv_heads) {
+        c.h = rest / n;
+        c.unit = rest - c.h * n - EXTRA;
         break;
       }
-      at += n;
+      rest -= n * p.kv_heads;
     }
+    begin_shared = c;
   }
   __syncthreads();
 
-  unsigned char *ring = smem + warp * F::STAGES * F::STAGE;
-  const uint32_t ring_at = smem_u32(ring);
+  const uint32_t ring_at = smem_u32(smem + warp * F::STAGES * F::STAGE);
   float *meet = reinterpret_cast<float *>(smem + F::RING);             // [WARPS][PASS][MEET_ROW]
   float4 *stats = reinterpret_cast<float4 *>(meet + WARPS * F::PASS * F::MEET_ROW);   // [WARPS][16]
-  uint32_t *masks = reinterpret_cast<uint32_t *>(stats + WARPS * 16) + warp * F::STAGES;
+  int *looks = reinterpret_cast<int *>(stats + WARPS * 16) + warp * F::STAGES * 2 * F::KEYS + lane % F::KEYS;
+  uint32_t *masks = reinterpret_cast<uint32_t *>(stats + WARPS * 16) + WARPS * F::STAGES * 2 * F::KEYS + warp * F::STAGES;
 
   Cursor at = begin_shared, ahead = at;
-  int64_t left = line1 - line0, left_ahead = left;
+  int left = end - begin, left_ahead = left;
+  skip_extra(at, left);
+  skip_extra(ahead, left_ahead);
 
-  // ---- copies: the tile of this warp at `ahead`, whose page number was read one step before
-  int page_ahead = -1, key_ahead = 0;
-  auto look = [&]() {
-    page_ahead = -1;
-    if (left_ahead <= 0) return;
-    const int v = ahead.unit * F::UNIT + warp * F::KEYS + lane;
-    if (lane < F::KEYS && v < ahead.seen.count) {
-      key_ahead = v < ahead.seen.sinks ? v : v - ahead.seen.sinks + ahead.seen.first;
-      page_ahead = p.page_table[ahead.s * p.table_stride + (key_ahead >> p.page_shift)];
-      if (page_ahead < 0 || page_ahead >= p.pages) {
-        bad = true;
-        page_ahead = -1;
-      }
-    }
-  };
-  const int page_mask = (1 << p.page_shift) - 1;
-  auto issue = [&](int stage) {
+  // ---- copies.  A tile is looked up STAGES tiles before its copies are issued: its
+  // pages' numbers (lane 16 i has block i's) come by a copy as well, into `looks` with the
+  // places in the page; -1 for positions that the query does not see.
+  constexpr int TILE_BLOCKS = F::KEYS / BLOCK;
+  auto look = [&](int stage) {
+    int place = -1;
     if (left_ahead > 0) {
-      const int offset = (ahead.h << p.page_shift) + (key_ahead & page_mask);
-      const uint32_t to = ring_at + stage * F::STAGE;
-      const uint32_t there = __ballot_sync(0xffffffffu, page_ahead >= 0);
-      if (lane == 0) masks[stage] = there;
-#pragma unroll
-      for (int i = 0; i < F::KEYS * F::CHUNKS / 32; ++i) {
-        const int row = (i * 32 + lane) / F::CHUNKS, c = (i * 32 + lane) % F::CHUNKS;
-        const int page = __shfl_sync(0xffffffffu, page_ahead, row), in_page = __shfl_sync(0xffffffffu, offset, row);
-        const bool ok = page >= 0;
-        const int64_t k = ok ? page * p.keys.page_stride + int64_t(in_page) * D : 0;
-        const int64_t v = ok ? page * p.values.page_stride + int64_t(in_page) * D : 0;
-        const int ck = F::CHUNKS >= 8 ? c ^ ((row & 1) << 2) : c;
-        const int cv = F::CHUNKS >= 8 ? c ^ ((row >> 1 & 3) << 1) : c ^ (row >> 1 & 3);
-        copy16(to + row * F::ROW + ck * 16, static_cast<const unsigned char *>(p.keys.data) + k * (FP8 ? 1 : 2) + c * 16, ok);
-        copy16(to + F::TILE + row * F::ROW + cv * 16, static_cast<const unsigned char *>(p.values.data) + v * (FP8 ? 1 : 2) + c * 16, ok);
-      }
-      if (FP8) {
-        const bool ok = page_ahead >= 0;
-        const int64_t from = ok ? ((int64_t(page_ahead) * p.kv_heads) << p.page_shift) + offset : 0;
-        copy4(to + 2 * F::TILE + lane * 4, p.keys.scales + from, ok);
-        copy4(to + 2 * F::TILE + (F::KEYS + lane) * 4, p.values.scales + from, ok);
+      const int block = ahead.unit * (F::UNIT / BLOCK) + warp * TILE_BLOCKS + lane / BLOCK;
+      const int position = block_position(ahead.seen, block) + lane % BLOCK;
+      if (lane < F::KEYS && block < ahead.seen.blocks && position < ahead.seen.length &&
+          (position >= ahead.seen.first || position < ahead.seen.sinks)) {
+        place = (ahead.h << p.page_shift) + (position & ((1 << p.page_shift) - 1));
+        copy4(smem_u32(looks + stage * 2 * F::KEYS), p.page_table + ahead.s * p.table_stride + (position >> p.page_shift), true);
       }
       --left_ahead;
-      if (++ahead.unit == ahead.units && left_ahead > 0) next_head<D, FP8>(p, ahead);
-      look();
+      if (++ahead.unit == ahead.units && left_ahead > 0) {
+        next_head<D, FP8>(p, ahead);
+        skip_extra(ahead, left_ahead);
+      }
     }
+    if (lane < F::KEYS) looks[(stage * 2 + 1) * F::KEYS] = place;
+  };
+  // A warp's instruction copies ROWS rows; this lane's are row lane / CHUNKS of them, its piece of
+  // a row lane % CHUNKS.
+  constexpr int ROWS = 32 / F::CHUNKS, COPIES = BLOCK / ROWS, SIZE = FP8 ? 1 : 2;
+  const int my_row = lane / F::CHUNKS, my_piece = lane % F::CHUNKS;
+  auto issue = [&](int stage) {
+    const uint32_t to = ring_at + stage * F::STAGE + my_row * F::ROW;
+    const int page = looks[stage * 2 * F::KEYS], place = lane < F::KEYS ? looks[(stage * 2 + 1) * F::KEYS] : -1;
+    const bool is_page = page >= 0 && page < p.pages, there = place >= 0 && is_page;
+    bad |= place >= 0 && !is_page;
+    const uint32_t all = __ballot_sync(0xffffffffu, there);
+    if (lane == 0) masks[stage] = all;
+    if (all) {
+#pragma unroll
+      for (int j = 0; j < TILE_BLOCKS; ++j) {
+        // from the page and place of the block's first position that the query sees
+        const uint32_t seen = all >> (j * BLOCK) & 0xffffu;
+        const int first = seen ? __ffs(seen) - 1 : 0;
+        const int64_t block_page = seen ? __shfl_sync(0xffffffffu, page, j * BLOCK + first) : 0;
+        const int block_place = (__shfl_sync(0xffffffffu, place, j * BLOCK + first) - first) * D + lane * (16 / SIZE);
+        const unsigned char *k = static_cast<const unsigned char *>(p.keys.data) + (block_page * p.keys.page_stride + block_place) * SIZE;
+        const unsigned char *v = static_cast<const unsigned char *>(p.values.data) + (block_page * p.values.page_stride + block_place) * SIZE;
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const int row = i * ROWS + my_row;   // of the block
+          const bool ok = seen >> row & 1;
+          const int ck = F::CHUNKS >= 8 ? my_piece ^ ((row & 1) << 2) : my_piece;
+          const int cv = F::CHUNKS >= 8 ? my_piece ^ ((row >> 1 & 3) << 1) : my_piece ^ (row >> 1 & 3);
+          copy16(to + (j * BLOCK + i * ROWS) * F::ROW + ck * 16, k + i * 512, ok);
+          copy16(to + F::TILE + (j * BLOCK + i * ROWS) * F::ROW + cv * 16, v + i * 512, ok);
+        }
+      }
+      if (FP8) {
+        const int64_t from = there ? ((int64_t(page) * p.kv_heads) << p.page_shift) + place : 0;
+        const uint32_t scales = ring_at + stage * F::STAGE + 2 * F::TILE + lane * 4;
+        copy4(scales, p.keys.scales + from, there);
+        copy4(scales + F::KEYS * 4, p.values.scales + from, there);
+      }
+    }
+    look(stage);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  look();
+#pragma unroll 1
+  for (int i = 0; i < F::STAGES; ++i) look(i);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
   for (int i = 0; i < F::STAGES; ++i) issue(i);
 
   // ---- sequences that see nothing
@@ -291,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
   int stage = 0;
   while (left > 0) {
     // ---- a segment: units at.unit .. of (at.s, at.h), as far as this CTA's part goes
-    const int unit0 = at.unit, count = int(left < at.units - at.unit ? left : int64_t(at.units - at.unit));
+    const int unit0 = at.unit, count = min(left, at.units - at.unit);
     const uint16_t *q = p.q + at.s * p.q_stride + int64_t(at.h) * group * D;
     uint32_t qb[NT][D / 16][2];          // of head 8 n + g
     float head_scale[NT][2];             // of heads 8 n + 2 t, + 1
@@ -531,8 +611,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
     // ---- the warps meet: rows PASS at a time, weighted to the common maximum
     const bool whole = count == at.units;
     // CTAs that have units of this (sequence, head), and where their parts are
-    const int64_t seg0 = line1 - left - unit0;   // its first unit on the line
-    const int cta0 = int(((seg0 + 1) * grid - 1) / total), cta1 = int(((seg0 + at.units) * grid - 1) / total);
+    const int place0 = end - left - unit0;   // its first unit on the line
+    const int cta0 = whole ? 0 : line.cta(place0), cta1 = whole ? 0 : line.cta(place0 + at.units - 1);
     float *parts = p.parts;
     const int slot = 2 * blockIdx.x + (int(blockIdx.x) == cta0);
 #pragma unroll
@@ -561,8 +641,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
           }
         }
       __syncthreads();
-      const int row = r0 + tid / (D / 4), col = tid % (D / 4) * 4;
-      if (row < r0 + F::PASS && row < group) {
+      for (int item = tid; item < F::PASS * (D / 4); item += THREADS) {
+        const int row = r0 + item / (D / 4), col = item % (D / 4) * 4;
+        if (row >= group) break;
         float all = -INFINITY, all_out = -INFINITY, n = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -582,12 +663,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
           o.z += v.z * f;
           o.w += v.w * f;
         }
-        const int head = at.h * group + row;
         if (whole) {
-          const float f = n != 0.f ? (FP8 ? exp2_fast(bo - b) : 1.f) / n : 0.f;
-          *reinterpret_cast<uint2 *>(p.output + at.s * p.output_stride + int64_t(head) * D + col) =
-              make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-          if (p.lse && col == 0) p.lse[int64_t(at.s) * p.heads + head] = n != 0.f ? (b + log2f(n)) * 0.69314718056f : -INFINITY;
+          store_row4<FP8>(p, at.s, at.h * group + row, col, D, all, n, all_out, o);
         } else {
           float *part = parts + int64_t(slot) * part_floats<D>();
           *reinterpret_cast<float4 *>(part + row * D + col) = o;
@@ -596,29 +673,65 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
       }
     }
     if (!whole) {
-      // ---- the last CTA of this (sequence, head) joins the parts
+      // the CTA that comes last joins the parts, once it has no other work
       __threadfence();
       __syncthreads();
-      if (tid == 0) last_shared = atomicAdd(p.counters + cta0, 1u) == unsigned(cta1 - cta0);
-      __syncthreads();
-      if (last_shared) {
-        __threadfence();
-        for (int item = tid; item < group * (D / 4); item += THREADS) {
-          const int row = item / (D / 4), col = item % (D / 4) * 4;
-          auto part = [&](int c) { return parts + int64_t(2 * c + (c == cta0)) * part_floats<D>(); };
-          float all = -INFINITY, all_out = -INFINITY, n = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int c = cta0; c <= cta1; ++c) {
-            const float4 st = __ldcg(reinterpret_cast<const float4 *>(part(c) + 16 * D + row * 4));
-            all = fmaxf(all, st.x);
-            all_out = fmaxf(all_out, st.z);
+      if (tid == 0 && atomicAdd(p.counters + cta0, 1u) == unsigned(cta1 - cta0)) {
+        p.counters[cta0] = 0;
+        joins[join_count++] = {at.s, at.h, cta0, cta1};
+      }
+    }
+    __syncthreads();   // stats may be written again
+    left -= count;
+    at.unit += count;
+    if (at.unit == at.units && left > 0) {
+      next_head<D, FP8>(p, at);
+      skip_extra(at, left);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+
+  // ---- joins: as many parts at a time as the ring has room for, all their reads under
+  // way together (while other CTAs read the cache, a trip to memory takes a microsecond)
+  for (int k = 0; k < join_count; ++k) {
+    const Join join = joins[k];
+    const int pieces = group * (D / 4 + 1), room = F::RING / 16 / pieces;   // of 16 bytes, a part's rows and stats
+    __threadfence();
+    for (int item0 = 0; item0 < group * (D / 4); item0 += THREADS) {
+      const int item = item0 + tid, row = item / (D / 4), col = item % (D / 4);
+      float all = -INFINITY, all_out = -INFINITY, n = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int c0 = join.cta0; c0 <= join.cta1; c0 += room) {
+        const int count = min(room, join.cta1 + 1 - c0);
+        if (item0 == 0 || count < join.cta1 + 1 - join.cta0) {   // else they are there
+          __syncthreads();
+#pragma unroll 4
+          for (int i = tid; i < count * pieces; i += THREADS) {
+            const int c = c0 + i / pieces, piece = i % pieces;
+            const float *from = p.parts + int64_t(2 * c + (c == join.cta0)) * part_floats<D>() +
+                                (piece < group * (D / 4) ? piece * 4 : 16 * D + (piece - group * (D / 4)) * 4);
+            copy16(smem_u32(smem) + i * 16, from, true);
           }
-          const float b = all == -INFINITY ? 0.f : all, bo = all_out == -INFINITY ? 0.f : all_out;
-#pragma unroll 8
-          for (int c = cta0; c <= cta1; ++c) {
-            const float4 st = __ldcg(reinterpret_cast<const float4 *>(part(c) + 16 * D + row * 4));
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(c) + row * D + col));
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncthreads();
+        }
+        if (row < group) {
+          const float4 *part = reinterpret_cast<const float4 *>(smem);
+          float now = all, now_out = all_out;
+#pragma unroll 4
+          for (int i = 0; i < count; ++i) {
+            const float4 st = part[i * pieces + group * (D / 4) + row];
+            now = fmaxf(now, st.x);
+            now_out = fmaxf(now_out, st.z);
+          }
+          const float b = now == -INFINITY ? 0.f : now, bo = now_out == -INFINITY ? 0.f : now_out;
+          const float keep = exp2_fast(all_out - bo);
+          n *= exp2_fast(all - b);
+          o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll 4
+          for (int i = 0; i < count; ++i) {
+            const float4 st = part[i * pieces + group * (D / 4) + row], v = part[i * pieces + row * (D / 4) + col];
             n += st.y * exp2_fast(st.x - b);
             const float f = exp2_fast(st.z - bo);
             o.x += v.x * f;
@@ -626,21 +739,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend_one(const AttendParams p)
             o.z += v.z * f;
             o.w += v.w * f;
           }
-          const int head = at.h * group + row;
-          const float f = n != 0.f ? (FP8 ? exp2_fast(bo - b) : 1.f) / n : 0.f;
-          *reinterpret_cast<uint2 *>(p.output + at.s * p.output_stride + int64_t(head) * D + col) =
-              make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-          if (p.lse && col == 0) p.lse[int64_t(at.s) * p.heads + head] = n != 0.f ? (b + log2f(n)) * 0.69314718056f : -INFINITY;
+          all = now;
+          all_out = now_out;
         }
-        if (tid == 0) p.counters[cta0] = 0;
       }
+      if (row < group) store_row4<FP8>(p, join.s, join.h * group + row, col * 4, D, all, n, all_out, o);
     }
-    __syncthreads();   // stats may be written again
-    left -= count;
-    at.unit += count;
-    if (at.unit == at.units && left > 0) next_head<D, FP8>(p, at);
+    __syncthreads();
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
   if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
 }
 
@@ -648,11 +754,11 @@ template <int D, bool FP8, int NT>
 cudaError_t launch(const AttendParams &p, int sms, cudaStream_t stream) {
   // what a sequence can see at most, in units
   int64_t most = int64_t(p.table_width) << p.page_shift;
-  if (p.window) most = std::min(most, int64_t(p.window) + p.sinks);
-  const int64_t units = (most + One<D, FP8>::UNIT - 1) / One<D, FP8>::UNIT * p.kv_heads * p.sequences;
+  if (p.window) most = std::min(most, int64_t(p.window) + p.sinks + 2 * BLOCK);
+  const int64_t places = (EXTRA + (most + One<D, FP8>::UNIT - 1) / One<D, FP8>::UNIT) * p.kv_heads * p.sequences;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(std::min<int64_t>(units, sms)));
-  cfg.blockDim = dim3(THREADS);
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(places, One<D, FP8>::SM_CTAS * sms)));
+  cfg.blockDim = dim3(One<D, FP8>::THREADS);
   cfg.dynamicSmemBytes = One<D, FP8>::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -686,7 +792,7 @@ cudaError_t attend_one_setup() {
   return e;
 }
 
-size_t attend_one_scratch(int sms) { return size_t(2) * sms * part_floats<128>() * sizeof(float); }
+size_t attend_one_scratch(int sms) { return size_t(2) * 2 * sms * part_floats<128>() * sizeof(float); }
 
 cudaError_t launch_attend_one(const AttendParams &p, int sms, cudaStream_t stream) {
   if (p.dim == 128) return p.fp8 ? launch_groups<128, true>(p, sms, stream) : launch_groups<128, false>(p, sms, stream);
