@@ -103,8 +103,11 @@ typedef struct {
  * and lse the logarithm of the lower sum (natural); a row that sees nothing
  * has zeros and minus infinity.  Positions that a query does not see may hold
  * anything.  Rows of output from q_starts[sequences] on are left as they are.
- * The softmax and all sums are held in FP32; weights of BF16 values are rounded
- * to BF16 for calls with q_starts or with more than 16 heads for each kv head.
+ * The softmax and all sums are held in FP32.  In calls with q_starts or with more
+ * than 16 heads for each kv head the weights are rounded to BF16, and over an
+ * 8-bit cache queries are off by at most 2^-17 of their head's largest element (0
+ * for elements from 2^-9 of it on); in the others weights keep 16 bits over a BF16
+ * cache and FP16's over an 8-bit one.
  * output and lse overlap no input. */
 typedef struct {
   int32_t tokens, sequences;

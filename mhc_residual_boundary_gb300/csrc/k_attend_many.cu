@@ -23,8 +23,9 @@
 //  10, 11    values of units that are hidden from some rows: P is zero there, but zero
 //            times an infinity is not.  Infinities and NaN in such units are set to zero
 //            before the product, and the rows that do see them are told (poison).  Over
-//            an 8-bit cache also keys and values to BF16 (exactly); the scales go to the
-//            columns of S and of P.
+//            an 8-bit cache also values to BF16 (exactly), for the product with P.  Keys are
+//            taken as they are, by queries in two 8-bit pieces, which the softmax warps
+//            make of their rows.  The scales go to the columns of S and of P.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -48,17 +49,20 @@ template <int D, bool FP8>
 struct Many {
   static constexpr int THREADS = 384;
   static constexpr int SLOT = KEYS * 2 * D;             // keys or values of a unit in BF16
-  static constexpr int SLOTS = D == 128 ? (FP8 ? 3 : 5) : (FP8 ? 6 : 8);
+  static constexpr int SLOTS = D == 128 ? (FP8 ? 2 : 5) : (FP8 ? 4 : 8);   // of both, 8-bit: of values
   static constexpr int RAW = FP8 ? KEYS * D : 0;        // the same as they are in an 8-bit cache
-  static constexpr int RAWS = FP8 ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int RAWS = FP8 ? (D == 128 ? 2 : 4) : 0;    // values to be converted
+  static constexpr int KSLOTS = FP8 ? (D == 128 ? 3 : 4) : 0;  // keys
   static constexpr int Q = ROWS * 2 * D;                // a tile's queries
   static constexpr int Q_AT = 0, SLOTS_AT = 2 * Q, RAW_AT = SLOTS_AT + SLOTS * SLOT;
-  static constexpr int SCALES_AT = RAW_AT + RAWS * RAW; // [INFOS][keys, values][KEYS]
+  static constexpr int K_AT = RAW_AT + RAWS * RAW;
+  static constexpr int SCALES_AT = K_AT + KSLOTS * RAW; // [INFOS][keys, values][KEYS]
   static constexpr int CONTROL_AT = SCALES_AT + (FP8 ? INFOS * 2 * KEYS * 4 : 0);
   // registers a thread: at the launch, then the softmax warps', the others'
   static constexpr int R_START = 168, R_SOFT = 208, R_REST = 88;
   static_assert(256 * R_SOFT + 128 * R_REST <= THREADS * R_START, "registers of a CTA");
-  static_assert((SLOTS + RAWS) / 2 + 2 <= INFOS && SLOTS / 2 <= READY, "notes outlive their unit");
+  static_assert((FP8 ? SLOTS + RAWS : SLOTS / 2) + 2 <= INFOS + 2 && (FP8 || SLOTS / 2 <= READY) && KSLOTS + 2 <= INFOS,
+                "notes outlive their unit");
 };
 
 // Notes of a unit, which the copying warp writes for the others.
@@ -92,12 +96,13 @@ struct Item {
 
 struct Control {
   uint64_t full[8], empty[8], raw_full[8], raw_empty[8], info_full[INFOS], ready[READY];
+  uint64_t k_full[4], k_empty[4], q_ready[2];   // 8-bit cache
   uint64_t q_full, q_empty, s_full[2], p_ready[2][2], o_full[2], drain;
   Info info[INFOS];
   Segment segment[SEGMENTS];
   uint32_t tmem;
   int abort;
-  int issued, q_issued;  // copies into the ring, of queries
+  int issued, k_issued, q_issued;  // copies into the ring (8-bit cache: of values), of keys, of queries
   int64_t warp_total[16];
   Item begin;
   int begin_place;
@@ -290,7 +295,7 @@ constexpr uint32_t S_COL(int X) { return X * 128; }
 constexpr uint32_t O_COL(int X) { return 256 + X * 128; }
 
 // Instruction descriptors: S = Q K^T, both K-major; O = P V, V's columns contiguous.
-constexpr uint32_t IDESC_S = tc::idesc_bf16_f32(ROWS, KEYS);
+constexpr uint32_t IDESC_S = tc::idesc_bf16_f32(ROWS, KEYS), IDESC_S8 = tc::idesc_e4m3_f32(ROWS, KEYS);
 template <int D>
 constexpr uint32_t idesc_o() { return tc::idesc_bf16_f32(ROWS, D) | 1u << 16; }
 
@@ -353,6 +358,56 @@ __device__ __forceinline__ void store32(uint16_t *const (&rows)[4], int c0, int 
     if (rows[k]) st_vec(rows[k] + c0 + lane % 4 * 8, piece[k]);
 }
 
+// A row of queries in two E4M3 pieces, for products with 8-bit keys: y = q 2^(7 - e) with
+// the largest |y| in [128, 256) is the sum of y rounded to E4M3 and the rest, which has no
+// more than E4M3's four bits either, down to 2^-2; below that the rest is rounded to a
+// multiple of 2^-9.  In place: 64 elements of BF16 give their row of 128 bytes to 64 of the
+// first piece and 64 of the second.  Returns 2^(e - 7), NaN for a row that is not finite.
+template <int D>
+__device__ __forceinline__ float split_queries(unsigned char *tile, int row) {
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(tile + i / 8 * ROWS * 128 + row * 128 + i % 8 * 16);
+    top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(__vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu));
+  }
+  const int e2 = int(max(top >> 16, top & 0xffffu) >> 7);
+  const int e = max(e2 - 127, -110);
+  const float up = __uint_as_float(uint32_t(127 + 7 - e) << 23);
+#pragma unroll 1
+  for (int h = 0; h < D / 64; ++h) {
+    unsigned char *at = tile + h * ROWS * 128 + row * 128;
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(at + ((i ^ (row & 7)) * 16));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        float y[4] = {bf16_lo(w[k]) * up, bf16_hi(w[k]) * up, bf16_lo(w[k + 1]) * up, bf16_hi(w[k + 1]) * up};
+        const uint32_t a = e4m3x4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          uint32_t f;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(uint16_t(a >> q * 8)));
+          float b0, b1;
+          asm("{.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;}" : "=f"(b0), "=f"(b1) : "r"(f));
+          y[q] -= b0;
+          y[q + 1] -= b1;
+        }
+        hi[i * 2 + k / 2] = a;
+        lo[i * 2 + k / 2] = e4m3x4(y[0], y[1], y[2], y[3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      *reinterpret_cast<uint4 *>(at + ((i ^ (row & 7)) * 16)) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+      *reinterpret_cast<uint4 *>(at + (((4 + i) ^ (row & 7)) * 16)) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+    }
+  }
+  return e2 == 255 ? NAN : __uint_as_float(uint32_t(127 + e - 7) << 23);
+}
+
 constexpr int part_floats(int dim) { return (dim + 2) * ROWS; }   // of one tile: [dim][row], maxima, sums
 
 template <int D, bool FP8>
@@ -363,10 +418,11 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
   const uint32_t lanes = uint32_t(warp * 32) << 16;
   const uint32_t s_at = tmem + S_COL(X) + lanes, o_at = tmem + O_COL(X) + lanes;
   const int group = p.heads / p.kv_heads, query = tid / group, head = tid % group;
-  const float scale = p.scale_log2, slack = GROWTH / scale;
+  float scale = p.scale_log2, slack = GROWTH / scale;   // (8-bit cache: of this row)
   const float *scales = reinterpret_cast<const float *>(smem + F::SCALES_AT);
-  uint32_t s_phase = 0, o_phase = 0;
-  Ring info, ready, slot;   // `slot`: the next unit's keys
+  uint32_t s_phase = 0, o_phase = 0, q_phase = 0;
+  Ring info, ready, slot;   // `slot`: the next unit's keys, 8-bit: values
+  bool fresh = true;        // a segment's first unit
   uint32_t bits[8];
   bool poisoned = false, any = false;
   float top = -INFINITY, sum = 0.f;
@@ -375,7 +431,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     const Ring my_info = info, my_ready = ready;
     info.next(INFOS);
     ready.next(READY);
-    slot.next(F::SLOTS);
+    if (!FP8) slot.next(F::SLOTS);
     const Ring my_value = slot;
     slot.next(F::SLOTS);
     tc::wait_or_abort_inline(&c.info_full[my_info.at], my_info.phase, abort);
@@ -384,6 +440,19 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     const uint32_t flags = u.flags;
     if (__any_sync(0xffffffffu, *abort) || (flags & STOP)) break;
     const Segment &seg = c.segment[segment % SEGMENTS];
+    if (FP8 && fresh) {
+      fresh = false;
+      if (seg.count[X] > 0) {
+        tc::wait_or_abort_inline(&c.q_full, q_phase, abort);
+        __syncwarp();
+        scale = p.scale_log2 * split_queries<D>(smem + F::Q_AT + X * F::Q, tid);
+        slack = GROWTH / scale;
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&c.q_ready[X]);
+      }
+      q_phase ^= 1u;
+    }
     if (flags >> X & 1) {
       const uint32_t pages = u.pages;
       tc::wait_or_abort_inline(&c.s_full[X], s_phase, abort);
@@ -519,6 +588,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     if (!(flags & LAST)) continue;
     // ---- the segment's end
     ++segment;
+    fresh = true;
     const bool had = any, live = query < seg.count[X];
     const float top_now = top, sum_now = sum;
     any = false;
@@ -629,13 +699,10 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
   const int lane = threadIdx.x % 32;
   volatile int *abort = &c.abort;
   const int unit_pages = KEYS >> p.page_shift, box = COLS * (FP8 ? 1 : 2) << p.page_shift;
-  uint64_t *full = FP8 ? c.raw_full : c.full, *empty = FP8 ? c.raw_empty : c.empty;
-  const int slots = FP8 ? F::RAWS : F::SLOTS;
-  const int slot_bytes = FP8 ? F::RAW : F::SLOT;
-  unsigned char *ring = smem + (FP8 ? F::RAW_AT : F::SLOTS_AT);
-  Ring at, info;
+  constexpr int BYTES = FP8 ? F::RAW : F::SLOT;
+  Ring ring, k_ring, info;
   uint32_t q_phase = 1;
-  int issued = 0, q_issued = 0;
+  int issued = 0, k_issued = 0, q_issued = 0;
   bool ok = !*static_cast<volatile int *>(&g_stall_copies), bad = false;
   // a unit's page numbers, one a lane; -1: not there
   auto look = [&](const Item &it, int j) {
@@ -687,7 +754,11 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
       const Unit u = unit_of(it, j);
       const uint32_t inside = __ballot_sync(0xffffffffu, lane < unit_pages && u.key0 + (lane << p.page_shift) < u.end);
       for (int kv = 0; kv < 2; ++kv) {
-        ok = tc::wait_or_abort(&empty[at.at], at.phase ^ 1u, abort);
+        const bool keys = FP8 && kv == 0;   // have a ring of their own
+        Ring &at = keys ? k_ring : ring;
+        uint64_t *full = (FP8 ? keys ? c.k_full : c.raw_full : c.full) + at.at;
+        uint64_t *empty = (FP8 ? keys ? c.k_empty : c.raw_empty : c.empty) + at.at;
+        ok = tc::wait_or_abort(empty, at.phase ^ 1u, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (kv == 0) {
@@ -712,15 +783,16 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
             tc::bulk_load(to + KEYS, p.values.scales + from, 4u << p.page_shift, &c.info_full[info.at]);
           }
         }
-        if (lane == 0) tc::mbar_arrive_expect_tx(&full[at.at], uint32_t(slot_bytes));
+        if (lane == 0) tc::mbar_arrive_expect_tx(full, uint32_t(BYTES));
         __syncwarp();
         if (lane < unit_pages) {
-          unsigned char *to = ring + size_t(at.at) * slot_bytes + lane * box;
+          unsigned char *to = smem + (FP8 ? keys ? F::K_AT : F::RAW_AT : F::SLOTS_AT) + at.at * BYTES + lane * box;
           for (int k = 0; k < HALVES; ++k)   // a page that is not there: zeros
-            tc::tma_load_3d(to + k * KEYS * 128, kv ? tm_v : tm_k, k * 64, it.h << p.page_shift, page, &full[at.at]);
+            tc::tma_load_3d(to + k * KEYS * 128, kv ? tm_v : tm_k, k * 64, it.h << p.page_shift, page, full);
         }
-        at.next(slots);
-        ++issued;
+        at.next(FP8 ? keys ? F::KSLOTS : F::RAWS : F::SLOTS);
+        if (keys) ++k_issued;
+        else ++issued;
       }
       if (!ok) break;
       info.next(INFOS);
@@ -730,6 +802,7 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
   // the others end (after a wait that gave up they have seen that as well)
   if (lane == 0) {
     c.issued = issued;
+    c.k_issued = k_issued;
     c.q_issued = q_issued;
     if (ok) {
       c.info[info.at].flags = STOP;
@@ -744,7 +817,10 @@ template <int D, bool FP8>
 __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32_t tmem) {
   using F = Many<D, FP8>;
   volatile int *abort = &c.abort;
-  const uint64_t q_desc = tc::desc_sw128(smem + F::Q_AT), k_desc = tc::desc_sw128(smem + F::SLOTS_AT);
+  // keys: rows of 128 bytes, 64 of them 8-bit ones of 64 elements (in the 64-byte swizzled layout)
+  const uint64_t q_desc = tc::desc_sw128(smem + F::Q_AT);
+  const uint64_t k_desc = FP8 && D == 64 ? tc::smem_desc(tc::smem_addr(smem + F::K_AT), 16, 512) | uint64_t(4) << 61
+                                         : tc::desc_sw128(smem + (FP8 ? F::K_AT : F::SLOTS_AT));
   // values: 64 columns of 8 positions are 1024 bytes, the next 8 positions behind them, the
   // next 64 columns KEYS * 128 bytes on
   const uint64_t v_desc = tc::smem_desc(tc::smem_addr(smem + F::SLOTS_AT), KEYS * 128, 1024) | uint64_t(2) << 61;
@@ -752,6 +828,8 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
   uint32_t q_phase = 0, p_phase[2] = {0, 0};
   bool ok = true, pending[2] = {false, false}, any[2] = {false, false};
   bool first = true, flush = false;           // a segment's first unit; the step behind its last one
+  Ring k_at;
+  uint32_t segment = 0, ready_phase[2] = {0, 0};
   while (ok) {
     uint32_t flags = 0;
     if (!flush) {
@@ -761,10 +839,19 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
       info.next(INFOS);
       if (flags & STOP) break;
       if (first) {
-        ok = tc::wait_or_abort(&c.q_full, q_phase, abort);
-        q_phase ^= 1u;
+        if (FP8) {
+          const Segment &seg = c.segment[segment++ % SEGMENTS];
+          for (int X = 0; X < 2 && ok; ++X)
+            if (seg.count[X] > 0) {
+              ok = tc::wait_or_abort(&c.q_ready[X], ready_phase[X], abort);
+              ready_phase[X] ^= 1u;
+            }
+        } else {
+          ok = tc::wait_or_abort(&c.q_full, q_phase, abort);
+          q_phase ^= 1u;
+        }
       }
-      ok = ok && tc::wait_or_abort(&c.full[at.at], at.phase, abort);
+      ok = ok && (FP8 ? tc::wait_or_abort(&c.k_full[k_at.at], k_at.phase, abort) : tc::wait_or_abort(&c.full[at.at], at.phase, abort));
       if (!ok) break;
     }
     if (!first) {
@@ -796,6 +883,14 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
         any[X] = false;
       } else if (flags >> X & 1) {
         tc::fence_after_sync();
+        if (FP8) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {   // 32 elements: of 64, of a piece
+            const int h = k / 4, piece = k / 2 % 2, half = k % 2;
+            tc::mma_e4m3(tmem + S_COL(X), q_desc + X * (F::Q >> 4) + h * (ROWS * 128 >> 4) + piece * 4 + half * 2,
+                         k_desc + k_at.at * (F::RAW >> 4) + h * 4 + half * 2, IDESC_S8, k != 0);
+          }
+        } else
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint64_t step = k / 4 * (ROWS * 128 >> 4) + k % 4 * 2;
@@ -807,9 +902,10 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
     }
     if (!ok) break;
     if (!flush) {
-      tc::mma_commit(&c.empty[at.at]);
+      tc::mma_commit(FP8 ? &c.k_empty[k_at.at] : &c.empty[at.at]);
       if (flags & LAST) tc::mma_commit(&c.q_empty);
-      at.next(F::SLOTS);
+      if (FP8) k_at.next(F::KSLOTS);
+      else at.next(F::SLOTS);
       value = at;
       at.next(F::SLOTS);
       value_ready = ready;
@@ -878,7 +974,7 @@ __device__ __forceinline__ void clean_role(unsigned char *smem, Control &c) {
   }
 }
 
-// 8-bit keys and values to BF16, two rows a thread; the values' NaN as clean_values.
+// 8-bit values to BF16, two rows a thread; NaN as clean_values.
 template <int D>
 __device__ __forceinline__ void convert_role(unsigned char *smem, Control &c) {
   using F = Many<D, true>;
@@ -890,54 +986,52 @@ __device__ __forceinline__ void convert_role(unsigned char *smem, Control &c) {
     const uint32_t flags = c.info[info.at].flags;
     if (flags & STOP) break;
     const bool hidden = hides(flags);
-    for (int kv = 0; kv < 2; ++kv) {
-      ok = __all_sync(0xffffffffu, tc::wait_or_abort(&c.raw_full[raw.at], raw.phase, abort) &&
-                                       tc::wait_or_abort(&c.empty[slot.at], slot.phase ^ 1u, abort));
-      if (!ok) break;
+    ok = __all_sync(0xffffffffu, tc::wait_or_abort(&c.raw_full[raw.at], raw.phase, abort) &&
+                                     tc::wait_or_abort(&c.empty[slot.at], slot.phase ^ 1u, abort));
+    if (!ok) break;
 #pragma unroll 1
-      for (int row = thread; row < KEYS; row += 64) {
-        const unsigned char *from = smem + F::RAW_AT + raw.at * F::RAW + row * D;
-        unsigned char *to = smem + F::SLOTS_AT + slot.at * F::SLOT + row * 128;
-        bool nan = false;
+    for (int row = thread; row < KEYS; row += 64) {
+      const unsigned char *from = smem + F::RAW_AT + raw.at * F::RAW + row * D;
+      unsigned char *to = smem + F::SLOTS_AT + slot.at * F::SLOT + row * 128;
+      bool nan = false;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int chunk = D == 128 ? i ^ (row & 7) : i ^ (row >> 1 & 3);   // as the copies laid them
-          const uint4 v = *reinterpret_cast<const uint4 *>(from + chunk * 16);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[8];
+      for (int i = 0; i < D / 16; ++i) {
+        const int chunk = D == 128 ? i ^ (row & 7) : i ^ (row >> 1 & 3);   // as the copies laid them
+        const uint4 v = *reinterpret_cast<const uint4 *>(from + chunk * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t h;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(w[k / 2] >> k % 2 * 16)));
+          float a, b;
+          asm("{.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;}" : "=f"(a), "=f"(b) : "r"(h));
+          o[k] = pack_bf16x2(a, b);
+        }
+        if (hidden) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(w[k / 2] >> k % 2 * 16)));
-            float a, b;
-            asm("{.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;}" : "=f"(a), "=f"(b) : "r"(h));
-            o[k] = pack_bf16x2(a, b);
+            const uint32_t bad = not_finite2(o[k]);
+            if (bad & 0x8000u) o[k] &= 0xffff0000u;
+            if (bad & 0x80000000u) o[k] &= 0x0000ffffu;
+            nan |= bad != 0;
           }
-          if (kv && hidden) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t bad = not_finite2(o[k]);
-              if (bad & 0x8000u) o[k] &= 0xffff0000u;
-              if (bad & 0x80000000u) o[k] &= 0x0000ffffu;
-              nan |= bad != 0;
-            }
-          }
-          unsigned char *half = to + i / 4 * KEYS * 128;
-          const int c0 = i % 4 * 2;
-          *reinterpret_cast<uint4 *>(half + ((c0 ^ (row & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4 *>(half + (((c0 + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        if (nan) atomicOr(c.info[info.at].poison + row / 32, 1u << row % 32);
+        unsigned char *half = to + i / 4 * KEYS * 128;
+        const int c0 = i % 4 * 2;
+        *reinterpret_cast<uint4 *>(half + ((c0 ^ (row & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(half + (((c0 + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(&c.full[slot.at]);
-        tc::mbar_arrive(&c.raw_empty[raw.at]);
-      }
-      raw.next(F::RAWS);
-      slot.next(F::SLOTS);
+      if (nan) atomicOr(c.info[info.at].poison + row / 32, 1u << row % 32);
     }
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tc::mbar_arrive(&c.full[slot.at]);
+      tc::mbar_arrive(&c.raw_empty[raw.at]);
+    }
+    raw.next(F::RAWS);
+    slot.next(F::SLOTS);
     info.next(INFOS);
   }
 }
@@ -962,6 +1056,11 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     }
     for (int i = 0; i < INFOS; ++i) tc::mbar_init(&c.info_full[i], 1);
     for (int i = 0; i < READY; ++i) tc::mbar_init(&c.ready[i], 2);
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&c.k_full[i], 1);
+      tc::mbar_init(&c.k_empty[i], 1);
+    }
+    for (int X = 0; X < 2; ++X) tc::mbar_init(&c.q_ready[X], 4);
     tc::mbar_init(&c.q_full, 1);
     tc::mbar_init(&c.q_empty, 1);
     for (int X = 0; X < 2; ++X) {
@@ -972,7 +1071,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     }
     tc::mbar_init(&c.drain, 1);
     tc::mbar_init_fence();
-    c.abort = c.issued = c.q_issued = 0;
+    c.abort = c.issued = c.k_issued = c.q_issued = 0;
   }
   if (warp == 9) tc::tmem_alloc(&c.tmem, 512);
   if (warp == 8 && lane == 0) {
@@ -1129,9 +1228,11 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     const int slots = FP8 ? F::RAWS : F::SLOTS;
     for (int i = max(0, c.issued - slots); i < c.issued; ++i)
       tc::mbar_wait_bounded(&full[i % slots], uint32_t(i / slots & 1), tc::SUB_WAIT_LIMIT);
+    if (FP8)
+      for (int i = max(0, c.k_issued - F::KSLOTS); i < c.k_issued; ++i)
+        tc::mbar_wait_bounded(&c.k_full[i % max(F::KSLOTS, 1)], uint32_t(i / max(F::KSLOTS, 1) & 1), tc::SUB_WAIT_LIMIT);
     if (c.q_issued > 0) tc::mbar_wait_bounded(&c.q_full, uint32_t(c.q_issued - 1 & 1), tc::SUB_WAIT_LIMIT);
-    const int units = (c.issued + 1) / 2;
-    for (int i = max(0, units - INFOS); FP8 && i < units; ++i)
+    for (int i = max(0, c.k_issued - INFOS); FP8 && i < c.k_issued; ++i)
       tc::mbar_wait_bounded(&c.info_full[i % INFOS], uint32_t(i / INFOS & 1), tc::SUB_WAIT_LIMIT);
   }
 }

@@ -8,9 +8,11 @@ Tolerances, from the arithmetic (w the softmax weights, sum w = 1):
 * the weight is rounded for the matrix product: to BF16 (2^-8 of itself) in calls
   with q_starts or more than 16 heads a kv head, to FP16 over an 8-bit cache in
   the others (2^-11 of itself, or 2^-25 of the largest below FP16's normals), to two
-  BF16 pieces (2^-16) over a BF16 one; the queries over an 8-bit cache go to FP16
-  with a power of two taken off, which changes an element by at most 2^-25 of the
-  row's largest: covered by S's factor when S counts the row's largest for it;
+  BF16 pieces (2^-16) over a BF16 one;
+* queries over an 8-bit cache have a power of two taken off each row: in FP16 that
+  changes an element by at most 2^-25 of the row's largest, in two E4M3 pieces (calls
+  with q_starts or more than 16 heads a kv head) by at most 2^-17 of it: S takes the
+  elements with that over 2^-20 added;
 * the output is rounded to BF16: half an ulp of what is rounded, which is off itself, and
   so may lie in the binade above;
 so an output is off by at most e + half an ulp at |out| + e, with
@@ -106,7 +108,7 @@ def define(inputs, *, window=0, sinks=0, scale=None, page, gone=()):
             out[i] = torch.einsum("kgn,knd->kgd", w, v[:, seen]).reshape(heads, d)
             mag[i] = torch.einsum("kgn,knd->kgd", w, v[:, seen].abs()).reshape(heads, d)
             lse[i] = torch.logsumexp(x, -1).flatten()
-            near = qi.abs() + 2.0 ** -8 * qi.abs().amax(-1, keepdim=True)
+            near = qi.abs() + query_rounding(inputs) / STEPS * qi.abs().amax(-1, keepdim=True)
             size[i] = (scale * torch.einsum("kgd,knd->kgn", near, k[:, seen].abs())).amax(-1).flatten()
     return out, lse, mag, size
 
@@ -116,6 +118,12 @@ def weight_rounding(inputs):
     if "q_starts" in inputs or heads // kv > 16:
         return 2.0 ** -8
     return 2.0 ** -11 if "k_scales" in inputs else 2.0 ** -16
+
+
+def query_rounding(inputs):
+    if "k_scales" not in inputs:
+        return 0.0
+    return 2.0 ** -17 if weight_rounding(inputs) == 2.0 ** -8 else 2.0 ** -25
 
 
 def half_ulp_bf16(x):

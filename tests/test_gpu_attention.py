@@ -162,13 +162,14 @@ def test_hidden_places_hold_anything(handles, several, fp8):
     a.check_errors()
 
 
-@pytest.mark.parametrize("d,window,sinks", [(128, 0, 0), (128, 70, 2), (64, 0, 0), (64, 33, 5)])
+@pytest.mark.parametrize("d,window,sinks,heads", [(128, 0, 0, 8), (128, 70, 2, 8), (64, 0, 0, 8), (64, 33, 5, 8),
+                                                  (128, 0, 0, 2), (128, 150, 2, 2), (64, 0, 0, 2)])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_values_that_some_rows_do_not_see(handles, fp8, d, window, sinks):
+def test_values_that_some_rows_do_not_see(handles, fp8, d, window, sinks, heads):
     """Infinities and NaN among the values reach the rows that see them, in their columns, and no others: neither
     earlier queries nor later ones that a window keeps from them, in one tile with those that do."""
     page, lengths, queries = 16, [300, 260, 40], [300, 90, 40]
-    inputs = make_inputs(59, lengths=lengths, queries=queries, heads=8, kv=2, d=d, page=page, fp8=fp8)
+    inputs = make_inputs(59, lengths=lengths, queries=queries, heads=heads, kv=2, d=d, page=page, fp8=fp8)
     values = inputs["v_cache"]
     spots = [(0, 100, 3, math.inf), (0, 101, 7, math.nan), (0, 40, d - 1, -math.inf), (0, 1, 5, math.inf),
              (0, 2, 5, -math.inf), (1, 200, 0, math.nan), (1, 259, 33, -math.inf), (2, 39, 1, math.inf)]
