@@ -123,7 +123,9 @@ mhc_status_t check_cache(mhc_attention_t *a, int pages, const void *k, int64_t k
   return check_strides(msg, strides);
 }
 
-size_t counter_bytes(const mhc_attention_t *a) { return size_t(8) * a->sm_count * sizeof(unsigned int); }
+// two CTAs an SM at most; two sets of counters (attend_many's tiles)
+int counter_ctas(const mhc_attention_t *a) { return 2 * a->sm_count; }
+size_t counter_bytes(const mhc_attention_t *a) { return size_t(2) * 3 * counter_ctas(a) * sizeof(unsigned int); }
 
 void release(mhc_attention_t *a) {
   if (a->turns) cudaFree(a->turns);
@@ -272,6 +274,12 @@ mhc_status_t mhc_attention_attend(mhc_attention_t *a, const mhc_attention_attend
   if (g->table_width < 1) return fail(msg, MHC_ERR_INVALID_ARG, "table_width must be positive");
   if (int64_t(g->table_width) * c.page_size > (1 << 30))
     return fail(msg, MHC_ERR_UNSUPPORTED, "a row of the page table holds more than 2^30 positions");
+  // places on the kernels' line (attend_join.cuh), of what the call may hold at most
+  const bool one = !g->q_starts && c.heads / c.kv_heads <= ATTEND_ONE_GROUP;
+  const int64_t positions = int64_t(g->table_width) * c.page_size;
+  const int64_t items = one ? g->sequences : g->sequences + g->tokens / (2 * (128 / (c.heads / c.kv_heads)));
+  if (items * c.kv_heads > INT32_MAX / (one ? 2 + positions / 64 : 6 + positions / 128))
+    return fail(msg, MHC_ERR_UNSUPPORTED, "tokens, sequences, kv_heads and table_width are too large together");
   mhc_status_t st = check_cache(a, g->pages, g->k_cache, g->k_page_stride, g->v_cache, g->v_page_stride, g->k_scales,
                                 g->v_scales);
   if (st != MHC_OK) return st;
@@ -318,9 +326,9 @@ mhc_status_t mhc_attention_attend(mhc_attention_t *a, const mhc_attention_attend
   p.lse = g->lse;
   p.parts = a->parts;
   p.counters = a->counters;
+  p.counter_ctas = counter_ctas(a);
   p.err = a->err;
   const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
-  const bool one = !g->q_starts && c.heads / c.kv_heads <= ATTEND_ONE_GROUP;
   return launched(a, one ? launch_attend_one(p, a->sm_count, on) : launch_attend_many(p, a->sm_count, on), "attend");
 }
 

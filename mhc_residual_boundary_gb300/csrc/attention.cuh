@@ -43,9 +43,10 @@ struct AttendParams {
   uint16_t *output;
   float *lse;                // may be null
   // scratch of the handle: parts of rows that several CTAs work on, and counters of
-  // the parts that are there (zero between calls), eight for each CTA
+  // the parts that are there (zero between calls), see attend_join.cuh
   float *parts;
   unsigned int *counters;
+  int counter_ctas;          // CTAs that there are counters for
   unsigned int *err;
   // set by the launcher of attend_many
   int tile_queries;          // queries of a tile

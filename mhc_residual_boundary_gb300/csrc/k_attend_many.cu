@@ -8,8 +8,7 @@
 // an item sees is not read.  The call's units form one line, sequence after sequence,
 // head after head, item after item, which is divided evenly over one CTA an SM: long
 // prompts and few rows over a long cache use every SM alike.  An item that lies in
-// several CTAs' parts goes to scratch; the CTA that comes last joins the parts in their
-// order, so that the bits do not depend on it.
+// several CTAs' parts goes to scratch and is joined (attend_join.cuh).
 //
 // A CTA's warps:
 //  0-3, 4-7  softmax of tile A, of tile B: a thread has a row.  S = Q K^T comes from
@@ -28,6 +27,7 @@
 //            make of their rows.  The scales go to the columns of S and of P.
 #include <algorithm>
 
+#include "attend_join.cuh"
 #include "attention.cuh"
 #include "device_common.cuh"
 #include "sublayer_tc.cuh"
@@ -38,6 +38,7 @@ namespace {
 constexpr int KEYS = 128;            // positions of a unit
 constexpr int ROWS = 128;            // rows of a tile
 constexpr int INFOS = 8;             // units whose notes are kept
+constexpr int CUT = 2;               // places that a cut through all rows costs besides EXTRA + 1
 constexpr int SEGMENTS = 4;          // the same of segments: queries of two are there at most, beside the one that is written out
 constexpr int READY = 4;             // units whose values may be looked through
 constexpr float GROWTH = 8.f;        // log2 of what P may reach
@@ -92,6 +93,7 @@ struct Item {
   int position;          // of the first query (may be negative)
   int sink_end, sink_units, first, end, units;   // positions [0, sink_end) and [first, end), in units
   __device__ __forceinline__ int places() const;
+  __device__ __forceinline__ int cost(int group) const;
 };
 
 struct Control {
@@ -103,9 +105,11 @@ struct Control {
   uint32_t tmem;
   int abort;
   int issued, k_issued, q_issued;  // copies into the ring (8-bit cache: of values), of keys, of queries
-  int64_t warp_total[16];
+  int warp_total[16];
   Item begin;
-  int begin_place;
+  int begin_place, bounds[2];
+  Join joins[4];         // of the first and last item of the part, either tile
+  int join_count, join_flag;
 };
 
 template <int D, bool FP8>
@@ -159,6 +163,8 @@ __device__ __forceinline__ bool next_item(const AttendParams &p, Item &it) {
 }
 
 __device__ __forceinline__ int Item::places() const { return units > 0 ? EXTRA + units : 0; }
+// Places that a cut inside it costs: by its rows.
+__device__ __forceinline__ int Item::cost(int group) const { return EXTRA + 1 + CUT * (count[0] + count[1]) * group / (2 * ROWS); }
 
 struct Unit {
   int key0, end;         // positions [key0, key0 + KEYS), those before `end` there
@@ -183,11 +189,6 @@ __device__ __forceinline__ bool whole(const AttendParams &p, const Item &it, con
          (!p.window || u.key0 >= to - p.window + 1 || u.key0 + KEYS <= p.sinks);
 }
 
-// A CTA's part of the line.
-struct Line {
-  int64_t begin, end, total, grid;
-};
-
 struct Ring {
   uint32_t at = 0, phase = 0;
   __device__ __forceinline__ void next(int n) {
@@ -204,21 +205,21 @@ struct Segments {
   Item it;
   int at;                // place in the item that the part begins (or goes on) at
   int from, to;
-  int64_t left;          // places of the part that are left
-  __device__ __forceinline__ Segments(const AttendParams &p, const Control &c, const Line &line)
-      : it(c.begin), at(c.begin_place), left(line.end - line.begin) {
+  int left, end;         // places of the part that are left, its end on the line
+  __device__ __forceinline__ Segments(const AttendParams &p, const Control &c)
+      : it(c.begin), at(c.begin_place), left(c.bounds[1] - c.bounds[0]), end(c.bounds[1]) {
     cut(p);
   }
   __device__ __forceinline__ void cut(const AttendParams &p) {
     while (left > 0) {
       from = max(at - EXTRA, 0);
-      to = int(min(int64_t(it.units), at - EXTRA + left));
+      to = min(it.units, at - EXTRA + left);
       if (to > from) return;
       advance(p);
     }
   }
   __device__ __forceinline__ void advance(const AttendParams &p) {
-    left -= min(left, int64_t(EXTRA + it.units - at));
+    left -= min(left, EXTRA + it.units - at);
     at = 0;
     if (left > 0 && !next_item(p, it)) left = 0;
   }
@@ -226,8 +227,8 @@ struct Segments {
     advance(p);
     cut(p);
   }
-  // The place of the item's first unit on the line.
-  __device__ __forceinline__ int64_t first(const Line &line) const { return line.end - left - at + EXTRA; }
+  // The item's first place on the line.
+  __device__ __forceinline__ int first() const { return end - left - at; }
 };
 
 // -------------------------------------------------------------- tensor cores
@@ -407,8 +408,6 @@ __device__ __forceinline__ float split_queries(unsigned char *tile, int row) {
   }
   return e2 == 255 ? NAN : __uint_as_float(uint32_t(127 + e - 7) << 23);
 }
-
-constexpr int part_floats(int dim) { return (dim + 2) * ROWS; }   // of one tile: [dim][row], maxima, sums
 
 template <int D, bool FP8>
 __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned char *smem, Control &c, uint32_t tmem, int X) {
@@ -611,10 +610,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     float *lse = p.lse ? p.lse + token * p.heads + seg.h * group + head : nullptr;
     const float inverse = sum_now != 0.f ? 1.f / sum_now : 0.f;
     const int cta0 = seg.cta0, cta1 = seg.cta1;
-    auto part = [&](int cta) {
-      return p.parts + (int64_t(2 * cta + (cta == cta0)) * 2 + X) * part_floats(D);
-    };
-    float *mine = part(blockIdx.x);
+    float *const part = p.parts + int64_t((2 * blockIdx.x + (int(blockIdx.x) == cta0)) * 2 + X) * part_floats(ROWS, D);
     // not unrolled: code that runs once an item comes from far, line after line
 #pragma unroll 1
     for (int k = 0; k < D / 32; ++k) {
@@ -637,9 +633,14 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = inverse == 0.f ? 0.f : v[i] * inverse;
         store32(rows, k * 32, lane, v);
-      } else if (had && live) {
+      } else if (live) {
+        if (!had) {   // saw nothing
 #pragma unroll
-        for (int i = 0; i < 32; ++i) mine[(k * 32 + i) * ROWS + tid] = v[i];
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<float4 *>(part + tid * D + k * 32 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     }
     poisoned = false;
@@ -650,43 +651,20 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     }
     tc::fence_before_sync();
     if (live) {
-      mine[D * ROWS + tid] = had ? top_now : -INFINITY;
-      mine[(D + 1) * ROWS + tid] = sum_now;
+      const float m = had ? top_now * scale : -INFINITY;
+      *reinterpret_cast<float4 *>(part + ROWS * D + tid * 4) = make_float4(m, sum_now, m, 0.f);
     }
-    // a warp's rows are joined by the same warp of the CTA that comes last
+    // who writes the last part of sixteen joins them, once there is no other work
     __threadfence();
     __syncwarp();
-    unsigned int *counter = p.counters + (2 * cta0 + X) * 4 + warp;
-    unsigned int before = 0;
-    if (lane == 0) before = atomicAdd(counter, 1u);
-    if (__shfl_sync(0xffffffffu, before, 0) != unsigned(cta1 - cta0)) continue;
-    __threadfence();
-    if (lane == 0) *counter = 0;
-    float all = -INFINITY, total = 0.f;
-    for (int k = cta0; k <= cta1 && live; ++k) all = fmaxf(all, __ldcg(part(k) + D * ROWS + tid));
-    const float b = all == -INFINITY ? 0.f : all;
-    for (int k = cta0; k <= cta1 && live; ++k)
-      total += __ldcg(part(k) + (D + 1) * ROWS + tid) * exp2_fast((__ldcg(part(k) + D * ROWS + tid) - b) * scale);
-    const float f = total != 0.f ? 1.f / total : 0.f;
-#pragma unroll 1
-    for (int k = 0; k < D; k += 32) {
-      float v[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.f;
-      for (int q = cta0; q <= cta1 && live; ++q) {
-        const float *from = part(q);
-        const float m = __ldcg(from + D * ROWS + tid);
-        if (m == -INFINITY) continue;   // saw nothing: it has no output
-        const float w = exp2_fast((m - b) * scale);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += __ldcg(from + (k + i) * ROWS + tid) * w;
+    if (lane == 0) {
+      const int join_group = (int(blockIdx.x) - cta0) / JOIN_WIDTH;
+      unsigned int *counter = JoinCounters{p.counters + 3 * p.counter_ctas * X, p.counter_ctas}.of_group(cta0, join_group);
+      if (atomicAdd(counter, 1u) == unsigned(4 * join_group_size(cta0, cta1, join_group) - 1)) {
+        *counter = 0;
+        c.joins[atomicAdd(&c.join_count, 1)] = {int(seg.token) + X * p.tile_queries, seg.h, seg.count[X] << 1 | X, cta0, cta1, join_group};
       }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= f;
-      store32(rows, k, lane, v);
     }
-    if (live && lse) *lse = total != 0.f ? (b * scale + log2f(total)) * 0.69314718056f : -INFINITY;
   }
 }
 
@@ -715,7 +693,7 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
     return there ? page : -1;
   };
   uint32_t segment = 0;
-  for (Segments seg(p, c, line); seg.left > 0 && ok; seg.next(p), ++segment) {
+  for (Segments seg(p, c); seg.left > 0 && ok; seg.next(p), ++segment) {
     const Item &it = seg.it;
     int page = look(it, seg.from);
     ok = tc::wait_or_abort(&c.q_empty, q_phase, abort);
@@ -733,9 +711,8 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
       n.from = seg.from;
       n.to = seg.to;
       n.units = it.units;
-      const int64_t at0 = seg.first(line);
-      n.cta0 = int(((at0 + 1) * line.grid - 1) / line.total);
-      n.cta1 = int(((at0 + it.units) * line.grid - 1) / line.total);
+      if (seg.from > 0 || seg.to < it.units)
+        line.owners(seg.first(), it.places(), it.cost(p.heads / p.kv_heads), n.cta0, n.cta1);
     }
     if (lane == 0) {
       const int tiles = it.count[1] > 0 ? 2 : 1;
@@ -1071,7 +1048,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     }
     tc::mbar_init(&c.drain, 1);
     tc::mbar_init_fence();
-    c.abort = c.issued = c.k_issued = c.q_issued = 0;
+    c.abort = c.issued = c.k_issued = c.q_issued = c.join_count = 0;
   }
   if (warp == 9) tc::tmem_alloc(&c.tmem, 512);
   if (warp == 8 && lane == 0) {
@@ -1086,7 +1063,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   // blocks are gone through by their warp
   const int chunk = (p.sequences + T - 1) / T;
   bool bad = false, hidden = false;
-  int64_t mine = 0;
+  int mine = 0;
   for (int i = 0; i < chunk; ++i) {
     const int s = tid * chunk + i;
     Item it;
@@ -1114,12 +1091,12 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
       for (int o = 16; o > 0; o /= 2) n += __shfl_xor_sync(0xffffffffu, n, o);
       if (lane == from) units = n;
     }
-    mine += int64_t(units) * p.kv_heads;
+    mine += units * p.kv_heads;
   }
-  int64_t upto = mine;   // inclusive
+  int upto = mine;   // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
   if (lane == 31) c.warp_total[warp] = upto;
@@ -1129,60 +1106,67 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   const uint32_t tmem = c.tmem;
   Line line;
   line.total = 0;
+#pragma unroll 1
   for (int w = 0; w < T / 32; ++w) {
     if (w < warp) upto += c.warp_total[w];
     line.total += c.warp_total[w];
   }
-  // CTAs that work: no more than there are units, so that each of them has some
-  line.grid = max(int64_t(1), min(int64_t(gridDim.x), line.total));
-  const int64_t cta = min(int64_t(blockIdx.x), line.grid);
-  line.begin = cta * line.total / line.grid;
-  line.end = min(cta + 1, line.grid) * line.total / line.grid;
-  const bool owner = line.begin < line.end && upto - mine <= line.begin && line.begin < upto;
-  if (uint32_t m = __ballot_sync(0xffffffffu, owner)) {
-    // the owner's warp finds the unit: its sequence, head, block
+  line.divide(gridDim.x);
+  const int cta = min(int(blockIdx.x), line.grid);
+  if (tid < 2 && cta + tid >= line.grid) c.bounds[tid] = line.total;   // nobody's place
+#pragma unroll 1
+  for (int k = 1; k >= 0; --k) {   // where this CTA's part ends and where it begins
+    const int place = line.begin(min(cta + k, line.grid));
+    const uint32_t m = __ballot_sync(0xffffffffu, upto - mine <= place && place < upto);
+    if (!m) continue;
+    // the warp that has the place finds its sequence, head, block
     const int from = __ffs(m) - 1;
-    int64_t rest = line.begin - (upto - mine);
-    rest = int64_t(__shfl_sync(0xffffffffu, rest, from));
+    int rest = place - __shfl_sync(0xffffffffu, upto - mine, from);
     bool seen_before = false;
+#pragma unroll 1
     for (int s = (warp * 32 + from) * chunk;; ++s) {
       Item it;
       load_sequence(p, it, s, seen_before);
       int n = 0;
+#pragma unroll 1
       for (int b = lane; b < it.blocks; b += 32) {
         load_block(p, it, b);
         n += it.places();
       }
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) n += __shfl_xor_sync(0xffffffffu, n, o);
-      if (rest >= int64_t(n) * p.kv_heads) {
-        rest -= int64_t(n) * p.kv_heads;
+      if (rest >= n * p.kv_heads) {
+        rest -= n * p.kv_heads;
         continue;
       }
-      it.h = int(rest / n);
-      int in_head = int(rest % n);
+      it.h = rest / n;
+      rest -= it.h * n;
+#pragma unroll 1
       for (int b0 = 0;; b0 += 32) {
         it.units = 0;
         if (b0 + lane < it.blocks) load_block(p, it, b0 + lane);
-        const int mine_here = it.places();
-        int to = mine_here;
+        const int here = it.places();
+        int to = here;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
           const int v = __shfl_up_sync(0xffffffffu, to, o);
           if (lane >= o) to += v;
         }
-        const uint32_t behind = __ballot_sync(0xffffffffu, to > in_head);
+        const uint32_t behind = __ballot_sync(0xffffffffu, to > rest);
         if (behind) {
           if (lane == __ffs(behind) - 1) {
+            const int first = place - (rest - (to - here));
+            c.bounds[k] = line.cut(place, first, here, it.cost(p.heads / p.kv_heads));
+            c.begin_place = c.bounds[k] - first;
             c.begin = it;
-            c.begin_place = in_head - (to - mine_here);
           }
           break;
         }
-        in_head -= __shfl_sync(0xffffffffu, to, 31);
+        rest -= __shfl_sync(0xffffffffu, to, 31);
       }
       break;
     }
+    __syncwarp();
   }
   __syncthreads();
 
@@ -1200,7 +1184,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   }
   if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
 
-  if (line.begin < line.end) {
+  if (c.bounds[0] < c.bounds[1]) {
     if (warp < 8) {
       registers_up<F::R_SOFT>();
       softmax_role<D, FP8>(p, smem, c, tmem, warp / 4);
@@ -1221,6 +1205,26 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   __syncthreads();
   tc::fence_after_sync();
   if (warp == 9) tc::tmem_dealloc(c.tmem, 512);
+  if (!c.abort && warp < 8) {   // those with the most registers
+    const int group = p.heads / p.kv_heads;
+#pragma unroll 1
+    for (int k = 0; k < c.join_count; ++k) {
+      const Join join = c.joins[k];   // s: its first query's row; block: queries and tile
+      const int X = join.block & 1;
+      join_parts<D>(smem, F::CONTROL_AT, tid, 256, [] { asm volatile("bar.sync 1, 256;" ::: "memory"); }, join,
+                    (join.block >> 1) * group, ROWS, JoinCounters{p.counters + 3 * p.counter_ctas * X, p.counter_ctas},
+                    [&](int cta, bool begins) { return p.parts + int64_t((2 * cta + begins) * 2 + X) * part_floats(ROWS, D); },
+                    [&](int row, int col, float all, float n, float, const float4 &o) {
+                      const int64_t token = join.s + row / group;
+                      const int head = join.h * group + row % group;
+                      const float f = n != 0.f ? 1.f / n : 0.f;
+                      *reinterpret_cast<uint2 *>(p.output + token * p.output_stride + int64_t(head) * D + col) =
+                          make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+                      if (p.lse && col == 0) p.lse[token * p.heads + head] = n != 0.f ? ((all == -INFINITY ? 0.f : all) + log2f(n)) * 0.69314718056f : -INFINITY;
+                    },
+                    &c.join_flag);
+    }
+  }
   if (tid == 0 && c.abort) {
     atomicOr(p.err, ATTN_ERR_WAIT);
     // copies in flight land before the CTA's shared memory goes
@@ -1309,7 +1313,7 @@ cudaError_t attend_many_setup() {
 
 cudaError_t attend_stall_copies(int on) { return cudaMemcpyToSymbol(g_stall_copies, &on, sizeof on); }
 
-size_t attend_many_scratch(int sms) { return size_t(4) * sms * part_floats(128) * sizeof(float); }
+size_t attend_many_scratch(int sms) { return size_t(4) * sms * part_floats(ROWS, 128) * sizeof(float); }
 
 cudaError_t launch_attend_many(const AttendParams &p, int sms, cudaStream_t stream) {
   if (p.dim == 128) return p.fp8 ? launch<128, true>(p, sms, stream) : launch<128, false>(p, sms, stream);

@@ -14,8 +14,8 @@
 //    segments' ends.
 //  * Warps work alone, each on its own tiles with its own running maxima, sums and
 //    outputs (heads x head_dim in registers), and meet at a segment's end.
-//  * A segment that is not a whole (sequence, head) goes to scratch; the CTA that
-//    comes last joins the parts, in their order, so that the bits do not depend on it.
+//  * A segment that is not a whole (sequence, head) goes to scratch and is joined with the
+//    others (attend_join.cuh).
 //
 // Products are m16n8k16, turned so that the positions are the 16 rows and the heads
 // the 8 columns (one or two groups of them): S^T = K Q^T and O^T = V^T P^T.  The order of
@@ -27,6 +27,7 @@
 // scale, 2^(x + log2 scale - its own running maximum), so that it uses FP16's upper range.
 #include <algorithm>
 
+#include "attend_join.cuh"
 #include "attention.cuh"
 #include "device_common.cuh"
 
@@ -34,6 +35,8 @@ namespace mhc {
 namespace {
 
 constexpr int EXTRA = 1;   // places on the line that a (sequence, head) takes besides its units
+constexpr int COST = 2;    // places that a cut inside one costs
+static_assert(COST > EXTRA, "a cut has a unit on either side");
 
 template <int D, bool FP8>
 struct One {
@@ -173,11 +176,6 @@ __device__ __forceinline__ void skip_extra(Cursor &c, int &left) {
   left -= n;
 }
 
-// A (sequence, head) whose parts are with the CTAs cta0 .. cta1.
-struct Join {
-  int s, h, cta0, cta1;
-};
-
 // Four elements of a head's output from its sums.
 template <bool FP8>
 __device__ __forceinline__ void store_row4(const AttendParams &p, int s, int head, int col, int dim, float all, float n,
@@ -189,21 +187,6 @@ __device__ __forceinline__ void store_row4(const AttendParams &p, int s, int hea
   if (p.lse && col == 0) p.lse[int64_t(s) * p.heads + head] = n != 0.f ? (b + log2f(n)) * 0.69314718056f : -INFINITY;
 }
 
-// Places of the line's CTA c: `total` divided by `grid`, the rest to the first ones.
-struct Line {
-  unsigned total, grid, each, more;
-  __device__ __forceinline__ unsigned begin(unsigned c) const { return c * each + min(c, more); }
-  __device__ __forceinline__ int cta(unsigned place) const {
-    const unsigned bound = more * (each + 1);
-    return int(place < bound ? place / (each + 1) : more + (place - bound) / each);
-  }
-};
-
-// One part of a (sequence, head) in scratch: [16][D] of output, then [16] of
-// (maximum, sum, maximum of the output's weights, -).
-template <int D>
-constexpr int part_floats() { return 16 * (D + 4); }
-
 template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)) k_attend_one(const AttendParams p) {
   using F = One<D, FP8>;
@@ -212,8 +195,9 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int warp_total[WARPS];
   __shared__ Cursor begin_shared;
+  __shared__ int bounds_shared[2];
   __shared__ Join joins[2];   // of the part's first and last (sequence, head)
-  __shared__ int join_count;
+  __shared__ int join_count, join_flag;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int group = p.heads / p.kv_heads;
   bool bad = false;
@@ -255,13 +239,14 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
     if (w < warp) upto += warp_total[w];
     line.total += warp_total[w];
   }
-  // CTAs that work: no more than there are places, so that each of them has some
-  line.grid = max(1u, min(gridDim.x, line.total));
-  line.each = line.total / line.grid;
-  line.more = line.total - line.each * line.grid;
-  const int begin = int(line.begin(min(blockIdx.x, line.grid))), end = int(line.begin(min(blockIdx.x + 1, line.grid)));
-  if (begin < end && upto - mine <= begin && begin < upto) {
-    int rest = begin - (upto - mine);
+  line.divide(gridDim.x);
+  const int cta = min(int(blockIdx.x), line.grid);
+  if (tid < 2 && cta + tid >= line.grid) bounds_shared[tid] = line.total;   // nobody's place
+#pragma unroll 1
+  for (int k = 1; k >= 0; --k) {   // where this CTA's part ends and where it begins
+    const int place = line.begin(min(cta + k, line.grid));
+    if (upto - mine > place || place >= upto) continue;
+    int rest = place - (upto - mine);
     bool seen_before = false;
     Cursor c;
 #pragma unroll 1
@@ -269,14 +254,18 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
       const int n = places_of(s, c, seen_before);
       if (rest < n * p.kv_heads) {
         c.h = rest / n;
-        c.unit = rest - c.h * n - EXTRA;
+        rest -= c.h * n;
+        const int at = line.cut(place, place - rest, n, COST);
+        c.unit = at - (place - rest) - EXTRA;
+        bounds_shared[k] = at;
         break;
       }
       rest -= n * p.kv_heads;
     }
-    begin_shared = c;
+    if (k == 0) begin_shared = c;
   }
   __syncthreads();
+  const int end = bounds_shared[1];
 
   const uint32_t ring_at = smem_u32(smem + warp * F::STAGES * F::STAGE);
   float *meet = reinterpret_cast<float *>(smem + F::RING);             // [WARPS][PASS][MEET_ROW]
@@ -284,10 +273,12 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
   int *looks = reinterpret_cast<int *>(stats + WARPS * 16) + warp * F::STAGES * 2 * F::KEYS + lane % F::KEYS;
   uint32_t *masks = reinterpret_cast<uint32_t *>(stats + WARPS * 16) + WARPS * F::STAGES * 2 * F::KEYS + warp * F::STAGES;
 
-  Cursor at = begin_shared, ahead = at;
-  int left = end - begin, left_ahead = left;
+  Cursor at = begin_shared, ahead;
+  int left = end - bounds_shared[0], left_ahead;
+  if (left > 0 && at.unit == at.units) next_head<D, FP8>(p, at);
   skip_extra(at, left);
-  skip_extra(ahead, left_ahead);
+  ahead = at;
+  left_ahead = left;
 
   // ---- copies.  A tile is looked up STAGES tiles before its copies are issued: its
   // pages' numbers (lane 16 i has block i's) come by a copy as well, into `looks` with the
@@ -368,6 +359,7 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
     }
   }
 
+  const JoinCounters counters = {p.counters, p.counter_ctas};
   int stage = 0;
   while (left > 0) {
     // ---- a segment: units at.unit .. of (at.s, at.h), as far as this CTA's part goes
@@ -612,9 +604,10 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
     const bool whole = count == at.units;
     // CTAs that have units of this (sequence, head), and where their parts are
     const int place0 = end - left - unit0;   // its first unit on the line
-    const int cta0 = whole ? 0 : line.cta(place0), cta1 = whole ? 0 : line.cta(place0 + at.units - 1);
-    float *parts = p.parts;
-    const int slot = 2 * blockIdx.x + (int(blockIdx.x) == cta0);
+    int cta0 = 0, cta1 = 0;
+    if (!whole) line.owners(place0 - EXTRA, EXTRA + at.units, COST, cta0, cta1);
+    auto part_of = [&](int c, bool begins) { return p.parts + int64_t(2 * c + begins) * part_floats(16, D); };
+    float *const part = part_of(blockIdx.x, int(blockIdx.x) == cta0);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -666,19 +659,22 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
         if (whole) {
           store_row4<FP8>(p, at.s, at.h * group + row, col, D, all, n, all_out, o);
         } else {
-          float *part = parts + int64_t(slot) * part_floats<D>();
           *reinterpret_cast<float4 *>(part + row * D + col) = o;
           if (col == 0) *reinterpret_cast<float4 *>(part + 16 * D + row * 4) = make_float4(all, n, all_out, 0.f);
         }
       }
     }
     if (!whole) {
-      // the CTA that comes last joins the parts, once it has no other work
+      // who writes the last part of sixteen joins them, once there is no other work
       __threadfence();
       __syncthreads();
-      if (tid == 0 && atomicAdd(p.counters + cta0, 1u) == unsigned(cta1 - cta0)) {
-        p.counters[cta0] = 0;
-        joins[join_count++] = {at.s, at.h, cta0, cta1};
+      if (tid == 0) {
+        const int join_group = (int(blockIdx.x) - cta0) / JOIN_WIDTH;
+        unsigned int *counter = counters.of_group(cta0, join_group);
+        if (atomicAdd(counter, 1u) == unsigned(join_group_size(cta0, cta1, join_group) - 1)) {
+          *counter = 0;
+          joins[join_count++] = {at.s, at.h, 0, cta0, cta1, join_group};
+        }
       }
     }
     __syncthreads();   // stats may be written again
@@ -691,61 +687,15 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 
-  // ---- joins: as many parts at a time as the ring has room for, all their reads under
-  // way together (while other CTAs read the cache, a trip to memory takes a microsecond)
+#pragma unroll 1
   for (int k = 0; k < join_count; ++k) {
     const Join join = joins[k];
-    const int pieces = group * (D / 4 + 1), room = F::RING / 16 / pieces;   // of 16 bytes, a part's rows and stats
-    __threadfence();
-    for (int item0 = 0; item0 < group * (D / 4); item0 += THREADS) {
-      const int item = item0 + tid, row = item / (D / 4), col = item % (D / 4);
-      float all = -INFINITY, all_out = -INFINITY, n = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int c0 = join.cta0; c0 <= join.cta1; c0 += room) {
-        const int count = min(room, join.cta1 + 1 - c0);
-        if (item0 == 0 || count < join.cta1 + 1 - join.cta0) {   // else they are there
-          __syncthreads();
-#pragma unroll 4
-          for (int i = tid; i < count * pieces; i += THREADS) {
-            const int c = c0 + i / pieces, piece = i % pieces;
-            const float *from = p.parts + int64_t(2 * c + (c == join.cta0)) * part_floats<D>() +
-                                (piece < group * (D / 4) ? piece * 4 : 16 * D + (piece - group * (D / 4)) * 4);
-            copy16(smem_u32(smem) + i * 16, from, true);
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          __syncthreads();
-        }
-        if (row < group) {
-          const float4 *part = reinterpret_cast<const float4 *>(smem);
-          float now = all, now_out = all_out;
-#pragma unroll 4
-          for (int i = 0; i < count; ++i) {
-            const float4 st = part[i * pieces + group * (D / 4) + row];
-            now = fmaxf(now, st.x);
-            now_out = fmaxf(now_out, st.z);
-          }
-          const float b = now == -INFINITY ? 0.f : now, bo = now_out == -INFINITY ? 0.f : now_out;
-          const float keep = exp2_fast(all_out - bo);
-          n *= exp2_fast(all - b);
-          o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
-#pragma unroll 4
-          for (int i = 0; i < count; ++i) {
-            const float4 st = part[i * pieces + group * (D / 4) + row], v = part[i * pieces + row * (D / 4) + col];
-            n += st.y * exp2_fast(st.x - b);
-            const float f = exp2_fast(st.z - bo);
-            o.x += v.x * f;
-            o.y += v.y * f;
-            o.z += v.z * f;
-            o.w += v.w * f;
-          }
-          all = now;
-          all_out = now_out;
-        }
-      }
-      if (row < group) store_row4<FP8>(p, join.s, join.h * group + row, col * 4, D, all, n, all_out, o);
-    }
-    __syncthreads();
+    join_parts<D>(smem, F::RING, tid, THREADS, [] { __syncthreads(); }, join, group, 16, counters,
+                  [&](int c, bool begins) { return p.parts + int64_t(2 * c + begins) * part_floats(16, D); },
+                  [&](int row, int col, float all, float n, float all_out, const float4 &o) {
+                    store_row4<FP8>(p, join.s, join.h * group + row, col, D, all, n, all_out, o);
+                  },
+                  &join_flag);
   }
   if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
 }
@@ -792,7 +742,7 @@ cudaError_t attend_one_setup() {
   return e;
 }
 
-size_t attend_one_scratch(int sms) { return size_t(2) * 2 * sms * part_floats<128>() * sizeof(float); }
+size_t attend_one_scratch(int sms) { return size_t(2) * 2 * sms * part_floats(16, 128) * sizeof(float); }
 
 cudaError_t launch_attend_one(const AttendParams &p, int sms, cudaStream_t stream) {
   if (p.dim == 128) return p.fp8 ? launch_groups<128, true>(p, sms, stream) : launch_groups<128, false>(p, sms, stream);

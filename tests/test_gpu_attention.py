@@ -130,6 +130,22 @@ def test_scale_and_large_scores(handles, several, fp8):
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("several", [False, True])
+def test_one_row_set_in_many_parts(handles, several, fp8):
+    """A long sequence of one kv head: every CTA has a part of it, and the parts are joined in two steps."""
+    lengths, queries = ([40000, 7], [3, 2]) if several else ([40000], None)
+    inputs = make_inputs(71, lengths=lengths, queries=queries, heads=8, kv=1, d=128, page=128, fp8=fp8)
+    a, out = attend(handles, inputs, 128)
+    check(out, inputs, page=128)
+    again = attend(handles, inputs, 128)[1]
+    assert all(torch.equal(out[n], again[n]) for n in out)
+    inputs = make_inputs(72, lengths=[90000], queries=[130] if several else None, heads=16, kv=1, d=64, page=64, fp8=fp8)
+    a, out = attend(handles, inputs, 64)
+    check(out, inputs, page=64)
+    a.check_errors()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("several", [False, True])
 def test_hidden_places_hold_anything(handles, several, fp8):
     """NaN and infinities behind a sequence's end, before its window, in pages of nobody and in rows of q_starts'
     other sequences change nothing."""
