@@ -24,7 +24,8 @@ namespace mhc {
 constexpr int JOIN_WIDTH = 16;   // parts that are joined at a time
 
 // A CTA's parts: two (of what began with an earlier CTA, of what begins with it), each
-// [rows][dim] and then [rows][4] floats.
+// [dim / 4][rows][4] floats and then [rows][4]: threads that have a row each write whole
+// lines.
 constexpr int part_floats(int rows, int dim) { return rows * (dim + 4); }
 
 // `total` places over `grid` CTAs: `each`, and one more for the first `more`.
@@ -101,36 +102,37 @@ __device__ __forceinline__ void join_parts(unsigned char *smem, int room, int ti
   __threadfence();
 #pragma unroll 1
   for (;;) {
-    const int pass = max(1, min(rows, room / (count * (D + 4) * 4)));   // rows at a time
+    // rows at a time; a part in shared memory is [dim / 4 + 1][n + 1][4], the last of the rows
+    // of stats
+    const int pass = max(1, min(rows, room / (count * (D + 4) * 4) - 1));
 #pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += pass) {
-      const int n = min(pass, rows - r0), pieces = n * (D / 4 + 1);   // of 16 bytes, a part's
+      const int n = min(pass, rows - r0), size = (D / 4 + 1) * (n + 1);   // of 16 bytes
       sync();
-#pragma unroll 1
-      for (int q = 0; q < count; ++q) {
-        const int c = first + q * step;
-        const float *from = part(c, c == join.cta0);
-#pragma unroll 2
-        for (int i = tid; i < pieces; i += threads)
-          join_copy16(to + (q * pieces + i) * 16, i < n * (D / 4) ? from + r0 * D + i * 4 : from + max_rows * D + (r0 + i - n * (D / 4)) * 4);
+      const int shift = 32 - __clz(n - 1);   // rows to a power of two
+#pragma unroll 4
+      for (int i = tid; i < count * (D / 4 + 1) << shift; i += threads) {
+        const int q = (i >> shift) / (D / 4 + 1), col = (i >> shift) % (D / 4 + 1), row = i & ((1 << shift) - 1), c = first + q * step;
+        if (row < n)
+          join_copy16(to + (q * size + col * (n + 1) + row) * 16, part(c, c == join.cta0) + (col * max_rows + r0 + row) * 4);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       sync();
 #pragma unroll 1
       for (int item = tid; item < n * (D / 4); item += threads) {
-        const int row = item / (D / 4), col = item % (D / 4) * 4;
-        const float4 *stats = there + n * (D / 4) + row, *values = there + item;
+        const int row = item / (D / 4), col = item % (D / 4);
+        const float4 *stats = there + D / 4 * (n + 1) + row, *values = there + col * (n + 1) + row;
         float all = -INFINITY, all_out = -INFINITY, sum = 0.f;
 #pragma unroll 2
         for (int q = 0; q < count; ++q) {
-          all = fmaxf(all, stats[q * pieces].x);
-          all_out = fmaxf(all_out, stats[q * pieces].z);
+          all = fmaxf(all, stats[q * size].x);
+          all_out = fmaxf(all_out, stats[q * size].z);
         }
         const float b = all == -INFINITY ? 0.f : all, bo = all_out == -INFINITY ? 0.f : all_out;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
         for (int q = 0; q < count; ++q) {
-          const float4 st = stats[q * pieces], v = values[q * pieces];
+          const float4 st = stats[q * size], v = values[q * size];
           sum += st.y * join_exp2(st.x - b);
           const float f = join_exp2(st.z - bo);
           o.x += v.x * f;
@@ -139,11 +141,11 @@ __device__ __forceinline__ void join_parts(unsigned char *smem, int room, int ti
           o.w += v.w * f;
         }
         if (last) {
-          final(r0 + row, col, all, sum, all_out, o);
+          final(r0 + row, col * 4, all, sum, all_out, o);
         } else {
-          float *mine = part(first, first == join.cta0) + (r0 + row) * D + col;
-          *reinterpret_cast<float4 *>(mine) = o;
-          if (col == 0) *reinterpret_cast<float4 *>(mine - row * D - r0 * D + max_rows * D + (r0 + row) * 4) = make_float4(all, sum, all_out, 0.f);
+          float *mine = part(first, first == join.cta0) + (r0 + row) * 4;
+          *reinterpret_cast<float4 *>(mine + col * max_rows * 4) = o;
+          if (col == 0) *reinterpret_cast<float4 *>(mine + D * max_rows) = make_float4(all, sum, all_out, 0.f);
         }
       }
     }

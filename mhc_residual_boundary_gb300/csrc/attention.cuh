@@ -51,6 +51,7 @@ struct AttendParams {
   // set by the launcher of attend_many
   int tile_queries;          // queries of a tile
   uint32_t all_pages;        // a bit for each page of a unit
+  bool whole_sectors;        // rows of output begin at multiples of 32 bytes
 };
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);

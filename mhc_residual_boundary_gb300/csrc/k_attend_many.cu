@@ -38,7 +38,7 @@ namespace {
 constexpr int KEYS = 128;            // positions of a unit
 constexpr int ROWS = 128;            // rows of a tile
 constexpr int INFOS = 8;             // units whose notes are kept
-constexpr int CUT = 2;               // places that a cut through all rows costs besides EXTRA + 1
+constexpr int CUT = 5;               // places that a cut through all rows costs besides EXTRA + 1
 constexpr int SEGMENTS = 4;          // the same of segments: queries of two are there at most, beside the one that is written out
 constexpr int READY = 4;             // units whose values may be looked through
 constexpr float GROWTH = 8.f;        // log2 of what P may reach
@@ -60,7 +60,7 @@ struct Many {
   static constexpr int SCALES_AT = K_AT + KSLOTS * RAW; // [INFOS][keys, values][KEYS]
   static constexpr int CONTROL_AT = SCALES_AT + (FP8 ? INFOS * 2 * KEYS * 4 : 0);
   // registers a thread: at the launch, then the softmax warps', the others'
-  static constexpr int R_START = 168, R_SOFT = 208, R_REST = 88;
+  static constexpr int R_START = 168, R_SOFT = 200, R_REST = 104;
   static_assert(256 * R_SOFT + 128 * R_REST <= THREADS * R_START, "registers of a CTA");
   static_assert((FP8 ? SLOTS + RAWS : SLOTS / 2) + 2 <= INFOS + 2 && (FP8 || SLOTS / 2 <= READY) && KSLOTS + 2 <= INFOS,
                 "notes outlive their unit");
@@ -327,36 +327,24 @@ __device__ __noinline__ void read_poison(const AttendParams &p, int s, int h, in
     }
 }
 
-// 32 columns of this lane's row of output from column c0 on.  Four lanes exchange
-// their rows' 16-byte pieces (two rounds of a transposition), so that they write 64
-// neighbouring bytes: rows[k] is the row of lane (lane & ~3) + k, null if it has none.
-__device__ __forceinline__ void store32(uint16_t *const (&rows)[4], int c0, int lane, const float (&v)[32]) {
-  uint4 piece[4];
+// 32 columns of a row of output, 32 bytes at a time: whole sectors of memory, without an
+// exchange between the lanes (that, for 64 neighbouring bytes of four lanes, took 214 us
+// for the 200 of 4096 queries of 48 heads).  Rows that begin at an odd multiple of 16 bytes take halves.
+__device__ __forceinline__ void store32(uint16_t *out, bool whole_sectors, const float (&v)[32]) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float *x = v + 8 * k;
-    piece[k] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  for (int i = 0; i < 32; i += 16) {
+    uint32_t r[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = pack_bf16x2(v[i + 2 * k], v[i + 2 * k + 1]);
+    if (whole_sectors) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + i), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                   "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                   : "memory");
+    } else {
+      st_vec(out + i, make_uint4(r[0], r[1], r[2], r[3]));
+      st_vec(out + i + 8, make_uint4(r[4], r[5], r[6], r[7]));
+    }
   }
-#pragma unroll
-  for (int bit = 1; bit <= 2; bit <<= 1)
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (!(k & bit)) {
-        const bool odd = lane & bit;
-        uint4 &lo = piece[k], &hi = piece[k | bit];
-        auto swap = [&](uint32_t &x, uint32_t &y) {
-          const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? x : y, bit);
-          if (odd) x = got;
-          else y = got;
-        };
-        swap(lo.x, hi.x);
-        swap(lo.y, hi.y);
-        swap(lo.z, hi.z);
-        swap(lo.w, hi.w);
-      }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (rows[k]) st_vec(rows[k] + c0 + lane % 4 * 8, piece[k]);
 }
 
 // A row of queries in two E4M3 pieces, for products with 8-bit keys: y = q 2^(7 - e) with
@@ -602,11 +590,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     }
     const bool item_whole = seg.from == 0 && seg.to == seg.units;
     const int64_t token = seg.token + X * p.tile_queries + query;
-    const uint64_t out = live ? reinterpret_cast<uint64_t>(p.output + token * p.output_stride + (int64_t(seg.h) * group + head) * D) : 0;
-    uint16_t *rows[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      rows[k] = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, out, (lane & ~3) + k));
+    uint16_t *out = p.output + token * p.output_stride + (int64_t(seg.h) * group + head) * D;
     float *lse = p.lse ? p.lse + token * p.heads + seg.h * group + head : nullptr;
     const float inverse = sum_now != 0.f ? 1.f / sum_now : 0.f;
     const int cta0 = seg.cta0, cta1 = seg.cta1;
@@ -632,7 +616,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       if (item_whole) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = inverse == 0.f ? 0.f : v[i] * inverse;
-        store32(rows, k * 32, lane, v);
+        if (live) store32(out + k * 32, p.whole_sectors, v);
       } else if (live) {
         if (!had) {   // saw nothing
 #pragma unroll
@@ -640,7 +624,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         }
 #pragma unroll
         for (int i = 0; i < 32; i += 4)
-          *reinterpret_cast<float4 *>(part + tid * D + k * 32 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          *reinterpret_cast<float4 *>(part + ((k * 32 + i) * ROWS / 4 + tid) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     }
     poisoned = false;
@@ -1113,18 +1097,21 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   }
   line.divide(gridDim.x);
   const int cta = min(int(blockIdx.x), line.grid);
-  if (tid < 2 && cta + tid >= line.grid) c.bounds[tid] = line.total;   // nobody's place
-#pragma unroll 1
-  for (int k = 1; k >= 0; --k) {   // where this CTA's part ends and where it begins
-    const int place = line.begin(min(cta + k, line.grid));
-    const uint32_t m = __ballot_sync(0xffffffffu, upto - mine <= place && place < upto);
-    if (!m) continue;
-    // the warp that has the place finds its sequence, head, block
-    const int from = __ffs(m) - 1;
-    int rest = place - __shfl_sync(0xffffffffu, upto - mine, from);
+  // warp k finds where this CTA's part begins (0), where it ends (1): the owner of the
+  // place tells it what lies before
+  const int place0 = line.begin(cta), place1 = line.begin(min(cta + 1, line.grid));
+  const int owner0 = __syncthreads_count(upto <= place0), owner1 = __syncthreads_count(upto <= place1);
+  if (tid == owner0) c.bounds[0] = upto - mine;
+  if (tid == owner1) c.bounds[1] = upto - mine;
+  __syncthreads();
+  const int place = warp ? place1 : place0;
+  if (warp < 2 && place >= line.total) c.bounds[warp] = line.total;
+  if (warp < 2 && place < line.total) {
+    int rest = place - c.bounds[warp];
+    __syncwarp();
     bool seen_before = false;
 #pragma unroll 1
-    for (int s = (warp * 32 + from) * chunk;; ++s) {
+    for (int s = (warp ? owner1 : owner0) * chunk;; ++s) {
       Item it;
       load_sequence(p, it, s, seen_before);
       int n = 0;
@@ -1156,9 +1143,12 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
         if (behind) {
           if (lane == __ffs(behind) - 1) {
             const int first = place - (rest - (to - here));
-            c.bounds[k] = line.cut(place, first, here, it.cost(p.heads / p.kv_heads));
-            c.begin_place = c.bounds[k] - first;
-            c.begin = it;
+            const int at = line.cut(place, first, here, it.cost(p.heads / p.kv_heads));
+            c.bounds[warp] = at;
+            if (warp == 0) {
+              c.begin_place = at - first;
+              c.begin = it;
+            }
           }
           break;
         }
@@ -1166,7 +1156,6 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
       }
       break;
     }
-    __syncwarp();
   }
   __syncthreads();
 
@@ -1258,6 +1247,7 @@ cudaError_t launch(const AttendParams &args, int sms, cudaStream_t stream) {
   AttendParams p = args;
   const int group = p.heads / p.kv_heads, page = 1 << p.page_shift;
   p.tile_queries = ROWS / group;
+  p.whole_sectors = reinterpret_cast<uintptr_t>(p.output) % 32 == 0 && p.output_stride % 16 == 0;
   p.all_pages = uint32_t((uint64_t(1) << (KEYS >> p.page_shift)) - 1);
   const int size = FP8 ? 1 : 2;
   CUtensorMap tm_q, tm_k, tm_v;

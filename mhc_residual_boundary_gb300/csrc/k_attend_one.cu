@@ -241,28 +241,36 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
   }
   line.divide(gridDim.x);
   const int cta = min(int(blockIdx.x), line.grid);
-  if (tid < 2 && cta + tid >= line.grid) bounds_shared[tid] = line.total;   // nobody's place
+  // thread k finds where this CTA's part begins (0), where it ends (1): the owner of the
+  // place tells it what lies before
+  const int place0 = line.begin(cta), place1 = line.begin(min(cta + 1, line.grid));
+  const int owner0 = __syncthreads_count(upto <= place0), owner1 = __syncthreads_count(upto <= place1);
+  if (tid == owner0) bounds_shared[0] = upto - mine;
+  if (tid == owner1) bounds_shared[1] = upto - mine;
+  __syncthreads();
+  if (tid < 2) {
+    const int place = tid ? place1 : place0;
+    if (place >= line.total) {
+      bounds_shared[tid] = line.total;
+    } else {
+      int rest = place - bounds_shared[tid];
+      bool seen_before = false;
+      Cursor c;
 #pragma unroll 1
-  for (int k = 1; k >= 0; --k) {   // where this CTA's part ends and where it begins
-    const int place = line.begin(min(cta + k, line.grid));
-    if (upto - mine > place || place >= upto) continue;
-    int rest = place - (upto - mine);
-    bool seen_before = false;
-    Cursor c;
-#pragma unroll 1
-    for (int s = tid * chunk;; ++s) {
-      const int n = places_of(s, c, seen_before);
-      if (rest < n * p.kv_heads) {
-        c.h = rest / n;
-        rest -= c.h * n;
-        const int at = line.cut(place, place - rest, n, COST);
-        c.unit = at - (place - rest) - EXTRA;
-        bounds_shared[k] = at;
-        break;
+      for (int s = (tid ? owner1 : owner0) * chunk;; ++s) {
+        const int n = places_of(s, c, seen_before);
+        if (rest < n * p.kv_heads) {
+          c.h = rest / n;
+          rest -= c.h * n;
+          const int at = line.cut(place, place - rest, n, COST);
+          c.unit = at - (place - rest) - EXTRA;
+          bounds_shared[tid] = at;
+          break;
+        }
+        rest -= n * p.kv_heads;
       }
-      rest -= n * p.kv_heads;
+      if (tid == 0) begin_shared = c;
     }
-    if (k == 0) begin_shared = c;
   }
   __syncthreads();
   const int end = bounds_shared[1];
@@ -603,9 +611,9 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
     // ---- the warps meet: rows PASS at a time, weighted to the common maximum
     const bool whole = count == at.units;
     // CTAs that have units of this (sequence, head), and where their parts are
-    const int place0 = end - left - unit0;   // its first unit on the line
+    const int unit_place = end - left - unit0;   // its first unit on the line
     int cta0 = 0, cta1 = 0;
-    if (!whole) line.owners(place0 - EXTRA, EXTRA + at.units, COST, cta0, cta1);
+    if (!whole) line.owners(unit_place - EXTRA, EXTRA + at.units, COST, cta0, cta1);
     auto part_of = [&](int c, bool begins) { return p.parts + int64_t(2 * c + begins) * part_floats(16, D); };
     float *const part = part_of(blockIdx.x, int(blockIdx.x) == cta0);
 #pragma unroll
@@ -659,8 +667,8 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
         if (whole) {
           store_row4<FP8>(p, at.s, at.h * group + row, col, D, all, n, all_out, o);
         } else {
-          *reinterpret_cast<float4 *>(part + row * D + col) = o;
-          if (col == 0) *reinterpret_cast<float4 *>(part + 16 * D + row * 4) = make_float4(all, n, all_out, 0.f);
+          *reinterpret_cast<float4 *>(part + (col / 4 * 16 + row) * 4) = o;
+          if (col == 0) *reinterpret_cast<float4 *>(part + (D / 4 * 16 + row) * 4) = make_float4(all, n, all_out, 0.f);
         }
       }
     }

@@ -274,6 +274,22 @@ def test_strides(handles):
         assert (wide[:, heads] == 5.0).all()
 
 
+@pytest.mark.parametrize("first, row", [(8, 256), (0, 264), (8, 264)])
+def test_output_rows_at_odd_multiples_of_16_bytes(handles, first, row):
+    heads, kv, d, page = 2, 1, 128, 16
+    for queries in (None, [200, 9]):
+        inputs = make_inputs(43, lengths=[333, 50], queries=queries, heads=heads, kv=kv, d=d, page=page, fp8=False)
+        t = inputs["q"].shape[0]
+        flat = torch.full((t * row + 16,), 5.0, dtype=BF16, device="cuda")
+        assert flat.data_ptr() % 32 == 0
+        output = flat[first:first + t * row].view(t, row)[:, :heads * d].unflatten(1, (heads, d))
+        out = handles(heads, kv, d, page, False).attend(inputs, {"output": output})
+        check(out, inputs, page=page)
+        untouched = torch.ones_like(flat, dtype=torch.bool)
+        untouched[first:first + t * row].view(t, row)[:, :heads * d] = False
+        assert (flat[untouched] == 5.0).all()
+
+
 def test_rows_behind_the_last_sequence_stay(handles):
     inputs = make_inputs(19, lengths=[100, 50], queries=[30, 7], heads=4, kv=2, d=64, page=16, fp8=False)
     want = define(inputs, page=16)
