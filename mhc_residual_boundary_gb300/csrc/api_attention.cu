@@ -255,7 +255,7 @@ mhc_status_t mhc_attention_append(mhc_attention_t *a, const mhc_attention_append
   p.keys = {g->k_cache, g->k_page_stride, g->k_scales};
   p.values = {g->v_cache, g->v_page_stride, g->v_scales};
   p.err = a->err;
-  return launched(a, launch_append(p, reinterpret_cast<cudaStream_t>(stream)), "append");
+  return launched(a, launch_append(p, a->sm_count, reinterpret_cast<cudaStream_t>(stream)), "append");
 }
 
 mhc_status_t mhc_attention_attend(mhc_attention_t *a, const mhc_attention_attend_args_t *g, mhc_stream_t stream) {

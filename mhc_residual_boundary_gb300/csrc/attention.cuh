@@ -54,7 +54,7 @@ struct AttendParams {
   bool whole_sectors;        // rows of output begin at multiples of 32 bytes
 };
 
-cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
+cudaError_t launch_append(const AppendParams &p, int sms, cudaStream_t stream);
 
 // One query a sequence, up to 16 heads for each kv head.
 constexpr int ATTEND_ONE_GROUP = 16;

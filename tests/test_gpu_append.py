@@ -63,6 +63,10 @@ CASES = [
     (20, 128, 1, 128, 32, 0, False),
     (301, 24, 3, 128, 16, 112, False),
     (64, 9, 9, 64, 16, 48, True),
+    # two and four tokens a CTA, and a last one with fewer
+    (903, 35, 5, 128, 64, 128, False),
+    (1001, 120, 8, 128, 16, 96, True),
+    (6003, 34, 2, 64, 32, 32, False),
 ]
 
 
