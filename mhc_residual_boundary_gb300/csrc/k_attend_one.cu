@@ -35,7 +35,11 @@ namespace mhc {
 namespace {
 
 constexpr int EXTRA = 1;   // places on the line that a (sequence, head) takes besides its units
-constexpr int COST = 2;    // places that a cut inside one costs
+// Places that a cut inside one costs: its parts' way through memory and a join, and with as
+// many (sequence, head) pairs as CTAs the CTA's second beginning, too, which an uneven load
+// is worth.  In us, 8 kv heads of 128, with 2 and with 5: 32 sequences of 300 positions 11.2 and
+// 8.3, of 500 15.6 and 11.4; with few pairs, which only cuts spread, 8 of 1000 9.2 and (with 4) 10.7.
+constexpr int COST = 2, COST_MANY = 5;
 static_assert(COST > EXTRA, "a cut has a unit on either side");
 
 template <int D, bool FP8>
@@ -49,7 +53,7 @@ struct One {
   static constexpr int STAGE = 2 * TILE + (FP8 ? KEYS * 8 : 0);
   static constexpr int STAGES = STAGE > 5000 ? 2 : 4;
   static constexpr int UNIT = WARPS * KEYS;
-  static constexpr int PASS = SM_CTAS == 1 && !FP8 ? 6 : 4;                          // rows that the warps meet over at a time
+  static constexpr int PASS = 8;                          // rows that the warps meet over at a time
   static constexpr int MEET_ROW = D;                      // floats
   static constexpr int RING = WARPS * STAGES * STAGE;
   static constexpr int LOOK = 2 * KEYS * 4;                 // bytes: a tile's page numbers and places
@@ -239,7 +243,12 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
     if (w < warp) upto += warp_total[w];
     line.total += warp_total[w];
   }
-  line.divide(gridDim.x);
+  // Two places a CTA at least with 32 units a pair, four with 64: a join of fewer parts
+  // ends sooner (one kv head of 32768 positions 23.2 us with one, 19.3 with four; 8 of 2000 11.5 and
+  // 9.7 with two; at 16 units one is as good as two).
+  const int pairs = p.sequences * p.kv_heads;
+  line.divide(min(int(gridDim.x), line.total >> (line.total >= 64 * pairs ? 2 : line.total >= 32 * pairs)));
+  const int cost = 2 * pairs >= int(gridDim.x) ? COST_MANY : COST;
   const int cta = min(int(blockIdx.x), line.grid);
   // thread k finds where this CTA's part begins (0), where it ends (1): the owner of the
   // place tells it what lies before
@@ -262,7 +271,7 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
         if (rest < n * p.kv_heads) {
           c.h = rest / n;
           rest -= c.h * n;
-          const int at = line.cut(place, place - rest, n, COST);
+          const int at = line.cut(place, place - rest, n, cost);
           c.unit = at - (place - rest) - EXTRA;
           bounds_shared[tid] = at;
           break;
@@ -613,7 +622,7 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
     // CTAs that have units of this (sequence, head), and where their parts are
     const int unit_place = end - left - unit0;   // its first unit on the line
     int cta0 = 0, cta1 = 0;
-    if (!whole) line.owners(unit_place - EXTRA, EXTRA + at.units, COST, cta0, cta1);
+    if (!whole) line.owners(unit_place - EXTRA, EXTRA + at.units, cost, cta0, cta1);
     auto part_of = [&](int c, bool begins) { return p.parts + int64_t(2 * c + begins) * part_floats(16, D); };
     float *const part = part_of(blockIdx.x, int(blockIdx.x) == cta0);
 #pragma unroll
@@ -625,13 +634,14 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
         if (g == 0) stats[warp * 16 + 8 * n + 2 * t + e] = make_float4(top[n][e], sum[n][e], FP8 ? top_out[n][e] : top[n][e], 0.f);
       }
     for (int r0 = 0; r0 < group; r0 += F::PASS) {
+      const int rows = min(F::PASS, group - r0);
       __syncthreads();   // stats are there; the buffer's last readers are done
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int row = 8 * n + 2 * t + e - r0;
-          if (row < 0 || row >= F::PASS) continue;
+          if (row < 0 || row >= rows) continue;
           // a lane's elements: whole pieces of PIECE, the rows of its tiles in pairs
           constexpr int PIECE = FP8 && D == 128 ? 16 : 8;
           float *m = meet + (warp * F::PASS + row) * F::MEET_ROW + g * PIECE;
@@ -642,9 +652,8 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
           }
         }
       __syncthreads();
-      for (int item = tid; item < F::PASS * (D / 4); item += THREADS) {
+      for (int item = tid; item < rows * (D / 4); item += THREADS) {
         const int row = r0 + item / (D / 4), col = item % (D / 4) * 4;
-        if (row >= group) break;
         float all = -INFINITY, all_out = -INFINITY, n = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
