@@ -546,22 +546,35 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       for (int k = 0; k < 4; ++k) {
         uint32_t (&v)[32] = x[k];
         uint32_t r[16];
+        // (two forms: the test for what is hidden in every unit took 448 us for the 425 of
+        // 3 x 1024 queries of 40 heads over 8000 positions)
+        auto weigh = [&](bool hidden) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float a, b;
-          fma_pair(a, b, v[2 * i], v[2 * i + 1], scale2, base2);
-          a = exp2_fast(a);
-          b = exp2_fast(b);
-          add_pair(sums[i % 2], a, b);
-          if (FP8) {   // the values' scales
-            uint32_t wa = __float_as_uint(a), wb = __float_as_uint(b);
-            mul_pair(wa, wb, *reinterpret_cast<const uint64_t *>(vs + k * 32 + 2 * i));
-            // what is hidden has none
-            a = masked && a == 0.f ? 0.f : __uint_as_float(wa);
-            b = masked && b == 0.f ? 0.f : __uint_as_float(wb);
+          for (int i = 0; i < 16; i += 2) {
+            float w[4];
+            fma_pair(w[0], w[1], v[2 * i], v[2 * i + 1], scale2, base2);
+            fma_pair(w[2], w[3], v[2 * i + 2], v[2 * i + 3], scale2, base2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = exp2_fast(w[e]);
+            add_pair(sums[0], w[0], w[1]);
+            add_pair(sums[1], w[2], w[3]);
+            if (FP8) {   // the values' scales
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(vs + k * 32 + 2 * i);
+              uint32_t u[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(w[e]);
+              mul_pair(u[0], u[1], f.x);
+              mul_pair(u[2], u[3], f.y);
+              // what is hidden has none
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = hidden && w[e] == 0.f ? 0.f : __uint_as_float(u[e]);
+            }
+            r[i] = pack_bf16x2(w[0], w[1]);
+            r[i + 1] = pack_bf16x2(w[2], w[3]);
           }
-          r[i] = pack_bf16x2(a, b);
-        }
+        };
+        if (FP8 && masked) weigh(true);
+        else weigh(false);
         tmem_st<16>(s_at + k * 16, r);
         if (k % 2) {   // half of P is there: its product can begin
           tmem_wait_st();
