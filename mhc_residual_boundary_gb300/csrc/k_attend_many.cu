@@ -37,10 +37,8 @@ namespace {
 
 constexpr int KEYS = 128;            // positions of a unit
 constexpr int ROWS = 128;            // rows of a tile
-constexpr int INFOS = 8;             // units whose notes are kept
+constexpr int INFOS = 8;             // units whose notes are kept, and segments: no more of them can be under way
 constexpr int CUT = 5;               // places that a cut through all rows costs besides EXTRA + 1
-constexpr int SEGMENTS = 4;          // the same of segments: queries of two are there at most, beside the one that is written out
-constexpr int READY = 4;             // units whose values may be looked through
 constexpr float GROWTH = 8.f;        // log2 of what P may reach
 constexpr int EXTRA = 3;             // places on the line that an item takes besides its units, for its beginning and end
 
@@ -62,8 +60,6 @@ struct Many {
   // registers a thread: at the launch, then the softmax warps', the others'
   static constexpr int R_START = 168, R_SOFT = 200, R_REST = 104;
   static_assert(256 * R_SOFT + 128 * R_REST <= THREADS * R_START, "registers of a CTA");
-  static_assert((FP8 ? SLOTS + RAWS : SLOTS / 2) + 2 <= INFOS + 2 && (FP8 || SLOTS / 2 <= READY) && KSLOTS + 2 <= INFOS,
-                "notes outlive their unit");
 };
 
 // Notes of a unit, which the copying warp writes for the others.
@@ -74,7 +70,8 @@ enum : uint32_t {
 struct Info {
   uint32_t flags;        // bits X: tile X has rows that see some of it, 2 + X: all rows see all of it
   int key0, end;         // positions [key0, key0 + KEYS), those before `end` there
-  uint32_t pages;        // bit i: page i is there
+  uint32_t all_there;    // no page is missing
+  uint32_t there[4];     // a bit for each position: its page is there
   uint32_t poison[4];    // positions whose values were set to zero in part
 };
 // Notes of a segment: units from .. to of an item's.
@@ -97,11 +94,12 @@ struct Item {
 };
 
 struct Control {
-  uint64_t full[8], empty[8], raw_full[8], raw_empty[8], info_full[INFOS], ready[READY];
+  uint64_t full[8], empty[8], raw_full[8], raw_empty[8];
+  uint64_t info_full[INFOS], info_empty[INFOS], ready[INFOS];
   uint64_t k_full[4], k_empty[4], q_ready[2];   // 8-bit cache
   uint64_t q_full, q_empty, s_full[2], p_ready[2][2], o_full[2], drain;
   Info info[INFOS];
-  Segment segment[SEGMENTS];
+  Segment segment[INFOS];
   uint32_t tmem;
   int abort;
   int issued, k_issued, q_issued;  // copies into the ring (8-bit cache: of values), of keys, of queries
@@ -330,12 +328,12 @@ __device__ __noinline__ void read_poison(const AttendParams &p, int s, int h, in
 // 32 columns of a row of output, 32 bytes at a time: whole sectors of memory, without an
 // exchange between the lanes (that, for 64 neighbouring bytes of four lanes, took 214 us
 // for the 200 of 4096 queries of 48 heads).  Rows that begin at an odd multiple of 16 bytes take halves.
-__device__ __forceinline__ void store32(uint16_t *out, bool whole_sectors, const float (&v)[32]) {
+__device__ __forceinline__ void store32(uint16_t *out, bool whole_sectors, const uint32_t (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; i += 16) {
     uint32_t r[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = pack_bf16x2(v[i + 2 * k], v[i + 2 * k + 1]);
+    for (int k = 0; k < 8; ++k) r[k] = pack_bf16x2(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
     if (whole_sectors) {
       asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + i), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                    "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -408,25 +406,21 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
   float scale = p.scale_log2, slack = GROWTH / scale;   // (8-bit cache: of this row)
   const float *scales = reinterpret_cast<const float *>(smem + F::SCALES_AT);
   uint32_t s_phase = 0, o_phase = 0, q_phase = 0;
-  Ring info, ready, slot;   // `slot`: the next unit's keys, 8-bit: values
+  Ring info;
   bool fresh = true;        // a segment's first unit
   uint32_t bits[8];
   bool poisoned = false, any = false;
   float top = -INFINITY, sum = 0.f;
 
   for (uint32_t segment = 0;;) {
-    const Ring my_info = info, my_ready = ready;
+    const Ring my_info = info;
     info.next(INFOS);
-    ready.next(READY);
-    if (!FP8) slot.next(F::SLOTS);
-    const Ring my_value = slot;
-    slot.next(F::SLOTS);
     tc::wait_or_abort_inline(&c.info_full[my_info.at], my_info.phase, abort);
     __syncwarp();
     const Info &u = c.info[my_info.at];
     const uint32_t flags = u.flags;
     if (__any_sync(0xffffffffu, *abort) || (flags & STOP)) break;
-    const Segment &seg = c.segment[segment % SEGMENTS];
+    const Segment &seg = c.segment[segment % INFOS];
     if (FP8 && fresh) {
       fresh = false;
       if (seg.count[X] > 0) {
@@ -441,44 +435,19 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       q_phase ^= 1u;
     }
     if (flags >> X & 1) {
-      const uint32_t pages = u.pages;
       tc::wait_or_abort_inline(&c.s_full[X], s_phase, abort);
       s_phase ^= 1u;
       __syncwarp();
       tc::fence_after_sync();
       const float *ks = scales + my_info.at * 2 * KEYS, *vs = ks + KEYS;
-      const bool whole = flags >> (2 + X) & 1, masked = !whole || pages != p.all_pages;
+      const bool whole = flags >> (2 + X) & 1, masked = !whole || !u.all_there;
       // columns 32 k .. of the unit that this row sees
       const int position = seg.position + X * p.tile_queries + query;
       const int upto = min(position, u.end - 1) - u.key0 + 1;
       const int low = p.window ? position - p.window + 1 - u.key0 : 0, sinks = p.sinks - u.key0;
       auto seen = [&](int k) {
-        uint32_t w = low_bits(upto - 32 * k) & (~low_bits(low - 32 * k) | low_bits(sinks - 32 * k));
-        for (uint32_t m = ~pages & p.all_pages; m; m &= m - 1) {
-          const int at = ((__ffs(m) - 1) << p.page_shift) - 32 * k;
-          w &= ~low_bits(at + (1 << p.page_shift)) | low_bits(at);
-        }
-        return w;
+        return u.there[k] & low_bits(upto - 32 * k) & (~low_bits(low - 32 * k) | low_bits(sinks - 32 * k));
       };
-      if (hides(flags)) {
-        // values that were set to zero (the product needs them there as well, so that
-        // nothing is waited for that is not needed anyway)
-        if (FP8) tc::wait_or_abort_inline(&c.full[my_value.at], my_value.phase, abort);
-        else tc::wait_or_abort_inline(&c.ready[my_ready.at], my_ready.phase, abort);
-        const volatile uint32_t *q = u.poison;
-        const uint4 poison = make_uint4(q[0], q[1], q[2], q[3]);
-        if (poison.x | poison.y | poison.z | poison.w) {
-          if (!poisoned) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) bits[i] = 0;
-            poisoned = true;
-          }
-          if (query < seg.count[X])
-            read_poison<D, FP8>(p, seg.s, seg.h, u.key0,
-                                make_uint4(poison.x & seen(0), poison.y & seen(1), poison.z & seen(2), poison.w & seen(3)), bits);
-        }
-        __syncwarp();
-      }
       // the row of S, 64 columns on their way while the others are worked on
       uint32_t x[4][32];
       float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -584,8 +553,32 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         }
       }
       sum += (tc::pair_lo(sums[0]) + tc::pair_hi(sums[0])) + (tc::pair_lo(sums[1]) + tc::pair_hi(sums[1]));
+      if (hides(flags)) {
+        // values that were set to zero; P is on its way, so the wait costs little
+        tc::wait_or_abort_inline(&c.ready[my_info.at], my_info.phase, abort);
+        const volatile uint32_t *q = u.poison;
+        const uint4 poison = make_uint4(q[0], q[1], q[2], q[3]);
+        if (poison.x | poison.y | poison.z | poison.w) {
+          if (!poisoned) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bits[i] = 0;
+            poisoned = true;
+          }
+          if (query < seg.count[X])
+            read_poison<D, FP8>(p, seg.s, seg.h, u.key0,
+                                make_uint4(poison.x & seen(0), poison.y & seen(1), poison.z & seen(2), poison.w & seen(3)), bits);
+        }
+      }
     }
-    if (!(flags & LAST)) continue;
+    // the notes (and, once its row is written, the segment's) may be written over
+    auto release = [&] {
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&c.info_empty[my_info.at]);
+    };
+    if (!(flags & LAST)) {
+      release();
+      continue;
+    }
     // ---- the segment's end
     ++segment;
     fresh = true;
@@ -594,7 +587,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     any = false;
     top = -INFINITY;
     sum = 0.f;
-    if (seg.count[X] == 0) continue;
+    if (seg.count[X] == 0) {
+      release();
+      continue;
+    }
     if (had) {
       tc::wait_or_abort_inline(&c.o_full[X], o_phase, abort);
       o_phase ^= 1u;
@@ -608,44 +604,60 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     const float inverse = sum_now != 0.f ? 1.f / sum_now : 0.f;
     const int cta0 = seg.cta0, cta1 = seg.cta1;
     float *const part = p.parts + int64_t((2 * blockIdx.x + (int(blockIdx.x) == cta0)) * 2 + X) * part_floats(ROWS, D);
-    // not unrolled: code that runs once an item comes from far, line after line
+    // Not unrolled, and what is rare is apart: code that runs once an item comes from far,
+    // line after line.
+    if (item_whole) {
+      if (live && !had) {   // saw nothing
+#pragma unroll 1
+        for (int i = 0; i < D; i += 8) st_vec(out + i, make_uint4(0, 0, 0, 0));
+      }
+      const uint64_t inverse2 = tc::pair(inverse, inverse);
+#pragma unroll 1
+      for (int k = 0; had && k < D / 32; ++k) {
+        uint32_t v[32];
+        tc::tmem_ld32_async(o_at + k * 32, v);
+        tc::tmem_wait_ld();
+        tc::tmem_hold(v);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) mul_pair(v[i], v[i + 1], inverse2);
+        if (live) store32(out + k * 32, p.whole_sectors, v);
+      }
+      if (poisoned && live) {
+#pragma unroll 1
+        for (int i = 0; i < D; ++i) {
+          float x = bf16_lo(out[i]);
+          if (bits[0 + i / 32] >> i % 32 & 1) x += INFINITY;
+          if (bits[4 + i / 32] >> i % 32 & 1) x -= INFINITY;
+          out[i] = uint16_t(pack_bf16x2(x, 0.f));
+        }
+      }
+      if (live && lse) *lse = sum_now != 0.f ? (top_now * scale + log2f(sum_now)) * 0.69314718056f : -INFINITY;
+      poisoned = false;
+      tc::fence_before_sync();
+      release();
+      continue;
+    }
 #pragma unroll 1
     for (int k = 0; k < D / 32; ++k) {
-      float v[32];
-      {
-        uint32_t (&r)[32] = reinterpret_cast<uint32_t (&)[32]>(v);
-        tc::tmem_ld32_async(o_at + k * 32, r);
-        tc::tmem_wait_ld();
-        tc::tmem_hold(r);
-      }
-      if (poisoned) {
-        const uint32_t plus = bits[k], minus = bits[4 + k];
+      uint32_t v[32];
+      tc::tmem_ld32_async(o_at + k * 32, v);
+      tc::tmem_wait_ld();
+      tc::tmem_hold(v);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (plus >> i & 1) v[i] += INFINITY;
-          if (minus >> i & 1) v[i] -= INFINITY;
-        }
-      }
-      if (item_whole) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = inverse == 0.f ? 0.f : v[i] * inverse;
-        if (live) store32(out + k * 32, p.whole_sectors, v);
-      } else if (live) {
-        if (!had) {   // saw nothing
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 32; i += 4)
-          *reinterpret_cast<float4 *>(part + ((k * 32 + i) * ROWS / 4 + tid) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      for (int i = 0; i < 32; i += 4)
+        if (live)
+          *reinterpret_cast<uint4 *>(part + ((k * 32 + i) * ROWS / 4 + tid) * 4) =
+              had ? make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_uint4(0, 0, 0, 0);   // (saw nothing)
+    }
+    if (poisoned && live) {
+#pragma unroll 1
+      for (int i = 0; i < D; ++i) {
+        float &x = part[(i / 4 * ROWS + tid) * 4 + i % 4];
+        if (bits[0 + i / 32] >> i % 32 & 1) x += INFINITY;
+        if (bits[4 + i / 32] >> i % 32 & 1) x -= INFINITY;
       }
     }
     poisoned = false;
-    if (item_whole) {
-      if (live && lse) *lse = sum_now != 0.f ? (top_now * scale + log2f(sum_now)) * 0.69314718056f : -INFINITY;
-      tc::fence_before_sync();
-      continue;
-    }
     tc::fence_before_sync();
     if (live) {
       const float m = had ? top_now * scale : -INFINITY;
@@ -662,6 +674,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         c.joins[atomicAdd(&c.join_count, 1)] = {int(seg.token) + X * p.tile_queries, seg.h, seg.count[X] << 1 | X, cta0, cta1, join_group};
       }
     }
+    release();
   }
 }
 
@@ -693,12 +706,13 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
   for (Segments seg(p, c); seg.left > 0 && ok; seg.next(p), ++segment) {
     const Item &it = seg.it;
     int page = look(it, seg.from);
-    ok = tc::wait_or_abort(&c.q_empty, q_phase, abort);
+    // the notes that come next, of a unit and so of a segment, are no longer read
+    ok = tc::wait_or_abort(&c.q_empty, q_phase, abort) && tc::wait_or_abort(&c.info_empty[info.at], info.phase ^ 1u, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     q_phase ^= 1u;
     if (lane == 0) {
-      Segment &n = c.segment[segment % SEGMENTS];
+      Segment &n = c.segment[segment % INFOS];
       n.s = it.s;
       n.h = it.h;
       n.token = it.query0 + it.block * 2 * p.tile_queries;
@@ -732,10 +746,17 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
         Ring &at = keys ? k_ring : ring;
         uint64_t *full = (FP8 ? keys ? c.k_full : c.raw_full : c.full) + at.at;
         uint64_t *empty = (FP8 ? keys ? c.k_empty : c.raw_empty : c.empty) + at.at;
-        ok = tc::wait_or_abort(empty, at.phase ^ 1u, abort);
+        ok = tc::wait_or_abort(empty, at.phase ^ 1u, abort) &&
+             (kv == 1 || tc::wait_or_abort(&c.info_empty[info.at], info.phase ^ 1u, abort));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (kv == 0) {
+          const uint32_t all = there | ~inside;   // a bit for each page
+          if (lane < 4) {
+            const int at0 = 32 * lane >> p.page_shift, at1 = 32 * lane + 16 >> p.page_shift;
+            c.info[info.at].there[lane] = (all >> at0 & 1 ? 0xffffu : 0u) | (all >> at1 & 1 ? 0xffff0000u : 0u);
+          }
+          __syncwarp();
           if (lane == 0) {
             Info &n = c.info[info.at];
             uint32_t flags = j + 1 == seg.to ? LAST : 0u;
@@ -744,7 +765,7 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
             n.flags = flags;
             n.key0 = u.key0;
             n.end = u.end;
-            n.pages = (there | ~inside) & p.all_pages;
+            n.all_there = (~all & p.all_pages) == 0;
             n.poison[0] = n.poison[1] = n.poison[2] = n.poison[3] = 0;
             if (FP8) tc::mbar_arrive_expect_tx(&c.info_full[info.at], uint32_t(__popc(there) * 8 << p.page_shift));
             else tc::mbar_arrive(&c.info_full[info.at]);
@@ -778,7 +799,7 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
     c.issued = issued;
     c.k_issued = k_issued;
     c.q_issued = q_issued;
-    if (ok) {
+    if (ok && tc::wait_or_abort(&c.info_empty[info.at], info.phase ^ 1u, abort)) {
       c.info[info.at].flags = STOP;
       tc::mbar_arrive(&c.info_full[info.at]);
     }
@@ -798,7 +819,7 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
   // values: 64 columns of 8 positions are 1024 bytes, the next 8 positions behind them, the
   // next 64 columns KEYS * 128 bytes on
   const uint64_t v_desc = tc::smem_desc(tc::smem_addr(smem + F::SLOTS_AT), KEYS * 128, 1024) | uint64_t(2) << 61;
-  Ring at, info, ready, value, value_ready;   // the next unit's keys; the unit before's values
+  Ring at, info, value, value_info;   // the next unit's keys; the unit before's values
   uint32_t q_phase = 0, p_phase[2] = {0, 0};
   bool ok = true, pending[2] = {false, false}, any[2] = {false, false};
   bool first = true, flush = false;           // a segment's first unit; the step behind its last one
@@ -810,11 +831,10 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
       ok = tc::wait_or_abort(&c.info_full[info.at], info.phase, abort);
       if (!ok) break;
       flags = c.info[info.at].flags;
-      info.next(INFOS);
       if (flags & STOP) break;
       if (first) {
         if (FP8) {
-          const Segment &seg = c.segment[segment++ % SEGMENTS];
+          const Segment &seg = c.segment[segment++ % INFOS];
           for (int X = 0; X < 2 && ok; ++X)
             if (seg.count[X] > 0) {
               ok = tc::wait_or_abort(&c.q_ready[X], ready_phase[X], abort);
@@ -830,7 +850,7 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
     }
     if (!first) {
       ok = FP8 ? tc::wait_or_abort(&c.full[value.at], value.phase, abort)
-               : tc::wait_or_abort(&c.ready[value_ready.at], value_ready.phase, abort);
+               : tc::wait_or_abort(&c.ready[value_info.at], value_info.phase, abort);
       if (!ok) break;
     }
 #pragma unroll
@@ -882,8 +902,8 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
       else at.next(F::SLOTS);
       value = at;
       at.next(F::SLOTS);
-      value_ready = ready;
-      ready.next(READY);
+      value_info = info;
+      info.next(INFOS);
     }
     first = flush;
     flush = !flush && (flags & LAST);
@@ -929,7 +949,7 @@ __device__ __forceinline__ void clean_role(unsigned char *smem, Control &c) {
   using F = Many<D, false>;
   const int thread = threadIdx.x % 64, lane = threadIdx.x % 32;
   volatile int *abort = &c.abort;
-  Ring slot, info, ready;
+  Ring slot, info;
   for (;;) {
     if (!__all_sync(0xffffffffu, tc::wait_or_abort(&c.info_full[info.at], info.phase, abort))) break;
     const uint32_t flags = c.info[info.at].flags;
@@ -941,10 +961,9 @@ __device__ __forceinline__ void clean_role(unsigned char *smem, Control &c) {
       tc::fence_proxy_async_smem();
     }
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&c.ready[ready.at]);
+    if (lane == 0) tc::mbar_arrive(&c.ready[info.at]);
     slot.next(F::SLOTS);
     info.next(INFOS);
-    ready.next(READY);
   }
 }
 
@@ -1002,6 +1021,7 @@ __device__ __forceinline__ void convert_role(unsigned char *smem, Control &c) {
     __syncwarp();
     if (lane == 0) {
       tc::mbar_arrive(&c.full[slot.at]);
+      tc::mbar_arrive(&c.ready[info.at]);
       tc::mbar_arrive(&c.raw_empty[raw.at]);
     }
     raw.next(F::RAWS);
@@ -1028,8 +1048,11 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
       tc::mbar_init(&c.raw_full[i], 1);
       tc::mbar_init(&c.raw_empty[i], 2);
     }
-    for (int i = 0; i < INFOS; ++i) tc::mbar_init(&c.info_full[i], 1);
-    for (int i = 0; i < READY; ++i) tc::mbar_init(&c.ready[i], 2);
+    for (int i = 0; i < INFOS; ++i) {
+      tc::mbar_init(&c.info_full[i], 1);
+      tc::mbar_init(&c.info_empty[i], 8);   // the softmax warps
+      tc::mbar_init(&c.ready[i], 2);
+    }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&c.k_full[i], 1);
       tc::mbar_init(&c.k_empty[i], 1);
