@@ -450,6 +450,14 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       };
       // the row of S, 64 columns on their way while the others are worked on
       uint32_t x[4][32];
+      // BF16: behind the other units' code and once more for the maximum, so that what most
+      // units need lies together (4096 queries of 48 heads 194 -> 189 us; 8-bit, where that
+      // takes more registers than there are, in place)
+      auto hide = [&](int k) {
+        const uint32_t w = seen(k);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[k][i] = w >> i & 1 ? x[k][i] : 0xff800000u;   // minus infinity
+      };
       float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       tc::tmem_ld32_async(s_at, x[0]);
       tc::tmem_ld32_async(s_at + 32, x[1]);
@@ -473,17 +481,23 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
             mul_pair(v[i + 2], v[i + 3], f.y);
           }
         }
-        if (masked) {
-          const uint32_t w = seen(k);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = w >> i & 1 ? v[i] : 0xff800000u;   // minus infinity
-        }
+        if (FP8 && masked) hide(k);
         // four chains
 #pragma unroll
         for (int i = 0; i < 32; i += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             m[e] = max3(m[e], __uint_as_float(v[i + 2 * e]), __uint_as_float(v[i + 2 * e + 1]));
+      }
+      if (!FP8 && masked) {
+        m[0] = m[1] = m[2] = m[3] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          hide(k);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            m[i / 2 % 4] = max3(m[i / 2 % 4], __uint_as_float(x[k][i]), __uint_as_float(x[k][i + 1]));
+        }
       }
       const float now = max3(m[0], m[1], fmaxf(m[2], m[3]));
       // the reference of the exponentials follows the maximum when it has grown far
