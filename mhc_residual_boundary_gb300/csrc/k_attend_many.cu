@@ -26,6 +26,7 @@
 //            taken as they are, by queries in two 8-bit pieces, which the softmax warps
 //            make of their rows.  The scales go to the columns of S and of P.
 #include <algorithm>
+#include <type_traits>
 
 #include "attend_join.cuh"
 #include "attention.cuh"
@@ -40,7 +41,7 @@ constexpr int ROWS = 128;            // rows of a tile
 constexpr int INFOS = 8;             // units whose notes are kept, and segments: no more of them can be under way
 constexpr int CUT = 5;               // places that a cut through all rows costs besides EXTRA + 1
 constexpr float GROWTH = 8.f;        // log2 of what P may reach
-constexpr int EXTRA = 3;             // places on the line that an item takes besides its units, for its beginning and end
+constexpr int EXTRA = 2;             // places on the line that an item takes besides its units, for its beginning and end
 
 __device__ int g_stall_copies;       // test hook: the copying warp issues no copies
 
@@ -58,7 +59,7 @@ struct Many {
   static constexpr int SCALES_AT = K_AT + KSLOTS * RAW; // [INFOS][keys, values][KEYS]
   static constexpr int CONTROL_AT = SCALES_AT + (FP8 ? INFOS * 2 * KEYS * 4 : 0);
   // registers a thread: at the launch, then the softmax warps', the others'
-  static constexpr int R_START = 168, R_SOFT = 200, R_REST = 104;
+  static constexpr int R_START = 168, R_SOFT = 208, R_REST = 88;
   static_assert(256 * R_SOFT + 128 * R_REST <= THREADS * R_START, "registers of a CTA");
 };
 
@@ -450,14 +451,17 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       };
       // the row of S, 64 columns on their way while the others are worked on
       uint32_t x[4][32];
-      // BF16: behind the other units' code and once more for the maximum, so that what most
-      // units need lies together (4096 queries of 48 heads 194 -> 189 us; 8-bit, where that
-      // takes more registers than there are, in place)
       auto hide = [&](int k) {
         const uint32_t w = seen(k);
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[k][i] = w >> i & 1 ? x[k][i] : 0xff800000u;   // minus infinity
       };
+      // The whole work twice, for units that hide something from some row and for the others:
+      // what most units need has to lie together, it is about what the SM's instruction
+      // caches hold (with the tests in their places 4096 queries of 48 heads took 189 us for
+      // 181 and 3 x 1024 of 40 heads over an 8-bit cache of 8000 positions 420 for 332).
+      auto work = [&](auto some) {
+      constexpr bool SOME = decltype(some)::value;
       float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       tc::tmem_ld32_async(s_at, x[0]);
       tc::tmem_ld32_async(s_at + 32, x[1]);
@@ -481,23 +485,13 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
             mul_pair(v[i + 2], v[i + 3], f.y);
           }
         }
-        if (FP8 && masked) hide(k);
+        if (SOME) hide(k);
         // four chains
 #pragma unroll
         for (int i = 0; i < 32; i += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             m[e] = max3(m[e], __uint_as_float(v[i + 2 * e]), __uint_as_float(v[i + 2 * e + 1]));
-      }
-      if (!FP8 && masked) {
-        m[0] = m[1] = m[2] = m[3] = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          hide(k);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            m[i / 2 % 4] = max3(m[i / 2 % 4], __uint_as_float(x[k][i]), __uint_as_float(x[k][i + 1]));
-        }
       }
       const float now = max3(m[0], m[1], fmaxf(m[2], m[3]));
       // the reference of the exponentials follows the maximum when it has grown far
@@ -517,7 +511,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
             tc::tmem_wait_ld();
             tc::tmem_hold(r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+            for (int i = 0; i < 32; i += 2) mul_pair(r[i], r[i + 1], tc::pair(f, f));
             tmem_st<32>(o_at + k, r);
           }
         }
@@ -529,44 +523,42 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       for (int k = 0; k < 4; ++k) {
         uint32_t (&v)[32] = x[k];
         uint32_t r[16];
-        // (two forms: the test for what is hidden in every unit took 448 us for the 425 of
-        // 3 x 1024 queries of 40 heads over 8000 positions)
-        auto weigh = [&](bool hidden) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float w[4];
-            fma_pair(w[0], w[1], v[2 * i], v[2 * i + 1], scale2, base2);
-            fma_pair(w[2], w[3], v[2 * i + 2], v[2 * i + 3], scale2, base2);
+        for (int i = 0; i < 16; i += 2) {
+          float w[4];
+          fma_pair(w[0], w[1], v[2 * i], v[2 * i + 1], scale2, base2);
+          fma_pair(w[2], w[3], v[2 * i + 2], v[2 * i + 3], scale2, base2);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = exp2_fast(w[e]);
-            add_pair(sums[0], w[0], w[1]);
-            add_pair(sums[1], w[2], w[3]);
-            if (FP8) {   // the values' scales
-              const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(vs + k * 32 + 2 * i);
-              uint32_t u[4];
+          for (int e = 0; e < 4; ++e) w[e] = exp2_fast(w[e]);
+          add_pair(sums[0], w[0], w[1]);
+          add_pair(sums[1], w[2], w[3]);
+          if (FP8) {   // the values' scales
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(vs + k * 32 + 2 * i);
+            uint32_t u[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(w[e]);
-              mul_pair(u[0], u[1], f.x);
-              mul_pair(u[2], u[3], f.y);
-              // what is hidden has none
+            for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(w[e]);
+            mul_pair(u[0], u[1], f.x);
+            mul_pair(u[2], u[3], f.y);
+            // what is hidden has none
 #pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = hidden && w[e] == 0.f ? 0.f : __uint_as_float(u[e]);
-            }
-            r[i] = pack_bf16x2(w[0], w[1]);
-            r[i + 1] = pack_bf16x2(w[2], w[3]);
+            for (int e = 0; e < 4; ++e) w[e] = SOME && w[e] == 0.f ? 0.f : __uint_as_float(u[e]);
           }
-        };
-        if (FP8 && masked) weigh(true);
-        else weigh(false);
+          r[i] = pack_bf16x2(w[0], w[1]);
+          r[i + 1] = pack_bf16x2(w[2], w[3]);
+        }
         tmem_st<16>(s_at + k * 16, r);
         if (k % 2) {   // half of P is there: its product can begin
           tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&c.p_ready[X][k / 2]);
+          __syncwarp();
         }
       }
       sum += (tc::pair_lo(sums[0]) + tc::pair_hi(sums[0])) + (tc::pair_lo(sums[1]) + tc::pair_hi(sums[1]));
+      };
+      if (masked) work(std::true_type{});
+      else work(std::false_type{});
       if (hides(flags)) {
         // values that were set to zero; P is on its way, so the wait costs little
         tc::wait_or_abort_inline(&c.ready[my_info.at], my_info.phase, abort);
@@ -582,6 +574,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
             read_poison<D, FP8>(p, seg.s, seg.h, u.key0,
                                 make_uint4(poison.x & seen(0), poison.y & seen(1), poison.z & seen(2), poison.w & seen(3)), bits);
         }
+        __syncwarp();
       }
     }
     // the notes (and, once its row is written, the segment's) may be written over
@@ -626,9 +619,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         for (int i = 0; i < D; i += 8) st_vec(out + i, make_uint4(0, 0, 0, 0));
       }
       const uint64_t inverse2 = tc::pair(inverse, inverse);
-#pragma unroll 1
+#pragma unroll (FP8 ? 1 : 2)
       for (int k = 0; had && k < D / 32; ++k) {
         uint32_t v[32];
+        __syncwarp();
         tc::tmem_ld32_async(o_at + k * 32, v);
         tc::tmem_wait_ld();
         tc::tmem_hold(v);
@@ -654,6 +648,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
 #pragma unroll 1
     for (int k = 0; k < D / 32; ++k) {
       uint32_t v[32];
+      __syncwarp();
       tc::tmem_ld32_async(o_at + k * 32, v);
       tc::tmem_wait_ld();
       tc::tmem_hold(v);
@@ -1000,8 +995,8 @@ __device__ __forceinline__ void convert_role(unsigned char *smem, Control &c) {
     for (int row = thread; row < KEYS; row += 64) {
       const unsigned char *from = smem + F::RAW_AT + raw.at * F::RAW + row * D;
       unsigned char *to = smem + F::SLOTS_AT + slot.at * F::SLOT + row * 128;
-      bool nan = false;
-#pragma unroll
+      uint32_t bad = 0;
+#pragma unroll 2
       for (int i = 0; i < D / 16; ++i) {
         const int chunk = D == 128 ? i ^ (row & 7) : i ^ (row >> 1 & 3);   // as the copies laid them
         const uint4 v = *reinterpret_cast<const uint4 *>(from + chunk * 16);
@@ -1015,21 +1010,23 @@ __device__ __forceinline__ void convert_role(unsigned char *smem, Control &c) {
           asm("{.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;}" : "=f"(a), "=f"(b) : "r"(h));
           o[k] = pack_bf16x2(a, b);
         }
-        if (hidden) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t bad = not_finite2(o[k]);
-            if (bad & 0x8000u) o[k] &= 0xffff0000u;
-            if (bad & 0x80000000u) o[k] &= 0x0000ffffu;
-            nan |= bad != 0;
-          }
-        }
+        for (int k = 0; k < 8; ++k) bad |= not_finite2(o[k]);
         unsigned char *half = to + i / 4 * KEYS * 128;
         const int c0 = i % 4 * 2;
         *reinterpret_cast<uint4 *>(half + ((c0 ^ (row & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4 *>(half + (((c0 + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      if (nan) atomicOr(c.info[info.at].poison + row / 32, 1u << row % 32);
+      if (hidden && bad) {   // (rare: apart, and not unrolled)
+        atomicOr(c.info[info.at].poison + row / 32, 1u << row % 32);
+#pragma unroll 1
+        for (int i = 0; i < D / 2; ++i) {
+          uint32_t *w = reinterpret_cast<uint32_t *>(to + i / 32 * KEYS * 128) + i % 32;
+          const uint32_t b = not_finite2(*w);
+          if (b & 0x8000u) *w &= 0xffff0000u;
+          if (b & 0x80000000u) *w &= 0x0000ffffu;
+        }
+      }
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
@@ -1223,6 +1220,9 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   }
   if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
 
+  // a warp's threads together again, here and behind the roles (of the warp with the products
+  // one thread has been at work): what follows is for whole warps
+  __syncwarp();
   if (c.bounds[0] < c.bounds[1]) {
     if (warp < 8) {
       registers_up<F::R_SOFT>();
@@ -1240,9 +1240,11 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
       }
     }
   }
+  __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  __syncwarp();
   if (warp == 9) tc::tmem_dealloc(c.tmem, 512);
   if (!c.abort && warp < 8) {   // those with the most registers
     const int group = p.heads / p.kv_heads;
@@ -1250,7 +1252,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     for (int k = 0; k < c.join_count; ++k) {
       const Join join = c.joins[k];   // s: its first query's row; block: queries and tile
       const int X = join.block & 1;
-      join_parts<D>(smem, F::CONTROL_AT, tid, 256, [] { asm volatile("bar.sync 1, 256;" ::: "memory"); }, join,
+      join_parts<D>(smem, F::CONTROL_AT, tid, 256, [] { asm volatile("barrier.sync 1, 256;" ::: "memory"); }, join,
                     (join.block >> 1) * group, ROWS, JoinCounters{p.counters + 3 * p.counter_ctas * X, p.counter_ctas},
                     [&](int cta, bool begins) { return p.parts + int64_t((2 * cta + begins) * 2 + X) * part_floats(ROWS, D); },
                     [&](int row, int col, float all, float n, float, const float4 &o) {
