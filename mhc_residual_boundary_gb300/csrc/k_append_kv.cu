@@ -11,7 +11,7 @@
 // upper 32 bits, signed, give the angle between -pi and pi.
 //
 // Bound by memory for many tokens: 8192 of 48 + 2 x 8 heads of 128 in BF16 read and write
-// 268 MB in 45 us, 6.0 TB/s; by latency for few: one token takes 1.6 us.
+// 268 MB in 42 us, 6.4 TB/s; by latency for few: one token takes 1.6 us.
 #include "attention.cuh"
 #include "device_common.cuh"
 #include "e4m3_scale.h"
@@ -41,7 +41,7 @@ __device__ __forceinline__ uint2 quant8(const float (&y)[8], float inv) {
 template <int DIM, int TOKENS>
 __global__ void __launch_bounds__(APPEND_THREADS, 4) k_append_kv(const AppendParams p) {
   constexpr int UNITS = DIM / 16;   // threads a head
-  __shared__ float2 turns[TOKENS][DIM / 2];  // cos, sin
+  __shared__ float2 turns[TOKENS][DIM / 2];  // cos, sin; of pair i at (i % 8) UNITS + i / 8: without bank conflicts (with them 45 us for 42)
   __shared__ int32_t slots[TOKENS];
   const int first = blockIdx.x * TOKENS, count = min(TOKENS, p.tokens - first);
   const int item = blockIdx.y * blockDim.x + threadIdx.x;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, 4) k_append_kv(const AppendPar
       const uint64_t w = uint64_t(int64_t(p.positions[first + n])) * p.turns[i];
       float s, c;
       sincospif(float(int32_t(w >> 32)) * 0x1p-31f, &s, &c);
-      turns[n][i] = make_float2(c, s);
+      turns[n][i % 8 * UNITS + i / 8] = make_float2(c, s);
     }
   }
   __syncthreads();
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, 4) k_append_kv(const AppendPar
       if (p.interleaved) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          const float2 ta = turn[unit * 8 + i / 2], tb = turn[unit * 8 + 4 + i / 2];
+          const float2 ta = turn[i / 2 * UNITS + unit], tb = turn[(4 + i / 2) * UNITS + unit];
           const float a0 = a[i], b0 = b[i];
           a[i] = a0 * ta.x - a[i + 1] * ta.y;
           a[i + 1] = a[i + 1] * ta.x + a0 * ta.y;
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, 4) k_append_kv(const AppendPar
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 t = turn[unit * 8 + i];
+          const float2 t = turn[i * UNITS + unit];
           const float a0 = a[i];
           a[i] = a0 * t.x - b[i] * t.y;
           b[i] = b[i] * t.x + a0 * t.y;
@@ -169,8 +169,8 @@ cudaError_t launch_append(const AppendParams &p, int sms, cudaStream_t stream) {
   // 16 + 2 x 2 heads of 64, 8192 tokens took 15.7 us in CTAs of 256 threads and take 9.3
   // Tokens a CTA, by the 256 threads that there would be for each SM with one: more loads
   // under way and fewer CTAs, against too few CTAs.  With 48 + 2 x 8 heads of 128, in us:
-  // 32 tokens 1.66, 2.00 and 2.82 with one, two and four, 608 tokens 4.9, 4.2 and 4.6,
-  // 2432 tokens 19.7, 16.9 and 16.0, 8192 tokens 60, 50 and 45.
+  // 32 tokens 1.58, 1.73 and 2.41 with one, two and four, 608 tokens 4.2, 3.3 and 3.7,
+  // 2432 tokens 17.9, 14.7 and 14.2, 8192 tokens 55, 44 and 42.
   const int64_t all = int64_t(p.tokens) * splits * threads / APPEND_THREADS / sms;
   return all < 3 ? launch<1>(p, splits, threads, stream) : all < 24 ? launch<2>(p, splits, threads, stream)
                                                                   : launch<4>(p, splits, threads, stream);

@@ -557,8 +557,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
       }
       sum += (tc::pair_lo(sums[0]) + tc::pair_hi(sums[0])) + (tc::pair_lo(sums[1]) + tc::pair_hi(sums[1]));
       };
-      if (masked) work(std::true_type{});
-      else work(std::false_type{});
+      if (!masked) work(std::false_type{});
+      else work(std::true_type{});
       if (hides(flags)) {
         // values that were set to zero; P is on its way, so the wait costs little
         tc::wait_or_abort_inline(&c.ready[my_info.at], my_info.phase, abort);
