@@ -320,8 +320,9 @@ mhc_status_t mhc_attention_attend(mhc_attention_t *a, const mhc_attention_attend
   p.keys = {const_cast<void *>(g->k_cache), g->k_page_stride, const_cast<float *>(g->k_scales)};
   p.values = {const_cast<void *>(g->v_cache), g->v_page_stride, const_cast<float *>(g->v_scales)};
   p.scale_log2 = g->scale * 1.44269504088896340736f;
-  p.window = g->window;
-  p.sinks = g->window ? g->sinks : 0;
+  // a window that no sequence fills is none: positions less a window stay in range
+  p.window = g->window < positions ? g->window : 0;
+  p.sinks = p.window ? int(std::min<int64_t>(g->sinks, positions)) : 0;
   p.output = static_cast<uint16_t *>(g->output);
   p.lse = g->lse;
   p.parts = a->parts;

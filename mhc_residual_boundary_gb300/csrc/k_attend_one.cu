@@ -254,7 +254,7 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
   // ends sooner (one kv head of 32768 positions 23.2 us with one, 19.3 with four; 8 of 2000 11.5 and
   // 9.7 with two; at 16 units one is as good as two).
   const int pairs = p.sequences * p.kv_heads;
-  line.divide(min(int(gridDim.x), line.total >> (line.total >= 64 * pairs ? 2 : line.total >= 32 * pairs)));
+  line.divide(min(int(gridDim.x), line.total >> (line.total / 64 >= pairs ? 2 : line.total / 32 >= pairs)));
   const int cost = 2 * pairs >= int(gridDim.x) ? COST_MANY : COST;
   const int cta = min(int(blockIdx.x), line.grid);
   // thread k finds where this CTA's part begins (0), where it ends (1): the owner of the

@@ -449,3 +449,19 @@ def test_refusals(handles):
     odd = torch.zeros(2 * 4 * 64 + 8, dtype=BF16, device="cuda")[1:513].view(2, 4, 64)
     refuse(capi.MhcError, "aligned", {"q": odd})
     a.check_errors()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("several", [False, True])
+def test_windows_of_any_size(handles, several, fp8):
+    """A window of at least the length hides nothing, up to the largest integer; also beside queries that lie before
+    their sequence."""
+    inputs = make_inputs(47, lengths=[5, 300, 41], queries=[9, 40, 41] if several else None, heads=8, kv=2, d=64, page=16,
+                         fp8=fp8)
+    want = define(inputs, page=16)
+    for window, sinks in ((301, 0), (2 ** 30, 2), (2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1)):
+        _, out = attend(handles, inputs, 16, window=window, sinks=sinks)
+        check(out, inputs, page=16, want=want)
+    want = define(inputs, page=16, window=3, sinks=10 ** 6)
+    _, out = attend(handles, inputs, 16, window=3, sinks=2 ** 31 - 1)
+    check(out, inputs, page=16, want=want)
