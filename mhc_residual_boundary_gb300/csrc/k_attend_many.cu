@@ -406,6 +406,9 @@ __device__ __forceinline__ float split_queries(unsigned char *tile, int row) {
   return e2 == 255 ? NAN : __uint_as_float(uint32_t(127 + e - 7) << 23);
 }
 
+// How far the maximum of the products may grow; finite, so that minus infinity grows.
+__device__ __forceinline__ float slack_of(float scale) { return fminf(GROWTH / scale, 3.4e38f); }
+
 template <int D, bool FP8>
 __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned char *smem, Control &c, uint32_t tmem, int X) {
   using F = Many<D, FP8>;
@@ -414,7 +417,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
   const uint32_t lanes = uint32_t(warp * 32) << 16;
   const uint32_t s_at = tmem + S_COL(X) + lanes, o_at = tmem + O_COL(X) + lanes;
   const int group = p.heads / p.kv_heads, query = tid / group, head = tid % group;
-  float scale = p.scale_log2, slack = GROWTH / scale;   // (8-bit cache: of this row)
+  float scale = p.scale_log2, slack = slack_of(scale);   // (8-bit cache: of this row)
   const float *scales = reinterpret_cast<const float *>(smem + F::SCALES_AT);
   uint32_t s_phase = 0, o_phase = 0, q_phase = 0;
   Ring info;
@@ -438,7 +441,9 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         tc::wait_or_abort_inline(&c.q_full, q_phase, abort);
         __syncwarp();
         scale = p.scale_log2 * split_queries<D>(smem + F::Q_AT + X * F::Q, tid);
-        slack = GROWTH / scale;
+        // no scale is zero (minus infinity times zero is not a number); NaN stays
+        scale = scale < 1.2e-38f ? 1.2e-38f : scale;
+        slack = slack_of(scale);
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&c.q_ready[X]);

@@ -465,3 +465,16 @@ def test_windows_of_any_size(handles, several, fp8):
     want = define(inputs, page=16, window=3, sinks=10 ** 6)
     _, out = attend(handles, inputs, 16, window=3, sinks=2 ** 31 - 1)
     check(out, inputs, page=16, want=want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("several", [False, True])
+def test_small_scales_and_queries(handles, several, fp8):
+    """Scales down to FP32's least and queries of zero: the weights are equal, lse is the logarithm of their number."""
+    inputs = make_inputs(53, lengths=[200, 37], queries=[9, 37] if several else None, heads=4, kv=2, d=128, page=16,
+                         fp8=fp8)
+    inputs["q"][0] = 0
+    for scale in (1.0, 1e-3, 1e-30, 1e-38, 2.0 ** -149):
+        _, out = attend(handles, inputs, 16, scale=scale)
+        check(out, inputs, page=16, scale=scale)
+
