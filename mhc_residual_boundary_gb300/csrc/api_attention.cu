@@ -267,7 +267,8 @@ mhc_status_t mhc_attention_attend(mhc_attention_t *a, const mhc_attention_attend
   if (!g->q_starts && g->tokens != g->sequences)
     return fail(msg, MHC_ERR_INVALID_ARG, "without q_starts every sequence has one token");
   if (g->window < 0 || g->sinks < 0) return fail(msg, MHC_ERR_INVALID_ARG, "window or sinks is negative");
-  if (!(g->scale > 0) || !std::isfinite(g->scale)) return fail(msg, MHC_ERR_INVALID_ARG, "scale must be positive and finite");
+  const float scale_log2 = g->scale * 1.44269504088896340736f;
+  if (!(g->scale > 0) || !std::isfinite(scale_log2)) return fail(msg, MHC_ERR_INVALID_ARG, "scale must be positive and finite");
   if (g->tokens == 0 || g->sequences == 0) return MHC_OK;
   if (g->tokens > (1 << 24) || g->sequences > (1 << 20))
     return fail(msg, MHC_ERR_UNSUPPORTED, "more than 2^24 tokens or 2^20 sequences");
@@ -319,7 +320,7 @@ mhc_status_t mhc_attention_attend(mhc_attention_t *a, const mhc_attention_attend
   p.page_table = g->page_table;
   p.keys = {const_cast<void *>(g->k_cache), g->k_page_stride, const_cast<float *>(g->k_scales)};
   p.values = {const_cast<void *>(g->v_cache), g->v_page_stride, const_cast<float *>(g->v_scales)};
-  p.scale_log2 = g->scale * 1.44269504088896340736f;
+  p.scale_log2 = scale_log2;
   // a window that no sequence fills is none: positions less a window stay in range
   p.window = g->window < positions ? g->window : 0;
   p.sinks = p.window ? int(std::min<int64_t>(g->sinks, positions)) : 0;

@@ -1171,9 +1171,12 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   if (warp < 2 && place < line.total) {
     int rest = place - c.bounds[warp];
     __syncwarp();
+    if (lane == 0) c.bounds[warp] = line.total;
+    __syncwarp();
     bool seen_before = false;
+    // (it ends at the break, unless lengths change under the call)
 #pragma unroll 1
-    for (int s = (warp ? owner1 : owner0) * chunk;; ++s) {
+    for (int s = (warp ? owner1 : owner0) * chunk; s < p.sequences; ++s) {
       Item it;
       load_sequence(p, it, s, seen_before);
       int n = 0;

@@ -272,8 +272,10 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
       int rest = place - bounds_shared[tid];
       bool seen_before = false;
       Cursor c;
+      bounds_shared[tid] = line.total;
+      // (it ends at the break, unless lengths change under the call)
 #pragma unroll 1
-      for (int s = (tid ? owner1 : owner0) * chunk;; ++s) {
+      for (int s = (tid ? owner1 : owner0) * chunk; s < p.sequences; ++s) {
         const int n = places_of(s, c, seen_before);
         if (rest < n * p.kv_heads) {
           c.h = rest / n;

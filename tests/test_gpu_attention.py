@@ -478,3 +478,10 @@ def test_small_scales_and_queries(handles, several, fp8):
         _, out = attend(handles, inputs, 16, scale=scale)
         check(out, inputs, page=16, scale=scale)
 
+
+
+def test_scales_that_are_not_finite_in_the_exponent_are_refused(handles):
+    from mhc_residual_boundary_gb300 import capi
+    inputs = make_inputs(59, lengths=[50], heads=4, kv=2, d=64, page=16, fp8=False)
+    with pytest.raises(capi.MhcError, match="scale"):
+        attend(handles, inputs, 16, scale=3e38)
