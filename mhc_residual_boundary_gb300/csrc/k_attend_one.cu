@@ -30,7 +30,7 @@
 // of 128, in 162 us, 6.6 TB/s (0.97 of a copy; 200 with products whose rows are heads, 191
 // with one CTA of eight warps an SM, 173 with cuts wherever an even division puts them).  8 bits, 16 heads a kv head: the conversions and
 // products share the time with the copies, 37 sequences of up to 16001 positions on 4 kv heads
-// in 70 us (4.6 TB/s).  Few positions: trips through memory one after another (lengths, pages,
+// in 67 us (4.8 TB/s).  Few positions: trips through memory one after another (lengths, pages,
 // rows, parts), 3.7 us for one unit, 8 for 700 positions cut and joined.
 #include <algorithm>
 
@@ -48,6 +48,7 @@ constexpr int EXTRA = 1;   // places on the line that a (sequence, head) takes b
 // 8.3, of 500 15.6 and 11.4; with few pairs, which only cuts spread, 8 of 1000 9.2 and (with 4) 10.7.
 constexpr int COST = 2, COST_MANY = 5;
 static_assert(COST > EXTRA, "a cut has a unit on either side");
+constexpr float GROWTH = 8.f;   // log2 of what a weight may reach
 
 template <int D, bool FP8>
 struct One {
@@ -514,37 +515,34 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
                 }
               }
           }
-        // ---- the running maxima, over the eight lanes of a head
-        float base[NT][2], base_out[NT][2];
+        // ---- the running references of the weights: a head's maximum, over its eight lanes, when
+        // some lane's has grown past the reference by more than GROWTH (weights are then at
+        // most 2^GROWTH).  Most tiles need no exchange of lanes (exchanged for every one: 70 us for
+        // the 66.6 of 37 sequences over an 8-bit cache, 9.9 for 9.3 of one over 700 positions).
         bool grew = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int o = 4; o < 32; o *= 2) {
-              now[n][e] = fmaxf(now[n][e], __shfl_xor_sync(0xffffffffu, now[n][e], o));
-              if (FP8) now_out[n][e] = fmaxf(now_out[n][e], __shfl_xor_sync(0xffffffffu, now_out[n][e], o));
-            }
-            now[n][e] = fmaxf(now[n][e], top[n][e]);
-            grew |= now[n][e] != top[n][e];
-            base_out[n][e] = base[n][e] = now[n][e] == -INFINITY ? 0.f : now[n][e];
-            if (FP8) {
-              now_out[n][e] = fmaxf(now_out[n][e], top_out[n][e]);
-              grew |= now_out[n][e] != top_out[n][e];
-              base_out[n][e] = now_out[n][e] == -INFINITY ? 0.f : now_out[n][e];
-            }
+            grew |= now[n][e] > top[n][e] + GROWTH;
+            if (FP8) grew |= now_out[n][e] > top_out[n][e] + GROWTH;
           }
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float f = exp2_fast(top[n][e] - base[n][e]);
-              const float fo = FP8 ? exp2_fast(top_out[n][e] - base_out[n][e]) : f;
+#pragma unroll
+              for (int o = 4; o < 32; o *= 2) {
+                now[n][e] = fmaxf(now[n][e], __shfl_xor_sync(0xffffffffu, now[n][e], o));
+                if (FP8) now_out[n][e] = fmaxf(now_out[n][e], __shfl_xor_sync(0xffffffffu, now_out[n][e], o));
+              }
+              const float up = fmaxf(now[n][e], top[n][e]), up_out = FP8 ? fmaxf(now_out[n][e], top_out[n][e]) : up;
+              const float f = up == -INFINITY ? 1.f : exp2_fast(top[n][e] - up);
+              const float fo = FP8 ? up_out == -INFINITY ? 1.f : exp2_fast(top_out[n][e] - up_out) : f;
               sum[n][e] *= f;
-              top[n][e] = now[n][e];
-              if (FP8) top_out[n][e] = now_out[n][e];
+              top[n][e] = up;
+              if (FP8) top_out[n][e] = up_out;
 #pragma unroll
               for (int i = 0; i < M_TILES; ++i) {
                 acc[n][i][e] *= fo;
@@ -552,6 +550,14 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
               }
             }
         }
+        float base[NT][2], base_out[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            base_out[n][e] = base[n][e] = top[n][e] == -INFINITY ? 0.f : top[n][e];
+            if (FP8) base_out[n][e] = top_out[n][e] == -INFINITY ? 0.f : top_out[n][e];
+          }
         // ---- weights and their sum, values times weights, 16 positions at a time
 #pragma unroll
         for (int j = 0; j < BLOCKS; ++j) {
