@@ -51,6 +51,7 @@ class Attention:
         self.heads, self.kv_heads, self.head_dim, self.page_size, self.fp8 = heads, kv_heads, head_dim, page_size, fp8
         self._index = self.device.index
         self._page = kv_heads * page_size * head_dim
+        self._cache_dtype, self._scale = F8 if fp8 else BF16, head_dim ** -0.5
         lib = capi.attention_calls()
         self._append, self._attend = lib["append"], lib["attend"]
         self.handle = capi.mhc_attention_create(self.config, self.device.index)
@@ -90,8 +91,10 @@ class Attention:
         return {"output": torch.empty(tokens, self.heads, self.head_dim, dtype=BF16, device=self.device),
                 "lse": torch.empty(tokens, self.heads, dtype=F32, device=self.device)}
 
-    # checks as in Sublayer: one test a tensor for the usual case, the message in
-    # a function that only a refusal reaches
+    # The checks run on every call, beside kernels of a few microseconds: the usual
+    # layout (dense caches, tokens whose heads are dense) passes one condition within the
+    # call, everything else goes through the functions below, tensor by tensor, to an
+    # argument or a refusal.
     def _ptr(self, name: str, t: torch.Tensor, dtype, shape: tuple) -> int:
         """Pointer of a dense tensor."""
         if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._index:
@@ -159,6 +162,39 @@ class Attention:
         outputs: k_cache, v_cache (with fp8 k_scales, v_scales) and, with q,
         q_out, which may be q itself.  q, k and v may be slices of one packed
         projection."""
+        k, v, positions, slots = inputs["k"], inputs["v"], inputs["positions"], inputs["slots"]
+        k_cache, v_cache, q, q_out = outputs["k_cache"], outputs["v_cache"], inputs.get("q"), outputs.get("q_out")
+        t, pages, kv, d, index = k.shape[0], k_cache.shape[0], self.kv_heads, self.head_dim, self._index
+        kv_shape, cache_shape, t_shape = (t, kv, d), (pages, kv, self.page_size, d), (t,)
+        dtype = self._cache_dtype
+        if (q is not None and q_out is not None and len(outputs) == (5 if self.fp8 else 3)
+                and k.dtype is BF16 and v.dtype is BF16 and q.dtype is BF16 and q_out.dtype is BF16
+                and k_cache.dtype is dtype and v_cache.dtype is dtype and positions.dtype is I32 and slots.dtype is I32
+                and k.shape == kv_shape and v.shape == kv_shape and q.shape == (q_shape := (t, self.heads, d))
+                and q_out.shape == q_shape and k_cache.shape == cache_shape and v_cache.shape == cache_shape
+                and positions.shape == t_shape and slots.shape == t_shape
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and positions.is_contiguous()
+                and slots.is_contiguous()
+                and (ks := k.stride())[1] == d == (vs := v.stride())[1] and (qs := q.stride())[1] == d
+                and (os := q_out.stride())[1] == d and ks[2] == vs[2] == qs[2] == os[2] == 1
+                and k.get_device() == index and v.get_device() == index and q.get_device() == index
+                and q_out.get_device() == index and k_cache.get_device() == index and v_cache.get_device() == index
+                and positions.get_device() == index and slots.get_device() == index):
+            k_scales, v_scales = self._scales(outputs, pages) if self.fp8 else (0, 0)
+            if t > 1:
+                qs, ks, vs, os = qs[0], ks[0], vs[0], os[0]
+            else:   # a single token's stride is never used
+                qs = os = self.heads * d
+                ks = vs = kv * d
+            args = APPEND_ARGS.pack(t, pages, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
+                                    slots.data_ptr(), q_out.data_ptr(), os, k_cache.data_ptr(), self._page,
+                                    v_cache.data_ptr(), self._page, k_scales, v_scales)
+        else:
+            args = self._append_args(inputs, outputs)
+        self._call(self._append, args, stream)
+        return outputs
+
+    def _append_args(self, inputs: dict, outputs: dict) -> bytes:
         k, v, q, q_out = inputs["k"], inputs["v"], inputs.get("q"), outputs.get("q_out")
         k_cache, v_cache = outputs["k_cache"], outputs["v_cache"]
         t, kv, pages = k.shape[0], self.kv_heads, k_cache.shape[0]
@@ -174,10 +210,8 @@ class Attention:
         k_scales, v_scales = self._scales(outputs, pages)
         if len(outputs) != 2 + 2 * self.fp8 + (q is not None):
             self._unknown(outputs, ("q_out", "k_cache", "v_cache", "k_scales", "v_scales"), "output")
-        self._call(self._append, APPEND_ARGS.pack(t, pages, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, positions, slots,
-                                                  op, os, k_cache.data_ptr(), kcs, v_cache.data_ptr(), vcs, k_scales,
-                                                  v_scales), stream)
-        return outputs
+        return APPEND_ARGS.pack(t, pages, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, positions, slots, op, os,
+                                k_cache.data_ptr(), kcs, v_cache.data_ptr(), vcs, k_scales, v_scales)
 
     def attend(self, inputs: dict, outputs: dict, *, window: int = 0, sinks: int = 0, scale: float | None = None,
                stream=None) -> dict:
@@ -194,6 +228,32 @@ class Attention:
         scores, head_dim ** -0.5 by default."""
         q, k_cache, v_cache, table = inputs["q"], inputs["k_cache"], inputs["v_cache"], inputs["pages"]
         lengths, starts, out, lse = inputs["lengths"], inputs.get("q_starts"), outputs["output"], outputs.get("lse")
+        t, s, pages, heads, d, index = q.shape[0], lengths.shape[0], k_cache.shape[0], self.heads, self.head_dim, self._index
+        q_shape, cache_shape, dtype = (t, heads, d), (pages, self.kv_heads, self.page_size, d), self._cache_dtype
+        if (q.dtype is BF16 and out.dtype is BF16 and k_cache.dtype is dtype and v_cache.dtype is dtype
+                and table.dtype is I32 and lengths.dtype is I32 and q.shape == q_shape and out.shape == q_shape
+                and k_cache.shape == cache_shape and v_cache.shape == cache_shape and lengths.shape == (s,)
+                and (shape := table.shape)[0] == s and len(shape) == 2
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and q.is_contiguous() and out.is_contiguous()
+                and table.is_contiguous() and lengths.is_contiguous()
+                and q.get_device() == index and out.get_device() == index and k_cache.get_device() == index
+                and v_cache.get_device() == index and table.get_device() == index and lengths.get_device() == index
+                and len(outputs) == (1 if lse is None else 2) and (self.fp8 or "k_scales" not in inputs)):
+            k_scales, v_scales = self._scales(inputs, pages) if self.fp8 or "v_scales" in inputs else (0, 0)
+            width, row = shape[1], heads * d
+            args = ATTEND_ARGS.pack(
+                t, s, pages, width, q.data_ptr(), row, 0 if starts is None else self._ptr("q_starts", starts, I32, (s + 1,)),
+                lengths.data_ptr(), table.data_ptr(), width, k_cache.data_ptr(), self._page, v_cache.data_ptr(), self._page,
+                k_scales, v_scales, self._scale if scale is None else scale, window, sinks, out.data_ptr(), row,
+                0 if lse is None else self._ptr("lse", lse, F32, (t, heads)))
+        else:
+            args = self._attend_args(inputs, outputs, window, sinks, scale)
+        self._call(self._attend, args, stream)
+        return outputs
+
+    def _attend_args(self, inputs: dict, outputs: dict, window: int, sinks: int, scale: float | None) -> bytes:
+        q, k_cache, v_cache, table = inputs["q"], inputs["k_cache"], inputs["v_cache"], inputs["pages"]
+        lengths, starts, out, lse = inputs["lengths"], inputs.get("q_starts"), outputs["output"], outputs.get("lse")
         t, s, pages, width = q.shape[0], lengths.shape[0], k_cache.shape[0], table.shape[1]
         qs, os = self._token_stride("q", q, t, self.heads), self._token_stride("output", out, t, self.heads)
         lengths_p = self._ptr("lengths", lengths, I32, (s,))
@@ -207,11 +267,9 @@ class Attention:
         lp = 0 if lse is None else self._ptr("lse", lse, F32, (t, self.heads))
         if len(outputs) != 1 + (lse is not None):
             self._unknown(outputs, ("output", "lse"), "output")
-        self._call(self._attend, ATTEND_ARGS.pack(t, s, pages, width, q.data_ptr(), qs, starts_p, lengths_p,
-                                                  table.data_ptr(), ts, k_cache.data_ptr(), kcs, v_cache.data_ptr(), vcs,
-                                                  k_scales, v_scales, self.head_dim ** -0.5 if scale is None else scale,
-                                                  window, sinks, out.data_ptr(), os, lp), stream)
-        return outputs
+        return ATTEND_ARGS.pack(t, s, pages, width, q.data_ptr(), qs, starts_p, lengths_p, table.data_ptr(), ts,
+                                k_cache.data_ptr(), kcs, v_cache.data_ptr(), vcs, k_scales, v_scales,
+                                self._scale if scale is None else scale, window, sinks, out.data_ptr(), os, lp)
 
     def check_errors(self) -> None:
         capi.mhc_attention_check_errors(self.handle)
