@@ -180,7 +180,15 @@ class Attention:
                 and k.get_device() == index and v.get_device() == index and q.get_device() == index
                 and q_out.get_device() == index and k_cache.get_device() == index and v_cache.get_device() == index
                 and positions.get_device() == index and slots.get_device() == index):
-            k_scales, v_scales = self._scales(outputs, pages) if self.fp8 else (0, 0)
+            k_scales = v_scales = 0
+            if self.fp8:
+                k_scales, v_scales, shape = outputs["k_scales"], outputs["v_scales"], cache_shape[:3]
+                if (k_scales.dtype is F32 and v_scales.dtype is F32 and k_scales.shape == shape and v_scales.shape == shape
+                        and k_scales.is_contiguous() and v_scales.is_contiguous() and k_scales.get_device() == index
+                        and v_scales.get_device() == index):
+                    k_scales, v_scales = k_scales.data_ptr(), v_scales.data_ptr()
+                else:
+                    k_scales, v_scales = self._scales(outputs, pages)
             if t > 1:
                 qs, ks, vs, os = qs[0], ks[0], vs[0], os[0]
             else:   # a single token's stride is never used
