@@ -485,3 +485,23 @@ def test_scales_that_are_not_finite_in_the_exponent_are_refused(handles):
     inputs = make_inputs(59, lengths=[50], heads=4, kv=2, d=64, page=16, fp8=False)
     with pytest.raises(capi.MhcError, match="scale"):
         attend(handles, inputs, 16, scale=3e38)
+
+
+def test_two_handles_at_once():
+    """Calls of two handles on two streams, side by side: the bits that each has alone."""
+    from mhc_residual_boundary_gb300 import Attention
+    calls = []
+    for seed, queries, fp8 in ((61, [300, 40], False), (62, [200, 90], True), (63, None, False)):
+        inputs = make_inputs(seed, lengths=[3000, 700], queries=queries, heads=8, kv=2, d=64, page=16, fp8=fp8)
+        a = Attention(heads=8, kv_heads=2, head_dim=64, page_size=16, fp8=fp8)
+        alone = a.attend(inputs, a.empty_outputs(inputs["q"].shape[0]))
+        calls.append((a, inputs, alone, a.empty_outputs(inputs["q"].shape[0]), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, inputs, _, out, stream in calls:
+            a.attend(inputs, out, stream=stream)
+    torch.cuda.synchronize()
+    for a, _, alone, out, _ in calls:
+        a.check_errors()
+        assert all(torch.equal(alone[n], out[n]) for n in alone)
+        a.close()
