@@ -49,6 +49,7 @@ constexpr int EXTRA = 1;   // places on the line that a (sequence, head) takes b
 constexpr int COST = 2, COST_MANY = 5;
 static_assert(COST > EXTRA, "a cut has a unit on either side");
 constexpr float GROWTH = 8.f;   // log2 of what a weight may reach
+constexpr float LEAST = 1.17549435e-38f;   // of a weight's second piece, 2^-126: nothing beside the first one
 
 template <int D, bool FP8>
 struct One {
@@ -572,9 +573,11 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
               if (FP8) {
                 pa[n][r] = transpose8(pack_f16x2(exp2_fast(y[n][j][2 * r] - base_out[n][0]), exp2_fast(y[n][j][2 * r + 1] - base_out[n][1])));
               } else {
-                const uint32_t w = pack_bf16x2(w0, w1);
+                // the first piece cut off, not rounded: the second is what is left, never negative and
+                // never zero, so that both times an infinity are the same infinity
+                const uint32_t w = __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
                 pa[n][r] = transpose8(w);
-                pb[n][r] = transpose8(pack_bf16x2(w0 - bf16_lo(w), w1 - bf16_hi(w)));
+                pb[n][r] = transpose8(pack_bf16x2(fmaxf(w0 - bf16_lo(w), LEAST), fmaxf(w1 - bf16_hi(w), LEAST)));
               }
             }
           const int row = j * 16 + 2 * t;   // this lane's positions: row, row + 1, row + 8, row + 9
