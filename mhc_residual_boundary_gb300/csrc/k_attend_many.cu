@@ -1230,10 +1230,21 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
       Item it;
       load_sequence(p, it, s, bad);
       const int n = min(it.queries, it.queries - it.length);
+      // (query, 16 bytes of its row), stepped: their product may be more than 2^31
       const int row = p.heads * D / 8;
-      for (int i = tid; i < n * row; i += T)
-        st_vec(p.output + (it.query0 + i / row) * p.output_stride + i % row * 8, make_uint4(0, 0, 0, 0));
-      for (int i = tid; p.lse && i < n * p.heads; i += T) p.lse[int64_t(it.query0) * p.heads + i] = -INFINITY;
+#pragma unroll 1
+      for (int i = tid / row, at = tid % row; i < n;) {
+        st_vec(p.output + (it.query0 + i) * p.output_stride + at * 8, make_uint4(0, 0, 0, 0));
+        i += T / row;
+        at += T % row;
+        if (at >= row) {
+          at -= row;
+          ++i;
+        }
+      }
+      const int64_t first = int64_t(it.query0) * p.heads, count = int64_t(n) * p.heads;
+#pragma unroll 1
+      for (int64_t i = tid; p.lse && i < count; i += T) p.lse[first + i] = -INFINITY;
     }
   }
   if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
