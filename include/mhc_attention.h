@@ -103,6 +103,9 @@ typedef struct {
  * and lse the logarithm of the lower sum (natural); a row that sees nothing
  * has zeros and minus infinity.  Positions that a query does not see may hold
  * anything.  Rows of output from q_starts[sequences] on are left as they are.
+ * A sequence with a start that is out of range (0 .. tokens) or whose two starts
+ * decrease, and every sequence behind it, has no queries: their rows are left as
+ * they are.
  * The softmax and all sums are held in FP32.  In calls with q_starts or with more
  * than 16 heads for each kv head the weights are rounded to BF16, and over an
  * 8-bit cache queries are off by at most 2^-17 of their head's largest element (0

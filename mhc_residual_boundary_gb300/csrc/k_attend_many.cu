@@ -114,7 +114,8 @@ struct Control {
   uint32_t tmem;
   int abort;
   int issued, k_issued, q_issued;  // copies into the ring (8-bit cache: of values), of keys, of queries
-  int warp_total[16];
+  uint32_t warp_total[16];
+  int warp_good[16];
   Item begin;
   int begin_place, bounds[2];
   Join joins[4];         // of the first and last item of the part, either tile
@@ -127,12 +128,12 @@ static_assert(smem_bytes<128, false>() <= 227 * 1024 && smem_bytes<128, true>() 
               smem_bytes<64, false>() <= 227 * 1024 && smem_bytes<64, true>() <= 227 * 1024, "a CTA's shared memory");
 
 // ----------------------------------------------------------------- items
-__device__ __forceinline__ void load_sequence(const AttendParams &p, Item &it, int s, bool &bad) {
+__device__ __forceinline__ void load_sequence(const AttendParams &p, Item &it, int s, bool &bad, bool &bad_start) {
   it.s = s;
   it.length = sequence_length(p, s, bad);
-  it.query0 = query_start(p, s, bad);
-  const int to = query_start(p, s + 1, bad);
-  bad |= to < it.query0;
+  it.query0 = query_start(p, s, bad_start);
+  const int to = query_start(p, s + 1, bad_start);
+  bad_start |= to < it.query0;
   it.queries = max(to - it.query0, 0);
   const int per = 2 * p.tile_queries;
   it.blocks = (it.queries + per - 1) / per;
@@ -166,7 +167,7 @@ __device__ __forceinline__ bool next_item(const AttendParams &p, Item &it) {
     if (it.blocks > 0 && it.length > 0 && ++it.h < p.kv_heads) continue;
     it.h = 0;
     if (it.s + 1 >= p.sequences) return false;
-    load_sequence(p, it, it.s + 1, bad);
+    load_sequence(p, it, it.s + 1, bad, bad);
     if (it.length == 0) it.blocks = 0;
   }
 }
@@ -1109,12 +1110,18 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   // blocks are gone through by their warp
   const int chunk = (p.sequences + T - 1) / T;
   bool bad = false, hidden = false;
-  int mine = 0;
+  int mine = 0, good = p.sequences;   // places, and the first sequence whose starts are no good
   for (int i = 0; i < chunk; ++i) {
     const int s = tid * chunk + i;
     Item it;
     it.blocks = it.queries = it.length = 0;
-    if (s < p.sequences) load_sequence(p, it, s, bad);
+    bool bad_start = false;
+    if (s < good) load_sequence(p, it, s, bad, bad_start);
+    if (bad_start) {
+      good = s;
+      it.blocks = it.queries = 0;
+    }
+    bad |= bad_start;
     hidden |= it.queries > it.length;   // queries that see nothing
     int units = 0;
     const bool many = it.blocks > 4;
@@ -1139,23 +1146,41 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     }
     mine += units * p.kv_heads;
   }
-  int upto = mine;   // inclusive
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) c.warp_total[warp] = upto;
-  tc::fence_before_sync();
-  const bool any_hidden = __syncthreads_or(hidden);
-  tc::fence_after_sync();
-  const uint32_t tmem = c.tmem;
+  if (lane == 0) c.warp_good[warp] = p.sequences;
+  __syncwarp();
+  if (good < p.sequences) atomicMin(&c.warp_good[warp], good);
+  // The sequences before the first whose starts are no good follow one another: they have no
+  // more queries than the call, and so no more places than the host has allowed.  The others
+  // have none; with them the sum may have wrapped, so it is taken again without.
   Line line;
-  line.total = 0;
+  int upto, sequences;
+  bool any_hidden;
+  uint32_t tmem;
 #pragma unroll 1
-  for (int w = 0; w < T / 32; ++w) {
-    if (w < warp) upto += c.warp_total[w];
-    line.total += c.warp_total[w];
+  for (bool again = false;; again = true) {
+    uint32_t sum = uint32_t(mine), total = 0;   // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) c.warp_total[warp] = sum;
+    tc::fence_before_sync();
+    any_hidden = __syncthreads_or(hidden);
+    tc::fence_after_sync();
+    tmem = c.tmem;
+    sequences = p.sequences;
+#pragma unroll 1
+    for (int w = 0; w < T / 32; ++w) {
+      if (w < warp) sum += c.warp_total[w];
+      total += c.warp_total[w];
+      sequences = min(sequences, c.warp_good[w]);
+    }
+    upto = int(sum);
+    line.total = int(total);
+    if (again || sequences == p.sequences) break;
+    if (tid * chunk > sequences) mine = 0;
+    __syncthreads();
   }
   line.divide(gridDim.x);
   const int cta = min(int(blockIdx.x), line.grid);
@@ -1178,7 +1203,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
 #pragma unroll 1
     for (int s = (warp ? owner1 : owner0) * chunk; s < p.sequences; ++s) {
       Item it;
-      load_sequence(p, it, s, seen_before);
+      load_sequence(p, it, s, seen_before, seen_before);
       int n = 0;
 #pragma unroll 1
       for (int b = lane; b < it.blocks; b += 32) {
@@ -1226,9 +1251,9 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
 
   // ---- queries before their sequence's first position see nothing
   if (any_hidden) {
-    for (int s = blockIdx.x; s < p.sequences; s += gridDim.x) {
+    for (int s = blockIdx.x; s < sequences; s += gridDim.x) {
       Item it;
-      load_sequence(p, it, s, bad);
+      load_sequence(p, it, s, bad, bad);
       const int n = min(it.queries, it.queries - it.length);
       // (query, 16 bytes of its row), stepped: their product may be more than 2^31
       const int row = p.heads * D / 8;
