@@ -361,7 +361,8 @@ __device__ __forceinline__ void store32(uint16_t *out, bool whole_sectors, const
 // the largest |y| in [128, 256) is the sum of y rounded to E4M3 and the rest, which has no
 // more than E4M3's four bits either, down to 2^-2; below that the rest is rounded to a
 // multiple of 2^-9.  In place: 64 elements of BF16 give their row of 128 bytes to 64 of the
-// first piece and 64 of the second.  Returns 2^(e - 7), NaN for a row that is not finite.
+// first piece and 64 of the second.  Returns 2^(e - 7).  A row that is not finite becomes NaN,
+// in its pieces and not in the factor: places that it does not see stay hidden.
 template <int D>
 __device__ __forceinline__ float split_queries(unsigned char *tile, int row) {
   uint32_t top = 0;
@@ -377,6 +378,7 @@ __device__ __forceinline__ float split_queries(unsigned char *tile, int row) {
   for (int h = 0; h < D / 64; ++h) {
     unsigned char *at = tile + h * ROWS * 128 + row * 128;
     uint32_t hi[16], lo[16];
+    const uint32_t nan = e2 == 255 ? 0x7f7f7f7fu : 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint4 v = *reinterpret_cast<const uint4 *>(at + ((i ^ (row & 7)) * 16));
@@ -394,7 +396,7 @@ __device__ __forceinline__ float split_queries(unsigned char *tile, int row) {
           y[q] -= b0;
           y[q + 1] -= b1;
         }
-        hi[i * 2 + k / 2] = a;
+        hi[i * 2 + k / 2] = a | nan;
         lo[i * 2 + k / 2] = e4m3x4(y[0], y[1], y[2], y[3]);
       }
     }
@@ -404,7 +406,7 @@ __device__ __forceinline__ float split_queries(unsigned char *tile, int row) {
       *reinterpret_cast<uint4 *>(at + (((4 + i) ^ (row & 7)) * 16)) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
     }
   }
-  return e2 == 255 ? NAN : __uint_as_float(uint32_t(127 + e - 7) << 23);
+  return __uint_as_float(uint32_t(127 + e - 7) << 23);
 }
 
 // How far the maximum of the products may grow; finite, so that minus infinity grows.
@@ -442,8 +444,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
         tc::wait_or_abort_inline(&c.q_full, q_phase, abort);
         __syncwarp();
         scale = p.scale_log2 * split_queries<D>(smem + F::Q_AT + X * F::Q, tid);
-        // no scale is zero (minus infinity times zero is not a number); NaN stays
-        scale = scale < 1.2e-38f ? 1.2e-38f : scale;
+        // no scale is zero or infinite (minus infinity times zero is not a number)
+        scale = fminf(fmaxf(scale, 1.2e-38f), 3.4e38f);
         slack = slack_of(scale);
         tc::fence_proxy_async_smem();
         __syncwarp();
