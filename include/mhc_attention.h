@@ -106,11 +106,14 @@ typedef struct {
  * A sequence with a start that is out of range (0 .. tokens) or whose two starts
  * decrease, and every sequence behind it, has no queries: their rows are left as
  * they are.
- * The softmax and all sums are held in FP32.  In calls with q_starts or with more
- * than 16 heads for each kv head the weights are rounded to BF16, and over an
- * 8-bit cache queries are off by at most 2^-17 of their head's largest element (0
- * for elements from 2^-9 of it on); in the others weights keep 16 bits over a BF16
- * cache and FP16's over an 8-bit one.
+ * The softmax and all sums are held in FP32.  Sums of finite values are finite,
+ * whatever their size, and values from 2^-90 on have all their bits (over an 8-bit
+ * cache, in calls with q_starts or more than 16 heads for each kv head: values from
+ * 2^-70 to 2^110).  In calls with q_starts or with more than 16 heads for each kv
+ * head the weights are rounded to BF16, and over an 8-bit cache queries are off by
+ * at most 2^-17 of their head's largest element (0 for elements from 2^-9 of it
+ * on); in the others weights keep 16 bits over a BF16 cache and FP16's over an
+ * 8-bit one.
  * output and lse overlap no input. */
 typedef struct {
   int32_t tokens, sequences;

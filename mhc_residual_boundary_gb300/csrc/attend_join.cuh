@@ -23,6 +23,12 @@ namespace mhc {
 
 constexpr int JOIN_WIDTH = 16;   // parts that are joined at a time
 
+// Weights go into sums of a BF16 cache's values 2^DOWN smaller than they are: at most 2^8 for each
+// of 2^30 positions, no sum of finite values leaves FP32's range, however near to its end they
+// are.  At the other end, sums stop at 2^-149: a position's part at 2^-111 of the output.
+constexpr float DOWN = 38.f, UP = 274877906944.f;
+static_assert(UP == float(1ull << 38), "2^DOWN");
+
 // A CTA's parts: two (of what began with an earlier CTA, of what begins with it), each
 // [dim / 4][rows][4] floats and then [rows][4]: threads that have a row each write whole
 // lines.

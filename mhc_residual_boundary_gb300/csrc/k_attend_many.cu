@@ -14,8 +14,8 @@
 //  0-3, 4-7  softmax of tile A, of tile B: a thread has a row.  S = Q K^T comes from
 //            tensor memory, P = exp(S - m) goes back over it in BF16; the output stays
 //            in tensor memory for the whole item and is rescaled only when the running
-//            maximum grows by more than 2^8 (P is then at most 2^8, and the sum of P
-//            is held in FP32).  At the item's end the thread writes its row.
+//            maximum grows by more than 2^8 (the sum of P is held in FP32; see DOWN_BY).
+//            At the item's end the thread writes its row.
 //  8         copies: queries, keys and values by TMA, page by page
 //  9         the products: O_A += P_A V(j), S_A(j + 1), O_B += P_B V(j), S_B(j + 1), so that
 //            one tile's softmax runs beside the other's products
@@ -50,7 +50,7 @@ constexpr int KEYS = 128;            // positions of a unit
 constexpr int ROWS = 128;            // rows of a tile
 constexpr int INFOS = 8;             // units whose notes are kept, and segments: no more of them can be under way
 constexpr int CUT = 5;               // places that a cut through all rows costs besides EXTRA + 1
-constexpr float GROWTH = 8.f;        // log2 of what P may reach
+constexpr float GROWTH = 8.f;        // log2 of what P may reach over the reference
 constexpr int EXTRA = 2;             // places on the line that an item takes besides its units, for its beginning and end
 
 __device__ int g_stall_copies;       // test hook: the copying warp issues no copies
@@ -412,6 +412,19 @@ __device__ __forceinline__ float split_queries(unsigned char *tile, int row) {
 // How far the maximum of the products may grow; finite, so that minus infinity grows.
 __device__ __forceinline__ float slack_of(float scale) { return fminf(GROWTH / scale, 3.4e38f); }
 
+// Over an 8-bit cache P has the value's scale in it, and both ends matter: it stops at BF16's
+// 2^-126, and 2^30 positions with values of 2^110 (2^20 with 2^120) have their sum.
+template <bool FP8>
+constexpr float DOWN_BY = FP8 ? 20.f : DOWN;
+template <bool FP8>
+constexpr float UP_BY = FP8 ? 1048576.f : UP;
+// What is added to x * scale: the reference becomes 2^-DOWN_BY.  As it is rounded it is part of
+// what lse is made of.
+template <bool FP8>
+__device__ __forceinline__ float exponent_base(float top, float scale) { return fmaf(-top, scale, -DOWN_BY<FP8>); }
+template <bool FP8>
+__device__ __forceinline__ float reference(float top, float scale) { return -(exponent_base<FP8>(top, scale) + DOWN_BY<FP8>); }
+
 template <int D, bool FP8>
 __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned char *smem, Control &c, uint32_t tmem, int X) {
   using F = Many<D, FP8>;
@@ -534,7 +547,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
           }
         }
       }
-      const float base = top == -INFINITY ? 0.f : -top * scale;
+      const float base = top == -INFINITY ? 0.f : exponent_base<FP8>(top, scale);
       const uint64_t scale2 = tc::pair(scale, scale), base2 = tc::pair(base, base);
       uint64_t sums[2] = {0ull, 0ull};
 #pragma unroll
@@ -657,7 +670,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
           out[i] = uint16_t(pack_bf16x2(x, 0.f));
         }
       }
-      if (live && lse) *lse = sum_now != 0.f ? (top_now * scale + log2f(sum_now)) * 0.69314718056f : -INFINITY;
+      if (live && lse) *lse = sum_now != 0.f ? (reference<FP8>(top_now, scale) + log2f(sum_now * UP_BY<FP8>)) * 0.69314718056f : -INFINITY;
       poisoned = false;
       tc::fence_before_sync();
       release();
@@ -687,7 +700,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &p, unsigned cha
     poisoned = false;
     tc::fence_before_sync();
     if (live) {
-      const float m = had ? top_now * scale : -INFINITY;
+      const float m = top_now != -INFINITY ? reference<FP8>(top_now, scale) : -INFINITY;
       *reinterpret_cast<float4 *>(part + ROWS * D + tid * 4) = make_float4(m, sum_now, m, 0.f);
     }
     // who writes the last part of sixteen joins them, once there is no other work
@@ -1317,7 +1330,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
                       const float f = n != 0.f ? 1.f / n : 0.f;
                       *reinterpret_cast<uint2 *>(p.output + token * p.output_stride + int64_t(head) * D + col) =
                           make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-                      if (p.lse && col == 0) p.lse[token * p.heads + head] = n != 0.f ? ((all == -INFINITY ? 0.f : all) + log2f(n)) * 0.69314718056f : -INFINITY;
+                      if (p.lse && col == 0) p.lse[token * p.heads + head] = n != 0.f ? ((all == -INFINITY ? 0.f : all) + log2f(n * UP_BY<FP8>)) * 0.69314718056f : -INFINITY;
                     },
                     &c.join_flag);
     }

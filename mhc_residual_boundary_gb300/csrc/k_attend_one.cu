@@ -194,7 +194,7 @@ template <bool FP8>
 __device__ __forceinline__ void store_row4(const AttendParams &p, int s, int head, int col, int dim, float all, float n,
                                            float all_out, const float4 &o) {
   const float b = all == -INFINITY ? 0.f : all, bo = all_out == -INFINITY ? 0.f : all_out;
-  const float f = n != 0.f ? (FP8 ? exp2_fast(bo - b) : 1.f) / n : 0.f;
+  const float f = n != 0.f ? (FP8 ? exp2_fast(bo - b) : UP) / n : 0.f;
   *reinterpret_cast<uint2 *>(p.output + s * p.output_stride + int64_t(head) * dim + col) =
       make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
   if (p.lse && col == 0) p.lse[int64_t(s) * p.heads + head] = n != 0.f ? (b + log2f(n)) * 0.69314718056f : -INFINITY;
@@ -573,11 +573,12 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
               if (FP8) {
                 pa[n][r] = transpose8(pack_f16x2(exp2_fast(y[n][j][2 * r] - base_out[n][0]), exp2_fast(y[n][j][2 * r + 1] - base_out[n][1])));
               } else {
+                const float v0 = w0 * (1.f / UP), v1 = w1 * (1.f / UP);
                 // the first piece cut off, not rounded: the second is what is left, never negative and
                 // never zero, so that both times an infinity are the same infinity
-                const uint32_t w = __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
+                const uint32_t w = __byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x7632);
                 pa[n][r] = transpose8(w);
-                pb[n][r] = transpose8(pack_bf16x2(fmaxf(w0 - bf16_lo(w), LEAST), fmaxf(w1 - bf16_hi(w), LEAST)));
+                pb[n][r] = transpose8(pack_bf16x2(fmaxf(v0 - bf16_lo(w), LEAST), fmaxf(v1 - bf16_hi(w), LEAST)));
               }
             }
           const int row = j * 16 + 2 * t;   // this lane's positions: row, row + 1, row + 8, row + 9
