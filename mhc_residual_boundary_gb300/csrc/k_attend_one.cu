@@ -22,9 +22,10 @@
 // the products' inner indexes is free as long as both factors use the same, and so is
 // that of O's rows: lanes take their fragments as whole 16-byte pieces of K's and V's
 // rows, and the fragments of Q and the rows of O^T follow.  Over a BF16 cache P goes in
-// as two BF16 pieces (16 bits of it), over an 8-bit one everything is FP16: E4M3 fits
+// as two positive BF16 pieces (16 bits of it), over an 8-bit one everything is FP16: E4M3 fits
 // it, Q is taken with a power of two off each head's row, and P carries the value's
-// scale, 2^(x + log2 scale - its own running maximum), so that it uses FP16's upper range.
+// scale, 2^(x + log2 scale - its own running maximum + 7): from 2^15 down to 2^-24, so that
+// what is lost of a weight below the normals is at most 2^-32 of the largest.
 //
 // Bound by memory where the caches are long: 64 sequences of 8192 positions, 48 heads on 8
 // of 128, in 162 us, 6.6 TB/s (0.97 of a copy; 200 with products whose rows are heads, 191
@@ -49,6 +50,7 @@ constexpr int EXTRA = 1;   // places on the line that a (sequence, head) takes b
 constexpr int COST = 2, COST_MANY = 5;
 static_assert(COST > EXTRA, "a cut has a unit on either side");
 constexpr float GROWTH = 8.f;   // log2 of what a weight may reach
+constexpr float ROOM = 7.f;     // log2 of FP16's largest weight over 2^GROWTH (8-bit cache)
 constexpr float LEAST = 1.17549435e-38f;   // of a weight's second piece, 2^-126: nothing beside the first one
 
 template <int D, bool FP8>
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             base_out[n][e] = base[n][e] = top[n][e] == -INFINITY ? 0.f : top[n][e];
-            if (FP8) base_out[n][e] = top_out[n][e] == -INFINITY ? 0.f : top_out[n][e];
+            if (FP8) base_out[n][e] = top_out[n][e] == -INFINITY ? 0.f : top_out[n][e] - ROOM;
           }
         // ---- weights and their sum, values times weights, 16 positions at a time
 #pragma unroll
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__((One<D, FP8>::THREADS), (One<D, FP8>::SM_CTAS)
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int o = 4; o < 32; o *= 2) sum[n][e] += __shfl_xor_sync(0xffffffffu, sum[n][e], o);
-        if (g == 0) stats[warp * 16 + 8 * n + 2 * t + e] = make_float4(top[n][e], sum[n][e], FP8 ? top_out[n][e] : top[n][e], 0.f);
+        if (g == 0) stats[warp * 16 + 8 * n + 2 * t + e] = make_float4(top[n][e], sum[n][e], FP8 ? top_out[n][e] - ROOM : top[n][e], 0.f);
       }
     for (int r0 = 0; r0 < group; r0 += F::PASS) {
       const int rows = min(F::PASS, group - r0);
