@@ -57,9 +57,10 @@ enum {
  * 64 or 128.  page_size: 16, 32, 64 or 128.  rotary_dim: the first elements of
  * a head that append rotates, a multiple of 16 up to head_dim, or 0 for none;
  * pair i of position p by the angle p * f(i), with f(i) = frequencies[i]
- * (rotary_dim / 2 finite values in host memory, read by create) or, where that
- * is NULL, theta^(-2i / rotary_dim).  The angle is reduced exactly: f(i) / 2 pi
- * is held in 64 bits behind the point. */
+ * (rotary_dim / 2 values between -2^40 and 2^40 in host memory, read by create) or,
+ * where that is NULL, theta^(-2i / rotary_dim), a double either way.  An angle's
+ * whole turns are dropped exactly: f(i) / 2 pi is held in 64 bits behind the
+ * point, and off by 2^-64 turns a position. */
 typedef struct {
   int32_t heads, kv_heads, head_dim, page_size;
   int32_t rotary_dim;

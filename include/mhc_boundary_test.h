@@ -34,6 +34,10 @@ mhc_status_t mhc_test_stall_sublayer_copies(int32_t on);
  * (mhc_attention_check_errors reports). */
 mhc_status_t mhc_test_stall_attention_copies(int32_t on);
 
+/* frequency / 2 pi behind the point, in units of 2^-64 turns, as append's
+ * angles are made of (|frequency| below 2^40).  Needs no GPU. */
+uint64_t mhc_test_attention_turns(double frequency);
+
 /* Where things lie in the shared memory of a CTA of the moe kernel, in bytes,
  * for a call of m tokens on a GPU of that many SMs.  Needs no GPU. */
 typedef struct {

@@ -182,6 +182,8 @@ def lib() -> ctypes.CDLL:
         h.mhc_test_stall_sublayer_copies.restype = st
         h.mhc_test_stall_attention_copies.argtypes = [ctypes.c_int32]
         h.mhc_test_stall_attention_copies.restype = st
+        h.mhc_test_attention_turns.argtypes = [ctypes.c_double]
+        h.mhc_test_attention_turns.restype = ctypes.c_uint64
         h.mhc_test_moe_form.argtypes = [ctypes.POINTER(mhc_sublayer_config_t), ctypes.c_int32, ctypes.c_int32,
                                         ctypes.POINTER(mhc_test_moe_form_t)]
         h.mhc_test_moe_form.restype = st
@@ -294,6 +296,11 @@ def mhc_test_stall_attention_copies(on: bool) -> None:
     status = lib().mhc_test_stall_attention_copies(1 if on else 0)
     if status != MHC_OK:
         raise MhcError(status, "could not set the stall flag")
+
+
+def mhc_test_attention_turns(frequency: float) -> int:
+    """Test hook: a frequency's turns a position, behind the point, in units of 2^-64 (needs no GPU)."""
+    return lib().mhc_test_attention_turns(frequency)
 
 
 def mhc_test_moe_form(config: mhc_sublayer_config_t, m: int, sms: int) -> mhc_test_moe_form_t:

@@ -127,6 +127,18 @@ mhc_status_t check_cache(mhc_attention_t *a, int pages, const void *k, int64_t k
 int counter_ctas(const mhc_attention_t *a) { return 2 * a->sm_count; }
 size_t counter_bytes(const mhc_attention_t *a) { return size_t(2) * 3 * counter_ctas(a) * sizeof(unsigned int); }
 
+// f / 2 pi behind the point, in 64 bits: within one of the last of them.  1 / 2 pi is the sum of
+// two doubles, off by 2^-110, so a product with less than 2^40 is off by less than 2^-67 (with
+// 1 / 2 pi in one double it is off by up to 2^-55 for f = 1 already, 2^-24 turns 2^31 positions on).
+constexpr double MOST_FREQUENCY = 0x1p40;
+uint64_t turns_of(double f) {
+  constexpr double INVERSE = 0x1.45f306dc9c883p-3, REST = -0x1.6b01ec5417056p-57;
+  const double t = f * INVERSE, rest = std::fma(f, REST, std::fma(f, INVERSE, -t));
+  const double high = std::ldexp(t - std::trunc(t), 64), whole = std::floor(high);   // exact
+  const double low = std::floor(high - whole + std::ldexp(rest, 64) + 0.5);
+  return uint64_t(__int128(whole)) + uint64_t(int64_t(low));
+}
+
 void release(mhc_attention_t *a) {
   if (a->turns) cudaFree(a->turns);
   if (a->counters) cudaFree(a->counters);
@@ -159,9 +171,9 @@ mhc_status_t mhc_attention_create(const mhc_attention_config_t *config, int devi
     return fail(msg, MHC_ERR_INVALID_ARG, "theta must be positive and finite");
   for (int i = 0; i < c.rotary_dim / 2; ++i) {
     const double f = c.frequencies ? c.frequencies[i] : std::pow(c.theta, -2.0 * i / c.rotary_dim);
-    if (!std::isfinite(f)) return fail(msg, MHC_ERR_INVALID_ARG, "frequency %d is not finite", i);
-    const double t = f / 6.283185307179586476925;
-    turns[i] = uint64_t(std::ldexp(t - std::floor(t), 64) >= 0x1p64 ? 0 : std::ldexp(t - std::floor(t), 64));
+    if (!(std::fabs(f) < MOST_FREQUENCY))
+      return fail(msg, MHC_ERR_INVALID_ARG, "frequency %d is not between -2^40 and 2^40", i);
+    turns[i] = turns_of(f);
   }
   int count = 0;
   if (cudaGetDeviceCount(&count) != cudaSuccess || device < 0 || device >= count)
@@ -374,3 +386,5 @@ const char *mhc_attention_last_error(const mhc_attention_t *a) {
 mhc_status_t mhc_test_stall_attention_copies(int32_t on) {
   return attend_stall_copies(on ? 1 : 0) == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
 }
+
+uint64_t mhc_test_attention_turns(double frequency) { return turns_of(frequency); }
