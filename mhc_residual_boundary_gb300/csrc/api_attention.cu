@@ -45,8 +45,9 @@ struct DeviceGuard {
   }
 };
 
+constexpr size_t MESSAGE = 512;   // bytes of one, at most
 mhc_status_t fail(std::string &slot, mhc_status_t status, const char *fmt, ...) {
-  char buf[512];
+  char buf[MESSAGE];
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(buf, sizeof buf, fmt, ap);
@@ -179,8 +180,11 @@ mhc_status_t mhc_attention_create(const mhc_attention_config_t *config, int devi
   if (cudaGetDeviceCount(&count) != cudaSuccess || device < 0 || device >= count)
     return fail(msg, MHC_ERR_CUDA, "device %d is not available", device);
   DeviceGuard guard(device);
+  std::string message;
+  message.reserve(MESSAGE);
   mhc_attention_t *a = new (std::nothrow) mhc_attention();
   if (!a) return fail(msg, MHC_ERR_OOM, "host allocation failed");
+  a->last_error.swap(message);   // room for what the calls say: nothing is thrown out of them
   a->cfg = c;
   a->cfg.frequencies = nullptr;
   a->device = device;
