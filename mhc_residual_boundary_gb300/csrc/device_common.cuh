@@ -86,6 +86,10 @@ __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A barrier of the CTA's threads, wherever the others of their warps are: __syncthreads() asks
+// for whole warps, which a branch of one thread may have left in two.
+__device__ __forceinline__ void sync_threads_apart() { asm volatile("barrier.sync 0;" ::: "memory"); }
+
 // --------------------------------------------------- mixes and MXFP8 steps
 // sigmoid(z) = 1 / (1 + exp(-z)) with a correctly rounded reciprocal.
 __device__ __forceinline__ float sigmoid(float z) {

@@ -53,6 +53,8 @@ constexpr int CUT = 5;               // places that a cut through all rows costs
 constexpr float GROWTH = 8.f;        // log2 of what P may reach over the reference
 constexpr int EXTRA = 2;             // places on the line that an item takes besides its units, for its beginning and end
 
+constexpr int TMEM_WARP = 11;        // has the tensor memory: a warp whose threads stay together
+
 __device__ int g_stall_copies;       // test hook: the copying warp issues no copies
 
 template <int D, bool FP8>
@@ -1112,7 +1114,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
     tc::mbar_init_fence();
     c.abort = c.issued = c.k_issued = c.q_issued = c.join_count = 0;
   }
-  if (warp == 9) tc::tmem_alloc(&c.tmem, 512);
+  if (warp == TMEM_WARP) tc::tmem_alloc(&c.tmem, 512);
   if (warp == 8 && lane == 0) {
     tc::tma_prefetch_desc(&tm_q);
     tc::tma_prefetch_desc(&tm_k);
@@ -1289,9 +1291,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   }
   if (bad) atomicOr(p.err, ATTN_ERR_INDEX);
 
-  // a warp's threads together again, here and behind the roles (of the warp with the products
-  // one thread has been at work): what follows is for whole warps
-  __syncwarp();
+  __syncwarp();   // setmaxnreg is for whole warps
   if (c.bounds[0] < c.bounds[1]) {
     if (warp < 8) {
       registers_up<F::R_SOFT>();
@@ -1309,12 +1309,17 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
       }
     }
   }
+  // The thread with the products comes apart from the rest of its warp, and __syncwarp() does not
+  // bring them together for good (seen by their masks): from here on that warp meets no
+  // instruction for whole warps.  The barrier counts threads, and the tensor memory is another
+  // warp's.  (With __syncthreads() here and the tensor memory in that warp, calls of few rows
+  // a tile ended in a launch failure now and then.)
   __syncwarp();
   tc::fence_before_sync();
-  __syncthreads();
+  sync_threads_apart();
   tc::fence_after_sync();
   __syncwarp();
-  if (warp == 9) tc::tmem_dealloc(c.tmem, 512);
+  if (warp == TMEM_WARP) tc::tmem_dealloc(c.tmem, 512);
   if (!c.abort && warp < 8) {   // those with the most registers
     const int group = p.heads / p.kv_heads;
 #pragma unroll 1
