@@ -106,6 +106,13 @@ struct Item {
   __device__ __forceinline__ int cost(int group) const;
 };
 
+// A wait for a phase also passes while the phase before the last one is open, so whoever waits at a
+// barrier has to see each of its phases.  Over a BF16 cache keys and values share a ring of slots, but
+// not who waits for them: `full` (keys) and `raw_full` (values) go with the units, not with the
+// slots.  (By slots, five of them, the third unit's values followed the first one's keys: they counted
+// as there when the first two units' values came before those keys.  The product took what was in
+// the slot, and the next copy into it, with that one on its way, ended the launch: one of some
+// 300000 calls over long caches.)
 struct Control {
   uint64_t full[8], empty[8], raw_full[8], raw_empty[8];
   uint64_t info_full[INFOS], info_empty[INFOS], ready[INFOS];
@@ -786,7 +793,7 @@ __device__ __forceinline__ void load_role(const AttendParams &p, unsigned char *
       for (int kv = 0; kv < 2; ++kv) {
         const bool keys = FP8 && kv == 0;   // have a ring of their own
         Ring &at = keys ? k_ring : ring;
-        uint64_t *full = (FP8 ? keys ? c.k_full : c.raw_full : c.full) + at.at;
+        uint64_t *full = FP8 ? (keys ? c.k_full : c.raw_full) + at.at : (kv ? c.raw_full : c.full) + info.at;
         uint64_t *empty = (FP8 ? keys ? c.k_empty : c.raw_empty : c.empty) + at.at;
         ok = tc::wait_or_abort(empty, at.phase ^ 1u, abort) &&
              (kv == 1 || tc::wait_or_abort(&c.info_empty[info.at], info.phase ^ 1u, abort));
@@ -887,7 +894,7 @@ __device__ __forceinline__ void mma_role(unsigned char *smem, Control &c, uint32
           q_phase ^= 1u;
         }
       }
-      ok = ok && (FP8 ? tc::wait_or_abort(&c.k_full[k_at.at], k_at.phase, abort) : tc::wait_or_abort(&c.full[at.at], at.phase, abort));
+      ok = ok && (FP8 ? tc::wait_or_abort(&c.k_full[k_at.at], k_at.phase, abort) : tc::wait_or_abort(&c.full[info.at], info.phase, abort));
       if (!ok) break;
     }
     if (!first) {
@@ -997,7 +1004,7 @@ __device__ __forceinline__ void clean_role(unsigned char *smem, Control &c) {
     const uint32_t flags = c.info[info.at].flags;
     if (flags & STOP) break;
     slot.next(F::SLOTS);
-    if (!__all_sync(0xffffffffu, tc::wait_or_abort(&c.full[slot.at], slot.phase, abort))) break;
+    if (!__all_sync(0xffffffffu, tc::wait_or_abort(&c.raw_full[info.at], info.phase, abort))) break;
     if (hides(flags)) {
       clean_values<D>(smem + F::SLOTS_AT + slot.at * F::SLOT, c.info[info.at].poison, thread, 64);
       tc::fence_proxy_async_smem();
@@ -1312,8 +1319,7 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   // The thread with the products comes apart from the rest of its warp, and __syncwarp() does not
   // bring them together for good (seen by their masks): from here on that warp meets no
   // instruction for whole warps.  The barrier counts threads, and the tensor memory is another
-  // warp's.  (With __syncthreads() here and the tensor memory in that warp, calls of few rows
-  // a tile ended in a launch failure now and then.)
+  // warp's.
   __syncwarp();
   tc::fence_before_sync();
   sync_threads_apart();
@@ -1343,10 +1349,13 @@ k_attend_many(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, co
   if (tid == 0 && c.abort) {
     atomicOr(p.err, ATTN_ERR_WAIT);
     // copies in flight land before the CTA's shared memory goes
-    uint64_t *full = FP8 ? c.raw_full : c.full;
-    const int slots = FP8 ? F::RAWS : F::SLOTS;
-    for (int i = max(0, c.issued - slots); i < c.issued; ++i)
-      tc::mbar_wait_bounded(&full[i % slots], uint32_t(i / slots & 1), tc::SUB_WAIT_LIMIT);
+    if (FP8) {
+      for (int i = max(0, c.issued - F::RAWS); i < c.issued; ++i)
+        tc::mbar_wait_bounded(&c.raw_full[i % max(F::RAWS, 1)], uint32_t(i / max(F::RAWS, 1) & 1), tc::SUB_WAIT_LIMIT);
+    } else {   // keys, values, keys, ...
+      for (int i = max(0, c.issued - 2 * INFOS); i < c.issued; ++i)
+        tc::mbar_wait_bounded(&(i % 2 ? c.raw_full : c.full)[i / 2 % INFOS], uint32_t(i / 2 / INFOS & 1), tc::SUB_WAIT_LIMIT);
+    }
     if (FP8)
       for (int i = max(0, c.k_issued - F::KSLOTS); i < c.k_issued; ++i)
         tc::mbar_wait_bounded(&c.k_full[i % max(F::KSLOTS, 1)], uint32_t(i / max(F::KSLOTS, 1) & 1), tc::SUB_WAIT_LIMIT);
