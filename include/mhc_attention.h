@@ -101,8 +101,8 @@ typedef struct {
  * position p = lengths[s] - n + i and sees the positions j <= p with, where window
  * > 0, j > p - window or j < sinks.  A query's row of output is
  *   sum over j of exp(x_j) v_j / sum over j of exp(x_j),  x_j = scale * q k_j,
- * and lse the logarithm of the lower sum (natural); a row that sees nothing
- * has zeros and minus infinity.  Positions that a query does not see may hold
+ * and lse the logarithm of the lower sum (natural); a row that sees nothing, or
+ * whose scores are all minus infinity, has zeros and minus infinity.  Positions that a query does not see may hold
  * anything.  Rows of output from q_starts[sequences] on are left as they are.
  * A sequence with a start that is out of range (0 .. tokens) or whose two starts
  * decrease, and every sequence behind it, has no queries: their rows are left as
@@ -113,8 +113,9 @@ typedef struct {
  * 2^-70 to 2^110).  In calls with q_starts or with more than 16 heads for each kv
  * head the weights are rounded to BF16, and over an 8-bit cache queries are off by
  * at most 2^-17 of their head's largest element (0 for elements from 2^-9 of it
- * on); in the others weights keep 16 bits over a BF16 cache and FP16's over an
- * 8-bit one.
+ * on); in the others weights keep 16 bits over a BF16 cache, and over an 8-bit one
+ * FP16's 11 (fewer below 2^-21 of the largest, where they are off by 2^-32 of it),
+ * and queries are off by at most 2^-25 of their head's largest element.
  * output and lse overlap no input. */
 typedef struct {
   int32_t tokens, sequences;

@@ -28,12 +28,13 @@
 //
 // Bound by the chain S, softmax, P of a tile: two tiles in turn keep the tensor cores at
 // work for 2048 of about 3000 clocks a unit (head_dim 128), and an item's ends cost two more
-// units' time.  48 heads on 8 of 128: a prompt of 4096 in 177 us (1160 TFLOP/s, 0.60 of a
+// units' time.  48 heads on 8 of 128: a prompt of 4096 in 178 us (1160 TFLOP/s, 0.60 of a
 // library product's rate), 1024 more queries over 16384 positions in 273 us (0.76).  What
 // runs once an item, and what few units need, is kept short or apart: instructions that
 // are not in the SM's caches cost more than those that are executed.  Few rows over a long
 // cache: the same chain with one tile, 8 sequences of 4 queries over up to 32768 positions in
-// 62 us, 4.8 TB/s.  Over an 8-bit cache the scales' loads and products come on top of the
+// 62 us, 4.8 TB/s, and 64 single tokens of 32 heads a kv head over up to 8192 in 97 us, 5.5 TB/s.
+// Over an 8-bit cache the scales' loads and products come on top of the
 // softmax: 3 x 1024 queries of 40 heads on 8 over up to 8000 positions in 306 us, 0.44.
 #include <algorithm>
 #include <type_traits>

@@ -4,8 +4,8 @@
 // The work is the reading of the cache: 4 d flops for every 2 d bytes (BF16) and
 // head of a group, far below what the tensor cores do in that time.  So:
 //  * Every row of the cache is read once, for all heads of its group, by 16-byte
-//    asynchronous copies into shared memory; a warp keeps STAGES - 1 tiles (about
-//    16 KB) on their way while it works on one.  Copies of places that are not there
+//    asynchronous copies into shared memory; a warp keeps STAGES - 1 tiles (one of 8 KB;
+//    three, 13 KB, of 8-bit heads of 64) on their way while it works on one.  Copies of places that are not there
 //    (behind the end, a page out of range) read nothing and leave zeros.
 //  * A sequence and kv head's visible positions (the first ones and the window, one
 //    behind the other) are cut into units of the warps' tiles.  The call's units form one
@@ -31,7 +31,7 @@
 // of 128, in 162 us, 6.6 TB/s (0.97 of a copy; 200 with products whose rows are heads, 191
 // with one CTA of eight warps an SM, 173 with cuts wherever an even division puts them).  8 bits, 16 heads a kv head: the conversions and
 // products share the time with the copies, 37 sequences of up to 16001 positions on 4 kv heads
-// in 67 us (4.8 TB/s).  Few positions: trips through memory one after another (lengths, pages,
+// in 67 us (4.8 TB/s); 12 heads a kv head over BF16, 64 of 8192, in 169 us.  Few positions: trips through memory one after another (lengths, pages,
 // rows, parts), 3.7 us for one unit, 8 for 700 positions cut and joined.
 #include <algorithm>
 

@@ -50,3 +50,22 @@ def test_queries_that_see_nothing_hold_anything(fp8, d, value):
             a.check_errors()
     assert (got["output"][37:] == 0).all() and (got["lse"][37:] == -math.inf).all()
     assert torch.isfinite(got["output"]).all()
+
+
+@pytest.mark.parametrize("several", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_minus_infinity_only(several, d):
+    """Rows whose scores are all minus infinity are as rows that see nothing; a finite score beside such ones is all
+    that counts."""
+    inputs = make_inputs(17, lengths=[1, 130, 200], queries=[1, 1, 1] if several else None, heads=8, kv=2, d=d, page=16,
+                         fp8=False)
+    inputs["q"][..., 0] = 1.0
+    inputs["k_cache"][..., 0] = -math.inf
+    at = int(inputs["pages"][2, 150 // 16]), 1, 150 % 16
+    inputs["k_cache"][at[0], at[1], at[2], 0] = 0.5
+    got = call(inputs, 16)
+    none = torch.ones(3, 8, dtype=torch.bool, device="cuda")
+    none[2, 4:] = False
+    assert (got["output"][none] == 0).all() and (got["lse"][none] == -math.inf).all()
+    value = inputs["v_cache"][at].expand(4, d)
+    assert torch.equal(got["output"][2, 4:], value) and torch.isfinite(got["lse"][2, 4:]).all()
