@@ -132,6 +132,8 @@ struct Control {
   int join_count, join_flag;
 };
 
+static_assert(INFOS <= 8, "keys and values have a barrier for each unit under way");
+
 template <int D, bool FP8>
 constexpr int smem_bytes() { return Many<D, FP8>::CONTROL_AT + int(sizeof(Control)); }
 static_assert(smem_bytes<128, false>() <= 227 * 1024 && smem_bytes<128, true>() <= 227 * 1024 &&
